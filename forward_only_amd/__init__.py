@@ -11,16 +11,21 @@ sizes).  All arithmetic runs in the library's HIP kernels; there is no CPU path.
     ...
     c = zo_probe_weights(ctx, Lp, Lm, L0, eps, delta)
     zo_update(ctx, theta, offset, step, c, eta)             # theta - eta * sum c_i z_i
+
+The language-model operators (zo_adapter_project, zo_head_logprobs, zo_token_logprobs,
+zo_group_loss) turn a batch of rows into such losses; their matrices may have rows further
+apart than their length, and what they allocate belongs to the stream they run on.
 """
 from __future__ import annotations
 
 import ctypes
+from typing import NamedTuple, Optional
 
 import torch
 
 from . import _lib
 from ._lib import (ZO_BF16, ZO_EHIP, ZO_EINVAL, ZO_ENOMEM, ZO_EUNSUPPORTED, ZO_FP32,  # noqa: F401
-                   ZO_MAX_NPERT, ZO_NOALLOC_SCRATCH_BYTES, ZO_OK, ZO_WEIGHTS_POWER, ZO_WEIGHTS_PRECOND,
+                   ZO_IGNORE_TOKEN, ZO_MAX_NPERT, ZO_MAX_RANK, ZO_MAX_TOP_K, ZO_NOALLOC_SCRATCH_BYTES, ZO_OK, ZO_WEIGHTS_POWER, ZO_WEIGHTS_PRECOND,
                    ZO_WEIGHTS_SPSA_MEAN, ZOError)
 
 __all__ = [
@@ -31,7 +36,9 @@ __all__ = [
     "zo_lowrank_quad_loss", "zo_mlp_workspace_bytes", "zo_mlp_loss", "zo_mlp_loss_perturbed",
     "zo_mlp_loss_pair", "zo_mlp_probes_workspace_bytes", "zo_mlp_loss_probes",
     "zo_mlp_loss_pair_noalloc", "zo_stream_rmw", "zo_tune_placement", "zo_set_slice_bytes",
-    "zo_get_slice_bytes", "library_path",
+    "zo_get_slice_bytes", "library_path", "TokenLogprobs", "HeadLogprobs",
+    "zo_token_logprobs", "zo_head_workspace_bytes", "zo_head_logprobs", "zo_group_loss",
+    "zo_adapter_workspace_bytes", "zo_adapter_project",
 ]
 
 
@@ -464,3 +471,210 @@ def zo_set_slice_bytes(ctx: Context, slice_bytes: int) -> None:
 
 def zo_get_slice_bytes(ctx: Context) -> int:
     return int(_lib.lib().zo_get_slice_bytes(ctx.handle))
+
+
+class TokenLogprobs(NamedTuple):
+    """Results of zo_token_logprobs; what was not asked for is None."""
+    logp: Optional[torch.Tensor]
+    entropy: Optional[torch.Tensor]
+    top_ids: Optional[torch.Tensor]
+    top_logp: Optional[torch.Tensor]
+
+
+class HeadLogprobs(NamedTuple):
+    """Results of zo_head_logprobs; what was not asked for is None."""
+    logp: Optional[torch.Tensor]
+    entropy: Optional[torch.Tensor]
+
+
+def _new(shape, dtype, stream):
+    """A new tensor that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device="cuda")
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device="cuda")
+
+
+def _matrix(t: torch.Tensor, name: str, dtype=None):
+    """(device pointer, rows, columns, elements between rows) of a 2-D tensor whose rows are
+    contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got shape {tuple(t.shape)}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor (got {t.device})")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device "
+                         f"cuda:{torch.cuda.current_device()}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), rows, cols, t.stride(0) if rows > 1 else cols
+
+
+def _vector(t, name: str, n: int, dtype):
+    """Device pointer of a contiguous 1-D tensor of n elements, or None."""
+    if t is None:
+        return None
+    p = _dev(t, name, dtype)
+    if t.dim() != 1 or t.numel() != n:
+        raise ValueError(f"{name} must hold {n} values in one dimension, got shape {tuple(t.shape)}")
+    return p
+
+
+def zo_token_logprobs(ctx: Context, logits: torch.Tensor, targets: torch.Tensor | None = None,
+                      top_k: int = 0, entropy: bool = True, out: TokenLogprobs | None = None,
+                      stream=None) -> TokenLogprobs:
+    """Log probability of each row's target, entropy (nats) and the top_k alternatives (ids
+    int64, log probabilities; value descending, then index ascending) from logits [rows,
+    vocab] in one pass.  targets: int64 [rows]; ZO_IGNORE_TOKEN rows are not read and give
+    0, 0, -1, 0; None gives no logp.  out: tensors of an earlier call of the same shapes."""
+    lp, rows, vocab, stride = _matrix(logits, "logits")
+    top_k = int(top_k)
+    code = _dtype_code(logits)
+    tp = _vector(targets, "targets", rows, torch.int64)
+    if not 0 <= top_k <= ZO_MAX_TOP_K:
+        raise ValueError(f"top_k must be in [0, {ZO_MAX_TOP_K}]")
+    if out is None:
+        out = TokenLogprobs(
+            None if tp is None else _new(rows, torch.float32, stream),
+            _new(rows, torch.float32, stream) if entropy else None,
+            _new((rows, top_k), torch.int64, stream) if top_k else None,
+            _new((rows, top_k), torch.float32, stream) if top_k else None)
+    if (out.logp is None) != (targets is None):
+        raise ValueError("logp goes with targets")
+    op, ep = _vector(out.logp, "logp", rows, torch.float32), _vector(out.entropy, "entropy", rows,
+                                                                     torch.float32)
+    ip = vp = None
+    if top_k:
+        ip, vp = _dev(out.top_ids, "top_ids", torch.int64), _dev(out.top_logp, "top_logp",
+                                                                 torch.float32)
+        if tuple(out.top_ids.shape) != (rows, top_k) or tuple(out.top_logp.shape) != (rows, top_k):
+            raise ValueError(f"top_ids and top_logp must have shape ({rows}, {top_k})")
+    _lib.check(_lib.lib().zo_token_logprobs(ctx.handle, lp, code, rows, vocab, stride, tp, op, ep,
+                                            top_k, ip, vp, _stream(stream)), "zo_token_logprobs")
+    return out
+
+
+def zo_head_workspace_bytes(rows: int, vocab: int) -> int:
+    return int(_lib.lib().zo_head_workspace_bytes(rows, vocab))
+
+
+def zo_head_logprobs(ctx: Context, hidden: torch.Tensor, weight: torch.Tensor,
+                     targets: torch.Tensor | None = None, entropy: bool = True,
+                     workspace: torch.Tensor | None = None, out: HeadLogprobs | None = None,
+                     stream=None) -> HeadLogprobs:
+    """Log probabilities of the targets and entropies of the logits hidden @ weight.T (hidden
+    [rows, d], weight [vocab, d] contiguous, one dtype, d a multiple of 8), which are never
+    stored; rows with the target ZO_IGNORE_TOKEN are not computed and give 0, 0."""
+    hp, rows, d, stride = _matrix(hidden, "hidden")
+    code = _dtype_code(hidden)
+    wp = _dev(weight, "weight", hidden.dtype)
+    if weight.dim() != 2 or weight.shape[1] != d:
+        raise ValueError(f"weight must have shape (vocab, {d}), got {tuple(weight.shape)}")
+    vocab = weight.shape[0]
+    tp = _vector(targets, "targets", rows, torch.int64)
+    if out is None:
+        out = HeadLogprobs(None if tp is None else _new(rows, torch.float32, stream),
+                           _new(rows, torch.float32, stream) if entropy else None)
+    if (out.logp is None) != (targets is None):
+        raise ValueError("logp goes with targets")
+    op, ep = _vector(out.logp, "logp", rows, torch.float32), _vector(out.entropy, "entropy", rows,
+                                                                     torch.float32)
+    if workspace is None:
+        workspace = _new(zo_head_workspace_bytes(rows, vocab), torch.uint8, stream)
+    _lib.check(_lib.lib().zo_head_logprobs(
+        ctx.handle, hp, stride, wp, code, rows, d, vocab, tp, op, ep, _dev(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream(stream)), "zo_head_logprobs")
+    return out
+
+
+def zo_group_loss(ctx: Context, logp: torch.Tensor, targets: torch.Tensor | None,
+                  starts: torch.Tensor, out: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+    """Mean negative log probability, float64, of the counted rows (target not
+    ZO_IGNORE_TOKEN) of each group [starts[g], starts[g + 1]); NaN for a group without any."""
+    rows = logp.numel()
+    lp, sp = _vector(logp, "logp", rows, torch.float32), _dev(starts, "starts", torch.int64)
+    tp = _vector(targets, "targets", rows, torch.int64)
+    n = starts.numel() - 1
+    if starts.dim() != 1 or n < 0:
+        raise ValueError("starts must hold the groups' first rows and the end of the last one")
+    if out is None:
+        out = _new(n, torch.float64, stream)
+    if out.numel() < n:
+        raise ValueError("out is too small")
+    _lib.check(_lib.lib().zo_group_loss(ctx.handle, lp, tp, sp, n, rows,
+                                        _dev(out, "out", torch.float64), _stream(stream)),
+               "zo_group_loss")
+    return out
+
+
+def zo_adapter_workspace_bytes(rows: int, d_in: int, d_out: int, n_adapters: int, rank: int,
+                               n_groups: int, regenerated: int = 0) -> int:
+    return int(_lib.lib().zo_adapter_workspace_bytes(rows, d_in, d_out, n_adapters, rank, n_groups,
+                                                     regenerated))
+
+
+def zo_adapter_project(ctx: Context, x: torch.Tensor, weight: torch.Tensor,
+                       adapters: torch.Tensor, rank: int, starts: torch.Tensor,
+                       ids: torch.Tensor, scale: float = 1.0, bias: torch.Tensor | None = None,
+                       probes: torch.Tensor | None = None, alphas: torch.Tensor | None = None,
+                       offset: int = 0, step: int = 0, probe0: int = 0,
+                       n_probes: int | None = None, bits: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                       stream=None) -> torch.Tensor:
+    """y = x W^T + bias + scale (x A_g^T) B_g^T for the rows of each group [starts[g],
+    starts[g + 1]), with the group's adapter ids[g] (-1: none) out of the flat buffer
+    `adapters` (each A [rank, d_in], then B [d_out, rank]), read as zo_perturb(alphas[g])
+    along probe probe0 + probes[g] of `step` would leave it (probes[g] -1: as it is).
+
+    x [rows, d_in], weight [d_out, d_in], bias [d_out] and adapters share a dtype; starts
+    int64 [groups + 1], ids and probes int32, alphas float32.  bits: (n_probes,
+    zo_bits_stride(adapters)) packed rows; without them the signs are regenerated and
+    n_probes has to be given.  Rows of no group are left as they were (undefined in a new
+    y)."""
+    xp, rows, d_in, xs = _matrix(x, "x")
+    code = _dtype_code(x)
+    wp = _dev(weight, "weight", x.dtype)
+    if weight.dim() != 2 or weight.shape[1] != d_in:
+        raise ValueError(f"weight must have shape (d_out, {d_in}), got {tuple(weight.shape)}")
+    d_out, rank = weight.shape[0], int(rank)
+    ap = _dev(adapters, "adapters", x.dtype)
+    per = rank * (d_in + d_out)
+    if rank < 0 or (adapters.numel() % per if per else adapters.numel()):
+        raise ValueError(f"adapters must hold a whole number of adapters of {per} values")
+    n_adapters = adapters.numel() // per if per else 0
+    sp = _dev(starts, "starts", torch.int64)
+    n = starts.numel() - 1
+    if starts.dim() != 1 or n < 0:
+        raise ValueError("starts must hold the groups' first rows and the end of the last one")
+    ip, bp = _vector(ids, "ids", n, torch.int32), _vector(bias, "bias", d_out, x.dtype)
+    if (probes is None) != (alphas is None):
+        raise ValueError("give both probes and alphas or neither")
+    pp, fp = _vector(probes, "probes", n, torch.int32), _vector(alphas, "alphas", n, torch.float32)
+    if probes is None:
+        n_probes, bits = 0, None
+    elif n_probes is None:
+        if bits is None:
+            raise ValueError("n_probes is needed to regenerate the signs")
+        n_probes = bits.shape[0]
+    kp = _rows(bits, n_probes, adapters.numel())
+    if out is None:
+        out = _new((rows, d_out), x.dtype, stream)
+    yp, yr, yc, ys = _matrix(out, "out", x.dtype)
+    if (yr, yc) != (rows, d_out):
+        raise ValueError(f"out must have shape ({rows}, {d_out}), got {tuple(out.shape)}")
+    if workspace is None:
+        workspace = _new(zo_adapter_workspace_bytes(rows, d_in, d_out, n_adapters, rank, n,
+                                                    n_probes if bits is None else 0),
+                         torch.uint8, stream)
+    _lib.check(_lib.lib().zo_adapter_project(
+        ctx.handle, xp, xs, wp, bp, code, rows, d_in, d_out, ap, n_adapters, rank, float(scale),
+        sp, ip, n, pp, fp, offset, step, probe0, n_probes, kp, _dev(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), yp, ys, _stream(stream)),
+        "zo_adapter_project")
+    return out

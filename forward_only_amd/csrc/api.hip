@@ -8,6 +8,8 @@
 #include "zo_launch.hpp"
 
 static_assert(ZO_MAX_NPERT == zo::kMaxNpert, "one probe-count limit");
+static_assert(ZO_MAX_TOP_K == zo::kMaxTopK && ZO_MAX_RANK == zo::kMaxRank &&
+                  ZO_IGNORE_TOKEN == zo::kIgnoreToken, "one set of limits");
 static_assert(2 * zo::kQuadProbes + 1 <= zo::kLowRankMax + 1,
               "the loss partials hold both signs of every probe of a fused pass and the clean loss");
 
@@ -50,6 +52,14 @@ void *scratch_on(int dev)
 }
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+template <unsigned kBytes>
+inline bool aligned(const void *p)
+{
+    return (reinterpret_cast<uintptr_t>(p) & (kBytes - 1)) == 0;
+}
+
+constexpr uint64_t kMaxRows = 0x7FFFFFFFu;   // of the language-model operators
 
 inline zo::Key key_of(const zo_ctx *c) { return {(uint32_t)c->seed, (uint32_t)(c->seed >> 32)}; }
 
@@ -524,6 +534,133 @@ zo_status zo_tune_placement(zo_ctx *c, void *d_buf, uint64_t bytes, void *stream
     if (out_gbps_whole) *out_gbps_whole = gbps[0];
     if (out_gbps_sliced) *out_gbps_sliced = gbps[1];
     return ZO_OK;
+}
+
+zo_status zo_token_logprobs(zo_ctx *c, const void *d_logits, zo_dtype dtype, uint64_t rows,
+                            uint32_t vocab, uint64_t row_stride, const int64_t *d_targets,
+                            float *d_logp, float *d_entropy, uint32_t top_k, int64_t *d_top_ids,
+                            float *d_top_logp, void *stream)
+{
+    if (!ctx_ok(c)) return ZO_EINVAL;
+    if (dtype != ZO_FP32 && dtype != ZO_BF16) return ZO_EINVAL;
+    if (rows > kMaxRows || vocab > kMaxRows) return ZO_EUNSUPPORTED;
+    if (rows == 0) return ZO_OK;
+    if (vocab == 0 || !d_logits) return ZO_EINVAL;
+    if ((d_targets == nullptr) != (d_logp == nullptr)) return ZO_EINVAL;
+    if (top_k > 0 && (!d_top_ids || !d_top_logp)) return ZO_EINVAL;
+    if (top_k > ZO_MAX_TOP_K) return ZO_EUNSUPPORTED;
+    if (top_k > vocab) return ZO_EINVAL;
+    if (!(dtype == ZO_BF16 ? aligned<2>(d_logits) : aligned<4>(d_logits))) return ZO_EINVAL;
+    if (!aligned<8>(d_targets) || !aligned<4>(d_logp) || !aligned<4>(d_entropy) ||
+        !aligned<8>(d_top_ids) || !aligned<4>(d_top_logp))
+        return ZO_EINVAL;
+    if (row_stride > (UINT64_MAX >> 4) / rows) return ZO_EINVAL;
+    if (!d_logp && !d_entropy && top_k == 0) return ZO_OK;
+    return from_hip(zo::launch_token_logprobs(d_logits, dtype == ZO_BF16, rows, vocab, row_stride,
+                                              d_targets, d_logp, d_entropy, top_k, d_top_ids,
+                                              d_top_logp, as_stream(stream)));
+}
+
+uint64_t zo_head_workspace_bytes(uint64_t rows, uint32_t vocab)
+{
+    return zo::head_space(rows, vocab, nullptr).bytes;
+}
+
+zo_status zo_head_logprobs(zo_ctx *c, const void *d_hidden, uint64_t hidden_stride,
+                           const void *d_weight, zo_dtype dtype, uint64_t rows, uint32_t d,
+                           uint32_t vocab, const int64_t *d_targets, float *d_logp,
+                           float *d_entropy, void *d_workspace, uint64_t workspace_bytes,
+                           void *stream)
+{
+    if (!ctx_ok(c)) return ZO_EINVAL;
+    if (dtype != ZO_FP32 && dtype != ZO_BF16) return ZO_EINVAL;
+    if (rows > kMaxRows || vocab > kMaxRows) return ZO_EUNSUPPORTED;
+    if (rows == 0) return ZO_OK;
+    if (vocab == 0 || d == 0 || d % 8u || hidden_stride % 8u) return ZO_EINVAL;
+    if (!d_hidden || !d_weight || !aligned16(d_hidden) || !aligned16(d_weight)) return ZO_EINVAL;
+    if ((d_targets == nullptr) != (d_logp == nullptr)) return ZO_EINVAL;
+    if (!d_logp && !d_entropy) return ZO_EINVAL;
+    if (!aligned<8>(d_targets) || !aligned<4>(d_logp) || !aligned<4>(d_entropy)) return ZO_EINVAL;
+    if (hidden_stride > (UINT64_MAX >> 4) / rows) return ZO_EINVAL;
+    if (!d_workspace || !aligned<256>(d_workspace) ||
+        workspace_bytes < zo_head_workspace_bytes(rows, vocab))
+        return ZO_EINVAL;
+    const zo::HeadArgs h = {rows, hidden_stride, d, vocab, d_targets, d_logp, d_entropy, d_workspace};
+    return from_hip(zo::launch_head_logprobs(h, dtype == ZO_BF16, d_hidden, d_weight,
+                                             as_stream(stream)));
+}
+
+zo_status zo_group_loss(zo_ctx *c, const float *d_logp, const int64_t *d_targets,
+                        const int64_t *d_starts, uint32_t n_groups, uint64_t rows,
+                        double *d_loss, void *stream)
+{
+    if (!ctx_ok(c)) return ZO_EINVAL;
+    if (n_groups > kMaxRows) return ZO_EUNSUPPORTED;
+    if (n_groups == 0) return ZO_OK;
+    if ((rows > 0 && !d_logp) || !d_starts || !d_loss) return ZO_EINVAL;
+    if (!aligned<4>(d_logp) || !aligned<8>(d_targets) || !aligned<8>(d_starts) || !aligned<8>(d_loss))
+        return ZO_EINVAL;
+    return from_hip(zo::launch_group_loss(d_logp, d_targets, d_starts, n_groups, rows, d_loss,
+                                          as_stream(stream)));
+}
+
+uint64_t zo_adapter_workspace_bytes(uint64_t rows, uint32_t d_in, uint32_t d_out,
+                                    uint32_t n_adapters, uint32_t rank, uint32_t n_groups,
+                                    uint32_t regenerated)
+{
+    const uint64_t params = (uint64_t)n_adapters * rank * ((uint64_t)d_in + d_out);
+    return zo::adapter_u_bytes(rows, rank, n_groups) + (uint64_t)regenerated * zo_bits_stride(params);
+}
+
+zo_status zo_adapter_project(zo_ctx *c, const void *d_x, uint64_t x_stride, const void *d_weight,
+                             const void *d_bias, zo_dtype dtype, uint64_t rows, uint32_t d_in,
+                             uint32_t d_out, const void *d_adapters, uint32_t n_adapters,
+                             uint32_t rank, float scale, const int64_t *d_starts,
+                             const int32_t *d_ids, uint32_t n_groups, const int32_t *d_probes,
+                             const float *d_alphas, uint64_t offset, uint32_t step,
+                             uint32_t probe0, uint32_t n_probes, const uint8_t *d_bits,
+                             void *d_workspace, uint64_t workspace_bytes, void *d_y,
+                             uint64_t y_stride, void *stream)
+{
+    if (!ctx_ok(c)) return ZO_EINVAL;
+    if (dtype != ZO_FP32 && dtype != ZO_BF16) return ZO_EINVAL;
+    if (rank > ZO_MAX_RANK || rows > kMaxRows || n_groups > kMaxRows) return ZO_EUNSUPPORTED;
+    if (d_in == 0 || d_in % 8u || d_out % 8u || rank % 8u || x_stride % 8u || y_stride % 8u)
+        return ZO_EINVAL;
+    if ((d_probes == nullptr) != (d_alphas == nullptr)) return ZO_EINVAL;
+    if (n_adapters > UINT64_MAX / 2 / ((uint64_t)ZO_MAX_RANK * ((uint64_t)d_in + d_out)))
+        return ZO_EINVAL;
+    const uint64_t params = (uint64_t)n_adapters * rank * ((uint64_t)d_in + d_out);
+    if (!range_ok(offset, params)) return ZO_EINVAL;
+    if (d_probes && n_probes > 0 && n_probes - 1 > UINT32_MAX - probe0) return ZO_EINVAL;
+    if (rows == 0 || d_out == 0 || n_groups == 0) return ZO_OK;
+    if (!d_x || !d_weight || !d_y || !d_starts || !d_ids || (params > 0 && !d_adapters))
+        return ZO_EINVAL;
+    if (!aligned16(d_x) || !aligned16(d_weight) || !aligned16(d_bias) || !aligned16(d_y) ||
+        !aligned16(d_adapters) || !aligned16(d_bits))
+        return ZO_EINVAL;
+    if (!aligned<8>(d_starts) || !aligned<4>(d_ids) || !aligned<4>(d_probes) || !aligned<4>(d_alphas))
+        return ZO_EINVAL;
+    if (x_stride > (UINT64_MAX >> 4) / rows || y_stride > (UINT64_MAX >> 4) / rows ||
+        (rows > 1 && y_stride < d_out))
+        return ZO_EINVAL;
+    const uint32_t regenerated = d_probes && !d_bits && params > 0 ? n_probes : 0;
+    const uint64_t need = zo_adapter_workspace_bytes(rows, d_in, d_out, n_adapters, rank, n_groups,
+                                                     regenerated);
+    if (need > 0 && (!d_workspace || !aligned<256>(d_workspace) || workspace_bytes < need))
+        return ZO_EINVAL;
+    float *u = static_cast<float *>(d_workspace);
+    zo::AdapterArgs a = {rows, d_in, d_out, rank, n_adapters, n_groups, n_probes, scale, d_starts,
+                         d_ids, d_probes, d_alphas, d_bits, zo_bits_stride(params)};
+    if (regenerated > 0) {
+        uint8_t *bits = static_cast<uint8_t *>(d_workspace) + zo::adapter_u_bytes(rows, rank, n_groups);
+        const hipError_t e = zo::launch_gen_probes(key_of(c), step, probe0, n_probes, offset, params,
+                                                   bits, c->num_cus, as_stream(stream));
+        if (e != hipSuccess) return from_hip(e);
+        a.bits = bits;
+    }
+    return from_hip(zo::launch_adapter_project(a, dtype == ZO_BF16, d_x, x_stride, d_weight, d_bias,
+                                               d_adapters, u, d_y, y_stride, as_stream(stream)));
 }
 
 }  // extern "C"

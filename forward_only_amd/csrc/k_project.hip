@@ -1,0 +1,546 @@
+// k_project.hip -- products of rows with a weight matrix on MFMA, x [rows, k] times w
+// [features, k] transposed, with two endings:
+//   zo_adapter_project  y = x w^T + bias + scale (x A_g^T) B_g^T, each group of rows with its
+//                       own low-rank adapter, moved along its own probe while it is read;
+//   zo_head_logprobs    softmax statistics of every row over all features, with the product
+//                       itself kept in registers.
+//
+// Tiles.  A workgroup computes kF features x kR rows.  Features are the MFMA's M dimension and
+// rows its N dimension, so that a lane holds several features of one row: a softmax over
+// features is mostly in-lane and a store of y writes neighbouring features.  Operands are read
+// in 16-byte pieces of one row (8 bf16 or 4 fp32 along k); for fp32 the four values of a piece
+// feed four successive 16x16x4 products, which pairs the same k of both operands.
+#include <math.h>
+
+#include "zo_lm.hpp"
+
+namespace zo {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// 16 zero bytes: what lanes past the end of k read.
+__device__ const u32x4 kZeros = {0, 0, 0, 0};
+
+struct Bf16 {
+    typedef uint16_t elem;
+    static constexpr int kPiece = 8;    // elements per 16-byte piece
+    static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ float widen(uint16_t v) { return bf16lo_to_f32(v); }
+    // The piece moved by +/-alpha, sign by bit (set: +), rounded as zo_perturb rounds it.
+    static __device__ __forceinline__ u32x4 move(u32x4 v, uint32_t signs, float alpha)
+    {
+        u32x4 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = (signs >> (2 * i)) & 1u ? alpha : -alpha;
+            const float b = (signs >> (2 * i + 1)) & 1u ? alpha : -alpha;
+            o[i] = pack_bf16x2(bf16lo_to_f32(v[i]) + a, bf16hi_to_f32(v[i]) + b);
+        }
+        return o;
+    }
+    // c + a * (8 fp32 values): the values enter as a bf16 and the bf16 of what it leaves, so
+    // that 16 bits of each value take part.
+    static __device__ __forceinline__ f32x4 mma_f32(u32x4 a, const float *v, f32x4 c)
+    {
+        u32x4 hi, lo;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            hi[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+            lo[i] = pack_bf16x2(v[2 * i] - bf16lo_to_f32(hi[i]), v[2 * i + 1] - bf16hi_to_f32(hi[i]));
+        }
+        return mma(a, hi, mma(a, lo, c));
+    }
+};
+
+struct Fp32 {
+    typedef float elem;
+    static constexpr int kPiece = 4;
+    static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[i]), __uint_as_float(b[i]),
+                                                     c, 0, 0, 0);
+        return c;
+    }
+    static __device__ __forceinline__ float widen(float v) { return v; }
+    static __device__ __forceinline__ u32x4 move(u32x4 v, uint32_t signs, float alpha)
+    {
+        u32x4 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            o[i] = __float_as_uint(__uint_as_float(v[i]) + ((signs >> i) & 1u ? alpha : -alpha));
+        return o;
+    }
+    static __device__ __forceinline__ f32x4 mma_f32(u32x4 a, const float *v, f32x4 c)
+    {
+        u32x4 b;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(v[i]);
+        return mma(a, b, c);
+    }
+};
+
+template <class T>
+__device__ __forceinline__ u32x4 piece_at(const typename T::elem *p)
+{
+    return *reinterpret_cast<const u32x4 *>(p);
+}
+
+// Sign bits of the piece that starts at local parameter e of packed row `bits`.
+template <class T>
+__device__ __forceinline__ uint32_t piece_signs(const uint8_t *bits, uint64_t e)
+{
+    return (uint32_t)bits[e >> 3] >> (e & 7u);
+}
+
+// ---- the adapters ---------------------------------------------------------------------
+
+// What a group of rows adds to the projection.
+struct Group {
+    bool none;             // nothing: no adapter
+    bool bad;              // an index outside its table: the group's rows become NaN
+    uint64_t base;         // first parameter of its adapter
+    const uint8_t *bits;   // its probe's packed row, or nullptr
+    float alpha;
+};
+
+__device__ __forceinline__ Group group_of(const AdapterArgs &a, uint32_t g)
+{
+    Group r = {true, false, 0, nullptr, 0.0f};
+    const int32_t id = a.ids[g];
+    const int32_t probe = a.probes ? a.probes[g] : -1;
+    if (id == -1) return r;
+    r.bad = id < -1 || (uint32_t)id >= a.n_adapters ||
+            (a.probes && (probe < -1 || (probe >= 0 && (uint32_t)probe >= a.n_probes)));
+    if (r.bad) return r;
+    r.none = false;
+    r.base = (uint64_t)(uint32_t)id * a.rank * ((uint64_t)a.d_in + a.d_out);
+    if (probe >= 0) {
+        r.bits = a.bits + (uint64_t)probe * a.bits_stride;
+        r.alpha = a.alphas[probe >= 0 ? g : 0];
+    }
+    return r;
+}
+
+// The last group of [0, n_groups) whose slot of 16-row tiles starts at or before `slot`.
+// Group g owns the slots from start_g / 16 + g on: at least as many as its rows fill.
+__device__ __forceinline__ uint32_t group_of_slot(const AdapterArgs &a, uint64_t slot)
+{
+    uint32_t lo = 0, hi = a.n_groups;
+    while (hi - lo > 1) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        if (clamp_row(a.starts[mid], a.rows) / 16 + mid <= slot)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// u[row][j] = x[row] . A_g[j], fp32: one workgroup per 16 rows of a group; its four waves
+// take every fourth 16-byte-piece group along k and add up in LDS.
+template <class T>
+__global__ __launch_bounds__(256) void k_shrink(AdapterArgs a, const typename T::elem *x,
+                                                uint64_t x_stride,
+                                                const typename T::elem *adapters, float *u)
+{
+    const uint64_t slot = blockIdx.x;
+    const uint32_t g = group_of_slot(a, slot);
+    const uint64_t start = clamp_row(a.starts[g], a.rows), end = clamp_row(a.starts[g + 1], a.rows);
+    if (slot < start / 16 + g) return;
+    const uint64_t row0 = start + (slot - (start / 16 + g)) * 16;
+    if (row0 >= end) return;
+    const Group gr = group_of(a, g);
+    if (gr.none) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int l16 = lane & 15, q = lane >> 4;
+    const uint64_t row = row0 + l16 < end ? row0 + l16 : end - 1;
+    const typename T::elem *xr = x + row * x_stride;
+    constexpr uint32_t kStep = 4 * T::kPiece;   // k covered by one fragment of 16 x 16
+    __shared__ float red[4][16][17];
+    for (uint32_t j0 = 0; j0 < a.rank; j0 += 16) {
+        const uint32_t j = j0 + l16 < a.rank ? j0 + l16 : a.rank - 1;
+        const uint64_t e0 = gr.base + (uint64_t)j * a.d_in;
+        f32x4 acc = {0, 0, 0, 0};
+        for (uint32_t k0 = wave * kStep; k0 < a.d_in; k0 += 4 * kStep) {
+            const uint32_t k = k0 + q * T::kPiece;
+            u32x4 fa = kZeros, fx = kZeros;
+            if (k < a.d_in) {
+                fx = piece_at<T>(xr + k);
+                fa = piece_at<T>(adapters + e0 + k);
+                if (gr.bits) fa = T::move(fa, piece_signs<T>(gr.bits, e0 + k), gr.alpha);
+            }
+            acc = T::mma(fa, fx, acc);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) red[wave][l16][4 * q + i] = acc[i];   // [row][adapter row]
+        __syncthreads();
+        const int r = threadIdx.x >> 4, c = threadIdx.x & 15;
+        if (row0 + r < end && j0 + c < a.rank)
+            u[(row0 + r) * a.rank + j0 + c] =
+                (red[0][r][c] + red[1][r][c]) + (red[2][r][c] + red[3][r][c]);
+    }
+}
+
+// ---- the product ----------------------------------------------------------------------
+
+struct ProductArgs {
+    uint64_t base, rows;   // places [base, base + rows) of the rows, or of the list's rows
+    uint64_t x_stride;
+    uint32_t k, features;
+};
+
+// How many of `rows` places from `base` on there are when only *count places hold a row.
+__device__ __forceinline__ uint64_t places(uint64_t base, uint64_t rows, const uint32_t *count)
+{
+    if (!count) return rows;
+    const uint64_t n = *count;
+    return n <= base ? 0 : (n - base < rows ? n - base : rows);
+}
+
+// Accumulators of one wave: kMF x kMR fragments of 16 features x 16 rows.
+template <class T, int kMF, int kMR>
+struct Tile {
+    f32x4 acc[kMF][kMR];
+};
+
+// Ending of zo_adapter_project.
+template <class T>
+struct EndProject {
+    AdapterArgs a;
+    const float *u;
+    const typename T::elem *adapters, *bias;
+    typename T::elem *y;
+    uint64_t y_stride;
+
+    template <int kMF, int kMR>
+    __device__ __forceinline__ void operator()(Tile<T, kMF, kMR> &t, uint32_t f0, uint64_t r0) const
+    {
+        const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+        const uint64_t lo = clamp_row(a.starts[0], a.rows);
+        const uint64_t hi = clamp_row(a.starts[a.n_groups], a.rows);
+        const uint64_t r1 = r0 + 16 * kMR < a.rows ? r0 + 16 * kMR : a.rows;
+        // groups that meet rows [r0, r1): from the last one that starts at or before r0
+        uint32_t g = 0, top = a.n_groups;
+        while (top - g > 1) {
+            const uint32_t mid = g + (top - g) / 2;
+            if (clamp_row(a.starts[mid], a.rows) <= r0)
+                g = mid;
+            else
+                top = mid;
+        }
+        for (; g < a.n_groups; ++g) {
+            const uint64_t s = clamp_row(a.starts[g], a.rows), e = clamp_row(a.starts[g + 1], a.rows);
+            if (s >= r1) break;
+            if (e <= r0 || e <= s) continue;
+            const Group gr = group_of(a, g);
+            if (gr.none && !gr.bad) continue;
+#pragma unroll
+            for (int n = 0; n < kMR; ++n) {
+                const uint64_t row = r0 + 16 * n + l16;
+                const bool in = row >= s && row < e;
+                if (gr.bad) {
+                    for (int m = 0; m < kMF; ++m)
+                        for (int i = 0; i < 4; ++i)
+                            t.acc[m][n][i] = in ? __builtin_nanf("") : t.acc[m][n][i];
+                    continue;
+                }
+                if (r0 + 16 * n + 16 <= s || r0 + 16 * n >= e) continue;
+                f32x4 add[kMF];
+                for (int m = 0; m < kMF; ++m) add[m] = f32x4{0, 0, 0, 0};
+                for (uint32_t j0 = 0; j0 < a.rank; j0 += 4 * T::kPiece) {
+                    const uint32_t j = j0 + q * T::kPiece;
+                    float v[T::kPiece];
+#pragma unroll
+                    for (int i = 0; i < T::kPiece; ++i)
+                        v[i] = in && j < a.rank ? a.scale * u[row * a.rank + j + i] : 0.0f;
+#pragma unroll
+                    for (int m = 0; m < kMF; ++m) {
+                        const uint32_t f = f0 + 16 * m + l16;
+                        u32x4 fb = kZeros;
+                        if (j < a.rank && f < a.d_out) {
+                            const uint64_t at = gr.base + (uint64_t)a.rank * a.d_in +
+                                                (uint64_t)f * a.rank + j;
+                            fb = piece_at<T>(adapters + at);
+                            if (gr.bits) fb = T::move(fb, piece_signs<T>(gr.bits, at), gr.alpha);
+                        }
+                        add[m] = T::mma_f32(fb, v, add[m]);
+                    }
+                }
+                for (int m = 0; m < kMF; ++m)
+                    for (int i = 0; i < 4; ++i)
+                        t.acc[m][n][i] = in ? t.acc[m][n][i] + add[m][i] : t.acc[m][n][i];
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < kMR; ++n) {
+            const uint64_t row = r0 + 16 * n + l16;
+            if (row < lo || row >= hi) continue;
+#pragma unroll
+            for (int m = 0; m < kMF; ++m) {
+                const uint32_t f = f0 + 16 * m + 4 * q;
+                if (f >= a.d_out) continue;
+                f32x4 v = t.acc[m][n];
+                if (bias)
+                    for (int i = 0; i < 4; ++i) v[i] += T::widen(bias[f + i]);
+                store4(y + row * y_stride + f, v);
+            }
+        }
+    }
+    static __device__ __forceinline__ void store4(float *p, f32x4 v) { *reinterpret_cast<f32x4 *>(p) = v; }
+    static __device__ __forceinline__ void store4(uint16_t *p, f32x4 v)
+    {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    }
+};
+
+// Ending of zo_head_logprobs: per wave tile and row (m, s, t) over the tile's features.
+struct EndHead {
+    uint32_t features;
+    uint64_t base, rows;        // places of this launch
+    const int64_t *targets;     // of all rows, or nullptr
+    const uint32_t *list;       // row of each place, or nullptr: place = row
+    const uint32_t *count;
+    float *m, *s, *t;           // [wave tile][place]
+    float *tl;                  // logit of each place's target
+
+    template <class T, int kMF, int kMR>
+    __device__ __forceinline__ void operator()(Tile<T, kMF, kMR> &t4, uint32_t f0, uint64_t r0) const
+    {
+        const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+        const uint32_t part = f0 / (16 * kMF);
+        if (f0 >= features) return;
+        const uint64_t have = places(base, rows, count);
+#pragma unroll
+        for (int n = 0; n < kMR; ++n) {
+            const uint64_t at = r0 + 16 * n + l16;
+            SoftStats st = SoftStats::empty();
+            int64_t tgt = -1;
+            if (targets && at < have) tgt = targets[list ? list[base + at] : base + at];
+            float top = -INFINITY;
+#pragma unroll
+            for (int m4 = 0; m4 < kMF; ++m4)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t f = f0 + 16 * m4 + 4 * q + i;
+                    if (f < features) top = fmaxf(top, t4.acc[m4][n][i]);
+                }
+            st.raise(top);
+#pragma unroll
+            for (int m4 = 0; m4 < kMF; ++m4)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t f = f0 + 16 * m4 + 4 * q + i;
+                    if (f < features) {
+                        st.add(t4.acc[m4][n][i]);
+                        if ((int64_t)f == tgt && at < have) tl[at] = t4.acc[m4][n][i];
+                    }
+                }
+            st.wave_merge(32, 16);
+            if (q == 0 && at < have) {
+                m[(uint64_t)part * rows + at] = st.m;
+                s[(uint64_t)part * rows + at] = st.s;
+                t[(uint64_t)part * rows + at] = st.t;
+            }
+        }
+    }
+};
+
+template <class T, int kWF, int kWR, int kMF, int kMR, class End>
+__global__ __launch_bounds__(kWF * kWR * 64) void k_product(
+    ProductArgs p, const typename T::elem *x, const typename T::elem *w, const uint32_t *list,
+    const uint32_t *count, End end)
+{
+    constexpr int kThreads = kWF * kWR * 64;
+    constexpr int kF = kWF * kMF * 16, kR = kWR * kMR * 16;
+    constexpr int kPieces = 8;                              // 16-byte pieces of a staged row
+    constexpr uint32_t kStep = kPieces * T::kPiece;
+    __shared__ u32x4 sw[kF * kPieces], sx[kR * kPieces];
+    const uint64_t rows = places(p.base, p.rows, count);
+    const uint32_t nf = (p.features + kF - 1) / kF;
+    const uint32_t f0 = blockIdx.x % nf * kF;
+    const uint64_t r0 = (uint64_t)(blockIdx.x / nf) * kR;
+    if (r0 >= rows) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int l16 = lane & 15, q = lane >> 4;
+    const int wf = wave % kWF, wr = wave / kWF;
+    Tile<T, kMF, kMR> t;
+    for (int m = 0; m < kMF; ++m)
+        for (int n = 0; n < kMR; ++n) t.acc[m][n] = f32x4{0, 0, 0, 0};
+    for (uint32_t k0 = 0; k0 < p.k; k0 += kStep) {
+        for (int i = tid; i < kF * kPieces; i += kThreads) {
+            const uint32_t f = f0 + i / kPieces, k = k0 + (i % kPieces) * T::kPiece;
+            sw[i] = f < p.features && k < p.k ? piece_at<T>(w + (uint64_t)f * p.k + k) : kZeros;
+        }
+        for (int i = tid; i < kR * kPieces; i += kThreads) {
+            const uint64_t r = r0 + i / kPieces;
+            const uint32_t k = k0 + (i % kPieces) * T::kPiece;
+            u32x4 v = kZeros;
+            if (r < rows && k < p.k)
+                v = piece_at<T>(x + (list ? list[p.base + r] : p.base + r) * p.x_stride + k);
+            sx[i] = v;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < kPieces / 4; ++c) {
+            u32x4 fa[kMF], fb[kMR];
+            for (int m = 0; m < kMF; ++m) fa[m] = sw[((wf * kMF + m) * 16 + l16) * kPieces + 4 * c + q];
+            for (int n = 0; n < kMR; ++n) fb[n] = sx[((wr * kMR + n) * 16 + l16) * kPieces + 4 * c + q];
+            for (int m = 0; m < kMF; ++m)
+                for (int n = 0; n < kMR; ++n) t.acc[m][n] = T::mma(fa[m], fb[n], t.acc[m][n]);
+        }
+        __syncthreads();
+    }
+    end(t, f0 + wf * kMF * 16, r0 + wr * kMR * 16);
+}
+
+// ---- joining the head's partial statistics ----------------------------------------------
+
+// The places of the rows that count, in order, and zeros for the others' outputs; one
+// workgroup.
+__global__ __launch_bounds__(1024) void k_counted(const int64_t *targets, uint64_t rows,
+                                                  uint32_t *list, uint32_t *count, float *logp,
+                                                  float *entropy)
+{
+    __shared__ uint32_t waves[16];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    uint32_t at = 0;
+    for (uint64_t r0 = 0; r0 < rows; r0 += 1024) {
+        const uint64_t r = r0 + tid;
+        const bool in = r < rows && targets[r] != kIgnoreToken;
+        const uint64_t votes = __ballot(in);
+        if (lane == 0) waves[wave] = __popcll(votes);
+        __syncthreads();
+        uint32_t before = at;
+        for (int w = 0; w < 16; ++w) {
+            if (w < wave) before += waves[w];
+            at += waves[w];
+        }
+        if (in) {
+            list[before + __popcll(votes & (((uint64_t)1 << lane) - 1))] = (uint32_t)r;
+        } else if (r < rows) {
+            if (logp) logp[r] = 0.0f;
+            if (entropy) entropy[r] = 0.0f;
+        }
+        __syncthreads();
+    }
+    if (tid == 0) *count = at;
+}
+
+__global__ __launch_bounds__(256) void k_head_join(const float *m, const float *s, const float *t,
+                                                   const float *tl, uint32_t parts,
+                                                   uint64_t base, uint64_t rows,
+                                                   const uint32_t *list, const uint32_t *count,
+                                                   const int64_t *targets, uint32_t features,
+                                                   float *logp, float *entropy)
+{
+    const uint64_t n = places(base, rows, count);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint64_t at = (uint64_t)blockIdx.x * 64 + lane;
+    SoftStats st = SoftStats::empty();
+    if (at < n)
+        for (uint32_t p = wave; p < parts; p += 4) {
+            SoftStats o;
+            o.m = m[(uint64_t)p * rows + at];
+            o.s = s[(uint64_t)p * rows + at];
+            o.t = t[(uint64_t)p * rows + at];
+            st.merge(o);
+        }
+    __shared__ SoftStats all[4][64];
+    all[wave][lane] = st;
+    __syncthreads();
+    if (wave || at >= n) return;
+    for (int w = 1; w < 4; ++w) st.merge(all[w][lane]);
+    const uint64_t row = list ? list[base + at] : base + at;
+    const float logs = logf(st.s);
+    if (logp) {
+        const int64_t tgt = targets[row];
+        logp[row] = tgt >= 0 && tgt < (int64_t)features ? (tl[at] - st.m) - logs : __builtin_nanf("");
+    }
+    if (entropy) entropy[row] = logs - st.t / st.s;
+}
+
+template <class T, int kWF, int kWR, int kMF, int kMR, class End>
+hipError_t product(const ProductArgs &p, const typename T::elem *x, const typename T::elem *w,
+                   const uint32_t *list, const uint32_t *count, const End &end, hipStream_t stream)
+{
+    const uint64_t nf = (p.features + kWF * kMF * 16 - 1) / (kWF * kMF * 16);
+    const uint64_t nr = (p.rows + kWR * kMR * 16 - 1) / (kWR * kMR * 16);
+    if (nf * nr > 0x7FFFFFFFull) return hipErrorInvalidValue;
+    k_product<T, kWF, kWR, kMF, kMR, End>
+        <<<(uint32_t)(nf * nr), kWF * kWR * 64, 0, stream>>>(p, x, w, list, count, end);
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t project(const AdapterArgs &a, const void *x, uint64_t x_stride, const void *w,
+                   const void *bias, const void *adapters, float *u, void *y, uint64_t y_stride,
+                   hipStream_t stream)
+{
+    typedef typename T::elem E;
+    const E *px = static_cast<const E *>(x), *pa = static_cast<const E *>(adapters);
+    if (a.rank && a.n_adapters) {
+        k_shrink<T><<<(uint32_t)(a.rows / 16 + a.n_groups), 256, 0, stream>>>(a, px, x_stride, pa, u);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    const ProductArgs p = {0, a.rows, x_stride, a.d_in, a.d_out};
+    const EndProject<T> end = {a, u, pa, static_cast<const E *>(bias), static_cast<E *>(y), y_stride};
+    return product<T, 2, 2, 2, 2>(p, px, static_cast<const E *>(w), nullptr, nullptr, end, stream);
+}
+
+template <class T>
+hipError_t head(const HeadArgs &h, const void *x, const void *w, hipStream_t stream)
+{
+    typedef typename T::elem E;
+    const HeadSpace sp = head_space(h.rows, h.features, h.workspace);
+    uint32_t *list = nullptr, *count = nullptr;
+    if (h.targets) {
+        list = sp.list;
+        count = sp.count;
+        k_counted<<<1, 1024, 0, stream>>>(h.targets, h.rows, list, count, h.logp, h.entropy);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    for (uint64_t base = 0; base < h.rows; base += kHeadPlaces) {
+        const uint64_t rows = h.rows - base < kHeadPlaces ? h.rows - base : kHeadPlaces;
+        const ProductArgs p = {base, rows, h.x_stride, h.k, h.features};
+        const EndHead end = {h.features, base, rows, h.targets, list, count, sp.m, sp.s, sp.t, sp.tl};
+        hipError_t e = product<T, 2, 2, 2, 2>(p, static_cast<const E *>(x), static_cast<const E *>(w),
+                                              list, count, end, stream);
+        if (e != hipSuccess) return e;
+        k_head_join<<<(uint32_t)((rows + 63) / 64), 256, 0, stream>>>(
+            sp.m, sp.s, sp.t, sp.tl, (h.features + kHeadPart - 1) / kHeadPart, base, rows, list, count,
+            h.targets, h.features, h.logp, h.entropy);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_adapter_project(const AdapterArgs &a, bool bf16, const void *x, uint64_t x_stride,
+                                  const void *w, const void *bias, const void *adapters, float *u,
+                                  void *y, uint64_t y_stride, hipStream_t stream)
+{
+    return bf16 ? project<Bf16>(a, x, x_stride, w, bias, adapters, u, y, y_stride, stream)
+                : project<Fp32>(a, x, x_stride, w, bias, adapters, u, y, y_stride, stream);
+}
+
+hipError_t launch_head_logprobs(const HeadArgs &h, bool bf16, const void *x, const void *w,
+                                hipStream_t stream)
+{
+    return bf16 ? head<Bf16>(h, x, w, stream) : head<Fp32>(h, x, w, stream);
+}
+
+}  // namespace zo

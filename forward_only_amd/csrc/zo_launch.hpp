@@ -125,6 +125,84 @@ hipError_t launch_mlp_loss_probes(const float *params, const float *X, const int
                                   Key key, double *out_plus, double *out_minus,
                                   double *out_clean, hipStream_t stream);
 
+// Target of a row that counts for nothing (ZO_IGNORE_TOKEN).
+constexpr int64_t kIgnoreToken = -100;
+// Most alternatives one zo_token_logprobs call gives.
+constexpr uint32_t kMaxTopK = 32;
+// Largest rank of an adapter.
+constexpr uint32_t kMaxRank = 128;
+
+// Per row of logits [rows][stride]: log probability of its target, entropy, top_k
+// alternatives (value descending, index ascending).  targets, entropy may be nullptr.
+hipError_t launch_token_logprobs(const void *logits, bool bf16, uint64_t rows, uint32_t vocab,
+                                 uint64_t stride, const int64_t *targets, float *logp,
+                                 float *entropy, uint32_t top_k, int64_t *top_ids,
+                                 float *top_logp, hipStream_t stream);
+
+// loss[g] = -mean of logp over the counted rows of [starts[g], starts[g + 1]).
+hipError_t launch_group_loss(const float *logp, const int64_t *targets, const int64_t *starts,
+                             uint32_t n_groups, uint64_t rows, double *loss, hipStream_t stream);
+
+// The groups of rows of one zo_adapter_project call (device pointers).
+struct AdapterArgs {
+    uint64_t rows;
+    uint32_t d_in, d_out, rank, n_adapters, n_groups, n_probes;
+    float scale;
+    const int64_t *starts;
+    const int32_t *ids, *probes;   // probes nullptr: no group is moved
+    const float *alphas;
+    const uint8_t *bits;           // n_probes packed rows over all adapters' parameters
+    uint64_t bits_stride;
+};
+// Bytes of x A^T, [rows][rank] floats.
+inline uint64_t adapter_u_bytes(uint64_t rows, uint32_t rank, uint32_t n_groups)
+{
+    (void)n_groups;
+    return (rows * rank * 4 + 255) / 256 * 256;
+}
+// u: adapter_u_bytes of workspace.
+hipError_t launch_adapter_project(const AdapterArgs &a, bool bf16, const void *x, uint64_t x_stride,
+                                  const void *w, const void *bias, const void *adapters, float *u,
+                                  void *y, uint64_t y_stride, hipStream_t stream);
+
+struct HeadArgs {
+    uint64_t rows, x_stride;
+    uint32_t k, features;
+    const int64_t *targets;        // nullptr: entropies of all rows
+    float *logp, *entropy;
+    void *workspace;
+};
+// Rows whose partial statistics are held at once, and the features of one partial.
+constexpr uint64_t kHeadPlaces = 16384;
+constexpr uint32_t kHeadPart = 32;
+struct HeadSpace {
+    uint32_t *count, *list;
+    float *m, *s, *t, *tl;
+    uint64_t bytes;
+};
+inline HeadSpace head_space(uint64_t rows, uint32_t features, void *base)
+{
+    const uint64_t places = rows < kHeadPlaces ? rows : kHeadPlaces;
+    const uint64_t parts = ((uint64_t)features + kHeadPart - 1) / kHeadPart;
+    uint64_t at = 0;
+    auto take = [&](uint64_t bytes) {
+        void *p = base ? static_cast<char *>(base) + at : nullptr;
+        at += (bytes + 255) / 256 * 256;
+        return p;
+    };
+    HeadSpace s;
+    s.count = static_cast<uint32_t *>(take(4));
+    s.list = static_cast<uint32_t *>(take(rows * 4));
+    s.m = static_cast<float *>(take(parts * places * 4));
+    s.s = static_cast<float *>(take(parts * places * 4));
+    s.t = static_cast<float *>(take(parts * places * 4));
+    s.tl = static_cast<float *>(take(places * 4));
+    s.bytes = at;
+    return s;
+}
+hipError_t launch_head_logprobs(const HeadArgs &h, bool bf16, const void *x, const void *w,
+                                hipStream_t stream);
+
 // Diagnostic: every 16-byte word of buf (bytes % 16 == 0) <- word ^ mask, in place;
 // slice_bytes > 0 (a multiple of 8 KiB) issues it as one launch per slice of that size.
 hipError_t launch_stream_rmw(void *buf, uint64_t bytes, uint32_t mask, int num_cus,

@@ -49,6 +49,10 @@
  *    results do not depend on them.  The passes over the parameters (zo_perturb,
  *    zo_perturb2, zo_stream_rmw) and the plane generator run one chunk per wave in a
  *    non-persistent grid.
+ *  - Language-model operators (zo_token_logprobs, zo_head_logprobs, zo_adapter_project,
+ *    zo_group_loss): launches only, like the step's calls, and no state in the context; their
+ *    workspaces belong to the caller, and two calls that may overlap (on two streams, or in
+ *    two captured graphs) need one each.
  */
 #ifndef ZO_H
 #define ZO_H
@@ -354,6 +358,122 @@ zo_status zo_mlp_loss_pair_noalloc(zo_ctx *ctx, const float *d_params, uint64_t 
                                    const int64_t *d_labels, uint32_t batch, uint32_t d_in,
                                    uint32_t d_hid, uint32_t d_out, double *d_loss_plus,
                                    double *d_loss_minus, void *stream);
+
+/* ---- Language-model operators ----------------------------------------------------------
+ * The ends of a language model's forward pass ("N forward passes, loss only" box of the
+ * flowchart in "Pretraining Transformers Without Backprop: What Two Zero-Order Papers
+ * Actually Measure") for steps whose parameters are low-rank adapters: many probes' rows in
+ * one batch share each load of the weights (zo_adapter_project), the last hidden states
+ * become log probabilities (zo_head_logprobs, or zo_token_logprobs where logits are at
+ * hand), and these one loss per probe and sign (zo_group_loss) for zo_probe_weights.
+ *
+ * Row indices on the device (targets, starts, ids, probes) are not seen by the host.  Values
+ * outside their range never lead to an access outside a buffer: starts are forced into
+ * [0, rows], and what depends on another bad index becomes NaN, so that zo_probe_weights
+ * drops the probe.  Inputs and outputs must not overlap. */
+
+/* Target of a row that counts for nothing: a prompt's or a padding's.  Such a row is not
+ * read; its log probability and entropy are 0, its alternatives -1 with 0. */
+#define ZO_IGNORE_TOKEN (-100)
+
+/* Most alternatives one zo_token_logprobs call gives. */
+#define ZO_MAX_TOP_K 32u
+
+/* Largest rank of an adapter. */
+#define ZO_MAX_RANK 128u
+
+/* Log probabilities of given tokens, with entropy and the top alternatives, from logits
+ * x [rows x vocab]: with lse = log sum_v e^x_v,
+ *   d_logp[row] = x_target - lse,   d_entropy[row] = lse - sum_v p_v x_v  (nats),
+ * and d_top_ids / d_top_logp [rows x top_k]: the top_k largest logits' indices (value
+ * descending, equal values lowest index first, NaN above all) and log probabilities.  One
+ * pass over the logits, fp32 sums, deterministic.  d_logits: device, rows of vocab elements
+ * of `dtype`, row_stride elements apart, each row contiguous, at any element-aligned address.
+ * d_targets: device int64 [rows], or NULL (no given tokens: d_logp must be NULL too);
+ * ZO_IGNORE_TOKEN as above, any other target outside [0, vocab) gives NaN.  d_entropy may be
+ * NULL; d_top_ids and d_top_logp may be NULL with top_k == 0.
+ * Logits of -inf have probability 0 (a target there gets -inf); a row of only -inf, or one
+ * that holds NaN or +inf, has NaN log probabilities and entropy.
+ * Errors: ZO_EINVAL for NULL pointers (with rows > 0), unknown dtype, vocab == 0 (with
+ * rows > 0), top_k > vocab, misaligned pointers; ZO_EUNSUPPORTED if top_k > ZO_MAX_TOP_K or
+ * rows or vocab exceed 2^31 - 1.  rows == 0 launches nothing. */
+zo_status zo_token_logprobs(zo_ctx *ctx, const void *d_logits, zo_dtype dtype, uint64_t rows,
+                            uint32_t vocab, uint64_t row_stride, const int64_t *d_targets,
+                            float *d_logp, float *d_entropy, uint32_t top_k, int64_t *d_top_ids,
+                            float *d_top_logp, void *stream);
+
+/* The same log probabilities and entropies from hidden states [rows x d] and the
+ * unembedding matrix [vocab x d]: logits h W^T are formed tile by tile in fp32 registers
+ * (products of dtype values, fp32 sums) and never stored.  Rows with the ignored target are
+ * not computed.  d_hidden: device, rows hidden_stride elements apart (a multiple of 8),
+ * 16-byte aligned; d_weight: device, contiguous, 16-byte aligned; both of `dtype`; d a
+ * multiple of 8.  d_targets, d_logp, d_entropy as zo_token_logprobs; at least one of d_logp
+ * and d_entropy.  d_workspace: device, 256-byte aligned, at least
+ * zo_head_workspace_bytes(rows, vocab) bytes.  Deterministic.
+ * Errors: ZO_EINVAL as zo_token_logprobs, shapes outside these limits, a workspace that is
+ * too small or misaligned; ZO_EUNSUPPORTED if rows or vocab exceed 2^31 - 1. */
+uint64_t zo_head_workspace_bytes(uint64_t rows, uint32_t vocab);
+zo_status zo_head_logprobs(zo_ctx *ctx, const void *d_hidden, uint64_t hidden_stride,
+                           const void *d_weight, zo_dtype dtype, uint64_t rows, uint32_t d,
+                           uint32_t vocab, const int64_t *d_targets, float *d_logp,
+                           float *d_entropy, void *d_workspace, uint64_t workspace_bytes,
+                           void *stream);
+
+/* One loss per group of rows: d_loss[g] = -(mean of d_logp over the rows of
+ * [d_starts[g], d_starts[g + 1]) whose target is not ZO_IGNORE_TOKEN), summed in fp64 in a
+ * fixed order.  A group without counted rows has the loss NaN (zo_probe_weights drops it).
+ * d_logp: device, rows floats; d_targets: device int64 [rows], or NULL (all rows count);
+ * d_starts: device int64 [n_groups + 1], non-decreasing; d_loss: device, n_groups doubles.
+ * Errors: ZO_EINVAL for NULL pointers (with n_groups > 0), misalignment; ZO_EUNSUPPORTED if
+ * n_groups exceeds 2^31 - 1. */
+zo_status zo_group_loss(zo_ctx *ctx, const float *d_logp, const int64_t *d_targets,
+                        const int64_t *d_starts, uint32_t n_groups, uint64_t rows,
+                        double *d_loss, void *stream);
+
+/* A shared projection with low-rank adapters of many requests, or of many probes, beside it:
+ *   y = x W^T + bias + scale (x A_g^T) B_g^T
+ * for each row of group g, the rows [d_starts[g], d_starts[g + 1]).  All rows share each load
+ * of W.  x A_g^T is kept in fp32 (with bf16 operands its two leading bf16 parts enter the
+ * second product); y is rounded once.
+ * d_x: device, rows x_stride elements apart (a multiple of 8), 16-byte aligned; d_weight:
+ * device [d_out x d_in] row-major, 16-byte aligned; d_bias: device [d_out] or NULL, 16-byte
+ * aligned; d_y: device, rows y_stride elements apart (a multiple of 8), 16-byte aligned; all,
+ * like the adapters, of `dtype`.  d_in, d_out and rank are multiples of 8.
+ * d_adapters: device, 16-byte aligned, n_adapters adapters one after another, each A
+ * [rank x d_in] then B [d_out x rank], row-major: one flat parameter buffer for zo_perturb
+ * and zo_update whose first element has the global index `offset` (a multiple of 128).
+ * d_starts: device int64 [n_groups + 1], non-decreasing; rows before the first start and from
+ * the last on are left as they were in y.  d_ids: device int32 [n_groups], the group's
+ * adapter, or -1 for none.
+ * d_probes, d_alphas: both NULL, or device int32 / float [n_groups]: the group's adapter is
+ * read as rnd(theta + alpha_g z), z the signs of probe probe0 + d_probes[g] of `step`, each
+ * element the value zo_perturb(alpha_g) would store; theta is not written, and one call
+ * evaluates every probe and sign ("How 1.5-SPSA Works" on "Stanford's 1.5-SPSA Trains
+ * OPT-30B Without Backpropagation").  d_probes[g] == -1 leaves the adapter as it is (the
+ * clean pass); otherwise d_probes[g] < n_probes.  d_bits: NULL (regenerate; the rows of all
+ * n_probes probes are written to the workspace first) or n_probes packed rows over all
+ * adapters' parameters, row i for probe probe0 + i, 16-byte aligned.
+ * An id or probe outside its table makes its group's rows NaN.
+ * d_workspace: device, 256-byte aligned, at least zo_adapter_workspace_bytes(...) bytes, with
+ * regenerated = n_probes if d_probes is given and d_bits is NULL, else 0.
+ * Errors: ZO_EINVAL for NULL pointers (with rows and n_groups > 0; d_adapters may be NULL
+ * with n_adapters == 0 or rank == 0), unknown dtype, shapes and strides outside these limits,
+ * misalignment, offset % 128 != 0 or range overflow, probe indices past 2^32 - 1, a
+ * workspace that is too small; ZO_EUNSUPPORTED if rank > ZO_MAX_RANK, or rows or n_groups
+ * exceed 2^31 - 1.  rows == 0, d_out == 0 or n_groups == 0 launches nothing. */
+uint64_t zo_adapter_workspace_bytes(uint64_t rows, uint32_t d_in, uint32_t d_out,
+                                    uint32_t n_adapters, uint32_t rank, uint32_t n_groups,
+                                    uint32_t regenerated);
+zo_status zo_adapter_project(zo_ctx *ctx, const void *d_x, uint64_t x_stride,
+                             const void *d_weight, const void *d_bias, zo_dtype dtype,
+                             uint64_t rows, uint32_t d_in, uint32_t d_out,
+                             const void *d_adapters, uint32_t n_adapters, uint32_t rank,
+                             float scale, const int64_t *d_starts, const int32_t *d_ids,
+                             uint32_t n_groups, const int32_t *d_probes, const float *d_alphas,
+                             uint64_t offset, uint32_t step, uint32_t probe0,
+                             uint32_t n_probes, const uint8_t *d_bits, void *d_workspace,
+                             uint64_t workspace_bytes, void *d_y, uint64_t y_stride,
+                             void *stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,74 @@
+"""Host-side checks of the language-model operators: refusals that need no GPU, workspace sizes,
+and that the references agree with torch's own float64 functions."""
+import math
+
+import pytest
+import torch
+
+import forward_only_amd as zo
+import lm_ref as ref
+from forward_only_amd import _lib
+
+
+def test_null_context_is_refused():
+    L = _lib.lib()
+    assert L.zo_token_logprobs(None, None, 0, 1, 8, 8, None, None, None, 0, None, None,
+                               None) == _lib.ZO_EINVAL
+    assert L.zo_head_logprobs(None, None, 8, None, 0, 1, 8, 8, None, None, None, None, 0,
+                              None) == _lib.ZO_EINVAL
+    assert L.zo_group_loss(None, None, None, None, 1, 1, None, None) == _lib.ZO_EINVAL
+    assert L.zo_adapter_project(None, None, 8, None, None, 0, 1, 8, 8, None, 0, 8, 1.0, None, None, 1,
+                                None, None, 0, 0, 0, 0, None, None, 0, None, 8, None) == _lib.ZO_EINVAL
+
+
+def test_workspace_sizes_grow_and_stay_bounded():
+    assert zo.zo_head_workspace_bytes(1, 50272) <= zo.zo_head_workspace_bytes(16384, 50272)
+    # beyond one launch's rows only the row list grows
+    a, b = (zo.zo_head_workspace_bytes(r, 50272) for r in (1 << 20, 1 << 21))
+    assert 0 < b - a <= 4 * (1 << 20) + 256
+    base = zo.zo_adapter_workspace_bytes(100, 64, 64, 2, 8, 3)
+    assert zo.zo_adapter_workspace_bytes(100, 64, 64, 2, 8, 3, 5) == base + 5 * zo.zo_bits_stride(2048)
+    assert zo.zo_adapter_workspace_bytes(0, 64, 64, 2, 8, 3) >= 0
+
+
+def test_cpu_tensors_are_refused():
+    x, t = torch.zeros(2, 8), torch.zeros(2, dtype=torch.int64)
+    for call in (lambda: zo.zo_token_logprobs(None, x, t), lambda: zo.zo_head_logprobs(None, x, x, t),
+                 lambda: zo.zo_group_loss(None, x[:, 0].contiguous(), t, t),
+                 lambda: zo.zo_adapter_project(None, x, x, x, 8, t, t.int())):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        zo.zo_token_logprobs(None, [1.0], t)
+
+
+def test_references_agree_with_torch():
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(5, 40, generator=g)
+    t = torch.tensor([3, -100, 39, 40, 0])
+    logp, entropy, ids, top = ref.token(x, t, 4)
+    p = torch.log_softmax(x.double(), dim=1)
+    want = torch.stack([p[0, 3], torch.tensor(0.0).double(), p[2, 39], torch.tensor(math.nan).double(),
+                        p[4, 0]])
+    ref.assert_close(logp, want, 1e-13, "logp")
+    h = -(p.exp() * p).sum(1)
+    h[1] = 0
+    ref.assert_close(entropy, h, 1e-13, "entropy")
+    v, i = p.topk(4, dim=1)
+    assert torch.equal(ids[0], i[0]) and (ids[1] == -1).all()
+    ref.assert_close(top[2], v[2], 1e-13, "top")
+    with pytest.raises(AssertionError):
+        ref.assert_close(logp, want + 1e-6, 1e-7, "a planted mistake")
+
+
+def test_project_reference_agrees_with_a_dense_adapter():
+    g = torch.Generator().manual_seed(2)
+    x, w = torch.randn(6, 16, generator=g), torch.randn(24, 16, generator=g)
+    ad = torch.randn(2 * 8 * 40, generator=g)
+    y, low, bound = ref.project(x, w, None, ad, 8, [0, 2, 2, 5], [1, 0, -1], 0.5)
+    per = 8 * 40
+    a, b = ad[per:per + 128].view(8, 16).double(), ad[per + 128:].view(24, 8).double()
+    dense = x[:2].double() @ (w.double() + 0.5 * b @ a).t()
+    ref.assert_close(y[:2], dense, 1e-12, "adapter 1")
+    ref.assert_close(y[2:5], x[2:5].double() @ w.double().t(), 1e-12, "none")
+    assert torch.isnan(y[5]).all() and (bound > 0).all()

@@ -141,6 +141,7 @@ zo_status zo_init(uint64_t seed, zo_ctx **out)
     }
     c->d_scratch = scratch_on(c->device);
     if (!c->d_scratch || zo::prepare_update() != hipSuccess ||
+        zo::prepare_products() != hipSuccess ||
         zo::launch_zero_u32(c->d_counter, 64, nullptr) != hipSuccess ||
         hipDeviceSynchronize() != hipSuccess) {
         (void)hipFree(c->d_partials);

@@ -45,17 +45,25 @@ struct Bf16 {
         }
         return o;
     }
-    // c + a * (8 fp32 values): the values enter as a bf16 and the bf16 of what it leaves, so
-    // that 16 bits of each value take part.
-    static __device__ __forceinline__ f32x4 mma_f32(u32x4 a, const float *v, f32x4 c)
-    {
+    // Eight fp32 values as an operand: the bf16 of each and the bf16 of what that leaves, so
+    // that 16 bits of each value take part in a product.
+    struct Wide {
         u32x4 hi, lo;
+    };
+    static __device__ __forceinline__ Wide wide(const float *v)
+    {
+        Wide w;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            hi[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-            lo[i] = pack_bf16x2(v[2 * i] - bf16lo_to_f32(hi[i]), v[2 * i + 1] - bf16hi_to_f32(hi[i]));
+            w.hi[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+            w.lo[i] = pack_bf16x2(v[2 * i] - bf16lo_to_f32(w.hi[i]),
+                                  v[2 * i + 1] - bf16hi_to_f32(w.hi[i]));
         }
-        return mma(a, hi, mma(a, lo, c));
+        return w;
+    }
+    static __device__ __forceinline__ f32x4 mma(u32x4 a, const Wide &b, f32x4 c)
+    {
+        return mma(a, b.hi, mma(a, b.lo, c));
     }
 };
 
@@ -79,12 +87,11 @@ struct Fp32 {
             o[i] = __float_as_uint(__uint_as_float(v[i]) + ((signs >> i) & 1u ? alpha : -alpha));
         return o;
     }
-    static __device__ __forceinline__ f32x4 mma_f32(u32x4 a, const float *v, f32x4 c)
+    typedef u32x4 Wide;
+    static __device__ __forceinline__ Wide wide(const float *v)
     {
-        u32x4 b;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(v[i]);
-        return mma(a, b, c);
+        return Wide{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                    __float_as_uint(v[3])};
     }
 };
 
@@ -243,42 +250,56 @@ struct EndProject {
             if (s >= r1) break;
             if (e <= r0 || e <= s) continue;
             const Group gr = group_of(a, g);
-            if (gr.none && !gr.bad) continue;
+            if (gr.bad) {
 #pragma unroll
-            for (int n = 0; n < kMR; ++n) {
-                const uint64_t row = r0 + 16 * n + l16;
-                const bool in = row >= s && row < e;
-                if (gr.bad) {
-                    for (int m = 0; m < kMF; ++m)
-                        for (int i = 0; i < 4; ++i)
-                            t.acc[m][n][i] = in ? __builtin_nanf("") : t.acc[m][n][i];
-                    continue;
+                for (int n = 0; n < kMR; ++n) {
+                    const uint64_t row = r0 + 16 * n + l16;
+                    const float nan = row >= s && row < e ? __builtin_nanf("") : 0.0f;
+#pragma unroll
+                    for (int m = 0; m < kMF; ++m) t.acc[m][n] += nan;
                 }
-                if (r0 + 16 * n + 16 <= s || r0 + 16 * n >= e) continue;
-                f32x4 add[kMF];
-                for (int m = 0; m < kMF; ++m) add[m] = f32x4{0, 0, 0, 0};
-                for (uint32_t j0 = 0; j0 < a.rank; j0 += 4 * T::kPiece) {
-                    const uint32_t j = j0 + q * T::kPiece;
-                    float v[T::kPiece];
+            }
+            if (gr.none) continue;
+            // The product is formed apart and added to the group's own rows, so that a NaN in
+            // its adapter does not reach the others through 0 * NaN.
+            for (uint32_t j0 = 0; j0 < a.rank; j0 += 4 * T::kPiece) {
+                const uint32_t j = j0 + q * T::kPiece;
+                typename T::Wide v[kMR];
 #pragma unroll
-                    for (int i = 0; i < T::kPiece; ++i)
-                        v[i] = in && j < a.rank ? a.scale * u[row * a.rank + j + i] : 0.0f;
+                for (int n = 0; n < kMR; ++n) {
+                    const uint64_t row = r0 + 16 * n + l16;
+                    const bool in = row >= s && row < e && j < a.rank;
+                    const f32x4 *pu = reinterpret_cast<const f32x4 *>(u + row * a.rank + j);
+                    float z[T::kPiece];
 #pragma unroll
-                    for (int m = 0; m < kMF; ++m) {
-                        const uint32_t f = f0 + 16 * m + l16;
-                        u32x4 fb = kZeros;
-                        if (j < a.rank && f < a.d_out) {
-                            const uint64_t at = gr.base + (uint64_t)a.rank * a.d_in +
-                                                (uint64_t)f * a.rank + j;
-                            fb = piece_at<T>(adapters + at);
-                            if (gr.bits) fb = T::move(fb, piece_signs<T>(gr.bits, at), gr.alpha);
-                        }
-                        add[m] = T::mma_f32(fb, v, add[m]);
+                    for (int i = 0; i < T::kPiece; i += 4) {
+                        const f32x4 w = in ? pu[i / 4] : f32x4{0, 0, 0, 0};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) z[i + k] = a.scale * w[k];
+                    }
+                    v[n] = T::wide(z);
+                }
+#pragma unroll
+                for (int m = 0; m < kMF; ++m) {
+                    const uint32_t f = f0 + 16 * m + l16;
+                    u32x4 fb = kZeros;
+                    if (j < a.rank && f < a.d_out) {
+                        const uint64_t at = gr.base + (uint64_t)a.rank * a.d_in +
+                                            (uint64_t)f * a.rank + j;
+                        fb = piece_at<T>(adapters + at);
+                        if (gr.bits) fb = T::move(fb, piece_signs<T>(gr.bits, at), gr.alpha);
+                    }
+#pragma unroll
+                    for (int n = 0; n < kMR; ++n) {
+                        const uint64_t row = r0 + 16 * n + l16;
+                        if (r0 + 16 * n + 16 <= s || r0 + 16 * n >= e) continue;
+                        const bool in = row >= s && row < e;
+                        const f32x4 add = T::mma(fb, v[n], f32x4{0, 0, 0, 0});
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            t.acc[m][n][i] = in ? t.acc[m][n][i] + add[i] : t.acc[m][n][i];
                     }
                 }
-                for (int m = 0; m < kMF; ++m)
-                    for (int i = 0; i < 4; ++i)
-                        t.acc[m][n][i] = in ? t.acc[m][n][i] + add[m][i] : t.acc[m][n][i];
             }
         }
 #pragma unroll
@@ -355,50 +376,101 @@ struct EndHead {
     }
 };
 
+// Tile of workgroup b of nf x nr: consecutive tiles run through eight row tiles, then the
+// next features, and each XCD (workgroup b runs on XCD b % 8) takes one contiguous range, so
+// that the tiles in flight on an XCD share their rows and weights in its L2.
+__device__ __forceinline__ bool tile_of(uint32_t b, uint32_t nf, uint32_t nr, uint32_t &f, uint32_t &r)
+{
+    const uint64_t n = (uint64_t)nf * nr;
+    const uint64_t x = b & 7u;
+    const uint64_t t = n * x / 8 + (b >> 3);
+    if (t >= n * (x + 1) / 8) return false;
+    constexpr uint32_t kDeep = 8;
+    const uint32_t group = (uint32_t)(t / ((uint64_t)kDeep * nf));
+    const uint32_t in = (uint32_t)(t - (uint64_t)group * kDeep * nf);
+    const uint32_t deep = nr - group * kDeep < kDeep ? nr - group * kDeep : kDeep;
+    f = in / deep;
+    r = group * kDeep + in % deep;
+    return true;
+}
+
+typedef const __attribute__((address_space(1))) void *gptr_t;
+typedef __attribute__((address_space(3))) void *lptr_t;
+
 template <class T, int kWF, int kWR, int kMF, int kMR, class End>
 __global__ __launch_bounds__(kWF * kWR * 64) void k_product(
     ProductArgs p, const typename T::elem *x, const typename T::elem *w, const uint32_t *list,
     const uint32_t *count, End end)
 {
-    constexpr int kThreads = kWF * kWR * 64;
+    constexpr int kWaves = kWF * kWR;
     constexpr int kF = kWF * kMF * 16, kR = kWR * kMR * 16;
     constexpr int kPieces = 8;                              // 16-byte pieces of a staged row
     constexpr uint32_t kStep = kPieces * T::kPiece;
-    __shared__ u32x4 sw[kF * kPieces], sx[kR * kPieces];
+    constexpr int kLoads = (kF + kR) / 8 / kWaves;          // 8 rows of 128 bytes per wave load
+    static_assert((kF + kR) % (8 * kWaves) == 0 && kF % 8 == 0, "whole loads");
+    extern __shared__ u32x4 stage[];                        // [2][kF + kR][kPieces]
     const uint64_t rows = places(p.base, p.rows, count);
-    const uint32_t nf = (p.features + kF - 1) / kF;
-    const uint32_t f0 = blockIdx.x % nf * kF;
-    const uint64_t r0 = (uint64_t)(blockIdx.x / nf) * kR;
-    if (r0 >= rows) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    uint32_t tf, tr;
+    if (!tile_of(blockIdx.x, (p.features + kF - 1) / kF, (uint32_t)((rows + kR - 1) / kR), tf, tr))
+        return;
+    const uint32_t f0 = tf * kF;
+    const uint64_t r0 = (uint64_t)tr * kR;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, q = lane >> 4;
     const int wf = wave % kWF, wr = wave / kWF;
+    // Staged row i holds its piece c at place c ^ (i / 2 % 8): sixteen rows read at one c then
+    // cover all banks once.
+    const typename T::elem *src[kLoads];
+    uint32_t piece[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int at = (i * kWaves + wave) * 8 + (lane >> 3);
+        piece[i] = ((lane & 7) ^ (at >> 1 & 7)) * T::kPiece;
+        if (at < kF) {
+            const uint32_t f = f0 + at < p.features ? f0 + at : p.features - 1;
+            src[i] = w + (uint64_t)f * p.k + piece[i];
+        } else {
+            const uint64_t r = r0 + (at - kF) < rows ? r0 + (at - kF) : rows - 1;
+            src[i] = x + (list ? list[p.base + r] : p.base + r) * p.x_stride + piece[i];
+        }
+    }
+    const auto issue = [&](uint32_t k0, int buf) {
+        const bool tail = k0 + kStep > p.k;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const void *g = src[i] + k0;
+            if (tail && k0 + piece[i] >= p.k) g = &kZeros;
+            u32x4 *l = stage + (buf * (kF + kR) + (i * kWaves + wave) * 8) * kPieces;
+            __builtin_amdgcn_global_load_lds((gptr_t)g, (lptr_t)l, 16, 0, 0);
+        }
+    };
     Tile<T, kMF, kMR> t;
+#pragma unroll
     for (int m = 0; m < kMF; ++m)
+#pragma unroll
         for (int n = 0; n < kMR; ++n) t.acc[m][n] = f32x4{0, 0, 0, 0};
+    issue(0, 0);
+    __syncthreads();
+    int buf = 0;
     for (uint32_t k0 = 0; k0 < p.k; k0 += kStep) {
-        for (int i = tid; i < kF * kPieces; i += kThreads) {
-            const uint32_t f = f0 + i / kPieces, k = k0 + (i % kPieces) * T::kPiece;
-            sw[i] = f < p.features && k < p.k ? piece_at<T>(w + (uint64_t)f * p.k + k) : kZeros;
-        }
-        for (int i = tid; i < kR * kPieces; i += kThreads) {
-            const uint64_t r = r0 + i / kPieces;
-            const uint32_t k = k0 + (i % kPieces) * T::kPiece;
-            u32x4 v = kZeros;
-            if (r < rows && k < p.k)
-                v = piece_at<T>(x + (list ? list[p.base + r] : p.base + r) * p.x_stride + k);
-            sx[i] = v;
-        }
-        __syncthreads();
+        if (k0 + kStep < p.k) issue(k0 + kStep, buf ^ 1);
+        const u32x4 *sw = stage + buf * (kF + kR) * kPieces, *sx = sw + kF * kPieces;
 #pragma unroll
         for (int c = 0; c < kPieces / 4; ++c) {
             u32x4 fa[kMF], fb[kMR];
-            for (int m = 0; m < kMF; ++m) fa[m] = sw[((wf * kMF + m) * 16 + l16) * kPieces + 4 * c + q];
-            for (int n = 0; n < kMR; ++n) fb[n] = sx[((wr * kMR + n) * 16 + l16) * kPieces + 4 * c + q];
+            const int at = (4 * c + q) ^ (l16 >> 1);
+#pragma unroll
+            for (int m = 0; m < kMF; ++m) fa[m] = sw[((wf * kMF + m) * 16 + l16) * kPieces + at];
+#pragma unroll
+            for (int n = 0; n < kMR; ++n) fb[n] = sx[((wr * kMR + n) * 16 + l16) * kPieces + at];
+#pragma unroll
             for (int m = 0; m < kMF; ++m)
+#pragma unroll
                 for (int n = 0; n < kMR; ++n) t.acc[m][n] = T::mma(fa[m], fb[n], t.acc[m][n]);
         }
         __syncthreads();
+        buf ^= 1;
     }
     end(t, f0 + wf * kMF * 16, r0 + wr * kMR * 16);
 }
@@ -476,9 +548,18 @@ hipError_t product(const ProductArgs &p, const typename T::elem *x, const typena
     const uint64_t nf = (p.features + kWF * kMF * 16 - 1) / (kWF * kMF * 16);
     const uint64_t nr = (p.rows + kWR * kMR * 16 - 1) / (kWR * kMR * 16);
     if (nf * nr > 0x7FFFFFFFull) return hipErrorInvalidValue;
+    constexpr uint32_t lds = 2 * (kWF * kMF + kWR * kMR) * 16 * 128;
     k_product<T, kWF, kWR, kMF, kMR, End>
-        <<<(uint32_t)(nf * nr), kWF * kWR * 64, 0, stream>>>(p, x, w, list, count, end);
+        <<<(uint32_t)((nf * nr + 7) / 8 * 8), kWF * kWR * 64, lds, stream>>>(p, x, w, list, count, end);
     return hipGetLastError();
+}
+
+template <class T, int kWF, int kWR, int kMF, int kMR, class End>
+hipError_t raise_lds_limit()
+{
+    return hipFuncSetAttribute(
+        reinterpret_cast<const void *>(&k_product<T, kWF, kWR, kMF, kMR, End>),
+        hipFuncAttributeMaxDynamicSharedMemorySize, 2 * (kWF * kMF + kWR * kMR) * 16 * 128);
 }
 
 template <class T>
@@ -495,7 +576,7 @@ hipError_t project(const AdapterArgs &a, const void *x, uint64_t x_stride, const
     }
     const ProductArgs p = {0, a.rows, x_stride, a.d_in, a.d_out};
     const EndProject<T> end = {a, u, pa, static_cast<const E *>(bias), static_cast<E *>(y), y_stride};
-    return product<T, 2, 2, 2, 2>(p, px, static_cast<const E *>(w), nullptr, nullptr, end, stream);
+    return product<T, 2, 4, 8, 4>(p, px, static_cast<const E *>(w), nullptr, nullptr, end, stream);
 }
 
 template <class T>
@@ -515,7 +596,7 @@ hipError_t head(const HeadArgs &h, const void *x, const void *w, hipStream_t str
         const uint64_t rows = h.rows - base < kHeadPlaces ? h.rows - base : kHeadPlaces;
         const ProductArgs p = {base, rows, h.x_stride, h.k, h.features};
         const EndHead end = {h.features, base, rows, h.targets, list, count, sp.m, sp.s, sp.t, sp.tl};
-        hipError_t e = product<T, 2, 2, 2, 2>(p, static_cast<const E *>(x), static_cast<const E *>(w),
+        hipError_t e = product<T, 2, 4, 8, 4>(p, static_cast<const E *>(x), static_cast<const E *>(w),
                                               list, count, end, stream);
         if (e != hipSuccess) return e;
         k_head_join<<<(uint32_t)((rows + 63) / 64), 256, 0, stream>>>(
@@ -527,7 +608,21 @@ hipError_t head(const HeadArgs &h, const void *x, const void *w, hipStream_t str
     return hipSuccess;
 }
 
+template <class T>
+hipError_t prepare()
+{
+    hipError_t e = raise_lds_limit<T, 2, 4, 8, 4, EndProject<T>>();
+    if (e == hipSuccess) e = raise_lds_limit<T, 2, 4, 8, 4, EndHead>();
+    return e;
+}
+
 }  // namespace
+
+hipError_t prepare_products()
+{
+    const hipError_t e = prepare<Bf16>();
+    return e == hipSuccess ? prepare<Fp32>() : e;
+}
 
 hipError_t launch_adapter_project(const AdapterArgs &a, bool bf16, const void *x, uint64_t x_stride,
                                   const void *w, const void *bias, const void *adapters, float *u,

@@ -143,6 +143,9 @@ hipError_t launch_token_logprobs(const void *logits, bool bf16, uint64_t rows, u
 hipError_t launch_group_loss(const float *logp, const int64_t *targets, const int64_t *starts,
                              uint32_t n_groups, uint64_t rows, double *loss, hipStream_t stream);
 
+// Raise the dynamic-LDS limits of the product kernels on the current device (from zo_init).
+hipError_t prepare_products();
+
 // The groups of rows of one zo_adapter_project call (device pointers).
 struct AdapterArgs {
     uint64_t rows;
@@ -174,7 +177,7 @@ struct HeadArgs {
 };
 // Rows whose partial statistics are held at once, and the features of one partial.
 constexpr uint64_t kHeadPlaces = 16384;
-constexpr uint32_t kHeadPart = 32;
+constexpr uint32_t kHeadPart = 128;
 struct HeadSpace {
     uint32_t *count, *list;
     float *m, *s, *t, *tl;

@@ -72,8 +72,9 @@ class Context:
 
 
 def _stream(stream=None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    # the raw handle of the current stream: 0.1 us, 2.8 us through a torch.cuda.Stream object
+    return (stream.cuda_stream if stream is not None
+            else torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -87,9 +88,9 @@ def _dtype_code(t: torch.Tensor) -> int:
 def _dev(t: torch.Tensor, name: str, dtype=None) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor (got {t.device})")
-    if t.device.index is not None and t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, not on the current device "
                          f"cuda:{torch.cuda.current_device()}")
     if not t.is_contiguous():
@@ -502,9 +503,9 @@ def _matrix(t: torch.Tensor, name: str, dtype=None):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != 2:
         raise ValueError(f"{name} must be a matrix, got shape {tuple(t.shape)}")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor (got {t.device})")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, not on the current device "
                          f"cuda:{torch.cuda.current_device()}")
     if dtype is not None and t.dtype != dtype:
@@ -544,16 +545,18 @@ def zo_token_logprobs(ctx: Context, logits: torch.Tensor, targets: torch.Tensor 
             _new(rows, torch.float32, stream) if entropy else None,
             _new((rows, top_k), torch.int64, stream) if top_k else None,
             _new((rows, top_k), torch.float32, stream) if top_k else None)
-    if (out.logp is None) != (targets is None):
-        raise ValueError("logp goes with targets")
-    op, ep = _vector(out.logp, "logp", rows, torch.float32), _vector(out.entropy, "entropy", rows,
-                                                                     torch.float32)
-    ip = vp = None
-    if top_k:
-        ip, vp = _dev(out.top_ids, "top_ids", torch.int64), _dev(out.top_logp, "top_logp",
-                                                                 torch.float32)
-        if tuple(out.top_ids.shape) != (rows, top_k) or tuple(out.top_logp.shape) != (rows, top_k):
-            raise ValueError(f"top_ids and top_logp must have shape ({rows}, {top_k})")
+        op, ep, ip, vp = (None if o is None else o.data_ptr() for o in out)
+    else:
+        if (out.logp is None) != (targets is None):
+            raise ValueError("logp goes with targets")
+        op = _vector(out.logp, "logp", rows, torch.float32)
+        ep = _vector(out.entropy, "entropy", rows, torch.float32)
+        ip = vp = None
+        if top_k:
+            ip = _dev(out.top_ids, "top_ids", torch.int64)
+            vp = _dev(out.top_logp, "top_logp", torch.float32)
+            if tuple(out.top_ids.shape) != (rows, top_k) or tuple(out.top_logp.shape) != (rows, top_k):
+                raise ValueError(f"top_ids and top_logp must have shape ({rows}, {top_k})")
     _lib.check(_lib.lib().zo_token_logprobs(ctx.handle, lp, code, rows, vocab, stride, tp, op, ep,
                                             top_k, ip, vp, _stream(stream)), "zo_token_logprobs")
     return out
@@ -580,10 +583,12 @@ def zo_head_logprobs(ctx: Context, hidden: torch.Tensor, weight: torch.Tensor,
     if out is None:
         out = HeadLogprobs(None if tp is None else _new(rows, torch.float32, stream),
                            _new(rows, torch.float32, stream) if entropy else None)
-    if (out.logp is None) != (targets is None):
-        raise ValueError("logp goes with targets")
-    op, ep = _vector(out.logp, "logp", rows, torch.float32), _vector(out.entropy, "entropy", rows,
-                                                                     torch.float32)
+        op, ep = (None if o is None else o.data_ptr() for o in out)
+    else:
+        if (out.logp is None) != (targets is None):
+            raise ValueError("logp goes with targets")
+        op = _vector(out.logp, "logp", rows, torch.float32)
+        ep = _vector(out.entropy, "entropy", rows, torch.float32)
     if workspace is None:
         workspace = _new(zo_head_workspace_bytes(rows, vocab), torch.uint8, stream)
     _lib.check(_lib.lib().zo_head_logprobs(

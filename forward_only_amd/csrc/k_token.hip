@@ -7,15 +7,14 @@
 // a larger maximum m' rescales them by r = e^{m - m'}: s <- s r, t <- (t + s (m - m')) r, and
 // two partial rows merge the same way.  Then lse = m + log s, logp = (x_t - m) - log s and the
 // entropy is log s - t / s, all in fp32.
-#include <float.h>
 #include <math.h>
+
+#include <type_traits>
 
 #include "zo_lm.hpp"
 
 namespace zo {
 namespace {
-
-constexpr int kTokenThreads = 256;
 
 template <class T>
 __device__ __forceinline__ float widen(T v);
@@ -34,69 +33,289 @@ __device__ __forceinline__ uint64_t top_key(float x, uint32_t idx)
     return ((uint64_t)o << 32) | (uint64_t)(0xFFFFFFFFu - idx);
 }
 
+// The value of a key (of -0: +0).
+__device__ __forceinline__ float key_value(uint64_t key)
+{
+    const uint32_t o = (uint32_t)(key >> 32);
+    return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// One row: elements [0, head) up to a 16-byte boundary, then `pieces` of 16 bytes, then the
+// rest.
 template <class T>
-__global__ __launch_bounds__(kTokenThreads) void k_token(
+struct Row {
+    static constexpr uint32_t kPiece = 16 / sizeof(T);
+    const T *p;
+    uint32_t vocab, head, pieces;
+
+    __device__ __forceinline__ Row(const T *row, uint32_t v) : p(row), vocab(v)
+    {
+        head = (uint32_t)(-(intptr_t)row & 15) / sizeof(T);
+        head = head < vocab ? head : vocab;
+        pieces = (vocab - head) / kPiece;
+    }
+    __device__ __forceinline__ uint32_t rest() const { return head + pieces * kPiece; }
+    __device__ __forceinline__ u32x4 piece(uint32_t i) const
+    {
+        return *reinterpret_cast<const u32x4 *>(p + head + (uint64_t)i * kPiece);
+    }
+    static __device__ __forceinline__ float value(const u32x4 &v, int i)
+    {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(v[i]);
+        else return i & 1 ? bf16hi_to_f32(v[i >> 1]) : bf16lo_to_f32(v[i >> 1]);
+    }
+    // -inf in every value.
+    static __device__ __forceinline__ u32x4 nothing()
+    {
+        const uint32_t w = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;
+        return u32x4{w, w, w, w};
+    }
+};
+
+constexpr uint64_t kFewRows = 512;
+constexpr int kUnroll = 4;              // pieces a thread loads before it uses them
+constexpr uint32_t kCandidates = 2048;  // keys that the search for the alternatives can hold
+
+// The place of each of 64 keys (one per lane, 0: none) among them, largest first.
+__device__ __forceinline__ uint32_t rank_in_wave(uint64_t key, const uint64_t *keys)
+{
+    uint32_t r = 0;
+#pragma unroll
+    for (int i = 0; i < kWave; i += 16) {
+        uint64_t other[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) other[u] = keys[i + u];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) r += other[u] > key ? 1u : 0u;
+    }
+    return r;
+}
+
+// The k-th largest of 64 keys, or 1 if fewer than k are there: a lower bound of the k-th
+// largest of everything those keys are maxima of.
+__device__ __forceinline__ uint64_t bound_of(const uint64_t *keys, uint32_t k)
+{
+    const uint64_t key = keys[threadIdx.x & (kWave - 1)];
+    const uint32_t r = rank_in_wave(key, keys);
+    const uint64_t who = __ballot(key != 0 && r == k - 1);
+    return who ? keys[__ffsll((unsigned long long)who) - 1] : 1;
+}
+
+// One workgroup per row, one pass over it: each thread loads four pieces, takes their largest
+// value first (it rescales the sums at most once per four pieces) and adds up.  What bounds it
+// is HBM for many rows and the latency of one round of loads for few.
+//
+// Alternatives.  The maxima of 64 parts of the row (one per kThreads / 64 threads) are at hand
+// from the pass; the k-th largest of them bounds the k-th largest value from below, so only
+// the pieces of threads whose own maximum reaches that bound are looked through again (the
+// row is in L2 by then), for a few more than k candidates, which are ranked by counting.  Keys hold
+// value and index, so ties neither widen the search nor leave the order open.  Rows where
+// that does not hold (NaN, only -inf, or more candidates than fit) take k passes of a search
+// for the largest key below the last.
+template <class T, int kThreads>
+__global__ __launch_bounds__(kThreads) void k_token(
     const T *logits, uint32_t vocab, uint64_t stride, const int64_t *targets, float *logp,
     float *entropy, uint32_t top_k, int64_t *top_ids, float *top_logp)
 {
-    const uint64_t row = blockIdx.x;
+    constexpr int kWaves = kThreads / kWave;
+    constexpr uint32_t kNone = 0xFFFFFFFFu, kHead = 0xFFFFFFFEu, kRest = 0xFFFFFFFDu;
+    const uint64_t at = blockIdx.x;
     const int tid = threadIdx.x;
-    const int64_t tgt = targets ? targets[row] : 0;
+    const int64_t tgt = targets ? targets[at] : 0;
     if (targets && tgt == kIgnoreToken) {
         if (tid == 0) {
-            logp[row] = 0.0f;
-            if (entropy) entropy[row] = 0.0f;
+            logp[at] = 0.0f;
+            if (entropy) entropy[at] = 0.0f;
         }
-        for (uint32_t i = tid; i < top_k; i += kTokenThreads) {
-            top_ids[row * top_k + i] = -1;
-            top_logp[row * top_k + i] = 0.0f;
+        for (uint32_t i = tid; i < top_k; i += kThreads) {
+            top_ids[at * top_k + i] = -1;
+            top_logp[at * top_k + i] = 0.0f;
         }
         return;
     }
-    const T *p = logits + row * stride;
+    const Row<T> row(logits + at * stride, vocab);
+    constexpr int kPiece = Row<T>::kPiece;
+    float target = __builtin_nanf("");
+    if (tid == 0 && targets && tgt >= 0 && tgt < (int64_t)vocab) target = widen(row.p[tgt]);
     SoftStats st = SoftStats::empty();
-    for (uint32_t v = tid; v < vocab; v += kTokenThreads) {
-        const float x = widen(p[v]);
+    float best = -INFINITY;     // largest value of this thread, and where it was first seen
+    uint32_t where = kNone;
+    const auto one = [&](float x, uint32_t place) {
         st.raise(x);
         st.add(x);
-    }
-    st.wave_merge();
-    __shared__ SoftStats parts[kTokenThreads / kWave];
-    __shared__ uint64_t keys[kTokenThreads / kWave];
-    if ((tid & (kWave - 1)) == 0) parts[tid / kWave] = st;
-    __syncthreads();
-    st = parts[0];
-    for (int w = 1; w < kTokenThreads / kWave; ++w) st.merge(parts[w]);
-    const float logs = logf(st.s);
-    if (tid == 0) {
-        if (targets) {
-            float lp = __builtin_nanf("");
-            if (tgt >= 0 && tgt < (int64_t)vocab) lp = (widen(p[tgt]) - st.m) - logs;
-            logp[row] = lp;
+        if (x > best || where == kNone) {
+            best = fmaxf(x, best);
+            where = place;
         }
-        if (entropy) entropy[row] = logs - st.t / st.s;
+    };
+    if ((uint32_t)tid < row.head) one(widen(row.p[tid]), kHead);
+    for (uint32_t i = tid; i < row.pieces; i += kUnroll * kThreads) {
+        u32x4 v[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            v[u] = i + u * kThreads < row.pieces ? row.piece(i + u * kThreads) : Row<T>::nothing();
+        float top = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+            for (int j = 0; j < kPiece; ++j) top = fmaxf(top, Row<T>::value(v[u], j));
+        if (top > best || where == kNone) {
+            best = top;
+            where = i;
+        }
+        st.raise(top);
+        const float m = st.m == -INFINITY ? 0.0f : st.m;
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+            for (int j = 0; j < kPiece; ++j) {
+                const float d = Row<T>::value(v[u], j) - m;
+                const float e = fast_exp(d);
+                st.s += e;
+                st.t = fmaf(e, fmaxf(d, -1e4f), st.t);     // d = -inf: e is 0, add 0
+            }
+    }
+    if (row.rest() + tid < vocab) one(widen(row.p[row.rest() + tid]), kRest);
+
+    __shared__ float parts[kWaves][3];
+    SoftStats all = st;
+    all.wave_merge();
+    if ((tid & (kWave - 1)) == 0) {
+        parts[tid / kWave][0] = all.m;
+        parts[tid / kWave][1] = all.s;
+        parts[tid / kWave][2] = all.t;
+    }
+    // The first largest element of each part, exactly: by the threads that hold its value.
+    __shared__ uint64_t tops[kWave];
+    __shared__ uint32_t found, flagged;
+    if (top_k) {
+        float part = best;
+#pragma unroll
+        for (int o = 1; o < kThreads / kWave; o <<= 1) part = fmaxf(part, __shfl_xor(part, o));
+        uint64_t key = 0;
+        if (best < part) {
+        } else if (where == kHead) {
+            key = top_key(best, tid);
+        } else if (where == kRest) {
+            key = top_key(best, row.rest() + tid);
+        } else if (where != kNone) {
+#pragma unroll
+            for (int u = kUnroll - 1; u >= 0; --u) {
+                const uint32_t i = where + u * kThreads;
+                if (i >= row.pieces) continue;
+                const u32x4 v = row.piece(i);
+#pragma unroll
+                for (int j = kPiece - 1; j >= 0; --j)
+                    if (Row<T>::value(v, j) == best) key = top_key(best, row.head + i * kPiece + j);
+            }
+        }
+#pragma unroll
+        for (int o = 1; o < kThreads / kWave; o <<= 1) {
+            const uint64_t other = __shfl_xor(key, o);
+            key = other > key ? other : key;
+        }
+        if (tid % (kThreads / kWave) == 0) tops[tid / (kThreads / kWave)] = key;
+        if (tid == 0) found = flagged = 0;
+    }
+    __syncthreads();
+    all = {parts[0][0], parts[0][1], parts[0][2]};
+    for (int w = 1; w < kWaves; ++w) all.merge({parts[w][0], parts[w][1], parts[w][2]});
+    const float logs = logf(all.s);
+    if (tid == 0) {
+        if (targets) logp[at] = (target - all.m) - logs;
+        if (entropy) entropy[at] = logs - all.t / all.s;
+    }
+    if (!top_k) return;
+
+    const auto give = [&](uint32_t place, uint64_t k) {
+        top_ids[at * top_k + place] = 0xFFFFFFFFu - (uint32_t)k;
+        top_logp[at * top_k + place] = (key_value(k) - all.m) - logs;
+    };
+    __shared__ uint64_t list[kCandidates + 8];   // read in eights
+    const bool plain = all.s == all.s && all.m > -INFINITY;
+    if (plain) {
+        const uint64_t bound = bound_of(tops, top_k);
+        const auto take = [&](float x, uint32_t idx) {
+            const uint64_t k = top_key(x, idx);
+            if (k < bound) return;
+            const uint32_t n = atomicAdd(&found, 1u);
+            if (n < kCandidates) list[n] = k;
+        };
+        __shared__ uint16_t flags[kThreads];
+        if (where != kNone && top_key(best, 0) >= bound) {
+            flags[atomicAdd(&flagged, 1u)] = (uint16_t)tid;
+            if ((uint32_t)tid < row.head) take(widen(row.p[tid]), tid);
+            if (row.rest() + tid < vocab) take(widen(row.p[row.rest() + tid]), row.rest() + tid);
+        }
+        __syncthreads();
+        // all threads share the flagged ones' pieces, so that their loads are in flight at once
+        const uint32_t per = (row.pieces + kThreads - 1) / kThreads, items = flagged * per;
+        for (uint32_t w = tid; w < items; w += kThreads) {
+            const uint32_t i = flags[w / per] + w % per * kThreads;
+            if (i >= row.pieces) continue;
+            const u32x4 v = row.piece(i);
+#pragma unroll
+            for (int j = 0; j < kPiece; ++j) take(Row<T>::value(v, j), row.head + i * kPiece + j);
+        }
+        __syncthreads();
+        uint32_t n = found;
+        if (n <= kCandidates) {
+            if (n > 2 * kWave) {
+                // many in one place of the row: bound them once more by the list's own parts
+                __syncthreads();
+                if (tid < kWave) {
+                    uint64_t k = 0;
+                    for (uint32_t i = tid; i < n; i += kWave) k = list[i] > k ? list[i] : k;
+                    tops[tid] = k;
+                }
+                if (tid == 0) found = 0;
+                __syncthreads();
+                const uint64_t again = bound_of(tops, top_k);
+                uint64_t mine[kCandidates / kThreads];
+#pragma unroll
+                for (uint32_t i = 0; i < kCandidates / kThreads; ++i)
+                    mine[i] = i * kThreads + tid < n ? list[i * kThreads + tid] : 0;
+                __syncthreads();
+#pragma unroll
+                for (uint32_t i = 0; i < kCandidates / kThreads; ++i)
+                    if (mine[i] >= again && mine[i]) list[atomicAdd(&found, 1u)] = mine[i];
+                __syncthreads();
+                n = found;
+            }
+            for (uint32_t i = tid; i < n; i += kThreads) {
+                const uint64_t k = list[i];
+                uint32_t place = 0;
+                for (uint32_t j = 0; j < n; j += 8) {
+                    uint64_t other[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) other[u] = list[j + u];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) place += j + u < n && other[u] > k ? 1u : 0u;
+                }
+                if (place < top_k) give(place, k);
+            }
+            return;
+        }
     }
     uint64_t below = ~(uint64_t)0;
     for (uint32_t i = 0; i < top_k; ++i) {
-        uint64_t best = 0;
-        for (uint32_t v = tid; v < vocab; v += kTokenThreads) {
-            const uint64_t k = top_key(widen(p[v]), v);
-            if (k < below && k > best) best = k;
+        uint64_t k = 0;
+        for (uint32_t v = tid; v < vocab; v += kThreads) {
+            const uint64_t c = top_key(widen(row.p[v]), v);
+            if (c < below && c > k) k = c;
         }
         for (int o = kWave / 2; o; o >>= 1) {
-            const uint64_t k = __shfl_xor(best, o);
-            best = k > best ? k : best;
+            const uint64_t c = __shfl_xor(k, o);
+            k = c > k ? c : k;
         }
         __syncthreads();
-        if ((tid & (kWave - 1)) == 0) keys[tid / kWave] = best;
+        if ((tid & (kWave - 1)) == 0) tops[tid / kWave] = k;
         __syncthreads();
-        for (int w = 0; w < kTokenThreads / kWave; ++w) best = keys[w] > best ? keys[w] : best;
-        if (tid == 0) {
-            const uint32_t id = 0xFFFFFFFFu - (uint32_t)best;
-            top_ids[row * top_k + i] = id;
-            top_logp[row * top_k + i] = (widen(p[id]) - st.m) - logs;
-        }
-        below = best;
+        for (int w = 0; w < kWaves; ++w) k = tops[w] > k ? tops[w] : k;
+        if (tid == 0) give(i, k);
+        below = k;
     }
 }
 
@@ -142,14 +361,28 @@ hipError_t launch_token_logprobs(const void *logits, bool bf16, uint64_t rows, u
                                  float *entropy, uint32_t top_k, int64_t *top_ids,
                                  float *top_logp, hipStream_t stream)
 {
+    // Few rows (up to two per CU): all of a row's loads should be in flight at once, so 1024
+    // threads take it.  Many rows hide each other's latency: the pass alone is then fastest
+    // with 256 threads (8192 rows of 50272 bf16: 149 us; 149 with 512, 207 with 1024), and the
+    // search for alternatives, serial within a row, with 512 (top 20: 200 us; 219 with 256,
+    // 312 with 1024).
+    const auto launch = [&](auto *p, auto threads) {
+        using E = std::remove_cv_t<std::remove_pointer_t<decltype(p)>>;
+        k_token<E, decltype(threads)::value><<<(uint32_t)rows, decltype(threads)::value, 0, stream>>>(
+            p, vocab, stride, targets, logp, entropy, top_k, top_ids, top_logp);
+    };
+    const auto typed = [&](auto *p) {
+        if (rows <= kFewRows)
+            launch(p, std::integral_constant<int, 1024>());
+        else if (top_k)
+            launch(p, std::integral_constant<int, 512>());
+        else
+            launch(p, std::integral_constant<int, 256>());
+    };
     if (bf16)
-        k_token<uint16_t><<<(uint32_t)rows, kTokenThreads, 0, stream>>>(
-            static_cast<const uint16_t *>(logits), vocab, stride, targets, logp, entropy, top_k,
-            top_ids, top_logp);
+        typed(static_cast<const uint16_t *>(logits));
     else
-        k_token<float><<<(uint32_t)rows, kTokenThreads, 0, stream>>>(
-            static_cast<const float *>(logits), vocab, stride, targets, logp, entropy, top_k,
-            top_ids, top_logp);
+        typed(static_cast<const float *>(logits));
     return hipGetLastError();
 }
 

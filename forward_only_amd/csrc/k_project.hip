@@ -33,6 +33,10 @@ struct Bf16 {
                                                        __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
     }
     static __device__ __forceinline__ float widen(uint16_t v) { return bf16lo_to_f32(v); }
+    static __device__ __forceinline__ float value(u32x4 v, int i)
+    {
+        return i & 1 ? bf16hi_to_f32(v[i >> 1]) : bf16lo_to_f32(v[i >> 1]);
+    }
     // The piece moved by +/-alpha, sign by bit (set: +), rounded as zo_perturb rounds it.
     static __device__ __forceinline__ u32x4 move(u32x4 v, uint32_t signs, float alpha)
     {
@@ -79,6 +83,7 @@ struct Fp32 {
         return c;
     }
     static __device__ __forceinline__ float widen(float v) { return v; }
+    static __device__ __forceinline__ float value(u32x4 v, int i) { return __uint_as_float(v[i]); }
     static __device__ __forceinline__ u32x4 move(u32x4 v, uint32_t signs, float alpha)
     {
         u32x4 o;
@@ -152,12 +157,15 @@ __device__ __forceinline__ uint32_t group_of_slot(const AdapterArgs &a, uint64_t
     return lo;
 }
 
-// u[row][j] = x[row] . A_g[j], fp32: one workgroup per 16 rows of a group; its four waves
-// take every fourth 16-byte-piece group along k and add up in LDS.
+// u[row][j] = x[row] . A_g[j], fp32, and group[row] = g: one workgroup per 16 rows of a group.
+// Its waves split k in interleaved runs of kRun fragments, all of whose loads are in flight at
+// once, and add up in LDS; 16 waves, because one workgroup has a whole adapter to read when
+// requests bring single rows (32 rows with an adapter each, rank 16 of 5120: ... us).
+constexpr int kShrinkWaves = 16;
 template <class T>
-__global__ __launch_bounds__(256) void k_shrink(AdapterArgs a, const typename T::elem *x,
-                                                uint64_t x_stride,
-                                                const typename T::elem *adapters, float *u)
+__global__ __launch_bounds__(kShrinkWaves * 64) void k_shrink(
+    AdapterArgs a, const typename T::elem *x, uint64_t x_stride, const typename T::elem *adapters,
+    float *u, int32_t *group)
 {
     const uint64_t slot = blockIdx.x;
     const uint32_t g = group_of_slot(a, slot);
@@ -165,6 +173,7 @@ __global__ __launch_bounds__(256) void k_shrink(AdapterArgs a, const typename T:
     if (slot < start / 16 + g) return;
     const uint64_t row0 = start + (slot - (start / 16 + g)) * 16;
     if (row0 >= end) return;
+    if (threadIdx.x < 16 && row0 + threadIdx.x < end) group[row0 + threadIdx.x] = (int32_t)g;
     const Group gr = group_of(a, g);
     if (gr.none) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -172,29 +181,44 @@ __global__ __launch_bounds__(256) void k_shrink(AdapterArgs a, const typename T:
     const uint64_t row = row0 + l16 < end ? row0 + l16 : end - 1;
     const typename T::elem *xr = x + row * x_stride;
     constexpr uint32_t kStep = 4 * T::kPiece;   // k covered by one fragment of 16 x 16
-    __shared__ float red[4][16][17];
+    constexpr int kRun = 5;
+    __shared__ float red[kShrinkWaves][16][17];
     for (uint32_t j0 = 0; j0 < a.rank; j0 += 16) {
         const uint32_t j = j0 + l16 < a.rank ? j0 + l16 : a.rank - 1;
         const uint64_t e0 = gr.base + (uint64_t)j * a.d_in;
         f32x4 acc = {0, 0, 0, 0};
-        for (uint32_t k0 = wave * kStep; k0 < a.d_in; k0 += 4 * kStep) {
-            const uint32_t k = k0 + q * T::kPiece;
-            u32x4 fa = kZeros, fx = kZeros;
-            if (k < a.d_in) {
-                fx = piece_at<T>(xr + k);
-                fa = piece_at<T>(adapters + e0 + k);
-                if (gr.bits) fa = T::move(fa, piece_signs<T>(gr.bits, e0 + k), gr.alpha);
+        for (uint32_t k0 = wave * kRun * kStep; k0 < a.d_in; k0 += kShrinkWaves * kRun * kStep) {
+            u32x4 fa[kRun], fx[kRun];
+            uint32_t sg[kRun];
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) {
+                const uint32_t k = k0 + i * kStep + q * T::kPiece;
+                fa[i] = fx[i] = kZeros;
+                sg[i] = 0;
+                if (k < a.d_in) {
+                    fx[i] = piece_at<T>(xr + k);
+                    fa[i] = piece_at<T>(adapters + e0 + k);
+                    if (gr.bits) sg[i] = piece_signs<T>(gr.bits, e0 + k);
+                }
             }
-            acc = T::mma(fa, fx, acc);
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) {
+                // past the end of k the moved zeros meet zeros of x
+                if (gr.bits) fa[i] = T::move(fa[i], sg[i], gr.alpha);
+                acc = T::mma(fa[i], fx[i], acc);
+            }
         }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 4; ++i) red[wave][l16][4 * q + i] = acc[i];   // [row][adapter row]
         __syncthreads();
         const int r = threadIdx.x >> 4, c = threadIdx.x & 15;
-        if (row0 + r < end && j0 + c < a.rank)
-            u[(row0 + r) * a.rank + j0 + c] =
-                (red[0][r][c] + red[1][r][c]) + (red[2][r][c] + red[3][r][c]);
+        if (r < 16 && row0 + r < end && j0 + c < a.rank) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kShrinkWaves; ++w) sum += red[w][r][c];
+            u[(row0 + r) * a.rank + j0 + c] = sum;
+        }
     }
 }
 
@@ -225,16 +249,64 @@ template <class T>
 struct EndProject {
     AdapterArgs a;
     const float *u;
+    const int32_t *group;
     const typename T::elem *adapters, *bias;
     typename T::elem *y;
     uint64_t y_stride;
 
+    // Many rows: the groups that meet the tile one after another, on MFMA.
     template <int kMF, int kMR>
     __device__ __forceinline__ void operator()(Tile<T, kMF, kMR> &t, uint32_t f0, uint64_t r0) const
     {
+        add_groups(t, f0, r0);
+        store(t, f0, r0);
+    }
+
+    // Few rows, each perhaps with an adapter of its own: every lane the products of its row, so
+    // that one round of loads serves all groups.
+    template <int kMF>
+    __device__ __forceinline__ void add_rows(Tile<T, kMF, 1> &t, uint32_t f0, uint64_t r0) const
+    {
         const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
-        const uint64_t lo = clamp_row(a.starts[0], a.rows);
-        const uint64_t hi = clamp_row(a.starts[a.n_groups], a.rows);
+        const uint64_t row = r0 + l16;
+        if (row >= a.rows) return;
+        const int32_t g = group[row];
+        if (g < 0 || (uint32_t)g >= a.n_groups) return;
+        const Group gr = group_of(a, (uint32_t)g);
+        if (gr.bad) {
+#pragma unroll
+            for (int m = 0; m < kMF; ++m) t.acc[m][0] += __builtin_nanf("");
+        }
+        if (gr.none) return;
+        for (uint32_t j = 0; j < a.rank; j += 8) {
+            const f32x4 *pu = reinterpret_cast<const f32x4 *>(u + row * a.rank + j);
+            const f32x4 ua = pu[0], ub = pu[1];
+#pragma unroll
+            for (int m = 0; m < kMF; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t f = f0 + 16 * m + 4 * q + i;
+                    if (f >= a.d_out) continue;
+                    const uint64_t at = gr.base + (uint64_t)a.rank * a.d_in + (uint64_t)f * a.rank + j;
+                    const uint32_t signs = gr.bits ? gr.bits[at >> 3] : 0;
+                    float s = 0.0f;
+#pragma unroll
+                    for (int h = 0; h < 8; h += T::kPiece) {
+                        u32x4 fb = piece_at<T>(adapters + at + h);
+                        if (gr.bits) fb = T::move(fb, signs >> h, gr.alpha);
+#pragma unroll
+                        for (int k = 0; k < T::kPiece; ++k)
+                            s = fmaf(T::value(fb, k), h + k < 4 ? ua[(h + k) & 3] : ub[(h + k) & 3], s);
+                    }
+                    t.acc[m][0][i] += a.scale * s;
+                }
+        }
+    }
+
+    template <int kMF, int kMR>
+    __device__ __forceinline__ void add_groups(Tile<T, kMF, kMR> &t, uint32_t f0, uint64_t r0) const
+    {
+        const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
         const uint64_t r1 = r0 + 16 * kMR < a.rows ? r0 + 16 * kMR : a.rows;
         // groups that meet rows [r0, r1): from the last one that starts at or before r0
         uint32_t g = 0, top = a.n_groups;
@@ -302,6 +374,14 @@ struct EndProject {
                 }
             }
         }
+    }
+
+    template <int kMF, int kMR>
+    __device__ __forceinline__ void store(Tile<T, kMF, kMR> &t, uint32_t f0, uint64_t r0) const
+    {
+        const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+        const uint64_t lo = clamp_row(a.starts[0], a.rows);
+        const uint64_t hi = clamp_row(a.starts[a.n_groups], a.rows);
 #pragma unroll
         for (int n = 0; n < kMR; ++n) {
             const uint64_t row = r0 + 16 * n + l16;
@@ -333,6 +413,14 @@ struct EndHead {
     const uint32_t *count;
     float *m, *s, *t;           // [wave tile][place]
     float *tl;                  // logit of each place's target
+
+    template <class T, int kMF>
+    __device__ __forceinline__ void add_rows(Tile<T, kMF, 1> &, uint32_t, uint64_t) const {}
+    template <class T, int kMF>
+    __device__ __forceinline__ void store(Tile<T, kMF, 1> &t4, uint32_t f0, uint64_t r0) const
+    {
+        (*this)(t4, f0, r0);
+    }
 
     template <class T, int kMF, int kMR>
     __device__ __forceinline__ void operator()(Tile<T, kMF, kMR> &t4, uint32_t f0, uint64_t r0) const
@@ -475,6 +563,86 @@ __global__ __launch_bounds__(kWF * kWR * 64) void k_product(
     end(t, f0 + wf * kMF * 16, r0 + wr * kMR * 16);
 }
 
+// Few rows.  What bounds the product is reading w once, so w goes straight from memory into
+// registers: a workgroup takes 16 kMF features and all rows, its eight waves split k in
+// interleaved blocks of kRun fragments (256 contiguous bytes of each bf16 row), and the waves'
+// sums meet in LDS.  x, read by every workgroup, comes from L2.
+constexpr int kFewWaves = 8;
+template <class T, int kMF, int kMR, class End>
+__global__ __launch_bounds__(kFewWaves * 64) void k_few(ProductArgs p, const typename T::elem *x,
+                                                        const typename T::elem *w, End end)
+{
+    constexpr uint32_t kStep = 4 * T::kPiece;
+    constexpr int kRun = 4;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l16 = lane & 15, q = lane >> 4;
+    const uint32_t f0 = blockIdx.x * (16 * kMF);
+    const typename T::elem *pw[kMF], *px[kMR];
+#pragma unroll
+    for (int m = 0; m < kMF; ++m) {
+        const uint32_t f = f0 + 16 * m + l16 < p.features ? f0 + 16 * m + l16 : p.features - 1;
+        pw[m] = w + (uint64_t)f * p.k + q * T::kPiece;
+    }
+#pragma unroll
+    for (int n = 0; n < kMR; ++n) {
+        const uint64_t r = (uint64_t)(16 * n + l16) < p.rows ? 16 * n + l16 : p.rows - 1;
+        px[n] = x + r * p.x_stride + q * T::kPiece;
+    }
+    Tile<T, kMF, kMR> t;
+#pragma unroll
+    for (int m = 0; m < kMF; ++m)
+#pragma unroll
+        for (int n = 0; n < kMR; ++n) t.acc[m][n] = f32x4{0, 0, 0, 0};
+    const uint32_t stride = kFewWaves * kRun * kStep;
+    uint32_t k0 = wave * kRun * kStep;
+    for (; k0 + kRun * kStep <= p.k; k0 += stride) {
+        u32x4 fw[kMF][kRun], fx[kMR][kRun];
+#pragma unroll
+        for (int m = 0; m < kMF; ++m)
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) fw[m][i] = piece_at<T>(pw[m] + k0 + i * kStep);
+#pragma unroll
+        for (int n = 0; n < kMR; ++n)
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) fx[n][i] = piece_at<T>(px[n] + k0 + i * kStep);
+#pragma unroll
+        for (int i = 0; i < kRun; ++i)
+#pragma unroll
+            for (int m = 0; m < kMF; ++m)
+#pragma unroll
+                for (int n = 0; n < kMR; ++n) t.acc[m][n] = T::mma(fw[m][i], fx[n][i], t.acc[m][n]);
+    }
+    for (int i = 0; i < kRun && k0 < p.k; ++i, k0 += kStep) {   // the last, short block
+        const bool in = k0 + q * T::kPiece < p.k;
+        u32x4 fx[kMR];
+#pragma unroll
+        for (int n = 0; n < kMR; ++n) fx[n] = in ? piece_at<T>(px[n] + k0) : kZeros;
+#pragma unroll
+        for (int m = 0; m < kMF; ++m) {
+            const u32x4 fw = in ? piece_at<T>(pw[m] + k0) : kZeros;
+#pragma unroll
+            for (int n = 0; n < kMR; ++n) t.acc[m][n] = T::mma(fw, fx[n], t.acc[m][n]);
+        }
+    }
+    __shared__ f32x4 sums[kFewWaves][kMF][kMR][64];
+#pragma unroll
+    for (int m = 0; m < kMF; ++m)
+#pragma unroll
+        for (int n = 0; n < kMR; ++n) sums[wave][m][n][lane] = t.acc[m][n];
+    __syncthreads();
+    if (wave >= kMR) return;
+    Tile<T, kMF, 1> own;
+#pragma unroll
+    for (int m = 0; m < kMF; ++m) {
+        own.acc[m][0] = sums[0][m][wave][lane];
+#pragma unroll
+        for (int v = 1; v < kFewWaves; ++v) own.acc[m][0] += sums[v][m][wave][lane];
+    }
+    end.add_rows(own, f0, 16 * wave);
+    end.store(own, f0, 16 * wave);
+}
+
 // ---- joining the head's partial statistics ----------------------------------------------
 
 // The places of the rows that count, in order, and zeros for the others' outputs; one
@@ -508,38 +676,44 @@ __global__ __launch_bounds__(1024) void k_counted(const int64_t *targets, uint64
     if (tid == 0) *count = at;
 }
 
-__global__ __launch_bounds__(256) void k_head_join(const float *m, const float *s, const float *t,
-                                                   const float *tl, uint32_t parts,
-                                                   uint64_t base, uint64_t rows,
-                                                   const uint32_t *list, const uint32_t *count,
-                                                   const int64_t *targets, uint32_t features,
-                                                   float *logp, float *entropy)
+// Joins the parts of each place: eight places per workgroup, 128 threads for each.
+__global__ __launch_bounds__(1024) void k_head_join(const float *m, const float *s, const float *t,
+                                                    const float *tl, uint32_t parts, uint64_t base,
+                                                    uint64_t rows, const uint32_t *list,
+                                                    const uint32_t *count, const int64_t *targets,
+                                                    uint32_t features, float *logp, float *entropy)
 {
     const uint64_t n = places(base, rows, count);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const uint64_t at = (uint64_t)blockIdx.x * 64 + lane;
+    const int of = threadIdx.x & 7, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint64_t at = (uint64_t)blockIdx.x * 8 + of;
+    if ((uint64_t)blockIdx.x * 8 >= n) return;
     SoftStats st = SoftStats::empty();
     if (at < n)
-        for (uint32_t p = wave; p < parts; p += 4) {
-            SoftStats o;
-            o.m = m[(uint64_t)p * rows + at];
-            o.s = s[(uint64_t)p * rows + at];
-            o.t = t[(uint64_t)p * rows + at];
-            st.merge(o);
-        }
-    __shared__ SoftStats all[4][64];
-    all[wave][lane] = st;
-    __syncthreads();
-    if (wave || at >= n) return;
-    for (int w = 1; w < 4; ++w) st.merge(all[w][lane]);
-    const uint64_t row = list ? list[base + at] : base + at;
-    const float logs = logf(st.s);
-    if (logp) {
-        const int64_t tgt = targets[row];
-        logp[row] = tgt >= 0 && tgt < (int64_t)features ? (tl[at] - st.m) - logs : __builtin_nanf("");
+        for (uint32_t p = threadIdx.x >> 3; p < parts; p += 128)
+            st.merge({m[(uint64_t)p * rows + at], s[(uint64_t)p * rows + at],
+                      t[(uint64_t)p * rows + at]});
+    st.wave_merge(32, 8);
+    __shared__ float all[16][8][3];
+    if (lane < 8) {
+        all[wave][of][0] = st.m;
+        all[wave][of][1] = st.s;
+        all[wave][of][2] = st.t;
     }
-    if (entropy) entropy[row] = logs - st.t / st.s;
+    __syncthreads();
+    if (threadIdx.x >= 8 || at >= n) return;
+    for (int w = 1; w < 16; ++w) st.merge({all[w][of][0], all[w][of][1], all[w][of][2]});
+    const uint64_t row = list ? list[base + at] : base + at;
+    const int64_t tgt = targets ? targets[row] : 0;
+    const bool ignore = targets && tgt == kIgnoreToken;
+    const float logs = logf(st.s);
+    if (logp)
+        logp[row] = ignore ? 0.0f
+                    : tgt >= 0 && tgt < (int64_t)features ? (tl[at] - st.m) - logs
+                                                          : __builtin_nanf("");
+    if (entropy) entropy[row] = ignore ? 0.0f : logs - st.t / st.s;
 }
+
+// ---- launches ---------------------------------------------------------------------------
 
 template <class T, int kWF, int kWR, int kMF, int kMR, class End>
 hipError_t product(const ProductArgs &p, const typename T::elem *x, const typename T::elem *w,
@@ -562,6 +736,27 @@ hipError_t raise_lds_limit()
         hipFuncAttributeMaxDynamicSharedMemorySize, 2 * (kWF * kMF + kWR * kMR) * 16 * 128);
 }
 
+// The product of at most kFewRows rows: features per workgroup by how many workgroups that
+// leaves.
+template <class T, int kMF, class End>
+hipError_t few_of(const ProductArgs &p, const typename T::elem *x, const typename T::elem *w,
+                  const End &end, hipStream_t stream)
+{
+    const uint32_t grid = (p.features + 16 * kMF - 1) / (16 * kMF);
+    if (p.rows <= 16)
+        k_few<T, kMF, 1, End><<<grid, kFewWaves * 64, 0, stream>>>(p, x, w, end);
+    else
+        k_few<T, kMF, 2, End><<<grid, kFewWaves * 64, 0, stream>>>(p, x, w, end);
+    return hipGetLastError();
+}
+template <class T, class End>
+hipError_t few(const ProductArgs &p, const typename T::elem *x, const typename T::elem *w,
+               const End &end, hipStream_t stream)
+{
+    return few_fragments(p.features) == 2 ? few_of<T, 2>(p, x, w, end, stream)
+                                          : few_of<T, 1>(p, x, w, end, stream);
+}
+
 template <class T>
 hipError_t project(const AdapterArgs &a, const void *x, uint64_t x_stride, const void *w,
                    const void *bias, const void *adapters, float *u, void *y, uint64_t y_stride,
@@ -569,14 +764,16 @@ hipError_t project(const AdapterArgs &a, const void *x, uint64_t x_stride, const
 {
     typedef typename T::elem E;
     const E *px = static_cast<const E *>(x), *pa = static_cast<const E *>(adapters);
-    if (a.rank && a.n_adapters) {
-        k_shrink<T><<<(uint32_t)(a.rows / 16 + a.n_groups), 256, 0, stream>>>(a, px, x_stride, pa, u);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
+    int32_t *group = reinterpret_cast<int32_t *>(u + a.rows * a.rank);
+    k_shrink<T><<<(uint32_t)(a.rows / 16 + a.n_groups), kShrinkWaves * 64, 0, stream>>>(
+        a, px, x_stride, pa, u, group);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     const ProductArgs p = {0, a.rows, x_stride, a.d_in, a.d_out};
-    const EndProject<T> end = {a, u, pa, static_cast<const E *>(bias), static_cast<E *>(y), y_stride};
-    return product<T, 2, 4, 8, 4>(p, px, static_cast<const E *>(w), nullptr, nullptr, end, stream);
+    const EndProject<T> end = {a, u, group, pa, static_cast<const E *>(bias), static_cast<E *>(y), y_stride};
+    const E *pw = static_cast<const E *>(w);
+    if (a.rows <= kFewRows) return few<T>(p, px, pw, end, stream);
+    return product<T, 2, 4, 8, 4>(p, px, pw, nullptr, nullptr, end, stream);
 }
 
 template <class T>
@@ -584,23 +781,25 @@ hipError_t head(const HeadArgs &h, const void *x, const void *w, hipStream_t str
 {
     typedef typename T::elem E;
     const HeadSpace sp = head_space(h.rows, h.features, h.workspace);
+    const bool small = h.rows <= kFewRows;
     uint32_t *list = nullptr, *count = nullptr;
-    if (h.targets) {
+    if (h.targets && !small) {
         list = sp.list;
         count = sp.count;
         k_counted<<<1, 1024, 0, stream>>>(h.targets, h.rows, list, count, h.logp, h.entropy);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
+    const E *px = static_cast<const E *>(x), *pw = static_cast<const E *>(w);
     for (uint64_t base = 0; base < h.rows; base += kHeadPlaces) {
         const uint64_t rows = h.rows - base < kHeadPlaces ? h.rows - base : kHeadPlaces;
         const ProductArgs p = {base, rows, h.x_stride, h.k, h.features};
         const EndHead end = {h.features, base, rows, h.targets, list, count, sp.m, sp.s, sp.t, sp.tl};
-        hipError_t e = product<T, 2, 4, 8, 4>(p, static_cast<const E *>(x), static_cast<const E *>(w),
-                                              list, count, end, stream);
+        hipError_t e = small ? few<T>(p, px, pw, end, stream)
+                             : product<T, 2, 4, 8, 4>(p, px, pw, list, count, end, stream);
         if (e != hipSuccess) return e;
-        k_head_join<<<(uint32_t)((rows + 63) / 64), 256, 0, stream>>>(
-            sp.m, sp.s, sp.t, sp.tl, (h.features + kHeadPart - 1) / kHeadPart, base, rows, list, count,
+        k_head_join<<<(uint32_t)((rows + 7) / 8), 1024, 0, stream>>>(
+            sp.m, sp.s, sp.t, sp.tl, (h.features + sp.part - 1) / sp.part, base, rows, list, count,
             h.targets, h.features, h.logp, h.entropy);
         e = hipGetLastError();
         if (e != hipSuccess) return e;

@@ -74,7 +74,7 @@ struct Row {
     }
 };
 
-constexpr uint64_t kFewRows = 512;
+constexpr uint64_t kTokenFewRows = 512;
 constexpr int kUnroll = 4;              // pieces a thread loads before it uses them
 constexpr uint32_t kCandidates = 2048;  // keys that the search for the alternatives can hold
 
@@ -372,7 +372,7 @@ hipError_t launch_token_logprobs(const void *logits, bool bf16, uint64_t rows, u
             p, vocab, stride, targets, logp, entropy, top_k, top_ids, top_logp);
     };
     const auto typed = [&](auto *p) {
-        if (rows <= kFewRows)
+        if (rows <= kTokenFewRows)
             launch(p, std::integral_constant<int, 1024>());
         else if (top_k)
             launch(p, std::integral_constant<int, 512>());

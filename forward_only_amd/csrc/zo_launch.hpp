@@ -157,11 +157,15 @@ struct AdapterArgs {
     const uint8_t *bits;           // n_probes packed rows over all adapters' parameters
     uint64_t bits_stride;
 };
-// Bytes of x A^T, [rows][rank] floats.
+// Rows that the product kernel for few rows takes, and the 16-feature fragments of one of its
+// workgroups: two where that still leaves two workgroups per CU.
+constexpr uint64_t kFewRows = 32;
+inline uint32_t few_fragments(uint32_t features) { return features >= 2 * 2 * 16 * 256 ? 2 : 1; }
+// Bytes of x A^T, [rows][rank] floats, and of each row's group.
 inline uint64_t adapter_u_bytes(uint64_t rows, uint32_t rank, uint32_t n_groups)
 {
     (void)n_groups;
-    return (rows * rank * 4 + 255) / 256 * 256;
+    return (rows * rank * 4 + rows * 4 + 255) / 256 * 256;
 }
 // u: adapter_u_bytes of workspace.
 hipError_t launch_adapter_project(const AdapterArgs &a, bool bf16, const void *x, uint64_t x_stride,
@@ -175,25 +179,26 @@ struct HeadArgs {
     float *logp, *entropy;
     void *workspace;
 };
-// Rows whose partial statistics are held at once, and the features of one partial.
+// Rows whose partial statistics are held at once.
 constexpr uint64_t kHeadPlaces = 16384;
-constexpr uint32_t kHeadPart = 128;
 struct HeadSpace {
     uint32_t *count, *list;
     float *m, *s, *t, *tl;
+    uint32_t part;             // features of one partial: a wave's in the product kernels
     uint64_t bytes;
 };
 inline HeadSpace head_space(uint64_t rows, uint32_t features, void *base)
 {
     const uint64_t places = rows < kHeadPlaces ? rows : kHeadPlaces;
-    const uint64_t parts = ((uint64_t)features + kHeadPart - 1) / kHeadPart;
+    HeadSpace s;
+    s.part = rows <= kFewRows ? 16 * few_fragments(features) : 128;
+    const uint64_t parts = ((uint64_t)features + s.part - 1) / s.part;
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {
         void *p = base ? static_cast<char *>(base) + at : nullptr;
         at += (bytes + 255) / 256 * 256;
         return p;
     };
-    HeadSpace s;
     s.count = static_cast<uint32_t *>(take(4));
     s.list = static_cast<uint32_t *>(take(rows * 4));
     s.m = static_cast<float *>(take(parts * places * 4));

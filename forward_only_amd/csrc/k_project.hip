@@ -563,6 +563,151 @@ __global__ __launch_bounds__(kWF * kWR * 64) void k_product(
     end(t, f0 + wf * kMF * 16, r0 + wr * kMR * 16);
 }
 
+// Many rows: 256 features x 256 rows by eight waves of 128 x 64, in which the two waves of a
+// SIMD take turns: four of the waves multiply while the other four read their next operands
+// from LDS, one barrier apart.  A step of 128 bytes of k has four such turns, one for each
+// quarter of a wave's tile:
+//   turn 0  reads features' first half and rows' first half   multiplies (F0, R0)
+//   turn 1  reads rows' second half                           multiplies (F0, R1)
+//   turn 2  reads features' second half                       multiplies (F1, R1)
+//   turn 3                                                    multiplies (F1, R0)
+// A quarter of the stage is free for the step after next as soon as both groups have read it,
+// so its loads go out one turn later and have about a step and a half to arrive; each turn
+// waits only for the loads that the next reader needs (counted waits, never all of them).
+// Loads past the end of k read zeros, so that the counts hold to the end.
+constexpr int kBigF = 256, kBigR = 256;
+
+// Wait until at most kLoads vector-memory loads are outstanding, and for all LDS reads if kLds.
+template <int kLoads, bool kLds>
+__device__ __forceinline__ void wait_for()
+{
+    __builtin_amdgcn_s_waitcnt((kLoads & 15) | (7 << 4) | ((kLds ? 0 : 15) << 8) | ((kLoads >> 4) << 14));
+}
+
+// A barrier that no LDS or global access moves across.
+__device__ __forceinline__ void turn_barrier()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+}
+
+template <class T, class End>
+__global__ __launch_bounds__(512, 2) void k_big(ProductArgs p, const typename T::elem *x,
+                                                const typename T::elem *w, const uint32_t *list,
+                                                const uint32_t *count, End end)
+{
+    constexpr int kPieces = 8;
+    constexpr uint32_t kStep = kPieces * T::kPiece;
+    constexpr int kPart = 128 * kPieces;                    // a quarter of a stage, in pieces
+    enum { F0, F1, R0, R1 };
+    extern __shared__ u32x4 stage[];                        // [2][F0, F1, R0, R1][128][kPieces]
+    const uint64_t rows = places(p.base, p.rows, count);
+    uint32_t tf, tr;
+    if (!tile_of(blockIdx.x, (p.features + kBigF - 1) / kBigF, (uint32_t)((rows + kBigR - 1) / kBigR),
+                 tf, tr))
+        return;
+    const uint32_t f0 = tf * kBigF;
+    const uint64_t r0 = (uint64_t)tr * kBigR;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l16 = lane & 15, q = lane >> 4;
+    const int wf = wave & 1, wr = wave >> 1;
+    // Staged row i holds its piece c at place c ^ (i / 2 % 8): sixteen rows read at one c then
+    // cover all banks once.  This wave stages rows 8 wave .. + 7 and 64 more of each quarter.
+    const uint32_t piece = (uint32_t)((lane & 7) ^ ((wave * 4 + (lane >> 4)) & 7)) * T::kPiece;
+    const typename T::elem *src[4][2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int i = j * 64 + wave * 8 + (lane >> 3);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t f = f0 + (i >> 6) * 128 + h * 64 + (i & 63);
+            src[F0 + h][j] = w + (uint64_t)(f < p.features ? f : p.features - 1) * p.k + piece;
+            const uint64_t at = r0 + (i >> 5) * 64 + h * 32 + (i & 31);
+            const uint64_t r = at < rows ? at : rows - 1;
+            src[R0 + h][j] = x + (list ? list[p.base + r] : p.base + r) * p.x_stride + piece;
+        }
+    }
+    const uint32_t steps = (p.k + kStep - 1) / kStep;
+    const auto issue = [&](int part, uint32_t step) {
+        const bool in = (uint64_t)step * kStep + piece < p.k;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const void *g = src[part][j] + (uint64_t)step * kStep;
+            if (!in) g = &kZeros;
+            u32x4 *l = stage + ((step & 1) * 4 + part) * kPart + (j * 64 + wave * 8) * kPieces;
+            __builtin_amdgcn_global_load_lds((gptr_t)g, (lptr_t)l, 16, 0, 0);
+        }
+    };
+    Tile<T, 8, 4> t;
+#pragma unroll
+    for (int m = 0; m < 8; ++m)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) t.acc[m][n] = f32x4{0, 0, 0, 0};
+    u32x4 ff[2][4], fr[2][2][2];
+    const auto read_f = [&](int part, uint32_t step) {
+        const u32x4 *s = stage + ((step & 1) * 4 + part) * kPart + (wf * 64 + l16) * kPieces;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) ff[c][m] = s[m * 16 * kPieces + ((4 * c + q) ^ (l16 >> 1))];
+    };
+    const auto read_r = [&](int h, uint32_t step) {
+        const u32x4 *s = stage + ((step & 1) * 4 + R0 + h) * kPart + (wr * 32 + l16) * kPieces;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) fr[h][c][n] = s[n * 16 * kPieces + ((4 * c + q) ^ (l16 >> 1))];
+    };
+    const auto multiply = [&](int hf, int hr) {
+        turn_barrier();
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+                    t.acc[4 * hf + m][2 * hr + n] =
+                        T::mma(ff[c][m], fr[hr][c][n], t.acc[4 * hf + m][2 * hr + n]);
+        __builtin_amdgcn_s_setprio(0);
+        turn_barrier();
+    };
+    for (uint32_t s = 0; s < 2; ++s) {
+        issue(F0, s);
+        issue(R0, s);
+        issue(R1, s);
+        issue(F1, s);
+    }
+    wait_for<12, false>();
+    turn_barrier();
+    if (wave >= 4) turn_barrier();              // one turn behind from here on
+    for (uint32_t s = 0; s < steps; ++s) {
+        read_f(F0, s);
+        read_r(0, s);
+        wait_for<10, true>();                   // R1 of this step
+        multiply(0, 0);
+        read_r(1, s);
+        issue(F0, s + 2);
+        issue(R0, s + 2);
+        wait_for<12, true>();                   // F1 of this step
+        multiply(0, 1);
+        read_f(F1, s);
+        issue(R1, s + 2);
+        wait_for<63, true>();
+        multiply(1, 1);
+        issue(F1, s + 2);
+        wait_for<12, false>();                  // F0 and R0 of the next step
+        multiply(1, 0);
+    }
+    if (wave < 4) turn_barrier();
+    wait_for<0, true>();
+    end(t, f0 + wf * 128, r0 + wr * 64);
+}
+
 // Few rows.  What bounds the product is reading w once, so w goes straight from memory into
 // registers: a workgroup takes 16 kMF features and all rows, its eight waves split k in
 // interleaved blocks of kRun fragments (256 contiguous bytes of each bf16 row), and the waves'
@@ -728,12 +873,14 @@ hipError_t product(const ProductArgs &p, const typename T::elem *x, const typena
     return hipGetLastError();
 }
 
-template <class T, int kWF, int kWR, int kMF, int kMR, class End>
-hipError_t raise_lds_limit()
+template <class T, class End>
+hipError_t big(const ProductArgs &p, const typename T::elem *x, const typename T::elem *w,
+               const uint32_t *list, const uint32_t *count, const End &end, hipStream_t stream)
 {
-    return hipFuncSetAttribute(
-        reinterpret_cast<const void *>(&k_product<T, kWF, kWR, kMF, kMR, End>),
-        hipFuncAttributeMaxDynamicSharedMemorySize, 2 * (kWF * kMF + kWR * kMR) * 16 * 128);
+    const uint64_t n = (((uint64_t)p.features + kBigF - 1) / kBigF) * ((p.rows + kBigR - 1) / kBigR);
+    if (n > 0x7FFFFFFFull - 8) return hipErrorInvalidValue;
+    k_big<T, End><<<(uint32_t)((n + 7) / 8 * 8), 512, 2 * 512 * 128, stream>>>(p, x, w, list, count, end);
+    return hipGetLastError();
 }
 
 // The product of at most kFewRows rows: features per workgroup by how many workgroups that
@@ -773,7 +920,7 @@ hipError_t project(const AdapterArgs &a, const void *x, uint64_t x_stride, const
     const EndProject<T> end = {a, u, group, pa, static_cast<const E *>(bias), static_cast<E *>(y), y_stride};
     const E *pw = static_cast<const E *>(w);
     if (a.rows <= kFewRows) return few<T>(p, px, pw, end, stream);
-    return product<T, 2, 4, 8, 4>(p, px, pw, nullptr, nullptr, end, stream);
+    return big<T>(p, px, pw, nullptr, nullptr, end, stream);
 }
 
 template <class T>
@@ -796,7 +943,7 @@ hipError_t head(const HeadArgs &h, const void *x, const void *w, hipStream_t str
         const ProductArgs p = {base, rows, h.x_stride, h.k, h.features};
         const EndHead end = {h.features, base, rows, h.targets, list, count, sp.m, sp.s, sp.t, sp.tl};
         hipError_t e = small ? few<T>(p, px, pw, end, stream)
-                             : product<T, 2, 4, 8, 4>(p, px, pw, list, count, end, stream);
+                             : big<T>(p, px, pw, list, count, end, stream);
         if (e != hipSuccess) return e;
         k_head_join<<<(uint32_t)((rows + 7) / 8), 1024, 0, stream>>>(
             sp.m, sp.s, sp.t, sp.tl, (h.features + sp.part - 1) / sp.part, base, rows, list, count,
@@ -810,9 +957,12 @@ hipError_t head(const HeadArgs &h, const void *x, const void *w, hipStream_t str
 template <class T>
 hipError_t prepare()
 {
-    hipError_t e = raise_lds_limit<T, 2, 4, 8, 4, EndProject<T>>();
-    if (e == hipSuccess) e = raise_lds_limit<T, 2, 4, 8, 4, EndHead>();
-    return e;
+    const auto raise = [](auto *kernel, int bytes) {
+        return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                   hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    };
+    const hipError_t e = raise(&k_big<T, EndProject<T>>, 2 * 512 * 128);
+    return e == hipSuccess ? raise(&k_big<T, EndHead>, 2 * 512 * 128) : e;
 }
 
 }  // namespace

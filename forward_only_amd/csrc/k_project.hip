@@ -567,14 +567,14 @@ __global__ __launch_bounds__(kWF * kWR * 64) void k_product(
 // SIMD take turns: four of the waves multiply while the other four read their next operands
 // from LDS, one barrier apart.  A step of 128 bytes of k has four such turns, one for each
 // quarter of a wave's tile:
-//   turn 0  reads features' first half and rows' first half   multiplies (F0, R0)
-//   turn 1  reads rows' second half                           multiplies (F0, R1)
-//   turn 2  reads features' second half                       multiplies (F1, R1)
-//   turn 3                                                    multiplies (F1, R0)
+//   turn 0  reads F0, the first half of its features        multiplies (F0, R0)
+//   turn 1  reads F1, the second half                       multiplies (F1, R0)
+//   turn 2  reads R1, the second half of its rows           multiplies (F1, R1)
+//   turn 3  reads R0, the first half, of the next step      multiplies (F0, R1)
 // A quarter of the stage is free for the step after next as soon as both groups have read it,
-// so its loads go out one turn later and have about a step and a half to arrive; each turn
-// waits only for the loads that the next reader needs (counted waits, never all of them).
-// Loads past the end of k read zeros, so that the counts hold to the end.
+// so its loads go out one turn later and have one and a half steps to arrive; each turn waits
+// for the loads that the next turn reads: all but the twelve issued since.  Loads past the end
+// of k read zeros, so that the counts hold to the end.
 constexpr int kBigF = 256, kBigR = 256;
 
 // Wait until at most kLoads vector-memory loads are outstanding, and for all LDS reads if kLds.
@@ -647,13 +647,13 @@ __global__ __launch_bounds__(512, 2) void k_big(ProductArgs p, const typename T:
     for (int m = 0; m < 8; ++m)
 #pragma unroll
         for (int n = 0; n < 4; ++n) t.acc[m][n] = f32x4{0, 0, 0, 0};
-    u32x4 ff[2][4], fr[2][2][2];
-    const auto read_f = [&](int part, uint32_t step) {
-        const u32x4 *s = stage + ((step & 1) * 4 + part) * kPart + (wf * 64 + l16) * kPieces;
+    u32x4 ff[2][2][4], fr[2][2][2];             // [half][c][fragment]
+    const auto read_f = [&](int h, uint32_t step) {
+        const u32x4 *s = stage + ((step & 1) * 4 + F0 + h) * kPart + (wf * 64 + l16) * kPieces;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int m = 0; m < 4; ++m) ff[c][m] = s[m * 16 * kPieces + ((4 * c + q) ^ (l16 >> 1))];
+            for (int m = 0; m < 4; ++m) ff[h][c][m] = s[m * 16 * kPieces + ((4 * c + q) ^ (l16 >> 1))];
     };
     const auto read_r = [&](int h, uint32_t step) {
         const u32x4 *s = stage + ((step & 1) * 4 + R0 + h) * kPart + (wr * 32 + l16) * kPieces;
@@ -663,6 +663,7 @@ __global__ __launch_bounds__(512, 2) void k_big(ProductArgs p, const typename T:
             for (int n = 0; n < 2; ++n) fr[h][c][n] = s[n * 16 * kPieces + ((4 * c + q) ^ (l16 >> 1))];
     };
     const auto multiply = [&](int hf, int hr) {
+        wait_for<12, true>();
         turn_barrier();
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
@@ -672,36 +673,35 @@ __global__ __launch_bounds__(512, 2) void k_big(ProductArgs p, const typename T:
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
                     t.acc[4 * hf + m][2 * hr + n] =
-                        T::mma(ff[c][m], fr[hr][c][n], t.acc[4 * hf + m][2 * hr + n]);
+                        T::mma(ff[hf][c][m], fr[hr][c][n], t.acc[4 * hf + m][2 * hr + n]);
         __builtin_amdgcn_s_setprio(0);
         turn_barrier();
     };
     for (uint32_t s = 0; s < 2; ++s) {
-        issue(F0, s);
         issue(R0, s);
-        issue(R1, s);
+        issue(F0, s);
         issue(F1, s);
+        issue(R1, s);
     }
-    wait_for<12, false>();
+    wait_for<12, false>();                      // R0 and F0 of step 0
+    turn_barrier();
+    read_r(0, 0);
+    wait_for<63, true>();
     turn_barrier();
     if (wave >= 4) turn_barrier();              // one turn behind from here on
     for (uint32_t s = 0; s < steps; ++s) {
-        read_f(F0, s);
-        read_r(0, s);
-        wait_for<10, true>();                   // R1 of this step
-        multiply(0, 0);
-        read_r(1, s);
-        issue(F0, s + 2);
+        read_f(0, s);
         issue(R0, s + 2);
-        wait_for<12, true>();                   // F1 of this step
-        multiply(0, 1);
-        read_f(F1, s);
-        issue(R1, s + 2);
-        wait_for<63, true>();
-        multiply(1, 1);
-        issue(F1, s + 2);
-        wait_for<12, false>();                  // F0 and R0 of the next step
+        multiply(0, 0);
+        read_f(1, s);
+        issue(F0, s + 2);
         multiply(1, 0);
+        read_r(1, s);
+        issue(F1, s + 2);
+        multiply(1, 1);
+        read_r(0, s + 1);
+        issue(R1, s + 2);
+        multiply(0, 1);
     }
     if (wave < 4) turn_barrier();
     wait_for<0, true>();

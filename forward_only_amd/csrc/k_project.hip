@@ -12,12 +12,15 @@
 // feed four successive 16x16x4 products, which pairs the same k of both operands.
 #include <math.h>
 
+#include <type_traits>
+
 #include "zo_lm.hpp"
 
 namespace zo {
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
@@ -30,6 +33,11 @@ struct Bf16 {
     static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c)
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                        __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
     }
     static __device__ __forceinline__ float widen(uint16_t v) { return bf16lo_to_f32(v); }
@@ -65,7 +73,8 @@ struct Bf16 {
         }
         return w;
     }
-    static __device__ __forceinline__ f32x4 mma(u32x4 a, const Wide &b, f32x4 c)
+    template <class Acc>
+    static __device__ __forceinline__ Acc mma(u32x4 a, const Wide &b, Acc c)
     {
         return mma(a, b.hi, mma(a, b.lo, c));
     }
@@ -79,6 +88,14 @@ struct Fp32 {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[i]), __uint_as_float(b[i]),
+                                                     c, 0, 0, 0);
+        return c;
+    }
+    static __device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[i]), __uint_as_float(b[i]),
                                                      c, 0, 0, 0);
         return c;
     }
@@ -238,10 +255,25 @@ __device__ __forceinline__ uint64_t places(uint64_t base, uint64_t rows, const u
     return n <= base ? 0 : (n - base < rows ? n - base : rows);
 }
 
-// Accumulators of one wave: kMF x kMR fragments of 16 features x 16 rows.
-template <class T, int kMF, int kMR>
+// Accumulators of one wave: kMF x kMR fragments of kSide features x kSide rows (16 or 32).
+// Lane l holds row l % kSide of a fragment; its value i belongs to feature
+// 8 (i / 4) + 4 (l / kSide) + i % 4.
+template <class T, int kSideOf, int kMFOf, int kMROf>
 struct Tile {
-    f32x4 acc[kMF][kMR];
+    static constexpr int kSide = kSideOf, kMF = kMFOf, kMR = kMROf;
+    static constexpr int kFours = kSide == 16 ? 1 : 4;      // runs of four features of a lane
+    static constexpr int kReach = 64 / kSide;               // 16-byte pieces of k per fragment
+    typedef std::conditional_t<kSide == 16, f32x4, f32x16> Acc;
+    Acc acc[kMF][kMR];
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int m = 0; m < kMF; ++m)
+#pragma unroll
+            for (int n = 0; n < kMR; ++n)
+#pragma unroll
+                for (int i = 0; i < 4 * kFours; ++i) acc[m][n][i] = 0.0f;
+    }
 };
 
 // Ending of zo_adapter_project.
@@ -254,18 +286,36 @@ struct EndProject {
     typename T::elem *y;
     uint64_t y_stride;
 
-    // Many rows: the groups that meet the tile one after another, on MFMA.
-    template <int kMF, int kMR>
-    __device__ __forceinline__ void operator()(Tile<T, kMF, kMR> &t, uint32_t f0, uint64_t r0) const
+    // The last group that starts at or before row r0 (else the first): all lanes look at once,
+    // 64 starts a round.
+    __device__ __forceinline__ uint32_t begin(uint64_t r0) const
     {
-        add_groups(t, f0, r0);
-        store(t, f0, r0);
+        const uint32_t lane = threadIdx.x & 63;
+        uint32_t g = 0, n = a.n_groups;
+        while (n > 1) {
+            const uint32_t step = (n + 63) / 64, at = lane * step;
+            const uint64_t below = __ballot(at < n && clamp_row(a.starts[g + (at < n ? at : 0)], a.rows) <= r0);
+            const uint32_t skip = below ? (__popcll(below) - 1) * step : 0;
+            g += skip;
+            n = n - skip < step ? n - skip : step;
+            if (!below) break;
+        }
+        return __builtin_amdgcn_readfirstlane(g);
+    }
+
+    // Many rows: the groups that meet the tile one after another, on MFMA.  `lds`: 8 KiB of
+    // this wave's own.
+    template <class Tl>
+    __device__ __forceinline__ void finish(Tl &t, uint32_t g, uint32_t f0, uint64_t r0, u32x4 *lds) const
+    {
+        add_groups(t, g, f0, r0);
+        store_rows(t, f0, r0, lds);
     }
 
     // Few rows, each perhaps with an adapter of its own: every lane the products of its row, so
     // that one round of loads serves all groups.
     template <int kMF>
-    __device__ __forceinline__ void add_rows(Tile<T, kMF, 1> &t, uint32_t f0, uint64_t r0) const
+    __device__ __forceinline__ void add_rows(Tile<T, 16, kMF, 1> &t, uint32_t f0, uint64_t r0) const
     {
         const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
         const uint64_t row = r0 + l16;
@@ -303,20 +353,12 @@ struct EndProject {
         }
     }
 
-    template <int kMF, int kMR>
-    __device__ __forceinline__ void add_groups(Tile<T, kMF, kMR> &t, uint32_t f0, uint64_t r0) const
+    template <class Tl>
+    __device__ __forceinline__ void add_groups(Tl &t, uint32_t g, uint32_t f0, uint64_t r0) const
     {
-        const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
-        const uint64_t r1 = r0 + 16 * kMR < a.rows ? r0 + 16 * kMR : a.rows;
-        // groups that meet rows [r0, r1): from the last one that starts at or before r0
-        uint32_t g = 0, top = a.n_groups;
-        while (top - g > 1) {
-            const uint32_t mid = g + (top - g) / 2;
-            if (clamp_row(a.starts[mid], a.rows) <= r0)
-                g = mid;
-            else
-                top = mid;
-        }
+        constexpr int kSide = Tl::kSide, kMF = Tl::kMF, kMR = Tl::kMR;
+        const int lane = threadIdx.x & 63, l = lane % kSide, q = lane / kSide;
+        const uint64_t r1 = r0 + kSide * kMR < a.rows ? r0 + kSide * kMR : a.rows;
         for (; g < a.n_groups; ++g) {
             const uint64_t s = clamp_row(a.starts[g], a.rows), e = clamp_row(a.starts[g + 1], a.rows);
             if (s >= r1) break;
@@ -325,7 +367,7 @@ struct EndProject {
             if (gr.bad) {
 #pragma unroll
                 for (int n = 0; n < kMR; ++n) {
-                    const uint64_t row = r0 + 16 * n + l16;
+                    const uint64_t row = r0 + kSide * n + l;
                     const float nan = row >= s && row < e ? __builtin_nanf("") : 0.0f;
 #pragma unroll
                     for (int m = 0; m < kMF; ++m) t.acc[m][n] += nan;
@@ -334,12 +376,12 @@ struct EndProject {
             if (gr.none) continue;
             // The product is formed apart and added to the group's own rows, so that a NaN in
             // its adapter does not reach the others through 0 * NaN.
-            for (uint32_t j0 = 0; j0 < a.rank; j0 += 4 * T::kPiece) {
+            for (uint32_t j0 = 0; j0 < a.rank; j0 += Tl::kReach * T::kPiece) {
                 const uint32_t j = j0 + q * T::kPiece;
                 typename T::Wide v[kMR];
 #pragma unroll
                 for (int n = 0; n < kMR; ++n) {
-                    const uint64_t row = r0 + 16 * n + l16;
+                    const uint64_t row = r0 + kSide * n + l;
                     const bool in = row >= s && row < e && j < a.rank;
                     const f32x4 *pu = reinterpret_cast<const f32x4 *>(u + row * a.rank + j);
                     float z[T::kPiece];
@@ -353,7 +395,7 @@ struct EndProject {
                 }
 #pragma unroll
                 for (int m = 0; m < kMF; ++m) {
-                    const uint32_t f = f0 + 16 * m + l16;
+                    const uint32_t f = f0 + kSide * m + l;
                     u32x4 fb = kZeros;
                     if (j < a.rank && f < a.d_out) {
                         const uint64_t at = gr.base + (uint64_t)a.rank * a.d_in +
@@ -363,12 +405,13 @@ struct EndProject {
                     }
 #pragma unroll
                     for (int n = 0; n < kMR; ++n) {
-                        const uint64_t row = r0 + 16 * n + l16;
-                        if (r0 + 16 * n + 16 <= s || r0 + 16 * n >= e) continue;
+                        const uint64_t row = r0 + kSide * n + l;
+                        if (r0 + kSide * n + kSide <= s || r0 + kSide * n >= e) continue;
                         const bool in = row >= s && row < e;
-                        const f32x4 add = T::mma(fb, v[n], f32x4{0, 0, 0, 0});
+                        typename Tl::Acc zero = {};
+                        const typename Tl::Acc add = T::mma(fb, v[n], zero);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
+                        for (int i = 0; i < 4 * Tl::kFours; ++i)
                             t.acc[m][n][i] = in ? t.acc[m][n][i] + add[i] : t.acc[m][n][i];
                     }
                 }
@@ -376,24 +419,76 @@ struct EndProject {
         }
     }
 
-    template <int kMF, int kMR>
-    __device__ __forceinline__ void store(Tile<T, kMF, kMR> &t, uint32_t f0, uint64_t r0) const
+    template <class Tl>
+    __device__ __forceinline__ void store(Tl &t, uint32_t f0, uint64_t r0) const
     {
-        const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+        constexpr int kSide = Tl::kSide, kMF = Tl::kMF, kMR = Tl::kMR;
+        const int lane = threadIdx.x & 63, l = lane % kSide, q = lane / kSide;
         const uint64_t lo = clamp_row(a.starts[0], a.rows);
         const uint64_t hi = clamp_row(a.starts[a.n_groups], a.rows);
 #pragma unroll
         for (int n = 0; n < kMR; ++n) {
-            const uint64_t row = r0 + 16 * n + l16;
+            const uint64_t row = r0 + kSide * n + l;
             if (row < lo || row >= hi) continue;
 #pragma unroll
-            for (int m = 0; m < kMF; ++m) {
+            for (int m = 0; m < kMF; ++m)
+#pragma unroll
+                for (int o = 0; o < Tl::kFours; ++o) {
+                    const uint32_t f = f0 + kSide * m + 8 * o + 4 * q;
+                    if (f >= a.d_out) continue;
+                    f32x4 v;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        v[i] = t.acc[m][n][4 * o + i];
+                        if (bias) v[i] += T::widen(bias[f + i]);
+                    }
+                    store4(y + row * y_stride + f, v);
+                }
+        }
+    }
+    // The same through LDS, 16 rows at a time: a lane then stores 16 bytes next to its
+    // neighbours', whole lines of y instead of 8 bytes of each of 16 rows.  Row i keeps its
+    // piece c at place c ^ i.
+    template <class Tl>
+    __device__ __forceinline__ void store_rows(Tl &t, uint32_t f0, uint64_t r0, u32x4 *lds) const
+    {
+        constexpr int kMF = Tl::kMF, kMR = Tl::kMR;
+        static_assert(Tl::kSide == 16, "lanes of 16 rows");
+        constexpr int kRowPieces = 16 * kMF / T::kPiece, kAtOnce = 64 / kRowPieces;
+        const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+        const uint64_t lo = clamp_row(a.starts[0], a.rows);
+        const uint64_t hi = clamp_row(a.starts[a.n_groups], a.rows);
+        float add[kMF][4];
+#pragma unroll
+        for (int m = 0; m < kMF; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
                 const uint32_t f = f0 + 16 * m + 4 * q;
-                if (f >= a.d_out) continue;
-                f32x4 v = t.acc[m][n];
-                if (bias)
-                    for (int i = 0; i < 4; ++i) v[i] += T::widen(bias[f + i]);
-                store4(y + row * y_stride + f, v);
+                add[m][i] = bias && f < a.d_out ? T::widen(bias[f + i]) : 0.0f;
+            }
+        const int piece = lane % kRowPieces;
+        const uint32_t f = f0 + piece * T::kPiece;
+#pragma unroll
+        for (int n = 0; n < kMR; ++n) {
+            wave_lds_sync();
+#pragma unroll
+            for (int m = 0; m < kMF; ++m) {
+                f32x4 v;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = t.acc[m][n][i] + add[m][i];
+                const int four = 4 * m + q, c = four * 4 / T::kPiece;
+                typename T::elem *at = reinterpret_cast<typename T::elem *>(
+                    lds + l16 * kRowPieces + (c ^ l16)) + four * 4 % T::kPiece;
+                store4(at, v);
+            }
+            wave_lds_sync();
+#pragma unroll
+            for (int i = 0; i < 16; i += kAtOnce) {
+                const int r = i + lane / kRowPieces;
+                const uint64_t row = r0 + 16 * n + r;
+                const u32x4 v = lds[r * kRowPieces + (piece ^ r)];
+                if (row >= lo && row < hi && f < a.d_out)
+                    *reinterpret_cast<u32x4 *>(y + row * y_stride + f) = v;
             }
         }
     }
@@ -414,47 +509,58 @@ struct EndHead {
     float *m, *s, *t;           // [wave tile][place]
     float *tl;                  // logit of each place's target
 
-    template <class T, int kMF>
-    __device__ __forceinline__ void add_rows(Tile<T, kMF, 1> &, uint32_t, uint64_t) const {}
-    template <class T, int kMF>
-    __device__ __forceinline__ void store(Tile<T, kMF, 1> &t4, uint32_t f0, uint64_t r0) const
+    template <class Tl>
+    __device__ __forceinline__ void add_rows(Tl &, uint32_t, uint64_t) const {}
+    __device__ __forceinline__ uint32_t begin(uint64_t) const { return 0; }
+    template <class Tl>
+    __device__ __forceinline__ void finish(Tl &tile, uint32_t, uint32_t f0, uint64_t r0, u32x4 *) const
     {
-        (*this)(t4, f0, r0);
+        store(tile, f0, r0);
     }
 
-    template <class T, int kMF, int kMR>
-    __device__ __forceinline__ void operator()(Tile<T, kMF, kMR> &t4, uint32_t f0, uint64_t r0) const
+    template <class Tl>
+    __device__ __forceinline__ void store(Tl &tile, uint32_t f0, uint64_t r0) const
     {
-        const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
-        const uint32_t part = f0 / (16 * kMF);
+        constexpr int kSide = Tl::kSide, kMF = Tl::kMF, kMR = Tl::kMR;
+        const int lane = threadIdx.x & 63, l = lane % kSide, q = lane / kSide;
+        const uint32_t part = f0 / (kSide * kMF);
         if (f0 >= features) return;
         const uint64_t have = places(base, rows, count);
 #pragma unroll
         for (int n = 0; n < kMR; ++n) {
-            const uint64_t at = r0 + 16 * n + l16;
+            const uint64_t at = r0 + kSide * n + l;
             SoftStats st = SoftStats::empty();
             int64_t tgt = -1;
             if (targets && at < have) tgt = targets[list ? list[base + at] : base + at];
+            const auto feature = [&](int m4, int i) { return f0 + kSide * m4 + 8 * (i / 4) + 4 * q + i % 4; };
+            if (f0 + kSide * kMF > features) {
+#pragma unroll
+                for (int m4 = 0; m4 < kMF; ++m4)
+#pragma unroll
+                    for (int i = 0; i < 4 * Tl::kFours; ++i)
+                        if (feature(m4, i) >= features) tile.acc[m4][n][i] = -INFINITY;
+            }
             float top = -INFINITY;
 #pragma unroll
             for (int m4 = 0; m4 < kMF; ++m4)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t f = f0 + 16 * m4 + 4 * q + i;
-                    if (f < features) top = fmaxf(top, t4.acc[m4][n][i]);
-                }
+                for (int i = 0; i < 4 * Tl::kFours; ++i) top = fmaxf(top, tile.acc[m4][n][i]);
             st.raise(top);
 #pragma unroll
             for (int m4 = 0; m4 < kMF; ++m4)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t f = f0 + 16 * m4 + 4 * q + i;
-                    if (f < features) {
-                        st.add(t4.acc[m4][n][i]);
-                        if ((int64_t)f == tgt && at < have) tl[at] = t4.acc[m4][n][i];
-                    }
-                }
-            st.wave_merge(32, 16);
+                for (int i = 0; i < 4 * Tl::kFours; ++i) st.add(tile.acc[m4][n][i]);
+            // few waves hold a row's target
+            const uint32_t in = (uint32_t)(tgt - f0);
+            const bool here = at < have && tgt >= (int64_t)f0 && tgt < (int64_t)features && in < kSide * kMF;
+            if (__any(here)) {
+#pragma unroll
+                for (int m4 = 0; m4 < kMF; ++m4)
+#pragma unroll
+                    for (int i = 0; i < 4 * Tl::kFours; ++i)
+                        if (here && feature(m4, i) - f0 == in) tl[at] = tile.acc[m4][n][i];
+            }
+            st.wave_merge(32, kSide);
             if (q == 0 && at < have) {
                 m[(uint64_t)part * rows + at] = st.m;
                 s[(uint64_t)part * rows + at] = st.s;
@@ -484,84 +590,6 @@ __device__ __forceinline__ bool tile_of(uint32_t b, uint32_t nf, uint32_t nr, ui
 
 typedef const __attribute__((address_space(1))) void *gptr_t;
 typedef __attribute__((address_space(3))) void *lptr_t;
-
-template <class T, int kWF, int kWR, int kMF, int kMR, class End>
-__global__ __launch_bounds__(kWF * kWR * 64) void k_product(
-    ProductArgs p, const typename T::elem *x, const typename T::elem *w, const uint32_t *list,
-    const uint32_t *count, End end)
-{
-    constexpr int kWaves = kWF * kWR;
-    constexpr int kF = kWF * kMF * 16, kR = kWR * kMR * 16;
-    constexpr int kPieces = 8;                              // 16-byte pieces of a staged row
-    constexpr uint32_t kStep = kPieces * T::kPiece;
-    constexpr int kLoads = (kF + kR) / 8 / kWaves;          // 8 rows of 128 bytes per wave load
-    static_assert((kF + kR) % (8 * kWaves) == 0 && kF % 8 == 0, "whole loads");
-    extern __shared__ u32x4 stage[];                        // [2][kF + kR][kPieces]
-    const uint64_t rows = places(p.base, p.rows, count);
-    uint32_t tf, tr;
-    if (!tile_of(blockIdx.x, (p.features + kF - 1) / kF, (uint32_t)((rows + kR - 1) / kR), tf, tr))
-        return;
-    const uint32_t f0 = tf * kF;
-    const uint64_t r0 = (uint64_t)tr * kR;
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int l16 = lane & 15, q = lane >> 4;
-    const int wf = wave % kWF, wr = wave / kWF;
-    // Staged row i holds its piece c at place c ^ (i / 2 % 8): sixteen rows read at one c then
-    // cover all banks once.
-    const typename T::elem *src[kLoads];
-    uint32_t piece[kLoads];
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-        const int at = (i * kWaves + wave) * 8 + (lane >> 3);
-        piece[i] = ((lane & 7) ^ (at >> 1 & 7)) * T::kPiece;
-        if (at < kF) {
-            const uint32_t f = f0 + at < p.features ? f0 + at : p.features - 1;
-            src[i] = w + (uint64_t)f * p.k + piece[i];
-        } else {
-            const uint64_t r = r0 + (at - kF) < rows ? r0 + (at - kF) : rows - 1;
-            src[i] = x + (list ? list[p.base + r] : p.base + r) * p.x_stride + piece[i];
-        }
-    }
-    const auto issue = [&](uint32_t k0, int buf) {
-        const bool tail = k0 + kStep > p.k;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const void *g = src[i] + k0;
-            if (tail && k0 + piece[i] >= p.k) g = &kZeros;
-            u32x4 *l = stage + (buf * (kF + kR) + (i * kWaves + wave) * 8) * kPieces;
-            __builtin_amdgcn_global_load_lds((gptr_t)g, (lptr_t)l, 16, 0, 0);
-        }
-    };
-    Tile<T, kMF, kMR> t;
-#pragma unroll
-    for (int m = 0; m < kMF; ++m)
-#pragma unroll
-        for (int n = 0; n < kMR; ++n) t.acc[m][n] = f32x4{0, 0, 0, 0};
-    issue(0, 0);
-    __syncthreads();
-    int buf = 0;
-    for (uint32_t k0 = 0; k0 < p.k; k0 += kStep) {
-        if (k0 + kStep < p.k) issue(k0 + kStep, buf ^ 1);
-        const u32x4 *sw = stage + buf * (kF + kR) * kPieces, *sx = sw + kF * kPieces;
-#pragma unroll
-        for (int c = 0; c < kPieces / 4; ++c) {
-            u32x4 fa[kMF], fb[kMR];
-            const int at = (4 * c + q) ^ (l16 >> 1);
-#pragma unroll
-            for (int m = 0; m < kMF; ++m) fa[m] = sw[((wf * kMF + m) * 16 + l16) * kPieces + at];
-#pragma unroll
-            for (int n = 0; n < kMR; ++n) fb[n] = sx[((wr * kMR + n) * 16 + l16) * kPieces + at];
-#pragma unroll
-            for (int m = 0; m < kMF; ++m)
-#pragma unroll
-                for (int n = 0; n < kMR; ++n) t.acc[m][n] = T::mma(fa[m], fb[n], t.acc[m][n]);
-        }
-        __syncthreads();
-        buf ^= 1;
-    }
-    end(t, f0 + wf * kMF * 16, r0 + wr * kMR * 16);
-}
 
 // Many rows: 256 features x 256 rows by eight waves of 128 x 64, in which the two waves of a
 // SIMD take turns: four of the waves multiply while the other four read their next operands
@@ -642,11 +670,8 @@ __global__ __launch_bounds__(512, 2) void k_big(ProductArgs p, const typename T:
             __builtin_amdgcn_global_load_lds((gptr_t)g, (lptr_t)l, 16, 0, 0);
         }
     };
-    Tile<T, 8, 4> t;
-#pragma unroll
-    for (int m = 0; m < 8; ++m)
-#pragma unroll
-        for (int n = 0; n < 4; ++n) t.acc[m][n] = f32x4{0, 0, 0, 0};
+    Tile<T, 16, 8, 4> t;
+    t.clear();
     u32x4 ff[2][2][4], fr[2][2][2];             // [half][c][fragment]
     const auto read_f = [&](int h, uint32_t step) {
         const u32x4 *s = stage + ((step & 1) * 4 + F0 + h) * kPart + (wf * 64 + l16) * kPieces;
@@ -677,11 +702,14 @@ __global__ __launch_bounds__(512, 2) void k_big(ProductArgs p, const typename T:
         __builtin_amdgcn_s_setprio(0);
         turn_barrier();
     };
+    uint32_t begun = 0;
+#pragma unroll
     for (uint32_t s = 0; s < 2; ++s) {
         issue(R0, s);
         issue(F0, s);
         issue(F1, s);
         issue(R1, s);
+        if (s == 0) begun = end.begin(r0 + wr * 64);
     }
     wait_for<12, false>();                      // R0 and F0 of step 0
     turn_barrier();
@@ -705,7 +733,8 @@ __global__ __launch_bounds__(512, 2) void k_big(ProductArgs p, const typename T:
     }
     if (wave < 4) turn_barrier();
     wait_for<0, true>();
-    end(t, f0 + wf * 128, r0 + wr * 64);
+    turn_barrier();                             // the stage is free: no load is under way
+    end.finish(t, begun, f0 + wf * 128, r0 + wr * 64, stage + wave * 512);
 }
 
 // Few rows.  What bounds the product is reading w once, so w goes straight from memory into
@@ -734,11 +763,8 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_few(ProductArgs p, const typ
         const uint64_t r = (uint64_t)(16 * n + l16) < p.rows ? 16 * n + l16 : p.rows - 1;
         px[n] = x + r * p.x_stride + q * T::kPiece;
     }
-    Tile<T, kMF, kMR> t;
-#pragma unroll
-    for (int m = 0; m < kMF; ++m)
-#pragma unroll
-        for (int n = 0; n < kMR; ++n) t.acc[m][n] = f32x4{0, 0, 0, 0};
+    Tile<T, 16, kMF, kMR> t;
+    t.clear();
     const uint32_t stride = kFewWaves * kRun * kStep;
     uint32_t k0 = wave * kRun * kStep;
     for (; k0 + kRun * kStep <= p.k; k0 += stride) {
@@ -777,7 +803,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_few(ProductArgs p, const typ
         for (int n = 0; n < kMR; ++n) sums[wave][m][n][lane] = t.acc[m][n];
     __syncthreads();
     if (wave >= kMR) return;
-    Tile<T, kMF, 1> own;
+    Tile<T, 16, kMF, 1> own;
 #pragma unroll
     for (int m = 0; m < kMF; ++m) {
         own.acc[m][0] = sums[0][m][wave][lane];
@@ -859,19 +885,6 @@ __global__ __launch_bounds__(1024) void k_head_join(const float *m, const float 
 }
 
 // ---- launches ---------------------------------------------------------------------------
-
-template <class T, int kWF, int kWR, int kMF, int kMR, class End>
-hipError_t product(const ProductArgs &p, const typename T::elem *x, const typename T::elem *w,
-                   const uint32_t *list, const uint32_t *count, const End &end, hipStream_t stream)
-{
-    const uint64_t nf = (p.features + kWF * kMF * 16 - 1) / (kWF * kMF * 16);
-    const uint64_t nr = (p.rows + kWR * kMR * 16 - 1) / (kWR * kMR * 16);
-    if (nf * nr > 0x7FFFFFFFull) return hipErrorInvalidValue;
-    constexpr uint32_t lds = 2 * (kWF * kMF + kWR * kMR) * 16 * 128;
-    k_product<T, kWF, kWR, kMF, kMR, End>
-        <<<(uint32_t)((nf * nr + 7) / 8 * 8), kWF * kWR * 64, lds, stream>>>(p, x, w, list, count, end);
-    return hipGetLastError();
-}
 
 template <class T, class End>
 hipError_t big(const ProductArgs &p, const typename T::elem *x, const typename T::elem *w,

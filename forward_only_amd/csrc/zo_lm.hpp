@@ -34,13 +34,13 @@ struct SoftStats {
             m = top;
         }
     }
-    // Add x <= m (or NaN).
+    // Add x <= m (or NaN).  The bound on d keeps 0 * -inf out of t: e is 0 far above it.
     __device__ __forceinline__ void add(float x)
     {
         const float d = x - (m == -INFINITY ? 0.0f : m);
         const float e = fast_exp(d);
         s += e;
-        t = e > 0.0f ? fmaf(e, d, t) : t;
+        t = fmaf(e, fmaxf(d, -1e4f), t);
     }
     __device__ __forceinline__ void merge(const SoftStats &o)
     {

@@ -41,6 +41,14 @@ struct Bf16 {
                                                        __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
     }
     static __device__ __forceinline__ float widen(uint16_t v) { return bf16lo_to_f32(v); }
+    static __device__ __forceinline__ void load4(const uint16_t *p, float *v)
+    {
+        const uint2 w = *reinterpret_cast<const uint2 *>(p);
+        v[0] = bf16lo_to_f32(w.x);
+        v[1] = bf16hi_to_f32(w.x);
+        v[2] = bf16lo_to_f32(w.y);
+        v[3] = bf16hi_to_f32(w.y);
+    }
     static __device__ __forceinline__ float value(u32x4 v, int i)
     {
         return i & 1 ? bf16hi_to_f32(v[i >> 1]) : bf16lo_to_f32(v[i >> 1]);
@@ -100,6 +108,11 @@ struct Fp32 {
         return c;
     }
     static __device__ __forceinline__ float widen(float v) { return v; }
+    static __device__ __forceinline__ void load4(const float *p, float *v)
+    {
+        const f32x4 w = *reinterpret_cast<const f32x4 *>(p);
+        for (int i = 0; i < 4; ++i) v[i] = w[i];
+    }
     static __device__ __forceinline__ float value(u32x4 v, int i) { return __uint_as_float(v[i]); }
     static __device__ __forceinline__ u32x4 move(u32x4 v, uint32_t signs, float alpha)
     {
@@ -134,28 +147,30 @@ __device__ __forceinline__ uint32_t piece_signs(const uint8_t *bits, uint64_t e)
 
 // What a group of rows adds to the projection.
 struct Group {
-    bool none;             // nothing: no adapter
+    uint64_t lo, hi;       // its rows
+    bool none;             // no adapter
     bool bad;              // an index outside its table: the group's rows become NaN
     uint64_t base;         // first parameter of its adapter
     const uint8_t *bits;   // its probe's packed row, or nullptr
     float alpha;
 };
 
+// Group g < n_groups, by loads that do not wait for each other.
 __device__ __forceinline__ Group group_of(const AdapterArgs &a, uint32_t g)
 {
-    Group r = {true, false, 0, nullptr, 0.0f};
+    const int64_t lo = a.starts[g], hi = a.starts[g + 1];
     const int32_t id = a.ids[g];
     const int32_t probe = a.probes ? a.probes[g] : -1;
-    if (id == -1) return r;
-    r.bad = id < -1 || (uint32_t)id >= a.n_adapters ||
-            (a.probes && (probe < -1 || (probe >= 0 && (uint32_t)probe >= a.n_probes)));
-    if (r.bad) return r;
-    r.none = false;
-    r.base = (uint64_t)(uint32_t)id * a.rank * ((uint64_t)a.d_in + a.d_out);
-    if (probe >= 0) {
-        r.bits = a.bits + (uint64_t)probe * a.bits_stride;
-        r.alpha = a.alphas[probe >= 0 ? g : 0];
-    }
+    const float alpha = a.probes ? a.alphas[g] : 0.0f;
+    Group r;
+    r.lo = clamp_row(lo, a.rows);
+    r.hi = clamp_row(hi, a.rows);
+    r.bad = id != -1 && (id < -1 || (uint32_t)id >= a.n_adapters || probe < -1 ||
+                         (probe >= 0 && (uint32_t)probe >= a.n_probes));
+    r.none = id == -1 || r.bad;
+    r.base = r.none ? 0 : (uint64_t)(uint32_t)id * a.rank * ((uint64_t)a.d_in + a.d_out);
+    r.bits = probe >= 0 && !r.none ? a.bits + (uint64_t)probe * a.bits_stride : nullptr;
+    r.alpha = alpha;
     return r;
 }
 
@@ -186,12 +201,12 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void k_shrink(
 {
     const uint64_t slot = blockIdx.x;
     const uint32_t g = group_of_slot(a, slot);
-    const uint64_t start = clamp_row(a.starts[g], a.rows), end = clamp_row(a.starts[g + 1], a.rows);
+    const Group gr = group_of(a, g);
+    const uint64_t start = gr.lo, end = gr.hi;
     if (slot < start / 16 + g) return;
     const uint64_t row0 = start + (slot - (start / 16 + g)) * 16;
     if (row0 >= end) return;
     if (threadIdx.x < 16 && row0 + threadIdx.x < end) group[row0 + threadIdx.x] = (int32_t)g;
-    const Group gr = group_of(a, g);
     if (gr.none) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int l16 = lane & 15, q = lane >> 4;
@@ -360,10 +375,10 @@ struct EndProject {
         const int lane = threadIdx.x & 63, l = lane % kSide, q = lane / kSide;
         const uint64_t r1 = r0 + kSide * kMR < a.rows ? r0 + kSide * kMR : a.rows;
         for (; g < a.n_groups; ++g) {
-            const uint64_t s = clamp_row(a.starts[g], a.rows), e = clamp_row(a.starts[g + 1], a.rows);
+            const Group gr = group_of(a, g);
+            const uint64_t s = gr.lo, e = gr.hi;
             if (s >= r1) break;
             if (e <= r0 || e <= s) continue;
-            const Group gr = group_of(a, g);
             if (gr.bad) {
 #pragma unroll
                 for (int n = 0; n < kMR; ++n) {
@@ -462,10 +477,14 @@ struct EndProject {
 #pragma unroll
         for (int m = 0; m < kMF; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 4; ++i) add[m][i] = 0.0f;
+        if (bias) {
+#pragma unroll
+            for (int m = 0; m < kMF; ++m) {
                 const uint32_t f = f0 + 16 * m + 4 * q;
-                add[m][i] = bias && f < a.d_out ? T::widen(bias[f + i]) : 0.0f;
+                if (f < a.d_out) T::load4(bias + f, add[m]);
             }
+        }
         const int piece = lane % kRowPieces;
         const uint32_t f = f0 + piece * T::kPiece;
 #pragma unroll
@@ -478,7 +497,7 @@ struct EndProject {
                 for (int i = 0; i < 4; ++i) v[i] = t.acc[m][n][i] + add[m][i];
                 const int four = 4 * m + q, c = four * 4 / T::kPiece;
                 typename T::elem *at = reinterpret_cast<typename T::elem *>(
-                    lds + l16 * kRowPieces + (c ^ l16)) + four * 4 % T::kPiece;
+                    lds + l16 * kRowPieces + (c ^ (l16 % kRowPieces))) + four * 4 % T::kPiece;
                 store4(at, v);
             }
             wave_lds_sync();
@@ -486,7 +505,7 @@ struct EndProject {
             for (int i = 0; i < 16; i += kAtOnce) {
                 const int r = i + lane / kRowPieces;
                 const uint64_t row = r0 + 16 * n + r;
-                const u32x4 v = lds[r * kRowPieces + (piece ^ r)];
+                const u32x4 v = lds[r * kRowPieces + (piece ^ (r % kRowPieces))];
                 if (row >= lo && row < hi && f < a.d_out)
                     *reinterpret_cast<u32x4 *>(y + row * y_stride + f) = v;
             }

@@ -562,8 +562,8 @@ def zo_token_logprobs(ctx: Context, logits: torch.Tensor, targets: torch.Tensor 
     return out
 
 
-def zo_head_workspace_bytes(rows: int, vocab: int) -> int:
-    return int(_lib.lib().zo_head_workspace_bytes(rows, vocab))
+def zo_head_workspace_bytes(rows: int, d: int, vocab: int) -> int:
+    return int(_lib.lib().zo_head_workspace_bytes(rows, d, vocab))
 
 
 def zo_head_logprobs(ctx: Context, hidden: torch.Tensor, weight: torch.Tensor,
@@ -590,7 +590,7 @@ def zo_head_logprobs(ctx: Context, hidden: torch.Tensor, weight: torch.Tensor,
         op = _vector(out.logp, "logp", rows, torch.float32)
         ep = _vector(out.entropy, "entropy", rows, torch.float32)
     if workspace is None:
-        workspace = _new(zo_head_workspace_bytes(rows, vocab), torch.uint8, stream)
+        workspace = _new(zo_head_workspace_bytes(rows, d, vocab), torch.uint8, stream)
     _lib.check(_lib.lib().zo_head_logprobs(
         ctx.handle, hp, stride, wp, code, rows, d, vocab, tp, op, ep, _dev(workspace, "workspace"),
         workspace.numel() * workspace.element_size(), _stream(stream)), "zo_head_logprobs")

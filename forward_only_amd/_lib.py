@@ -60,7 +60,7 @@ SIGNATURES = {
                                         _u32, _u32, _u32, _vp, _vp, _vp]),
     "zo_token_logprobs": (_int, [_vp, _vp, _int, _u64, _u32, _u64, _vp, _vp, _vp, _u32, _vp, _vp,
                                  _vp]),
-    "zo_head_workspace_bytes": (_u64, [_u64, _u32]),
+    "zo_head_workspace_bytes": (_u64, [_u64, _u32, _u32]),
     "zo_head_logprobs": (_int, [_vp, _vp, _u64, _vp, _int, _u64, _u32, _u32, _vp, _vp, _vp, _vp,
                                 _u64, _vp]),
     "zo_group_loss": (_int, [_vp, _vp, _vp, _vp, _u32, _u64, _vp, _vp]),

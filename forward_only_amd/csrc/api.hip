@@ -562,9 +562,12 @@ zo_status zo_token_logprobs(zo_ctx *c, const void *d_logits, zo_dtype dtype, uin
                                               d_top_logp, as_stream(stream)));
 }
 
-uint64_t zo_head_workspace_bytes(uint64_t rows, uint32_t vocab)
+uint64_t zo_head_workspace_bytes(uint64_t rows, uint32_t d, uint32_t vocab)
 {
-    return zo::head_space(rows, vocab, nullptr).bytes;
+    // the larger of both types', whose tiles may differ
+    const uint64_t a = zo::head_space(rows, d, vocab, true, nullptr).bytes;
+    const uint64_t b = zo::head_space(rows, d, vocab, false, nullptr).bytes;
+    return a > b ? a : b;
 }
 
 zo_status zo_head_logprobs(zo_ctx *c, const void *d_hidden, uint64_t hidden_stride,
@@ -584,7 +587,7 @@ zo_status zo_head_logprobs(zo_ctx *c, const void *d_hidden, uint64_t hidden_stri
     if (!aligned<8>(d_targets) || !aligned<4>(d_logp) || !aligned<4>(d_entropy)) return ZO_EINVAL;
     if (hidden_stride > (UINT64_MAX >> 4) / rows) return ZO_EINVAL;
     if (!d_workspace || !aligned<256>(d_workspace) ||
-        workspace_bytes < zo_head_workspace_bytes(rows, vocab))
+        workspace_bytes < zo_head_workspace_bytes(rows, d, vocab))
         return ZO_EINVAL;
     const zo::HeadArgs h = {rows, hidden_stride, d, vocab, d_targets, d_logp, d_entropy, d_workspace};
     return from_hip(zo::launch_head_logprobs(h, dtype == ZO_BF16, d_hidden, d_weight,
@@ -610,7 +613,11 @@ uint64_t zo_adapter_workspace_bytes(uint64_t rows, uint32_t d_in, uint32_t d_out
                                     uint32_t regenerated)
 {
     const uint64_t params = (uint64_t)n_adapters * rank * ((uint64_t)d_in + d_out);
-    return zo::adapter_u_bytes(rows, rank, n_groups) + (uint64_t)regenerated * zo_bits_stride(params);
+    // slices of the larger of both types', whose tiles may differ
+    const bool big = zo::product_shape(rows, d_out, d_in, true) == zo::Shape::big ||
+                     zo::product_shape(rows, d_out, d_in, false) == zo::Shape::big;
+    return zo::adapter_u_bytes(rows, rank, n_groups) + (big ? zo::kBigSliceBytes : 0) +
+           (uint64_t)regenerated * zo_bits_stride(params);
 }
 
 zo_status zo_adapter_project(zo_ctx *c, const void *d_x, uint64_t x_stride, const void *d_weight,
@@ -650,18 +657,22 @@ zo_status zo_adapter_project(zo_ctx *c, const void *d_x, uint64_t x_stride, cons
                                                      regenerated);
     if (need > 0 && (!d_workspace || !aligned<256>(d_workspace) || workspace_bytes < need))
         return ZO_EINVAL;
-    float *u = static_cast<float *>(d_workspace);
+    float *u = static_cast<float *>(d_workspace), *slices = nullptr;
+    if (zo::product_shape(rows, d_out, d_in, dtype == ZO_BF16) == zo::Shape::big)
+        slices = u + zo::adapter_u_bytes(rows, rank, n_groups) / sizeof(float);
     zo::AdapterArgs a = {rows, d_in, d_out, rank, n_adapters, n_groups, n_probes, scale, d_starts,
                          d_ids, d_probes, d_alphas, d_bits, zo_bits_stride(params)};
     if (regenerated > 0) {
-        uint8_t *bits = static_cast<uint8_t *>(d_workspace) + zo::adapter_u_bytes(rows, rank, n_groups);
+        uint8_t *bits = static_cast<uint8_t *>(d_workspace) +
+                        (need - (uint64_t)regenerated * zo_bits_stride(params));
         const hipError_t e = zo::launch_gen_probes(key_of(c), step, probe0, n_probes, offset, params,
                                                    bits, c->num_cus, as_stream(stream));
         if (e != hipSuccess) return from_hip(e);
         a.bits = bits;
     }
     return from_hip(zo::launch_adapter_project(a, dtype == ZO_BF16, d_x, x_stride, d_weight, d_bias,
-                                               d_adapters, u, d_y, y_stride, as_stream(stream)));
+                                               d_adapters, u, slices, d_y, y_stride,
+                                               as_stream(stream)));
 }
 
 }  // extern "C"

@@ -29,6 +29,7 @@ __device__ const u32x4 kZeros = {0, 0, 0, 0};
 
 struct Bf16 {
     typedef uint16_t elem;
+    static constexpr bool kBf16 = true;
     static constexpr int kPiece = 8;    // elements per 16-byte piece
     static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c)
     {
@@ -90,6 +91,7 @@ struct Bf16 {
 
 struct Fp32 {
     typedef float elem;
+    static constexpr bool kBf16 = false;
     static constexpr int kPiece = 4;
     static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c)
     {
@@ -260,6 +262,7 @@ struct ProductArgs {
     uint64_t base, rows;   // places [base, base + rows) of the rows, or of the list's rows
     uint64_t x_stride;
     uint32_t k, features;
+    float *slices;         // workspace of the sliced tiles, or nullptr: none are sliced
 };
 
 // How many of `rows` places from `base` on there are when only *count places hold a row.
@@ -294,6 +297,7 @@ struct Tile {
 // Ending of zo_adapter_project.
 template <class T>
 struct EndProject {
+    static constexpr bool kSlices = false;
     AdapterArgs a;
     const float *u;
     const int32_t *group;
@@ -520,6 +524,7 @@ struct EndProject {
 
 // Ending of zo_head_logprobs: per wave tile and row (m, s, t) over the tile's features.
 struct EndHead {
+    static constexpr bool kSlices = false;
     uint32_t features;
     uint64_t base, rows;        // places of this launch
     const int64_t *targets;     // of all rows, or nullptr
@@ -589,22 +594,23 @@ struct EndHead {
     }
 };
 
-// Tile of workgroup b of nf x nr: consecutive tiles run through eight row tiles, then the
-// next features, and each XCD (workgroup b runs on XCD b % 8) takes one contiguous range, so
-// that the tiles in flight on an XCD share their rows and weights in its L2.
-__device__ __forceinline__ bool tile_of(uint32_t b, uint32_t nf, uint32_t nr, uint32_t &f, uint32_t &r)
+// Tile t of nf x nr: consecutive tiles run through eight row tiles, then the next features, so
+// that tiles in flight together share rows and weights in L2.
+__device__ __forceinline__ void tile_at(uint32_t t, uint32_t nf, uint32_t nr, uint32_t &f, uint32_t &r)
 {
-    const uint64_t n = (uint64_t)nf * nr;
-    const uint64_t x = b & 7u;
-    const uint64_t t = n * x / 8 + (b >> 3);
-    if (t >= n * (x + 1) / 8) return false;
     constexpr uint32_t kDeep = 8;
-    const uint32_t group = (uint32_t)(t / ((uint64_t)kDeep * nf));
-    const uint32_t in = (uint32_t)(t - (uint64_t)group * kDeep * nf);
+    const uint32_t group = t / (kDeep * nf), in = t - group * kDeep * nf;
     const uint32_t deep = nr - group * kDeep < kDeep ? nr - group * kDeep : kDeep;
     f = in / deep;
     r = group * kDeep + in % deep;
-    return true;
+}
+// Which of n tiles workgroup b takes: each XCD (workgroup b runs on XCD b % 8) one contiguous
+// range.  n or more: none.
+__device__ __forceinline__ uint32_t tile_of_xcd(uint32_t b, uint32_t n)
+{
+    const uint64_t x = b & 7u;
+    const uint64_t t = n * x / 8 + (b >> 3);
+    return t < n * (x + 1) / 8 ? (uint32_t)t : n;
 }
 
 typedef const __attribute__((address_space(1))) void *gptr_t;
@@ -622,7 +628,27 @@ typedef __attribute__((address_space(3))) void *lptr_t;
 // so its loads go out one turn later and have one and a half steps to arrive; each turn waits
 // for the loads that the next turn reads: all but the twelve issued since.  Loads past the end
 // of k read zeros, so that the counts hold to the end.
+//
+// Tiles run one per CU, so their number is cut into whole rounds of kSlots and a rest.  When the
+// rest fills at most half a round, each of its tiles is cut along k into as many slices as
+// fit into the round; their sums, 256 KiB each, are added in order by k_slices.
 constexpr int kBigF = 256, kBigR = 256;
+
+struct Cut {
+    uint32_t nf, nr;           // tiles of features and of rows
+    uint32_t whole, rest;      // tiles done whole, and the sliced ones (or all whole: rest = 0)
+    uint32_t slices;
+    __device__ __forceinline__ Cut(const ProductArgs &p, uint64_t rows, uint32_t steps)
+    {
+        nf = (p.features + kBigF - 1) / kBigF;
+        nr = (uint32_t)((rows + kBigR - 1) / kBigR);
+        const uint32_t n = nf * nr;
+        const uint32_t over = n % kBigSlots;
+        slices = big_slices(over, steps);
+        rest = p.slices && slices > 1 ? over : 0;
+        whole = n - rest;
+    }
+};
 
 // Wait until at most kLoads vector-memory loads are outstanding, and for all LDS reads if kLds.
 template <int kLoads, bool kLds>
@@ -652,10 +678,21 @@ __global__ __launch_bounds__(512, 2) void k_big(ProductArgs p, const typename T:
     enum { F0, F1, R0, R1 };
     extern __shared__ u32x4 stage[];                        // [2][F0, F1, R0, R1][128][kPieces]
     const uint64_t rows = places(p.base, p.rows, count);
+    const uint32_t steps = (p.k + kStep - 1) / kStep;
+    const Cut cut(p, rows, steps);
+    uint32_t tile, first = 0, last = steps;
+    if constexpr (End::kSlices) {
+        const uint32_t slice = blockIdx.x % cut.slices;
+        if (blockIdx.x / cut.slices >= cut.rest) return;
+        tile = cut.whole + blockIdx.x / cut.slices;
+        first = (uint32_t)((uint64_t)steps * slice / cut.slices);
+        last = (uint32_t)((uint64_t)steps * (slice + 1) / cut.slices);
+    } else {
+        tile = tile_of_xcd(blockIdx.x, cut.whole);
+        if (tile >= cut.whole) return;
+    }
     uint32_t tf, tr;
-    if (!tile_of(blockIdx.x, (p.features + kBigF - 1) / kBigF, (uint32_t)((rows + kBigR - 1) / kBigR),
-                 tf, tr))
-        return;
+    tile_at(tile, cut.nf, cut.nr, tf, tr);
     const uint32_t f0 = tf * kBigF;
     const uint64_t r0 = (uint64_t)tr * kBigR;
     const int lane = threadIdx.x & 63;
@@ -678,9 +715,8 @@ __global__ __launch_bounds__(512, 2) void k_big(ProductArgs p, const typename T:
             src[R0 + h][j] = x + (list ? list[p.base + r] : p.base + r) * p.x_stride + piece;
         }
     }
-    const uint32_t steps = (p.k + kStep - 1) / kStep;
     const auto issue = [&](int part, uint32_t step) {
-        const bool in = (uint64_t)step * kStep + piece < p.k;
+        const bool in = step < last && (uint64_t)step * kStep + piece < p.k;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const void *g = src[part][j] + (uint64_t)step * kStep;
@@ -721,22 +757,22 @@ __global__ __launch_bounds__(512, 2) void k_big(ProductArgs p, const typename T:
         __builtin_amdgcn_s_setprio(0);
         turn_barrier();
     };
-    uint32_t begun = 0;
+        uint32_t begun = 0;
 #pragma unroll
     for (uint32_t s = 0; s < 2; ++s) {
-        issue(R0, s);
-        issue(F0, s);
-        issue(F1, s);
-        issue(R1, s);
+        issue(R0, first + s);
+        issue(F0, first + s);
+        issue(F1, first + s);
+        issue(R1, first + s);
         if (s == 0) begun = end.begin(r0 + wr * 64);
     }
-    wait_for<12, false>();                      // R0 and F0 of step 0
+    wait_for<12, false>();                      // R0 and F0 of the first step
     turn_barrier();
-    read_r(0, 0);
+    read_r(0, first);
     wait_for<63, true>();
     turn_barrier();
     if (wave >= 4) turn_barrier();              // one turn behind from here on
-    for (uint32_t s = 0; s < steps; ++s) {
+    for (uint32_t s = first; s < last; ++s) {
         read_f(0, s);
         issue(R0, s + 2);
         multiply(0, 0);
@@ -754,6 +790,131 @@ __global__ __launch_bounds__(512, 2) void k_big(ProductArgs p, const typename T:
     wait_for<0, true>();
     turn_barrier();                             // the stage is free: no load is under way
     end.finish(t, begun, f0 + wf * 128, r0 + wr * 64, stage + wave * 512);
+}
+
+// The ending of a slice: its sums, to be added by k_slices.
+struct EndSlice {
+    static constexpr bool kSlices = true;
+    float *slices;
+    __device__ __forceinline__ uint32_t begin(uint64_t) const { return 0; }
+    template <class Tl>
+    __device__ __forceinline__ void finish(Tl &t, uint32_t, uint32_t, uint64_t, u32x4 *) const
+    {
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        f32x4 *to = reinterpret_cast<f32x4 *>(slices) + ((uint64_t)blockIdx.x * 8 + wave) * 32 * 64 + lane;
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int m = 0; m < 8; ++m) to[(n * 8 + m) * 64] = t.acc[m][n];
+    }
+};
+
+// Sums the slices of the last tiles and ends them: each wave one wave's tile of k_big, 16 rows.
+template <class T, class End>
+__global__ __launch_bounds__(256) void k_slices(ProductArgs p, const uint32_t *count, End end)
+{
+    __shared__ u32x4 lds[4 * 512];
+    const uint64_t rows = places(p.base, p.rows, count);
+    const Cut cut(p, rows, (p.k + 8 * T::kPiece - 1) / (8 * T::kPiece));
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t i = blockIdx.x / 8;          // 32 waves' shares of a tile, four to a workgroup
+    if (i >= cut.rest || cut.slices < 2) return;
+    const uint32_t of = blockIdx.x % 8, n = wave;
+    uint32_t tf, tr;
+    tile_at(cut.whole + i, cut.nf, cut.nr, tf, tr);
+    const f32x4 *from = reinterpret_cast<const f32x4 *>(p.slices) +
+                        ((uint64_t)i * cut.slices * 8 + of) * 32 * 64 + (n * 8) * 64 + lane;
+    Tile<T, 16, 8, 1> t;
+    t.clear();
+    for (uint32_t s = 0; s < cut.slices; ++s)
+#pragma unroll
+        for (int m = 0; m < 8; ++m) t.acc[m][0] += from[(uint64_t)s * 8 * 32 * 64 + m * 64];
+    const uint32_t f0 = tf * kBigF + (of & 1) * 128;
+    const uint64_t r0 = (uint64_t)tr * kBigR + (of >> 1) * 64 + n * 16;
+    if (r0 >= rows) return;
+    end.finish(t, end.begin(r0), f0, r0, lds + wave * 512);
+}
+
+// Middling sizes, where tiles of 256 x 256 would leave CUs without one: 64 features x 64 rows
+// by four waves.  Such a tile multiplies for a tenth of a microsecond a step, far less than a
+// load takes, so four stages are under way at once; a step waits for its own alone.
+constexpr int kMidStages = 4;
+template <class T, class End>
+__global__ __launch_bounds__(256) void k_mid(ProductArgs p, const typename T::elem *x,
+                                             const typename T::elem *w, const uint32_t *list,
+                                             const uint32_t *count, End end)
+{
+    constexpr int kSize = 64, kPieces = 8;
+    constexpr uint32_t kStep = kPieces * T::kPiece;
+    __shared__ u32x4 stage[kMidStages * 2 * kSize * kPieces];   // [stage][features, rows][kSize][kPieces]
+    const uint64_t rows = places(p.base, p.rows, count);
+    const uint32_t nf = (p.features + kSize - 1) / kSize, nr = (uint32_t)((rows + kSize - 1) / kSize);
+    const uint32_t tile = tile_of_xcd(blockIdx.x, nf * nr);
+    if (tile >= nf * nr) return;
+    uint32_t tf, tr;
+    tile_at(tile, nf, nr, tf, tr);
+    const uint32_t f0 = tf * kSize;
+    const uint64_t r0 = (uint64_t)tr * kSize;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l16 = lane & 15, q = lane >> 4;
+    const int wf = wave & 1, wr = wave >> 1;
+    // pieces placed as in k_big; this wave stages rows 8 wave .. + 7 of every 32 of both sides
+    const uint32_t piece = (uint32_t)((lane & 7) ^ ((wave * 4 + (lane >> 4)) & 7)) * T::kPiece;
+    const typename T::elem *src[2][2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int i = j * 32 + wave * 8 + (lane >> 3);
+        const uint32_t f = f0 + i < p.features ? f0 + i : p.features - 1;
+        src[0][j] = w + (uint64_t)f * p.k + piece;
+        const uint64_t r = r0 + i < rows ? r0 + i : rows - 1;
+        src[1][j] = x + (list ? list[p.base + r] : p.base + r) * p.x_stride + piece;
+    }
+    const uint32_t steps = (p.k + kStep - 1) / kStep;
+    const auto issue = [&](uint32_t step) {
+        const bool in = (uint64_t)step * kStep + piece < p.k;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const void *g = src[h][j] + (uint64_t)step * kStep;
+                if (!in) g = &kZeros;
+                u32x4 *l = stage + ((step % kMidStages * 2 + h) * kSize + j * 32 + wave * 8) * kPieces;
+                __builtin_amdgcn_global_load_lds((gptr_t)g, (lptr_t)l, 16, 0, 0);
+            }
+    };
+    Tile<T, 16, 2, 2> t;
+    t.clear();
+    const auto g = end.begin(r0 + wr * 32);
+#pragma unroll
+    for (uint32_t s = 0; s < kMidStages - 1; ++s) issue(s);
+    for (uint32_t s = 0; s < steps; ++s) {
+        wait_for<4 * (kMidStages - 2), true>();     // this step's loads
+        turn_barrier();                             // everyone's; and the last step's readers are done
+        issue(s + kMidStages - 1);
+        const u32x4 *sw = stage + (s % kMidStages * 2 * kSize + wf * 32 + l16) * kPieces;
+        const u32x4 *sx = stage + ((s % kMidStages * 2 + 1) * kSize + wr * 32 + l16) * kPieces;
+        u32x4 ff[2][2], fr[2][2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int at = (4 * c + q) ^ (l16 >> 1);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                ff[c][m] = sw[m * 16 * kPieces + at];
+                fr[c][m] = sx[m * 16 * kPieces + at];
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int n = 0; n < 2; ++n) t.acc[m][n] = T::mma(ff[c][m], fr[c][n], t.acc[m][n]);
+    }
+    wait_for<0, true>();
+    turn_barrier();                                 // the stage is free: no load is under way
+    end.finish(t, g, f0 + wf * 32, r0 + wr * 32, stage + wave * 512);
 }
 
 // Few rows.  What bounds the product is reading w once, so w goes straight from memory into
@@ -910,8 +1071,32 @@ hipError_t big(const ProductArgs &p, const typename T::elem *x, const typename T
                const uint32_t *list, const uint32_t *count, const End &end, hipStream_t stream)
 {
     const uint64_t n = (((uint64_t)p.features + kBigF - 1) / kBigF) * ((p.rows + kBigR - 1) / kBigR);
+    if (n > 0x3FFFFFFFull) return hipErrorInvalidValue;
+    // without a count the tiles are known: no workgroups for slices that there are not
+    const uint32_t over = (uint32_t)(n % kBigSlots);
+    const uint32_t steps = (p.k + 8 * T::kPiece - 1) / (8 * T::kPiece);
+    const bool sliced = p.slices && steps >= 2 * kBigSliceSteps && (count || big_slices(over, steps) > 1);
+    hipError_t e = hipSuccess;
+    if (count || !sliced || n > over) {
+        k_big<T, End><<<(uint32_t)((n + 7) / 8 * 8), 512, 2 * 512 * 128, stream>>>(p, x, w, list, count, end);
+        e = hipGetLastError();
+    }
+    if (e != hipSuccess || !sliced) return e;
+    k_big<T, EndSlice><<<kBigSlots, 512, 2 * 512 * 128, stream>>>(p, x, w, list, count, EndSlice{p.slices});
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const uint32_t most = count ? kBigSlots / 2 : over;
+    k_slices<T, End><<<most * 8, 256, 0, stream>>>(p, count, end);
+    return hipGetLastError();
+}
+
+template <class T, class End>
+hipError_t mid(const ProductArgs &p, const typename T::elem *x, const typename T::elem *w,
+               const uint32_t *list, const uint32_t *count, const End &end, hipStream_t stream)
+{
+    const uint64_t n = ((uint64_t)p.features + 63) / 64 * ((p.rows + 63) / 64);
     if (n > 0x7FFFFFFFull - 8) return hipErrorInvalidValue;
-    k_big<T, End><<<(uint32_t)((n + 7) / 8 * 8), 512, 2 * 512 * 128, stream>>>(p, x, w, list, count, end);
+    k_mid<T, End><<<(uint32_t)((n + 7) / 8 * 8), 256, 0, stream>>>(p, x, w, list, count, end);
     return hipGetLastError();
 }
 
@@ -929,17 +1114,22 @@ hipError_t few_of(const ProductArgs &p, const typename T::elem *x, const typenam
     return hipGetLastError();
 }
 template <class T, class End>
-hipError_t few(const ProductArgs &p, const typename T::elem *x, const typename T::elem *w,
-               const End &end, hipStream_t stream)
+hipError_t by_shape(Shape shape, const ProductArgs &p, const typename T::elem *x, const typename T::elem *w,
+                    const uint32_t *list, const uint32_t *count, const End &end, hipStream_t stream)
 {
-    return few_fragments(p.features) == 2 ? few_of<T, 2>(p, x, w, end, stream)
-                                          : few_of<T, 1>(p, x, w, end, stream);
+    switch (shape) {
+    case Shape::few1: return few_of<T, 1>(p, x, w, end, stream);
+    case Shape::few2: return few_of<T, 2>(p, x, w, end, stream);
+    case Shape::mid: return mid<T>(p, x, w, list, count, end, stream);
+    case Shape::big: break;
+    }
+    return big<T>(p, x, w, list, count, end, stream);
 }
 
 template <class T>
 hipError_t project(const AdapterArgs &a, const void *x, uint64_t x_stride, const void *w,
-                   const void *bias, const void *adapters, float *u, void *y, uint64_t y_stride,
-                   hipStream_t stream)
+                   const void *bias, const void *adapters, float *u, float *slices, void *y,
+                   uint64_t y_stride, hipStream_t stream)
 {
     typedef typename T::elem E;
     const E *px = static_cast<const E *>(x), *pa = static_cast<const E *>(adapters);
@@ -948,19 +1138,18 @@ hipError_t project(const AdapterArgs &a, const void *x, uint64_t x_stride, const
         a, px, x_stride, pa, u, group);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const ProductArgs p = {0, a.rows, x_stride, a.d_in, a.d_out};
+    const ProductArgs p = {0, a.rows, x_stride, a.d_in, a.d_out, slices};
     const EndProject<T> end = {a, u, group, pa, static_cast<const E *>(bias), static_cast<E *>(y), y_stride};
     const E *pw = static_cast<const E *>(w);
-    if (a.rows <= kFewRows) return few<T>(p, px, pw, end, stream);
-    return big<T>(p, px, pw, nullptr, nullptr, end, stream);
+    return by_shape<T>(product_shape(a.rows, a.d_out, a.d_in, T::kBf16), p, px, pw, nullptr, nullptr, end, stream);
 }
 
 template <class T>
 hipError_t head(const HeadArgs &h, const void *x, const void *w, hipStream_t stream)
 {
     typedef typename T::elem E;
-    const HeadSpace sp = head_space(h.rows, h.features, h.workspace);
-    const bool small = h.rows <= kFewRows;
+    const HeadSpace sp = head_space(h.rows, h.k, h.features, T::kBf16, h.workspace);
+    const bool small = sp.shape <= Shape::few2;
     uint32_t *list = nullptr, *count = nullptr;
     if (h.targets && !small) {
         list = sp.list;
@@ -972,13 +1161,12 @@ hipError_t head(const HeadArgs &h, const void *x, const void *w, hipStream_t str
     const E *px = static_cast<const E *>(x), *pw = static_cast<const E *>(w);
     for (uint64_t base = 0; base < h.rows; base += kHeadPlaces) {
         const uint64_t rows = h.rows - base < kHeadPlaces ? h.rows - base : kHeadPlaces;
-        const ProductArgs p = {base, rows, h.x_stride, h.k, h.features};
+        const ProductArgs p = {base, rows, h.x_stride, h.k, h.features, sp.slices};
         const EndHead end = {h.features, base, rows, h.targets, list, count, sp.m, sp.s, sp.t, sp.tl};
-        hipError_t e = small ? few<T>(p, px, pw, end, stream)
-                             : big<T>(p, px, pw, list, count, end, stream);
+        hipError_t e = by_shape<T>(sp.shape, p, px, pw, list, count, end, stream);
         if (e != hipSuccess) return e;
         k_head_join<<<(uint32_t)((rows + 7) / 8), 1024, 0, stream>>>(
-            sp.m, sp.s, sp.t, sp.tl, (h.features + sp.part - 1) / sp.part, base, rows, list, count,
+            sp.m, sp.s, sp.t, sp.tl, sp.parts, base, rows, list, count,
             h.targets, h.features, h.logp, h.entropy);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -993,7 +1181,8 @@ hipError_t prepare()
         return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                    hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     };
-    const hipError_t e = raise(&k_big<T, EndProject<T>>, 2 * 512 * 128);
+    hipError_t e = raise(&k_big<T, EndProject<T>>, 2 * 512 * 128);
+    if (e == hipSuccess) e = raise(&k_big<T, EndSlice>, 2 * 512 * 128);
     return e == hipSuccess ? raise(&k_big<T, EndHead>, 2 * 512 * 128) : e;
 }
 
@@ -1007,10 +1196,10 @@ hipError_t prepare_products()
 
 hipError_t launch_adapter_project(const AdapterArgs &a, bool bf16, const void *x, uint64_t x_stride,
                                   const void *w, const void *bias, const void *adapters, float *u,
-                                  void *y, uint64_t y_stride, hipStream_t stream)
+                                  float *slices, void *y, uint64_t y_stride, hipStream_t stream)
 {
-    return bf16 ? project<Bf16>(a, x, x_stride, w, bias, adapters, u, y, y_stride, stream)
-                : project<Fp32>(a, x, x_stride, w, bias, adapters, u, y, y_stride, stream);
+    return bf16 ? project<Bf16>(a, x, x_stride, w, bias, adapters, u, slices, y, y_stride, stream)
+                : project<Fp32>(a, x, x_stride, w, bias, adapters, u, slices, y, y_stride, stream);
 }
 
 hipError_t launch_head_logprobs(const HeadArgs &h, bool bf16, const void *x, const void *w,

@@ -157,20 +157,54 @@ struct AdapterArgs {
     const uint8_t *bits;           // n_probes packed rows over all adapters' parameters
     uint64_t bits_stride;
 };
-// Rows that the product kernel for few rows takes, and the 16-feature fragments of one of its
-// workgroups: two where that still leaves two workgroups per CU.
-constexpr uint64_t kFewRows = 32;
-inline uint32_t few_fragments(uint32_t features) { return features >= 2 * 2 * 16 * 256 ? 2 : 1; }
+// How a product of rows x features is cut into workgroups: 16 or 32 features and all of at
+// most 32 rows; tiles of 64 x 64; tiles of 256 x 256.
+enum class Shape { few1, few2, mid, big };
+// Tiles of 256 x 256 that run at once (one per CU), the most slices of one along k, the fewest
+// steps of 128 bytes of k that make a slice, and the workspace of all slices of a call.
+constexpr uint32_t kBigSlots = 256, kBigSlices = 16, kBigSliceSteps = 4;
+constexpr uint64_t kBigSliceBytes = (uint64_t)kBigSlots * 256 * 256 * 4;
+// Slices of each of `over` tiles that do not fill a round.
+__host__ __device__ constexpr uint32_t big_slices(uint32_t over, uint32_t steps)
+{
+    uint32_t s = over ? kBigSlots / over : 1;
+    s = s > kBigSlices ? kBigSlices : s;
+    return s > steps / kBigSliceSteps ? steps / kBigSliceSteps : s;
+}
+// The shape by estimated time.  Measured per step of 128 bytes of k: a round of 256 tiles of
+// 256 x 256 takes 1.45 us (bf16; fp32 7.5), a round of 512 tiles of 64 x 64 0.48 us (1.17),
+// or 0.33 us in bf16 while they are at most one per CU; slices cost 25 us to write and add up.
+inline Shape product_shape(uint64_t rows, uint32_t features, uint32_t k, bool bf16)
+{
+    // two fragments of features where that still leaves two workgroups per CU
+    if (rows <= 32) return features >= 2 * 2 * 16 * 256 ? Shape::few2 : Shape::few1;
+    const auto tiles = [&](uint64_t size) {
+        return ((uint64_t)features + size - 1) / size * ((rows + size - 1) / size);
+    };
+    const uint32_t steps = (k + (bf16 ? 63 : 31)) / (bf16 ? 64 : 32);
+    const uint64_t m = tiles(64), b = tiles(256), over = b % kBigSlots;
+    const double mid = !bf16    ? 1.17 * ((m + 511) / 512)
+                       : m <= 256 ? 0.33
+                                  : 0.48 * ((m + 511) / 512);
+    const uint32_t slices = big_slices((uint32_t)over, steps);
+    const double part = over == 0 ? 0.0 : slices > 1 ? 1.0 / slices : 1.0;
+    const double big = (bf16 ? 1.45 : 7.5) * ((double)(b / kBigSlots) + part);
+    return steps * big + (over && slices > 1 ? 25.0 : 0.0) <= steps * mid ? Shape::big : Shape::mid;
+}
+inline uint32_t shape_part(Shape s)   // features of one partial softmax: a wave's
+{
+    return s == Shape::few1 ? 16 : s == Shape::big ? 128 : 32;
+}
 // Bytes of x A^T, [rows][rank] floats, and of each row's group.
 inline uint64_t adapter_u_bytes(uint64_t rows, uint32_t rank, uint32_t n_groups)
 {
     (void)n_groups;
     return (rows * rank * 4 + rows * 4 + 255) / 256 * 256;
 }
-// u: adapter_u_bytes of workspace.
+// u: adapter_u_bytes of workspace; slices: kBigSliceBytes if the shape is big, else nullptr.
 hipError_t launch_adapter_project(const AdapterArgs &a, bool bf16, const void *x, uint64_t x_stride,
                                   const void *w, const void *bias, const void *adapters, float *u,
-                                  void *y, uint64_t y_stride, hipStream_t stream);
+                                  float *slices, void *y, uint64_t y_stride, hipStream_t stream);
 
 struct HeadArgs {
     uint64_t rows, x_stride;
@@ -183,16 +217,18 @@ struct HeadArgs {
 constexpr uint64_t kHeadPlaces = 16384;
 struct HeadSpace {
     uint32_t *count, *list;
-    float *m, *s, *t, *tl;
-    uint32_t part;             // features of one partial: a wave's in the product kernels
+    float *m, *s, *t, *tl, *slices;
+    Shape shape;
+    uint32_t parts;            // partial statistics of a row
     uint64_t bytes;
 };
-inline HeadSpace head_space(uint64_t rows, uint32_t features, void *base)
+inline HeadSpace head_space(uint64_t rows, uint32_t k, uint32_t features, bool bf16, void *base)
 {
     const uint64_t places = rows < kHeadPlaces ? rows : kHeadPlaces;
     HeadSpace s;
-    s.part = rows <= kFewRows ? 16 * few_fragments(features) : 128;
-    const uint64_t parts = ((uint64_t)features + s.part - 1) / s.part;
+    s.shape = product_shape(places, features, k, bf16);
+    s.parts = (features + shape_part(s.shape) - 1) / shape_part(s.shape);
+    const uint64_t parts = s.parts;
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {
         void *p = base ? static_cast<char *>(base) + at : nullptr;
@@ -205,6 +241,7 @@ inline HeadSpace head_space(uint64_t rows, uint32_t features, void *base)
     s.s = static_cast<float *>(take(parts * places * 4));
     s.t = static_cast<float *>(take(parts * places * 4));
     s.tl = static_cast<float *>(take(places * 4));
+    s.slices = s.shape == Shape::big ? static_cast<float *>(take(kBigSliceBytes)) : nullptr;
     s.bytes = at;
     return s;
 }

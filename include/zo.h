@@ -409,10 +409,10 @@ zo_status zo_token_logprobs(zo_ctx *ctx, const void *d_logits, zo_dtype dtype, u
  * 16-byte aligned; d_weight: device, contiguous, 16-byte aligned; both of `dtype`; d a
  * multiple of 8.  d_targets, d_logp, d_entropy as zo_token_logprobs; at least one of d_logp
  * and d_entropy.  d_workspace: device, 256-byte aligned, at least
- * zo_head_workspace_bytes(rows, vocab) bytes.  Deterministic.
+ * zo_head_workspace_bytes(rows, d, vocab) bytes.  Deterministic.
  * Errors: ZO_EINVAL as zo_token_logprobs, shapes outside these limits, a workspace that is
  * too small or misaligned; ZO_EUNSUPPORTED if rows or vocab exceed 2^31 - 1. */
-uint64_t zo_head_workspace_bytes(uint64_t rows, uint32_t vocab);
+uint64_t zo_head_workspace_bytes(uint64_t rows, uint32_t d, uint32_t vocab);
 zo_status zo_head_logprobs(zo_ctx *ctx, const void *d_hidden, uint64_t hidden_stride,
                            const void *d_weight, zo_dtype dtype, uint64_t rows, uint32_t d,
                            uint32_t vocab, const int64_t *d_targets, float *d_logp,

@@ -22,9 +22,9 @@ def test_null_context_is_refused():
 
 
 def test_workspace_sizes_grow_and_stay_bounded():
-    assert zo.zo_head_workspace_bytes(1, 50272) <= zo.zo_head_workspace_bytes(16384, 50272)
+    assert zo.zo_head_workspace_bytes(1, 768, 50272) <= zo.zo_head_workspace_bytes(16384, 768, 50272)
     # beyond one launch's rows only the row list grows
-    a, b = (zo.zo_head_workspace_bytes(r, 50272) for r in (1 << 20, 1 << 21))
+    a, b = (zo.zo_head_workspace_bytes(r, 768, 50272) for r in (1 << 20, 1 << 21))
     assert 0 < b - a <= 4 * (1 << 20) + 256
     base = zo.zo_adapter_workspace_bytes(100, 64, 64, 2, 8, 3)
     assert zo.zo_adapter_workspace_bytes(100, 64, 64, 2, 8, 3, 5) == base + 5 * zo.zo_bits_stride(2048)

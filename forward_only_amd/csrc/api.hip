@@ -60,6 +60,11 @@ inline bool aligned(const void *p)
 }
 
 constexpr uint64_t kMaxRows = 0x7FFFFFFFu;   // of the language-model operators
+// The rows of a product's left operand reach at most 64 GiB (32 bits of 16-byte units).
+inline bool reach_ok(uint64_t rows, uint64_t stride, uint64_t k, bool bf16)
+{
+    return (rows - 1) * stride + k <= ((uint64_t)1 << 36) / (bf16 ? 2 : 4);
+}
 
 inline zo::Key key_of(const zo_ctx *c) { return {(uint32_t)c->seed, (uint32_t)(c->seed >> 32)}; }
 
@@ -586,6 +591,7 @@ zo_status zo_head_logprobs(zo_ctx *c, const void *d_hidden, uint64_t hidden_stri
     if (!d_logp && !d_entropy) return ZO_EINVAL;
     if (!aligned<8>(d_targets) || !aligned<4>(d_logp) || !aligned<4>(d_entropy)) return ZO_EINVAL;
     if (hidden_stride > (UINT64_MAX >> 4) / rows) return ZO_EINVAL;
+    if (!reach_ok(rows, hidden_stride, d, dtype == ZO_BF16)) return ZO_EUNSUPPORTED;
     if (!d_workspace || !aligned<256>(d_workspace) ||
         workspace_bytes < zo_head_workspace_bytes(rows, d, vocab))
         return ZO_EINVAL;
@@ -652,6 +658,7 @@ zo_status zo_adapter_project(zo_ctx *c, const void *d_x, uint64_t x_stride, cons
     if (x_stride > (UINT64_MAX >> 4) / rows || y_stride > (UINT64_MAX >> 4) / rows ||
         (rows > 1 && y_stride < d_out))
         return ZO_EINVAL;
+    if (!reach_ok(rows, x_stride, d_in, dtype == ZO_BF16)) return ZO_EUNSUPPORTED;
     const uint32_t regenerated = d_probes && !d_bits && params > 0 ? n_probes : 0;
     const uint64_t need = zo_adapter_workspace_bytes(rows, d_in, d_out, n_adapters, rank, n_groups,
                                                      regenerated);

@@ -414,6 +414,7 @@ struct EndProject {
                 }
 #pragma unroll
                 for (int m = 0; m < kMF; ++m) {
+                    if (m % 4 == 0) asm volatile("" ::: "memory");   // four loads at once: no spills
                     const uint32_t f = f0 + kSide * m + l;
                     u32x4 fb = kZeros;
                     if (j < a.rank && f < a.d_out) {
@@ -702,24 +703,28 @@ __global__ __launch_bounds__(512, 2) void k_big(ProductArgs p, const typename T:
     // Staged row i holds its piece c at place c ^ (i / 2 % 8): sixteen rows read at one c then
     // cover all banks once.  This wave stages rows 8 wave .. + 7 and 64 more of each quarter.
     const uint32_t piece = (uint32_t)((lane & 7) ^ ((wave * 4 + (lane >> 4)) & 7)) * T::kPiece;
-    const typename T::elem *src[4][2];
+    // Sources in 16-byte units from the tile's first weight and from x: registers are short
+    // here, and 32 bits of units reach 64 GiB.
+    const u32x4 *const from_w = reinterpret_cast<const u32x4 *>(w + (uint64_t)f0 * p.k);
+    const u32x4 *const from_x = reinterpret_cast<const u32x4 *>(x);
+    uint32_t src[4][2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int i = j * 64 + wave * 8 + (lane >> 3);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint32_t f = f0 + (i >> 6) * 128 + h * 64 + (i & 63);
-            src[F0 + h][j] = w + (uint64_t)(f < p.features ? f : p.features - 1) * p.k + piece;
+            const uint32_t f = (i >> 6) * 128 + h * 64 + (i & 63);
+            src[F0 + h][j] = (uint32_t)(((uint64_t)(f0 + f < p.features ? f : p.features - 1 - f0) * p.k + piece) / T::kPiece);
             const uint64_t at = r0 + (i >> 5) * 64 + h * 32 + (i & 31);
             const uint64_t r = at < rows ? at : rows - 1;
-            src[R0 + h][j] = x + (list ? list[p.base + r] : p.base + r) * p.x_stride + piece;
+            src[R0 + h][j] = (uint32_t)(((list ? list[p.base + r] : p.base + r) * p.x_stride + piece) / T::kPiece);
         }
     }
     const auto issue = [&](int part, uint32_t step) {
         const bool in = step < last && (uint64_t)step * kStep + piece < p.k;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const void *g = src[part][j] + (uint64_t)step * kStep;
+            const u32x4 *g = (part < R0 ? from_w : from_x) + (uint64_t)step * kPieces + src[part][j];
             if (!in) g = &kZeros;
             u32x4 *l = stage + ((step & 1) * 4 + part) * kPart + (j * 64 + wave * 8) * kPieces;
             __builtin_amdgcn_global_load_lds((gptr_t)g, (lptr_t)l, 16, 0, 0);

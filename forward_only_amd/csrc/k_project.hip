@@ -138,13 +138,6 @@ __device__ __forceinline__ u32x4 piece_at(const typename T::elem *p)
     return *reinterpret_cast<const u32x4 *>(p);
 }
 
-// Sign bits of the piece that starts at local parameter e of packed row `bits`.
-template <class T>
-__device__ __forceinline__ uint32_t piece_signs(const uint8_t *bits, uint64_t e)
-{
-    return (uint32_t)bits[e >> 3] >> (e & 7u);
-}
-
 // ---- the adapters ---------------------------------------------------------------------
 
 // What a group of rows adds to the projection.
@@ -176,81 +169,114 @@ __device__ __forceinline__ Group group_of(const AdapterArgs &a, uint32_t g)
     return r;
 }
 
-// The last group of [0, n_groups) whose slot of 16-row tiles starts at or before `slot`.
-// Group g owns the slots from start_g / 16 + g on: at least as many as its rows fill.
-__device__ __forceinline__ uint32_t group_of_slot(const AdapterArgs &a, uint64_t slot)
+// The last group whose `value` is at most `at` (else the first), for values that do not fall
+// from group to group: all lanes look at once, 64 groups a round.
+template <class Value>
+__device__ __forceinline__ uint32_t last_group(uint32_t n_groups, uint64_t at, Value value)
 {
-    uint32_t lo = 0, hi = a.n_groups;
-    while (hi - lo > 1) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        if (clamp_row(a.starts[mid], a.rows) / 16 + mid <= slot)
-            lo = mid;
-        else
-            hi = mid;
+    const uint32_t lane = threadIdx.x & 63;
+    uint32_t g = 0, n = n_groups;
+    while (n > 1) {
+        const uint32_t step = (n + 63) / 64, i = lane * step;
+        const uint64_t below = __ballot(i < n && value(g + (i < n ? i : 0)) <= at);
+        if (!below) break;
+        const uint32_t skip = (__popcll(below) - 1) * step;
+        g += skip;
+        n = n - skip < step ? n - skip : step;
     }
-    return lo;
+    return __builtin_amdgcn_readfirstlane(g);
 }
 
-// u[row][j] = x[row] . A_g[j], fp32, and group[row] = g: one workgroup per 16 rows of a group.
-// Its waves split k in interleaved runs of kRun fragments, all of whose loads are in flight at
-// once, and add up in LDS; 16 waves, because one workgroup has a whole adapter to read when
-// requests bring single rows (32 rows with an adapter each, rank 16 of 5120: ... us).
+// u[row][j] = x[row] . A_g[j], fp32, and group[row] = g: one workgroup per 16 kRF rows of a
+// group, which owns the slots of that many rows from start_g / (16 kRF) + g on, at least as
+// many as its rows fill.  A wave takes 16 rows, 32 rows of A at a time, and its share of k in
+// interleaved runs of kRun fragments, all of whose loads are in flight at once; the shares add
+// up in LDS.  kRF = 1 (16 shares of k) when requests bring single rows and a workgroup's time is
+// that of reading an adapter; kRF = 4 for long groups, so that four times fewer workgroups
+// read it.
 constexpr int kShrinkWaves = 16;
-template <class T>
+template <class T, int kRF>
 __global__ __launch_bounds__(kShrinkWaves * 64) void k_shrink(
     AdapterArgs a, const typename T::elem *x, uint64_t x_stride, const typename T::elem *adapters,
     float *u, int32_t *group)
 {
+    constexpr int kRows = 16 * kRF, kShares = kShrinkWaves / kRF;
     const uint64_t slot = blockIdx.x;
-    const uint32_t g = group_of_slot(a, slot);
+    const uint32_t g = last_group(a.n_groups, slot,
+                                  [&](uint32_t i) { return clamp_row(a.starts[i], a.rows) / kRows + i; });
     const Group gr = group_of(a, g);
     const uint64_t start = gr.lo, end = gr.hi;
-    if (slot < start / 16 + g) return;
-    const uint64_t row0 = start + (slot - (start / 16 + g)) * 16;
+    if (slot < start / kRows + g) return;
+    const uint64_t row0 = start + (slot - (start / kRows + g)) * kRows;
     if (row0 >= end) return;
-    if (threadIdx.x < 16 && row0 + threadIdx.x < end) group[row0 + threadIdx.x] = (int32_t)g;
+    if (threadIdx.x < kRows && row0 + threadIdx.x < end) group[row0 + threadIdx.x] = (int32_t)g;
     if (gr.none) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rf = wave % kRF, share = wave / kRF;
     const int l16 = lane & 15, q = lane >> 4;
-    const uint64_t row = row0 + l16 < end ? row0 + l16 : end - 1;
+    const uint64_t row = row0 + 16 * rf + l16 < end ? row0 + 16 * rf + l16 : end - 1;
     const typename T::elem *xr = x + row * x_stride;
     constexpr uint32_t kStep = 4 * T::kPiece;   // k covered by one fragment of 16 x 16
     constexpr int kRun = 5;
-    __shared__ float red[kShrinkWaves][16][17];
-    for (uint32_t j0 = 0; j0 < a.rank; j0 += 16) {
-        const uint32_t j = j0 + l16 < a.rank ? j0 + l16 : a.rank - 1;
-        const uint64_t e0 = gr.base + (uint64_t)j * a.d_in;
-        f32x4 acc = {0, 0, 0, 0};
-        for (uint32_t k0 = wave * kRun * kStep; k0 < a.d_in; k0 += kShrinkWaves * kRun * kStep) {
-            u32x4 fa[kRun], fx[kRun];
-            uint32_t sg[kRun];
+    __shared__ float red[kShares][kRows][33];
+    for (uint32_t j0 = 0; j0 < a.rank; j0 += 32) {
+        const bool two = j0 + 16 < a.rank;
+        uint64_t e0[2];
 #pragma unroll
-            for (int i = 0; i < kRun; ++i) {
-                const uint32_t k = k0 + i * kStep + q * T::kPiece;
-                fa[i] = fx[i] = kZeros;
-                sg[i] = 0;
-                if (k < a.d_in) {
-                    fx[i] = piece_at<T>(xr + k);
-                    fa[i] = piece_at<T>(adapters + e0 + k);
-                    if (gr.bits) sg[i] = piece_signs<T>(gr.bits, e0 + k);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kRun; ++i) {
-                // past the end of k the moved zeros meet zeros of x
-                if (gr.bits) fa[i] = T::move(fa[i], sg[i], gr.alpha);
-                acc = T::mma(fa[i], fx[i], acc);
-            }
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t j = j0 + 16 * h + l16 < a.rank ? j0 + 16 * h + l16 : a.rank - 1;
+            e0[h] = gr.base + (uint64_t)j * a.d_in;
         }
+        f32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+        // Loads without branches between them, so that they all go out before the first wait;
+        // past the end of k both sides read zeros (which a move makes +-alpha times 0).
+        const auto take = [&](auto halves, auto moved) {
+            constexpr int kHalves = decltype(halves)::value;
+            for (uint32_t k0 = share * kRun * kStep; k0 < a.d_in; k0 += kShares * kRun * kStep) {
+                u32x4 fx[kRun], fa[kHalves][kRun];
+                uint8_t sg[kHalves][kRun];
+#pragma unroll
+                for (int i = 0; i < kRun; ++i) {
+                    const uint32_t k = k0 + i * kStep + q * T::kPiece;
+                    const bool in = k < a.d_in;
+                    fx[i] = *(in ? reinterpret_cast<const u32x4 *>(xr + k) : &kZeros);
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h) {
+                        const uint64_t at = e0[h] + k;
+                        fa[h][i] = *(in ? reinterpret_cast<const u32x4 *>(adapters + at) : &kZeros);
+                        if (decltype(moved)::value) sg[h][i] = gr.bits[(in ? at : e0[h]) >> 3];
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kRun; ++i)
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h) {
+                        const uint32_t k = k0 + i * kStep + q * T::kPiece;
+                        if (decltype(moved)::value)
+                            fa[h][i] = T::move(fa[h][i], sg[h][i] >> ((e0[h] + k) & 7), gr.alpha);
+                        acc[h] = T::mma(fa[h][i], fx[i], acc[h]);
+                    }
+            }
+        };
+        typedef std::integral_constant<int, 1> One;
+        typedef std::integral_constant<int, 2> Two;
+        if (gr.bits)
+            two ? take(Two{}, std::true_type{}) : take(One{}, std::true_type{});
+        else
+            two ? take(Two{}, std::false_type{}) : take(One{}, std::false_type{});
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) red[wave][l16][4 * q + i] = acc[i];   // [row][adapter row]
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) red[share][16 * rf + l16][16 * h + 4 * q + i] = acc[h][i];
         __syncthreads();
-        const int r = threadIdx.x >> 4, c = threadIdx.x & 15;
-        if (r < 16 && row0 + r < end && j0 + c < a.rank) {
+        for (int o = threadIdx.x; o < kRows * 32; o += kShrinkWaves * 64) {
+            const int r = o / 32, c = o % 32;
+            if (row0 + r >= end || j0 + c >= a.rank) continue;
             float sum = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kShrinkWaves; ++w) sum += red[w][r][c];
+            for (int w = 0; w < kShares; ++w) sum += red[w][r][c];
             u[(row0 + r) * a.rank + j0 + c] = sum;
         }
     }
@@ -305,21 +331,10 @@ struct EndProject {
     typename T::elem *y;
     uint64_t y_stride;
 
-    // The last group that starts at or before row r0 (else the first): all lanes look at once,
-    // 64 starts a round.
+    // The last group that starts at or before row r0 (else the first).
     __device__ __forceinline__ uint32_t begin(uint64_t r0) const
     {
-        const uint32_t lane = threadIdx.x & 63;
-        uint32_t g = 0, n = a.n_groups;
-        while (n > 1) {
-            const uint32_t step = (n + 63) / 64, at = lane * step;
-            const uint64_t below = __ballot(at < n && clamp_row(a.starts[g + (at < n ? at : 0)], a.rows) <= r0);
-            const uint32_t skip = below ? (__popcll(below) - 1) * step : 0;
-            g += skip;
-            n = n - skip < step ? n - skip : step;
-            if (!below) break;
-        }
-        return __builtin_amdgcn_readfirstlane(g);
+        return last_group(a.n_groups, r0, [&](uint32_t i) { return clamp_row(a.starts[i], a.rows); });
     }
 
     // Many rows: the groups that meet the tile one after another, on MFMA.  `lds`: 8 KiB of
@@ -347,25 +362,36 @@ struct EndProject {
             for (int m = 0; m < kMF; ++m) t.acc[m][0] += __builtin_nanf("");
         }
         if (gr.none) return;
+        const uint64_t first = gr.base + (uint64_t)a.rank * a.d_in;
         for (uint32_t j = 0; j < a.rank; j += 8) {
             const f32x4 *pu = reinterpret_cast<const f32x4 *>(u + row * a.rank + j);
             const f32x4 ua = pu[0], ub = pu[1];
+            u32x4 fb[kMF][4][8 / T::kPiece];
+            uint8_t sg[kMF][4];
 #pragma unroll
             for (int m = 0; m < kMF; ++m)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t f = f0 + 16 * m + 4 * q + i;
-                    if (f >= a.d_out) continue;
-                    const uint64_t at = gr.base + (uint64_t)a.rank * a.d_in + (uint64_t)f * a.rank + j;
-                    const uint32_t signs = gr.bits ? gr.bits[at >> 3] : 0;
+                    const uint64_t at = first + (uint64_t)(f < a.d_out ? f : a.d_out - 1) * a.rank + j;
+#pragma unroll
+                    for (int h = 0; h < 8 / T::kPiece; ++h) fb[m][i][h] = piece_at<T>(adapters + at + h * T::kPiece);
+                    sg[m][i] = *(gr.bits ? gr.bits + (at >> 3) : reinterpret_cast<const uint8_t *>(&kZeros));
+                }
+#pragma unroll
+            for (int m = 0; m < kMF; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
                     float s = 0.0f;
 #pragma unroll
-                    for (int h = 0; h < 8; h += T::kPiece) {
-                        u32x4 fb = piece_at<T>(adapters + at + h);
-                        if (gr.bits) fb = T::move(fb, signs >> h, gr.alpha);
+                    for (int h = 0; h < 8 / T::kPiece; ++h) {
+                        const u32x4 v = gr.bits ? T::move(fb[m][i][h], sg[m][i] >> (h * T::kPiece), gr.alpha)
+                                                : fb[m][i][h];
 #pragma unroll
-                        for (int k = 0; k < T::kPiece; ++k)
-                            s = fmaf(T::value(fb, k), h + k < 4 ? ua[(h + k) & 3] : ub[(h + k) & 3], s);
+                        for (int k = 0; k < T::kPiece; ++k) {
+                            const int c = h * T::kPiece + k;
+                            s = fmaf(T::value(v, k), c < 4 ? ua[c & 3] : ub[c & 3], s);
+                        }
                     }
                     t.acc[m][0][i] += a.scale * s;
                 }
@@ -395,6 +421,7 @@ struct EndProject {
             if (gr.none) continue;
             // The product is formed apart and added to the group's own rows, so that a NaN in
             // its adapter does not reach the others through 0 * NaN.
+            const uint64_t first = gr.base + (uint64_t)a.rank * a.d_in;
             for (uint32_t j0 = 0; j0 < a.rank; j0 += Tl::kReach * T::kPiece) {
                 const uint32_t j = j0 + q * T::kPiece;
                 typename T::Wide v[kMR];
@@ -402,37 +429,47 @@ struct EndProject {
                 for (int n = 0; n < kMR; ++n) {
                     const uint64_t row = r0 + kSide * n + l;
                     const bool in = row >= s && row < e && j < a.rank;
-                    const f32x4 *pu = reinterpret_cast<const f32x4 *>(u + row * a.rank + j);
+                    const f32x4 *pu = reinterpret_cast<const f32x4 *>(u + (in ? row * a.rank + j : s * a.rank));
                     float z[T::kPiece];
 #pragma unroll
                     for (int i = 0; i < T::kPiece; i += 4) {
-                        const f32x4 w = in ? pu[i / 4] : f32x4{0, 0, 0, 0};
+                        f32x4 w = pu[i / 4];
+                        if (!in) w = f32x4{0, 0, 0, 0};
 #pragma unroll
                         for (int k = 0; k < 4; ++k) z[i + k] = a.scale * w[k];
                     }
                     v[n] = T::wide(z);
                 }
+                // Loads without branches between them, four at once (eight would spill); lanes
+                // past the rank meet zeros of u, lanes past the features are not stored.
+                constexpr int kAtOnce = kMF < 4 ? kMF : 4;
 #pragma unroll
-                for (int m = 0; m < kMF; ++m) {
-                    if (m % 4 == 0) asm volatile("" ::: "memory");   // four loads at once: no spills
-                    const uint32_t f = f0 + kSide * m + l;
-                    u32x4 fb = kZeros;
-                    if (j < a.rank && f < a.d_out) {
-                        const uint64_t at = gr.base + (uint64_t)a.rank * a.d_in +
-                                            (uint64_t)f * a.rank + j;
-                        fb = piece_at<T>(adapters + at);
-                        if (gr.bits) fb = T::move(fb, piece_signs<T>(gr.bits, at), gr.alpha);
+                for (int m0 = 0; m0 < kMF; m0 += kAtOnce) {
+                    asm volatile("" ::: "memory");
+                    u32x4 fb[kAtOnce];
+                    uint8_t sg[kAtOnce];
+#pragma unroll
+                    for (int m = 0; m < kAtOnce; ++m) {
+                        const uint32_t f = f0 + kSide * (m0 + m) + l;
+                        const uint64_t at = first + (uint64_t)(f < a.d_out ? f : a.d_out - 1) * a.rank +
+                                            (j < a.rank ? j : 0);
+                        fb[m] = piece_at<T>(adapters + at);
+                        sg[m] = *(gr.bits ? gr.bits + (at >> 3) : reinterpret_cast<const uint8_t *>(&kZeros));
                     }
 #pragma unroll
-                    for (int n = 0; n < kMR; ++n) {
-                        const uint64_t row = r0 + kSide * n + l;
-                        if (r0 + kSide * n + kSide <= s || r0 + kSide * n >= e) continue;
-                        const bool in = row >= s && row < e;
-                        typename Tl::Acc zero = {};
-                        const typename Tl::Acc add = T::mma(fb, v[n], zero);
+                    for (int m = 0; m < kAtOnce; ++m) {
+                        if (gr.bits) fb[m] = T::move(fb[m], sg[m] >> (j & 7), gr.alpha);
 #pragma unroll
-                        for (int i = 0; i < 4 * Tl::kFours; ++i)
-                            t.acc[m][n][i] = in ? t.acc[m][n][i] + add[i] : t.acc[m][n][i];
+                        for (int n = 0; n < kMR; ++n) {
+                            const uint64_t row = r0 + kSide * n + l;
+                            if (r0 + kSide * n + kSide <= s || r0 + kSide * n >= e) continue;
+                            const bool in = row >= s && row < e;
+                            typename Tl::Acc zero = {};
+                            const typename Tl::Acc add = T::mma(fb[m], v[n], zero);
+#pragma unroll
+                            for (int i = 0; i < 4 * Tl::kFours; ++i)
+                                t.acc[m0 + m][n][i] = in ? t.acc[m0 + m][n][i] + add[i] : t.acc[m0 + m][n][i];
+                        }
                     }
                 }
             }
@@ -1139,8 +1176,14 @@ hipError_t project(const AdapterArgs &a, const void *x, uint64_t x_stride, const
     typedef typename T::elem E;
     const E *px = static_cast<const E *>(x), *pa = static_cast<const E *>(adapters);
     int32_t *group = reinterpret_cast<int32_t *>(u + a.rows * a.rank);
-    k_shrink<T><<<(uint32_t)(a.rows / 16 + a.n_groups), kShrinkWaves * 64, 0, stream>>>(
-        a, px, x_stride, pa, u, group);
+    // 64 rows per workgroup where the groups are long enough to fill them and still every
+    // other CU gets one
+    if (a.rows / 64 >= kBigSlots / 2 && a.rows / a.n_groups >= 64)
+        k_shrink<T, 4><<<(uint32_t)(a.rows / 64 + a.n_groups), kShrinkWaves * 64, 0, stream>>>(
+            a, px, x_stride, pa, u, group);
+    else
+        k_shrink<T, 1><<<(uint32_t)(a.rows / 16 + a.n_groups), kShrinkWaves * 64, 0, stream>>>(
+            a, px, x_stride, pa, u, group);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const ProductArgs p = {0, a.rows, x_stride, a.d_in, a.d_out, slices};

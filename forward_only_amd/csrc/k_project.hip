@@ -138,6 +138,73 @@ __device__ __forceinline__ u32x4 piece_at(const typename T::elem *p)
     return *reinterpret_cast<const u32x4 *>(p);
 }
 
+// ---- operands through LDS ---------------------------------------------------------------
+
+typedef const __attribute__((address_space(1))) void *gptr_t;
+typedef __attribute__((address_space(3))) void *lptr_t;
+
+// Wait until at most kLoads vector-memory loads are outstanding, and for all LDS reads if kLds.
+template <int kLoads, bool kLds>
+__device__ __forceinline__ void wait_for()
+{
+    __builtin_amdgcn_s_waitcnt((kLoads & 15) | (7 << 4) | ((kLds ? 0 : 15) << 8) | ((kLoads >> 4) << 14));
+}
+
+// A barrier that no LDS or global access moves across.
+__device__ __forceinline__ void turn_barrier()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+}
+
+// One wave's own operands: kRows16 blocks of 16 rows, 128 bytes of k a step, kStages steps under
+// way.  A fragment wants neighbouring lanes in different rows; loaded like that straight into
+// registers, a lane's 16 bytes take a cycle of the address unit each (13 bytes a cycle were
+// measured).  Loads to LDS take eight rows of 128 bytes instead, and the fragment is read from
+// there.  The wave waits for its own loads alone, so there is no barrier.
+//
+// Staged row i holds its piece c at place c ^ (i / 2 % 8): sixteen rows read at one c then cover
+// all banks once.
+template <class T, int kRows16, int kStages>
+struct Feed {
+    static constexpr int kPieces = 8, kLoads = 2 * kRows16;
+    static constexpr uint32_t kStep = kPieces * T::kPiece;
+    static constexpr int kStage = kRows16 * 16 * kPieces;       // pieces of one stage
+    u32x4 *lds;
+    uint32_t k, piece;
+    const typename T::elem *src[kLoads];
+
+    // row(i): where row i of the blocks begins.
+    template <class Row>
+    __device__ __forceinline__ Feed(u32x4 *own, uint32_t of_k, Row row) : lds(own), k(of_k)
+    {
+        const int lane = threadIdx.x & 63;
+        piece = (uint32_t)((lane & 7) ^ (lane >> 4)) * T::kPiece;   // + 4 in the odd eights of rows
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) src[j] = row(j * 8 + (lane >> 3));
+    }
+    __device__ __forceinline__ uint32_t steps() const { return (k + kStep - 1) / kStep; }
+    __device__ __forceinline__ void issue(uint32_t step, uint32_t stage) const
+    {
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const uint64_t at = (uint64_t)step * kStep + (j % 2 ? piece ^ (4 * T::kPiece) : piece);
+            const void *g = at < k ? static_cast<const void *>(src[j] + at) : &kZeros;
+            __builtin_amdgcn_global_load_lds((gptr_t)g, (lptr_t)(lds + stage * kStage + j * 8 * kPieces),
+                                             16, 0, 0);
+        }
+    }
+    // Fragment c (of two) of block b.
+    __device__ __forceinline__ u32x4 fragment(uint32_t stage, int b, int c) const
+    {
+        const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+        return lds[stage * kStage + (b * 16 + l16) * kPieces + ((4 * c + q) ^ (l16 >> 1))];
+    }
+};
+
 // ---- the adapters ---------------------------------------------------------------------
 
 // What a group of rows adds to the projection.
@@ -651,9 +718,6 @@ __device__ __forceinline__ uint32_t tile_of_xcd(uint32_t b, uint32_t n)
     return t < n * (x + 1) / 8 ? (uint32_t)t : n;
 }
 
-typedef const __attribute__((address_space(1))) void *gptr_t;
-typedef __attribute__((address_space(3))) void *lptr_t;
-
 // Many rows: 256 features x 256 rows by eight waves of 128 x 64, in which the two waves of a
 // SIMD take turns: four of the waves multiply while the other four read their next operands
 // from LDS, one barrier apart.  A step of 128 bytes of k has four such turns, one for each
@@ -687,23 +751,6 @@ struct Cut {
         whole = n - rest;
     }
 };
-
-// Wait until at most kLoads vector-memory loads are outstanding, and for all LDS reads if kLds.
-template <int kLoads, bool kLds>
-__device__ __forceinline__ void wait_for()
-{
-    __builtin_amdgcn_s_waitcnt((kLoads & 15) | (7 << 4) | ((kLds ? 0 : 15) << 8) | ((kLoads >> 4) << 14));
-}
-
-// A barrier that no LDS or global access moves across.
-__device__ __forceinline__ void turn_barrier()
-{
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("" ::: "memory");
-}
 
 template <class T, class End>
 __global__ __launch_bounds__(512, 2) void k_big(ProductArgs p, const typename T::elem *x,
@@ -959,81 +1006,80 @@ __global__ __launch_bounds__(256) void k_mid(ProductArgs p, const typename T::el
     end.finish(t, g, f0 + wf * 32, r0 + wr * 32, stage + wave * 512);
 }
 
-// Few rows.  What bounds the product is reading w once, so w goes straight from memory into
-// registers: a workgroup takes 16 kMF features and all rows, its eight waves split k in
-// interleaved blocks of kRun fragments (256 contiguous bytes of each bf16 row), and the waves'
-// sums meet in LDS.  x, read by every workgroup, comes from L2.
-constexpr int kFewWaves = 8;
+// Few rows.  What bounds the product is reading w once: a workgroup takes 16 kMF features and
+// all rows, four waves take every fourth step of k, and their sums meet in LDS.  kMR more waves
+// form the adapters' products meanwhile, add everything up and end 16 rows each.
+constexpr int kFewWaves = 4, kFewStages = 3;
+template <class T, int kMF, int kMR>
+constexpr uint32_t few_lds() { return kFewWaves * kFewStages * (kMF + kMR) * 16 * 128; }
+
 template <class T, int kMF, int kMR, class End>
-__global__ __launch_bounds__(kFewWaves * 64) void k_few(ProductArgs p, const typename T::elem *x,
-                                                        const typename T::elem *w, End end)
+__global__ __launch_bounds__((kFewWaves + kMR) * 64) void k_few(ProductArgs p,
+                                                                const typename T::elem *x,
+                                                                const typename T::elem *w, End end)
 {
-    constexpr uint32_t kStep = 4 * T::kPiece;
-    constexpr int kRun = 4;
+    typedef Feed<T, kMF + kMR, kFewStages> F;
+    extern __shared__ u32x4 stage[];            // [wave][stage][features, rows], then [wave] of sums
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int l16 = lane & 15, q = lane >> 4;
     const uint32_t f0 = blockIdx.x * (16 * kMF);
-    const typename T::elem *pw[kMF], *px[kMR];
-#pragma unroll
-    for (int m = 0; m < kMF; ++m) {
-        const uint32_t f = f0 + 16 * m + l16 < p.features ? f0 + 16 * m + l16 : p.features - 1;
-        pw[m] = w + (uint64_t)f * p.k + q * T::kPiece;
-    }
-#pragma unroll
-    for (int n = 0; n < kMR; ++n) {
-        const uint64_t r = (uint64_t)(16 * n + l16) < p.rows ? 16 * n + l16 : p.rows - 1;
-        px[n] = x + r * p.x_stride + q * T::kPiece;
-    }
-    Tile<T, 16, kMF, kMR> t;
-    t.clear();
-    const uint32_t stride = kFewWaves * kRun * kStep;
-    uint32_t k0 = wave * kRun * kStep;
-    for (; k0 + kRun * kStep <= p.k; k0 += stride) {
-        u32x4 fw[kMF][kRun], fx[kMR][kRun];
+    f32x4 *sums = reinterpret_cast<f32x4 *>(stage);
+    if (wave >= kFewWaves) {
+        const int n = wave - kFewWaves;
+        Tile<T, 16, kMF, 1> own;
+        own.clear();
+        end.add_rows(own, f0, 16 * n);
+        __syncthreads();                        // the stages are free
+        __syncthreads();                        // the sums are there
 #pragma unroll
         for (int m = 0; m < kMF; ++m)
 #pragma unroll
-            for (int i = 0; i < kRun; ++i) fw[m][i] = piece_at<T>(pw[m] + k0 + i * kStep);
+            for (int v = 0; v < kFewWaves; ++v) own.acc[m][0] += sums[((v * kMF + m) * kMR + n) * 64 + lane];
+        end.store(own, f0, 16 * n);
+        return;
+    }
+    const F feed(stage + wave * kFewStages * F::kStage, p.k, [&](int i) {
+        if (i < 16 * kMF) {
+            const uint32_t f = f0 + i < p.features ? f0 + i : p.features - 1;
+            return w + (uint64_t)f * p.k;
+        }
+        const uint64_t r = (uint64_t)(i - 16 * kMF) < p.rows ? i - 16 * kMF : p.rows - 1;
+        return x + r * p.x_stride;
+    });
+    Tile<T, 16, kMF, kMR> t;
+    t.clear();
+    const uint32_t steps = feed.steps();
 #pragma unroll
-        for (int n = 0; n < kMR; ++n)
+    for (int i = 0; i < kFewStages - 1; ++i) feed.issue(wave + i * kFewWaves, i);
+    uint32_t at = 0, to = kFewStages - 1;
+    for (uint32_t s = wave; s < steps; s += kFewWaves) {
+        wait_for<F::kLoads * (kFewStages - 2), true>();
+        asm volatile("" ::: "memory");
+        u32x4 fw[2][kMF], fx[2][kMR];
 #pragma unroll
-            for (int i = 0; i < kRun; ++i) fx[n][i] = piece_at<T>(px[n] + k0 + i * kStep);
+        for (int c = 0; c < 2; ++c) {
 #pragma unroll
-        for (int i = 0; i < kRun; ++i)
+            for (int m = 0; m < kMF; ++m) fw[c][m] = feed.fragment(at, m, c);
+#pragma unroll
+            for (int n = 0; n < kMR; ++n) fx[c][n] = feed.fragment(at, kMF + n, c);
+        }
+        feed.issue(s + (kFewStages - 1) * kFewWaves, to);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int m = 0; m < kMF; ++m)
 #pragma unroll
-                for (int n = 0; n < kMR; ++n) t.acc[m][n] = T::mma(fw[m][i], fx[n][i], t.acc[m][n]);
+                for (int n = 0; n < kMR; ++n) t.acc[m][n] = T::mma(fw[c][m], fx[c][n], t.acc[m][n]);
+        at = at + 1 == kFewStages ? 0 : at + 1;
+        to = to + 1 == kFewStages ? 0 : to + 1;
     }
-    for (int i = 0; i < kRun && k0 < p.k; ++i, k0 += kStep) {   // the last, short block
-        const bool in = k0 + q * T::kPiece < p.k;
-        u32x4 fx[kMR];
-#pragma unroll
-        for (int n = 0; n < kMR; ++n) fx[n] = in ? piece_at<T>(px[n] + k0) : kZeros;
-#pragma unroll
-        for (int m = 0; m < kMF; ++m) {
-            const u32x4 fw = in ? piece_at<T>(pw[m] + k0) : kZeros;
-#pragma unroll
-            for (int n = 0; n < kMR; ++n) t.acc[m][n] = T::mma(fw, fx[n], t.acc[m][n]);
-        }
-    }
-    __shared__ f32x4 sums[kFewWaves][kMF][kMR][64];
+    wait_for<0, true>();
+    __syncthreads();
 #pragma unroll
     for (int m = 0; m < kMF; ++m)
 #pragma unroll
-        for (int n = 0; n < kMR; ++n) sums[wave][m][n][lane] = t.acc[m][n];
+        for (int n = 0; n < kMR; ++n) sums[((wave * kMF + m) * kMR + n) * 64 + lane] = t.acc[m][n];
     __syncthreads();
-    if (wave >= kMR) return;
-    Tile<T, 16, kMF, 1> own;
-#pragma unroll
-    for (int m = 0; m < kMF; ++m) {
-        own.acc[m][0] = sums[0][m][wave][lane];
-#pragma unroll
-        for (int v = 1; v < kFewWaves; ++v) own.acc[m][0] += sums[v][m][wave][lane];
-    }
-    end.add_rows(own, f0, 16 * wave);
-    end.store(own, f0, 16 * wave);
 }
 
 // ---- joining the head's partial statistics ----------------------------------------------
@@ -1150,9 +1196,9 @@ hipError_t few_of(const ProductArgs &p, const typename T::elem *x, const typenam
 {
     const uint32_t grid = (p.features + 16 * kMF - 1) / (16 * kMF);
     if (p.rows <= 16)
-        k_few<T, kMF, 1, End><<<grid, kFewWaves * 64, 0, stream>>>(p, x, w, end);
+        k_few<T, kMF, 1, End><<<grid, (kFewWaves + 1) * 64, few_lds<T, kMF, 1>(), stream>>>(p, x, w, end);
     else
-        k_few<T, kMF, 2, End><<<grid, kFewWaves * 64, 0, stream>>>(p, x, w, end);
+        k_few<T, kMF, 2, End><<<grid, (kFewWaves + 2) * 64, few_lds<T, kMF, 2>(), stream>>>(p, x, w, end);
     return hipGetLastError();
 }
 template <class T, class End>
@@ -1229,9 +1275,21 @@ hipError_t prepare()
         return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                    hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     };
-    hipError_t e = raise(&k_big<T, EndProject<T>>, 2 * 512 * 128);
-    if (e == hipSuccess) e = raise(&k_big<T, EndSlice>, 2 * 512 * 128);
-    return e == hipSuccess ? raise(&k_big<T, EndHead>, 2 * 512 * 128) : e;
+    const hipError_t all[] = {
+        raise(&k_big<T, EndProject<T>>, 2 * 512 * 128),
+        raise(&k_big<T, EndSlice>, 2 * 512 * 128),
+        raise(&k_big<T, EndHead>, 2 * 512 * 128),
+        raise(&k_few<T, 1, 1, EndProject<T>>, few_lds<T, 1, 1>()),
+        raise(&k_few<T, 1, 2, EndProject<T>>, few_lds<T, 1, 2>()),
+        raise(&k_few<T, 2, 1, EndProject<T>>, few_lds<T, 2, 1>()),
+        raise(&k_few<T, 2, 2, EndProject<T>>, few_lds<T, 2, 2>()),
+        raise(&k_few<T, 1, 1, EndHead>, few_lds<T, 1, 1>()),
+        raise(&k_few<T, 1, 2, EndHead>, few_lds<T, 1, 2>()),
+        raise(&k_few<T, 2, 1, EndHead>, few_lds<T, 2, 1>()),
+        raise(&k_few<T, 2, 2, EndHead>, few_lds<T, 2, 2>())};
+    for (const hipError_t e : all)
+        if (e != hipSuccess) return e;
+    return hipSuccess;
 }
 
 }  // namespace

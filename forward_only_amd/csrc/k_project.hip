@@ -254,20 +254,26 @@ __device__ __forceinline__ uint32_t last_group(uint32_t n_groups, uint64_t at, V
     return __builtin_amdgcn_readfirstlane(g);
 }
 
-// u[row][j] = x[row] . A_g[j], fp32, and group[row] = g: one workgroup per 16 kRF rows of a
-// group, which owns the slots of that many rows from start_g / (16 kRF) + g on, at least as
-// many as its rows fill.  A wave takes 16 rows, 32 rows of A at a time, and its share of k in
-// interleaved runs of kRun fragments, all of whose loads are in flight at once; the shares add
-// up in LDS.  kRF = 1 (16 shares of k) when requests bring single rows and a workgroup's time is
-// that of reading an adapter; kRF = 4 for long groups, so that four times fewer workgroups
-// read it.
-constexpr int kShrinkWaves = 16;
-template <class T, int kRF>
-__global__ __launch_bounds__(kShrinkWaves * 64) void k_shrink(
+// u[row][j] = x[row] . A_g[j], fp32, and group[row] = g: one workgroup per 16 kXF rows of a
+// group, which owns the slots of that many rows from start_g / (16 kXF) + g on, at least as
+// many as its rows fill.  The waves share k and feed themselves; their sums meet in LDS.  16
+// kAF rows of A are taken at a time.  What bounds it is the latency of the first loads when
+// requests bring single rows (16 rows and eight waves), else reading x once and A once per
+// workgroup (32 rows and four waves).
+constexpr int kShrinkStages = 3;
+template <int kXF>
+constexpr int shrink_waves() { return kXF == 1 ? 8 : 4; }
+template <int kXF, int kAF>
+constexpr uint32_t shrink_lds() { return shrink_waves<kXF>() * kShrinkStages * (kXF + kAF) * 16 * 128; }
+
+template <class T, int kXF, int kAF>
+__global__ __launch_bounds__(shrink_waves<kXF>() * 64) void k_shrink(
     AdapterArgs a, const typename T::elem *x, uint64_t x_stride, const typename T::elem *adapters,
     float *u, int32_t *group)
 {
-    constexpr int kRows = 16 * kRF, kShares = kShrinkWaves / kRF;
+    typedef Feed<T, kXF + kAF, kShrinkStages> F;
+    constexpr int kRows = 16 * kXF, kShares = shrink_waves<kXF>();
+    extern __shared__ u32x4 stage[];            // [wave][stage][x, A], then [wave] of sums
     const uint64_t slot = blockIdx.x;
     const uint32_t g = last_group(a.n_groups, slot,
                                   [&](uint32_t i) { return clamp_row(a.starts[i], a.rows) / kRows + i; });
@@ -280,72 +286,94 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void k_shrink(
     if (gr.none) return;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int rf = wave % kRF, share = wave / kRF;
     const int l16 = lane & 15, q = lane >> 4;
-    const uint64_t row = row0 + 16 * rf + l16 < end ? row0 + 16 * rf + l16 : end - 1;
-    const typename T::elem *xr = x + row * x_stride;
-    constexpr uint32_t kStep = 4 * T::kPiece;   // k covered by one fragment of 16 x 16
-    constexpr int kRun = 5;
-    __shared__ float red[kShares][kRows][33];
-    for (uint32_t j0 = 0; j0 < a.rank; j0 += 32) {
-        const bool two = j0 + 16 < a.rank;
-        uint64_t e0[2];
+    float *sums = reinterpret_cast<float *>(stage);
+    for (uint32_t j0 = 0; j0 < a.rank; j0 += 16 * kAF) {
+        const auto row_of_a = [&](int i) { return j0 + i < a.rank ? j0 + i : a.rank - 1; };
+        const F feed(stage + wave * kShrinkStages * F::kStage, a.d_in, [&](int i) {
+            if (i < kRows) return x + (row0 + i < end ? row0 + i : end - 1) * x_stride;
+            return adapters + gr.base + (uint64_t)row_of_a(i - kRows) * a.d_in;
+        });
+        f32x4 acc[kAF][kXF];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t j = j0 + 16 * h + l16 < a.rank ? j0 + 16 * h + l16 : a.rank - 1;
-            e0[h] = gr.base + (uint64_t)j * a.d_in;
-        }
-        f32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-        // Loads without branches between them, so that they all go out before the first wait;
-        // past the end of k both sides read zeros (which a move makes +-alpha times 0).
-        const auto take = [&](auto halves, auto moved) {
-            constexpr int kHalves = decltype(halves)::value;
-            for (uint32_t k0 = share * kRun * kStep; k0 < a.d_in; k0 += kShares * kRun * kStep) {
-                u32x4 fx[kRun], fa[kHalves][kRun];
-                uint8_t sg[kHalves][kRun];
+        for (int h = 0; h < kAF; ++h)
 #pragma unroll
-                for (int i = 0; i < kRun; ++i) {
-                    const uint32_t k = k0 + i * kStep + q * T::kPiece;
-                    const bool in = k < a.d_in;
-                    fx[i] = *(in ? reinterpret_cast<const u32x4 *>(xr + k) : &kZeros);
+            for (int n = 0; n < kXF; ++n) acc[h][n] = f32x4{0, 0, 0, 0};
+        uint64_t e0[kAF];
 #pragma unroll
-                    for (int h = 0; h < kHalves; ++h) {
-                        const uint64_t at = e0[h] + k;
-                        fa[h][i] = *(in ? reinterpret_cast<const u32x4 *>(adapters + at) : &kZeros);
-                        if (decltype(moved)::value) sg[h][i] = gr.bits[(in ? at : e0[h]) >> 3];
+        for (int h = 0; h < kAF; ++h) e0[h] = gr.base + (uint64_t)row_of_a(16 * h + l16) * a.d_in;
+        const uint32_t steps = feed.steps();
+        const auto take = [&](auto moved) {
+            constexpr bool kMoved = decltype(moved)::value;
+            uint8_t sg[2][kAF];
+            const auto signs = [&](uint32_t step) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int h = 0; h < kAF; ++h) {
+                        const uint64_t k = (uint64_t)step * F::kStep + (4 * c + q) * T::kPiece;
+                        sg[c][h] = gr.bits[(e0[h] + (k < a.d_in ? k : 0)) >> 3];
                     }
+            };
+            if constexpr (kMoved) signs(wave);
+#pragma unroll
+            for (int i = 0; i < kShrinkStages - 1; ++i) feed.issue(wave + i * kShares, i);
+            uint32_t at = 0, to = kShrinkStages - 1;
+            for (uint32_t s = wave; s < steps; s += kShares) {
+                wait_for<F::kLoads * (kShrinkStages - 2), true>();
+                asm volatile("" ::: "memory");
+                u32x4 fa[2][kAF], fx[2][kXF];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                    for (int n = 0; n < kXF; ++n) fx[c][n] = feed.fragment(at, n, c);
+#pragma unroll
+                    for (int h = 0; h < kAF; ++h) fa[c][h] = feed.fragment(at, kXF + h, c);
                 }
+                if constexpr (kMoved) {
+                    // past the end of k the moved zeros, +-alpha, meet zeros of x
 #pragma unroll
-                for (int i = 0; i < kRun; ++i)
+                    for (int c = 0; c < 2; ++c)
 #pragma unroll
-                    for (int h = 0; h < kHalves; ++h) {
-                        const uint32_t k = k0 + i * kStep + q * T::kPiece;
-                        if (decltype(moved)::value)
-                            fa[h][i] = T::move(fa[h][i], sg[h][i] >> ((e0[h] + k) & 7), gr.alpha);
-                        acc[h] = T::mma(fa[h][i], fx[i], acc[h]);
-                    }
+                        for (int h = 0; h < kAF; ++h)
+                            fa[c][h] = T::move(fa[c][h], sg[c][h] >> ((4 * c + q) * T::kPiece & 7), gr.alpha);
+                    signs(s + kShares);         // before the loads that the next wait leaves out
+                }
+                feed.issue(s + (kShrinkStages - 1) * kShares, to);
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int h = 0; h < kAF; ++h)
+#pragma unroll
+                        for (int n = 0; n < kXF; ++n) acc[h][n] = T::mma(fa[c][h], fx[c][n], acc[h][n]);
+                at = at + 1 == kShrinkStages ? 0 : at + 1;
+                to = to + 1 == kShrinkStages ? 0 : to + 1;
             }
         };
-        typedef std::integral_constant<int, 1> One;
-        typedef std::integral_constant<int, 2> Two;
         if (gr.bits)
-            two ? take(Two{}, std::true_type{}) : take(One{}, std::true_type{});
+            take(std::true_type{});
         else
-            two ? take(Two{}, std::false_type{}) : take(One{}, std::false_type{});
-        __syncthreads();
+            take(std::false_type{});
+        wait_for<0, true>();
+        __syncthreads();                        // the stages are free
+        constexpr int kPitch = 16 * kAF + 1;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < kAF; ++h)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) red[share][16 * rf + l16][16 * h + 4 * q + i] = acc[h][i];
+            for (int n = 0; n < kXF; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sums[(wave * kRows + 16 * n + l16) * kPitch + 16 * h + 4 * q + i] = acc[h][n][i];
         __syncthreads();
-        for (int o = threadIdx.x; o < kRows * 32; o += kShrinkWaves * 64) {
-            const int r = o / 32, c = o % 32;
+        for (int o = threadIdx.x; o < kRows * 16 * kAF; o += kShares * 64) {
+            const int r = o / (16 * kAF), c = o % (16 * kAF);
             if (row0 + r >= end || j0 + c >= a.rank) continue;
             float sum = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kShares; ++w) sum += red[w][r][c];
+            for (int w = 0; w < kShares; ++w) sum += sums[(w * kRows + r) * kPitch + c];
             u[(row0 + r) * a.rank + j0 + c] = sum;
         }
+        __syncthreads();
     }
 }
 
@@ -1115,7 +1143,9 @@ __global__ __launch_bounds__(1024) void k_counted(const int64_t *targets, uint64
     if (tid == 0) *count = at;
 }
 
-// Joins the parts of each place: eight places per workgroup, 128 threads for each.
+// Joins the parts of each place: kOf places per workgroup of 1024 threads.  Eight read whole
+// sectors; one, when there are few rows, has its parts in one or two rounds of loads.
+template <int kOf>
 __global__ __launch_bounds__(1024) void k_head_join(const float *m, const float *s, const float *t,
                                                     const float *tl, uint32_t parts, uint64_t base,
                                                     uint64_t rows, const uint32_t *list,
@@ -1123,23 +1153,23 @@ __global__ __launch_bounds__(1024) void k_head_join(const float *m, const float 
                                                     uint32_t features, float *logp, float *entropy)
 {
     const uint64_t n = places(base, rows, count);
-    const int of = threadIdx.x & 7, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const uint64_t at = (uint64_t)blockIdx.x * 8 + of;
-    if ((uint64_t)blockIdx.x * 8 >= n) return;
+    const int of = threadIdx.x % kOf, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint64_t at = (uint64_t)blockIdx.x * kOf + of;
+    if ((uint64_t)blockIdx.x * kOf >= n) return;
     SoftStats st = SoftStats::empty();
     if (at < n)
-        for (uint32_t p = threadIdx.x >> 3; p < parts; p += 128)
+        for (uint32_t p = threadIdx.x / kOf; p < parts; p += 1024 / kOf)
             st.merge({m[(uint64_t)p * rows + at], s[(uint64_t)p * rows + at],
                       t[(uint64_t)p * rows + at]});
-    st.wave_merge(32, 8);
-    __shared__ float all[16][8][3];
-    if (lane < 8) {
+    st.wave_merge(32, kOf);
+    __shared__ float all[16][kOf][3];
+    if (lane < kOf) {
         all[wave][of][0] = st.m;
         all[wave][of][1] = st.s;
         all[wave][of][2] = st.t;
     }
     __syncthreads();
-    if (threadIdx.x >= 8 || at >= n) return;
+    if (threadIdx.x >= kOf || at >= n) return;
     for (int w = 1; w < 16; ++w) st.merge({all[w][of][0], all[w][of][1], all[w][of][2]});
     const uint64_t row = list ? list[base + at] : base + at;
     const int64_t tgt = targets ? targets[row] : 0;
@@ -1222,14 +1252,20 @@ hipError_t project(const AdapterArgs &a, const void *x, uint64_t x_stride, const
     typedef typename T::elem E;
     const E *px = static_cast<const E *>(x), *pa = static_cast<const E *>(adapters);
     int32_t *group = reinterpret_cast<int32_t *>(u + a.rows * a.rank);
-    // 64 rows per workgroup where the groups are long enough to fill them and still every
-    // other CU gets one
-    if (a.rows / 64 >= kBigSlots / 2 && a.rows / a.n_groups >= 64)
-        k_shrink<T, 4><<<(uint32_t)(a.rows / 64 + a.n_groups), kShrinkWaves * 64, 0, stream>>>(
-            a, px, x_stride, pa, u, group);
+    // 32 rows per workgroup where the groups are long enough to fill them and still every CU
+    // gets one
+    const auto shrink = [&](auto kXF, auto kAF) {
+        constexpr int kX = decltype(kXF)::value, kA = decltype(kAF)::value;
+        k_shrink<T, kX, kA><<<(uint32_t)(a.rows / (16 * kX) + a.n_groups), shrink_waves<kX>() * 64,
+                              shrink_lds<kX, kA>(), stream>>>(a, px, x_stride, pa, u, group);
+    };
+    typedef std::integral_constant<int, 1> One;
+    typedef std::integral_constant<int, 2> Two;
+    const bool long_groups = a.rows / 32 >= kBigSlots && a.rows / a.n_groups >= 32;
+    if (a.rank <= 16)
+        long_groups ? shrink(Two{}, One{}) : shrink(One{}, One{});
     else
-        k_shrink<T, 1><<<(uint32_t)(a.rows / 16 + a.n_groups), kShrinkWaves * 64, 0, stream>>>(
-            a, px, x_stride, pa, u, group);
+        long_groups ? shrink(Two{}, Two{}) : shrink(One{}, Two{});
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const ProductArgs p = {0, a.rows, x_stride, a.d_in, a.d_out, slices};
@@ -1259,9 +1295,16 @@ hipError_t head(const HeadArgs &h, const void *x, const void *w, hipStream_t str
         const EndHead end = {h.features, base, rows, h.targets, list, count, sp.m, sp.s, sp.t, sp.tl};
         hipError_t e = by_shape<T>(sp.shape, p, px, pw, list, count, end, stream);
         if (e != hipSuccess) return e;
-        k_head_join<<<(uint32_t)((rows + 7) / 8), 1024, 0, stream>>>(
-            sp.m, sp.s, sp.t, sp.tl, sp.parts, base, rows, list, count,
-            h.targets, h.features, h.logp, h.entropy);
+        const auto join = [&](auto of) {
+            constexpr int kOf = decltype(of)::value;
+            k_head_join<kOf><<<(uint32_t)((rows + kOf - 1) / kOf), 1024, 0, stream>>>(
+                sp.m, sp.s, sp.t, sp.tl, sp.parts, base, rows, list, count, h.targets, h.features, h.logp,
+                h.entropy);
+        };
+        if (rows <= 256)
+            join(std::integral_constant<int, 1>{});
+        else
+            join(std::integral_constant<int, 8>{});
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -1279,6 +1322,10 @@ hipError_t prepare()
         raise(&k_big<T, EndProject<T>>, 2 * 512 * 128),
         raise(&k_big<T, EndSlice>, 2 * 512 * 128),
         raise(&k_big<T, EndHead>, 2 * 512 * 128),
+        raise(&k_shrink<T, 1, 1>, shrink_lds<1, 1>()),
+        raise(&k_shrink<T, 1, 2>, shrink_lds<1, 2>()),
+        raise(&k_shrink<T, 2, 1>, shrink_lds<2, 1>()),
+        raise(&k_shrink<T, 2, 2>, shrink_lds<2, 2>()),
         raise(&k_few<T, 1, 1, EndProject<T>>, few_lds<T, 1, 1>()),
         raise(&k_few<T, 1, 2, EndProject<T>>, few_lds<T, 1, 2>()),
         raise(&k_few<T, 2, 1, EndProject<T>>, few_lds<T, 2, 1>()),

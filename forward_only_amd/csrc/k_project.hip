@@ -926,31 +926,42 @@ struct EndSlice {
     }
 };
 
-// Sums the slices of the last tiles and ends them: each wave one wave's tile of k_big, 16 rows.
+// Sums the slices of the last tiles and ends them: a workgroup takes 16 rows of one wave's tile
+// of k_big; its four waves share the slices, and the first adds up and ends.
 template <class T, class End>
 __global__ __launch_bounds__(256) void k_slices(ProductArgs p, const uint32_t *count, End end)
 {
-    __shared__ u32x4 lds[4 * 512];
+    __shared__ u32x4 lds[3 * 8 * 64];
     const uint64_t rows = places(p.base, p.rows, count);
     const Cut cut(p, rows, (p.k + 8 * T::kPiece - 1) / (8 * T::kPiece));
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t i = blockIdx.x / 8;          // 32 waves' shares of a tile, four to a workgroup
+    const uint32_t i = blockIdx.x / 32, of = blockIdx.x / 4 % 8, n = blockIdx.x % 4;
     if (i >= cut.rest || cut.slices < 2) return;
-    const uint32_t of = blockIdx.x % 8, n = wave;
     uint32_t tf, tr;
     tile_at(cut.whole + i, cut.nf, cut.nr, tf, tr);
+    const uint32_t f0 = tf * kBigF + (of & 1) * 128;
+    const uint64_t r0 = (uint64_t)tr * kBigR + (of >> 1) * 64 + n * 16;
+    if (r0 >= rows) return;
     const f32x4 *from = reinterpret_cast<const f32x4 *>(p.slices) +
                         ((uint64_t)i * cut.slices * 8 + of) * 32 * 64 + (n * 8) * 64 + lane;
     Tile<T, 16, 8, 1> t;
     t.clear();
-    for (uint32_t s = 0; s < cut.slices; ++s)
+#pragma unroll 2
+    for (uint32_t s = wave; s < cut.slices; s += 4)
 #pragma unroll
         for (int m = 0; m < 8; ++m) t.acc[m][0] += from[(uint64_t)s * 8 * 32 * 64 + m * 64];
-    const uint32_t f0 = tf * kBigF + (of & 1) * 128;
-    const uint64_t r0 = (uint64_t)tr * kBigR + (of >> 1) * 64 + n * 16;
-    if (r0 >= rows) return;
-    end.finish(t, end.begin(r0), f0, r0, lds + wave * 512);
+    f32x4 *sums = reinterpret_cast<f32x4 *>(lds);
+    if (wave)
+#pragma unroll
+        for (int m = 0; m < 8; ++m) sums[((wave - 1) * 8 + m) * 64 + lane] = t.acc[m][0];
+    __syncthreads();
+    if (wave) return;
+#pragma unroll
+    for (int v = 0; v < 3; ++v)
+#pragma unroll
+        for (int m = 0; m < 8; ++m) t.acc[m][0] += sums[(v * 8 + m) * 64 + lane];
+    end.finish(t, end.begin(r0), f0, r0, lds);
 }
 
 // Middling sizes, where tiles of 256 x 256 would leave CUs without one: 64 features x 64 rows
@@ -1204,7 +1215,7 @@ hipError_t big(const ProductArgs &p, const typename T::elem *x, const typename T
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     const uint32_t most = count ? kBigSlots / 2 : over;
-    k_slices<T, End><<<most * 8, 256, 0, stream>>>(p, count, end);
+    k_slices<T, End><<<most * 32, 256, 0, stream>>>(p, count, end);
     return hipGetLastError();
 }
 

@@ -520,10 +520,12 @@ def _vector(t, name: str, n: int, dtype):
     """Device pointer of a contiguous 1-D tensor of n elements, or None."""
     if t is None:
         return None
-    p = _dev(t, name, dtype)
-    if t.dim() != 1 or t.numel() != n:
-        raise ValueError(f"{name} must hold {n} values in one dimension, got shape {tuple(t.shape)}")
-    return p
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.dim() == 1
+            and t.numel() == n and t.is_contiguous()
+            and t.get_device() == torch.cuda.current_device()):
+        return t.data_ptr()
+    _dev(t, name, dtype)       # says what is wrong, unless it is the shape
+    raise ValueError(f"{name} must hold {n} values in one dimension, got shape {tuple(t.shape)}")
 
 
 def zo_token_logprobs(ctx: Context, logits: torch.Tensor, targets: torch.Tensor | None = None,
@@ -590,10 +592,13 @@ def zo_head_logprobs(ctx: Context, hidden: torch.Tensor, weight: torch.Tensor,
         op = _vector(out.logp, "logp", rows, torch.float32)
         ep = _vector(out.entropy, "entropy", rows, torch.float32)
     if workspace is None:
-        workspace = _new(zo_head_workspace_bytes(rows, d, vocab), torch.uint8, stream)
-    _lib.check(_lib.lib().zo_head_logprobs(
-        ctx.handle, hp, stride, wp, code, rows, d, vocab, tp, op, ep, _dev(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), _stream(stream)), "zo_head_logprobs")
+        wb = zo_head_workspace_bytes(rows, d, vocab)
+        workspace = _new(wb, torch.uint8, stream)
+        ws = workspace.data_ptr()
+    else:
+        ws, wb = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+    _lib.check(_lib.lib().zo_head_logprobs(ctx.handle, hp, stride, wp, code, rows, d, vocab, tp, op, ep,
+                                           ws, wb, _stream(stream)), "zo_head_logprobs")
     return out
 
 
@@ -602,18 +607,19 @@ def zo_group_loss(ctx: Context, logp: torch.Tensor, targets: torch.Tensor | None
                   stream=None) -> torch.Tensor:
     """Mean negative log probability, float64, of the counted rows (target not
     ZO_IGNORE_TOKEN) of each group [starts[g], starts[g + 1]); NaN for a group without any."""
-    rows = logp.numel()
-    lp, sp = _vector(logp, "logp", rows, torch.float32), _dev(starts, "starts", torch.int64)
-    tp = _vector(targets, "targets", rows, torch.int64)
-    n = starts.numel() - 1
-    if starts.dim() != 1 or n < 0:
+    rows, n = logp.numel(), starts.numel() - 1
+    if n < 0:
         raise ValueError("starts must hold the groups' first rows and the end of the last one")
+    lp, sp = _vector(logp, "logp", rows, torch.float32), _vector(starts, "starts", n + 1, torch.int64)
+    tp = _vector(targets, "targets", rows, torch.int64)
     if out is None:
         out = _new(n, torch.float64, stream)
-    if out.numel() < n:
-        raise ValueError("out is too small")
-    _lib.check(_lib.lib().zo_group_loss(ctx.handle, lp, tp, sp, n, rows,
-                                        _dev(out, "out", torch.float64), _stream(stream)),
+        op = out.data_ptr()
+    else:
+        if out.numel() < n:
+            raise ValueError("out is too small")
+        op = _dev(out, "out", torch.float64)
+    _lib.check(_lib.lib().zo_group_loss(ctx.handle, lp, tp, sp, n, rows, op, _stream(stream)),
                "zo_group_loss")
     return out
 
@@ -653,10 +659,10 @@ def zo_adapter_project(ctx: Context, x: torch.Tensor, weight: torch.Tensor,
     if rank < 0 or (adapters.numel() % per if per else adapters.numel()):
         raise ValueError(f"adapters must hold a whole number of adapters of {per} values")
     n_adapters = adapters.numel() // per if per else 0
-    sp = _dev(starts, "starts", torch.int64)
     n = starts.numel() - 1
-    if starts.dim() != 1 or n < 0:
+    if n < 0:
         raise ValueError("starts must hold the groups' first rows and the end of the last one")
+    sp = _vector(starts, "starts", n + 1, torch.int64)
     ip, bp = _vector(ids, "ids", n, torch.int32), _vector(bias, "bias", d_out, x.dtype)
     if (probes is None) != (alphas is None):
         raise ValueError("give both probes and alphas or neither")
@@ -670,16 +676,20 @@ def zo_adapter_project(ctx: Context, x: torch.Tensor, weight: torch.Tensor,
     kp = _rows(bits, n_probes, adapters.numel())
     if out is None:
         out = _new((rows, d_out), x.dtype, stream)
-    yp, yr, yc, ys = _matrix(out, "out", x.dtype)
-    if (yr, yc) != (rows, d_out):
-        raise ValueError(f"out must have shape ({rows}, {d_out}), got {tuple(out.shape)}")
+        yp, ys = out.data_ptr(), d_out
+    else:
+        yp, yr, yc, ys = _matrix(out, "out", x.dtype)
+        if (yr, yc) != (rows, d_out):
+            raise ValueError(f"out must have shape ({rows}, {d_out}), got {tuple(out.shape)}")
     if workspace is None:
-        workspace = _new(zo_adapter_workspace_bytes(rows, d_in, d_out, n_adapters, rank, n,
-                                                    n_probes if bits is None else 0),
-                         torch.uint8, stream)
+        wb = zo_adapter_workspace_bytes(rows, d_in, d_out, n_adapters, rank, n,
+                                        n_probes if bits is None else 0)
+        workspace = _new(wb, torch.uint8, stream)
+        ws = workspace.data_ptr()
+    else:
+        ws, wb = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
     _lib.check(_lib.lib().zo_adapter_project(
         ctx.handle, xp, xs, wp, bp, code, rows, d_in, d_out, ap, n_adapters, rank, float(scale),
-        sp, ip, n, pp, fp, offset, step, probe0, n_probes, kp, _dev(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), yp, ys, _stream(stream)),
+        sp, ip, n, pp, fp, offset, step, probe0, n_probes, kp, ws, wb, yp, ys, _stream(stream)),
         "zo_adapter_project")
     return out

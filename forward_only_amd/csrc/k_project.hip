@@ -1045,18 +1045,22 @@ __global__ __launch_bounds__(256) void k_mid(ProductArgs p, const typename T::el
     end.finish(t, g, f0 + wf * 32, r0 + wr * 32, stage + wave * 512);
 }
 
-// Few rows.  What bounds the product is reading w once: a workgroup takes 16 kMF features and
+// Few rows.  What bounds the product is reading w once: a workgroup takes 16 kFewF features and
 // all rows, four waves take every fourth step of k, and their sums meet in LDS.  kMR more waves
-// form the adapters' products meanwhile, add everything up and end 16 rows each.
-constexpr int kFewWaves = 4, kFewStages = 3;
-template <class T, int kMF, int kMR>
-constexpr uint32_t few_lds() { return kFewWaves * kFewStages * (kMF + kMR) * 16 * 128; }
+// form the adapters' products meanwhile, add everything up and end 16 rows each.  32 features:
+// with 16, x is read from L2 as often again (32 rows, 5120 to 5120, bf16: 14.8 us; 12.0 with
+// 32).  Three stages: two leave too little under way, four one workgroup per CU (8 rows, 5120
+// to 50272: 94 and 97 us; 88 with three, 5.8 TB/s).
+constexpr int kFewF = 2, kFewWaves = 4, kFewStages = 3;
+template <int kMR>
+constexpr uint32_t few_lds() { return kFewWaves * kFewStages * (kFewF + kMR) * 16 * 128; }
 
-template <class T, int kMF, int kMR, class End>
+template <class T, int kMR, class End>
 __global__ __launch_bounds__((kFewWaves + kMR) * 64) void k_few(ProductArgs p,
                                                                 const typename T::elem *x,
                                                                 const typename T::elem *w, End end)
 {
+    constexpr int kMF = kFewF;
     typedef Feed<T, kMF + kMR, kFewStages> F;
     extern __shared__ u32x4 stage[];            // [wave][stage][features, rows], then [wave] of sums
     const int lane = threadIdx.x & 63;
@@ -1229,26 +1233,24 @@ hipError_t mid(const ProductArgs &p, const typename T::elem *x, const typename T
     return hipGetLastError();
 }
 
-// The product of at most kFewRows rows: features per workgroup by how many workgroups that
-// leaves.
-template <class T, int kMF, class End>
-hipError_t few_of(const ProductArgs &p, const typename T::elem *x, const typename T::elem *w,
-                  const End &end, hipStream_t stream)
+template <class T, class End>
+hipError_t few(const ProductArgs &p, const typename T::elem *x, const typename T::elem *w,
+               const End &end, hipStream_t stream)
 {
-    const uint32_t grid = (p.features + 16 * kMF - 1) / (16 * kMF);
+    const uint32_t grid = (p.features + 16 * kFewF - 1) / (16 * kFewF);
     if (p.rows <= 16)
-        k_few<T, kMF, 1, End><<<grid, (kFewWaves + 1) * 64, few_lds<T, kMF, 1>(), stream>>>(p, x, w, end);
+        k_few<T, 1, End><<<grid, (kFewWaves + 1) * 64, few_lds<1>(), stream>>>(p, x, w, end);
     else
-        k_few<T, kMF, 2, End><<<grid, (kFewWaves + 2) * 64, few_lds<T, kMF, 2>(), stream>>>(p, x, w, end);
+        k_few<T, 2, End><<<grid, (kFewWaves + 2) * 64, few_lds<2>(), stream>>>(p, x, w, end);
     return hipGetLastError();
 }
+
 template <class T, class End>
 hipError_t by_shape(Shape shape, const ProductArgs &p, const typename T::elem *x, const typename T::elem *w,
                     const uint32_t *list, const uint32_t *count, const End &end, hipStream_t stream)
 {
     switch (shape) {
-    case Shape::few1: return few_of<T, 1>(p, x, w, end, stream);
-    case Shape::few2: return few_of<T, 2>(p, x, w, end, stream);
+    case Shape::few: return few<T>(p, x, w, end, stream);
     case Shape::mid: return mid<T>(p, x, w, list, count, end, stream);
     case Shape::big: break;
     }
@@ -1290,7 +1292,7 @@ hipError_t head(const HeadArgs &h, const void *x, const void *w, hipStream_t str
 {
     typedef typename T::elem E;
     const HeadSpace sp = head_space(h.rows, h.k, h.features, T::kBf16, h.workspace);
-    const bool small = sp.shape <= Shape::few2;
+    const bool small = sp.shape == Shape::few;
     uint32_t *list = nullptr, *count = nullptr;
     if (h.targets && !small) {
         list = sp.list;
@@ -1337,14 +1339,10 @@ hipError_t prepare()
         raise(&k_shrink<T, 1, 2>, shrink_lds<1, 2>()),
         raise(&k_shrink<T, 2, 1>, shrink_lds<2, 1>()),
         raise(&k_shrink<T, 2, 2>, shrink_lds<2, 2>()),
-        raise(&k_few<T, 1, 1, EndProject<T>>, few_lds<T, 1, 1>()),
-        raise(&k_few<T, 1, 2, EndProject<T>>, few_lds<T, 1, 2>()),
-        raise(&k_few<T, 2, 1, EndProject<T>>, few_lds<T, 2, 1>()),
-        raise(&k_few<T, 2, 2, EndProject<T>>, few_lds<T, 2, 2>()),
-        raise(&k_few<T, 1, 1, EndHead>, few_lds<T, 1, 1>()),
-        raise(&k_few<T, 1, 2, EndHead>, few_lds<T, 1, 2>()),
-        raise(&k_few<T, 2, 1, EndHead>, few_lds<T, 2, 1>()),
-        raise(&k_few<T, 2, 2, EndHead>, few_lds<T, 2, 2>())};
+        raise(&k_few<T, 1, EndProject<T>>, few_lds<1>()),
+        raise(&k_few<T, 2, EndProject<T>>, few_lds<2>()),
+        raise(&k_few<T, 1, EndHead>, few_lds<1>()),
+        raise(&k_few<T, 2, EndHead>, few_lds<2>())};
     for (const hipError_t e : all)
         if (e != hipSuccess) return e;
     return hipSuccess;

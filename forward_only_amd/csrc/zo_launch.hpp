@@ -157,9 +157,9 @@ struct AdapterArgs {
     const uint8_t *bits;           // n_probes packed rows over all adapters' parameters
     uint64_t bits_stride;
 };
-// How a product of rows x features is cut into workgroups: 16 or 32 features and all of at
-// most 32 rows; tiles of 64 x 64; tiles of 256 x 256.
-enum class Shape { few1, few2, mid, big };
+// How a product of rows x features is cut into workgroups: 32 features and all of at most 32
+// rows; tiles of 64 x 64; tiles of 256 x 256.
+enum class Shape { few, mid, big };
 // Tiles of 256 x 256 that run at once (one per CU), the most slices of one along k, the fewest
 // steps of 128 bytes of k that make a slice, and the workspace of all slices of a call.
 constexpr uint32_t kBigSlots = 256, kBigSlices = 16, kBigSliceSteps = 4;
@@ -176,8 +176,7 @@ __host__ __device__ constexpr uint32_t big_slices(uint32_t over, uint32_t steps)
 // or 0.33 us in bf16 while they are at most one per CU; slices cost 25 us to write and add up.
 inline Shape product_shape(uint64_t rows, uint32_t features, uint32_t k, bool bf16)
 {
-    // two fragments of features where that still leaves two workgroups per CU
-    if (rows <= 32) return features >= 2 * 2 * 16 * 256 ? Shape::few2 : Shape::few1;
+    if (rows <= 32) return Shape::few;
     const auto tiles = [&](uint64_t size) {
         return ((uint64_t)features + size - 1) / size * ((rows + size - 1) / size);
     };
@@ -193,7 +192,7 @@ inline Shape product_shape(uint64_t rows, uint32_t features, uint32_t k, bool bf
 }
 inline uint32_t shape_part(Shape s)   // features of one partial softmax: a wave's
 {
-    return s == Shape::few1 ? 16 : s == Shape::big ? 128 : 32;
+    return s == Shape::big ? 128 : 32;
 }
 // Bytes of x A^T, [rows][rank] floats, and of each row's group.
 inline uint64_t adapter_u_bytes(uint64_t rows, uint32_t rank, uint32_t n_groups)

@@ -583,7 +583,7 @@ zo_status zo_head_logprobs(zo_ctx *c, const void *d_hidden, uint64_t hidden_stri
 {
     if (!ctx_ok(c)) return ZO_EINVAL;
     if (dtype != ZO_FP32 && dtype != ZO_BF16) return ZO_EINVAL;
-    if (rows > kMaxRows || vocab > kMaxRows) return ZO_EUNSUPPORTED;
+    if (rows > kMaxRows || vocab > kMaxRows || d > kMaxRows) return ZO_EUNSUPPORTED;
     if (rows == 0) return ZO_OK;
     if (vocab == 0 || d == 0 || d % 8u || hidden_stride % 8u) return ZO_EINVAL;
     if (!d_hidden || !d_weight || !aligned16(d_hidden) || !aligned16(d_weight)) return ZO_EINVAL;
@@ -638,7 +638,9 @@ zo_status zo_adapter_project(zo_ctx *c, const void *d_x, uint64_t x_stride, cons
 {
     if (!ctx_ok(c)) return ZO_EINVAL;
     if (dtype != ZO_FP32 && dtype != ZO_BF16) return ZO_EINVAL;
-    if (rank > ZO_MAX_RANK || rows > kMaxRows || n_groups > kMaxRows) return ZO_EUNSUPPORTED;
+    if (rank > ZO_MAX_RANK || rows > kMaxRows || n_groups > kMaxRows || d_in > kMaxRows ||
+        d_out > kMaxRows)
+        return ZO_EUNSUPPORTED;
     if (d_in == 0 || d_in % 8u || d_out % 8u || rank % 8u || x_stride % 8u || y_stride % 8u)
         return ZO_EINVAL;
     if ((d_probes == nullptr) != (d_alphas == nullptr)) return ZO_EINVAL;

@@ -748,16 +748,17 @@ __device__ __forceinline__ uint32_t tile_of_xcd(uint32_t b, uint32_t n)
 
 // Many rows: 256 features x 256 rows by eight waves of 128 x 64, in which the two waves of a
 // SIMD take turns: four of the waves multiply while the other four read their next operands
-// from LDS, one barrier apart.  A step of 128 bytes of k has four such turns, one for each
-// quarter of a wave's tile:
-//   turn 0  reads F0, the first half of its features        multiplies (F0, R0)
-//   turn 1  reads F1, the second half                       multiplies (F1, R0)
-//   turn 2  reads R1, the second half of its rows           multiplies (F1, R1)
-//   turn 3  reads R0, the first half, of the next step      multiplies (F0, R1)
-// A quarter of the stage is free for the step after next as soon as both groups have read it,
-// so its loads go out one turn later and have one and a half steps to arrive; each turn waits
-// for the loads that the next turn reads: all but the twelve issued since.  Loads past the end
-// of k read zeros, so that the counts hold to the end.
+// from LDS, one barrier apart.  A step of 128 bytes of k has two such turns, one for each half
+// of a wave's features:
+//   turn 0  reads F0, the first half of its features, and its rows R   multiplies (F0, R)
+//   turn 1  reads F1, the second half                                  multiplies (F1, R)
+// A part of the stage is free for the step after next as soon as both groups have read it, so
+// its loads go out one turn later and have one and a half steps to arrive; each turn waits for
+// the loads that the next turn reads: all but the eight issued since.  Loads past the end of k
+// read zeros, so that the counts hold to the end.  Four turns of a quarter each, with operands
+// read one turn ahead, were no faster and took 96 registers for operands instead of 64.
+// What bounds it: MFMA issue 65% of the cycles at a clock that the load lowers (LDS reads and
+// writes take as many cycles as the products): 1475 TFLOP/s of bf16 at 4096 x 50272 x 7168.
 //
 // Tiles run one per CU, so their number is cut into whole rounds of kSlots and a rest.  When the
 // rest fills at most half a round, each of its tiles is cut along k into as many slices as
@@ -844,23 +845,26 @@ __global__ __launch_bounds__(512, 2) void k_big(ProductArgs p, const typename T:
     };
     Tile<T, 16, 8, 4> t;
     t.clear();
-    u32x4 ff[2][2][4], fr[2][2][2];             // [half][c][fragment]
+    u32x4 ff[2][4], fr[2][4];                   // [c][fragment]
     const auto read_f = [&](int h, uint32_t step) {
         const u32x4 *s = stage + ((step & 1) * 4 + F0 + h) * kPart + (wf * 64 + l16) * kPieces;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int m = 0; m < 4; ++m) ff[h][c][m] = s[m * 16 * kPieces + ((4 * c + q) ^ (l16 >> 1))];
+            for (int m = 0; m < 4; ++m) ff[c][m] = s[m * 16 * kPieces + ((4 * c + q) ^ (l16 >> 1))];
     };
-    const auto read_r = [&](int h, uint32_t step) {
-        const u32x4 *s = stage + ((step & 1) * 4 + R0 + h) * kPart + (wr * 32 + l16) * kPieces;
+    const auto read_r = [&](uint32_t step) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int h = 0; h < 2; ++h) {
+            const u32x4 *s = stage + ((step & 1) * 4 + R0 + h) * kPart + (wr * 32 + l16) * kPieces;
 #pragma unroll
-            for (int n = 0; n < 2; ++n) fr[h][c][n] = s[n * 16 * kPieces + ((4 * c + q) ^ (l16 >> 1))];
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int n = 0; n < 2; ++n) fr[c][2 * h + n] = s[n * 16 * kPieces + ((4 * c + q) ^ (l16 >> 1))];
+        }
     };
-    const auto multiply = [&](int hf, int hr) {
-        wait_for<12, true>();
+    const auto multiply = [&](int hf) {
+        wait_for<8, true>();
         turn_barrier();
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
@@ -868,40 +872,33 @@ __global__ __launch_bounds__(512, 2) void k_big(ProductArgs p, const typename T:
 #pragma unroll
             for (int m = 0; m < 4; ++m)
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-                    t.acc[4 * hf + m][2 * hr + n] =
-                        T::mma(ff[hf][c][m], fr[hr][c][n], t.acc[4 * hf + m][2 * hr + n]);
+                for (int n = 0; n < 4; ++n)
+                    t.acc[4 * hf + m][n] = T::mma(ff[c][m], fr[c][n], t.acc[4 * hf + m][n]);
         __builtin_amdgcn_s_setprio(0);
         turn_barrier();
     };
-        uint32_t begun = 0;
-#pragma unroll
-    for (uint32_t s = 0; s < 2; ++s) {
-        issue(R0, first + s);
-        issue(F0, first + s);
-        issue(F1, first + s);
-        issue(R1, first + s);
-        if (s == 0) begun = end.begin(r0 + wr * 64);
-    }
-    wait_for<12, false>();                      // R0 and F0 of the first step
-    turn_barrier();
-    read_r(0, first);
-    wait_for<63, true>();
+    uint32_t begun = 0;
+    issue(F0, first);
+    issue(R0, first);
+    issue(R1, first);
+    issue(F1, first);
+    begun = end.begin(r0 + wr * 64);
+    issue(F0, first + 1);
+    issue(R0, first + 1);
+    issue(R1, first + 1);
+    wait_for<8, false>();                       // F0, R0 and R1 of the first step
     turn_barrier();
     if (wave >= 4) turn_barrier();              // one turn behind from here on
     for (uint32_t s = first; s < last; ++s) {
         read_f(0, s);
-        issue(R0, s + 2);
-        multiply(0, 0);
+        read_r(s);
+        issue(F1, s + 1);
+        multiply(0);
         read_f(1, s);
         issue(F0, s + 2);
-        multiply(1, 0);
-        read_r(1, s);
-        issue(F1, s + 2);
-        multiply(1, 1);
-        read_r(0, s + 1);
+        issue(R0, s + 2);
         issue(R1, s + 2);
-        multiply(0, 1);
+        multiply(1);
     }
     if (wave < 4) turn_barrier();
     wait_for<0, true>();
@@ -1014,9 +1011,9 @@ __global__ __launch_bounds__(256) void k_mid(ProductArgs p, const typename T::el
     };
     Tile<T, 16, 2, 2> t;
     t.clear();
-    const auto g = end.begin(r0 + wr * 32);
 #pragma unroll
     for (uint32_t s = 0; s < kMidStages - 1; ++s) issue(s);
+    const auto g = end.begin(r0 + wr * 32);
     for (uint32_t s = 0; s < steps; ++s) {
         wait_for<4 * (kMidStages - 2), true>();     // this step's loads
         turn_barrier();                             // everyone's; and the last step's readers are done
@@ -1128,30 +1125,43 @@ __global__ __launch_bounds__((kFewWaves + kMR) * 64) void k_few(ProductArgs p,
 // ---- joining the head's partial statistics ----------------------------------------------
 
 // The places of the rows that count, in order, and zeros for the others' outputs; one
-// workgroup.
+// workgroup, eight rows of a thread in flight at once.
 __global__ __launch_bounds__(1024) void k_counted(const int64_t *targets, uint64_t rows,
                                                   uint32_t *list, uint32_t *count, float *logp,
                                                   float *entropy)
 {
-    __shared__ uint32_t waves[16];
+    constexpr int kAtOnce = 8;
+    __shared__ uint32_t waves[kAtOnce][16];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     uint32_t at = 0;
-    for (uint64_t r0 = 0; r0 < rows; r0 += 1024) {
-        const uint64_t r = r0 + tid;
-        const bool in = r < rows && targets[r] != kIgnoreToken;
-        const uint64_t votes = __ballot(in);
-        if (lane == 0) waves[wave] = __popcll(votes);
-        __syncthreads();
-        uint32_t before = at;
-        for (int w = 0; w < 16; ++w) {
-            if (w < wave) before += waves[w];
-            at += waves[w];
+    for (uint64_t r0 = 0; r0 < rows; r0 += 1024 * kAtOnce) {
+        int64_t t[kAtOnce];
+        uint64_t votes[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const uint64_t r = r0 + i * 1024 + tid;
+            t[i] = targets[r < rows ? r : 0];
         }
-        if (in) {
-            list[before + __popcll(votes & (((uint64_t)1 << lane) - 1))] = (uint32_t)r;
-        } else if (r < rows) {
-            if (logp) logp[r] = 0.0f;
-            if (entropy) entropy[r] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            votes[i] = __ballot(r0 + i * 1024 + tid < rows && t[i] != kIgnoreToken);
+            if (lane == 0) waves[i][wave] = __popcll(votes[i]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            uint32_t before = at;
+            for (int w = 0; w < 16; ++w) {
+                if (w < wave) before += waves[i][w];
+                at += waves[i][w];
+            }
+            const uint64_t r = r0 + i * 1024 + tid;
+            if (votes[i] >> lane & 1) {
+                list[before + __popcll(votes[i] & (((uint64_t)1 << lane) - 1))] = (uint32_t)r;
+            } else if (r < rows) {
+                if (logp) logp[r] = 0.0f;
+                if (entropy) entropy[r] = 0.0f;
+            }
         }
         __syncthreads();
     }

@@ -411,8 +411,8 @@ zo_status zo_token_logprobs(zo_ctx *ctx, const void *d_logits, zo_dtype dtype, u
  * and d_entropy.  d_workspace: device, 256-byte aligned, at least
  * zo_head_workspace_bytes(rows, d, vocab) bytes.  Deterministic.
  * Errors: ZO_EINVAL as zo_token_logprobs, shapes outside these limits, a workspace that is
- * too small or misaligned; ZO_EUNSUPPORTED if rows or vocab exceed 2^31 - 1, or the rows of
- * d_hidden reach over more than 64 GiB. */
+ * too small or misaligned; ZO_EUNSUPPORTED if rows, d or vocab exceed 2^31 - 1, or the rows
+ * of d_hidden reach over more than 64 GiB. */
 uint64_t zo_head_workspace_bytes(uint64_t rows, uint32_t d, uint32_t vocab);
 zo_status zo_head_logprobs(zo_ctx *ctx, const void *d_hidden, uint64_t hidden_stride,
                            const void *d_weight, zo_dtype dtype, uint64_t rows, uint32_t d,
@@ -460,8 +460,8 @@ zo_status zo_group_loss(zo_ctx *ctx, const float *d_logp, const int64_t *d_targe
  * Errors: ZO_EINVAL for NULL pointers (with rows and n_groups > 0; d_adapters may be NULL
  * with n_adapters == 0 or rank == 0), unknown dtype, shapes and strides outside these limits,
  * misalignment, offset % 128 != 0 or range overflow, probe indices past 2^32 - 1, a
- * workspace that is too small; ZO_EUNSUPPORTED if rank > ZO_MAX_RANK, rows or n_groups exceed
- * 2^31 - 1, or the rows of d_x reach over more than 64 GiB.  rows == 0, d_out == 0 or n_groups == 0 launches nothing. */
+ * workspace that is too small; ZO_EUNSUPPORTED if rank > ZO_MAX_RANK, rows, n_groups, d_in or
+ * d_out exceed 2^31 - 1, or the rows of d_x reach over more than 64 GiB.  rows == 0, d_out == 0 or n_groups == 0 launches nothing. */
 uint64_t zo_adapter_workspace_bytes(uint64_t rows, uint32_t d_in, uint32_t d_out,
                                     uint32_t n_adapters, uint32_t rank, uint32_t n_groups,
                                     uint32_t regenerated);

@@ -20,10 +20,13 @@ update run in libzo's kernels on torch's current stream.  Losses stay on the dev
 """
 from __future__ import annotations
 
+from typing import NamedTuple, Optional
+
 import numpy as np
 import torch
 
-from . import zo_perturb, zo_perturb2, zo_probe_weights, zo_restore_update, zo_update
+from . import (zo_group_loss, zo_perturb, zo_perturb2, zo_probe_weights, zo_restore_update,
+               zo_update)
 
 
 def applied_eps(eps: float) -> float:
@@ -129,3 +132,78 @@ def spsa_step_fused(ctx, theta: torch.Tensor, *, step: int, npert: int, eps: flo
     c = zo_probe_weights(ctx, Lp, Lm, L0, a, delta, out=b.get("c"))
     zo_update(ctx, theta, offset, step, c, eta, bits)
     return {"L0": L0, "Lp": Lp, "Lm": Lm, "c": c}
+
+
+class AdapterGroups(NamedTuple):
+    """The groups of one batch of probes: what zo_adapter_project needs besides the operands.
+    `zo_adapter_project(ctx, x, weight, adapters, rank, **groups.of_project())`."""
+    starts: torch.Tensor
+    ids: torch.Tensor
+    probes: torch.Tensor
+    alphas: torch.Tensor
+    offset: int = 0
+    step: int = 0
+    probe0: int = 0
+    n_probes: int = 0
+    bits: Optional[torch.Tensor] = None
+
+    def of_project(self) -> dict:
+        return self._asdict()
+
+
+def adapter_probe_groups(n_probes: int, rows: int, alpha: float, *, clean: bool = True,
+                         adapter: int = 0, offset: int = 0, step: int = 0, probe0: int = 0,
+                         bits=None, device="cuda") -> AdapterGroups:
+    """Groups of a batch that holds `rows` rows for theta + alpha z_i and `rows` for
+    theta - alpha z_i of each probe probe0 + i (groups 2 i and 2 i + 1), then, with `clean`,
+    `rows` for the adapter as it is."""
+    g = torch.arange(2 * n_probes + (1 if clean else 0), dtype=torch.int32)
+    moved = g < 2 * n_probes
+    probes = torch.where(moved, g // 2, torch.full_like(g, -1))
+    sign = torch.where(g % 2 == 0, 1.0, -1.0) * moved
+    return AdapterGroups(
+        starts=(torch.arange(g.numel() + 1) * rows).to(device), ids=torch.full_like(g, adapter).to(device),
+        probes=probes.to(device), alphas=(sign * alpha).to(torch.float32).to(device), offset=offset,
+        step=step, probe0=probe0, n_probes=n_probes, bits=bits)
+
+
+def spsa_step_adapters(ctx, adapters: torch.Tensor, *, step: int, npert: int, eps: float, eta: float,
+                       delta: float, logp_of, targets: torch.Tensor, offset: int = 0, bits=None,
+                       probes_per_batch: int = 32, buffers: dict | None = None) -> dict:
+    """One step on a flat buffer of one low-rank adapter, in which batches of probes run
+    through the model together and share each load of its weights.
+
+    targets: int64 [rows] of the batch's rows (ZO_IGNORE_TOKEN rows do not count).
+    logp_of(groups) runs the model on the batch's rows once per group, in the order of
+    adapter_probe_groups -- its adapted projections with zo_adapter_project(ctx, x, weight,
+    adapters, rank, **groups.of_project()) -- and returns the targets' log probabilities,
+    float32 [groups * rows] (zo_head_logprobs or zo_token_logprobs, with targets repeated
+    once per group).  The loss of a group is its mean negative log probability
+    (zo_group_loss).  At most probes_per_batch probes go through the model at once; the
+    adapters are only written by the update.  Other arguments and the result as
+    spsa_step_fused.
+    """
+    if probes_per_batch < 1:
+        raise ValueError("probes_per_batch must be positive")
+    rows = targets.numel()
+
+    def losses(probe0, n, alpha, packed, plus, minus, clean):
+        done = 0
+        while True:
+            m = min(n - done, probes_per_batch)
+            groups = adapter_probe_groups(
+                m, rows, alpha, clean=done == 0, offset=offset, step=step, probe0=probe0 + done,
+                bits=None if packed is None else packed[done:done + m], device=adapters.device)
+            logp = logp_of(groups)
+            loss = zo_group_loss(ctx, logp, targets.repeat(groups.ids.numel()), groups.starts)
+            plus[done:done + m] = loss[0:2 * m:2]
+            minus[done:done + m] = loss[1:2 * m:2]
+            if done == 0:
+                clean.copy_(loss[2 * m:])
+            done += m
+            if done >= n:
+                return
+
+    return spsa_step_fused(ctx, adapters, step=step, npert=npert, eps=eps, eta=eta, delta=delta,
+                           offset=offset, bits=bits, buffers=buffers, loss_probes_at=losses,
+                           probes_give_clean=True)

@@ -411,6 +411,59 @@ def test_step_with_adapters(ctx, dtype, mode):
     assert torch.equal(want, theta) and not torch.equal(theta, before)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("mode", ["bits", "regen"])
+@pytest.mark.parametrize("npert,per", [(5, 32), (5, 2), (1, 1), (0, 4)])
+def test_spsa_step_adapters(ctx, dtype, mode, npert, per):
+    """The step in batches of probes equals one forward per probe and sign at adapters that
+    zo_perturb moved, then the weights and zo_update."""
+    from forward_only_amd.step import spsa_step_adapters
+    rank, d_in, d_out, vocab, T, offset, step = 16, 64, 72, 211, 9, 128, 4
+    p = _problem([T], d_in, d_out, rank, 1, dtype, seed=21)
+    gen = torch.Generator().manual_seed(22)
+    head = _rand(gen, vocab, d_out, std=0.3, dtype=dtype).cuda()
+    t = torch.randint(0, vocab, (T,), generator=gen)
+    t[:4] = zo.ZO_IGNORE_TOKEN
+    t = t.cuda()
+    d = {k: v.cuda() for k, v in p.items()}
+    theta = d["ad"].clone()
+    eps, eta, delta = 2.0 ** -6, 1e-3, 1e-6
+    bits = None
+    if mode == "bits" and npert:
+        bits = zo.zo_gen_probes(ctx, step, 0, npert, offset, theta.numel())
+
+    def logp_of(groups):
+        G = groups.ids.numel()
+        y = zo.zo_adapter_project(ctx, d["x"].repeat(G, 1), d["w"], theta, rank, bias=d["bias"],
+                                  **groups.of_project())
+        return zo.zo_head_logprobs(ctx, y, head, t.repeat(G), entropy=False).logp
+
+    res = spsa_step_adapters(ctx, theta, step=step, npert=npert, eps=eps, eta=eta, delta=delta,
+                             logp_of=logp_of, targets=t, offset=offset, bits=bits, probes_per_batch=per)
+    one = torch.tensor([0, T]).cuda()
+    none = torch.zeros(1, dtype=torch.int32).cuda()
+
+    def loss(th):
+        y = zo.zo_adapter_project(ctx, d["x"], d["w"], th, rank, one, none, bias=d["bias"])
+        lp = zo.zo_head_logprobs(ctx, y, head, t, entropy=False).logp
+        return zo.zo_group_loss(ctx, lp, t, one).item()
+
+    # the same products in tiles of another shape: sums in another order (fp32, relative 1e-6 of
+    # the logits), and in bf16 now and then the next value of y (2^-8 of a term of a logit)
+    tol = 3e-2 if dtype == BF else 2e-5
+    assert abs(res["L0"].item() - loss(d["ad"])) < tol
+    for i in range(npert):
+        for a, got in ((eps, res["Lp"]), (-eps, res["Lm"])):
+            th = d["ad"].clone()
+            zo.zo_perturb(ctx, th, offset, step, i, a)
+            assert abs(got[i].item() - loss(th)) < tol
+    want = d["ad"].clone()
+    c = zo.zo_probe_weights(ctx, res["Lp"], res["Lm"], res["L0"], eps, delta)
+    assert torch.equal(c, res["c"])
+    zo.zo_update(ctx, want, offset, step, c, eta, bits)
+    assert torch.equal(want, theta)
+
+
 def test_streams_and_replayed_graph(ctx):
     p = [{k: v.cuda() for k, v in _problem([30, 50, 1], 264, 136, 16, 2, BF, seed=s).items()} for s in (1, 2)]
     gen = torch.Generator().manual_seed(5)

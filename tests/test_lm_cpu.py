@@ -72,3 +72,15 @@ def test_project_reference_agrees_with_a_dense_adapter():
     ref.assert_close(y[:2], dense, 1e-12, "adapter 1")
     ref.assert_close(y[2:5], x[2:5].double() @ w.double().t(), 1e-12, "none")
     assert torch.isnan(y[5]).all() and (bound > 0).all()
+
+
+def test_probe_groups_of_a_batch():
+    from forward_only_amd.step import adapter_probe_groups
+    g = adapter_probe_groups(3, 5, 0.25, probe0=7, step=2, offset=128, device="cpu")
+    assert g.starts.tolist() == [0, 5, 10, 15, 20, 25, 30, 35] and g.starts.dtype == torch.int64
+    assert g.probes.tolist() == [0, 0, 1, 1, 2, 2, -1] and g.probes.dtype == torch.int32
+    assert g.alphas.tolist() == [0.25, -0.25, 0.25, -0.25, 0.25, -0.25, 0.0]
+    assert g.ids.tolist() == [0] * 7 and g.of_project()["n_probes"] == 3
+    assert adapter_probe_groups(2, 4, 1.0, clean=False, device="cpu").probes.tolist() == [0, 0, 1, 1]
+    only = adapter_probe_groups(0, 4, 1.0, device="cpu")
+    assert only.probes.tolist() == [-1] and only.starts.tolist() == [0, 4]

@@ -1194,8 +1194,12 @@ __global__ __launch_bounds__(1024) void k_head_join(const float *m, const float 
         all[wave][of][2] = st.t;
     }
     __syncthreads();
-    if (threadIdx.x >= kOf || at >= n) return;
-    for (int w = 1; w < 16; ++w) st.merge({all[w][of][0], all[w][of][1], all[w][of][2]});
+    if (wave) return;
+    st = SoftStats::empty();
+#pragma unroll
+    for (int w = lane / kOf; w < 16; w += kWave / kOf) st.merge({all[w][of][0], all[w][of][1], all[w][of][2]});
+    st.wave_merge(32, kOf);
+    if (lane >= kOf || at >= n) return;
     const uint64_t row = list ? list[base + at] : base + at;
     const int64_t tgt = targets ? targets[row] : 0;
     const bool ignore = targets && tgt == kIgnoreToken;

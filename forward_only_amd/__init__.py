@@ -492,6 +492,9 @@ def _new(shape, dtype, stream):
     """A new tensor that belongs to the stream the call runs on."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device="cuda")
+    if stream.device.index != torch.cuda.current_device():
+        raise ValueError(f"stream is on {stream.device}, not on the current device "
+                         f"cuda:{torch.cuda.current_device()}")
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device="cuda")
 

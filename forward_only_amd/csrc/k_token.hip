@@ -75,6 +75,7 @@ struct Row {
 };
 
 constexpr uint64_t kTokenFewRows = 512;
+constexpr uint32_t kTokenLong = 16384;  // two pieces or more for each of 1024 threads
 constexpr uint32_t kCandidates = 2048;  // keys that the search for the alternatives can hold
 
 // The place of each of 64 keys (one per lane, 0: none) among them, largest first.
@@ -97,8 +98,10 @@ __device__ __forceinline__ uint64_t bound_of(const uint64_t *keys, uint32_t k)
 }
 
 // One workgroup per row, one pass over it: each thread loads four pieces, takes their largest
-// value first (it rescales the sums at most once per four pieces) and adds up.  What bounds it
-// is HBM for many rows and the latency of one round of loads for few.
+// value first (it rescales the sums at most once per four pieces) and adds up.  A value costs
+// 12.4 issue slots (widen, half a max3, subtract, scale, an exponential of four, add, bound,
+// multiply-add), which is what bounds many bf16 rows, next to HBM (16384 rows of 50272: 280 us,
+// 5.9 TB/s); few rows are bound by the latency of a round of loads and of the search.
 //
 // Alternatives.  The maxima of 64 parts of the row (one per kThreads / 64 threads) are at hand
 // from the pass; the k-th largest of them bounds the k-th largest value from below, so only
@@ -153,11 +156,13 @@ __global__ __launch_bounds__(kThreads) void k_token(
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
             v[u] = i + u * kThreads < row.pieces ? row.piece(i + u * kThreads) : Row<T>::nothing();
+        float x[kUnroll * kPiece];
         float top = -INFINITY;
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-            for (int j = 0; j < kPiece; ++j) top = fmaxf(top, Row<T>::value(v[u], j));
+        for (int j = 0; j < kUnroll * kPiece; ++j) {
+            x[j] = Row<T>::value(v[j / kPiece], j % kPiece);
+            top = fmaxf(top, x[j]);
+        }
         if (top > best || where == kNone) {
             best = top;
             where = i;
@@ -165,14 +170,12 @@ __global__ __launch_bounds__(kThreads) void k_token(
         st.raise(top);
         const float m = st.m == -INFINITY ? 0.0f : st.m;
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-            for (int j = 0; j < kPiece; ++j) {
-                const float d = Row<T>::value(v[u], j) - m;
-                const float e = fast_exp(d);
-                st.s += e;
-                st.t = fmaf(e, fmaxf(d, -1e4f), st.t);     // d = -inf: e is 0, add 0
-            }
+        for (int j = 0; j < kUnroll * kPiece; ++j) {
+            const float d = x[j] - m;
+            const float e = fast_exp(d);
+            st.s += e;
+            st.t = fmaf(e, fmaxf(d, -1e4f), st.t);     // d = -inf: e is 0, add 0
+        }
     }
     if (row.rest() + tid < vocab) one(widen(row.p[row.rest() + tid]), kRest);
 
@@ -352,18 +355,18 @@ hipError_t launch_token_logprobs(const void *logits, bool bf16, uint64_t rows, u
                                  float *entropy, uint32_t top_k, int64_t *top_ids,
                                  float *top_logp, hipStream_t stream)
 {
-    // Few rows (up to two per CU): all of a row's loads should be in flight at once, so 1024
-    // threads take it.  Many rows hide each other's latency: the pass alone is then fastest
-    // with 256 threads (8192 rows of 50272 bf16: 149 us; 149 with 512, 207 with 1024), and the
-    // search for alternatives, serial within a row, with 512 (top 20: 200 us; 219 with 256,
-    // 312 with 1024).
+    // Few long rows (up to two per CU): all of a row's loads should be in flight at once, so
+    // 1024 threads take it.  Many rows hide each other's latency: the pass alone is then
+    // fastest with 256 threads (8192 rows of 50272 bf16: 149 us; 149 with 512, 207 with 1024),
+    // and the search for alternatives, serial within a row, with 512 (top 20: 200 us; 219 with
+    // 256, 312 with 1024).
     const auto launch = [&](auto *p, auto threads) {
         using E = std::remove_cv_t<std::remove_pointer_t<decltype(p)>>;
         k_token<E, decltype(threads)::value><<<(uint32_t)rows, decltype(threads)::value, 0, stream>>>(
             p, vocab, stride, targets, logp, entropy, top_k, top_ids, top_logp);
     };
     const auto typed = [&](auto *p) {
-        if (rows <= kTokenFewRows)
+        if (rows <= kTokenFewRows && vocab >= kTokenLong)
             launch(p, std::integral_constant<int, 1024>());
         else if (top_k)
             launch(p, std::integral_constant<int, 512>());

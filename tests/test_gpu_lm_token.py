@@ -275,3 +275,25 @@ def test_streams_and_replayed_graph(ctx):
         for a, b in zip(out, want[i]):
             assert torch.equal(a, b)
         both(x[1 - i])
+
+
+@pytest.mark.parametrize("rows", [2, 600])
+@pytest.mark.parametrize("vocab", [40, 700, 2100, 4095, 16383, 16384, 20000])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_most_alternatives_at_every_workgroup_size(ctx, rows, vocab, dtype):
+    """32 alternatives where the row is short for its workgroup, with ties and masked values."""
+    x = _logits(rows, vocab, dtype, vocab + rows, std=1.0)
+    x[0, :] = -math.inf
+    x[0, 3:30:2] = 1.0                       # fewer allowed than asked for
+    x[1] = torch.round(x[1].float()).to(dtype)
+    _check(ctx, x, None, 32)
+    _check(ctx, x, torch.arange(rows) % 32 * 0 + 3, 7)
+
+
+def test_stream_of_another_device_is_refused(ctx):
+    class Other:
+        device = torch.device("cuda", torch.cuda.current_device() + 1)
+        cuda_stream = 0
+    x = torch.zeros(2, 64, device="cuda")
+    with pytest.raises(ValueError):
+        zo.zo_token_logprobs(ctx, x, None, stream=Other())

@@ -71,10 +71,10 @@ class Context:
             pass
 
 
-def _stream(stream=None) -> int:
+def _stream(stream=None, dev: int | None = None) -> int:
     # the raw handle of the current stream: 0.1 us, 2.8 us through a torch.cuda.Stream object
-    return (stream.cuda_stream if stream is not None
-            else torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    return (stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(
+        torch.cuda.current_device() if dev is None else dev))
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -519,13 +519,14 @@ def _matrix(t: torch.Tensor, name: str, dtype=None):
     return t.data_ptr(), rows, cols, t.stride(0) if rows > 1 else cols
 
 
-def _vector(t, name: str, n: int, dtype):
-    """Device pointer of a contiguous 1-D tensor of n elements, or None."""
+def _vector(t, name: str, n: int, dtype, dev: int | None = None):
+    """Device pointer of a contiguous 1-D tensor of n elements, or None.  dev: the current
+    device, where it is known from another argument's check."""
     if t is None:
         return None
     if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.dim() == 1
             and t.numel() == n and t.is_contiguous()
-            and t.get_device() == torch.cuda.current_device()):
+            and t.get_device() == (torch.cuda.current_device() if dev is None else dev)):
         return t.data_ptr()
     _dev(t, name, dtype)       # says what is wrong, unless it is the shape
     raise ValueError(f"{name} must hold {n} values in one dimension, got shape {tuple(t.shape)}")
@@ -539,9 +540,10 @@ def zo_token_logprobs(ctx: Context, logits: torch.Tensor, targets: torch.Tensor 
     vocab] in one pass.  targets: int64 [rows]; ZO_IGNORE_TOKEN rows are not read and give
     0, 0, -1, 0; None gives no logp.  out: tensors of an earlier call of the same shapes."""
     lp, rows, vocab, stride = _matrix(logits, "logits")
+    dev = logits.get_device()
     top_k = int(top_k)
     code = _dtype_code(logits)
-    tp = _vector(targets, "targets", rows, torch.int64)
+    tp = _vector(targets, "targets", rows, torch.int64, dev)
     if not 0 <= top_k <= ZO_MAX_TOP_K:
         raise ValueError(f"top_k must be in [0, {ZO_MAX_TOP_K}]")
     if out is None:
@@ -563,7 +565,7 @@ def zo_token_logprobs(ctx: Context, logits: torch.Tensor, targets: torch.Tensor 
             if tuple(out.top_ids.shape) != (rows, top_k) or tuple(out.top_logp.shape) != (rows, top_k):
                 raise ValueError(f"top_ids and top_logp must have shape ({rows}, {top_k})")
     _lib.check(_lib.lib().zo_token_logprobs(ctx.handle, lp, code, rows, vocab, stride, tp, op, ep,
-                                            top_k, ip, vp, _stream(stream)), "zo_token_logprobs")
+                                            top_k, ip, vp, _stream(stream, dev)), "zo_token_logprobs")
     return out
 
 
@@ -579,12 +581,13 @@ def zo_head_logprobs(ctx: Context, hidden: torch.Tensor, weight: torch.Tensor,
     [rows, d], weight [vocab, d] contiguous, one dtype, d a multiple of 8), which are never
     stored; rows with the target ZO_IGNORE_TOKEN are not computed and give 0, 0."""
     hp, rows, d, stride = _matrix(hidden, "hidden")
+    dev = hidden.get_device()
     code = _dtype_code(hidden)
     wp = _dev(weight, "weight", hidden.dtype)
     if weight.dim() != 2 or weight.shape[1] != d:
         raise ValueError(f"weight must have shape (vocab, {d}), got {tuple(weight.shape)}")
     vocab = weight.shape[0]
-    tp = _vector(targets, "targets", rows, torch.int64)
+    tp = _vector(targets, "targets", rows, torch.int64, dev)
     if out is None:
         out = HeadLogprobs(None if tp is None else _new(rows, torch.float32, stream),
                            _new(rows, torch.float32, stream) if entropy else None)
@@ -601,7 +604,7 @@ def zo_head_logprobs(ctx: Context, hidden: torch.Tensor, weight: torch.Tensor,
     else:
         ws, wb = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
     _lib.check(_lib.lib().zo_head_logprobs(ctx.handle, hp, stride, wp, code, rows, d, vocab, tp, op, ep,
-                                           ws, wb, _stream(stream)), "zo_head_logprobs")
+                                           ws, wb, _stream(stream, dev)), "zo_head_logprobs")
     return out
 
 
@@ -613,8 +616,9 @@ def zo_group_loss(ctx: Context, logp: torch.Tensor, targets: torch.Tensor | None
     rows, n = logp.numel(), starts.numel() - 1
     if n < 0:
         raise ValueError("starts must hold the groups' first rows and the end of the last one")
-    lp, sp = _vector(logp, "logp", rows, torch.float32), _vector(starts, "starts", n + 1, torch.int64)
-    tp = _vector(targets, "targets", rows, torch.int64)
+    lp, dev = _vector(logp, "logp", rows, torch.float32), logp.get_device()
+    sp = _vector(starts, "starts", n + 1, torch.int64, dev)
+    tp = _vector(targets, "targets", rows, torch.int64, dev)
     if out is None:
         out = _new(n, torch.float64, stream)
         op = out.data_ptr()
@@ -622,7 +626,7 @@ def zo_group_loss(ctx: Context, logp: torch.Tensor, targets: torch.Tensor | None
         if out.numel() < n:
             raise ValueError("out is too small")
         op = _dev(out, "out", torch.float64)
-    _lib.check(_lib.lib().zo_group_loss(ctx.handle, lp, tp, sp, n, rows, op, _stream(stream)),
+    _lib.check(_lib.lib().zo_group_loss(ctx.handle, lp, tp, sp, n, rows, op, _stream(stream, dev)),
                "zo_group_loss")
     return out
 
@@ -652,6 +656,7 @@ def zo_adapter_project(ctx: Context, x: torch.Tensor, weight: torch.Tensor,
     n_probes has to be given.  Rows of no group are left as they were (undefined in a new
     y)."""
     xp, rows, d_in, xs = _matrix(x, "x")
+    dev = x.get_device()
     code = _dtype_code(x)
     wp = _dev(weight, "weight", x.dtype)
     if weight.dim() != 2 or weight.shape[1] != d_in:
@@ -665,11 +670,12 @@ def zo_adapter_project(ctx: Context, x: torch.Tensor, weight: torch.Tensor,
     n = starts.numel() - 1
     if n < 0:
         raise ValueError("starts must hold the groups' first rows and the end of the last one")
-    sp = _vector(starts, "starts", n + 1, torch.int64)
-    ip, bp = _vector(ids, "ids", n, torch.int32), _vector(bias, "bias", d_out, x.dtype)
+    sp = _vector(starts, "starts", n + 1, torch.int64, dev)
+    ip, bp = _vector(ids, "ids", n, torch.int32, dev), _vector(bias, "bias", d_out, x.dtype, dev)
     if (probes is None) != (alphas is None):
         raise ValueError("give both probes and alphas or neither")
-    pp, fp = _vector(probes, "probes", n, torch.int32), _vector(alphas, "alphas", n, torch.float32)
+    pp = _vector(probes, "probes", n, torch.int32, dev)
+    fp = _vector(alphas, "alphas", n, torch.float32, dev)
     if probes is None:
         n_probes, bits = 0, None
     elif n_probes is None:
@@ -693,6 +699,6 @@ def zo_adapter_project(ctx: Context, x: torch.Tensor, weight: torch.Tensor,
         ws, wb = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
     _lib.check(_lib.lib().zo_adapter_project(
         ctx.handle, xp, xs, wp, bp, code, rows, d_in, d_out, ap, n_adapters, rank, float(scale),
-        sp, ip, n, pp, fp, offset, step, probe0, n_probes, kp, ws, wb, yp, ys, _stream(stream)),
+        sp, ip, n, pp, fp, offset, step, probe0, n_probes, kp, ws, wb, yp, ys, _stream(stream, dev)),
         "zo_adapter_project")
     return out

@@ -74,9 +74,6 @@ struct Row {
     }
 };
 
-constexpr uint64_t kTokenFewRows = 512;
-constexpr uint32_t kTokenLong = 16384;  // two pieces or more for each of 1024 threads
-constexpr uint32_t kCandidates = 2048;  // keys that the search for the alternatives can hold
 
 // The place of each of 64 keys (one per lane, 0: none) among them, largest first.
 __device__ __forceinline__ uint32_t rank_in_wave(uint64_t key, const uint64_t *keys)
@@ -121,6 +118,9 @@ __global__ __launch_bounds__(kThreads) void k_token(
     // with four, 15.1 with eight)
     constexpr int kUnroll = kThreads == 1024 ? 2 : 4;
     constexpr uint32_t kNone = 0xFFFFFFFFu, kHead = 0xFFFFFFFEu, kRest = 0xFFFFFFFDu;
+    // keys that the search for the alternatives can hold: rows of one value everywhere bring up
+    // to 32 pieces per thread of a part
+    constexpr uint32_t kCandidates = kThreads == 64 ? 512 : 2048;
     const uint64_t at = blockIdx.x;
     const int tid = threadIdx.x;
     const int64_t tgt = targets ? targets[at] : 0;
@@ -356,19 +356,23 @@ hipError_t launch_token_logprobs(const void *logits, bool bf16, uint64_t rows, u
                                  float *top_logp, hipStream_t stream)
 {
     // Few long rows (up to two per CU): all of a row's loads should be in flight at once, so
-    // 1024 threads take it.  Many rows hide each other's latency: the pass alone is then
-    // fastest with 256 threads (8192 rows of 50272 bf16: 149 us; 149 with 512, 207 with 1024),
-    // and the search for alternatives, serial within a row, with 512 (top 20: 200 us; 219 with
-    // 256, 312 with 1024).
+    // 1024 threads take it.  Many rows hide each other's latency, and the search for
+    // alternatives, serial within a row, should hold up few threads while the pass needs enough
+    // of them.  Measured at 8192 rows, no / 32 alternatives, with 64, 256 and 512 threads:
+    // 8 KB a row 17/35, 29/50, 56/88 us; 16 KB 27/66, 30/59, 56/95; 32 KB 57/144, 53/96, 60/121;
+    // 64 KB 94/312, 92/162, 88/145.
     const auto launch = [&](auto *p, auto threads) {
         using E = std::remove_cv_t<std::remove_pointer_t<decltype(p)>>;
         k_token<E, decltype(threads)::value><<<(uint32_t)rows, decltype(threads)::value, 0, stream>>>(
             p, vocab, stride, targets, logp, entropy, top_k, top_ids, top_logp);
     };
     const auto typed = [&](auto *p) {
-        if (rows <= kTokenFewRows && vocab >= kTokenLong)
+        const uint64_t bytes = (uint64_t)vocab * sizeof(*p);
+        if (rows <= 512 && bytes >= 32768)
             launch(p, std::integral_constant<int, 1024>());
-        else if (top_k)
+        else if (bytes <= 12288)
+            launch(p, std::integral_constant<int, 64>());
+        else if (top_k && bytes >= 65536)
             launch(p, std::integral_constant<int, 512>());
         else
             launch(p, std::integral_constant<int, 256>());

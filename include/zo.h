@@ -84,8 +84,8 @@ typedef enum { ZO_FP32 = 0, ZO_BF16 = 1 } zo_dtype;
 
 /* Create a context for probe seed `seed` on the current HIP device.  Allocates the host
  * context and a small device area (the non-finite counter and reduction partials), looks
- * up this device's copy of the library's static scratch, and raises the update kernel's
- * dynamic-LDS limit on this device (so that no later call makes a runtime call besides its
+ * up this device's copy of the library's static scratch, and raises the update's and
+ * the products' dynamic-LDS limits on this device (so that no later call makes a runtime call besides its
  * launches).  Errors: ZO_EINVAL if out is NULL; ZO_ENOMEM / ZO_EHIP if an allocation or
  * runtime call fails (for example when no GPU is present).  *out is set only on success. */
 zo_status zo_init(uint64_t seed, zo_ctx **out);

@@ -60,6 +60,10 @@ inline bool aligned(const void *p)
 }
 
 constexpr uint64_t kMaxRows = 0x7FFFFFFFu;   // of the language-model operators
+// Of the products: one launch holds all tiles and all groups, and a tile of weights is
+// addressed by 32 bits of 16-byte units.
+constexpr uint64_t kMaxWidth = 1u << 26, kMaxFeatures = 1u << 24, kMaxGroups = 1u << 22;
+constexpr uint64_t kMaxProjectRows = 1u << 25, kMaxProjected = (uint64_t)1 << 35;
 // The rows of a product's left operand reach at most 64 GiB (32 bits of 16-byte units).
 inline bool reach_ok(uint64_t rows, uint64_t stride, uint64_t k, bool bf16)
 {
@@ -583,7 +587,7 @@ zo_status zo_head_logprobs(zo_ctx *c, const void *d_hidden, uint64_t hidden_stri
 {
     if (!ctx_ok(c)) return ZO_EINVAL;
     if (dtype != ZO_FP32 && dtype != ZO_BF16) return ZO_EINVAL;
-    if (rows > kMaxRows || vocab > kMaxRows || d > kMaxRows) return ZO_EUNSUPPORTED;
+    if (rows > kMaxRows || vocab > kMaxFeatures || d > kMaxWidth) return ZO_EUNSUPPORTED;
     if (rows == 0) return ZO_OK;
     if (vocab == 0 || d == 0 || d % 8u || hidden_stride % 8u) return ZO_EINVAL;
     if (!d_hidden || !d_weight || !aligned16(d_hidden) || !aligned16(d_weight)) return ZO_EINVAL;
@@ -638,8 +642,8 @@ zo_status zo_adapter_project(zo_ctx *c, const void *d_x, uint64_t x_stride, cons
 {
     if (!ctx_ok(c)) return ZO_EINVAL;
     if (dtype != ZO_FP32 && dtype != ZO_BF16) return ZO_EINVAL;
-    if (rank > ZO_MAX_RANK || rows > kMaxRows || n_groups > kMaxRows || d_in > kMaxRows ||
-        d_out > kMaxRows)
+    if (rank > ZO_MAX_RANK || rows > kMaxProjectRows || n_groups > kMaxGroups || d_in > kMaxWidth ||
+        d_out > kMaxFeatures || rows * d_out > kMaxProjected)
         return ZO_EUNSUPPORTED;
     if (d_in == 0 || d_in % 8u || d_out % 8u || rank % 8u || x_stride % 8u || y_stride % 8u)
         return ZO_EINVAL;
@@ -662,6 +666,7 @@ zo_status zo_adapter_project(zo_ctx *c, const void *d_x, uint64_t x_stride, cons
         return ZO_EINVAL;
     if (!reach_ok(rows, x_stride, d_in, dtype == ZO_BF16)) return ZO_EUNSUPPORTED;
     const uint32_t regenerated = d_probes && !d_bits && params > 0 ? n_probes : 0;
+    if (regenerated > 0 && zo_bits_stride(params) > UINT64_MAX / 2 / regenerated) return ZO_EINVAL;
     const uint64_t need = zo_adapter_workspace_bytes(rows, d_in, d_out, n_adapters, rank, n_groups,
                                                      regenerated);
     if (need > 0 && (!d_workspace || !aligned<256>(d_workspace) || workspace_bytes < need))

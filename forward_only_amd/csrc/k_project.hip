@@ -757,8 +757,9 @@ __device__ __forceinline__ uint32_t tile_of_xcd(uint32_t b, uint32_t n)
 // the loads that the next turn reads: all but the eight issued since.  Loads past the end of k
 // read zeros, so that the counts hold to the end.  Four turns of a quarter each, with operands
 // read one turn ahead, were no faster and took 96 registers for operands instead of 64.
-// What bounds it: MFMA issue 65% of the cycles at a clock that the load lowers (LDS reads and
-// writes take as many cycles as the products): 1475 TFLOP/s of bf16 at 4096 x 50272 x 7168.
+// What bounds it: MFMA issue, 77% of the cycles at 1.8 GHz, a clock that the load lowers (LDS
+// reads and writes take about as many cycles as the products): 1475 TFLOP/s of bf16 at
+// 4096 x 50272 x 7168.
 //
 // Tiles run one per CU, so their number is cut into whole rounds of kSlots and a rest.  When the
 // rest fills at most half a round, each of its tiles is cut along k into as many slices as
@@ -1218,7 +1219,7 @@ hipError_t big(const ProductArgs &p, const typename T::elem *x, const typename T
                const uint32_t *list, const uint32_t *count, const End &end, hipStream_t stream)
 {
     const uint64_t n = (((uint64_t)p.features + kBigF - 1) / kBigF) * ((p.rows + kBigR - 1) / kBigR);
-    if (n > 0x3FFFFFFFull) return hipErrorInvalidValue;
+    if (n > kLaunchThreads / 512) return hipErrorInvalidValue;
     // without a count the tiles are known: no workgroups for slices that there are not
     const uint32_t over = (uint32_t)(n % kBigSlots);
     const uint32_t steps = (p.k + 8 * T::kPiece - 1) / (8 * T::kPiece);
@@ -1242,7 +1243,7 @@ hipError_t mid(const ProductArgs &p, const typename T::elem *x, const typename T
                const uint32_t *list, const uint32_t *count, const End &end, hipStream_t stream)
 {
     const uint64_t n = ((uint64_t)p.features + 63) / 64 * ((p.rows + 63) / 64);
-    if (n > 0x7FFFFFFFull - 8) return hipErrorInvalidValue;
+    if (n > kLaunchThreads / 256) return hipErrorInvalidValue;
     k_mid<T, End><<<(uint32_t)((n + 7) / 8 * 8), 256, 0, stream>>>(p, x, w, list, count, end);
     return hipGetLastError();
 }

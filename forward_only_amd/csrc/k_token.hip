@@ -363,32 +363,40 @@ hipError_t launch_token_logprobs(const void *logits, bool bf16, uint64_t rows, u
     // 64 KB 94/312, 92/162, 88/145.
     const auto launch = [&](auto *p, auto threads) {
         using E = std::remove_cv_t<std::remove_pointer_t<decltype(p)>>;
-        k_token<E, decltype(threads)::value><<<(uint32_t)rows, decltype(threads)::value, 0, stream>>>(
-            p, vocab, stride, targets, logp, entropy, top_k, top_ids, top_logp);
+        constexpr int kThreads = decltype(threads)::value;
+        const auto from = [](auto *base, uint64_t i) { return base ? base + i : base; };
+        // a launch holds fewer than 2^32 threads
+        constexpr uint64_t kRows = kLaunchThreads / kThreads;
+        hipError_t e = hipSuccess;
+        for (uint64_t r = 0; r < rows && e == hipSuccess; r += kRows) {
+            k_token<E, kThreads><<<(uint32_t)(rows - r < kRows ? rows - r : kRows), kThreads, 0, stream>>>(
+                p + r * stride, vocab, stride, from(targets, r), from(logp, r), from(entropy, r), top_k,
+                from(top_ids, r * top_k), from(top_logp, r * top_k));
+            e = hipGetLastError();
+        }
+        return e;
     };
     const auto typed = [&](auto *p) {
         const uint64_t bytes = (uint64_t)vocab * sizeof(*p);
-        if (rows <= 512 && bytes >= 32768)
-            launch(p, std::integral_constant<int, 1024>());
-        else if (bytes <= 12288)
-            launch(p, std::integral_constant<int, 64>());
-        else if (top_k && bytes >= 65536)
-            launch(p, std::integral_constant<int, 512>());
-        else
-            launch(p, std::integral_constant<int, 256>());
+        if (rows <= 512 && bytes >= 32768) return launch(p, std::integral_constant<int, 1024>());
+        if (bytes <= 12288) return launch(p, std::integral_constant<int, 64>());
+        if (top_k && bytes >= 65536) return launch(p, std::integral_constant<int, 512>());
+        return launch(p, std::integral_constant<int, 256>());
     };
-    if (bf16)
-        typed(static_cast<const uint16_t *>(logits));
-    else
-        typed(static_cast<const float *>(logits));
-    return hipGetLastError();
+    return bf16 ? typed(static_cast<const uint16_t *>(logits)) : typed(static_cast<const float *>(logits));
 }
 
 hipError_t launch_group_loss(const float *logp, const int64_t *targets, const int64_t *starts,
                              uint32_t n_groups, uint64_t rows, double *loss, hipStream_t stream)
 {
-    k_group_loss<<<n_groups, kGroupThreads, 0, stream>>>(logp, targets, starts, rows, loss);
-    return hipGetLastError();
+    constexpr uint32_t kGroups = kLaunchThreads / kGroupThreads;
+    hipError_t e = hipSuccess;
+    for (uint64_t g = 0; g < n_groups && e == hipSuccess; g += kGroups) {
+        const uint32_t n = n_groups - g < kGroups ? (uint32_t)(n_groups - g) : kGroups;
+        k_group_loss<<<n, kGroupThreads, 0, stream>>>(logp, targets, starts + g, rows, loss + g);
+        e = hipGetLastError();
+    }
+    return e;
 }
 
 }  // namespace zo

@@ -127,6 +127,9 @@ hipError_t launch_mlp_loss_probes(const float *params, const float *X, const int
 
 // Target of a row that counts for nothing (ZO_IGNORE_TOKEN).
 constexpr int64_t kIgnoreToken = -100;
+// Most threads that the language-model operators put into one launch (the hardware's limit is
+// 2^32 - 1).
+constexpr uint64_t kLaunchThreads = (uint64_t)1 << 31;
 // Most alternatives one zo_token_logprobs call gives.
 constexpr uint32_t kMaxTopK = 32;
 // Largest rank of an adapter.

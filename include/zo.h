@@ -84,10 +84,11 @@ typedef enum { ZO_FP32 = 0, ZO_BF16 = 1 } zo_dtype;
 
 /* Create a context for probe seed `seed` on the current HIP device.  Allocates the host
  * context and a small device area (the non-finite counter and reduction partials), looks
- * up this device's copy of the library's static scratch, and raises the update's and
- * the products' dynamic-LDS limits on this device (so that no later call makes a runtime call besides its
- * launches).  Errors: ZO_EINVAL if out is NULL; ZO_ENOMEM / ZO_EHIP if an allocation or
- * runtime call fails (for example when no GPU is present).  *out is set only on success. */
+ * up this device's copy of the library's static scratch, and raises the update's and the
+ * products' dynamic-LDS limits on this device (so that no later call makes a runtime call
+ * besides its launches).  Errors: ZO_EINVAL if out is NULL; ZO_ENOMEM / ZO_EHIP if an
+ * allocation or runtime call fails (for example when no GPU is present).  *out is set only on
+ * success. */
 zo_status zo_init(uint64_t seed, zo_ctx **out);
 
 /* Release a context (NULL is allowed).  Synchronizes the device first. */
@@ -411,8 +412,8 @@ zo_status zo_token_logprobs(zo_ctx *ctx, const void *d_logits, zo_dtype dtype, u
  * and d_entropy.  d_workspace: device, 256-byte aligned, at least
  * zo_head_workspace_bytes(rows, d, vocab) bytes.  Deterministic.
  * Errors: ZO_EINVAL as zo_token_logprobs, shapes outside these limits, a workspace that is
- * too small or misaligned; ZO_EUNSUPPORTED if rows, d or vocab exceed 2^31 - 1, or the rows
- * of d_hidden reach over more than 64 GiB. */
+ * too small or misaligned; ZO_EUNSUPPORTED if rows exceed 2^31 - 1, d 2^26 or vocab 2^24, or
+ * the rows of d_hidden reach over more than 64 GiB. */
 uint64_t zo_head_workspace_bytes(uint64_t rows, uint32_t d, uint32_t vocab);
 zo_status zo_head_logprobs(zo_ctx *ctx, const void *d_hidden, uint64_t hidden_stride,
                            const void *d_weight, zo_dtype dtype, uint64_t rows, uint32_t d,
@@ -454,14 +455,17 @@ zo_status zo_group_loss(zo_ctx *ctx, const float *d_logp, const int64_t *d_targe
  * clean pass); otherwise d_probes[g] < n_probes.  d_bits: NULL (regenerate; the rows of all
  * n_probes probes are written to the workspace first) or n_probes packed rows over all
  * adapters' parameters, row i for probe probe0 + i, 16-byte aligned.
- * An id or probe outside its table makes its group's rows NaN.
+ * An id or probe outside its table makes its group's rows NaN.  What a non-finite value of an
+ * adapter, or of x A_g^T, enters in its group's rows becomes non-finite, an infinity perhaps
+ * NaN; other groups' rows do not see it.
  * d_workspace: device, 256-byte aligned, at least zo_adapter_workspace_bytes(...) bytes, with
  * regenerated = n_probes if d_probes is given and d_bits is NULL, else 0.
  * Errors: ZO_EINVAL for NULL pointers (with rows and n_groups > 0; d_adapters may be NULL
  * with n_adapters == 0 or rank == 0), unknown dtype, shapes and strides outside these limits,
  * misalignment, offset % 128 != 0 or range overflow, probe indices past 2^32 - 1, a
- * workspace that is too small; ZO_EUNSUPPORTED if rank > ZO_MAX_RANK, rows, n_groups, d_in or
- * d_out exceed 2^31 - 1, or the rows of d_x reach over more than 64 GiB.  rows == 0, d_out == 0 or n_groups == 0 launches nothing. */
+ * workspace that is too small; ZO_EUNSUPPORTED if rank > ZO_MAX_RANK, rows exceed 2^25,
+ * n_groups 2^22, d_in 2^26, d_out 2^24 or rows * d_out 2^35, or the rows of d_x reach over
+ * more than 64 GiB.  rows == 0, d_out == 0 or n_groups == 0 launches nothing. */
 uint64_t zo_adapter_workspace_bytes(uint64_t rows, uint32_t d_in, uint32_t d_out,
                                     uint32_t n_adapters, uint32_t rank, uint32_t n_groups,
                                     uint32_t regenerated);

@@ -100,3 +100,74 @@ def test_weights_beyond_4_gib(ctx, rows):
     ref.assert_close(got.logp, logp, 2 * off + E + 2 * ref.U32 * spread, "logp")
     # |t / s| <= log V + 1 < 15 here
     ref.assert_close(got.entropy, torch.log(s) - mean, 32 * off + 31 * E, "entropy")
+
+
+def test_more_rows_and_groups_than_one_launch_holds(ctx):
+    # 2^31 threads a launch: 2^25 rows of one wave each, 2^23 groups of 256 threads
+    rows, vocab = (1 << 25) + 5, 2
+    x = torch.zeros(rows, vocab, dtype=BF, device="cuda")
+    x[-9:, 1] = 1.0
+    t = torch.ones(rows, dtype=torch.int64, device="cuda")
+    t[1 << 25] = zo.ZO_IGNORE_TOKEN
+    got = zo.zo_token_logprobs(ctx, x, t, top_k=1)
+    for p, q in zip(got, zo.zo_token_logprobs(ctx, x[-9:], t[-9:], top_k=1)):
+        assert torch.equal(p[-9:], q)
+    # two equal logits: -log 2, one fp32 logarithm
+    assert (got.logp[:-9] - math.log(0.5)).abs().max().item() <= 1e-6
+    assert not got.top_ids[:-9].any()
+    groups = (1 << 23) + 3
+    starts = torch.arange(groups + 1, device="cuda") * 3
+    loss = zo.zo_group_loss(ctx, got.logp[:3 * groups], t[:3 * groups], starts)
+    want = got.logp[:3 * groups].double().view(groups, 3).sum(dim=1) / -3.0
+    # sums of three equal fp32 values are exact in fp64
+    assert torch.allclose(loss, want, rtol=4 * torch.finfo(torch.float64).eps, atol=0.0)
+
+
+def test_sizes_beyond_a_launch_are_refused(ctx):
+    L, h = zo._lib.lib(), ctx.handle
+    p = torch.zeros(64, device="cuda").data_ptr()
+    UNSUP = zo.ZO_EUNSUPPORTED
+
+    def head(rows, d, vocab):
+        return L.zo_head_logprobs(h, p, d, p, 1, rows, d, vocab, p, p, p, p, 1 << 62, None)
+
+    def project(rows, d_in, d_out, groups):
+        return L.zo_adapter_project(h, p, d_in, p, None, 1, rows, d_in, d_out, p, 1, 8, 1.0, p, p, groups,
+                                    None, None, 0, 0, 0, 0, None, p, 1 << 62, p, d_out, None)
+
+    assert head(1, 8, (1 << 24) + 8) == UNSUP and head(1, (1 << 26) + 8, 8) == UNSUP
+    assert head((1 << 31) - 1, 64, 8) == UNSUP      # 256 GiB of hidden states
+    assert project((1 << 25) + 1, 8, 8, 1) == UNSUP and project(1, 8, 8, (1 << 22) + 1) == UNSUP
+    assert project(1, (1 << 26) + 8, 8, 1) == UNSUP and project(1, 8, (1 << 24) + 8, 1) == UNSUP
+    assert project(1 << 25, 8, 1032, 1) == UNSUP
+
+
+def test_probe_rows_past_64_bits_are_refused(ctx):
+    # 2^31 probes of 2^33 bytes each: 2^64, which is 0 in 64 bits
+    L, h = zo._lib.lib(), ctx.handle
+    p = torch.zeros(64, device="cuda").data_ptr()
+    assert zo.zo_bits_stride(1 << 36) == 1 << 33
+    assert L.zo_adapter_project(h, p, 1016, p, None, 1, 1, 1016, 8, p, 1 << 23, 8, 1.0, p, p, 1, p, p,
+                                0, 0, 0, 1 << 31, None, p, 1 << 40, p, 8, None) == zo.ZO_EINVAL
+
+
+def test_large_grids(ctx):
+    """As many groups as one call takes, most of them empty, and many rows of few features."""
+    groups, rows, d = 1 << 22, 5000, 64
+    x, w, ad = _rand(1, rows, d), _rand(2, d, d, std=0.1), _rand(3, 8 * 2 * d, std=0.1)
+    starts = torch.zeros(groups + 1, dtype=torch.int64, device="cuda")
+    starts[groups // 2 + 1:] = rows
+    ids = torch.full((groups,), -1, dtype=torch.int32, device="cuda")
+    ids[groups // 2] = 0
+    got = zo.zo_adapter_project(ctx, x, w, ad, 8, starts, ids)
+    one = torch.tensor([0, rows], device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert torch.equal(got, zo.zo_adapter_project(ctx, x, w, ad, 8, *one))
+    rows = 1 << 22
+    far = torch.zeros(rows, 8, dtype=BF, device="cuda")
+    far[-700:] = _rand(4, 700, 8)
+    w, ad = _rand(5, 8, 8), _rand(6, 8 * 16)
+    starts = torch.tensor([0, rows], device="cuda")
+    got = zo.zo_adapter_project(ctx, far, w, ad, 8, starts, one[1])
+    assert torch.equal(got[-700:], zo.zo_adapter_project(ctx, far[-700:], w, ad, 8,
+                                                         torch.tensor([0, 700], device="cuda"), one[1]))
+    assert not got[:-700].any()

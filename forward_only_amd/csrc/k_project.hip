@@ -142,6 +142,7 @@ __device__ __forceinline__ u32x4 piece_at(const typename T::elem *p)
 
 typedef const __attribute__((address_space(1))) void *gptr_t;
 typedef __attribute__((address_space(3))) void *lptr_t;
+constexpr int kNonTemporal = 2;     // cache policy of a load
 
 // Wait until at most kLoads vector-memory loads are outstanding, and for all LDS reads if kLds.
 template <int kLoads, bool kLds>
@@ -168,7 +169,9 @@ __device__ __forceinline__ void turn_barrier()
 //
 // Staged row i holds its piece c at place c ^ (i / 2 % 8): sixteen rows read at one c then cover
 // all banks once.
-template <class T, int kRows16, int kStages>
+//
+// The first kOnce blocks are loaded past the caches.
+template <class T, int kRows16, int kStages, int kOnce = 0>
 struct Feed {
     static constexpr int kPieces = 8, kLoads = 2 * kRows16;
     static constexpr uint32_t kStep = kPieces * T::kPiece;
@@ -193,8 +196,11 @@ struct Feed {
         for (int j = 0; j < kLoads; ++j) {
             const uint64_t at = (uint64_t)step * kStep + (j % 2 ? piece ^ (4 * T::kPiece) : piece);
             const void *g = at < k ? static_cast<const void *>(src[j] + at) : &kZeros;
-            __builtin_amdgcn_global_load_lds((gptr_t)g, (lptr_t)(lds + stage * kStage + j * 8 * kPieces),
-                                             16, 0, 0);
+            u32x4 *to = lds + stage * kStage + j * 8 * kPieces;
+            if (j < 2 * kOnce)
+                __builtin_amdgcn_global_load_lds((gptr_t)g, (lptr_t)to, 16, 0, kNonTemporal);
+            else
+                __builtin_amdgcn_global_load_lds((gptr_t)g, (lptr_t)to, 16, 0, 0);
         }
     }
     // Fragment c (of two) of block b.
@@ -1049,17 +1055,16 @@ __global__ __launch_bounds__(256) void k_mid(ProductArgs p, const typename T::el
 // with 16, x is read from L2 as often again (32 rows, 5120 to 5120, bf16: 14.8 us; 12.0 with
 // 32).  Three stages: two leave too little under way, four one workgroup per CU (8 rows, 5120
 // to 50272: 94 and 97 us; 88 with three, 5.8 TB/s).
-constexpr int kFewF = 2, kFewWaves = 4, kFewStages = 3;
-template <int kMR>
-constexpr uint32_t few_lds() { return kFewWaves * kFewStages * (kFewF + kMR) * 16 * 128; }
+constexpr int kFewWaves = 4, kFewStages = 3;
+template <int kMR, int kMF>
+constexpr uint32_t few_lds() { return kFewWaves * kFewStages * (kMF + kMR) * 16 * 128; }
 
-template <class T, int kMR, class End>
+template <class T, int kMR, int kMF, bool kOnce, class End>
 __global__ __launch_bounds__((kFewWaves + kMR) * 64) void k_few(ProductArgs p,
                                                                 const typename T::elem *x,
                                                                 const typename T::elem *w, End end)
 {
-    constexpr int kMF = kFewF;
-    typedef Feed<T, kMF + kMR, kFewStages> F;
+    typedef Feed<T, kMF + kMR, kFewStages, kOnce ? kMF : 0> F;
     extern __shared__ u32x4 stage[];            // [wave][stage][features, rows], then [wave] of sums
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -1252,11 +1257,29 @@ template <class T, class End>
 hipError_t few(const ProductArgs &p, const typename T::elem *x, const typename T::elem *w,
                const End &end, hipStream_t stream)
 {
-    const uint32_t grid = (p.features + 16 * kFewF - 1) / (16 * kFewF);
-    if (p.rows <= 16)
-        k_few<T, 1, End><<<grid, (kFewWaves + 1) * 64, few_lds<1>(), stream>>>(p, x, w, end);
+    const auto launch = [&](auto of, auto wide, auto once) {
+        constexpr int kMR = decltype(of)::value, kMF = decltype(wide)::value;
+        k_few<T, kMR, kMF, decltype(once)::value, End>
+            <<<(p.features + 16 * kMF - 1) / (16 * kMF), (kFewWaves + kMR) * 64, few_lds<kMR, kMF>(),
+               stream>>>(p, x, w, end);
+    };
+    const auto sized = [&](auto once) {
+        const std::integral_constant<int, 1> one;
+        const std::integral_constant<int, 2> two;
+        const std::integral_constant<int, 4> four;
+        if (p.rows <= 16)
+            launch(one, two, once);
+        else if (few_features(p.rows, p.features) == 32)
+            launch(two, two, once);
+        else
+            launch(two, four, once);
+    };
+    // weights of bf16 5120 -> 50272 (515 MB): 8 rows 95 -> 84 us, 32 rows 119 -> 115;
+    // 5120 -> 20480 (210 MB) in the cache: 34 -> 38 and 39 -> 52, out of it 43 -> 38 and 54 -> 52
+    if ((uint64_t)p.features * p.k * sizeof(*w) > kLastCache)
+        sized(std::true_type());
     else
-        k_few<T, 2, End><<<grid, (kFewWaves + 2) * 64, few_lds<2>(), stream>>>(p, x, w, end);
+        sized(std::false_type());
     return hipGetLastError();
 }
 
@@ -1354,10 +1377,18 @@ hipError_t prepare()
         raise(&k_shrink<T, 1, 2>, shrink_lds<1, 2>()),
         raise(&k_shrink<T, 2, 1>, shrink_lds<2, 1>()),
         raise(&k_shrink<T, 2, 2>, shrink_lds<2, 2>()),
-        raise(&k_few<T, 1, EndProject<T>>, few_lds<1>()),
-        raise(&k_few<T, 2, EndProject<T>>, few_lds<2>()),
-        raise(&k_few<T, 1, EndHead>, few_lds<1>()),
-        raise(&k_few<T, 2, EndHead>, few_lds<2>())};
+        raise(&k_few<T, 1, 2, false, EndProject<T>>, few_lds<1, 2>()),
+        raise(&k_few<T, 1, 2, true, EndProject<T>>, few_lds<1, 2>()),
+        raise(&k_few<T, 2, 2, false, EndProject<T>>, few_lds<2, 2>()),
+        raise(&k_few<T, 2, 2, true, EndProject<T>>, few_lds<2, 2>()),
+        raise(&k_few<T, 2, 4, false, EndProject<T>>, few_lds<2, 4>()),
+        raise(&k_few<T, 2, 4, true, EndProject<T>>, few_lds<2, 4>()),
+        raise(&k_few<T, 1, 2, false, EndHead>, few_lds<1, 2>()),
+        raise(&k_few<T, 1, 2, true, EndHead>, few_lds<1, 2>()),
+        raise(&k_few<T, 2, 2, false, EndHead>, few_lds<2, 2>()),
+        raise(&k_few<T, 2, 2, true, EndHead>, few_lds<2, 2>()),
+        raise(&k_few<T, 2, 4, false, EndHead>, few_lds<2, 4>()),
+        raise(&k_few<T, 2, 4, true, EndHead>, few_lds<2, 4>())};
     for (const hipError_t e : all)
         if (e != hipSuccess) return e;
     return hipSuccess;

@@ -57,9 +57,13 @@ struct Row {
         pieces = (vocab - head) / kPiece;
     }
     __device__ __forceinline__ uint32_t rest() const { return head + pieces * kPiece; }
+    // kOnce: not looked at again, so not kept in the caches.
+    template <bool kOnce = false>
     __device__ __forceinline__ u32x4 piece(uint32_t i) const
     {
-        return *reinterpret_cast<const u32x4 *>(p + head + (uint64_t)i * kPiece);
+        const u32x4 *at = reinterpret_cast<const u32x4 *>(p + head + (uint64_t)i * kPiece);
+        if constexpr (kOnce) return __builtin_nontemporal_load(at);
+        else return *at;
     }
     static __device__ __forceinline__ float value(const u32x4 &v, int i)
     {
@@ -96,7 +100,7 @@ __device__ __forceinline__ uint64_t bound_of(const uint64_t *keys, uint32_t k)
 
 // One workgroup per row, one pass over it: each thread loads four pieces, takes their largest
 // value first (it rescales the sums at most once per four pieces) and adds up.  A value costs
-// 12.4 issue slots (widen, half a max3, subtract, scale, an exponential of four, add, bound,
+// 11.4 issue slots (widen, half a max3, scale and subtract, an exponential of four, add, bound,
 // multiply-add), which is what bounds many bf16 rows, next to HBM (16384 rows of 50272: 280 us,
 // 5.9 TB/s); few rows are bound by the latency of a round of loads and of the search.
 //
@@ -107,7 +111,7 @@ __device__ __forceinline__ uint64_t bound_of(const uint64_t *keys, uint32_t k)
 // value and index, so ties neither widen the search nor leave the order open.  Rows where
 // that does not hold (NaN, only -inf, or more candidates than fit) take k passes of a search
 // for the largest key below the last.
-template <class T, int kThreads>
+template <class T, int kThreads, bool kOnce>
 __global__ __launch_bounds__(kThreads) void k_token(
     const T *logits, uint32_t vocab, uint64_t stride, const int64_t *targets, float *logp,
     float *entropy, uint32_t top_k, int64_t *top_ids, float *top_logp)
@@ -139,7 +143,7 @@ __global__ __launch_bounds__(kThreads) void k_token(
     constexpr int kPiece = Row<T>::kPiece;
     float target = __builtin_nanf("");
     if (tid == 0 && targets && tgt >= 0 && tgt < (int64_t)vocab) target = widen(row.p[tgt]);
-    SoftStats st = SoftStats::empty();
+    BinaryStats st = BinaryStats::empty();
     float best = -INFINITY;     // largest value of this thread, and where it was first seen
     uint32_t where = kNone;
     const auto one = [&](float x, uint32_t place) {
@@ -155,7 +159,8 @@ __global__ __launch_bounds__(kThreads) void k_token(
         u32x4 v[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
-            v[u] = i + u * kThreads < row.pieces ? row.piece(i + u * kThreads) : Row<T>::nothing();
+            v[u] = i + u * kThreads < row.pieces ? row.template piece<kOnce>(i + u * kThreads)
+                                                 : Row<T>::nothing();
         float x[kUnroll * kPiece];
         float top = -INFINITY;
 #pragma unroll
@@ -168,25 +173,26 @@ __global__ __launch_bounds__(kThreads) void k_token(
             where = i;
         }
         st.raise(top);
-        const float m = st.m == -INFINITY ? 0.0f : st.m;
 #pragma unroll
-        for (int j = 0; j < kUnroll * kPiece; ++j) {
-            const float d = x[j] - m;
-            const float e = fast_exp(d);
-            st.s += e;
-            st.t = fmaf(e, fmaxf(d, -1e4f), st.t);     // d = -inf: e is 0, add 0
-        }
+        for (int j = 0; j < kUnroll * kPiece; ++j) st.add(x[j]);
     }
     if (row.rest() + tid < vocab) one(widen(row.p[row.rest() + tid]), kRest);
 
     __shared__ float parts[kWaves][3];
-    SoftStats all = st;
-    all.wave_merge();
-    if ((tid & (kWave - 1)) == 0) {
-        parts[tid / kWave][0] = all.m;
-        parts[tid / kWave][1] = all.s;
-        parts[tid / kWave][2] = all.t;
-    }
+    const auto leave = [&](SoftStats own) {
+        own.wave_merge();
+        if ((tid & (kWave - 1)) == 0) {
+            parts[tid / kWave][0] = own.m;
+            parts[tid / kWave][1] = own.s;
+            parts[tid / kWave][2] = own.t;
+        }
+    };
+    const auto join = [&] {
+        SoftStats a = {parts[0][0], parts[0][1], parts[0][2]};
+        for (int w = 1; w < kWaves; ++w) a.merge({parts[w][0], parts[w][1], parts[w][2]});
+        return a;
+    };
+    leave(st.natural());
     // The first largest element of each part, exactly: by the threads that hold its value.
     __shared__ uint64_t tops[kWave];
     __shared__ uint32_t found, flagged;
@@ -220,8 +226,19 @@ __global__ __launch_bounds__(kThreads) void k_token(
         if (tid == 0) found = flagged = 0;
     }
     __syncthreads();
-    all = {parts[0][0], parts[0][1], parts[0][2]};
-    for (int w = 1; w < kWaves; ++w) all.merge({parts[w][0], parts[w][1], parts[w][2]});
+    SoftStats all = join();
+    if (!BinaryStats::holds(all)) {
+        SoftStats own = SoftStats::empty();
+        for (uint32_t v = tid; v < vocab; v += kThreads) {
+            const float x = widen(row.p[v]);
+            own.raise(x);
+            own.add(x);
+        }
+        __syncthreads();
+        leave(own);
+        __syncthreads();
+        all = join();
+    }
     const float logs = logf(all.s);
     if (tid == 0) {
         if (targets) logp[at] = (target - all.m) - logs;
@@ -361,7 +378,11 @@ hipError_t launch_token_logprobs(const void *logits, bool bf16, uint64_t rows, u
     // of them.  Measured at 8192 rows, no / 32 alternatives, with 64, 256 and 512 threads:
     // 8 KB a row 17/35, 29/50, 56/88 us; 16 KB 27/66, 30/59, 56/95; 32 KB 57/144, 53/96, 60/121;
     // 64 KB 94/312, 92/162, 88/145.
-    const auto launch = [&](auto *p, auto threads) {
+    // Logits that the last cache does not hold are read past the caches, unless the search
+    // wants their rows again: 4096 bf16 rows of 50272 (412 MB) just written 96 -> 79 us, else
+    // 80 -> 74, 16384 rows 282 -> 257; 2048 rows (206 MB) just written 35 -> 41, so smaller ones
+    // are not.  With alternatives 2051 fp32 rows of 32003, half ignored, 34 -> 36.
+    const auto launch = [&](auto *p, auto threads, auto once) {
         using E = std::remove_cv_t<std::remove_pointer_t<decltype(p)>>;
         constexpr int kThreads = decltype(threads)::value;
         const auto from = [](auto *base, uint64_t i) { return base ? base + i : base; };
@@ -369,7 +390,8 @@ hipError_t launch_token_logprobs(const void *logits, bool bf16, uint64_t rows, u
         constexpr uint64_t kRows = kLaunchThreads / kThreads;
         hipError_t e = hipSuccess;
         for (uint64_t r = 0; r < rows && e == hipSuccess; r += kRows) {
-            k_token<E, kThreads><<<(uint32_t)(rows - r < kRows ? rows - r : kRows), kThreads, 0, stream>>>(
+            const uint32_t n = (uint32_t)(rows - r < kRows ? rows - r : kRows);
+            k_token<E, kThreads, decltype(once)::value><<<n, kThreads, 0, stream>>>(
                 p + r * stride, vocab, stride, from(targets, r), from(logp, r), from(entropy, r), top_k,
                 from(top_ids, r * top_k), from(top_logp, r * top_k));
             e = hipGetLastError();
@@ -378,10 +400,15 @@ hipError_t launch_token_logprobs(const void *logits, bool bf16, uint64_t rows, u
     };
     const auto typed = [&](auto *p) {
         const uint64_t bytes = (uint64_t)vocab * sizeof(*p);
-        if (rows <= 512 && bytes >= 32768) return launch(p, std::integral_constant<int, 1024>());
-        if (bytes <= 12288) return launch(p, std::integral_constant<int, 64>());
-        if (top_k && bytes >= 65536) return launch(p, std::integral_constant<int, 512>());
-        return launch(p, std::integral_constant<int, 256>());
+        const std::false_type kept;
+        const std::true_type once;
+        if (rows <= 512 && bytes >= 32768) return launch(p, std::integral_constant<int, 1024>(), kept);
+        if (top_k && bytes >= 65536) return launch(p, std::integral_constant<int, 512>(), kept);
+        const std::integral_constant<int, 64> wave;
+        const std::integral_constant<int, 256> waves;
+        if (top_k || rows * bytes <= kLastCache)
+            return bytes <= 12288 ? launch(p, wave, kept) : launch(p, waves, kept);
+        return bytes <= 12288 ? launch(p, wave, once) : launch(p, waves, once);
     };
     return bf16 ? typed(static_cast<const uint16_t *>(logits)) : typed(static_cast<const float *>(logits));
 }

@@ -130,6 +130,9 @@ constexpr int64_t kIgnoreToken = -100;
 // Most threads that the language-model operators put into one launch (the hardware's limit is
 // 2^32 - 1).
 constexpr uint64_t kLaunchThreads = (uint64_t)1 << 31;
+// Bytes of the last cache (256 MB).  What is read once and does not fit is read past it: the
+// loads then run at 6.4 TB/s instead of 5.8.
+constexpr uint64_t kLastCache = (uint64_t)256 << 20;
 // Most alternatives one zo_token_logprobs call gives.
 constexpr uint32_t kMaxTopK = 32;
 // Largest rank of an adapter.
@@ -193,9 +196,17 @@ inline Shape product_shape(uint64_t rows, uint32_t features, uint32_t k, bool bf
     const double big = (bf16 ? 1.45 : 7.5) * ((double)(b / kBigSlots) + part);
     return steps * big + (over && slices > 1 ? 25.0 : 0.0) <= steps * mid ? Shape::big : Shape::mid;
 }
-inline uint32_t shape_part(Shape s)   // features of one partial softmax: a wave's
+// Features of a workgroup of Shape::few.  With more than 16 rows a CU holds one, and a round of
+// 64 features takes 1.6 times one of 32.
+inline uint32_t few_features(uint64_t rows, uint32_t features)
 {
-    return s == Shape::big ? 128 : 32;
+    const auto rounds = [&](uint32_t each) { return ((features - 1) / each + 256) / 256; };
+    return rows > 16 && 1.6 * rounds(64) <= rounds(32) ? 64 : 32;
+}
+// Features of one partial softmax: a wave's.
+inline uint32_t shape_part(Shape s, uint64_t rows, uint32_t features)
+{
+    return s == Shape::big ? 128 : s == Shape::mid ? 32 : few_features(rows, features);
 }
 // Bytes of x A^T, [rows][rank] floats, and of each row's group.
 inline uint64_t adapter_u_bytes(uint64_t rows, uint32_t rank, uint32_t n_groups)
@@ -229,7 +240,8 @@ inline HeadSpace head_space(uint64_t rows, uint32_t k, uint32_t features, bool b
     const uint64_t places = rows < kHeadPlaces ? rows : kHeadPlaces;
     HeadSpace s;
     s.shape = product_shape(places, features, k, bf16);
-    s.parts = (features + shape_part(s.shape) - 1) / shape_part(s.shape);
+    const uint32_t part = shape_part(s.shape, places, features);
+    s.parts = (features + part - 1) / part;
     const uint64_t parts = s.parts;
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {

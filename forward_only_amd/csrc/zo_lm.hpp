@@ -62,6 +62,47 @@ struct SoftStats {
     }
 };
 
+// The same statistics against powers of two, one operation a value shorter: with m2 = m log2 e,
+// rounded, s = sum 2^y and t = sum 2^y y over y = x log2 e - m2, one multiply-add each.  m
+// starts at -kReach: lower values, masks among them, add nothing.  Up to |m| = kReach the
+// rounding of m2 moves y by 1/16 at most; it is the same for all y and natural() takes it out.
+struct BinaryStats {
+    static constexpr float kReach = 1048576.0f;
+    float m, m2, s, t;
+
+    static __device__ __forceinline__ BinaryStats empty() { return {-kReach, -kReach * kLog2e, 0.0f, 0.0f}; }
+    __device__ __forceinline__ void raise(float top)
+    {
+        if (top > m) {
+            const float next = top * kLog2e, d = m2 - next;
+            const float r = __builtin_amdgcn_exp2f(d);
+            t = r > 0.0f ? fmaf(s, d, t) * r : t * 0.0f;   // t * 0 keeps a NaN
+            s *= r;
+            m = top;
+            m2 = next;
+        }
+    }
+    __device__ __forceinline__ void add(float x)
+    {
+        const float y = fmaf(x, kLog2e, -m2);
+        const float e = __builtin_amdgcn_exp2f(y);
+        s += e;
+        t = fmaf(e, fmaxf(y, -1e4f), t);       // y = -inf: e is 0, add 0
+    }
+    // y = (x - m) log2 e + c.
+    __device__ __forceinline__ SoftStats natural() const
+    {
+        const float c = fmaf(m, kLog2e, -m2), f = __builtin_amdgcn_exp2f(-c);
+        return {m, s * f, fmaf(-c, s, t) * f * 0.69314718055994530942f};
+    }
+    // Whether joined statistics are within reach: the maximum not above it, nor so far below
+    // that the sum has lost it.  NaN and +inf are NaN either way.
+    static __device__ __forceinline__ bool holds(const SoftStats &all)
+    {
+        return !(all.s < 0.5f) && !(all.m > kReach && all.m < INFINITY);
+    }
+};
+
 // A row index from device memory, forced into [0, rows].
 __device__ __forceinline__ uint64_t clamp_row(int64_t r, uint64_t rows)
 {

@@ -189,3 +189,29 @@ def test_two_streams_at_once_and_graphs_on_large_tiles(ctx):
     graphs[0].replay()
     torch.cuda.synchronize()
     assert same(outs[0], want[1])
+
+
+# up to 16 and 32 rows beside many features, ragged, the last two beyond the 256 MB that the
+# last cache holds
+WIDE = [([16], 72, 16400), ([17], 72, 16384), ([9, 1, 14], 136, 16424), ([32], 264, 20000),
+        ([3, 2], 4104, 33000), ([20, 0, 7], 4104, 33000)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("lengths,d_in,d_out", WIDE)
+def test_few_rows_and_many_features(ctx, lengths, d_in, d_out, dtype):
+    _project(ctx, lengths, d_in, d_out, 24, dtype, sum(lengths) + d_out, probes=2)
+    _head(ctx, sum(lengths), d_in, d_out + 3, dtype, 0.2, d_out)
+
+
+def test_logits_beyond_the_last_cache(ctx):
+    """More than 256 MB: rows as short as one wave takes, and longer, equal to parts' results."""
+    for rows, vocab in ((70001, 2003), (11000, 13001)):
+        x = torch.randn(rows, vocab, generator=_gen(rows), device="cuda").mul_(3).to(BF)
+        t = torch.arange(rows, device="cuda") % vocab
+        t[::7] = zo.ZO_IGNORE_TOKEN
+        got = zo.zo_token_logprobs(ctx, x, t)
+        for r0 in range(0, rows, rows // 3):
+            part = slice(r0, r0 + rows // 3)
+            want = zo.zo_token_logprobs(ctx, x[part], t[part])
+            assert torch.equal(got.logp[part], want.logp) and torch.equal(got.entropy[part], want.entropy)

@@ -297,3 +297,20 @@ def test_stream_of_another_device_is_refused(ctx):
     x = torch.zeros(2, 64, device="cuda")
     with pytest.raises(ValueError):
         zo.zo_token_logprobs(ctx, x, None, stream=Other())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shift", [1e3, -1e3, 1e6, -1e6, 2.0 ** 20 - 4, 4 - 2.0 ** 20, -2.0 ** 20 - 90, -3e6, 1e9,
+                                   -1e9, 1e30, -1e30, 3e38, -3e38])
+def test_rows_far_from_zero(ctx, dtype, shift):
+    """Logits around a large value, and some there beside ordinary ones."""
+    vocab = 2085
+    x = (_logits(9, vocab, torch.float32, 11) + shift).to(dtype)
+    x[3, 700:] = _logits(1, vocab - 700, dtype, 12)[0]          # whole threads in either range
+    x[4, ::2] = _logits(1, vocab, dtype, 13)[0, ::2]
+    x[5, :] = shift
+    x[6, 1:] = -math.inf
+    x[7, 40:] = torch.finfo(dtype).min
+    x[8, 900] = math.nan
+    _check(ctx, x, torch.tensor([0, 1, 2, 3, 4, 5, 0, 7, 8]), 0)
+    _check(ctx, x[:6], torch.tensor([vocab - 1, 699, 700, 701, 5, 9]), 3)

@@ -1095,8 +1095,13 @@ __global__ __launch_bounds__((kFewWaves + kMR) * 64) void k_few(ProductArgs p,
     Tile<T, 16, kMF, kMR> t;
     t.clear();
     const uint32_t steps = feed.steps();
+    // Each workgroup begins elsewhere in k: rows a power of two apart lie on the same memory
+    // channels, and all workgroups would walk over them together (8 rows, bf16 8192 to 28672: 98
+    // us begun together, 74 apart; 4096 to 18000 39 and 27; 5120 to 50272 84 either way).
+    const uint32_t turn = (blockIdx.x * 0x9E3779B1u >> 8) % steps;
+    const auto turned = [&](uint32_t s) { return s >= steps ? s : s + turn < steps ? s + turn : s + turn - steps; };
 #pragma unroll
-    for (int i = 0; i < kFewStages - 1; ++i) feed.issue(wave + i * kFewWaves, i);
+    for (int i = 0; i < kFewStages - 1; ++i) feed.issue(turned(wave + i * kFewWaves), i);
     uint32_t at = 0, to = kFewStages - 1;
     for (uint32_t s = wave; s < steps; s += kFewWaves) {
         wait_for<F::kLoads * (kFewStages - 2), true>();
@@ -1109,7 +1114,7 @@ __global__ __launch_bounds__((kFewWaves + kMR) * 64) void k_few(ProductArgs p,
 #pragma unroll
             for (int n = 0; n < kMR; ++n) fx[c][n] = feed.fragment(at, kMF + n, c);
         }
-        feed.issue(s + (kFewStages - 1) * kFewWaves, to);
+        feed.issue(turned(s + (kFewStages - 1) * kFewWaves), to);
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll

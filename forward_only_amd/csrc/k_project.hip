@@ -1271,13 +1271,14 @@ hipError_t few(const ProductArgs &p, const typename T::elem *x, const typename T
     const auto sized = [&](auto once) {
         const std::integral_constant<int, 1> one;
         const std::integral_constant<int, 2> two;
+        const std::integral_constant<int, 3> three;
         const std::integral_constant<int, 4> four;
         if (p.rows <= 16)
             launch(one, two, once);
-        else if (few_features(p.rows, p.features) == 32)
-            launch(two, two, once);
+        else if (p.rows <= 32)
+            few_features(p.rows, p.features) == 32 ? launch(two, two, once) : launch(two, four, once);
         else
-            launch(two, four, once);
+            p.rows <= 48 ? launch(three, two, once) : launch(four, two, once);
     };
     // weights of bf16 5120 -> 50272 (515 MB): 8 rows 95 -> 84 us, 32 rows 119 -> 115;
     // 5120 -> 20480 (210 MB) in the cache: 34 -> 38 and 39 -> 52, out of it 43 -> 38 and 54 -> 52
@@ -1388,12 +1389,20 @@ hipError_t prepare()
         raise(&k_few<T, 2, 2, true, EndProject<T>>, few_lds<2, 2>()),
         raise(&k_few<T, 2, 4, false, EndProject<T>>, few_lds<2, 4>()),
         raise(&k_few<T, 2, 4, true, EndProject<T>>, few_lds<2, 4>()),
+        raise(&k_few<T, 3, 2, false, EndProject<T>>, few_lds<3, 2>()),
+        raise(&k_few<T, 3, 2, true, EndProject<T>>, few_lds<3, 2>()),
+        raise(&k_few<T, 4, 2, false, EndProject<T>>, few_lds<4, 2>()),
+        raise(&k_few<T, 4, 2, true, EndProject<T>>, few_lds<4, 2>()),
         raise(&k_few<T, 1, 2, false, EndHead>, few_lds<1, 2>()),
         raise(&k_few<T, 1, 2, true, EndHead>, few_lds<1, 2>()),
         raise(&k_few<T, 2, 2, false, EndHead>, few_lds<2, 2>()),
         raise(&k_few<T, 2, 2, true, EndHead>, few_lds<2, 2>()),
         raise(&k_few<T, 2, 4, false, EndHead>, few_lds<2, 4>()),
-        raise(&k_few<T, 2, 4, true, EndHead>, few_lds<2, 4>())};
+        raise(&k_few<T, 2, 4, true, EndHead>, few_lds<2, 4>()),
+        raise(&k_few<T, 3, 2, false, EndHead>, few_lds<3, 2>()),
+        raise(&k_few<T, 3, 2, true, EndHead>, few_lds<3, 2>()),
+        raise(&k_few<T, 4, 2, false, EndHead>, few_lds<4, 2>()),
+        raise(&k_few<T, 4, 2, true, EndHead>, few_lds<4, 2>())};
     for (const hipError_t e : all)
         if (e != hipSuccess) return e;
     return hipSuccess;

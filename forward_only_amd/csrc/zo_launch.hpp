@@ -163,8 +163,10 @@ struct AdapterArgs {
     const uint8_t *bits;           // n_probes packed rows over all adapters' parameters
     uint64_t bits_stride;
 };
-// How a product of rows x features is cut into workgroups: 32 features and all of at most 32
-// rows; tiles of 64 x 64; tiles of 256 x 256.
+// How a product of rows x features is cut into workgroups: 32 features (or 64) and all of at
+// most 32 rows, or 64 rows while that is one workgroup per CU in bf16, three in fp32 (64 rows,
+// bf16 7168 to 7168: 39 us in tiles of 64 x 64, 22 so; 5120 to 20480 44 and 48; fp32 2048 to
+// 2048 50 and 25); tiles of 64 x 64; tiles of 256 x 256.
 enum class Shape { few, mid, big };
 // Tiles of 256 x 256 that run at once (one per CU), the most slices of one along k, the fewest
 // steps of 128 bytes of k that make a slice, and the workspace of all slices of a call.
@@ -179,18 +181,17 @@ __host__ __device__ constexpr uint32_t big_slices(uint32_t over, uint32_t steps)
 }
 // The shape by estimated time.  Measured per step of 128 bytes of k: a round of 256 tiles of
 // 256 x 256 takes 1.45 us (bf16; fp32 7.5), a round of 512 tiles of 64 x 64 0.48 us (1.17),
-// or 0.33 us in bf16 while they are at most one per CU; slices cost 25 us to write and add up.
+// or 0.33 us (0.77) while they are at most one per CU (fp32 128 rows, 4096 to 8192: 106 us; in
+// sliced tiles of 256 x 256 165); slices cost 25 us to write and add up.
 inline Shape product_shape(uint64_t rows, uint32_t features, uint32_t k, bool bf16)
 {
-    if (rows <= 32) return Shape::few;
+    if (rows <= 32 || (rows <= 64 && features <= 32u * 256 * (bf16 ? 1 : 3))) return Shape::few;
     const auto tiles = [&](uint64_t size) {
         return ((uint64_t)features + size - 1) / size * ((rows + size - 1) / size);
     };
     const uint32_t steps = (k + (bf16 ? 63 : 31)) / (bf16 ? 64 : 32);
     const uint64_t m = tiles(64), b = tiles(256), over = b % kBigSlots;
-    const double mid = !bf16    ? 1.17 * ((m + 511) / 512)
-                       : m <= 256 ? 0.33
-                                  : 0.48 * ((m + 511) / 512);
+    const double mid = m <= 256 ? (bf16 ? 0.33 : 0.77) : (bf16 ? 0.48 : 1.17) * ((m + 511) / 512);
     const uint32_t slices = big_slices((uint32_t)over, steps);
     const double part = over == 0 ? 0.0 : slices > 1 ? 1.0 / slices : 1.0;
     const double big = (bf16 ? 1.45 : 7.5) * ((double)(b / kBigSlots) + part);
@@ -201,7 +202,7 @@ inline Shape product_shape(uint64_t rows, uint32_t features, uint32_t k, bool bf
 inline uint32_t few_features(uint64_t rows, uint32_t features)
 {
     const auto rounds = [&](uint32_t each) { return ((features - 1) / each + 256) / 256; };
-    return rows > 16 && 1.6 * rounds(64) <= rounds(32) ? 64 : 32;
+    return rows > 16 && rows <= 32 && 1.6 * rounds(64) <= rounds(32) ? 64 : 32;
 }
 // Features of one partial softmax: a wave's.
 inline uint32_t shape_part(Shape s, uint64_t rows, uint32_t features)

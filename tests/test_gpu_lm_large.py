@@ -197,6 +197,11 @@ WIDE = [([16], 72, 16400), ([17], 72, 16384), ([9, 1, 14], 136, 16424), ([32], 2
         ([3, 2], 4104, 33000), ([20, 0, 7], 4104, 33000)]
 
 
+# 33 to 64 rows: all of them in a workgroup up to 8192 features
+WIDE += [([33], 72, 40), ([5, 0, 43], 136, 8192), ([48], 1032, 8184), ([40, 9], 776, 72), ([1] * 64, 520, 8192),
+         ([64], 16400, 8192), ([30, 33], 264, 8200), ([65], 264, 8192)]
+
+
 @pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("lengths,d_in,d_out", WIDE)
 def test_few_rows_and_many_features(ctx, lengths, d_in, d_out, dtype):

@@ -37,7 +37,7 @@ def _far_rows(x, reach):
 
 
 # few, middling and many rows; the last on tiles of 256 x 256
-@pytest.mark.parametrize("rows,d_in,d_out", [(20, 256, 72), (50, 256, 72), (700, 4104, 5000)])
+@pytest.mark.parametrize("rows,d_in,d_out", [(20, 256, 72), (50, 256, 72), (90, 256, 72), (700, 4104, 5000)])
 def test_far_rows(ctx, rows, d_in, d_out):
     x, w, ad = _rand(1, rows, d_in), _rand(2, d_out, d_in, std=0.05), _rand(3, 16 * (d_in + d_out), std=0.1)
     starts, ids = torch.tensor([0, rows]).cuda(), torch.zeros(1, dtype=torch.int32).cuda()

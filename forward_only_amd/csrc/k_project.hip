@@ -1049,12 +1049,13 @@ __global__ __launch_bounds__(256) void k_mid(ProductArgs p, const typename T::el
     end.finish(t, g, f0 + wf * 32, r0 + wr * 32, stage + wave * 512);
 }
 
-// Few rows.  What bounds the product is reading w once: a workgroup takes 16 kFewF features and
+// Few rows.  What bounds the product is reading w once: a workgroup takes 16 kMF features and
 // all rows, four waves take every fourth step of k, and their sums meet in LDS.  kMR more waves
 // form the adapters' products meanwhile, add everything up and end 16 rows each.  32 features:
 // with 16, x is read from L2 as often again (32 rows, 5120 to 5120, bf16: 14.8 us; 12.0 with
-// 32).  Three stages: two leave too little under way, four one workgroup per CU (8 rows, 5120
-// to 50272: 94 and 97 us; 88 with three, 5.8 TB/s).
+// 32); 64 where that takes fewer rounds (few_features; 32 rows, 5120 to 50272: 115 us, 106 with
+// 64).  Three stages: two leave too little under way, four one workgroup per CU (8 rows, 5120
+// to 50272, through the caches: 94 and 97 us; 88 with three; 81 past them, 6.4 TB/s).
 constexpr int kFewWaves = 4, kFewStages = 3;
 template <int kMR, int kMF>
 constexpr uint32_t few_lds() { return kFewWaves * kFewStages * (kMF + kMR) * 16 * 128; }

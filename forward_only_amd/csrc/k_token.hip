@@ -99,10 +99,12 @@ __device__ __forceinline__ uint64_t bound_of(const uint64_t *keys, uint32_t k)
 }
 
 // One workgroup per row, one pass over it: each thread loads four pieces, takes their largest
-// value first (it rescales the sums at most once per four pieces) and adds up.  A value costs
-// 11.4 issue slots (widen, half a max3, scale and subtract, an exponential of four, add, bound,
-// multiply-add), which is what bounds many bf16 rows, next to HBM (16384 rows of 50272: 280 us,
-// 5.9 TB/s); few rows are bound by the latency of a round of loads and of the search.
+// value first (it rescales the sums at most once per four pieces) and adds up.  Many rows are
+// bound by VALU issue (98% of the cycles) close to HBM's rate, once they are read past the caches
+// (16384 bf16 rows of 50272: 257 us, 6.4 TB/s): a value costs 11.3 issue slots (widen, half a
+// max3, scale and subtract, an exponential of four, add, bound, multiply-add); with one more,
+// sums against e, it took 268 us.  Few rows are bound by the latency of a round of loads and of the search.  Rows whose statistics leave
+// BinaryStats' reach are passed over again in SoftStats (3.3 times the time, if all do).
 //
 // Alternatives.  The maxima of 64 parts of the row (one per kThreads / 64 threads) are at hand
 // from the pass; the k-th largest of them bounds the k-th largest value from below, so only

@@ -425,6 +425,7 @@ struct Tile {
 template <class T>
 struct EndProject {
     static constexpr bool kSlices = false;
+    static constexpr uint32_t kRowwise = 4;
     AdapterArgs a;
     const float *u;
     const int32_t *group;
@@ -443,15 +444,30 @@ struct EndProject {
     template <class Tl>
     __device__ __forceinline__ void finish(Tl &t, uint32_t g, uint32_t f0, uint64_t r0, u32x4 *lds) const
     {
-        add_groups(t, g, f0, r0);
+        if constexpr (Tl::kMF == 2) {
+            // A wave's tile that more than kRowwise groups meet takes the rows' way instead, which
+            // does not go through them one by one (32 rows a wave; rank 16, groups of 1, 4 and 8
+            // rows: bf16 520 rows, 768 to 768 52 -> 24, 22 -> 18 and 19 us either way; fp32
+            // 64 -> 43, 35 -> 32 and 32 either way).
+            const uint64_t r1 = r0 + 16 * Tl::kMR < a.rows ? r0 + 16 * Tl::kMR : a.rows;
+            if (r0 < r1 && begin(r1 - 1) - g > kRowwise) {
+#pragma unroll
+                for (int n = 0; n < Tl::kMR; ++n) add_rows(t, n, f0, r0 + 16 * n);
+            } else {
+                add_groups(t, g, f0, r0);
+            }
+        } else {
+            add_groups(t, g, f0, r0);
+        }
         store_rows(t, f0, r0, lds);
     }
 
-    // Few rows, each perhaps with an adapter of its own: every lane the products of its row, so
+    // Rows that each may have an adapter of their own: every lane the products of its row, so
     // that one round of loads serves all groups.
-    template <int kMF>
-    __device__ __forceinline__ void add_rows(Tile<T, 16, kMF, 1> &t, uint32_t f0, uint64_t r0) const
+    template <class Tl>
+    __device__ __forceinline__ void add_rows(Tl &t, int n, uint32_t f0, uint64_t r0) const
     {
+        constexpr int kMF = Tl::kMF;
         const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
         const uint64_t row = r0 + l16;
         if (row >= a.rows) return;
@@ -460,7 +476,7 @@ struct EndProject {
         const Group gr = group_of(a, (uint32_t)g);
         if (gr.bad) {
 #pragma unroll
-            for (int m = 0; m < kMF; ++m) t.acc[m][0] += __builtin_nanf("");
+            for (int m = 0; m < kMF; ++m) t.acc[m][n] += __builtin_nanf("");
         }
         if (gr.none) return;
         const uint64_t first = gr.base + (uint64_t)a.rank * a.d_in;
@@ -494,7 +510,7 @@ struct EndProject {
                             s = fmaf(T::value(v, k), c < 4 ? ua[c & 3] : ub[c & 3], s);
                         }
                     }
-                    t.acc[m][0][i] += a.scale * s;
+                    t.acc[m][n][i] += a.scale * s;
                 }
         }
     }
@@ -673,7 +689,7 @@ struct EndHead {
     float *tl;                  // logit of each place's target
 
     template <class Tl>
-    __device__ __forceinline__ void add_rows(Tl &, uint32_t, uint64_t) const {}
+    __device__ __forceinline__ void add_rows(Tl &, int, uint32_t, uint64_t) const {}
     __device__ __forceinline__ uint32_t begin(uint64_t) const { return 0; }
     template <class Tl>
     __device__ __forceinline__ void finish(Tl &tile, uint32_t, uint32_t f0, uint64_t r0, u32x4 *) const
@@ -1075,7 +1091,7 @@ __global__ __launch_bounds__((kFewWaves + kMR) * 64) void k_few(ProductArgs p,
         const int n = wave - kFewWaves;
         Tile<T, 16, kMF, 1> own;
         own.clear();
-        end.add_rows(own, f0, 16 * n);
+        end.add_rows(own, 0, f0, 16 * n);
         __syncthreads();                        // the stages are free
         __syncthreads();                        // the sums are there
 #pragma unroll

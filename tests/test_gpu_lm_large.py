@@ -220,3 +220,15 @@ def test_logits_beyond_the_last_cache(ctx):
             part = slice(r0, r0 + rows // 3)
             want = zo.zo_token_logprobs(ctx, x[part], t[part])
             assert torch.equal(got.logp[part], want.logp) and torch.equal(got.entropy[part], want.entropy)
+
+
+# tiles of 64 x 64 that many short groups meet: a row each, empty ones between, a long one last
+SHORT = [([1] * 70, 296, 240), ([1, 0, 2, 0, 0, 3] * 12 + [40], 136, 1000), ([5] * 30, 520, 264),
+         ([0] * 300 + [1] * 40 + [0] * 70 + [90], 72, 72), ([1] * 100, 1032, 4104)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("lengths,d_in,d_out", SHORT)
+@pytest.mark.parametrize("rank,probes", [(8, 0), (64, 2)])
+def test_short_groups(ctx, lengths, d_in, d_out, rank, probes, dtype):
+    _project(ctx, lengths, d_in, d_out, rank, dtype, sum(lengths) + d_out, probes, lead=2, tail=3)

@@ -24,12 +24,12 @@ template <>
 __device__ __forceinline__ float widen<uint16_t>(uint16_t v) { return bf16lo_to_f32(v); }
 
 // A 64-bit key that orders values (all NaN equal and above +inf, -0 equal to +0), then lower
-// indices first.
+// indices first.  Never 0 nor ~0, which stand for no key and for the bound above all keys.
 __device__ __forceinline__ uint64_t top_key(float x, uint32_t idx)
 {
     const uint32_t b = __float_as_uint(x + 0.0f);
     uint32_t o = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-    if (x != x) o = 0xFFFFFFFFu;
+    if (x != x) o = 0xFFFFFFFEu;        // a NaN again in key_value
     return ((uint64_t)o << 32) | (uint64_t)(0xFFFFFFFFu - idx);
 }
 

@@ -314,3 +314,23 @@ def test_rows_far_from_zero(ctx, dtype, shift):
     x[8, 900] = math.nan
     _check(ctx, x, torch.tensor([0, 1, 2, 3, 4, 5, 0, 7, 8]), 0)
     _check(ctx, x[:6], torch.tensor([vocab - 1, 699, 700, 701, 5, 9]), 3)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,vocab", [(6, 1), (6, 7), (6, 32), (6, 33), (6, 700), (6, 20011), (520, 33000)])
+def test_nan_at_the_first_index(ctx, dtype, rows, vocab):
+    """NaN ranks above all values wherever it stands: first of the row, all of it, beside +inf;
+    up to as many alternatives as the row has values, at every workgroup size."""
+    x = _logits(rows, vocab, dtype, vocab)
+    x[0, 0] = math.nan
+    x[1, :] = math.nan
+    x[2, 0] = -math.nan
+    x[2, vocab - 1] = math.inf
+    x[3, 0] = math.inf
+    x[3, vocab // 2] = math.nan
+    x[4, ::2] = math.nan
+    t = torch.arange(rows) % vocab
+    for k in sorted({1, min(2, vocab), min(32, vocab)}):
+        got = _check(ctx, x, t, k)
+        assert int(got.top_ids.min()) >= 0 and int(got.top_ids.max()) < vocab
+        assert torch.isnan(got.top_logp[:5]).all()

@@ -623,10 +623,8 @@ uint64_t zo_adapter_workspace_bytes(uint64_t rows, uint32_t d_in, uint32_t d_out
                                     uint32_t regenerated)
 {
     const uint64_t params = (uint64_t)n_adapters * rank * ((uint64_t)d_in + d_out);
-    // slices of the larger of both types', whose tiles may differ
-    const bool big = zo::product_shape(rows, d_out, d_in, true) == zo::Shape::big ||
-                     zo::product_shape(rows, d_out, d_in, false) == zo::Shape::big;
-    return zo::adapter_u_bytes(rows, rank, n_groups) + (big ? zo::kBigSliceBytes : 0) +
+    return zo::adapter_u_bytes(rows, rank, n_groups) +
+           (zo::slices_up_to(rows, d_out, d_in) ? zo::kBigSliceBytes : 0) +
            (uint64_t)regenerated * zo_bits_stride(params);
 }
 

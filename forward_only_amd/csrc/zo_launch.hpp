@@ -209,6 +209,24 @@ inline uint32_t shape_part(Shape s, uint64_t rows, uint32_t features)
 {
     return s == Shape::big ? 128 : s == Shape::mid ? 32 : few_features(rows, features);
 }
+// The most of `rows` rows or fewer that take a shape that is big, or one that is not; 0: none do.
+// A caller keeps one workspace for its largest batch, and a smaller one may need more for its
+// shape, so that sizes look at all counts.  From 64 rows on a shape lasts to the next multiple of
+// 64; up to 32 rows it is few.
+inline uint64_t most_rows(bool big, uint64_t rows, uint32_t features, uint32_t k, bool bf16)
+{
+    for (uint64_t r = rows; r > 0; r = r > 64 ? (r - 1) / 64 * 64 : r > 32 ? 32 : 0)
+        if ((product_shape(r, features, k, bf16) == Shape::big) == big) return r;
+    return 0;
+}
+// Whether a workspace for up to `rows` rows holds slices, of either type; beyond kShapeRows
+// always, so that the search stays short.
+constexpr uint64_t kShapeRows = 4096;
+inline bool slices_up_to(uint64_t rows, uint32_t features, uint32_t k)
+{
+    return rows > kShapeRows || most_rows(true, rows, features, k, true) ||
+           most_rows(true, rows, features, k, false);
+}
 // Bytes of x A^T, [rows][rank] floats, and of each row's group.
 inline uint64_t adapter_u_bytes(uint64_t rows, uint32_t rank, uint32_t n_groups)
 {
@@ -243,7 +261,10 @@ inline HeadSpace head_space(uint64_t rows, uint32_t k, uint32_t features, bool b
     s.shape = product_shape(places, features, k, bf16);
     const uint32_t part = shape_part(s.shape, places, features);
     s.parts = (features + part - 1) / part;
-    const uint64_t parts = s.parts;
+    // the most partial statistics of this and of all smaller counts
+    const auto partial = [&](uint64_t n, uint64_t each) { return (features + each - 1) / each * n; };
+    const uint64_t other = partial(most_rows(false, places, features, k, bf16), 32);
+    const uint64_t big = partial(places, 128), most = big > other ? big : other;
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {
         void *p = base ? static_cast<char *>(base) + at : nullptr;
@@ -252,11 +273,15 @@ inline HeadSpace head_space(uint64_t rows, uint32_t k, uint32_t features, bool b
     };
     s.count = static_cast<uint32_t *>(take(4));
     s.list = static_cast<uint32_t *>(take(rows * 4));
-    s.m = static_cast<float *>(take(parts * places * 4));
-    s.s = static_cast<float *>(take(parts * places * 4));
-    s.t = static_cast<float *>(take(parts * places * 4));
+    s.m = static_cast<float *>(take(most * 4));
+    s.s = static_cast<float *>(take(most * 4));
+    s.t = static_cast<float *>(take(most * 4));
     s.tl = static_cast<float *>(take(places * 4));
-    s.slices = s.shape == Shape::big ? static_cast<float *>(take(kBigSliceBytes)) : nullptr;
+    s.slices = nullptr;
+    if (slices_up_to(places, features, k)) {
+        float *slices = static_cast<float *>(take(kBigSliceBytes));
+        if (s.shape == Shape::big) s.slices = slices;
+    }
     s.bytes = at;
     return s;
 }

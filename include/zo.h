@@ -371,7 +371,8 @@ zo_status zo_mlp_loss_pair_noalloc(zo_ctx *ctx, const float *d_params, uint64_t 
  * Row indices on the device (targets, starts, ids, probes) are not seen by the host.  Values
  * outside their range never lead to an access outside a buffer: starts are forced into
  * [0, rows], and what depends on another bad index becomes NaN, so that zo_probe_weights
- * drops the probe.  Inputs and outputs must not overlap. */
+ * drops the probe.  Inputs and outputs must not overlap.  Workspace sizes never fall as rows
+ * grow: a workspace for the largest batch serves every smaller one. */
 
 /* Target of a row that counts for nothing: a prompt's or a padding's.  Such a row is not
  * read; its log probability and entropy are 0, its alternatives -1 with 0. */

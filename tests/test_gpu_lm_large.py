@@ -232,3 +232,29 @@ SHORT = [([1] * 70, 296, 240), ([1, 0, 2, 0, 0, 3] * 12 + [40], 136, 1000), ([5]
 @pytest.mark.parametrize("rank,probes", [(8, 0), (64, 2)])
 def test_short_groups(ctx, lengths, d_in, d_out, rank, probes, dtype):
     _project(ctx, lengths, d_in, d_out, rank, dtype, sum(lengths) + d_out, probes, lead=2, tail=3)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("most,d_in,d_out", [(300, 5120, 5120), (1100, 136, 9000), (40, 264, 20000)])
+def test_one_workspace_for_the_largest_batch(ctx, dtype, most, d_in, d_out):
+    """Fewer rows in the largest batch's workspace, which holds old values, as in their own."""
+    gen = _gen(most)
+    x, w = _rand(gen, most, d_in, dtype=dtype), _rand(gen, d_out, d_in, std=0.05, dtype=dtype)
+    ad = _rand(gen, 2 * 16 * (d_in + d_out), std=0.1, dtype=dtype)
+    t = torch.randint(0, d_out, (most,), generator=gen, device="cuda")
+    t[::5] = zo.ZO_IGNORE_TOKEN
+    ids, probes = torch.tensor([0, 1], dtype=torch.int32).cuda(), torch.tensor([1, -1], dtype=torch.int32).cuda()
+    kw = dict(probes=probes, alphas=torch.tensor([1e-2, 0.0]).cuda(), step=3, n_probes=2)
+    project = torch.full((zo.zo_adapter_workspace_bytes(most, d_in, d_out, 2, 16, 2, 2),), 255,
+                         dtype=torch.uint8, device="cuda")
+    head = torch.full((zo.zo_head_workspace_bytes(most, d_in, d_out),), 255, dtype=torch.uint8, device="cuda")
+    for rows in (most, 260, 257, 256, 129, 65, 64, 33, 32, 17, 16, 5):
+        if rows > most:
+            continue
+        starts = torch.tensor([0, rows // 3, rows], device="cuda")
+        a = zo.zo_adapter_project(ctx, x[:rows], w, ad, 16, starts, ids, workspace=project, **kw)
+        b = zo.zo_adapter_project(ctx, x[:rows], w, ad, 16, starts, ids, **kw)
+        assert torch.equal(a, b), rows
+        a = zo.zo_head_logprobs(ctx, x[:rows], w, t[:rows], workspace=head)
+        b = zo.zo_head_logprobs(ctx, x[:rows], w, t[:rows])
+        assert torch.equal(a.logp, b.logp) and torch.equal(a.entropy, b.entropy), rows

@@ -84,3 +84,21 @@ def test_probe_groups_of_a_batch():
     assert adapter_probe_groups(2, 4, 1.0, clean=False, device="cpu").probes.tolist() == [0, 0, 1, 1]
     only = adapter_probe_groups(0, 4, 1.0, device="cpu")
     assert only.probes.tolist() == [-1] and only.starts.tolist() == [0, 4]
+
+
+@pytest.mark.parametrize("narrow,wide", [(5120, 5120), (768, 2304), (5120, 20480), (64, 64), (40008, 64),
+                                         (7168, 7168), (2048, 520), (768, 50272), (5120, 50272), (4104, 5003)])
+def test_a_workspace_for_many_rows_serves_fewer(narrow, wide):
+    """Sizes never fall as rows grow, though the products' tiles change with them."""
+    most = 0
+    for rows in list(range(0, 1200)) + list(range(1200, 9000, 61)) + [1 << 20, 1 << 25]:
+        need = zo.zo_adapter_workspace_bytes(rows, narrow, wide // 8 * 8, 1, 16, 8, 3)
+        assert need >= most, rows
+        most = need
+    most = 0
+    for rows in list(range(0, 1200)) + list(range(1200, 20000, 61)) + [1 << 20, 1 << 30]:
+        need = zo.zo_head_workspace_bytes(rows, narrow, wide)
+        assert need >= most, rows
+        most = need
+    # slices of tiles, 64 MiB, the list of rows, and at most one statistic of 32 features a row
+    assert zo.zo_head_workspace_bytes(16384, narrow, wide) <= (1 << 26) + 16384 * (8 + 12 * (wide // 32 + 1)) + 2048

@@ -72,9 +72,19 @@ class Context:
 
 
 def _stream(stream=None, dev: int | None = None) -> int:
+    """dev: the device of the operands, where the caller has checked it; a stream of another
+    device is refused then."""
+    if stream is not None:
+        if dev is not None:
+            _on_device(stream, dev)
+        return stream.cuda_stream
     # the raw handle of the current stream: 0.1 us, 2.8 us through a torch.cuda.Stream object
-    return (stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(
-        torch.cuda.current_device() if dev is None else dev))
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev is None else dev)
+
+
+def _on_device(stream, dev: int) -> None:
+    if stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device}, not on the current device cuda:{dev}")
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -492,9 +502,7 @@ def _new(shape, dtype, stream):
     """A new tensor that belongs to the stream the call runs on."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device="cuda")
-    if stream.device.index != torch.cuda.current_device():
-        raise ValueError(f"stream is on {stream.device}, not on the current device "
-                         f"cuda:{torch.cuda.current_device()}")
+    _on_device(stream, torch.cuda.current_device())
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device="cuda")
 

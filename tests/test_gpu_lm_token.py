@@ -334,3 +334,23 @@ def test_nan_at_the_first_index(ctx, dtype, rows, vocab):
         got = _check(ctx, x, t, k)
         assert int(got.top_ids.min()) >= 0 and int(got.top_ids.max()) < vocab
         assert torch.isnan(got.top_logp[:5]).all()
+
+
+def test_stream_of_another_device_is_refused_with_all_outputs_given(ctx):
+    class Other:
+        device = torch.device("cuda", torch.cuda.current_device() + 1)
+        cuda_stream = 0
+    x, w = torch.zeros(2, 64, device="cuda"), torch.zeros(64, 64, device="cuda")
+    t, starts = torch.zeros(2, dtype=torch.int64, device="cuda"), torch.tensor([0, 2], device="cuda")
+    ids = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    rows, y, loss = torch.zeros(2, device="cuda"), x.clone(), torch.zeros(1, dtype=torch.float64, device="cuda")
+    for call in (lambda **k: zo.zo_token_logprobs(ctx, x, t, out=zo.TokenLogprobs(rows, rows.clone(), None, None), **k),
+                 lambda **k: zo.zo_head_logprobs(ctx, x, w, t, out=zo.HeadLogprobs(rows, rows.clone()), workspace=ws, **k),
+                 lambda **k: zo.zo_group_loss(ctx, rows, t, starts, out=loss, **k),
+                 lambda **k: zo.zo_adapter_project(ctx, x, w, x[:0], 0, starts, ids, out=y, workspace=ws, **k)):
+        with pytest.raises(ValueError):
+            call(stream=Other())
+        torch.cuda.synchronize()
+        call(stream=torch.cuda.Stream())
+        torch.cuda.synchronize()

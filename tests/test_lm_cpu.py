@@ -102,3 +102,14 @@ def test_a_workspace_for_many_rows_serves_fewer(narrow, wide):
         most = need
     # slices of tiles, 64 MiB, the list of rows, and at most one statistic of 32 features a row
     assert zo.zo_head_workspace_bytes(16384, narrow, wide) <= (1 << 26) + 16384 * (8 + 12 * (wide // 32 + 1)) + 2048
+
+
+class _OtherStream:
+    device = torch.device("cuda", 1)
+    cuda_stream = 0
+
+
+def test_stream_of_another_device_is_refused_without_allocations():
+    with pytest.raises(ValueError):
+        zo._stream(_OtherStream(), 0)
+    assert zo._stream(_OtherStream(), 1) == 0

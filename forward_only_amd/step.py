@@ -157,14 +157,18 @@ def adapter_probe_groups(n_probes: int, rows: int, alpha: float, *, clean: bool 
     """Groups of a batch that holds `rows` rows for theta + alpha z_i and `rows` for
     theta - alpha z_i of each probe probe0 + i (groups 2 i and 2 i + 1), then, with `clean`,
     `rows` for the adapter as it is."""
-    g = torch.arange(2 * n_probes + (1 if clean else 0), dtype=torch.int32)
-    moved = g < 2 * n_probes
-    probes = torch.where(moved, g // 2, torch.full_like(g, -1))
-    sign = torch.where(g % 2 == 0, 1.0, -1.0) * moved
-    return AdapterGroups(
-        starts=(torch.arange(g.numel() + 1) * rows).to(device), ids=torch.full_like(g, adapter).to(device),
-        probes=probes.to(device), alphas=(sign * alpha).to(torch.float32).to(device), offset=offset,
-        step=step, probe0=probe0, n_probes=n_probes, bits=bits)
+    moved = 2 * n_probes
+    n = moved + (1 if clean else 0)
+    # made on the device, by launches alone: a copy from the host would block, and end a capture
+    starts = torch.arange(n + 1, dtype=torch.int64, device=device) * rows
+    ids = torch.full((n,), adapter, dtype=torch.int32, device=device)
+    probes = torch.arange(n, dtype=torch.int32, device=device).div(2, rounding_mode="floor")
+    probes[moved:].fill_(-1)
+    alphas = torch.zeros(n, dtype=torch.float32, device=device)
+    alphas[0:moved:2].fill_(alpha)
+    alphas[1:moved:2].fill_(-alpha)
+    return AdapterGroups(starts=starts, ids=ids, probes=probes, alphas=alphas, offset=offset,
+                         step=step, probe0=probe0, n_probes=n_probes, bits=bits)
 
 
 def spsa_step_adapters(ctx, adapters: torch.Tensor, *, step: int, npert: int, eps: float, eta: float,

@@ -498,3 +498,48 @@ def test_streams_and_replayed_graph(ctx):
         for a, b in zip(out, want[i]):
             assert torch.equal(torch.nan_to_num(a, 99.0), torch.nan_to_num(b, 99.0))
         both(p[1 - i]["x"])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("mode", ["bits", "regen"])
+def test_step_with_adapters_captured_and_replayed(ctx, dtype, mode):
+    """A whole step in two batches, captured once and replayed, equals the eager step each time."""
+    from forward_only_amd.step import spsa_step_adapters
+    rank, d_in, d_out, vocab, T, npert = 8, 64, 72, 131, 11, 5
+    p = {k: v.cuda() for k, v in _problem([T], d_in, d_out, rank, 1, dtype, seed=31).items()}
+    gen = torch.Generator().manual_seed(32)
+    head = _rand(gen, vocab, d_out, std=0.3, dtype=dtype).cuda()
+    t = torch.randint(0, vocab, (T,), generator=gen)
+    t[::4] = zo.ZO_IGNORE_TOKEN
+    t = t.cuda()
+    theta = p["ad"].clone()
+    bits = zo.zo_gen_probes(ctx, 2, 0, npert, 0, theta.numel()) if mode == "bits" else None
+
+    def logp_of(groups):
+        n = groups.ids.numel()
+        y = zo.zo_adapter_project(ctx, p["x"].repeat(n, 1), p["w"], theta, rank, **groups.of_project())
+        return zo.zo_head_logprobs(ctx, y, head, t.repeat(n), entropy=False).logp
+
+    def step():
+        return spsa_step_adapters(ctx, theta, step=2, npert=npert, eps=2.0 ** -7, eta=1e-2, delta=1e-6,
+                                  logp_of=logp_of, targets=t, bits=bits, probes_per_batch=3)
+
+    def eager(start):
+        theta.copy_(start)
+        r = step()
+        return [theta.clone()] + [r[k].clone() for k in ("L0", "Lp", "Lm", "c")]
+
+    starts = [p["ad"], (p["ad"].float() * 0.5).to(dtype)]
+    want = [eager(s) for s in starts]
+    assert not torch.equal(want[0][0], starts[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for i in (0, 1, 1, 0):
+        theta.copy_(starts[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip([theta] + [out[k] for k in ("L0", "Lp", "Lm", "c")], want[i]):
+            assert torch.equal(a, b)
+        eager(starts[1 - i])

@@ -113,3 +113,25 @@ def test_stream_of_another_device_is_refused_without_allocations():
     with pytest.raises(ValueError):
         zo._stream(_OtherStream(), 0)
     assert zo._stream(_OtherStream(), 1) == 0
+
+
+def test_probe_groups_are_made_on_their_device():
+    """No tensor of the host takes part, so that a step can be captured into a graph."""
+    from torch.utils._python_dispatch import TorchDispatchMode
+    from torch.utils._pytree import tree_flatten
+
+    from forward_only_amd.step import adapter_probe_groups
+    seen = []
+
+    class Watch(TorchDispatchMode):
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            out = func(*args, **(kwargs or {}))
+            seen.extend((str(func), t.device.type) for t in tree_flatten((args, kwargs, out))[0]
+                        if isinstance(t, torch.Tensor))
+            return out
+
+    for n, clean in ((3, True), (2, False), (0, True)):
+        with Watch():
+            g = adapter_probe_groups(n, 5, 0.25, clean=clean, device="meta")
+        assert g.starts.device.type == g.ids.device.type == "meta"
+    assert seen and not [s for s in seen if s[1] != "meta"]

@@ -622,8 +622,9 @@ uint64_t zo_adapter_workspace_bytes(uint64_t rows, uint32_t d_in, uint32_t d_out
                                     uint32_t n_adapters, uint32_t rank, uint32_t n_groups,
                                     uint32_t regenerated)
 {
+    (void)n_groups;     // groups take no room of their own
     const uint64_t params = (uint64_t)n_adapters * rank * ((uint64_t)d_in + d_out);
-    return zo::adapter_u_bytes(rows, rank, n_groups) +
+    return zo::adapter_u_bytes(rows, rank) +
            (zo::slices_up_to(rows, d_out, d_in) ? zo::kBigSliceBytes : 0) +
            (uint64_t)regenerated * zo_bits_stride(params);
 }
@@ -671,7 +672,7 @@ zo_status zo_adapter_project(zo_ctx *c, const void *d_x, uint64_t x_stride, cons
         return ZO_EINVAL;
     float *u = static_cast<float *>(d_workspace), *slices = nullptr;
     if (zo::product_shape(rows, d_out, d_in, dtype == ZO_BF16) == zo::Shape::big)
-        slices = u + zo::adapter_u_bytes(rows, rank, n_groups) / sizeof(float);
+        slices = u + zo::adapter_u_bytes(rows, rank) / sizeof(float);
     zo::AdapterArgs a = {rows, d_in, d_out, rank, n_adapters, n_groups, n_probes, scale, d_starts,
                          d_ids, d_probes, d_alphas, d_bits, zo_bits_stride(params)};
     if (regenerated > 0) {

@@ -20,7 +20,6 @@ namespace zo {
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
@@ -34,11 +33,6 @@ struct Bf16 {
     static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c)
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
-                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-    }
-    static __device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c)
-    {
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                        __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
     }
     static __device__ __forceinline__ float widen(uint16_t v) { return bf16lo_to_f32(v); }
@@ -82,8 +76,7 @@ struct Bf16 {
         }
         return w;
     }
-    template <class Acc>
-    static __device__ __forceinline__ Acc mma(u32x4 a, const Wide &b, Acc c)
+    static __device__ __forceinline__ f32x4 mma(u32x4 a, const Wide &b, f32x4 c)
     {
         return mma(a, b.hi, mma(a, b.lo, c));
     }
@@ -98,14 +91,6 @@ struct Fp32 {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[i]), __uint_as_float(b[i]),
-                                                     c, 0, 0, 0);
-        return c;
-    }
-    static __device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c)
-    {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[i]), __uint_as_float(b[i]),
                                                      c, 0, 0, 0);
         return c;
     }
@@ -400,16 +385,12 @@ __device__ __forceinline__ uint64_t places(uint64_t base, uint64_t rows, const u
     return n <= base ? 0 : (n - base < rows ? n - base : rows);
 }
 
-// Accumulators of one wave: kMF x kMR fragments of kSide features x kSide rows (16 or 32).
-// Lane l holds row l % kSide of a fragment; its value i belongs to feature
-// 8 (i / 4) + 4 (l / kSide) + i % 4.
-template <class T, int kSideOf, int kMFOf, int kMROf>
+// Accumulators of one wave: kMF x kMR fragments of 16 features x 16 rows.  Lane l holds row
+// l % 16 of a fragment; its value i belongs to feature 4 (l / 16) + i.
+template <int kMFOf, int kMROf>
 struct Tile {
-    static constexpr int kSide = kSideOf, kMF = kMFOf, kMR = kMROf;
-    static constexpr int kFours = kSide == 16 ? 1 : 4;      // runs of four features of a lane
-    static constexpr int kReach = 64 / kSide;               // 16-byte pieces of k per fragment
-    typedef std::conditional_t<kSide == 16, f32x4, f32x16> Acc;
-    Acc acc[kMF][kMR];
+    static constexpr int kMF = kMFOf, kMR = kMROf;
+    f32x4 acc[kMF][kMR];
     __device__ __forceinline__ void clear()
     {
 #pragma unroll
@@ -417,7 +398,7 @@ struct Tile {
 #pragma unroll
             for (int n = 0; n < kMR; ++n)
 #pragma unroll
-                for (int i = 0; i < 4 * kFours; ++i) acc[m][n][i] = 0.0f;
+                for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
     }
 };
 
@@ -518,9 +499,9 @@ struct EndProject {
     template <class Tl>
     __device__ __forceinline__ void add_groups(Tl &t, uint32_t g, uint32_t f0, uint64_t r0) const
     {
-        constexpr int kSide = Tl::kSide, kMF = Tl::kMF, kMR = Tl::kMR;
-        const int lane = threadIdx.x & 63, l = lane % kSide, q = lane / kSide;
-        const uint64_t r1 = r0 + kSide * kMR < a.rows ? r0 + kSide * kMR : a.rows;
+        constexpr int kMF = Tl::kMF, kMR = Tl::kMR;
+        const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+        const uint64_t r1 = r0 + 16 * kMR < a.rows ? r0 + 16 * kMR : a.rows;
         for (; g < a.n_groups; ++g) {
             const Group gr = group_of(a, g);
             const uint64_t s = gr.lo, e = gr.hi;
@@ -529,7 +510,7 @@ struct EndProject {
             if (gr.bad) {
 #pragma unroll
                 for (int n = 0; n < kMR; ++n) {
-                    const uint64_t row = r0 + kSide * n + l;
+                    const uint64_t row = r0 + 16 * n + l16;
                     const float nan = row >= s && row < e ? __builtin_nanf("") : 0.0f;
 #pragma unroll
                     for (int m = 0; m < kMF; ++m) t.acc[m][n] += nan;
@@ -539,12 +520,12 @@ struct EndProject {
             // The product is formed apart and added to the group's own rows, so that a NaN in
             // its adapter does not reach the others through 0 * NaN.
             const uint64_t first = gr.base + (uint64_t)a.rank * a.d_in;
-            for (uint32_t j0 = 0; j0 < a.rank; j0 += Tl::kReach * T::kPiece) {
+            for (uint32_t j0 = 0; j0 < a.rank; j0 += 4 * T::kPiece) {
                 const uint32_t j = j0 + q * T::kPiece;
                 typename T::Wide v[kMR];
 #pragma unroll
                 for (int n = 0; n < kMR; ++n) {
-                    const uint64_t row = r0 + kSide * n + l;
+                    const uint64_t row = r0 + 16 * n + l16;
                     const bool in = row >= s && row < e && j < a.rank;
                     const f32x4 *pu = reinterpret_cast<const f32x4 *>(u + (in ? row * a.rank + j : s * a.rank));
                     float z[T::kPiece];
@@ -567,7 +548,7 @@ struct EndProject {
                     uint8_t sg[kAtOnce];
 #pragma unroll
                     for (int m = 0; m < kAtOnce; ++m) {
-                        const uint32_t f = f0 + kSide * (m0 + m) + l;
+                        const uint32_t f = f0 + 16 * (m0 + m) + l16;
                         const uint64_t at = first + (uint64_t)(f < a.d_out ? f : a.d_out - 1) * a.rank +
                                             (j < a.rank ? j : 0);
                         fb[m] = piece_at<T>(adapters + at);
@@ -578,13 +559,13 @@ struct EndProject {
                         if (gr.bits) fb[m] = T::move(fb[m], sg[m] >> (j & 7), gr.alpha);
 #pragma unroll
                         for (int n = 0; n < kMR; ++n) {
-                            const uint64_t row = r0 + kSide * n + l;
-                            if (r0 + kSide * n + kSide <= s || r0 + kSide * n >= e) continue;
+                            const uint64_t row = r0 + 16 * n + l16;
+                            if (r0 + 16 * n + 16 <= s || r0 + 16 * n >= e) continue;
                             const bool in = row >= s && row < e;
-                            typename Tl::Acc zero = {};
-                            const typename Tl::Acc add = T::mma(fb[m], v[n], zero);
+                            f32x4 zero = {};
+                            const f32x4 add = T::mma(fb[m], v[n], zero);
 #pragma unroll
-                            for (int i = 0; i < 4 * Tl::kFours; ++i)
+                            for (int i = 0; i < 4; ++i)
                                 t.acc[m0 + m][n][i] = in ? t.acc[m0 + m][n][i] + add[i] : t.acc[m0 + m][n][i];
                         }
                     }
@@ -596,28 +577,26 @@ struct EndProject {
     template <class Tl>
     __device__ __forceinline__ void store(Tl &t, uint32_t f0, uint64_t r0) const
     {
-        constexpr int kSide = Tl::kSide, kMF = Tl::kMF, kMR = Tl::kMR;
-        const int lane = threadIdx.x & 63, l = lane % kSide, q = lane / kSide;
+        constexpr int kMF = Tl::kMF, kMR = Tl::kMR;
+        const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
         const uint64_t lo = clamp_row(a.starts[0], a.rows);
         const uint64_t hi = clamp_row(a.starts[a.n_groups], a.rows);
 #pragma unroll
         for (int n = 0; n < kMR; ++n) {
-            const uint64_t row = r0 + kSide * n + l;
+            const uint64_t row = r0 + 16 * n + l16;
             if (row < lo || row >= hi) continue;
 #pragma unroll
-            for (int m = 0; m < kMF; ++m)
+            for (int m = 0; m < kMF; ++m) {
+                const uint32_t f = f0 + 16 * m + 4 * q;
+                if (f >= a.d_out) continue;
+                f32x4 v;
 #pragma unroll
-                for (int o = 0; o < Tl::kFours; ++o) {
-                    const uint32_t f = f0 + kSide * m + 8 * o + 4 * q;
-                    if (f >= a.d_out) continue;
-                    f32x4 v;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        v[i] = t.acc[m][n][4 * o + i];
-                        if (bias) v[i] += T::widen(bias[f + i]);
-                    }
-                    store4(y + row * y_stride + f, v);
+                for (int i = 0; i < 4; ++i) {
+                    v[i] = t.acc[m][n][i];
+                    if (bias) v[i] += T::widen(bias[f + i]);
                 }
+                store4(y + row * y_stride + f, v);
+            }
         }
     }
     // The same through LDS, 16 rows at a time: a lane then stores 16 bytes next to its
@@ -627,7 +606,6 @@ struct EndProject {
     __device__ __forceinline__ void store_rows(Tl &t, uint32_t f0, uint64_t r0, u32x4 *lds) const
     {
         constexpr int kMF = Tl::kMF, kMR = Tl::kMR;
-        static_assert(Tl::kSide == 16, "lanes of 16 rows");
         constexpr int kRowPieces = 16 * kMF / T::kPiece, kAtOnce = 64 / kRowPieces;
         const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
         const uint64_t lo = clamp_row(a.starts[0], a.rows);
@@ -700,46 +678,46 @@ struct EndHead {
     template <class Tl>
     __device__ __forceinline__ void store(Tl &tile, uint32_t f0, uint64_t r0) const
     {
-        constexpr int kSide = Tl::kSide, kMF = Tl::kMF, kMR = Tl::kMR;
-        const int lane = threadIdx.x & 63, l = lane % kSide, q = lane / kSide;
-        const uint32_t part = f0 / (kSide * kMF);
+        constexpr int kMF = Tl::kMF, kMR = Tl::kMR;
+        const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+        const uint32_t part = f0 / (16 * kMF);
         if (f0 >= features) return;
         const uint64_t have = places(base, rows, count);
 #pragma unroll
         for (int n = 0; n < kMR; ++n) {
-            const uint64_t at = r0 + kSide * n + l;
+            const uint64_t at = r0 + 16 * n + l16;
             SoftStats st = SoftStats::empty();
             int64_t tgt = -1;
             if (targets && at < have) tgt = targets[list ? list[base + at] : base + at];
-            const auto feature = [&](int m4, int i) { return f0 + kSide * m4 + 8 * (i / 4) + 4 * q + i % 4; };
-            if (f0 + kSide * kMF > features) {
+            const auto feature = [&](int m4, int i) { return f0 + 16 * m4 + 4 * q + i; };
+            if (f0 + 16 * kMF > features) {
 #pragma unroll
                 for (int m4 = 0; m4 < kMF; ++m4)
 #pragma unroll
-                    for (int i = 0; i < 4 * Tl::kFours; ++i)
+                    for (int i = 0; i < 4; ++i)
                         if (feature(m4, i) >= features) tile.acc[m4][n][i] = -INFINITY;
             }
             float top = -INFINITY;
 #pragma unroll
             for (int m4 = 0; m4 < kMF; ++m4)
 #pragma unroll
-                for (int i = 0; i < 4 * Tl::kFours; ++i) top = fmaxf(top, tile.acc[m4][n][i]);
+                for (int i = 0; i < 4; ++i) top = fmaxf(top, tile.acc[m4][n][i]);
             st.raise(top);
 #pragma unroll
             for (int m4 = 0; m4 < kMF; ++m4)
 #pragma unroll
-                for (int i = 0; i < 4 * Tl::kFours; ++i) st.add(tile.acc[m4][n][i]);
+                for (int i = 0; i < 4; ++i) st.add(tile.acc[m4][n][i]);
             // few waves hold a row's target
             const uint32_t in = (uint32_t)(tgt - f0);
-            const bool here = at < have && tgt >= (int64_t)f0 && tgt < (int64_t)features && in < kSide * kMF;
+            const bool here = at < have && tgt >= (int64_t)f0 && tgt < (int64_t)features && in < 16 * kMF;
             if (__any(here)) {
 #pragma unroll
                 for (int m4 = 0; m4 < kMF; ++m4)
 #pragma unroll
-                    for (int i = 0; i < 4 * Tl::kFours; ++i)
+                    for (int i = 0; i < 4; ++i)
                         if (here && feature(m4, i) - f0 == in) tl[at] = tile.acc[m4][n][i];
             }
-            st.wave_merge(32, kSide);
+            st.wave_merge(32, 16);
             if (q == 0 && at < have) {
                 m[(uint64_t)part * rows + at] = st.m;
                 s[(uint64_t)part * rows + at] = st.s;
@@ -866,7 +844,7 @@ __global__ __launch_bounds__(512, 2) void k_big(ProductArgs p, const typename T:
             __builtin_amdgcn_global_load_lds((gptr_t)g, (lptr_t)l, 16, 0, 0);
         }
     };
-    Tile<T, 16, 8, 4> t;
+    Tile<8, 4> t;
     t.clear();
     u32x4 ff[2][4], fr[2][4];                   // [c][fragment]
     const auto read_f = [&](int h, uint32_t step) {
@@ -965,7 +943,7 @@ __global__ __launch_bounds__(256) void k_slices(ProductArgs p, const uint32_t *c
     if (r0 >= rows) return;
     const f32x4 *from = reinterpret_cast<const f32x4 *>(p.slices) +
                         ((uint64_t)i * cut.slices * 8 + of) * 32 * 64 + (n * 8) * 64 + lane;
-    Tile<T, 16, 8, 1> t;
+    Tile<8, 1> t;
     t.clear();
 #pragma unroll 2
     for (uint32_t s = wave; s < cut.slices; s += 4)
@@ -1032,7 +1010,7 @@ __global__ __launch_bounds__(256) void k_mid(ProductArgs p, const typename T::el
                 __builtin_amdgcn_global_load_lds((gptr_t)g, (lptr_t)l, 16, 0, 0);
             }
     };
-    Tile<T, 16, 2, 2> t;
+    Tile<2, 2> t;
     t.clear();
 #pragma unroll
     for (uint32_t s = 0; s < kMidStages - 1; ++s) issue(s);
@@ -1089,7 +1067,7 @@ __global__ __launch_bounds__((kFewWaves + kMR) * 64) void k_few(ProductArgs p,
     f32x4 *sums = reinterpret_cast<f32x4 *>(stage);
     if (wave >= kFewWaves) {
         const int n = wave - kFewWaves;
-        Tile<T, 16, kMF, 1> own;
+        Tile<kMF, 1> own;
         own.clear();
         end.add_rows(own, 0, f0, 16 * n);
         __syncthreads();                        // the stages are free
@@ -1109,7 +1087,7 @@ __global__ __launch_bounds__((kFewWaves + kMR) * 64) void k_few(ProductArgs p,
         const uint64_t r = (uint64_t)(i - 16 * kMF) < p.rows ? i - 16 * kMF : p.rows - 1;
         return x + r * p.x_stride;
     });
-    Tile<T, 16, kMF, kMR> t;
+    Tile<kMF, kMR> t;
     t.clear();
     const uint32_t steps = feed.steps();
     // Each workgroup begins elsewhere in k: rows a power of two apart lie on the same memory

@@ -228,9 +228,8 @@ inline bool slices_up_to(uint64_t rows, uint32_t features, uint32_t k)
            most_rows(true, rows, features, k, false);
 }
 // Bytes of x A^T, [rows][rank] floats, and of each row's group.
-inline uint64_t adapter_u_bytes(uint64_t rows, uint32_t rank, uint32_t n_groups)
+inline uint64_t adapter_u_bytes(uint64_t rows, uint32_t rank)
 {
-    (void)n_groups;
     return (rows * rank * 4 + rows * 4 + 255) / 256 * 256;
 }
 // u: adapter_u_bytes of workspace; slices: kBigSliceBytes if the shape is big, else nullptr.

@@ -461,6 +461,7 @@ zo_status zo_group_loss(zo_ctx *ctx, const float *d_logp, const int64_t *d_targe
  * NaN; other groups' rows do not see it.
  * d_workspace: device, 256-byte aligned, at least zo_adapter_workspace_bytes(...) bytes, with
  * regenerated = n_probes if d_probes is given and d_bits is NULL, else 0.
+ * (n_groups changes nothing about the size.)
  * Errors: ZO_EINVAL for NULL pointers (with rows and n_groups > 0; d_adapters may be NULL
  * with n_adapters == 0 or rank == 0), unknown dtype, shapes and strides outside these limits,
  * misalignment, offset % 128 != 0 or range overflow, probe indices past 2^32 - 1, a

@@ -543,3 +543,64 @@ def test_step_with_adapters_captured_and_replayed(ctx, dtype, mode):
         for a, b in zip([theta] + [out[k] for k in ("L0", "Lp", "Lm", "c")], want[i]):
             assert torch.equal(a, b)
         eager(starts[1 - i])
+
+
+# few rows; 64 x 64 tiles, group by group and row by row; 256 x 256 tiles, whole and in slices
+@pytest.mark.parametrize("lengths,d_in,d_out", [([3, 4], 64, 72), ([30, 50, 1], 264, 136), ([1] * 90, 72, 264),
+                                                ([1100], 136, 9000), ([400, 300], 4104, 5000)])
+@pytest.mark.parametrize("rank", [8, 64, 128])
+def test_fp32_adapter_product_keeps_32_bits(ctx, lengths, d_in, d_out, rank):
+    """fp32 alone, without the bound of bf16's two parts: W is 0 and each row of x has one value,
+    so that x W^T is exact and x A^T rounds once.  What is left of y = scale u B^T rounds twice a
+    term (product and sum), once for u, scale and the result each, and once per eight terms where
+    parts are added: (2 + 1/8) rank + 3 half steps of the terms' magnitudes."""
+    gen = torch.Generator().manual_seed(rank + d_out)
+    rows, adapters = sum(lengths), 2
+    x = torch.zeros(rows, d_in)
+    x[torch.arange(rows), torch.arange(rows) * 7 % d_in] = torch.randn(rows, generator=gen)
+    w = torch.zeros(d_out, d_in)
+    ad = torch.randn(adapters * rank * (d_in + d_out), generator=gen)
+    starts = torch.tensor([0] + lengths).cumsum(0)
+    ids = torch.arange(len(lengths), dtype=torch.int32) % adapters
+    got = zo.zo_adapter_project(ctx, x.cuda(), w.cuda(), ad.cuda(), rank, starts.cuda(), ids.cuda(), scale=0.3)
+    y, low, _ = ref.project(x, w, None, ad, rank, starts, ids, float(torch.tensor(0.3)))
+    ref.assert_close(got, y, (2.125 * rank + 3) * ref.U32 * low + 1e-30, "y")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("mode", ["bits", "regen"])
+def test_adapters_of_two_projections_in_one_buffer(ctx, dtype, mode):
+    """Each projection takes its part of the flat buffer, of its indices and of stored rows; every
+    group's rows equal those at the whole buffer moved by zo_perturb."""
+    from forward_only_amd.step import adapter_probe_groups
+    rank, d, wide, T, n, offset, step = 8, 72, 112, 7, 3, 256, 6
+    gen = torch.Generator().manual_seed(41)
+    x, w1, w2 = (_rand(gen, *s, std=0.2, dtype=dtype).cuda() for s in ((T, d), (wide, d), (d, wide)))
+    per = rank * (d + wide)
+    begin = (per + 127) // 128 * 128            # where the second adapter begins
+    assert begin > per
+    theta = _rand(gen, begin + per, std=0.1, dtype=dtype).cuda()
+    bits = zo.zo_gen_probes(ctx, step, 0, n, offset, theta.numel()) if mode == "bits" else None
+    groups = adapter_probe_groups(n, T, 2.0 ** -6, offset=offset, step=step, bits=bits)
+    G = groups.ids.numel()
+
+    def model(th, moved):
+        y = x.repeat(G, 1)
+        for w, a, b in ((w1, 0, per), (w2, begin, begin + per)):
+            kw = {"starts": groups.starts, "ids": groups.ids}
+            if moved:
+                kw = groups.of_project()
+                kw["offset"] += a
+                if bits is not None:
+                    kw["bits"] = bits[:, a // 8:][:, :zo.zo_bits_stride(b - a)].contiguous()
+            y = zo.zo_adapter_project(ctx, y, w, th[a:b], rank, **kw)
+        return y
+
+    got = model(theta, True)
+    for g in range(G):
+        th = theta.clone()
+        p = int(groups.probes[g])
+        if p >= 0:
+            zo.zo_perturb(ctx, th, offset, step, p, float(groups.alphas[g]))
+        want = model(th, False)
+        assert torch.equal(got[g * T:(g + 1) * T], want[g * T:(g + 1) * T]), g

@@ -8,6 +8,12 @@ Bounds (u = 2^-24, half an fp32 step; u_bf16 = 2^-8, half a bf16 step, both rela
     another in each of 256 threads, then a tree, each merge rescaling once more.  Hence
       E = (V / 256 + 64) u   bounds the absolute error of log s,
       logp: E + u (|x_t - m| + |logp|),  entropy: E (1 + |t / s|) + E |t / s|, |t / s| <= 13.
+    Where E is not a sum of worst cases: rows of up to 12 KB are added by 64 threads, up to
+    V / 64 = 96 terms one after another, worst case 96 + 64 against E = 88 u at V = 6144; and the
+    head adds up to 32 features in a lane and then joins parts.  There E counts on roundings of
+    random sign: an error uniform within u of a partial sum that grows to the whole gives eight
+    standard deviations of 8 sqrt(96 / 9) u = 26 u for 96 terms, which with the terms' 32 u stays
+    below E.
   * a product of k terms summed in fp32: rounding errors of random sign, k of them, each at
     most u times a partial sum; 8 sqrt(k) u |x| |w| (2-norms) is eight standard deviations
     or more.

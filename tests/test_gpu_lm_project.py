@@ -604,3 +604,44 @@ def test_adapters_of_two_projections_in_one_buffer(ctx, dtype, mode):
             zo.zo_perturb(ctx, th, offset, step, p, float(groups.alphas[g]))
         want = model(th, False)
         assert torch.equal(got[g * T:(g + 1) * T], want[g * T:(g + 1) * T]), g
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("rows,d,vocab", [(9, 64, 333), (60, 64, 8000), (130, 64, 333), (700, 4104, 5003)])
+def test_head_whatever_ignored_rows_hold(ctx, rows, d, vocab, dtype):
+    """Padding of NaN and infinities: zeros for it, and not a bit of the other rows moves."""
+    gen = torch.Generator().manual_seed(rows)
+    hidden = _rand(gen, rows, d, dtype=dtype).cuda()
+    weight = _rand(gen, vocab, d, std=0.1, dtype=dtype).cuda()
+    t = torch.arange(rows, device="cuda") % vocab
+    skip = torch.arange(rows, device="cuda") % 3 != 1
+    t[skip] = zo.ZO_IGNORE_TOKEN
+    clean = zo.zo_head_logprobs(ctx, hidden, weight, t)
+    hidden[skip] = math.nan
+    hidden[0] = math.inf
+    got = zo.zo_head_logprobs(ctx, hidden, weight, t)
+    for a, b in zip(got, clean):
+        assert torch.equal(a, b) and not a[skip].any() and torch.isfinite(a).all()
+    t[:] = zo.ZO_IGNORE_TOKEN
+    got = zo.zo_head_logprobs(ctx, hidden, weight, t)
+    assert not got.logp.any() and not got.entropy.any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("rows", [20, 90, 700])
+def test_one_row_read_as_many(ctx, rows, dtype):
+    """Rows no elements apart: the same row for every group."""
+    d_in, d_out = 4104, 5000
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x, w, ad = (torch.randn(*s, generator=gen, device="cuda").mul(0.05).to(dtype)
+                for s in ((1, d_in), (d_out, d_in), (2 * 16 * (d_in + d_out),)))
+    starts = torch.tensor([0, rows // 2, rows - 1, rows], device="cuda")
+    ids = torch.tensor([0, 1, -1], dtype=torch.int32, device="cuda")
+    many = x.expand(rows, d_in)
+    assert many.stride(0) == 0
+    got = zo.zo_adapter_project(ctx, many, w, ad, 16, starts, ids)
+    assert torch.equal(got, zo.zo_adapter_project(ctx, many.contiguous(), w, ad, 16, starts, ids))
+    t = torch.arange(rows, device="cuda")
+    head = w[:1001]
+    a, b = (zo.zo_head_logprobs(ctx, v, head, t) for v in (many, many.contiguous()))
+    assert torch.equal(a.logp, b.logp) and torch.equal(a.entropy, b.entropy)

@@ -587,7 +587,8 @@ def zo_head_logprobs(ctx: Context, hidden: torch.Tensor, weight: torch.Tensor,
                      stream=None) -> HeadLogprobs:
     """Log probabilities of the targets and entropies of the logits hidden @ weight.T (hidden
     [rows, d], weight [vocab, d] contiguous, one dtype, d a multiple of 8), which are never
-    stored; rows with the target ZO_IGNORE_TOKEN are not computed and give 0, 0."""
+    stored; rows with the target ZO_IGNORE_TOKEN give 0, 0 and, beyond 64 rows, are not computed.
+    workspace: at least zo_head_workspace_bytes of the largest batch that it serves."""
     hp, rows, d, stride = _matrix(hidden, "hidden")
     dev = hidden.get_device()
     code = _dtype_code(hidden)

@@ -182,10 +182,14 @@ def spsa_step_adapters(ctx, adapters: torch.Tensor, *, step: int, npert: int, ep
     adapter_probe_groups -- its adapted projections with zo_adapter_project(ctx, x, weight,
     adapters, rank, **groups.of_project()) -- and returns the targets' log probabilities,
     float32 [groups * rows] (zo_head_logprobs or zo_token_logprobs, with targets repeated
-    once per group).  The loss of a group is its mean negative log probability
-    (zo_group_loss).  At most probes_per_batch probes go through the model at once; the
-    adapters are only written by the update.  Other arguments and the result as
-    spsa_step_fused.
+    once per group).  With adapters of several projections in the buffer, each beginning at a
+    multiple of 128, a projection takes its part [a, b): adapters[a:b], offset + a, and of
+    stored rows bits[:, a // 8:][:, :zo_bits_stride(b - a)].contiguous().  The loss of a group
+    is its mean negative log probability (zo_group_loss).  At most probes_per_batch probes go
+    through the model at once; the adapters are only written by the update.  The step's calls
+    can be captured into a graph.  The losses of a group differ in rounding with its place and
+    with the batch (order of sums), so that a probe that moves nothing may leave a difference
+    of that size.  Other arguments and the result as spsa_step_fused.
     """
     if probes_per_batch < 1:
         raise ValueError("probes_per_batch must be positive")

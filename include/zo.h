@@ -372,10 +372,16 @@ zo_status zo_mlp_loss_pair_noalloc(zo_ctx *ctx, const float *d_params, uint64_t 
  * outside their range never lead to an access outside a buffer: starts are forced into
  * [0, rows], and what depends on another bad index becomes NaN, so that zo_probe_weights
  * drops the probe.  Inputs and outputs must not overlap.  Workspace sizes never fall as rows
- * grow: a workspace for the largest batch serves every smaller one. */
+ * grow: a workspace for the largest batch serves every smaller one.
+ *
+ * Every call is deterministic: repeated on the same arguments it gives the same bits.  But the
+ * order of a row's sums depends on its place in the batch and on the batch's rows and groups, so
+ * that both signs of a probe, the clean pass and a call of one group alone agree within the
+ * rounding of fp32 sums (and of y in bf16), not bit for bit as the fused losses above do.  A
+ * difference of two losses below that rounding is noise. */
 
-/* Target of a row that counts for nothing: a prompt's or a padding's.  Such a row is not
- * read; its log probability and entropy are 0, its alternatives -1 with 0. */
+/* Target of a row that counts for nothing: a prompt's or a padding's.  Whatever such a row
+ * holds, its log probability and entropy are 0, its alternatives -1 with 0. */
 #define ZO_IGNORE_TOKEN (-100)
 
 /* Most alternatives one zo_token_logprobs call gives. */
@@ -392,8 +398,8 @@ zo_status zo_mlp_loss_pair_noalloc(zo_ctx *ctx, const float *d_params, uint64_t 
  * pass over the logits, fp32 sums, deterministic.  d_logits: device, rows of vocab elements
  * of `dtype`, row_stride elements apart, each row contiguous, at any element-aligned address.
  * d_targets: device int64 [rows], or NULL (no given tokens: d_logp must be NULL too);
- * ZO_IGNORE_TOKEN as above, any other target outside [0, vocab) gives NaN.  d_entropy may be
- * NULL; d_top_ids and d_top_logp may be NULL with top_k == 0.
+ * ZO_IGNORE_TOKEN as above (the row is not read), any other target outside [0, vocab) gives
+ * NaN.  d_entropy may be NULL; d_top_ids and d_top_logp may be NULL with top_k == 0.
  * Logits of -inf have probability 0 (a target there gets -inf); a row of only -inf, or one
  * that holds NaN or +inf, has NaN log probabilities and entropy.
  * Errors: ZO_EINVAL for NULL pointers (with rows > 0), unknown dtype, vocab == 0 (with
@@ -407,7 +413,8 @@ zo_status zo_token_logprobs(zo_ctx *ctx, const void *d_logits, zo_dtype dtype, u
 /* The same log probabilities and entropies from hidden states [rows x d] and the
  * unembedding matrix [vocab x d]: logits h W^T are formed tile by tile in fp32 registers
  * (products of dtype values, fp32 sums) and never stored.  Rows with the ignored target are
- * not computed.  d_hidden: device, rows hidden_stride elements apart (a multiple of 8),
+ * not computed, but in batches of at most 64 rows, where the weights are read in any case, they
+ * may be.  d_hidden: device, rows hidden_stride elements apart (a multiple of 8),
  * 16-byte aligned; d_weight: device, contiguous, 16-byte aligned; both of `dtype`; d a
  * multiple of 8.  d_targets, d_logp, d_entropy as zo_token_logprobs; at least one of d_logp
  * and d_entropy.  d_workspace: device, 256-byte aligned, at least
@@ -436,8 +443,8 @@ zo_status zo_group_loss(zo_ctx *ctx, const float *d_logp, const int64_t *d_targe
 /* A shared projection with low-rank adapters of many requests, or of many probes, beside it:
  *   y = x W^T + bias + scale (x A_g^T) B_g^T
  * for each row of group g, the rows [d_starts[g], d_starts[g + 1]).  All rows share each load
- * of W.  x A_g^T is kept in fp32 (with bf16 operands its two leading bf16 parts enter the
- * second product); y is rounded once.
+ * of W.  x A_g^T is kept in fp32; with bf16 operands it enters the second product as it is or
+ * as its two leading bf16 parts (16 bits), by the batch's rows and groups.  y is rounded once.
  * d_x: device, rows x_stride elements apart (a multiple of 8), 16-byte aligned; d_weight:
  * device [d_out x d_in] row-major, 16-byte aligned; d_bias: device [d_out] or NULL, 16-byte
  * aligned; d_y: device, rows y_stride elements apart (a multiple of 8), 16-byte aligned; all,

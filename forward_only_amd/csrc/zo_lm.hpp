@@ -1,5 +1,5 @@
 // zo_lm.hpp -- device helpers of the language-model operators (k_token, k_project): softmax
-// statistics in one pass, clamped row indices, and 16-byte fragments of both parameter types.
+// statistics in one pass, against e and against 2, and clamped row indices.
 #pragma once
 
 #include <hip/hip_runtime.h>

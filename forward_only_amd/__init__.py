@@ -12,8 +12,8 @@ sizes).  All arithmetic runs in the library's HIP kernels; there is no CPU path.
     c = zo_probe_weights(ctx, Lp, Lm, L0, eps, delta)
     zo_update(ctx, theta, offset, step, c, eta)             # theta - eta * sum c_i z_i
 
-The language-model operators (zo_adapter_project, zo_head_logprobs, zo_token_logprobs,
-zo_group_loss) turn a batch of rows into such losses; their matrices may have rows further
+The language-model operators (zo_adapter_project, zo_q4_project, zo_head_logprobs,
+zo_token_logprobs, zo_distill_loss, zo_group_loss) turn a batch of rows into such losses; their matrices may have rows further
 apart than their length, and what they allocate belongs to the stream they run on.
 """
 from __future__ import annotations
@@ -25,7 +25,7 @@ import torch
 
 from . import _lib
 from ._lib import (ZO_BF16, ZO_EHIP, ZO_EINVAL, ZO_ENOMEM, ZO_EUNSUPPORTED, ZO_FP32,  # noqa: F401
-                   ZO_IGNORE_TOKEN, ZO_MAX_NPERT, ZO_MAX_RANK, ZO_MAX_TOP_K, ZO_NOALLOC_SCRATCH_BYTES, ZO_OK, ZO_WEIGHTS_POWER, ZO_WEIGHTS_PRECOND,
+                   ZO_IGNORE_TOKEN, ZO_MAX_NPERT, ZO_MAX_RANK, ZO_MAX_TEACHER, ZO_MAX_TOP_K, ZO_NOALLOC_SCRATCH_BYTES, ZO_OK, ZO_WEIGHTS_POWER, ZO_WEIGHTS_PRECOND,
                    ZO_WEIGHTS_SPSA_MEAN, ZOError)
 
 __all__ = [
@@ -38,7 +38,8 @@ __all__ = [
     "zo_mlp_loss_pair_noalloc", "zo_stream_rmw", "zo_tune_placement", "zo_set_slice_bytes",
     "zo_get_slice_bytes", "library_path", "TokenLogprobs", "HeadLogprobs",
     "zo_token_logprobs", "zo_head_workspace_bytes", "zo_head_logprobs", "zo_group_loss",
-    "zo_adapter_workspace_bytes", "zo_adapter_project",
+    "zo_adapter_workspace_bytes", "zo_adapter_project", "DistillLoss", "zo_distill_loss", "Q4Weight",
+    "zo_q4_quantize", "zo_q4_pack", "zo_q4_unpack", "zo_q4_workspace_bytes", "zo_q4_project",
 ]
 
 
@@ -87,12 +88,16 @@ def _on_device(stream, dev: int) -> None:
         raise ValueError(f"stream is on {stream.device}, not on the current device cuda:{dev}")
 
 
-def _dtype_code(t: torch.Tensor) -> int:
-    if t.dtype == torch.float32:
+def _code_of(dtype) -> int:
+    if dtype == torch.float32:
         return ZO_FP32
-    if t.dtype == torch.bfloat16:
+    if dtype == torch.bfloat16:
         return ZO_BF16
-    raise TypeError(f"parameters must be float32 or bfloat16, got {t.dtype}")
+    raise TypeError(f"parameters must be float32 or bfloat16, got {dtype}")
+
+
+def _dtype_code(t: torch.Tensor) -> int:
+    return _code_of(t.dtype)
 
 
 def _dev(t: torch.Tensor, name: str, dtype=None) -> int:
@@ -646,6 +651,46 @@ def zo_adapter_workspace_bytes(rows: int, d_in: int, d_out: int, n_adapters: int
                                                      regenerated))
 
 
+def _adapters(adapters: torch.Tensor, rank: int, d_in: int, d_out: int, dtype):
+    """(device pointer, number) of the adapters in a flat buffer."""
+    ap = _dev(adapters, "adapters", dtype)
+    per = rank * (d_in + d_out)
+    if rank < 0 or (adapters.numel() % per if per else adapters.numel()):
+        raise ValueError(f"adapters must hold a whole number of adapters of {per} values")
+    return ap, adapters.numel() // per if per else 0
+
+
+def _groups(starts, ids, probes, alphas, n_probes, bits, params: int, dev: int):
+    """(groups, starts, ids, probes, alphas, n_probes, bits) as the library takes them."""
+    n = starts.numel() - 1
+    if n < 0:
+        raise ValueError("starts must hold the groups' first rows and the end of the last one")
+    sp = _vector(starts, "starts", n + 1, torch.int64, dev)
+    ip = _vector(ids, "ids", n, torch.int32, dev)
+    if (probes is None) != (alphas is None):
+        raise ValueError("give both probes and alphas or neither")
+    pp = _vector(probes, "probes", n, torch.int32, dev)
+    fp = _vector(alphas, "alphas", n, torch.float32, dev)
+    if probes is None:
+        n_probes, bits = 0, None
+    elif n_probes is None:
+        if bits is None:
+            raise ValueError("n_probes is needed to regenerate the signs")
+        n_probes = bits.shape[0]
+    return n, sp, ip, pp, fp, n_probes, _rows(bits, n_probes, params)
+
+
+def _projected(out, rows: int, d_out: int, dtype, stream):
+    """(device pointer, elements between rows, tensor) of a projection's output."""
+    if out is None:
+        out = _new((rows, d_out), dtype, stream)
+        return out.data_ptr(), d_out, out
+    yp, yr, yc, ys = _matrix(out, "out", dtype)
+    if (yr, yc) != (rows, d_out):
+        raise ValueError(f"out must have shape ({rows}, {d_out}), got {tuple(out.shape)}")
+    return yp, ys, out
+
+
 def zo_adapter_project(ctx: Context, x: torch.Tensor, weight: torch.Tensor,
                        adapters: torch.Tensor, rank: int, starts: torch.Tensor,
                        ids: torch.Tensor, scale: float = 1.0, bias: torch.Tensor | None = None,
@@ -671,37 +716,13 @@ def zo_adapter_project(ctx: Context, x: torch.Tensor, weight: torch.Tensor,
     if weight.dim() != 2 or weight.shape[1] != d_in:
         raise ValueError(f"weight must have shape (d_out, {d_in}), got {tuple(weight.shape)}")
     d_out, rank = weight.shape[0], int(rank)
-    ap = _dev(adapters, "adapters", x.dtype)
-    per = rank * (d_in + d_out)
-    if rank < 0 or (adapters.numel() % per if per else adapters.numel()):
-        raise ValueError(f"adapters must hold a whole number of adapters of {per} values")
-    n_adapters = adapters.numel() // per if per else 0
-    n = starts.numel() - 1
-    if n < 0:
-        raise ValueError("starts must hold the groups' first rows and the end of the last one")
-    sp = _vector(starts, "starts", n + 1, torch.int64, dev)
-    ip, bp = _vector(ids, "ids", n, torch.int32, dev), _vector(bias, "bias", d_out, x.dtype, dev)
-    if (probes is None) != (alphas is None):
-        raise ValueError("give both probes and alphas or neither")
-    pp = _vector(probes, "probes", n, torch.int32, dev)
-    fp = _vector(alphas, "alphas", n, torch.float32, dev)
-    if probes is None:
-        n_probes, bits = 0, None
-    elif n_probes is None:
-        if bits is None:
-            raise ValueError("n_probes is needed to regenerate the signs")
-        n_probes = bits.shape[0]
-    kp = _rows(bits, n_probes, adapters.numel())
-    if out is None:
-        out = _new((rows, d_out), x.dtype, stream)
-        yp, ys = out.data_ptr(), d_out
-    else:
-        yp, yr, yc, ys = _matrix(out, "out", x.dtype)
-        if (yr, yc) != (rows, d_out):
-            raise ValueError(f"out must have shape ({rows}, {d_out}), got {tuple(out.shape)}")
+    ap, n_adapters = _adapters(adapters, rank, d_in, d_out, x.dtype)
+    n, sp, ip, pp, fp, n_probes, kp = _groups(starts, ids, probes, alphas, n_probes, bits, adapters.numel(), dev)
+    bp = _vector(bias, "bias", d_out, x.dtype, dev)
+    yp, ys, out = _projected(out, rows, d_out, x.dtype, stream)
     if workspace is None:
         wb = zo_adapter_workspace_bytes(rows, d_in, d_out, n_adapters, rank, n,
-                                        n_probes if bits is None else 0)
+                                        n_probes if kp is None else 0)
         workspace = _new(wb, torch.uint8, stream)
         ws = workspace.data_ptr()
     else:
@@ -710,4 +731,193 @@ def zo_adapter_project(ctx: Context, x: torch.Tensor, weight: torch.Tensor,
         ctx.handle, xp, xs, wp, bp, code, rows, d_in, d_out, ap, n_adapters, rank, float(scale),
         sp, ip, n, pp, fp, offset, step, probe0, n_probes, kp, ws, wb, yp, ys, _stream(stream, dev)),
         "zo_adapter_project")
+    return out
+
+
+class DistillLoss(NamedTuple):
+    """Results of zo_distill_loss; grad is None where it was not asked for."""
+    loss: torch.Tensor
+    grad: Optional[torch.Tensor]
+
+
+def zo_distill_loss(ctx: Context, logits: torch.Tensor, teacher_ids: torch.Tensor,
+                    teacher_logits: torch.Tensor, targets: torch.Tensor | None = None,
+                    temperature: float = 1.0, grad: bool = False,
+                    row_grad: torch.Tensor | None = None, out: DistillLoss | None = None,
+                    stream=None) -> DistillLoss:
+    """Divergence of a teacher's top logits from the distribution of logits [rows, vocab], per row
+    (float32): with p = softmax(teacher_logits / T) over the row's entries (teacher_ids int64
+    [rows, k], -1 for none; teacher_logits float32, logits or log probabilities) and
+    Q = softmax(logits / T), T^2 sum_j p_j (log p_j - log Q_j).  grad: also the gradient of
+    sum(row_grad * loss) with respect to the logits, in their dtype (row_grad float32 [rows];
+    None: ones).  Rows with the target ZO_IGNORE_TOKEN, and rows without entries, give 0.
+    out: tensors of an earlier call of the same shapes; out.grad may be the logits themselves."""
+    lp, rows, vocab, stride = _matrix(logits, "logits")
+    dev = logits.get_device()
+    code = _dtype_code(logits)
+    k = teacher_ids.shape[1] if teacher_ids.dim() == 2 else -1
+    if tuple(teacher_ids.shape) != (rows, k) or teacher_logits.shape != teacher_ids.shape:
+        raise ValueError(f"teacher_ids and teacher_logits must have one shape ({rows}, k), got "
+                         f"{tuple(teacher_ids.shape)} and {tuple(teacher_logits.shape)}")
+    if not 0 <= k <= ZO_MAX_TEACHER:
+        raise ValueError(f"at most {ZO_MAX_TEACHER} entries a row")
+    idp, hp = _dev(teacher_ids, "teacher_ids", torch.int64), _dev(teacher_logits, "teacher_logits", torch.float32)
+    if not 0.0 < float(temperature) < float("inf"):
+        raise ValueError("temperature must be positive and finite")
+    tp = _vector(targets, "targets", rows, torch.int64, dev)
+    if row_grad is not None and not (grad or (out is not None and out.grad is not None)):
+        raise ValueError("row_grad goes with grad")
+    rp = _vector(row_grad, "row_grad", rows, torch.float32, dev)
+    if out is None:
+        out = DistillLoss(_new(rows, torch.float32, stream),
+                          _new((rows, vocab), logits.dtype, stream) if grad else None)
+    op, gp, gs = _vector(out.loss, "loss", rows, torch.float32, dev), None, vocab
+    if out.grad is not None:
+        gp, gr, gc, gs = _matrix(out.grad, "grad", logits.dtype)
+        if (gr, gc) != (rows, vocab):
+            raise ValueError(f"grad must have shape ({rows}, {vocab}), got {tuple(out.grad.shape)}")
+    elif grad:
+        raise ValueError("out has no grad")
+    _lib.check(_lib.lib().zo_distill_loss(ctx.handle, lp, code, rows, vocab, stride, idp, hp, k, tp,
+                                          float(temperature), op, rp, gp, gs, _stream(stream, dev)),
+               "zo_distill_loss")
+    return out
+
+
+class Q4Weight(NamedTuple):
+    """A matrix [d_out, d_in] in 4 bits: codes uint8 [ceil(d_out / 16), ceil(d_in / 128), 1024] in the
+    library's blocks (zo_q4_quantize, zo_q4_pack), scales [d_in / group, d_out] of the activations'
+    dtype, zeros (zero points) of the same shape or None (8), and d_in."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    zeros: Optional[torch.Tensor]
+    d_in: int
+
+    @property
+    def shape(self):
+        return self.scales.shape[1], self.d_in
+
+
+def _q4(weight: Q4Weight, dtype=None):
+    """(codes, scales, zeros, d_out, d_in, group) of a matrix in 4 bits."""
+    codes, scales, zeros, d_in = weight
+    sp = _dev(scales, "scales", dtype)
+    _dtype_code(scales)
+    if scales.dim() != 2 or d_in <= 0 or d_in % max(1, scales.shape[0]):
+        raise ValueError(f"scales must have shape (groups, d_out) with d_in = {d_in} a multiple of groups")
+    groups, d_out = scales.shape
+    cp = _dev(codes, "codes", torch.uint8)
+    if tuple(codes.shape) != (-(-d_out // 16), -(-d_in // 128), 1024):
+        raise ValueError(f"codes must have shape ({-(-d_out // 16)}, {-(-d_in // 128)}, 1024), got {tuple(codes.shape)}")
+    zp = None
+    if zeros is not None:
+        zp = _dev(zeros, "zeros", scales.dtype)
+        if zeros.shape != scales.shape:
+            raise ValueError(f"zeros must have the scales' shape {tuple(scales.shape)}, got {tuple(zeros.shape)}")
+    if groups == 0 or d_in // groups not in (32, 64, 128):
+        raise ValueError(f"groups must hold 32, 64 or 128 values, got {d_in} / {groups}")
+    return cp, sp, zp, d_out, d_in, d_in // groups
+
+
+def _codes(d_out: int, d_in: int, out, stream):
+    shape = (-(-d_out // 16), -(-d_in // 128), 1024)
+    if out is None:
+        return _new(shape, torch.uint8, stream)
+    if tuple(out.shape) != shape:
+        raise ValueError(f"codes must have shape {shape}, got {tuple(out.shape)}")
+    return out
+
+
+def zo_q4_quantize(ctx: Context, weight: torch.Tensor, group: int = 128, out: Q4Weight | None = None,
+                   stream=None) -> Q4Weight:
+    """weight [d_out, d_in] in 4 bits with one scale, max |w| / 7, per `group` values of a row."""
+    wp, d_out, d_in, ws = _matrix(weight, "weight")
+    if group not in (32, 64, 128) or d_in % group or d_in == 0:
+        raise ValueError(f"groups of 32, 64 or 128 values must fill the rows, got {group} for {d_in}")
+    shape = (d_in // group, d_out)
+    if out is None:
+        out = Q4Weight(_codes(d_out, d_in, None, stream), _new(shape, weight.dtype, stream), None, d_in)
+    elif out.zeros is not None or tuple(out.scales.shape) != shape or out.d_in != d_in:
+        raise ValueError(f"out must have scales of shape {shape} and no zeros")
+    codes = _codes(d_out, d_in, out.codes, stream)
+    _lib.check(_lib.lib().zo_q4_quantize(
+        ctx.handle, wp, ws, _dtype_code(weight), d_out, d_in, group, _dev(codes, "codes", torch.uint8),
+        _dev(out.scales, "scales", weight.dtype), _stream(stream, weight.get_device())), "zo_q4_quantize")
+    return out
+
+
+def zo_q4_pack(ctx: Context, values: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Codes in the library's blocks of values uint8 [d_out, d_in], 0 .. 15 each (the low four bits)."""
+    vp = _dev(values, "values", torch.uint8)
+    if values.dim() != 2:
+        raise ValueError(f"values must be a matrix, got shape {tuple(values.shape)}")
+    d_out, d_in = values.shape
+    out = _codes(d_out, d_in, out, stream)
+    _lib.check(_lib.lib().zo_q4_pack(ctx.handle, vp, d_out, d_in, _dev(out, "codes", torch.uint8),
+                                     _stream(stream, values.get_device())), "zo_q4_pack")
+    return out
+
+
+def zo_q4_unpack(ctx: Context, weight: Q4Weight, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The matrix [d_out, d_in] that the codes stand for, of the scales' dtype."""
+    cp, sp, zp, d_out, d_in, group = _q4(weight)
+    dtype = weight.scales.dtype
+    if out is None:
+        out = _new((d_out, d_in), dtype, stream)
+    elif tuple(out.shape) != (d_out, d_in):
+        raise ValueError(f"out must have shape ({d_out}, {d_in}), got {tuple(out.shape)}")
+    _lib.check(_lib.lib().zo_q4_unpack(ctx.handle, cp, sp, zp, _dtype_code(weight.scales), d_out, d_in, group,
+                                       _dev(out, "out", dtype), _stream(stream, weight.scales.get_device())),
+               "zo_q4_unpack")
+    return out
+
+
+def zo_q4_workspace_bytes(rows: int, d_in: int, d_out: int, dtype: torch.dtype, n_adapters: int = 0,
+                          rank: int = 0, regenerated: int = 0) -> int:
+    return int(_lib.lib().zo_q4_workspace_bytes(rows, d_in, d_out, _code_of(dtype), n_adapters, rank, regenerated))
+
+
+def zo_q4_project(ctx: Context, x: torch.Tensor, weight: Q4Weight, adapters: torch.Tensor | None = None,
+                  rank: int = 0, starts: torch.Tensor | None = None, ids: torch.Tensor | None = None,
+                  scale: float = 1.0, bias: torch.Tensor | None = None,
+                  probes: torch.Tensor | None = None, alphas: torch.Tensor | None = None,
+                  offset: int = 0, step: int = 0, probe0: int = 0,
+                  n_probes: int | None = None, bits: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+    """zo_adapter_project with the weights in 4 bits, read as they are held; x shares the dtype of the
+    scales.  Without adapters, starts and ids all rows are x W^T + bias.  workspace: at least
+    zo_q4_workspace_bytes of the largest batch that it serves."""
+    xp, rows, d_in, xs = _matrix(x, "x")
+    dev = x.get_device()
+    code = _dtype_code(x)
+    cp, scp, zp, d_out, k, group = _q4(weight, x.dtype)
+    if k != d_in:
+        raise ValueError(f"weight must have {d_in} columns, got {k}")
+    rank = int(rank)
+    ap, n_adapters = None, 0
+    if adapters is not None:
+        ap, n_adapters = _adapters(adapters, rank, d_in, d_out, x.dtype)
+    if starts is None:
+        if adapters is not None or ids is not None or probes is not None or alphas is not None:
+            raise ValueError("adapters, ids, probes and alphas go with starts")
+        n, sp, ip, pp, fp, n_probes, kp, rank = 0, None, None, None, None, 0, None, 0
+    else:
+        n, sp, ip, pp, fp, n_probes, kp = _groups(starts, ids, probes, alphas, n_probes, bits,
+                                                  0 if adapters is None else adapters.numel(), dev)
+        if ip is None:
+            raise ValueError("ids go with starts")
+    bp = _vector(bias, "bias", d_out, x.dtype, dev)
+    yp, ys, out = _projected(out, rows, d_out, x.dtype, stream)
+    if workspace is None:
+        wb = int(_lib.lib().zo_q4_workspace_bytes(rows, d_in, d_out, code, n_adapters, rank,
+                                                  n_probes if kp is None else 0))
+        workspace = _new(wb, torch.uint8, stream)
+        ws = workspace.data_ptr()
+    else:
+        ws, wb = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+    _lib.check(_lib.lib().zo_q4_project(
+        ctx.handle, xp, xs, cp, scp, zp, group, bp, code, rows, d_in, d_out, ap, n_adapters, rank, float(scale),
+        sp, ip, n, pp, fp, offset, step, probe0, n_probes, kp, ws, wb, yp, ys, _stream(stream, dev)),
+        "zo_q4_project")
     return out

@@ -20,6 +20,7 @@ ZO_MAX_NPERT = 512
 ZO_IGNORE_TOKEN = -100
 ZO_MAX_TOP_K = 32
 ZO_MAX_RANK = 128
+ZO_MAX_TEACHER = 128
 ZO_NOALLOC_SCRATCH_BYTES = 1 << 20
 
 _vp = ctypes.c_void_p
@@ -68,6 +69,16 @@ SIGNATURES = {
     "zo_adapter_project": (_int, [_vp, _vp, _u64, _vp, _vp, _int, _u64, _u32, _u32, _vp, _u32,
                                   _u32, _f32, _vp, _vp, _u32, _vp, _vp, _u64, _u32, _u32, _u32,
                                   _vp, _vp, _u64, _vp, _u64, _vp]),
+    "zo_distill_loss": (_int, [_vp, _vp, _int, _u64, _u32, _u64, _vp, _vp, _u32, _vp, _f32, _vp, _vp,
+                               _vp, _u64, _vp]),
+    "zo_q4_code_bytes": (_u64, [_u32, _u32]),
+    "zo_q4_quantize": (_int, [_vp, _vp, _u64, _int, _u32, _u32, _u32, _vp, _vp, _vp]),
+    "zo_q4_pack": (_int, [_vp, _vp, _u32, _u32, _vp, _vp]),
+    "zo_q4_unpack": (_int, [_vp, _vp, _vp, _vp, _int, _u32, _u32, _u32, _vp, _vp]),
+    "zo_q4_workspace_bytes": (_u64, [_u64, _u32, _u32, _int, _u32, _u32, _u32]),
+    "zo_q4_project": (_int, [_vp, _vp, _u64, _vp, _vp, _vp, _u32, _vp, _int, _u64, _u32, _u32, _vp,
+                             _u32, _u32, _f32, _vp, _vp, _u32, _vp, _vp, _u64, _u32, _u32, _u32,
+                             _vp, _vp, _u64, _vp, _u64, _vp]),
     "zo_stream_rmw": (_int, [_vp, _vp, _u64, _u32, _vp]),
     "zo_tune_placement": (_int, [_vp, _vp, _u64, _vp, _vp, _vp, _vp]),
     "zo_set_slice_bytes": (_int, [_vp, _u64]),

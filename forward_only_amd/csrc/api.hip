@@ -8,7 +8,7 @@
 #include "zo_launch.hpp"
 
 static_assert(ZO_MAX_NPERT == zo::kMaxNpert, "one probe-count limit");
-static_assert(ZO_MAX_TOP_K == zo::kMaxTopK && ZO_MAX_RANK == zo::kMaxRank &&
+static_assert(ZO_MAX_TEACHER == zo::kMaxTeacher && ZO_MAX_TOP_K == zo::kMaxTopK && ZO_MAX_RANK == zo::kMaxRank &&
                   ZO_IGNORE_TOKEN == zo::kIgnoreToken, "one set of limits");
 static_assert(2 * zo::kQuadProbes + 1 <= zo::kLowRankMax + 1,
               "the loss partials hold both signs of every probe of a fused pass and the clean loss");
@@ -104,6 +104,79 @@ inline bool range_ok(uint64_t offset, uint64_t n)
     return true;
 }
 
+// What zo_adapter_project and zo_q4_project are called with; plain: no groups at all.
+struct AdapterCall {
+    const void *x;
+    uint64_t x_stride;
+    const void *weight, *bias;
+    zo_dtype dtype;
+    uint64_t rows;
+    uint32_t d_in, d_out;
+    const void *adapters;
+    uint32_t n_adapters, rank;
+    const int64_t *starts;
+    const int32_t *ids;
+    uint32_t n_groups;
+    bool plain;
+    const int32_t *probes;
+    const float *alphas;
+    uint64_t offset;
+    uint32_t probe0, n_probes;
+    const uint8_t *bits;
+    const void *y;
+    uint64_t y_stride;
+};
+
+// Their common checks; `nothing` if there is nothing to compute.
+zo_status adapter_call_ok(const AdapterCall &a, bool &nothing)
+{
+    if (a.dtype != ZO_FP32 && a.dtype != ZO_BF16) return ZO_EINVAL;
+    if (a.rank > ZO_MAX_RANK || a.rows > kMaxProjectRows || a.n_groups > kMaxGroups || a.d_in > kMaxWidth ||
+        a.d_out > kMaxFeatures || a.rows * a.d_out > kMaxProjected)
+        return ZO_EUNSUPPORTED;
+    if (a.d_in == 0 || a.d_in % 8u || a.d_out % 8u || a.rank % 8u || a.x_stride % 8u || a.y_stride % 8u)
+        return ZO_EINVAL;
+    if ((a.probes == nullptr) != (a.alphas == nullptr)) return ZO_EINVAL;
+    if (a.n_adapters > UINT64_MAX / 2 / ((uint64_t)ZO_MAX_RANK * ((uint64_t)a.d_in + a.d_out)))
+        return ZO_EINVAL;
+    const uint64_t params = (uint64_t)a.n_adapters * a.rank * ((uint64_t)a.d_in + a.d_out);
+    if (!range_ok(a.offset, params)) return ZO_EINVAL;
+    if (a.probes && a.n_probes > 0 && a.n_probes - 1 > UINT32_MAX - a.probe0) return ZO_EINVAL;
+    nothing = a.rows == 0 || a.d_out == 0 || (a.n_groups == 0 && !a.plain);
+    if (nothing) return ZO_OK;
+    if (!a.x || !a.weight || !a.y || (!a.plain && (!a.starts || !a.ids)) || (params > 0 && !a.adapters))
+        return ZO_EINVAL;
+    if (!aligned16(a.x) || !aligned16(a.weight) || !aligned16(a.bias) || !aligned16(a.y) ||
+        !aligned16(a.adapters) || !aligned16(a.bits))
+        return ZO_EINVAL;
+    if (!aligned<8>(a.starts) || !aligned<4>(a.ids) || !aligned<4>(a.probes) || !aligned<4>(a.alphas))
+        return ZO_EINVAL;
+    if (a.x_stride > (UINT64_MAX >> 4) / a.rows || a.y_stride > (UINT64_MAX >> 4) / a.rows ||
+        (a.rows > 1 && a.y_stride < a.d_out))
+        return ZO_EINVAL;
+    if (!reach_ok(a.rows, a.x_stride, a.d_in, a.dtype == ZO_BF16)) return ZO_EUNSUPPORTED;
+    return ZO_OK;
+}
+
+// Shapes of weights in 4 bits.
+zo_status q4_shape(zo_dtype dtype, uint32_t d_out, uint32_t d_in, uint32_t group)
+{
+    if (dtype != ZO_FP32 && dtype != ZO_BF16) return ZO_EINVAL;
+    if (group != 32 && group != 64 && group != 128) return ZO_EINVAL;
+    if (d_in % group || d_out % 8u) return ZO_EINVAL;
+    if (d_in > kMaxWidth || d_out > kMaxFeatures || zo::q4_blocks(d_out, d_in) > ((uint64_t)1 << 25))
+        return ZO_EUNSUPPORTED;
+    return ZO_OK;
+}
+// Four neighbouring scales or zeros are one load.
+inline bool q4_aligned(zo_dtype dtype, const void *p) { return dtype == ZO_BF16 ? aligned<8>(p) : aligned16(p); }
+// Workspace of the unpacked weights.
+inline uint64_t q4_unpacked_bytes(uint64_t rows, uint32_t d_in, uint32_t d_out, zo_dtype dtype)
+{
+    const bool bf16 = dtype == ZO_BF16;
+    return zo::q4_few(rows, bf16) ? 0 : ((uint64_t)d_in * d_out * (bf16 ? 2 : 4) + 255) / 256 * 256;
+}
+
 }  // namespace
 
 extern "C" {
@@ -150,7 +223,7 @@ zo_status zo_init(uint64_t seed, zo_ctx **out)
     }
     c->d_scratch = scratch_on(c->device);
     if (!c->d_scratch || zo::prepare_update() != hipSuccess ||
-        zo::prepare_products() != hipSuccess ||
+        zo::prepare_products() != hipSuccess || zo::prepare_q4() != hipSuccess ||
         zo::launch_zero_u32(c->d_counter, 64, nullptr) != hipSuccess ||
         hipDeviceSynchronize() != hipSuccess) {
         (void)hipFree(c->d_partials);
@@ -640,30 +713,13 @@ zo_status zo_adapter_project(zo_ctx *c, const void *d_x, uint64_t x_stride, cons
                              uint64_t y_stride, void *stream)
 {
     if (!ctx_ok(c)) return ZO_EINVAL;
-    if (dtype != ZO_FP32 && dtype != ZO_BF16) return ZO_EINVAL;
-    if (rank > ZO_MAX_RANK || rows > kMaxProjectRows || n_groups > kMaxGroups || d_in > kMaxWidth ||
-        d_out > kMaxFeatures || rows * d_out > kMaxProjected)
-        return ZO_EUNSUPPORTED;
-    if (d_in == 0 || d_in % 8u || d_out % 8u || rank % 8u || x_stride % 8u || y_stride % 8u)
-        return ZO_EINVAL;
-    if ((d_probes == nullptr) != (d_alphas == nullptr)) return ZO_EINVAL;
-    if (n_adapters > UINT64_MAX / 2 / ((uint64_t)ZO_MAX_RANK * ((uint64_t)d_in + d_out)))
-        return ZO_EINVAL;
+    const AdapterCall call = {d_x, x_stride, d_weight, d_bias, dtype, rows, d_in, d_out, d_adapters, n_adapters, rank,
+                              d_starts, d_ids, n_groups, false, d_probes, d_alphas, offset, probe0, n_probes, d_bits,
+                              d_y, y_stride};
+    bool nothing = false;
+    const zo_status st = adapter_call_ok(call, nothing);
+    if (st != ZO_OK || nothing) return st;
     const uint64_t params = (uint64_t)n_adapters * rank * ((uint64_t)d_in + d_out);
-    if (!range_ok(offset, params)) return ZO_EINVAL;
-    if (d_probes && n_probes > 0 && n_probes - 1 > UINT32_MAX - probe0) return ZO_EINVAL;
-    if (rows == 0 || d_out == 0 || n_groups == 0) return ZO_OK;
-    if (!d_x || !d_weight || !d_y || !d_starts || !d_ids || (params > 0 && !d_adapters))
-        return ZO_EINVAL;
-    if (!aligned16(d_x) || !aligned16(d_weight) || !aligned16(d_bias) || !aligned16(d_y) ||
-        !aligned16(d_adapters) || !aligned16(d_bits))
-        return ZO_EINVAL;
-    if (!aligned<8>(d_starts) || !aligned<4>(d_ids) || !aligned<4>(d_probes) || !aligned<4>(d_alphas))
-        return ZO_EINVAL;
-    if (x_stride > (UINT64_MAX >> 4) / rows || y_stride > (UINT64_MAX >> 4) / rows ||
-        (rows > 1 && y_stride < d_out))
-        return ZO_EINVAL;
-    if (!reach_ok(rows, x_stride, d_in, dtype == ZO_BF16)) return ZO_EUNSUPPORTED;
     const uint32_t regenerated = d_probes && !d_bits && params > 0 ? n_probes : 0;
     if (regenerated > 0 && zo_bits_stride(params) > UINT64_MAX / 2 / regenerated) return ZO_EINVAL;
     const uint64_t need = zo_adapter_workspace_bytes(rows, d_in, d_out, n_adapters, rank, n_groups,
@@ -686,6 +742,137 @@ zo_status zo_adapter_project(zo_ctx *c, const void *d_x, uint64_t x_stride, cons
     return from_hip(zo::launch_adapter_project(a, dtype == ZO_BF16, d_x, x_stride, d_weight, d_bias,
                                                d_adapters, u, slices, d_y, y_stride,
                                                as_stream(stream)));
+}
+
+zo_status zo_distill_loss(zo_ctx *c, const void *d_logits, zo_dtype dtype, uint64_t rows,
+                          uint32_t vocab, uint64_t row_stride, const int64_t *d_teacher_ids,
+                          const float *d_teacher_logits, uint32_t k, const int64_t *d_targets,
+                          float temperature, float *d_loss, const float *d_row_grad, void *d_grad,
+                          uint64_t grad_stride, void *stream)
+{
+    if (!ctx_ok(c)) return ZO_EINVAL;
+    if (dtype != ZO_FP32 && dtype != ZO_BF16) return ZO_EINVAL;
+    if (!(temperature > 0.0f) || !(temperature <= 3.402823466e38f)) return ZO_EINVAL;
+    if (rows > kMaxRows || vocab > kMaxRows || k > ZO_MAX_TEACHER) return ZO_EUNSUPPORTED;
+    if (rows == 0) return ZO_OK;
+    if (vocab == 0 || !d_logits || !d_loss || (k > 0 && (!d_teacher_ids || !d_teacher_logits)))
+        return ZO_EINVAL;
+    const bool two = dtype == ZO_BF16;
+    if (!(two ? aligned<2>(d_logits) && aligned<2>(d_grad) : aligned<4>(d_logits) && aligned<4>(d_grad)))
+        return ZO_EINVAL;
+    if (!aligned<8>(d_teacher_ids) || !aligned<4>(d_teacher_logits) || !aligned<8>(d_targets) ||
+        !aligned<4>(d_loss) || !aligned<4>(d_row_grad))
+        return ZO_EINVAL;
+    if (row_stride > (UINT64_MAX >> 4) / rows || grad_stride > (UINT64_MAX >> 4) / rows) return ZO_EINVAL;
+    if (d_grad) {
+        if (rows > 1 && grad_stride < vocab) return ZO_EINVAL;
+        if (d_grad != d_logits || (rows > 1 && grad_stride != row_stride)) {
+            const uintptr_t size = two ? 2 : 4;
+            const uintptr_t a = reinterpret_cast<uintptr_t>(d_logits), b = reinterpret_cast<uintptr_t>(d_grad);
+            const uintptr_t la = ((rows - 1) * row_stride + vocab) * size, lb = ((rows - 1) * grad_stride + vocab) * size;
+            if (a < b + lb && b < a + la) return ZO_EINVAL;
+        }
+    }
+    const zo::DistillArgs a = {d_logits, rows, vocab, row_stride, d_teacher_ids, d_teacher_logits, k, d_targets,
+                               temperature, d_loss, d_row_grad, d_grad, grad_stride};
+    return from_hip(zo::launch_distill(a, two, as_stream(stream)));
+}
+
+uint64_t zo_q4_code_bytes(uint32_t d_out, uint32_t d_in) { return zo::q4_blocks(d_out, d_in) * 1024; }
+
+zo_status zo_q4_quantize(zo_ctx *c, const void *d_w, uint64_t w_stride, zo_dtype dtype, uint32_t d_out,
+                         uint32_t d_in, uint32_t group, void *d_codes, void *d_scales, void *stream)
+{
+    if (!ctx_ok(c)) return ZO_EINVAL;
+    const zo_status st = q4_shape(dtype, d_out, d_in, group);
+    if (st != ZO_OK) return st;
+    if (d_out == 0 || d_in == 0) return ZO_OK;
+    if (!d_w || !d_codes || !d_scales || !aligned16(d_w) || !aligned16(d_codes) || !q4_aligned(dtype, d_scales))
+        return ZO_EINVAL;
+    if (w_stride % 8u || w_stride > (UINT64_MAX >> 4) / d_out || (d_out > 1 && w_stride < d_in)) return ZO_EINVAL;
+    return from_hip(zo::launch_q4_quantize(d_w, w_stride, dtype == ZO_BF16, d_out, d_in, group, d_codes, d_scales,
+                                           as_stream(stream)));
+}
+
+zo_status zo_q4_pack(zo_ctx *c, const uint8_t *d_values, uint32_t d_out, uint32_t d_in, void *d_codes,
+                     void *stream)
+{
+    if (!ctx_ok(c)) return ZO_EINVAL;
+    const zo_status st = q4_shape(ZO_FP32, d_out, d_in, 32);
+    if (st != ZO_OK) return st;
+    if (d_out == 0 || d_in == 0) return ZO_OK;
+    if (!d_values || !d_codes || !aligned<8>(d_values) || !aligned16(d_codes)) return ZO_EINVAL;
+    return from_hip(zo::launch_q4_pack(d_values, d_out, d_in, d_codes, as_stream(stream)));
+}
+
+zo_status zo_q4_unpack(zo_ctx *c, const void *d_codes, const void *d_scales, const void *d_zeros, zo_dtype dtype,
+                       uint32_t d_out, uint32_t d_in, uint32_t group, void *d_w, void *stream)
+{
+    if (!ctx_ok(c)) return ZO_EINVAL;
+    const zo_status st = q4_shape(dtype, d_out, d_in, group);
+    if (st != ZO_OK) return st;
+    if (d_out == 0 || d_in == 0) return ZO_OK;
+    if (!d_codes || !d_scales || !d_w || !aligned16(d_codes) || !aligned16(d_w) || !q4_aligned(dtype, d_scales) ||
+        !q4_aligned(dtype, d_zeros))
+        return ZO_EINVAL;
+    return from_hip(zo::launch_q4_unpack({d_codes, d_scales, d_zeros, group}, dtype == ZO_BF16, d_out, d_in, d_w,
+                                         as_stream(stream)));
+}
+
+uint64_t zo_q4_workspace_bytes(uint64_t rows, uint32_t d_in, uint32_t d_out, zo_dtype dtype, uint32_t n_adapters,
+                               uint32_t rank, uint32_t regenerated)
+{
+    return zo_adapter_workspace_bytes(rows, d_in, d_out, n_adapters, rank, 0, regenerated) +
+           q4_unpacked_bytes(rows, d_in, d_out, dtype);
+}
+
+zo_status zo_q4_project(zo_ctx *c, const void *d_x, uint64_t x_stride, const void *d_codes, const void *d_scales,
+                        const void *d_zeros, uint32_t group, const void *d_bias, zo_dtype dtype, uint64_t rows,
+                        uint32_t d_in, uint32_t d_out, const void *d_adapters, uint32_t n_adapters, uint32_t rank,
+                        float scale, const int64_t *d_starts, const int32_t *d_ids, uint32_t n_groups,
+                        const int32_t *d_probes, const float *d_alphas, uint64_t offset, uint32_t step,
+                        uint32_t probe0, uint32_t n_probes, const uint8_t *d_bits, void *d_workspace,
+                        uint64_t workspace_bytes, void *d_y, uint64_t y_stride, void *stream)
+{
+    if (!ctx_ok(c)) return ZO_EINVAL;
+    zo_status st = q4_shape(dtype, d_out, d_in, group);
+    if (st != ZO_OK) return st;
+    // without groups there are no adapters, probes or signs
+    const bool plain = !d_starts && !d_ids && n_groups == 0;
+    if (plain && (n_adapters > 0 || d_probes || d_alphas)) return ZO_EINVAL;
+    AdapterCall call = {d_x, x_stride, d_codes, d_bias, dtype, rows, d_in, d_out, d_adapters, n_adapters, rank, d_starts,
+                        d_ids, n_groups, plain, d_probes, d_alphas, offset, probe0, n_probes, d_bits, d_y, y_stride};
+    bool nothing = false;
+    st = adapter_call_ok(call, nothing);
+    if (st != ZO_OK || nothing) return st;
+    if (!d_scales || !q4_aligned(dtype, d_scales) || !q4_aligned(dtype, d_zeros)) return ZO_EINVAL;
+    const uint64_t params = (uint64_t)n_adapters * rank * ((uint64_t)d_in + d_out);
+    const uint32_t regenerated = d_probes && !d_bits && params > 0 ? n_probes : 0;
+    if (regenerated > 0 && zo_bits_stride(params) > UINT64_MAX / 2 / regenerated) return ZO_EINVAL;
+    const uint64_t need = zo_q4_workspace_bytes(rows, d_in, d_out, dtype, n_adapters, rank, regenerated);
+    if (need > 0 && (!d_workspace || !aligned<256>(d_workspace) || workspace_bytes < need)) return ZO_EINVAL;
+    // x A^T and the rows' groups, unpacked weights, slices, signs
+    char *at = static_cast<char *>(d_workspace);
+    float *u = reinterpret_cast<float *>(at);
+    at += zo::adapter_u_bytes(rows, rank);
+    void *unpacked = at;
+    at += q4_unpacked_bytes(rows, d_in, d_out, dtype);
+    float *slices = nullptr;
+    if (!zo::q4_few(rows, dtype == ZO_BF16) &&
+        zo::product_shape(rows, d_out, d_in, dtype == ZO_BF16) == zo::Shape::big)
+        slices = reinterpret_cast<float *>(at);
+    zo::AdapterArgs a = {rows, d_in, d_out, rank, n_adapters, n_groups, n_probes, scale, d_starts,
+                         d_ids, d_probes, d_alphas, d_bits, zo_bits_stride(params)};
+    if (regenerated > 0) {
+        uint8_t *bits = static_cast<uint8_t *>(d_workspace) +
+                        (need - (uint64_t)regenerated * zo_bits_stride(params));
+        const hipError_t e = zo::launch_gen_probes(key_of(c), step, probe0, n_probes, offset, params,
+                                                   bits, c->num_cus, as_stream(stream));
+        if (e != hipSuccess) return from_hip(e);
+        a.bits = bits;
+    }
+    return from_hip(zo::launch_q4_project(a, dtype == ZO_BF16, d_x, x_stride, {d_codes, d_scales, d_zeros, group},
+                                          d_bias, d_adapters, u, slices, unpacked, d_y, y_stride, as_stream(stream)));
 }
 
 }  // extern "C"

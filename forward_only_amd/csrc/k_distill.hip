@@ -1,0 +1,309 @@
+// k_distill.hip -- the divergence of a teacher's top logits from a model's distribution, per row of
+// the model's logits, with its gradient (zo_distill_loss).
+//
+// With p = softmax_j(t_j / T) over the row's entries and q = softmax_v(x_v / T),
+//   loss = T^2 sum_j p_j (log p_j - log q_{id_j}),   d loss / d x_v = T (q_v - sum_{id_j = v} p_j).
+// With m = max_v x_v and s = sum_v e^{(x_v - m) / T}, log q_v = (x_v - m) / T - log s; all in
+// fp32, the gradient rounded once.
+#include <math.h>
+
+#include <type_traits>
+
+#include "zo_lm.hpp"
+
+namespace zo {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// Sixteen bytes at any element's address.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
+template <class T>
+__device__ __forceinline__ float widen(T v);
+template <>
+__device__ __forceinline__ float widen<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float widen<uint16_t>(uint16_t v) { return bf16lo_to_f32(v); }
+
+template <class T>
+__device__ __forceinline__ T narrow(float v);
+template <>
+__device__ __forceinline__ float narrow<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ uint16_t narrow<uint16_t>(float v) { return (uint16_t)pack_bf16x2(v, 0.0f); }
+
+// Sixteen bytes of a row: kPiece values.
+template <class T>
+struct Piece {
+    static constexpr int kPiece = 16 / sizeof(T);
+    static __device__ __forceinline__ float value(const u32x4 &v, int i)
+    {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(v[i]);
+        else return i & 1 ? bf16hi_to_f32(v[i >> 1]) : bf16lo_to_f32(v[i >> 1]);
+    }
+    static __device__ __forceinline__ u32x4 of(const float *f)
+    {
+        if constexpr (sizeof(T) == 4)
+            return u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+        else
+            return u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                         pack_bf16x2(f[6], f[7])};
+    }
+    static __device__ __forceinline__ u32x4 nothing()   // -inf in every value
+    {
+        const uint32_t w = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;
+        return u32x4{w, w, w, w};
+    }
+};
+
+// The running maximum m and s = sum e^{(x - m) / T}, with c = log2(e) / T; values of -inf add nothing
+// while m is -inf, a NaN or +inf makes s NaN.
+struct Sums {
+    float m, s;
+    __device__ __forceinline__ void raise(float top, float c)
+    {
+        if (top > m) {
+            s *= __builtin_amdgcn_exp2f((m - top) * c);
+            m = top;
+        }
+    }
+    __device__ __forceinline__ void add(float x, float c)
+    {
+        s += __builtin_amdgcn_exp2f((x - (m == -INFINITY ? 0.0f : m)) * c);
+    }
+    __device__ __forceinline__ void merge(const Sums &o, float c)
+    {
+        raise(o.m, c);
+        s += o.s * (o.m == m ? 1.0f : __builtin_amdgcn_exp2f((o.m - m) * c));
+    }
+};
+
+struct Teacher {
+    const int64_t *ids;       // [rows][k]; -1: no entry
+    const float *logits;
+    uint32_t k;
+};
+
+// One workgroup per row.  kHold > 0: the row stays in registers, kHold pieces a thread, between the
+// sums and the gradient; 0: it is read again for the gradient.
+template <class T, int kThreads, int kHold, bool kGrad>
+__global__ __launch_bounds__(kThreads) void k_distill(const T *logits, uint32_t vocab, uint64_t stride,
+                                                      Teacher teacher, const int64_t *targets, float tau,
+                                                      float *loss, const float *row_grad, T *grad,
+                                                      uint64_t grad_stride)
+{
+    typedef Piece<T> P;
+    constexpr int kPiece = P::kPiece, kWaves = kThreads / kWave, kEntries = kMaxTeacher / kWave;
+    constexpr int kUnroll = 4;
+    __shared__ int64_t ids[kMaxTeacher];
+    __shared__ float share[kMaxTeacher], parts[kWaves][2], bounds[2];
+    __shared__ int state[2];          // entries, bad ids
+    const uint64_t at = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+    const T *row = logits + at * stride;
+    T *out = kGrad ? grad + at * grad_stride : nullptr;
+    const uint32_t head_of = (uint32_t)(-(intptr_t)row & 15) / sizeof(T);
+    const uint32_t head = head_of < vocab ? head_of : vocab;
+    const uint32_t pieces = (vocab - head) / kPiece, rest = head + pieces * kPiece;
+    const auto piece_at = [&](uint32_t i) { return *reinterpret_cast<const u32x4 *>(row + head + (uint64_t)i * kPiece); };
+    const float inv = 1.0f / tau, c = kLog2e * inv;
+
+    const auto nothing = [&] {        // a row that counts for nothing
+        if (tid == 0) loss[at] = 0.0f;
+        if constexpr (kGrad) {
+            for (uint32_t i = tid; i < vocab / kPiece; i += kThreads)
+                *reinterpret_cast<u32x4_any *>(out + (uint64_t)i * kPiece) = u32x4{0, 0, 0, 0};
+            const uint32_t i = vocab / kPiece * kPiece + tid;
+            if (i < vocab) out[i] = narrow<T>(0.0f);
+        }
+    };
+    if (targets && targets[at] == kIgnoreToken) return nothing();
+    Sums st = {-INFINITY, 0.0f};
+    u32x4 held[kHold ? kHold : 1];
+    float first = 0.0f, last = 0.0f;  // the values before and behind the pieces
+    const bool has_first = (uint32_t)tid < head, has_last = rest + tid < vocab;
+    if constexpr (kHold > 0) {
+#pragma unroll
+        for (int u = 0; u < kHold; ++u) {
+            const uint32_t i = u * kThreads + tid;
+            held[u] = i < pieces ? piece_at(i) : P::nothing();
+        }
+    }
+    if (has_first) first = widen(row[tid]);
+    if (has_last) last = widen(row[rest + tid]);
+    // the teacher's distribution, by the first wave
+    float x_of[kEntries] = {}, p_of[kEntries] = {}, t_of[kEntries] = {};
+    int64_t id_of[kEntries];
+    if (wave == 0) {
+        int n = 0, bad = 0;
+        float top = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < kEntries; ++e) {
+            const uint32_t j = e * kWave + lane;
+            const bool in = j < teacher.k;
+            id_of[e] = in ? teacher.ids[at * teacher.k + j] : -1;
+            t_of[e] = id_of[e] != -1 ? teacher.logits[at * teacher.k + j] : -INFINITY;
+            const bool ok = id_of[e] >= 0 && id_of[e] < (int64_t)vocab;
+            x_of[e] = ok ? widen(row[id_of[e]]) : 0.0f;
+            n += __popcll(__ballot(id_of[e] != -1));
+            bad += __popcll(__ballot(id_of[e] != -1 && !ok));
+            top = fmaxf(top, t_of[e]);
+        }
+        for (int o = kWave / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+        float sum = 0.0f;
+#pragma unroll
+        for (int e = 0; e < kEntries; ++e) {
+            t_of[e] = id_of[e] != -1 ? (t_of[e] - top) * inv : -INFINITY;
+            p_of[e] = __builtin_amdgcn_exp2f(t_of[e] * kLog2e);
+            sum += p_of[e];
+        }
+        for (int o = kWave / 2; o; o >>= 1) sum += __shfl_xor(sum, o);
+        const float logs = logf(sum);
+#pragma unroll
+        for (int e = 0; e < kEntries; ++e) {
+            p_of[e] /= sum;
+            t_of[e] -= logs;
+            ids[e * kWave + lane] = id_of[e];
+            share[e * kWave + lane] = p_of[e];
+        }
+        if (lane == 0) {
+            state[0] = n;
+            state[1] = bad || !(sum > 0.0f);        // NaN: the teacher has no distribution
+        }
+    }
+    if constexpr (kHold > 0) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kHold; ++u)
+#pragma unroll
+            for (int j = 0; j < kPiece; ++j) top = fmaxf(top, P::value(held[u], j));
+        st.m = top;
+#pragma unroll
+        for (int u = 0; u < kHold; ++u)
+#pragma unroll
+            for (int j = 0; j < kPiece; ++j) st.add(P::value(held[u], j), c);
+    } else {
+        for (uint32_t i = tid; i < pieces; i += kUnroll * kThreads) {
+            u32x4 v[kUnroll];
+            float top = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) v[u] = i + u * kThreads < pieces ? piece_at(i + u * kThreads) : P::nothing();
+#pragma unroll
+            for (int j = 0; j < kUnroll * kPiece; ++j) top = fmaxf(top, P::value(v[j / kPiece], j % kPiece));
+            st.raise(top, c);
+#pragma unroll
+            for (int j = 0; j < kUnroll * kPiece; ++j) st.add(P::value(v[j / kPiece], j % kPiece), c);
+        }
+    }
+    if (has_first) {
+        st.raise(first, c);
+        st.add(first, c);
+    }
+    if (has_last) {
+        st.raise(last, c);
+        st.add(last, c);
+    }
+    for (int o = kWave / 2; o; o >>= 1) {
+        const Sums b = {__shfl_xor(st.m, o), __shfl_xor(st.s, o)};
+        st.merge(b, c);
+    }
+    if (lane == 0) {
+        parts[wave][0] = st.m;
+        parts[wave][1] = st.s;
+    }
+    __syncthreads();
+    if (state[0] == 0) return nothing();
+    if (wave == 0) {
+        Sums all = {parts[0][0], parts[0][1]};
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) all.merge({parts[w][0], parts[w][1]}, c);
+        if (state[1]) all.s = __builtin_nanf("");
+        const float logs = logf(all.s);
+        float sum = 0.0f;
+#pragma unroll
+        for (int e = 0; e < kEntries; ++e) {
+            const float d = t_of[e] - ((x_of[e] - all.m) * inv - logs);
+            sum += p_of[e] == 0.0f ? 0.0f : p_of[e] * d;     // a NaN of either stays
+        }
+        for (int o = kWave / 2; o; o >>= 1) sum += __shfl_xor(sum, o);
+        if (lane == 0) {
+            loss[at] = tau * tau * sum;
+            bounds[0] = all.m;
+            bounds[1] = all.s;
+        }
+    }
+    if constexpr (kGrad) {
+        __syncthreads();
+        const float m = bounds[0], log2s = log2f(bounds[1]);
+        const float g = tau * (row_grad ? row_grad[at] : 1.0f);
+        const auto q_of = [&](float x) { return __builtin_amdgcn_exp2f(fmaf(x - m, c, -log2s)); };
+        const auto store = [&](uint32_t i, const u32x4 &v) {
+            float f[kPiece];
+#pragma unroll
+            for (int j = 0; j < kPiece; ++j) f[j] = g * q_of(P::value(v, j));
+            *reinterpret_cast<u32x4_any *>(out + head + (uint64_t)i * kPiece) = P::of(f);
+        };
+        if constexpr (kHold > 0) {
+#pragma unroll
+            for (int u = 0; u < kHold; ++u) {
+                const uint32_t i = u * kThreads + tid;
+                if (i < pieces) store(i, held[u]);
+            }
+        } else {
+            for (uint32_t i = tid; i < pieces; i += kThreads) store(i, piece_at(i));
+        }
+        if (has_first) out[tid] = narrow<T>(g * q_of(first));
+        if (has_last) out[rest + tid] = narrow<T>(g * q_of(last));
+        // the entries' own places again, with what the teacher wants there; an id that comes twice
+        // is written twice with the same value
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        if (wave == 0) {
+#pragma unroll
+            for (int e = 0; e < kEntries; ++e) {
+                const bool ok = id_of[e] >= 0 && id_of[e] < (int64_t)vocab;
+                if (!ok) continue;
+                float p = 0.0f;
+                for (uint32_t j = 0; j < teacher.k; ++j) p += ids[j] == id_of[e] ? share[j] : 0.0f;
+                out[id_of[e]] = narrow<T>(g * (q_of(x_of[e]) - p));
+            }
+        }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_distill(const DistillArgs &a, bool bf16, hipStream_t stream)
+{
+    const auto launch = [&](auto *p, auto threads, auto hold, auto with) {
+        using E = std::remove_cv_t<std::remove_pointer_t<decltype(p)>>;
+        constexpr int kThreads = decltype(threads)::value;
+        const auto from = [](auto *base, uint64_t i) { return base ? base + i : base; };
+        constexpr uint64_t kRows = kLaunchThreads / kThreads;
+        hipError_t e = hipSuccess;
+        for (uint64_t r = 0; r < a.rows && e == hipSuccess; r += kRows) {
+            const uint32_t n = (uint32_t)(a.rows - r < kRows ? a.rows - r : kRows);
+            const Teacher t = {from(a.ids, r * a.k), from(a.teacher, r * a.k), a.k};
+            k_distill<E, kThreads, decltype(hold)::value, decltype(with)::value><<<n, kThreads, 0, stream>>>(
+                p + r * a.stride, a.vocab, a.stride, t, from(a.targets, r), a.tau, a.loss + r,
+                from(a.row_grad, r), from(static_cast<E *>(a.grad), r * a.grad_stride), a.grad_stride);
+            e = hipGetLastError();
+        }
+        return e;
+    };
+    const auto typed = [&](auto *p) {
+        const uint64_t pieces = (uint64_t)a.vocab * sizeof(*p) / 16;
+        const std::integral_constant<int, 256> few;
+        const std::integral_constant<int, 1024> many;
+        const std::integral_constant<int, 0> none;
+        if (!a.grad) return launch(p, few, none, std::false_type());
+        const std::true_type with;
+        if (pieces <= 256 * 8) return launch(p, few, std::integral_constant<int, 8>(), with);
+        if (pieces <= 1024 * 8) return launch(p, many, std::integral_constant<int, 8>(), with);
+        if (pieces <= 1024 * 16) return launch(p, many, std::integral_constant<int, 16>(), with);
+        return launch(p, many, none, with);
+    };
+    return bf16 ? typed(static_cast<const uint16_t *>(a.logits)) : typed(static_cast<const float *>(a.logits));
+}
+
+}  // namespace zo

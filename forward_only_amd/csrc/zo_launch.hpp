@@ -149,6 +149,27 @@ hipError_t launch_token_logprobs(const void *logits, bool bf16, uint64_t rows, u
 hipError_t launch_group_loss(const float *logp, const int64_t *targets, const int64_t *starts,
                              uint32_t n_groups, uint64_t rows, double *loss, hipStream_t stream);
 
+// Most entries of a teacher's row.
+constexpr uint32_t kMaxTeacher = 128;
+
+// One zo_distill_loss call (device pointers); targets, row_grad and grad may be nullptr.
+struct DistillArgs {
+    const void *logits;
+    uint64_t rows;
+    uint32_t vocab;
+    uint64_t stride;
+    const int64_t *ids;            // [rows][k]
+    const float *teacher;
+    uint32_t k;
+    const int64_t *targets;
+    float tau;
+    float *loss;
+    const float *row_grad;
+    void *grad;
+    uint64_t grad_stride;
+};
+hipError_t launch_distill(const DistillArgs &a, bool bf16, hipStream_t stream);
+
 // Raise the dynamic-LDS limits of the product kernels on the current device (from zo_init).
 hipError_t prepare_products();
 
@@ -236,6 +257,31 @@ inline uint64_t adapter_u_bytes(uint64_t rows, uint32_t rank)
 hipError_t launch_adapter_project(const AdapterArgs &a, bool bf16, const void *x, uint64_t x_stride,
                                   const void *w, const void *bias, const void *adapters, float *u,
                                   float *slices, void *y, uint64_t y_stride, hipStream_t stream);
+
+// Its first half, x A_g^T (and each row's group) into u.
+hipError_t launch_adapter_shrink(const AdapterArgs &a, bool bf16, const void *x, uint64_t x_stride,
+                                 const void *adapters, float *u, hipStream_t stream);
+
+// Weights in 4 bits: codes in blocks, scales and zeros (or nullptr) [d_in / group][d_out].
+struct Q4Weights {
+    const void *codes, *scales, *zeros;
+    uint32_t group;
+};
+inline uint64_t q4_blocks(uint32_t d_out, uint32_t d_in)
+{
+    return ((uint64_t)d_out + 15) / 16 * (((uint64_t)d_in + 127) / 128);
+}
+// Whether so many rows are multiplied with the codes as they are; more with unpacked weights.
+inline bool q4_few(uint64_t rows, bool bf16) { return rows <= (bf16 ? 64 : 32); }
+hipError_t prepare_q4();
+hipError_t launch_q4_quantize(const void *w, uint64_t stride, bool bf16, uint32_t d_out, uint32_t d_in, uint32_t group,
+                              void *codes, void *scales, hipStream_t stream);
+hipError_t launch_q4_pack(const uint8_t *values, uint32_t d_out, uint32_t d_in, void *codes, hipStream_t stream);
+hipError_t launch_q4_unpack(const Q4Weights &q, bool bf16, uint32_t d_out, uint32_t d_in, void *w, hipStream_t stream);
+// As launch_adapter_project; unpacked: d_out * d_in elements unless q4_few.
+hipError_t launch_q4_project(const AdapterArgs &a, bool bf16, const void *x, uint64_t x_stride, const Q4Weights &w,
+                             const void *bias, const void *adapters, float *u, float *slices, void *unpacked, void *y,
+                             uint64_t y_stride, hipStream_t stream);
 
 struct HeadArgs {
     uint64_t rows, x_stride;

@@ -489,6 +489,89 @@ zo_status zo_adapter_project(zo_ctx *ctx, const void *d_x, uint64_t x_stride,
                              uint64_t workspace_bytes, void *d_y, uint64_t y_stride,
                              void *stream);
 
+/* Most entries of a teacher's row. */
+#define ZO_MAX_TEACHER 128u
+
+/* Divergence of a teacher's top logits from the model's distribution, per row, at the temperature
+ * T: with p = softmax_j(t_j / T) over the row's entries and Q = softmax_v(x_v / T) over all logits x,
+ *   d_loss[row] = T^2 sum_j p_j (log p_j - log Q_{id_j}),
+ * and, unless d_grad is NULL, the gradient of sum_row d_row_grad[row] d_loss[row],
+ *   d_grad[row][v] = d_row_grad[row] T (Q_v - sum_{j: id_j = v} p_j)
+ * (d_row_grad NULL: 1 for each row), of the logits' dtype, rounded once.  All sums are fp32; one pass over the
+ * logits where a row is at most 256 KiB or no gradient is wanted, deterministic.
+ * d_teacher_ids: device int64 [rows x k], -1 for no entry; d_teacher_logits: device float [rows x k],
+ * logits or log probabilities (zo_token_logprobs' alternatives are both of a teacher).  An id may come
+ * twice.  d_targets: NULL, or device int64 [rows], where only ZO_IGNORE_TOKEN has a meaning: such a
+ * row, and one without entries, has loss and gradient 0, whatever it holds.
+ * Logits of -inf have Q = 0: an entry there with p > 0 gives the loss +inf, with a finite gradient.
+ * A row of only -inf, one that holds NaN or +inf, one whose entries' logits are all -inf or hold NaN or
+ * +inf, and one with an id that is neither -1 nor in [0, vocab), has a loss and a gradient of NaN.
+ * d_logits: device, rows row_stride elements apart, d_grad: rows grad_stride elements apart, each row
+ * contiguous, at any element-aligned address.  d_grad may be d_logits with the same stride: the
+ * gradient then takes the logits' place.
+ * Errors: ZO_EINVAL for NULL pointers (with rows > 0; the teacher's with k > 0), unknown dtype, vocab == 0
+ * (with rows > 0), a temperature that is not positive and finite, grad_stride < vocab (with more than one
+ * row), d_grad within the logits in another way, misaligned pointers; ZO_EUNSUPPORTED if k >
+ * ZO_MAX_TEACHER or rows or vocab exceed 2^31 - 1.  rows == 0 launches nothing. */
+zo_status zo_distill_loss(zo_ctx *ctx, const void *d_logits, zo_dtype dtype, uint64_t rows,
+                          uint32_t vocab, uint64_t row_stride, const int64_t *d_teacher_ids,
+                          const float *d_teacher_logits, uint32_t k, const int64_t *d_targets,
+                          float temperature, float *d_loss, const float *d_row_grad, void *d_grad,
+                          uint64_t grad_stride, void *stream);
+
+/* ---- Weights in 4 bits -------------------------------------------------------------------
+ * W[f][k] = s (q - z) with codes q in 0 .. 15 and, for each feature f and each group of `group`
+ * neighbouring values of k (32, 64 or 128), a scale s and a zero point z: d_scales and d_zeros, device
+ * [d_in / group][d_out] of the activations' dtype, 8-byte (bf16) or 16-byte (fp32) aligned; without
+ * d_zeros z = 8.  d_in is a multiple of group, d_out of 8.
+ * d_codes: device, 16-byte aligned, zo_q4_code_bytes(d_out, d_in) bytes, in blocks of 16 features x 128
+ * values of k, 1024 bytes each, [ceil(d_out / 16)][ceil(d_in / 128)].  Within a block the code of feature f
+ * and value k lies in byte 16 (16 (k / 8 % 4) + f % 16) + 4 (k / 32 % 4) + b, b = 2 (k % 2) + k / 4 % 2, in the low
+ * half if k / 2 % 2 == 0, else in the high half.  What lies beyond the matrix is not used. */
+uint64_t zo_q4_code_bytes(uint32_t d_out, uint32_t d_in);
+
+/* Codes and scales of a matrix: s = max |w| / 7 over a group, rounded to the dtype, q = 8 + w / s rounded to
+ * the nearest whole number, ties to even, within 0 .. 15.  A group of zeros has s = 0, q = 8; one
+ * that holds an infinity or a NaN has s = NaN.  d_w: device, d_out rows of d_in elements, w_stride apart
+ * (a multiple of 8), 16-byte aligned.  Deterministic.
+ * Errors (all zo_q4_ calls): ZO_EINVAL for NULL pointers (unless d_out or d_in is 0), unknown dtype, shapes and
+ * strides outside these limits, misalignment; ZO_EUNSUPPORTED if d_in exceeds 2^26, d_out 2^24 or the
+ * codes 2^35 bytes. */
+zo_status zo_q4_quantize(zo_ctx *ctx, const void *d_w, uint64_t w_stride, zo_dtype dtype,
+                         uint32_t d_out, uint32_t d_in, uint32_t group, void *d_codes,
+                         void *d_scales, void *stream);
+
+/* Codes of values quantized elsewhere: d_values, device bytes [d_out x d_in], 8-byte aligned, of which the
+ * low four bits count; d_in a multiple of 32. */
+zo_status zo_q4_pack(zo_ctx *ctx, const uint8_t *d_values, uint32_t d_out, uint32_t d_in,
+                     void *d_codes, void *stream);
+
+/* The weights that codes stand for, s (q - z) in fp32 rounded to the dtype: d_w [d_out x d_in] row-major,
+ * 16-byte aligned. */
+zo_status zo_q4_unpack(zo_ctx *ctx, const void *d_codes, const void *d_scales, const void *d_zeros,
+                       zo_dtype dtype, uint32_t d_out, uint32_t d_in, uint32_t group, void *d_w,
+                       void *stream);
+
+/* zo_adapter_project with W in 4 bits: y = x W^T + bias + scale (x A_g^T) B_g^T, all weights read as
+ * they are held.  x, scales, zeros, bias, adapters and y share `dtype`.  d_starts and d_ids may both be NULL
+ * with n_groups == 0: all rows without adapters.  Up to 64 rows (fp32: 32) the weights are not
+ * rounded; beyond, they are unpacked into the workspace first, rounded to the dtype.  x beyond 2^100 may
+ * overflow on the way (a code enters as 128 + q, fp32 sums).  A weight that is NaN or infinite makes its
+ * feature NaN or infinite in every row, a value of x that is makes its row so, perhaps NaN.
+ * d_workspace: at least zo_q4_workspace_bytes(...) bytes, 256-byte aligned; sizes never fall as rows grow.
+ * Everything else, and errors, as zo_adapter_project and above. */
+uint64_t zo_q4_workspace_bytes(uint64_t rows, uint32_t d_in, uint32_t d_out, zo_dtype dtype,
+                               uint32_t n_adapters, uint32_t rank, uint32_t regenerated);
+zo_status zo_q4_project(zo_ctx *ctx, const void *d_x, uint64_t x_stride, const void *d_codes,
+                        const void *d_scales, const void *d_zeros, uint32_t group,
+                        const void *d_bias, zo_dtype dtype, uint64_t rows, uint32_t d_in,
+                        uint32_t d_out, const void *d_adapters, uint32_t n_adapters, uint32_t rank,
+                        float scale, const int64_t *d_starts, const int32_t *d_ids,
+                        uint32_t n_groups, const int32_t *d_probes, const float *d_alphas,
+                        uint64_t offset, uint32_t step, uint32_t probe0, uint32_t n_probes,
+                        const uint8_t *d_bits, void *d_workspace, uint64_t workspace_bytes,
+                        void *d_y, uint64_t y_stride, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

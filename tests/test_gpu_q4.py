@@ -1,0 +1,320 @@
+"""Weights in 4 bits: zo_q4_quantize, zo_q4_pack, zo_q4_unpack and zo_q4_project against their 64-bit
+definitions (bounds: lm_more_ref, lm_ref)."""
+import math
+
+import pytest
+import torch
+
+import forward_only_amd as zo
+import lm_more_ref as more
+import lm_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+F32, BF = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    c = zo.zo_init(5)
+    yield c
+    c.close()
+
+
+def _weight(d_out, d_in, group, dtype, zeros=False, seed=0):
+    g = torch.Generator().manual_seed(seed + d_out + 5 * d_in)
+    values = torch.randint(0, 16, (d_out, d_in), generator=g, dtype=torch.uint8)
+    scales = (0.01 * (0.5 + torch.rand(d_in // group, d_out, generator=g))).to(dtype)
+    z = (8 + 2 * torch.randn(d_in // group, d_out, generator=g)).to(dtype) if zeros else None
+    return values, scales, z
+
+
+def _held(ctx, values, scales, zeros):
+    return zo.Q4Weight(zo.zo_q4_pack(ctx, values.cuda()), scales.cuda(), None if zeros is None else zeros.cuda(),
+                       values.shape[1])
+
+
+@pytest.mark.parametrize("d_out,d_in", [(8, 32), (16, 128), (24, 160), (40, 96), (136, 1056), (520, 384)])
+def test_pack_and_unpack(ctx, d_out, d_in):
+    values, scales, zeros = _weight(d_out, d_in, 32, F32, True)
+    codes = zo.zo_q4_pack(ctx, values.cuda())
+    assert torch.equal(more.values_of(codes.cpu(), d_out, d_in), values.int())
+    assert torch.equal(more.values_of(more.pack(values), d_out, d_in), values.int())
+    assert torch.equal(zo.zo_q4_pack(ctx, (values | 0xA0).cuda()), codes)       # the low four bits count
+    for dtype in (F32, BF):
+        for z in (None, zeros):
+            q = zo.Q4Weight(codes, scales.to(dtype).cuda(), None if z is None else z.to(dtype).cuda(), d_in)
+            got = zo.zo_q4_unpack(ctx, q)
+            zz = None if z is None else z.to(dtype)
+            want = more.weights(values, scales.to(dtype), zz)
+            # q - z and its product with s round once each, then the type
+            half = ref.UBF if dtype == BF else 0.0
+            ref.assert_close(got, want, (half + 2.01 * ref.U32) * want.abs() + 16 * ref.U32 *
+                             scales.to(dtype).double().abs().max(), "weights")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("d_out,groups,pad", [(8, 1, 0), (24, 3, 8), (136, 5, 0), (1032, 2, 24)])
+def test_quantize(ctx, d_out, groups, pad, group, dtype):
+    d_in = groups * group
+    g = torch.Generator().manual_seed(d_out + group)
+    w = (torch.randn(d_out, d_in + pad, generator=g) * 0.02).to(dtype)
+    w[0, :group] = 0
+    w[1, 3] = 0.07
+    w[1, :group:2] = (0.005 * torch.arange(-(group // 4), group // 4)).to(dtype)[:len(w[1, :group:2])]   # ties
+    w[2] *= 1e-36
+    w[3] *= 1e36
+    w[4] = torch.where(torch.arange(d_in + pad) % 2 == 0, w[4], torch.zeros(()).to(dtype))
+    q = zo.zo_q4_quantize(ctx, w.cuda()[:, :d_in], group)
+    values, scales = more.quantize(w[:, :d_in], group)
+    assert torch.equal(q.scales.cpu(), scales)
+    assert torch.equal(more.values_of(q.codes.cpu(), d_out, d_in), values.int())
+    again = zo.zo_q4_quantize(ctx, w.cuda()[:, :d_in].contiguous(), group, out=q)
+    assert again is q and torch.equal(more.values_of(q.codes.cpu(), d_out, d_in), values.int())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_quantize_exact_ties_and_extremes(ctx, dtype):
+    w = torch.zeros(16, 64)
+    w[0, :16] = torch.arange(16) / 2.0 - 3.5      # scale 0.5: every quotient whole or a half
+    w[0, 16:47] = torch.arange(-7, 8.5, 0.5)[:31] / 2.0
+    w[1, 0], w[1, 1] = 2.0 ** -126, 2.0 ** -127   # the smallest values
+    w[2, 0], w[2, 5] = 3e38, -1.5e38
+    w[3, 0] = 2.0 ** -133
+    w[4, 7] = math.inf
+    w[5, 8] = -math.inf
+    w[6, 9] = math.nan
+    w[7, 32:] = 1.0                               # another group is another's
+    w[7, 3] = math.nan
+    w = w.to(dtype)
+    q = zo.zo_q4_quantize(ctx, w.cuda(), 32)
+    values, scales = more.quantize(w, 32)
+    got = q.scales.cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(scales))
+    assert torch.isnan(got[0, 4:8]).all() and torch.isfinite(got[1]).all()
+    assert torch.equal(got.nan_to_num(-1), scales.nan_to_num(-1))
+    fine = ~torch.isnan(scales).t().repeat_interleave(32, dim=1)
+    assert torch.equal(more.values_of(q.codes.cpu(), 16, 64)[fine], values.int()[fine])
+    assert torch.isnan(zo.zo_q4_unpack(ctx, q)[4, :32]).all()
+
+
+def _problem(lengths, d_in, d_out, rank, adapters, dtype, seed=0, tail=0):
+    g = torch.Generator().manual_seed(seed + d_in + 3 * d_out)
+    rows = sum(lengths) + tail
+    n = lambda *s, std=1.0: (torch.randn(*s, generator=g) * std).to(dtype)  # noqa: E731
+    return {"x": n(rows, d_in), "bias": n(d_out), "ad": n(adapters * rank * (d_in + d_out), std=0.1),
+            "starts": torch.tensor([0] + list(lengths)).cumsum(0),
+            "ids": torch.randint(-1, adapters, (len(lengths),), generator=g, dtype=torch.int32)}
+
+
+def _few(rows, dtype):
+    """Rows whose weights are not rounded."""
+    return rows <= (64 if dtype == BF else 32)
+
+
+def _check(ctx, p, weight, rank, scale=0.5, bias=True, probes=None, alphas=None, bits=None, out=None, x=None,
+           plain=False):
+    values, scales, zeros = weight
+    dtype = scales.dtype
+    d = {k: v.cuda() for k, v in p.items()}
+    kw, z = {}, None
+    if probes is not None:
+        kw, z = {"probes": probes.cuda(), "alphas": alphas.cuda(), "bits": bits.cuda()}, ref.signs(bits, p["ad"].numel())
+    if not plain:
+        kw |= {"adapters": d["ad"], "rank": rank, "starts": d["starts"], "ids": d["ids"], "scale": scale}
+    q = _held(ctx, *weight)
+    call = lambda o=None: zo.zo_q4_project(ctx, d["x"] if x is None else x, q, bias=d["bias"] if bias else None,  # noqa: E731
+                                           out=o, **kw)
+    got = call(out)
+    torch.cuda.synchronize()
+    w = more.weights(values, scales, zeros)
+    rows = p["x"].shape[0]
+    if not _few(rows, dtype):
+        w = w.to(dtype).double()
+    n = 1 if plain else len(p["ids"])
+    y, low, sums = ref.project(p["x"], w, p["bias"] if bias else None, p["ad"], 0 if plain else rank,
+                               [0, rows] if plain else p["starts"], [-1] if plain else p["ids"], scale, probes, alphas, z)
+    assert n == 1 or not plain
+    half = ref.UBF if dtype == BF else ref.U32
+    # fp32: unpacked weights round twice before the product, as zo_q4_unpack
+    xw = p["x"].double().abs() @ w.abs().t()
+    bound = half * y.abs().nan_to_num(0) + (2.0 ** -15 + 128 * ref.U32) * low + sums * 1.01 + 1e-30
+    bound = bound + (more.q4_bound(p["x"], scales, zeros, dtype) if _few(rows, dtype) else 2.01 * ref.U32 * xw
+                     + 16 * ref.U32 * p["x"].double().abs().sum(dim=1, keepdim=True) * scales.double().abs().max())
+    if not _few(rows, dtype) and dtype == BF:
+        # s (q - z) in fp32 may fall to the other side of a tie of the type: one step of one weight
+        bound = bound + 2 * ref.UBF * (p["x"].double().abs() * w.abs().max()).amax(dim=1, keepdim=True)
+    inside = ~torch.isnan(y[:, 0])
+    ref.assert_close(got.cpu()[inside], y[inside], bound[inside], "y")
+    again = call()
+    assert torch.equal(again[inside.cuda()], got[inside.cuda()])         # deterministic
+    return got, q
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("group,zeros", [(32, False), (32, True), (64, False), (64, True), (128, False), (128, True)])
+@pytest.mark.parametrize("rows,d_in,d_out", [(1, 128, 8), (5, 384, 40), (16, 640, 136), (17, 256, 1032), (33, 1152, 72),
+                                             (64, 384, 264), (65, 256, 72), (130, 512, 328)])
+def test_plain_rows(ctx, rows, d_in, d_out, group, zeros, dtype):
+    p = _problem([rows], d_in, d_out, 8, 1, dtype)
+    _check(ctx, p, _weight(d_out, d_in, group, dtype, zeros), 0, plain=True)
+    _check(ctx, p, _weight(d_out, d_in, group, dtype, zeros, seed=9), 0, plain=True, bias=False)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("d_in", [32, 64, 96, 160, 224, 1056])
+def test_rows_that_end_within_a_block(ctx, d_in, dtype):
+    for rows in (3, 70):
+        p = _problem([rows], d_in, 24, 8, 1, dtype)
+        _check(ctx, p, _weight(24, d_in, 32, dtype, True), 0, plain=True)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("lengths,d_in,d_out,rank,adapters", [
+    ([1], 128, 8, 8, 1), ([1, 1, 1], 64, 72, 8, 2), ([3, 0, 5], 96, 16, 16, 3), ([17, 16, 15, 1], 160, 264, 24, 2),
+    ([1] * 40, 96, 328, 8, 7), ([130, 70, 1, 0, 55], 128, 136, 40, 3), ([5, 9], 1056, 40, 128, 2),
+    ([1] * 32, 2048, 640, 16, 32), ([100, 33, 180], 768, 520, 16, 2)])
+def test_adapters(ctx, lengths, d_in, d_out, rank, adapters, dtype):
+    p = _problem(lengths, d_in, d_out, rank, adapters, dtype)
+    _check(ctx, p, _weight(d_out, d_in, 32, dtype), rank)
+    _check(ctx, p, _weight(d_out, d_in, 32, dtype, True), rank, scale=-2.0, bias=False)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("rows", [1, 2, 15, 16, 17, 31, 32, 33, 47, 48, 49, 63, 64, 65, 100, 129, 257, 777])
+def test_row_counts(ctx, rows, dtype):
+    p = _problem([rows // 3, rows - rows // 3], 256, 272, 16, 2, dtype, seed=rows)
+    _check(ctx, p, _weight(272, 256, 64, dtype), 16)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("lengths", [[4, 0, 9, 1], [1] * 9, [70, 200, 3]])
+def test_probes_equal_perturb_in_place(ctx, lengths, dtype):
+    """Stored rows, regenerated rows and adapters moved by zo_perturb give the same bits."""
+    rank, adapters, d_in, d_out, offset, step, probe0 = 16, 2, 160, 72, 1280, 3, 5
+    p = _problem(lengths, d_in, d_out, rank, adapters, dtype, seed=1)
+    n, G = p["ad"].numel(), len(lengths)
+    probes = torch.tensor([(g % 4) - 1 for g in range(G)], dtype=torch.int32)
+    alphas = torch.tensor([1e-3 * (-1) ** g * (1 + g) for g in range(G)])
+    bits = zo.zo_gen_probes(ctx, step, probe0, 3, offset, n).cpu()
+    got, q = _check(ctx, p, _weight(d_out, d_in, 32, dtype), rank, probes=probes, alphas=alphas, bits=bits)
+    d = {k: v.cuda() for k, v in p.items()}
+    kw = {"rank": rank, "starts": d["starts"], "ids": d["ids"], "scale": 0.5, "bias": d["bias"]}
+    regen = zo.zo_q4_project(ctx, d["x"], q, d["ad"], probes=probes.cuda(), alphas=alphas.cuda(), offset=offset,
+                             step=step, probe0=probe0, n_probes=3, **kw)
+    assert torch.equal(got, regen)
+    for g in range(G):
+        th = d["ad"].clone()
+        if probes[g] >= 0:
+            zo.zo_perturb(ctx, th, offset, step, probe0 + int(probes[g]), float(alphas[g]))
+        one = zo.zo_q4_project(ctx, d["x"], q, th, **kw)
+        lo, hi = int(p["starts"][g]), int(p["starts"][g + 1])
+        assert torch.equal(one[lo:hi], got[lo:hi]), g
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("rows", [20, 200])
+def test_rows_of_no_group_bad_indices_and_strides(ctx, rows, dtype):
+    d_in, d_out = 96, 72
+    p = _problem([rows], d_in, d_out, 8, 2, dtype, seed=2, tail=9)
+    n = rows // 4
+    p["starts"] = torch.tensor([2, 2 + n, 2 + 2 * n, 2 + 3 * n])
+    p["ids"] = torch.tensor([0, 5, -1], dtype=torch.int32)
+    weight = _weight(d_out, d_in, 32, dtype)
+    wide = torch.full((rows + 9, d_in + 16), math.nan, dtype=dtype, device="cuda")
+    wide[:, :d_in] = p["x"].cuda()
+    whole = torch.full((rows + 9, d_out + 24), 7.0, dtype=dtype, device="cuda")
+    q = _held(ctx, *weight)
+    kw = {"rank": 8, "starts": p["starts"].cuda(), "ids": p["ids"].cuda(), "bias": p["bias"].cuda()}
+    got = zo.zo_q4_project(ctx, wide[:, :d_in], q, p["ad"].cuda(), out=whole[:, :d_out], **kw)
+    assert torch.isnan(got[2 + n:2 + 2 * n]).all()
+    assert torch.isfinite(got[2:2 + n]).all() and torch.isfinite(got[2 + 2 * n:2 + 3 * n]).all()
+    assert (whole[:2] == 7).all() and (whole[2 + 3 * n:] == 7).all() and (whole[:, d_out:] == 7).all()
+    tight = zo.zo_q4_project(ctx, p["x"].cuda(), q, p["ad"].cuda(), **kw)
+    inside = slice(2, 2 + n)
+    assert torch.equal(tight[inside], got[inside])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("rows", [3, 40, 100])
+def test_nan_stays_with_its_row_and_feature(ctx, rows, dtype):
+    p = _problem([rows], 128, 40, 8, 1, dtype, seed=3)
+    values, scales, _ = _weight(40, 128, 32, dtype)
+    p["x"][1, 5] = math.nan
+    scales[2, 7] = math.nan
+    q = _held(ctx, values, scales, None)
+    y = zo.zo_q4_project(ctx, p["x"].cuda(), q)
+    assert torch.isnan(y[1]).all() and torch.isnan(y[:, 7]).all()
+    keep = torch.ones_like(y, dtype=torch.bool)
+    keep[1], keep[:, 7] = False, False
+    assert torch.isfinite(y[keep]).all()
+
+
+def test_one_workspace_streams_and_graphs(ctx):
+    p = _problem([40, 100, 60], 256, 136, 16, 2, BF, seed=4)
+    q = _held(ctx, *_weight(136, 256, 64, BF))
+    d = {k: v.cuda() for k, v in p.items()}
+    ws = torch.empty(zo.zo_q4_workspace_bytes(200, 256, 136, BF, 2, 16), dtype=torch.uint8, device="cuda")
+    kw = {"rank": 16, "starts": d["starts"], "ids": d["ids"], "workspace": ws}
+    eager = zo.zo_q4_project(ctx, d["x"], q, d["ad"], **kw)
+    small = zo.zo_q4_project(ctx, d["x"][:8], q, d["ad"], rank=16, starts=torch.tensor([0, 5, 8], device="cuda"),
+                             ids=d["ids"][:2], workspace=ws)
+    assert torch.isfinite(small).all()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = zo.zo_q4_project(ctx, d["x"], q, d["ad"], rank=16, starts=d["starts"], ids=d["ids"], stream=side)
+    side.synchronize()
+    assert torch.equal(other, eager)
+    out = torch.empty_like(eager)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        zo.zo_q4_project(ctx, d["x"], q, d["ad"], out=out, **kw)
+    for seed in range(3):
+        d["x"].copy_(_problem([40, 100, 60], 256, 136, 16, 2, BF, seed=30 + seed)["x"])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, zo.zo_q4_project(ctx, d["x"], q, d["ad"], rank=16, starts=d["starts"], ids=d["ids"]))
+
+
+def test_nothing_to_compute(ctx):
+    q = _held(ctx, *_weight(16, 64, 32, F32))
+    assert zo.zo_q4_project(ctx, torch.zeros(0, 64, device="cuda"), q).shape == (0, 16)
+    out = torch.full((3, 16), 7.0, device="cuda")
+    zo.zo_q4_project(ctx, torch.zeros(3, 64, device="cuda"), q, torch.zeros(8 * 80, device="cuda"), 8,
+                     torch.zeros(1, dtype=torch.int64, device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda"),
+                     out=out)
+    assert (out == 7).all()
+
+
+def test_refusals(ctx):
+    values, scales, zeros = _weight(16, 64, 32, F32, True)
+    q = _held(ctx, values, scales, zeros)
+    x = torch.zeros(3, 64, device="cuda")
+    starts, ids = torch.tensor([0, 3], device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ad = torch.zeros(8 * 80, device="cuda")
+    for bad in (q._replace(codes=q.codes[:, :0]), q._replace(scales=q.scales[:, :8]), q._replace(d_in=96),
+                q._replace(zeros=q.zeros[:1]), q._replace(scales=q.scales[:1], zeros=None, d_in=63),
+                q._replace(scales=torch.zeros(4, 16, device="cuda"), zeros=None)):
+        with pytest.raises(ValueError):
+            zo.zo_q4_project(ctx, x, bad)
+    with pytest.raises(TypeError):
+        zo.zo_q4_project(ctx, x.bfloat16(), q)
+    with pytest.raises(TypeError):
+        zo.zo_q4_project(ctx, x, q._replace(codes=q.codes.view(torch.int8)))
+    with pytest.raises(ValueError):
+        zo.zo_q4_project(ctx, x, q, ad, 8)
+    with pytest.raises(ValueError):
+        zo.zo_q4_project(ctx, x, q, ad, 8, starts)
+    with pytest.raises(ValueError):
+        zo.zo_q4_project(ctx, x, q, ad, 8, starts, ids, probes=ids)
+    with pytest.raises(zo.ZOError):
+        zo.zo_q4_project(ctx, x, q, ad, 8, starts, ids, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(zo.ZOError):
+        zo.zo_q4_project(ctx, torch.zeros(3, 68, device="cuda")[:, 4:], q)
+    with pytest.raises(ValueError):
+        zo.zo_q4_quantize(ctx, torch.zeros(8, 48, device="cuda"), 32)
+    with pytest.raises(zo.ZOError):
+        zo.zo_q4_quantize(ctx, torch.zeros(12, 64, device="cuda"), 32)
+    with pytest.raises(zo.ZOError):
+        zo.zo_q4_pack(ctx, torch.zeros(8, 48, dtype=torch.uint8, device="cuda"))

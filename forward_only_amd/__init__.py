@@ -38,7 +38,8 @@ __all__ = [
     "zo_mlp_loss_pair_noalloc", "zo_stream_rmw", "zo_tune_placement", "zo_set_slice_bytes",
     "zo_get_slice_bytes", "library_path", "TokenLogprobs", "HeadLogprobs",
     "zo_token_logprobs", "zo_head_workspace_bytes", "zo_head_logprobs", "zo_group_loss",
-    "zo_adapter_workspace_bytes", "zo_adapter_project", "DistillLoss", "zo_distill_loss", "Q4Weight",
+    "zo_adapter_workspace_bytes", "zo_adapter_project", "DistillLoss", "zo_distill_loss",
+    "HeadGrad", "zo_head_grad_workspace_bytes", "zo_head_grad", "Q4Weight",
     "zo_q4_quantize", "zo_q4_pack", "zo_q4_unpack", "zo_q4_workspace_bytes", "zo_q4_project",
 ]
 
@@ -781,6 +782,58 @@ def zo_distill_loss(ctx: Context, logits: torch.Tensor, teacher_ids: torch.Tenso
     _lib.check(_lib.lib().zo_distill_loss(ctx.handle, lp, code, rows, vocab, stride, idp, hp, k, tp,
                                           float(temperature), op, rp, gp, gs, _stream(stream, dev)),
                "zo_distill_loss")
+    return out
+
+
+class HeadGrad(NamedTuple):
+    """Results of zo_head_grad; a gradient that was not asked for is None."""
+    logp: torch.Tensor
+    hidden_grad: Optional[torch.Tensor]
+    weight_grad: Optional[torch.Tensor]
+
+
+def zo_head_grad_workspace_bytes(rows: int, d: int, vocab: int, dtype: torch.dtype) -> int:
+    return int(_lib.lib().zo_head_grad_workspace_bytes(rows, d, vocab, _code_of(dtype)))
+
+
+def zo_head_grad(ctx: Context, hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
+                 row_grad: torch.Tensor | None = None, hidden_grad: bool = True, weight_grad: bool = True,
+                 workspace: torch.Tensor | None = None, out: HeadGrad | None = None,
+                 stream=None) -> HeadGrad:
+    """Log probabilities of the targets from hidden [rows, d] and weight [vocab, d], as
+    zo_head_logprobs, with the gradients of -sum(row_grad * logp) (row_grad float32 [rows]; None:
+    ones) with respect to both, in their dtype; the logits are never stored.  Rows with the
+    target ZO_IGNORE_TOKEN give 0 and take no part.  workspace: at least
+    zo_head_grad_workspace_bytes of the largest batch that it serves; out: tensors of an earlier call."""
+    hp, rows, d, stride = _matrix(hidden, "hidden")
+    dev = hidden.get_device()
+    code = _dtype_code(hidden)
+    wp = _dev(weight, "weight", hidden.dtype)
+    if weight.dim() != 2 or weight.shape[1] != d:
+        raise ValueError(f"weight must have shape (vocab, {d}), got {tuple(weight.shape)}")
+    vocab = weight.shape[0]
+    if targets is None:
+        raise ValueError("targets are needed")
+    tp, rp = _vector(targets, "targets", rows, torch.int64, dev), _vector(row_grad, "row_grad", rows, torch.float32, dev)
+    if out is None:
+        out = HeadGrad(_new(rows, torch.float32, stream),
+                       _new((rows, d), hidden.dtype, stream) if hidden_grad else None,
+                       _new((vocab, d), hidden.dtype, stream) if weight_grad else None)
+    op, gp = _vector(out.logp, "logp", rows, torch.float32, dev), [None, None]
+    for i, (t, name, shape) in enumerate(((out.hidden_grad, "hidden_grad", (rows, d)),
+                                          (out.weight_grad, "weight_grad", (vocab, d)))):
+        if t is not None:
+            gp[i] = _dev(t, name, hidden.dtype)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if workspace is None:
+        wb = int(_lib.lib().zo_head_grad_workspace_bytes(rows, d, vocab, code))
+        workspace = _new(wb, torch.uint8, stream)
+        ws = workspace.data_ptr()
+    else:
+        ws, wb = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+    _lib.check(_lib.lib().zo_head_grad(ctx.handle, hp, stride, wp, code, rows, d, vocab, tp, rp, op, gp[0], gp[1],
+                                       ws, wb, _stream(stream, dev)), "zo_head_grad")
     return out
 
 

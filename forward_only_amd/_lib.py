@@ -71,6 +71,9 @@ SIGNATURES = {
                                   _vp, _vp, _u64, _vp, _u64, _vp]),
     "zo_distill_loss": (_int, [_vp, _vp, _int, _u64, _u32, _u64, _vp, _vp, _u32, _vp, _f32, _vp, _vp,
                                _vp, _u64, _vp]),
+    "zo_head_grad_workspace_bytes": (_u64, [_u64, _u32, _u32, _int]),
+    "zo_head_grad": (_int, [_vp, _vp, _u64, _vp, _int, _u64, _u32, _u32, _vp, _vp, _vp, _vp, _vp, _vp,
+                            _u64, _vp]),
     "zo_q4_code_bytes": (_u64, [_u32, _u32]),
     "zo_q4_quantize": (_int, [_vp, _vp, _u64, _int, _u32, _u32, _u32, _vp, _vp, _vp]),
     "zo_q4_pack": (_int, [_vp, _vp, _u32, _u32, _vp, _vp]),

@@ -64,6 +64,7 @@ constexpr uint64_t kMaxRows = 0x7FFFFFFFu;   // of the language-model operators
 // addressed by 32 bits of 16-byte units.
 constexpr uint64_t kMaxWidth = 1u << 26, kMaxFeatures = 1u << 24, kMaxGroups = 1u << 22;
 constexpr uint64_t kMaxProjectRows = 1u << 25, kMaxProjected = (uint64_t)1 << 35;
+constexpr uint64_t kMaxGradWidth = 1u << 20;
 // The rows of a product's left operand reach at most 64 GiB (32 bits of 16-byte units).
 inline bool reach_ok(uint64_t rows, uint64_t stride, uint64_t k, bool bf16)
 {
@@ -223,7 +224,7 @@ zo_status zo_init(uint64_t seed, zo_ctx **out)
     }
     c->d_scratch = scratch_on(c->device);
     if (!c->d_scratch || zo::prepare_update() != hipSuccess ||
-        zo::prepare_products() != hipSuccess || zo::prepare_q4() != hipSuccess ||
+        zo::prepare_products() != hipSuccess || zo::prepare_q4() != hipSuccess || zo::prepare_head_grad() != hipSuccess ||
         zo::launch_zero_u32(c->d_counter, 64, nullptr) != hipSuccess ||
         hipDeviceSynchronize() != hipSuccess) {
         (void)hipFree(c->d_partials);
@@ -873,6 +874,35 @@ zo_status zo_q4_project(zo_ctx *c, const void *d_x, uint64_t x_stride, const voi
     }
     return from_hip(zo::launch_q4_project(a, dtype == ZO_BF16, d_x, x_stride, {d_codes, d_scales, d_zeros, group},
                                           d_bias, d_adapters, u, slices, unpacked, d_y, y_stride, as_stream(stream)));
+}
+
+uint64_t zo_head_grad_workspace_bytes(uint64_t rows, uint32_t d, uint32_t vocab, zo_dtype dtype)
+{
+    return zo::head_grad_space(rows, d, vocab, dtype == ZO_BF16, nullptr).bytes;
+}
+
+zo_status zo_head_grad(zo_ctx *c, const void *d_hidden, uint64_t hidden_stride, const void *d_weight, zo_dtype dtype,
+                       uint64_t rows, uint32_t d, uint32_t vocab, const int64_t *d_targets, const float *d_row_grad,
+                       float *d_logp, void *d_hidden_grad, void *d_weight_grad, void *d_workspace,
+                       uint64_t workspace_bytes, void *stream)
+{
+    if (!ctx_ok(c)) return ZO_EINVAL;
+    if (dtype != ZO_FP32 && dtype != ZO_BF16) return ZO_EINVAL;
+    if (rows > kMaxProjectRows || vocab > kMaxFeatures || d > kMaxGradWidth || rows * d > kMaxProjected)
+        return ZO_EUNSUPPORTED;
+    if (vocab == 0 || d == 0 || d % 8u || hidden_stride % 8u) return ZO_EINVAL;
+    if (!aligned16(d_hidden_grad) || !aligned16(d_weight_grad)) return ZO_EINVAL;
+    const zo::HeadGradArgs h = {rows, hidden_stride, d, vocab, d_targets, d_row_grad, d_logp, d_hidden_grad, d_weight_grad,
+                                d_workspace};
+    if (rows == 0) return from_hip(zo::launch_head_grad(h, dtype == ZO_BF16, d_hidden, d_weight, as_stream(stream)));
+    if (!d_hidden || !d_weight || !d_targets || !aligned16(d_hidden) || !aligned16(d_weight)) return ZO_EINVAL;
+    if (!aligned<8>(d_targets) || !aligned<4>(d_row_grad) || !aligned<4>(d_logp)) return ZO_EINVAL;
+    if (!d_logp && !d_hidden_grad && !d_weight_grad) return ZO_EINVAL;
+    if (hidden_stride > (UINT64_MAX >> 4) / rows) return ZO_EINVAL;
+    if (!d_workspace || !aligned<256>(d_workspace) ||
+        workspace_bytes < zo_head_grad_workspace_bytes(rows, d, vocab, dtype))
+        return ZO_EINVAL;
+    return from_hip(zo::launch_head_grad(h, dtype == ZO_BF16, d_hidden, d_weight, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -132,7 +132,8 @@ __global__ __launch_bounds__(1024) void k_head_join(const float *m, const float 
                                                     const float *tl, uint32_t parts, uint64_t base,
                                                     uint64_t rows, const uint32_t *list,
                                                     const uint32_t *count, const int64_t *targets,
-                                                    uint32_t features, float *logp, float *entropy)
+                                                    uint32_t features, float *logp, float *entropy,
+                                                    float2 *norms)
 {
     const uint64_t n = places(base, rows, count);
     const int of = threadIdx.x % kOf, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -161,10 +162,9 @@ __global__ __launch_bounds__(1024) void k_head_join(const float *m, const float 
     const int64_t tgt = targets ? targets[row] : 0;
     const bool ignore = targets && tgt == kIgnoreToken;
     const float logs = logf(st.s);
-    if (logp)
-        logp[row] = ignore ? 0.0f
-                    : tgt >= 0 && tgt < (int64_t)features ? (tl[at] - st.m) - logs
-                                                          : __builtin_nanf("");
+    const bool known = tgt >= 0 && tgt < (int64_t)features;
+    if (logp) logp[row] = ignore ? 0.0f : known ? (tl[at] - st.m) - logs : __builtin_nanf("");
+    if (norms) norms[base + at] = make_float2(st.m, known ? logs : __builtin_nanf(""));
     if (entropy) entropy[row] = ignore ? 0.0f : logs - st.t / st.s;
 }
 
@@ -216,26 +216,29 @@ hipError_t head(const HeadArgs &h, const void *x, const void *w, hipStream_t str
     typedef typename T::elem E;
     const HeadSpace sp = head_space(h.rows, h.k, h.features, T::kBf16, h.workspace);
     const bool small = sp.shape == Shape::few;
-    uint32_t *list = nullptr, *count = nullptr;
-    if (h.targets && !small) {
-        list = sp.list;
-        count = sp.count;
-        k_counted<<<1, 1024, 0, stream>>>(h.targets, h.rows, list, count, h.logp, h.entropy);
-        const hipError_t e = hipGetLastError();
+    // rows of x by place, what each place's row is, and how many there are
+    const uint32_t *from = nullptr, *list = nullptr, *count = nullptr;
+    if (h.count) {
+        list = h.list;
+        count = h.count;
+    } else if (h.targets && !small) {
+        const hipError_t e = launch_counted(h.targets, h.rows, sp.list, sp.count, h.logp, h.entropy, stream);
         if (e != hipSuccess) return e;
+        from = list = sp.list;
+        count = sp.count;
     }
     const E *px = static_cast<const E *>(x), *pw = static_cast<const E *>(w);
     for (uint64_t base = 0; base < h.rows; base += kHeadPlaces) {
         const uint64_t rows = h.rows - base < kHeadPlaces ? h.rows - base : kHeadPlaces;
         const ProductArgs p = {base, rows, h.x_stride, h.k, h.features, sp.slices};
         const EndHead end = {h.features, base, rows, h.targets, list, count, sp.m, sp.s, sp.t, sp.tl};
-        hipError_t e = by_shape<T>(sp.shape, p, px, pw, list, count, end, stream);
+        hipError_t e = by_shape<T>(sp.shape, p, px, pw, from, count, end, stream);
         if (e != hipSuccess) return e;
         const auto join = [&](auto of) {
             constexpr int kOf = decltype(of)::value;
             k_head_join<kOf><<<(uint32_t)((rows + kOf - 1) / kOf), 1024, 0, stream>>>(
                 sp.m, sp.s, sp.t, sp.tl, sp.parts, base, rows, list, count, h.targets, h.features, h.logp,
-                h.entropy);
+                h.entropy, static_cast<float2 *>(h.norms));
         };
         if (rows <= 256)
             join(std::integral_constant<int, 1>{});
@@ -288,6 +291,13 @@ hipError_t prepare()
 }
 
 }  // namespace
+
+hipError_t launch_counted(const int64_t *targets, uint64_t rows, uint32_t *list, uint32_t *count, float *logp,
+                          float *entropy, hipStream_t stream)
+{
+    k_counted<<<1, 1024, 0, stream>>>(targets, rows, list, count, logp, entropy);
+    return hipGetLastError();
+}
 
 hipError_t prepare_products()
 {

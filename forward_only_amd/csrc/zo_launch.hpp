@@ -289,7 +289,16 @@ struct HeadArgs {
     const int64_t *targets;        // nullptr: entropies of all rows
     float *logp, *entropy;
     void *workspace;
+    // Given: x holds the rows that count, one a place, list says which they are, and norms
+    // ([places] of two floats: a row's largest logit and the logarithm of its sum; NaN for a
+    // target outside the vocabulary) may be wanted.
+    const uint32_t *list = nullptr, *count = nullptr;
+    void *norms = nullptr;
 };
+// list: the rows whose target is not ignored, in order; count: how many; zeros for the others'
+// logp and entropy (or nullptr).
+hipError_t launch_counted(const int64_t *targets, uint64_t rows, uint32_t *list, uint32_t *count, float *logp,
+                          float *entropy, hipStream_t stream);
 // Rows whose partial statistics are held at once.
 constexpr uint64_t kHeadPlaces = 16384;
 struct HeadSpace {
@@ -332,6 +341,65 @@ inline HeadSpace head_space(uint64_t rows, uint32_t k, uint32_t features, bool b
 }
 hipError_t launch_head_logprobs(const HeadArgs &h, bool bf16, const void *x, const void *w,
                                 hipStream_t stream);
+
+struct HeadGradArgs {
+    uint64_t rows, x_stride;
+    uint32_t d, features;
+    const int64_t *targets;
+    const float *row_grad;         // nullptr: 1 for each row
+    float *logp;                   // or nullptr
+    void *hidden_grad, *weight_grad;   // of the operands' type; or nullptr
+    void *workspace;
+};
+// Bytes of a piece's gradients of the logits, and the most features of a piece.
+constexpr uint64_t kGradPieceBytes = (uint64_t)1 << 29;
+constexpr uint32_t kGradPiece = 32768;
+struct HeadGradSpace {
+    uint32_t *count, *list;
+    void *norms, *x, *xt, *d, *dt, *wt, *head;
+    float *sum, *slices;
+    uint32_t piece, pieces;        // features of a piece (a multiple of 8), and their number
+    uint64_t pitch;                // places, to a multiple of 8
+    uint64_t bytes;
+};
+inline HeadGradSpace head_grad_space(uint64_t rows, uint32_t d, uint32_t features, bool bf16, void *base)
+{
+    const uint64_t size = bf16 ? 2 : 4;
+    HeadGradSpace s;
+    s.pitch = (rows + 7) / 8 * 8;
+    // pieces of one size, of whole tiles where there are several
+    const uint64_t fits = s.pitch ? kGradPieceBytes / (s.pitch * size) / 256 * 256 : kGradPiece;
+    const uint64_t most = fits < 256 ? 256 : fits > kGradPiece ? kGradPiece : fits;
+    s.pieces = (uint32_t)(((uint64_t)features + most - 1) / most);
+    const uint64_t each = s.pieces ? ((uint64_t)features + s.pieces - 1) / s.pieces : 0;
+    s.piece = (uint32_t)(s.pieces > 1 ? (each + 255) / 256 * 256 : (each + 7) / 8 * 8);
+    // what never falls as rows grow: at most so much for a piece, at least 256 features
+    const uint64_t whole = ((uint64_t)features + 255) / 256 * 256 < kGradPiece ? ((uint64_t)features + 255) / 256 * 256 : kGradPiece;
+    const uint64_t least = s.pitch * 256 * size;
+    const uint64_t cap = kGradPieceBytes > least ? kGradPieceBytes : least;
+    const uint64_t piece_bytes = s.pitch * whole * size < cap ? s.pitch * whole * size : cap;
+    uint64_t at = 0;
+    auto take = [&](uint64_t bytes) {
+        void *p = base ? static_cast<char *>(base) + at : nullptr;
+        at += (bytes + 255) / 256 * 256;
+        return p;
+    };
+    s.count = static_cast<uint32_t *>(take(4));
+    s.list = static_cast<uint32_t *>(take(rows * 4));
+    s.norms = take(rows * 8);
+    s.x = take(rows * d * size);
+    s.xt = take(s.pitch * d * size);
+    s.d = take(piece_bytes);
+    s.dt = take(piece_bytes);
+    s.wt = take(whole * d * size);
+    s.sum = static_cast<float *>(take(rows * d * 4));
+    s.slices = static_cast<float *>(take(kBigSliceBytes));
+    s.head = base ? static_cast<char *>(base) + at : nullptr;
+    s.bytes = at + head_space(rows, d, features, bf16, nullptr).bytes;
+    return s;
+}
+hipError_t prepare_head_grad();
+hipError_t launch_head_grad(const HeadGradArgs &h, bool bf16, const void *x, const void *w, hipStream_t stream);
 
 // Diagnostic: every 16-byte word of buf (bytes % 16 == 0) <- word ^ mask, in place;
 // slice_bytes > 0 (a multiple of 8 KiB) issues it as one launch per slice of that size.

@@ -372,8 +372,17 @@ __global__ __launch_bounds__(shrink_waves<kXF>() * 64) void k_shrink(
 struct ProductArgs {
     uint64_t base, rows;   // places [base, base + rows) of the rows, or of the list's rows
     uint64_t x_stride;
-    uint32_t k, features;
+    uint32_t k, features;  // of rows k apart in w
     float *slices;         // workspace of the sliced tiles, or nullptr: none are sliced
+    // Where the values of k are rows that count: how many do, on the device; both operands hold
+    // zeros from there to the next multiple of 8.
+    const uint32_t *k_count = nullptr;
+    __device__ __forceinline__ uint32_t depth() const
+    {
+        if (!k_count) return k;
+        const uint32_t n = (*k_count + 7) / 8 * 8;
+        return n < k ? n : k;
+    }
 };
 
 // How many of `rows` places from `base` on there are when only *count places hold a row.
@@ -720,10 +729,11 @@ __global__ __launch_bounds__(512, 2) void k_big(ProductArgs p, const typename T:
     enum { F0, F1, R0, R1 };
     extern __shared__ u32x4 stage[];                        // [2][F0, F1, R0, R1][128][kPieces]
     const uint64_t rows = places(p.base, p.rows, count);
-    const uint32_t steps = (p.k + kStep - 1) / kStep;
+    const uint32_t depth = p.depth(), steps = (depth + kStep - 1) / kStep;
     const Cut cut(p, rows, steps);
     uint32_t tile, first = 0, last = steps;
     if constexpr (End::kSlices) {
+        if (cut.rest == 0) return;
         const uint32_t slice = blockIdx.x % cut.slices;
         if (blockIdx.x / cut.slices >= cut.rest) return;
         tile = cut.whole + blockIdx.x / cut.slices;
@@ -762,7 +772,7 @@ __global__ __launch_bounds__(512, 2) void k_big(ProductArgs p, const typename T:
         }
     }
     const auto issue = [&](int part, uint32_t step) {
-        const bool in = step < last && (uint64_t)step * kStep + piece < p.k;
+        const bool in = step < last && (uint64_t)step * kStep + piece < depth;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const u32x4 *g = (part < R0 ? from_w : from_x) + (uint64_t)step * kPieces + src[part][j];
@@ -858,7 +868,7 @@ __global__ __launch_bounds__(256) void k_slices(ProductArgs p, const uint32_t *c
 {
     __shared__ u32x4 lds[3 * 8 * 64];
     const uint64_t rows = places(p.base, p.rows, count);
-    const Cut cut(p, rows, (p.k + 8 * T::kPiece - 1) / (8 * T::kPiece));
+    const Cut cut(p, rows, (p.depth() + 8 * T::kPiece - 1) / (8 * T::kPiece));
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t i = blockIdx.x / 32, of = blockIdx.x / 4 % 8, n = blockIdx.x % 4;
@@ -924,9 +934,9 @@ __global__ __launch_bounds__(256) void k_mid(ProductArgs p, const typename T::el
         const uint64_t r = r0 + i < rows ? r0 + i : rows - 1;
         src[1][j] = x + (list ? list[p.base + r] : p.base + r) * p.x_stride + piece;
     }
-    const uint32_t steps = (p.k + kStep - 1) / kStep;
+    const uint32_t depth = p.depth(), steps = (depth + kStep - 1) / kStep;
     const auto issue = [&](uint32_t step) {
-        const bool in = (uint64_t)step * kStep + piece < p.k;
+        const bool in = (uint64_t)step * kStep + piece < depth;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -1006,7 +1016,7 @@ __global__ __launch_bounds__((kFewWaves + kMR) * 64) void k_few(ProductArgs p,
         end.store(own, f0, 16 * n);
         return;
     }
-    const F feed(stage + wave * kFewStages * F::kStage, p.k, [&](int i) {
+    const F feed(stage + wave * kFewStages * F::kStage, p.depth(), [&](int i) {
         if (i < 16 * kMF) {
             const uint32_t f = f0 + i < p.features ? f0 + i : p.features - 1;
             return w + (uint64_t)f * p.k;
@@ -1020,7 +1030,7 @@ __global__ __launch_bounds__((kFewWaves + kMR) * 64) void k_few(ProductArgs p,
     // Each workgroup begins elsewhere in k: rows a power of two apart lie on the same memory
     // channels, and all workgroups would walk over them together (8 rows, bf16 8192 to 28672: 98
     // us begun together, 74 apart; 4096 to 18000 39 and 27; 5120 to 50272 84 either way).
-    const uint32_t turn = (blockIdx.x * 0x9E3779B1u >> 8) % steps;
+    const uint32_t turn = steps ? (blockIdx.x * 0x9E3779B1u >> 8) % steps : 0;
     const auto turned = [&](uint32_t s) { return s >= steps ? s : s + turn < steps ? s + turn : s + turn - steps; };
 #pragma unroll
     for (int i = 0; i < kFewStages - 1; ++i) feed.issue(turned(wave + i * kFewWaves), i);
@@ -1068,7 +1078,7 @@ hipError_t big(const ProductArgs &p, const typename T::elem *x, const typename T
     const uint32_t steps = (p.k + 8 * T::kPiece - 1) / (8 * T::kPiece);
     const bool sliced = p.slices && steps >= 2 * kBigSliceSteps && (count || big_slices(over, steps) > 1);
     hipError_t e = hipSuccess;
-    if (count || !sliced || n > over) {
+    if (count || p.k_count || !sliced || n > over) {
         k_big<T, End><<<(uint32_t)((n + 7) / 8 * 8), 512, 2 * 512 * 128, stream>>>(p, x, w, list, count, end);
         e = hipGetLastError();
     }

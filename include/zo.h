@@ -519,6 +519,28 @@ zo_status zo_distill_loss(zo_ctx *ctx, const void *d_logits, zo_dtype dtype, uin
                           float temperature, float *d_loss, const float *d_row_grad, void *d_grad,
                           uint64_t grad_stride, void *stream);
 
+/* Log probabilities of given tokens from hidden states h [rows x d] and the unembedding matrix
+ * W [vocab x d], as zo_head_logprobs, with the gradients of sum_row d_row_grad[row] (-logp[row]):
+ *   D[row][v] = d_row_grad[row] (softmax(h W^T)[row][v] - [v = target]),
+ *   d_hidden_grad = D W [rows x d],  d_weight_grad = D^T h [vocab x d]
+ * (d_row_grad, device float [rows], NULL: 1 for each row).  Logits are formed in fp32, tile by tile, and
+ * never stored; D is rounded to the dtype, in pieces of the vocabulary that the workspace holds, and
+ * multiplied with fp32 sums; the gradients are rounded once.  Rows with the ignored target are not computed
+ * in batches of more than 64 rows; their logp and gradient are 0 and they add nothing to d_weight_grad, whatever
+ * they hold.  A target outside the vocabulary, or a row that holds NaN or an infinity, makes the row's logp and
+ * gradient NaN, and d_weight_grad with them.  Deterministic.
+ * d_targets: device int64 [rows].  d_logp, d_hidden_grad and d_weight_grad may each be NULL; the gradients are
+ * of `dtype`, contiguous, 16-byte aligned.  d_workspace: device, 256-byte aligned, at least
+ * zo_head_grad_workspace_bytes(rows, d, vocab, dtype) bytes, which never fall as rows grow.  rows == 0 gives
+ * a d_weight_grad of zeros.
+ * Errors: as zo_head_logprobs; ZO_EUNSUPPORTED if rows exceed 2^25, d 2^20, vocab 2^24 or rows * d 2^35. */
+uint64_t zo_head_grad_workspace_bytes(uint64_t rows, uint32_t d, uint32_t vocab, zo_dtype dtype);
+zo_status zo_head_grad(zo_ctx *ctx, const void *d_hidden, uint64_t hidden_stride,
+                       const void *d_weight, zo_dtype dtype, uint64_t rows, uint32_t d,
+                       uint32_t vocab, const int64_t *d_targets, const float *d_row_grad,
+                       float *d_logp, void *d_hidden_grad, void *d_weight_grad, void *d_workspace,
+                       uint64_t workspace_bytes, void *stream);
+
 /* ---- Weights in 4 bits -------------------------------------------------------------------
  * W[f][k] = s (q - z) with codes q in 0 .. 15 and, for each feature f and each group of `group`
  * neighbouring values of k (32, 64 or 128), a scale s and a zero point z: d_scales and d_zeros, device

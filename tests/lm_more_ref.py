@@ -118,3 +118,44 @@ def distill(x, ids, t, targets, temperature):
         none = none | (targets == IGNORE)
     loss, grad = loss.masked_fill(none, 0.0), T * grad.masked_fill(none[:, None], 0.0)
     return loss, grad, lb, T * gb
+
+
+def head_grad(h, w, targets, g, dtype):
+    """(logp, dh, dW, bounds of the three) in 64 bits, CPU.
+
+    The logits carry lm_ref's bound of a product, e = 8 sqrt(d) u |h| |w| (at most over a row's
+    features), and log s E as in lm_ref: a share p is off by p (2 e + E + 4 u (|l - m| + |log s|)) or
+    less, D by that, its product with g and the rounding to the type.  The products add
+    8 sqrt(terms) u of their operands' 2-norms."""
+    H, W, G = h.double(), w.double(), g.double()
+    rows, d = h.shape
+    vocab = w.shape[0]
+    half = UBF if dtype == torch.bfloat16 else U32
+    count = targets != IGNORE
+    H = torch.where(count[:, None], H, torch.zeros_like(H))
+    ok = (targets >= 0) & (targets < vocab)
+    at = torch.where(ok, targets, torch.zeros_like(targets))
+    x = H @ W.t()
+    m = x.amax(dim=1, keepdim=True)
+    logs = torch.log(torch.exp(x - m).sum(dim=1, keepdim=True))
+    p = torch.exp((x - m) - logs)
+    e = 8 * math.sqrt(d) * U32 * torch.linalg.vector_norm(H, dim=1) * torch.linalg.vector_norm(W, dim=1).max()
+    E = (vocab / 256 + 64) * U32
+    logp = (x - m - logs).gather(1, at[:, None])[:, 0]
+    D = p.clone()
+    D[torch.arange(rows), at] -= 1.0
+    gz = torch.where(count, G, torch.zeros_like(G))[:, None]
+    D = D * gz
+    off = gz.abs() * p * (2 * e[:, None] + E + 4 * U32 * ((x - m).abs() + logs.abs())) + (half + 3 * U32) * D.abs() \
+        + gz.abs() * U32 * p
+    norm = torch.linalg.vector_norm
+    dh, dw = D @ W, D.t() @ H
+    bh = off @ W.abs() + 8 * math.sqrt(vocab) * U32 * norm(D, dim=1)[:, None] * norm(W, dim=0)[None, :] + half * dh.abs()
+    bw = off.t() @ H.abs() + 8 * math.sqrt(rows) * U32 * norm(D, dim=0)[:, None] * norm(H, dim=0)[None, :] + half * dw.abs()
+    bl = 2 * e + E + 2 * U32 * ((x - m).gather(1, at[:, None])[:, 0].abs() + logp.abs())
+    bad = count & ~ok
+    logp = logp.masked_fill(bad, math.nan).masked_fill(~count, 0.0)
+    dh = dh.masked_fill(bad[:, None], math.nan)
+    if bool(bad.any()):
+        dw = torch.full_like(dw, math.nan)
+    return logp, dh, dw, bl, bh, bw

@@ -1,0 +1,168 @@
+"""zo_head_grad against its 64-bit definition (bounds: lm_more_ref), differences and zo_head_logprobs."""
+import math
+
+import pytest
+import torch
+
+import forward_only_amd as zo
+import lm_more_ref as more
+import lm_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+F32, BF = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    c = zo.zo_init(11)
+    yield c
+    c.close()
+
+
+def _case(rows, d, vocab, dtype, ignore=0.0, seed=0):
+    g = torch.Generator().manual_seed(seed + 3 * rows + d + 7 * vocab)
+    h = torch.randn(rows, d, generator=g).to(dtype)
+    w = (torch.randn(vocab, d, generator=g) * 2.5 / math.sqrt(d)).to(dtype)
+    t = torch.randint(0, vocab, (rows,), generator=g)
+    t[torch.rand(rows, generator=g) < ignore] = ref.IGNORE
+    return h, w, t, (torch.rand(rows, generator=g) + 0.5) * (1 - 2 * (torch.rand(rows, generator=g) < 0.3).float())
+
+
+def _check(ctx, h, w, t, g, dtype, x=None, **kw):
+    got = zo.zo_head_grad(ctx, h.cuda() if x is None else x, w.cuda(), t.cuda(), row_grad=g.cuda(), **kw)
+    torch.cuda.synchronize()
+    logp, dh, dw, bl, bh, bw = more.head_grad(h, w, t, g, dtype)
+    ref.assert_close(got.logp, logp, bl + 1e-30, "logp")
+    ref.assert_close(got.hidden_grad, dh, bh * 1.01 + 1e-30, "hidden_grad")
+    ref.assert_close(got.weight_grad, dw, bw * 1.01 + 1e-30, "weight_grad")
+    return got
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("rows,d,vocab", [(1, 8, 1), (1, 64, 40), (3, 40, 9), (8, 256, 1003), (33, 72, 260), (64, 128, 777),
+                                          (65, 128, 264), (130, 264, 515), (257, 64, 2050), (300, 776, 300), (1030, 136, 700),
+                                          (5, 1032, 5003)])
+def test_matches_reference(ctx, rows, d, vocab, dtype):
+    h, w, t, g = _case(rows, d, vocab, dtype)
+    got = _check(ctx, h, w, t, g, dtype)
+    again = zo.zo_head_grad(ctx, h.cuda(), w.cuda(), t.cuda(), row_grad=g.cuda())
+    for a, b in zip(got, again):
+        assert torch.equal(a, b)                                    # deterministic
+    h, w, t, g = _case(rows, d, vocab, dtype, ignore=0.6, seed=5)
+    _check(ctx, h, w, t, g, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("rows", [40, 200])
+def test_ignored_rows_take_no_part(ctx, rows, dtype):
+    h, w, t, g = _case(rows, 72, 300, dtype, seed=1)
+    t[::3] = ref.IGNORE
+    h[::3] = math.nan
+    g[::3] = math.nan
+    _check(ctx, torch.where((t == ref.IGNORE)[:, None], torch.zeros_like(h), h), w, t,
+           torch.where(t == ref.IGNORE, torch.zeros_like(g), g), dtype, x=h.cuda())
+    got = zo.zo_head_grad(ctx, h.cuda(), w.cuda(), t.cuda(), row_grad=g.cuda())
+    assert torch.isfinite(got.weight_grad).all() and not got.hidden_grad[::3].any() and not got.logp[::3].any()
+    none = zo.zo_head_grad(ctx, h.cuda(), w.cuda(), torch.full_like(t, ref.IGNORE).cuda())
+    assert not none.weight_grad.any() and not none.hidden_grad.any() and not none.logp.any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("rows", [6, 100])
+def test_bad_targets_and_values(ctx, rows, dtype):
+    h, w, t, g = _case(rows, 64, 100, dtype, seed=2)
+    t[2], t[4] = 100, -1
+    got = _check(ctx, h, w, t, g, dtype)
+    assert torch.isnan(got.hidden_grad[2]).all() and torch.isnan(got.weight_grad).all()
+    assert torch.isfinite(got.hidden_grad[[0, 1, 3, 5]]).all()
+    h, w, t, g = _case(rows, 64, 100, dtype, seed=2)
+    h[1, 3] = math.nan
+    got = zo.zo_head_grad(ctx, h.cuda(), w.cuda(), t.cuda())
+    assert torch.isnan(got.logp[1]) and torch.isnan(got.hidden_grad[1]).all()
+    assert torch.isfinite(got.hidden_grad[0]).all() and torch.isfinite(got.logp[[0, 2, 3]]).all()
+
+
+def test_pieces_of_the_vocabulary(ctx):
+    """More features than one piece holds, of whole tiles and not."""
+    for rows, d, vocab, dtype in ((70, 64, 40007, BF), (9, 40, 70001, BF), (70, 16, 33000, F32)):
+        h, w, t, g = _case(rows, d, vocab, dtype, ignore=0.2, seed=3)
+        _check(ctx, h, w, t, g, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_one_gradient_or_none(ctx, dtype):
+    h, w, t, g = (v.cuda() for v in _case(90, 136, 500, dtype, ignore=0.3, seed=4))
+    both = zo.zo_head_grad(ctx, h, w, t, row_grad=g)
+    a = zo.zo_head_grad(ctx, h, w, t, row_grad=g, weight_grad=False)
+    b = zo.zo_head_grad(ctx, h, w, t, row_grad=g, hidden_grad=False)
+    c = zo.zo_head_grad(ctx, h, w, t, hidden_grad=False, weight_grad=False)
+    assert a.weight_grad is None and b.hidden_grad is None and c.hidden_grad is None
+    assert torch.equal(a.hidden_grad, both.hidden_grad) and torch.equal(b.weight_grad, both.weight_grad)
+    for o in (a, b, c):
+        assert torch.equal(o.logp, both.logp)
+    alone = zo.zo_head_logprobs(ctx, h, w, t, entropy=False)
+    # the same sums of the same products, in the order of rows by place instead of by row
+    ref.assert_close(both.logp, alone.logp.double().cpu(), 1e-4, "logp")
+
+
+def test_gradient_against_differences(ctx):
+    h, w, t, g = _case(12, 40, 90, F32, ignore=0.2, seed=6)
+    got = zo.zo_head_grad(ctx, h.cuda(), w.cuda(), t.cuda(), row_grad=g.cuda())
+    gen = torch.Generator().manual_seed(2)
+    loss = lambda hh, ww: -(g.double() * more.head_grad(hh, ww, t, g, F32)[0]).sum()  # noqa: E731
+    for _ in range(4):
+        dh, dw, e = torch.randn(12, 40, generator=gen).double(), torch.randn(90, 40, generator=gen).double(), 1e-5
+        H, W = h.double(), w.double()
+        num = (loss(H + e * dh, W + e * dw) - loss(H - e * dh, W - e * dw)) / (2 * e)
+        ana = (got.hidden_grad.double().cpu() * dh).sum() + (got.weight_grad.double().cpu() * dw).sum()
+        # truncation e^2 and cancellation 1e-15 / e of values of about 100
+        assert abs(float(num - ana)) < 1e-3
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_strides_workspace_streams_and_graph(ctx, dtype):
+    h, w, t, g = _case(100, 72, 300, dtype, ignore=0.3, seed=7)
+    wide = torch.full((100, 96), math.nan, dtype=dtype, device="cuda")
+    wide[:, 8:80] = h.cuda()
+    ws = torch.empty(zo.zo_head_grad_workspace_bytes(400, 72, 300, dtype), dtype=torch.uint8, device="cuda")
+    got = _check(ctx, h, w, t, g, dtype, x=wide[:, 8:80], workspace=ws)
+    d = [v.cuda() for v in (h, w, t, g)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    other = zo.zo_head_grad(ctx, d[0], d[1], d[2], row_grad=d[3], stream=side)
+    side.synchronize()
+    for a, b in zip(got, other):
+        assert torch.equal(a, b)
+    out = zo.HeadGrad(*(torch.empty_like(v) for v in got))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        zo.zo_head_grad(ctx, d[0], d[1], d[2], row_grad=d[3], workspace=ws, out=out)
+    for seed in range(3):
+        n = _case(100, 72, 300, dtype, ignore=0.2 + 0.3 * seed, seed=40 + seed)
+        d[0].copy_(n[0])
+        d[2].copy_(n[2])
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = zo.zo_head_grad(ctx, d[0], d[1], d[2], row_grad=d[3])
+        for a, b in zip(out, eager):
+            assert torch.equal(a, b)
+
+
+def test_no_rows_and_refusals(ctx):
+    w = torch.ones(40, 16, device="cuda")
+    none = zo.zo_head_grad(ctx, torch.zeros(0, 16, device="cuda"), w, torch.zeros(0, dtype=torch.int64, device="cuda"))
+    assert none.logp.shape == (0,) and not none.weight_grad.any()
+    h, t = torch.zeros(3, 16, device="cuda"), torch.zeros(3, dtype=torch.int64, device="cuda")
+    with pytest.raises(ValueError):
+        zo.zo_head_grad(ctx, h, w[:, :8].contiguous(), t)
+    with pytest.raises(ValueError):
+        zo.zo_head_grad(ctx, h, w, None)
+    with pytest.raises(ValueError):
+        zo.zo_head_grad(ctx, h, w, t, out=zo.HeadGrad(torch.empty(3, device="cuda"), h[:2], None))
+    with pytest.raises(TypeError):
+        zo.zo_head_grad(ctx, h, w.bfloat16(), t)
+    with pytest.raises(zo.ZOError):
+        zo.zo_head_grad(ctx, torch.zeros(3, 12, device="cuda"), torch.zeros(5, 12, device="cuda"), t)
+    with pytest.raises(zo.ZOError):
+        zo.zo_head_grad(ctx, h, w, t, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))

@@ -157,6 +157,8 @@ __global__ __launch_bounds__(256) void k_unpack(const u32x4 *codes, const typena
 
 // ---- few rows ---------------------------------------------------------------------------
 
+constexpr uint32_t kAndOr = 0xEA;                   // (a & b) | c
+
 // Codes as operands, exactly: bf16 kOffset + q (seven bits behind the leading one hold 128 + q),
 // fp32 q.
 struct CodesBf16 {
@@ -167,10 +169,15 @@ struct CodesBf16 {
     {
         u32x4 f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = (w >> (4 * i) & 0x000F000Fu) | 0x43004300u;
+        for (int i = 0; i < 4; ++i) f[i] = ZO_BITOP3(w >> (4 * i), 0x000F000Fu, 0x43004300u, kAndOr);
         return f;
     }
-    static __device__ __forceinline__ u32x4 ones() { return u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}; }
+    // All ones, or all -(128 + 8).
+    static __device__ __forceinline__ u32x4 all(bool one)
+    {
+        const uint32_t w = one ? 0x3F803F80u : 0xC308C308u;
+        return u32x4{w, w, w, w};
+    }
 };
 struct CodesFp32 {
     typedef Fp32 T;
@@ -183,10 +190,10 @@ struct CodesFp32 {
         for (int i = 0; i < 4; ++i) f[i] = __float_as_uint((float)(w >> code_shift(4 * h + i) & 15u));
         return f;
     }
-    static __device__ __forceinline__ u32x4 ones()
+    static __device__ __forceinline__ u32x4 all(bool one)
     {
-        const uint32_t o = __float_as_uint(1.0f);
-        return u32x4{o, o, o, o};
+        const uint32_t w = __float_as_uint(one ? 1.0f : -8.0f);
+        return u32x4{w, w, w, w};
     }
 };
 
@@ -195,155 +202,262 @@ struct Q4Args {
     uint32_t d_in, d_out, blocks;                   // blocks along k
 };
 
-// Few rows.  What bounds the product is reading the codes once: a workgroup takes 16 kMF features
-// and all rows, four waves take every fourth block of k, and their sums meet in LDS; kMR more waves
-// form the adapters' products meanwhile, add everything up and end 16 rows each (as k_few).
-// Codes go straight to registers, a block a load; x through LDS.  A group's sum of products with codes is formed apart
-// and enters the row's sum as s (sum x (o + q) - (o + z) sum x), the sums of x by products with
-// ones, so that the weights are not rounded: every product is exact, all sums are fp32.
-constexpr int kQ4Waves = 4;
-template <class T, int kMR>
-constexpr int q4_stages() { return T::kBf16 ? (kMR <= 2 ? 3 : 2) : (kMR == 1 ? 3 : 2); }
-template <class T>
-constexpr int q4_steps() { return kBlockK / (8 * T::kPiece); }
-template <class T, int kMR>
-constexpr uint32_t q4_lds() { return kQ4Waves * q4_stages<T, kMR>() * q4_steps<T>() * kMR * 16 * 128; }
+// Few rows.  What bounds the product is reading the codes once: a workgroup takes 16 kMF kFG
+// features and all rows, its waves being kFG of features times kKG that share the blocks of k among
+// them.  Codes go straight to registers, a block a load, kStages - 1 blocks ahead.  The sums of
+// the shares meet in LDS; before the first block wave (f, g) adds the adapters' products of its
+// features and of the rows g, g + kKG, .. (of 16) to its own.
+//
+// x goes through LDS.  kWhole: all of it before the first block, after which the waves run
+// free of each other; while that is at most kQ4Whole bytes.  Otherwise in steps of a block, which the waves of
+// a share read together.
+//
+// A group's sum of products with codes is formed apart and enters the row's sum as
+// s (sum x (o + q) - (o + z) sum x), so that the weights are not rounded: every product is exact, all
+// sums are fp32.  The sums of x are products with ones; without zero points with -(o + 8), which
+// the products with the codes then start from.  A group's sums are used one group later, so that
+// the products of the next are under way meanwhile.
+template <class T, int kMR, int kMF, int kKG, int kSplit, bool kPoints, bool kWhole>
+constexpr int q4_stages()
+{
+    const int stage = kWhole ? 0 : kKG * kMR * 16 * kBlockK * (T::kBf16 ? 2 : 4);
+    const int held = kMF * (4 + kSplit * (T::kBf16 ? 2 : 4) * (kPoints ? 2 : 1));   // registers
+    return 4 * stage <= 65536 && 4 * held <= 64 ? 4 : 3 * stage <= 98304 && 3 * held <= 80 ? 3 : 2;
+}
+// Bytes of LDS; whole: of a row of x.
+template <class T, int kMR, int kMF, int kFG, int kKG, int kSplit, bool kPoints, bool kWhole>
+uint32_t q4_lds(uint64_t rows, uint32_t whole)
+{
+    const uint32_t x = kWhole ? (uint32_t)rows * whole
+                              : q4_stages<T, kMR, kMF, kKG, kSplit, kPoints, kWhole>() * kKG * kMR * 16 * kBlockK * (T::kBf16 ? 2 : 4);
+    const uint32_t sums = kFG * kKG * kMF * kMR * 1024;
+    return x > sums ? x : sums;
+}
 
-template <class C, int kMR, int kMF, int kSplit, bool kZeros, class End>
-__global__ __launch_bounds__((kQ4Waves + kMR) * 64) void k_q4_few(Q4Args p, const typename C::T::elem *x,
-                                                                  const u32x4 *codes,
-                                                                  const typename C::T::elem *scales,
-                                                                  const typename C::T::elem *zeros, End end)
+// Four neighbouring scales as they are held.
+__device__ __forceinline__ uint2 held4(const uint16_t *p) { return *reinterpret_cast<const uint2 *>(p); }
+__device__ __forceinline__ f32x4 held4(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
+__device__ __forceinline__ f32x4 four(uint2 v)
+{
+    return f32x4{bf16lo_to_f32(v.x), bf16hi_to_f32(v.x), bf16lo_to_f32(v.y), bf16hi_to_f32(v.y)};
+}
+__device__ __forceinline__ f32x4 four(f32x4 v) { return v; }
+
+template <class C, int kMR, int kMF, int kFG, int kKG, int kSplit, bool kPoints, bool kWhole, class End>
+__global__ __launch_bounds__(kFG * kKG * 64) void k_q4_few(Q4Args p, const typename C::T::elem *x,
+                                                           const u32x4 *codes,
+                                                           const typename C::T::elem *scales,
+                                                           const typename C::T::elem *zeros, End end)
 {
     typedef typename C::T T;
-    constexpr int kStages = q4_stages<T, kMR>(), kSteps = q4_steps<T>(), kC = 4 / kSplit;
-    typedef Feed<T, kMR, kStages * kSteps> F;
-    static_assert(F::kStep * kSteps == kBlockK, "whole steps of x in a block");
-    static_assert(kMF * kMR * 1024 * kQ4Waves <= (int)q4_lds<T, kMR>(), "the sums fit");
-    extern __shared__ u32x4 stage[];                // [wave][stage][step][rows], then [wave] of sums
-    const int lane = threadIdx.x & 63, q = lane >> 4;
+    constexpr int kStages = q4_stages<T, kMR, kMF, kKG, kSplit, kPoints, kWhole>(), kC = 4 / kSplit;
+    constexpr bool kLate = kMR <= 2 && !kPoints && kFG * kKG <= 8;   // else registers are short
+    constexpr int kSteps = kBlockK / (8 * T::kPiece);       // of 128 bytes of x in a block
+    constexpr int kStep = kMR * 16 * 8;                     // pieces of such a step
+    constexpr int kFeeds = 2 * kMR * kSteps;                // loads of 1024 bytes of x in a block
+    constexpr int kFeed = kWhole ? 0 : kFeeds / kFG;        // of these, a wave's
+    static_assert(kWhole || kFeeds % kFG == 0, "the waves of a share load equal parts of x");
+    static_assert(!kWhole || kMR == 1, "at most 16 rows");
+    extern __shared__ u32x4 stage[];                        // [stage][share][step][rows][8], or x; then the sums
+    const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t f0 = blockIdx.x * (16 * kMF);
-    f32x4 *sums = reinterpret_cast<f32x4 *>(stage);
-    if (wave >= kQ4Waves) {
-        const int n = wave - kQ4Waves;
-        Tile<kMF, 1> own;
-        own.clear();
-        end.add_rows(own, 0, f0, 16 * n);
-        __syncthreads();                            // the stages are free
-        __syncthreads();                            // the sums are there
+    const int fg = wave % kFG, kg = wave / kFG;
+    const uint32_t f0 = (blockIdx.x * kFG + fg) * (16 * kMF);
+    // this wave's part of x: load i is step i / (2 kMR), eight rows i % (2 kMR); pieces placed as in Feed
+    const typename T::elem *src[kFeed ? kFeed : 1];
+    uint32_t piece[kFeed ? kFeed : 1];
 #pragma unroll
-        for (int m = 0; m < kMF; ++m)
-#pragma unroll
-            for (int v = 0; v < kQ4Waves; ++v) own.acc[m][0] += sums[((v * kMF + m) * kMR + n) * 64 + lane];
-        end.store(own, f0, 16 * n);
-        return;
+    for (int j = 0; j < kFeed; ++j) {
+        const int i = fg * kFeed + j, r = i % (2 * kMR) * 8 + (lane >> 3);
+        piece[j] = (uint32_t)(i / (2 * kMR) * 8 + ((lane & 7) ^ (r >> 1 & 7))) * T::kPiece;
+        src[j] = x + ((uint64_t)r < p.rows ? r : p.rows - 1) * p.x_stride;
     }
-    const F feed(stage + wave * kStages * kSteps * F::kStage, p.d_in, [&](int i) {
-        const uint64_t r = (uint64_t)i < p.rows ? i : p.rows - 1;
-        return x + r * p.x_stride;
-    });
-    Tile<kMF, kMR> t;
-    t.clear();
-    u32x4 word[kStages][kMF];
-    f32x4 s[kStages][kMF][kSplit], z[kStages][kMF][kSplit];
-    // features and groups past the last read the last: nothing of theirs is kept
+    // features past the last read the last: nothing of theirs is kept
     const uint32_t groups = (p.d_in + kC * 32 - 1) / (kC * 32);
     const u32x4 *from[kMF];
     uint32_t of[kMF];
 #pragma unroll
     for (int m = 0; m < kMF; ++m) {
-        const uint32_t f = f0 + 16 * m < p.d_out ? f0 + 16 * m : f0;
+        const uint32_t f = f0 + 16 * m < p.d_out ? f0 + 16 * m : (p.d_out - 1) / 16 * 16;
         from[m] = codes + (uint64_t)(f / 16) * p.blocks * 64 + lane;
         of[m] = f + 4 * q < p.d_out ? f + 4 * q : f;
     }
-    const auto issue = [&](uint32_t b, int slot) {
+    // Each workgroup begins elsewhere in k, off the others' memory channels.
+    const uint32_t turn = (blockIdx.x * 0x9E3779B1u >> 8) % p.blocks;
+    const uint32_t steps = (p.blocks + kKG - 1) / kKG;
+    // The block of a step; past the share's last, any.
+    const auto block_of = [&](uint32_t step) {
+        uint32_t b = step * kKG + kg + turn;
+        b = b >= p.blocks ? b - p.blocks : b;
+        return b >= p.blocks ? 0 : b;
+    };
+    u32x4 word[kStages][kMF];
+    decltype(held4(scales)) s[kStages][kMF][kSplit], z[kStages][kMF][kSplit];
+    const auto issue = [&](uint32_t step, int slot) {
+        const uint32_t b = block_of(step);
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) feed.issue(b * kSteps + i, slot * kSteps + i);
-        const uint32_t at = b < p.blocks ? b : p.blocks - 1;
+        for (int j = 0; j < kFeed; ++j) {
+            // past the end of k any values: their group is left out
+            const uint32_t k = b * kBlockK + piece[j];
+            const typename T::elem *g = src[j] + (k < p.d_in ? k : 0);
+            u32x4 *l = stage + ((slot * kKG + kg) * kFeeds + fg * kFeed + j) * 64;
+            __builtin_amdgcn_global_load_lds((gptr_t)g, (lptr_t)l, 16, 0, 0);
+        }
 #pragma unroll
         for (int m = 0; m < kMF; ++m) {
-            word[slot][m] = from[m][(uint64_t)at * 64];
+            word[slot][m] = from[m][(uint64_t)b * 64];
 #pragma unroll
             for (int g = 0; g < kSplit; ++g) {
-                const uint32_t group = at * kSplit + g < groups ? at * kSplit + g : groups - 1;
-                float v[4];
-                T::load4(scales + (uint64_t)group * p.d_out + of[m], v);
-                s[slot][m][g] = f32x4{v[0], v[1], v[2], v[3]};
-                if constexpr (kZeros) {
-                    T::load4(zeros + (uint64_t)group * p.d_out + of[m], v);
-                    z[slot][m][g] = f32x4{v[0], v[1], v[2], v[3]};
-                }
+                const uint32_t group = kSplit == 1 || b * kSplit + g < groups ? b * kSplit + g : groups - 1;
+                s[slot][m][g] = held4(scales + (uint64_t)group * p.d_out + of[m]);
+                if constexpr (kPoints) z[slot][m][g] = held4(zeros + (uint64_t)group * p.d_out + of[m]);
             }
         }
-        asm volatile("" ::: "memory");              // a wait counts whole blocks' loads
+        asm volatile("" ::: "memory");                      // a wait counts whole blocks' loads
     };
-    constexpr int kLoads = F::kLoads * kSteps + kMF * (1 + kSplit * (kZeros ? 2 : 1));
+    // the loads of a block that are surely apart: a wait for fewer is none too short
+    constexpr int kLoads = kFeed + kMF;
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue(wave + i * kQ4Waves, i);
-    for (uint32_t b0 = wave; b0 < p.blocks; b0 += kQ4Waves * kStages) {
+    for (int i = 0; i < kStages - 1; ++i) issue(i, i);
+    const uint32_t pitch = p.d_in / T::kPiece + 1;          // of a whole row of x, in pieces: banks
+    if constexpr (kWhole) {
+        for (uint32_t r = 0; r < p.rows; ++r)
+            for (uint32_t i = threadIdx.x; i < p.d_in / T::kPiece; i += kFG * kKG * 64)
+                stage[r * pitch + i] = piece_at<T>(x + r * p.x_stride + i * T::kPiece);
+        __syncthreads();
+    }
+    const uint32_t own_row = ((uint32_t)l16 < p.rows ? l16 : (uint32_t)p.rows - 1) * pitch;
+    Tile<kMF, kMR> t;
+    t.clear();
 #pragma unroll
-        for (int u = 0; u < kStages; ++u) {
-            const uint32_t b = b0 + u * kQ4Waves;
-            wait_for<kLoads * (kStages - 2), true>();
-            asm volatile("" ::: "memory");
-            issue(b + (kStages - 1) * kQ4Waves, (u + kStages - 1) % kStages);
+    for (int n = 0; n < kMR; ++n)
+        if (n % kKG == kg) end.add_rows(t, n, f0, 16 * n);
+    struct Sums {
+        f32x4 part[kMF][kMR], sum[kMR], by[kMF], zero[kMF];
+    };
+    Sums last = {};
+    const auto add = [&](const Sums &g) {
 #pragma unroll
-            for (int g = 0; g < kSplit; ++g) {
-                f32x4 part[kMF][kMR], sum[kMR];
+        for (int m = 0; m < kMF; ++m)
 #pragma unroll
-                for (int n = 0; n < kMR; ++n) {
-                    sum[n] = f32x4{0, 0, 0, 0};
+            for (int n = 0; n < kMR; ++n)
 #pragma unroll
-                    for (int m = 0; m < kMF; ++m) part[m][n] = f32x4{0, 0, 0, 0};
+                for (int i = 0; i < 4; ++i) {
+                    float v = g.part[m][n][i];
+                    if constexpr (kPoints) v = fmaf(-(C::kOffset + g.zero[m][i]), g.sum[n][i], v);
+                    t.acc[m][n][i] = fmaf(g.by[m][i], v, t.acc[m][n][i]);
                 }
+    };
+    const auto use = [&](uint32_t step, int u) {
+        if (step * kKG + kg >= p.blocks) return;
+        const uint32_t b = block_of(step);
+        const u32x4 *own = stage + (u * kKG + kg) * kFeeds * 64;
 #pragma unroll
-                for (int c = g * kC; c < (g + 1) * kC; ++c)
+        for (int g = 0; g < kSplit; ++g) {
+            if (kSplit > 1 && b * kSplit + g >= groups) break;
+            u32x4 fx[kC][C::kParts][kMR];
 #pragma unroll
-                    for (int h = 0; h < C::kParts; ++h) {
-                        // values 32 c + 8 q + 4 h .. of the block: bf16 fragment c % 2 of step
-                        // c / 2; fp32 pieces 2 q + h of step c
-                        u32x4 fx[kMR];
+            for (int c = 0; c < kC; ++c)
 #pragma unroll
-                        for (int n = 0; n < kMR; ++n) {
-                            if constexpr (T::kBf16) {
-                                fx[n] = feed.fragment(u * kSteps + c / 2, n, c % 2);
-                            } else {
-                                const int l16 = lane & 15;
-                                fx[n] = feed.lds[(u * kSteps + c) * F::kStage + (n * 16 + l16) * F::kPieces +
-                                                 ((2 * q + h) ^ (l16 >> 1))];
-                            }
-                            sum[n] = T::mma(C::ones(), fx[n], sum[n]);
-                        }
+                for (int h = 0; h < C::kParts; ++h) {
+                    // values 32 k + 8 q + 4 h .. of the block: bf16 piece 4 (k % 2) + q of
+                    // step k / 2, fp32 piece 2 q + h of step k
+                    const int k = g * kC + c, step_of = T::kBf16 ? k / 2 : k, at = T::kBf16 ? 4 * (k & 1) + q : 2 * q + h;
 #pragma unroll
-                        for (int m = 0; m < kMF; ++m) {
-                            const u32x4 fw = C::part(word[u][m][c], h);
+                    for (int n = 0; n < kMR; ++n) {
+                        if constexpr (kWhole) fx[c][h][n] = stage[own_row + b * (kBlockK / T::kPiece) + step_of * 8 + at];
+                        else fx[c][h][n] = own[step_of * kStep + (n * 16 + l16) * 8 + (at ^ (l16 >> 1))];
+                    }
+                }
+            Sums now;
 #pragma unroll
-                            for (int n = 0; n < kMR; ++n) part[m][n] = T::mma(fw, fx[n], part[m][n]);
-                        }
+            for (int n = 0; n < kMR; ++n) {
+                now.sum[n] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int c = 0; c < kC; ++c)
+#pragma unroll
+                    for (int h = 0; h < C::kParts; ++h) now.sum[n] = T::mma(C::all(kPoints), fx[c][h][n], now.sum[n]);
+            }
+#pragma unroll
+            for (int m = 0; m < kMF; ++m)
+#pragma unroll
+                for (int n = 0; n < kMR; ++n) now.part[m][n] = kPoints ? f32x4{0, 0, 0, 0} : now.sum[n];
+#pragma unroll
+            for (int c = 0; c < kC; ++c)
+#pragma unroll
+                for (int h = 0; h < C::kParts; ++h)
+#pragma unroll
+                    for (int m = 0; m < kMF; ++m) {
+                        const u32x4 fw = C::part(word[u][m][g * kC + c], h);
+#pragma unroll
+                        for (int n = 0; n < kMR; ++n) now.part[m][n] = T::mma(fw, fx[c][h][n], now.part[m][n]);
                     }
 #pragma unroll
-                for (int m = 0; m < kMF; ++m)
-#pragma unroll
-                    for (int n = 0; n < kMR; ++n)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float zero = C::kOffset + (kZeros ? z[u][m][g][i] : 8.0f);
-                            t.acc[m][n][i] = fmaf(s[u][m][g][i], fmaf(-zero, sum[n][i], part[m][n][i]), t.acc[m][n][i]);
-                        }
+            for (int m = 0; m < kMF; ++m) {
+                now.by[m] = four(s[u][m][g]);
+                now.zero[m] = kPoints ? four(z[u][m][g]) : f32x4{0, 0, 0, 0};
+            }
+            if constexpr (kLate) {
+                add(last);
+                last = now;
+            } else {
+                add(now);
             }
         }
+    };
+    const auto ready = [&](auto behind) {
+        if constexpr (kWhole) return;
+        wait_for<kLoads * decltype(behind)::value, true>();
+        turn_barrier();                                     // the share's; the last step's readers are done
+    };
+    // whole rounds of the stages, and the rest apart, so that no path joins the loop with loads of
+    // other registers under way
+    uint32_t s0 = 0;
+    for (; s0 + kStages <= steps; s0 += kStages) {
+#pragma unroll
+        for (int u = 0; u < kStages; ++u) {
+            ready(std::integral_constant<int, kStages - 2>());
+            issue(s0 + u + kStages - 1, (u + kStages - 1) % kStages);
+            use(s0 + u, u);
+        }
     }
+#pragma unroll
+    for (int u = 0; u < kStages - 1; ++u)
+        if (s0 + u < steps) {
+            ready(std::integral_constant<int, 0>());
+            use(s0 + u, u);
+        }
+    if constexpr (kLate) add(last);
     wait_for<0, true>();
     __syncthreads();
+    f32x4 *sums = reinterpret_cast<f32x4 *>(stage);         // [share][features][m][n]
 #pragma unroll
     for (int m = 0; m < kMF; ++m)
 #pragma unroll
-        for (int n = 0; n < kMR; ++n) sums[((wave * kMF + m) * kMR + n) * 64 + lane] = t.acc[m][n];
+        for (int n = 0; n < kMR; ++n)
+            if (n % kKG != kg) sums[(((kg * kFG + fg) * kMF + m) * kMR + n) * 64 + lane] = t.acc[m][n];
     __syncthreads();
+#pragma unroll
+    for (int n = 0; n < kMR; ++n) {
+        if (n % kKG != kg) continue;
+        Tile<kMF, 1> own;
+#pragma unroll
+        for (int m = 0; m < kMF; ++m) {
+            own.acc[m][0] = t.acc[m][n];
+#pragma unroll
+            for (int v = 1; v < kKG; ++v)                   // the shares after this one, in turn
+                own.acc[m][0] += sums[((((kg + v) % kKG * kFG + fg) * kMF + m) * kMR + n) * 64 + lane];
+        }
+        end.store(own, f0, 16 * n);
+    }
 }
 
 // ---- launches ---------------------------------------------------------------------------
+
+// Most bytes of x that a workgroup holds whole.
+constexpr uint64_t kQ4Whole = 65536;
+template <class T>
+uint32_t whole_row(uint32_t d_in) { return (d_in / T::kPiece + 1) * 16; }
 
 uint32_t block_grid(uint32_t d_out, uint32_t d_in)
 {
@@ -351,48 +465,84 @@ uint32_t block_grid(uint32_t d_out, uint32_t d_in)
     return (uint32_t)((blocks + 3) / 4);
 }
 
-template <class C, int kMR, int kMF>
+struct Q4Call {
+    uint64_t rows;
+    uint32_t d_in, d_out, group;
+    bool zeros;
+};
+
+// f(kernel, features of a workgroup, threads, bytes of LDS) for the kernel that a call takes.
+template <class C, class F>
+void q4_kernel(const Q4Call &a, F f)
+{
+    typedef typename C::T T;
+    const uint32_t row = whole_row<T>(a.d_in);
+    const auto sized = [&](auto kMR, auto kMF, auto kFG, auto kKG, auto kWhole) {
+        constexpr int R = decltype(kMR)::value, M = decltype(kMF)::value, G = decltype(kFG)::value, K = decltype(kKG)::value;
+        constexpr bool W = decltype(kWhole)::value;
+        const auto split = [&](auto kSplit) {
+            constexpr int S = decltype(kSplit)::value;
+            if (a.zeros)
+                f(&k_q4_few<C, R, M, G, K, S, true, W, EndProject<T>>, 16 * M * G, G * K * 64, q4_lds<T, R, M, G, K, S, true, W>(a.rows, row));
+            else
+                f(&k_q4_few<C, R, M, G, K, S, false, W, EndProject<T>>, 16 * M * G, G * K * 64, q4_lds<T, R, M, G, K, S, false, W>(a.rows, row));
+        };
+        a.group == 128 ? split(std::integral_constant<int, 1>()) : a.group == 64 ? split(std::integral_constant<int, 2>())
+                                                                                 : split(std::integral_constant<int, 4>());
+    };
+    const std::integral_constant<int, 1> one;
+    const std::integral_constant<int, 2> two;
+    const std::integral_constant<int, 4> four;
+    const std::integral_constant<int, 8> eight;
+    const std::true_type whole;
+    const std::false_type steps;
+    // workgroups of 128 features where these are enough for the CUs
+    const bool wide = a.d_out >= 128u * 160;
+    if (a.rows <= 16 && a.rows * row <= kQ4Whole)
+        wide ? sized(one, one, two, four, whole) : sized(one, one, one, eight, whole);
+    else if (a.rows <= 16)
+        wide ? sized(one, two, four, two, steps) : sized(one, one, two, eight, steps);
+    else if (a.rows <= 32) {
+        const std::integral_constant<int, T::kBf16 ? 8 : 4> most;   // shares whose steps of x fit into LDS
+        wide ? sized(two, two, four, two, steps) : sized(two, one, two, most, steps);
+    }
+    else if constexpr (T::kBf16)
+        wide ? sized(four, two, four, two, steps) : sized(four, one, two, four, steps);
+}
+
+template <class C>
 hipError_t few_q4(const AdapterArgs &a, const Q4Weights &w, const void *x, uint64_t x_stride, const void *bias,
                   const void *adapters, float *u, void *y, uint64_t y_stride, hipStream_t stream)
 {
     typedef typename C::T T;
     typedef typename T::elem E;
+    const Q4Args p = {a.rows, x_stride, a.d_in, a.d_out, (a.d_in + kBlockK - 1) / kBlockK};
     const EndProject<T> end = {a, u, reinterpret_cast<int32_t *>(u + a.rows * a.rank), static_cast<const E *>(adapters),
                                static_cast<const E *>(bias), static_cast<E *>(y), y_stride};
-    const Q4Args p = {a.rows, x_stride, a.d_in, a.d_out, (a.d_in + kBlockK - 1) / kBlockK};
-    const auto launch = [&](auto split, auto zeros) {
-        k_q4_few<C, kMR, kMF, decltype(split)::value, decltype(zeros)::value, EndProject<T>>
-            <<<(a.d_out + 16 * kMF - 1) / (16 * kMF), (kQ4Waves + kMR) * 64, q4_lds<T, kMR>(), stream>>>(
-                p, static_cast<const E *>(x), static_cast<const u32x4 *>(w.codes), static_cast<const E *>(w.scales),
-                static_cast<const E *>(w.zeros), end);
-    };
-    const auto sized = [&](auto zeros) {
-        if (w.group == 128) launch(std::integral_constant<int, 1>(), zeros);
-        else if (w.group == 64) launch(std::integral_constant<int, 2>(), zeros);
-        else launch(std::integral_constant<int, 4>(), zeros);
-    };
-    w.zeros ? sized(std::true_type()) : sized(std::false_type());
+    q4_kernel<C>({a.rows, a.d_in, a.d_out, w.group, w.zeros != nullptr},
+                 [&](auto *kernel, uint32_t features, uint32_t threads, uint32_t lds) {
+        kernel<<<(a.d_out + features - 1) / features, threads, lds, stream>>>(
+            p, static_cast<const E *>(x), static_cast<const u32x4 *>(w.codes), static_cast<const E *>(w.scales),
+            static_cast<const E *>(w.zeros), end);
+    });
     return hipGetLastError();
 }
 
-template <class C, int kMR, int kMF>
+// Raises the LDS limit of every kernel that a call may take.
+template <class C>
 hipError_t prepare_few()
 {
-    typedef typename C::T T;
     hipError_t e = hipSuccess;
-    const auto raise = [&](auto split, auto zeros) {
-        if (e == hipSuccess)
-            e = hipFuncSetAttribute(reinterpret_cast<const void *>(
-                                        &k_q4_few<C, kMR, kMF, decltype(split)::value, decltype(zeros)::value, EndProject<T>>),
-                                    hipFuncAttributeMaxDynamicSharedMemorySize, q4_lds<T, kMR>());
-    };
-    const auto both = [&](auto split) {
-        raise(split, std::true_type());
-        raise(split, std::false_type());
-    };
-    both(std::integral_constant<int, 1>());
-    both(std::integral_constant<int, 2>());
-    both(std::integral_constant<int, 4>());
+    for (const uint64_t rows : {1, 16, 32, 64})
+        for (const uint32_t d_in : {128u, 1u << 20})
+            for (const uint32_t d_out : {8u, 1u << 20})
+                for (const uint32_t group : {32, 64, 128})
+                    for (const bool zeros : {false, true})
+                        q4_kernel<C>({rows, d_in, d_out, group, zeros}, [&](auto *kernel, uint32_t, uint32_t, uint32_t lds) {
+                            if (e == hipSuccess)
+                                e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                                        lds > kQ4Whole ? lds : kQ4Whole);
+                        });
     return e;
 }
 
@@ -400,11 +550,8 @@ hipError_t prepare_few()
 
 hipError_t prepare_q4()
 {
-    const hipError_t all[] = {prepare_few<CodesBf16, 1, 2>(), prepare_few<CodesBf16, 2, 2>(), prepare_few<CodesBf16, 3, 2>(),
-                              prepare_few<CodesBf16, 4, 2>(), prepare_few<CodesFp32, 1, 2>(), prepare_few<CodesFp32, 2, 2>()};
-    for (const hipError_t e : all)
-        if (e != hipSuccess) return e;
-    return hipSuccess;
+    const hipError_t e = prepare_few<CodesBf16>();
+    return e == hipSuccess ? prepare_few<CodesFp32>() : e;
 }
 
 hipError_t launch_q4_quantize(const void *w, uint64_t stride, bool bf16, uint32_t d_out, uint32_t d_in, uint32_t group,
@@ -456,15 +603,8 @@ hipError_t launch_q4_project(const AdapterArgs &a, bool bf16, const void *x, uin
     }
     const hipError_t e = launch_adapter_shrink(a, bf16, x, x_stride, adapters, u, stream);
     if (e != hipSuccess) return e;
-    const auto few = [&](auto codes, auto rows) {
-        return few_q4<decltype(codes), decltype(rows)::value, 2>(a, w, x, x_stride, bias, adapters, u, y, y_stride, stream);
-    };
-    const std::integral_constant<int, 1> one;
-    const std::integral_constant<int, 2> two;
-    if (!bf16) return a.rows <= 16 ? few(CodesFp32(), one) : few(CodesFp32(), two);
-    if (a.rows <= 16) return few(CodesBf16(), one);
-    if (a.rows <= 32) return few(CodesBf16(), two);
-    return a.rows <= 48 ? few(CodesBf16(), std::integral_constant<int, 3>()) : few(CodesBf16(), std::integral_constant<int, 4>());
+    return bf16 ? few_q4<CodesBf16>(a, w, x, x_stride, bias, adapters, u, y, y_stride, stream)
+                : few_q4<CodesFp32>(a, w, x, x_stride, bias, adapters, u, y, y_stride, stream);
 }
 
 }  // namespace zo

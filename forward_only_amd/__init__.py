@@ -802,8 +802,8 @@ def zo_head_grad(ctx: Context, hidden: torch.Tensor, weight: torch.Tensor, targe
                  stream=None) -> HeadGrad:
     """Log probabilities of the targets from hidden [rows, d] and weight [vocab, d], as
     zo_head_logprobs, with the gradients of -sum(row_grad * logp) (row_grad float32 [rows]; None:
-    ones) with respect to both, in their dtype; the logits are never stored.  Rows with the
-    target ZO_IGNORE_TOKEN give 0 and take no part.  workspace: at least
+    ones) with respect to both, in their dtype; logits are held for a piece of the rows at a
+    time, in the workspace.  Rows with the target ZO_IGNORE_TOKEN give 0 and take no part.  workspace: at least
     zo_head_grad_workspace_bytes of the largest batch that it serves; out: tensors of an earlier call."""
     hp, rows, d, stride = _matrix(hidden, "hidden")
     dev = hidden.get_device()

@@ -888,7 +888,8 @@ zo_status zo_head_grad(zo_ctx *c, const void *d_hidden, uint64_t hidden_stride, 
 {
     if (!ctx_ok(c)) return ZO_EINVAL;
     if (dtype != ZO_FP32 && dtype != ZO_BF16) return ZO_EINVAL;
-    if (rows > kMaxProjectRows || vocab > kMaxFeatures || d > kMaxGradWidth || rows * d > kMaxProjected)
+    if (rows > kMaxProjectRows || vocab > kMaxFeatures || d > kMaxGradWidth || rows * d > kMaxProjected ||
+        (uint64_t)vocab * d > kMaxProjected)
         return ZO_EUNSUPPORTED;
     if (vocab == 0 || d == 0 || d % 8u || hidden_stride % 8u) return ZO_EINVAL;
     if (!aligned16(d_hidden_grad) || !aligned16(d_weight_grad)) return ZO_EINVAL;

@@ -3,25 +3,32 @@
 //
 //   l = h W^T,  p = softmax(l),  D[r][v] = g_r (p[r][v] - [v = t_r]),  dh = D W,  dW = D^T h
 //
-// The logits are formed twice and never stored: once for each row's largest and sum
-// (zo_head_logprobs), and, when these are known, once more in pieces of the features, of which D
-// is left, rounded to the type, as it is and turned over.  Each piece then adds to dh, in fp32, and
-// gives its rows of dW.  Rows that do not count are left out: the others stand one after
-// another in the workspace, as they are and turned over.  All four products take their operands
-// along the neighbouring values that they sum over, so the pieces of W are turned over, too.
+// Rows that do not count are left out: the others stand one after another in the workspace. They are
+// taken in pieces of at most kGradLogits logits, which stand there in fp32 while a piece is worked on:
+// forming them a second time would cost a fourth product of three (4096 rows, bf16 7168 to 50272: 9.4
+// ms in all, the products 2.05 each).  With each row's largest and sum known, they become
+// p - [v = t], rounded to the type, as it is for dh (g enters behind the product, in fp32) and times
+// g, turned over, for dW.  The products take their operands along the neighbouring values that they
+// sum over, so h and W are turned over, too.  Pieces after the first add to dW in fp32.
+//
+// Few rows: reading W twice and writing dW bounds it (k_outer).
 #include "zo_product.hpp"
 
 namespace zo {
 namespace {
 
+// How many of the counted rows are in each piece.
+__global__ void k_pieces(const uint32_t *count, uint64_t piece, uint32_t pieces, uint32_t *counts)
+{
+    for (uint32_t i = threadIdx.x; i < pieces; i += 256) counts[i] = (uint32_t)places(i * piece, piece, count);
+}
+
 // y[c][r] = x[row(r)][c] for `rows` places r (as many as *count, if given) and `cols` columns c, zeros
-// from there to the next multiple of 8 places; kCopy: also copy[r] = x[row(r)].  y's rows lie
-// `pitch` apart, a multiple of 8.  A workgroup takes 64 x 64 values through LDS.  What bounds it is
-// reading and writing them.
-template <class T, bool kCopy>
+// from there to the next multiple of 8 places.  y's rows lie `pitch` apart, a multiple of 8.  A
+// workgroup takes 64 x 64 values through LDS.  What bounds it is reading and writing them.
+template <class T>
 __global__ __launch_bounds__(256) void k_turn(const typename T::elem *x, uint64_t stride, uint64_t rows,
-                                              const uint32_t *count, const uint32_t *list, uint32_t cols,
-                                              typename T::elem *y, uint64_t pitch, typename T::elem *copy)
+                                              const uint32_t *count, uint32_t cols, typename T::elem *y, uint64_t pitch)
 {
     typedef typename T::elem E;
     constexpr int kPiece = T::kPiece, kRowPieces = 64 / kPiece, kPitch = 64 + 4 / (int)sizeof(E);
@@ -34,11 +41,7 @@ __global__ __launch_bounds__(256) void k_turn(const typename T::elem *x, uint64_
     for (int i = threadIdx.x; i < 64 * kRowPieces; i += 256) {
         const int r = i / kRowPieces, c = i % kRowPieces * kPiece;
         u32x4 v = {0, 0, 0, 0};
-        if (r0 + r < have && c0 + c < cols) {
-            const uint64_t row = list ? list[r0 + r] : r0 + r;
-            v = piece_at<T>(x + row * stride + c0 + c);
-            if constexpr (kCopy) *reinterpret_cast<u32x4 *>(copy + (r0 + r) * cols + c0 + c) = v;
-        }
+        if (r0 + r < have && c0 + c < cols) v = piece_at<T>(x + (r0 + r) * stride + c0 + c);
         const E *e = reinterpret_cast<const E *>(&v);
 #pragma unroll
         for (int j = 0; j < kPiece; ++j) tile[r * kPitch + c + j] = e[j];
@@ -56,76 +59,26 @@ __global__ __launch_bounds__(256) void k_turn(const typename T::elem *x, uint64_
     }
 }
 
-// The ending that leaves D of a piece of the features, rounded to the type: d [place][pitch_d] with
-// zeros behind the features, dt [feature][pitch_t] with zeros from the last place to the next multiple of 8.
-// Either may be nullptr.
+// The rows that count, one after another.
 template <class T>
-struct EndGrad {
-    static constexpr bool kSlices = false;
-    typedef typename T::elem E;
-    uint32_t first, features;      // of this piece
-    uint64_t rows;
-    const int64_t *targets;
-    const uint32_t *list, *count;
-    const float2 *norms;
-    const float *row_grad;
-    E *d, *dt;
-    uint64_t pitch_d, pitch_t;
-
-    template <class Tl>
-    __device__ __forceinline__ void add_rows(Tl &, int, uint32_t, uint64_t) const {}
-    __device__ __forceinline__ uint32_t begin(uint64_t) const { return 0; }
-    template <class Tl>
-    __device__ __forceinline__ void finish(Tl &tile, uint32_t, uint32_t f0, uint64_t r0, u32x4 *) const
-    {
-        store(tile, f0, r0);
+__global__ __launch_bounds__(256) void k_gather(const typename T::elem *x, uint64_t stride, uint64_t rows,
+                                                const uint32_t *count, const uint32_t *list, uint32_t d,
+                                                typename T::elem *out)
+{
+    const uint64_t have = places(0, rows, count);
+    for (uint64_t at = blockIdx.x; at < have; at += gridDim.x) {
+        const typename T::elem *from = x + (uint64_t)list[at] * stride;
+        for (uint32_t i = threadIdx.x; i < d / T::kPiece; i += 256)
+            reinterpret_cast<u32x4 *>(out + at * d)[i] = piece_at<T>(from + i * T::kPiece);
     }
-    static __device__ __forceinline__ void store1(float *p, float v) { *p = v; }
-    static __device__ __forceinline__ void store1(uint16_t *p, float v) { *p = (uint16_t)pack_bf16x2(v, 0.0f); }
+}
 
-    template <class Tl>
-    __device__ __forceinline__ void store(Tl &tile, uint32_t f0, uint64_t r0) const
-    {
-        constexpr int kMF = Tl::kMF, kMR = Tl::kMR;
-        const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
-        const uint64_t have = places(0, rows, count), padded = (have + 7) / 8 * 8;
-#pragma unroll
-        for (int n = 0; n < kMR; ++n) {
-            const uint64_t at = r0 + 16 * n + l16;
-            if (at >= padded) continue;
-            const bool in = at < have;
-            const uint64_t row = in ? list[at] : 0;
-            const float2 norm = in ? norms[at] : make_float2(0.0f, 0.0f);
-            const float g = in ? (row_grad ? row_grad[row] : 1.0f) : 0.0f;
-            const int64_t tgt = in ? targets[row] - first : -1;
-#pragma unroll
-            for (int m = 0; m < kMF; ++m) {
-                const uint32_t f = f0 + 16 * m + 4 * q;
-                f32x4 v;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float p = fast_exp((tile.acc[m][n][i] - norm.x) - norm.y);
-                    v[i] = g * (p - (tgt == (int64_t)(f + i) ? 1.0f : 0.0f));
-                    if (!in || f + i >= features) v[i] = 0.0f;
-                }
-                if (d && in && f < pitch_d) EndProject<T>::store4(d + at * pitch_d + f, v);
-                if (dt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (f + i < features) store1(dt + (uint64_t)(f + i) * pitch_t + at, v[i]);
-            }
-        }
-    }
-};
-
-// The ending that adds a piece's part of dh in fp32.
-struct EndSum {
+// The ending that keeps the logits beside their statistics: [place][pitch] fp32.
+struct EndLogits {
     static constexpr bool kSlices = false;
-    uint32_t features;
-    uint64_t rows;
-    const uint32_t *count;
-    float *sum;                    // [place][features]
-    bool more;                     // parts are there already
+    EndHead head;
+    float *logits;
+    uint64_t pitch;
 
     template <class Tl>
     __device__ __forceinline__ void add_rows(Tl &, int, uint32_t, uint64_t) const {}
@@ -139,7 +92,7 @@ struct EndSum {
     __device__ __forceinline__ void store(Tl &tile, uint32_t f0, uint64_t r0) const
     {
         const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
-        const uint64_t have = places(0, rows, count);
+        const uint64_t have = places(head.base, head.rows, head.count);
 #pragma unroll
         for (int n = 0; n < Tl::kMR; ++n) {
             const uint64_t at = r0 + 16 * n + l16;
@@ -147,33 +100,196 @@ struct EndSum {
 #pragma unroll
             for (int m = 0; m < Tl::kMF; ++m) {
                 const uint32_t f = f0 + 16 * m + 4 * q;
+                if (f < pitch) *reinterpret_cast<f32x4 *>(logits + at * pitch + f) = tile.acc[m][n];
+            }
+        }
+        head.store(tile, f0, r0);
+    }
+};
+
+struct RowsOf {
+    const int64_t *targets;
+    const uint32_t *list, *count;  // of this piece
+    const float2 *norms;
+    const float *row_grad;
+    uint64_t rows;
+    uint32_t features;
+};
+
+// d[r][v] = p - [v = t_r] and dt[v][r] = g_r (p - [v = t_r]) of a piece's places (either may be
+// nullptr), zeros behind the features and from the last place to the next multiple of 8.  A workgroup
+// takes 64 x 64 values, turned over through LDS.  What bounds it is reading 4 and writing 4 bytes a value.
+template <class T>
+__global__ __launch_bounds__(256) void k_shares(const float *logits, RowsOf a, typename T::elem *d, typename T::elem *dt,
+                                                uint64_t pitch_v, uint64_t pitch_x)
+{
+    typedef typename T::elem E;
+    constexpr int kPitch = 64 + 4 / (int)sizeof(E);
+    __shared__ E tile[64 * kPitch];
+    const uint64_t have = places(0, a.rows, a.count), padded = (have + 7) / 8 * 8;
+    const uint64_t r0 = (uint64_t)blockIdx.y * 64;
+    const uint32_t f0 = blockIdx.x * 64;
+    if (r0 >= padded) return;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < 64 * 16; i += 256) {
+        const int r = i / 16, f = i % 16 * 4;
+        const uint64_t at = r0 + r;
+        const bool in = at < have && f0 + f < pitch_v;
+        f32x4 v = {0, 0, 0, 0};
+        float g = 0.0f;
+        if (in) {
+            const uint64_t row = a.list[at];
+            const float2 norm = a.norms[at];
+            const int64_t tgt = a.targets[row] - f0;
+            g = a.row_grad ? a.row_grad[row] : 1.0f;
+            const f32x4 l = *reinterpret_cast<const f32x4 *>(logits + at * pitch_v + f0 + f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p = fast_exp((l[j] - norm.x) - norm.y);
+                v[j] = f0 + f + j < a.features ? p - (tgt == f + j ? 1.0f : 0.0f) : 0.0f;
+            }
+            if (d) EndProject<T>::store4(d + at * pitch_v + f0 + f, v);
+        }
+        f32x4 scaled;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) scaled[j] = in ? g * v[j] : 0.0f;
+        E e[4];
+        if constexpr (T::kBf16) {
+            const uint32_t lo = pack_bf16x2(scaled[0], scaled[1]), hi = pack_bf16x2(scaled[2], scaled[3]);
+            e[0] = (E)lo, e[1] = (E)(lo >> 16), e[2] = (E)hi, e[3] = (E)(hi >> 16);
+        } else {
+            for (int j = 0; j < 4; ++j) e[j] = scaled[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tile[r * kPitch + f + j] = e[j];
+    }
+    if (!dt) return;
+    __syncthreads();
+    constexpr int kPiece = T::kPiece, kRowPieces = 64 / kPiece;
+#pragma unroll
+    for (int i = threadIdx.x; i < 64 * kRowPieces; i += 256) {
+        const int f = i / kRowPieces, r = i % kRowPieces * kPiece;
+        if (f0 + f >= a.features || r0 + r >= padded) continue;
+        u32x4 v;
+        E *e = reinterpret_cast<E *>(&v);
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) e[j] = tile[(r + j) * kPitch + f];
+        *reinterpret_cast<u32x4 *>(dt + (uint64_t)(f0 + f) * pitch_x + r0 + r) = v;
+    }
+}
+
+// The ending of both gradients.  dh: row list[place], times its g.  dW (no list): rows as they are;
+// with several pieces their sums stand in `sum` until the last piece that has rows.
+template <class T>
+struct EndRows {
+    static constexpr bool kSlices = false;
+    typedef typename T::elem E;
+    uint32_t features;
+    uint64_t rows;
+    const uint32_t *list, *count;
+    const float *row_grad;
+    E *out;                        // [row][features]
+    float *sum;                    // or nullptr: one piece
+    const uint32_t *all;           // counted rows of all pieces
+    uint64_t before, after;        // rows up to this piece, and with it
+
+    template <class Tl>
+    __device__ __forceinline__ void add_rows(Tl &, int, uint32_t, uint64_t) const {}
+    __device__ __forceinline__ uint32_t begin(uint64_t) const { return 0; }
+    // Whether the tile is to be rounded and stored; else its sums stand in `sum`.
+    template <class Tl>
+    __device__ __forceinline__ bool complete(Tl &t, uint32_t f0, uint64_t r0) const
+    {
+        if (!sum) return true;
+        const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+        const uint64_t n_all = *all;
+        if (before > 0 && before >= n_all) return false;
+        const bool last = n_all <= after;
+#pragma unroll
+        for (int n = 0; n < Tl::kMR; ++n) {
+            const uint64_t row = r0 + 16 * n + l16;
+            if (row >= rows) continue;
+#pragma unroll
+            for (int m = 0; m < Tl::kMF; ++m) {
+                const uint32_t f = f0 + 16 * m + 4 * q;
                 if (f >= features) continue;
-                f32x4 *to = reinterpret_cast<f32x4 *>(sum + at * features + f);
-                *to = more ? *to + tile.acc[m][n] : tile.acc[m][n];
+                f32x4 *at = reinterpret_cast<f32x4 *>(sum + row * features + f);
+                if (before > 0) t.acc[m][n] += *at;
+                if (!last) *at = t.acc[m][n];
+            }
+        }
+        return last;
+    }
+    // Where place `at` goes, or nullptr.
+    __device__ __forceinline__ E *row_of(uint64_t at, uint64_t have) const
+    {
+        if (at >= have) return nullptr;
+        return out + (list ? list[at] : at) * features;
+    }
+    __device__ __forceinline__ float times(uint64_t at, uint64_t have) const
+    {
+        return list && row_grad && at < have ? row_grad[list[at]] : 1.0f;
+    }
+    template <class Tl>
+    __device__ __forceinline__ void store(Tl &t, uint32_t f0, uint64_t r0) const
+    {
+        if (!complete(t, f0, r0)) return;
+        const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+        const uint64_t have = places(0, rows, count);
+#pragma unroll
+        for (int n = 0; n < Tl::kMR; ++n) {
+            E *to = row_of(r0 + 16 * n + l16, have);
+            const float g = times(r0 + 16 * n + l16, have);
+            if (!to) continue;
+#pragma unroll
+            for (int m = 0; m < Tl::kMF; ++m) {
+                const uint32_t f = f0 + 16 * m + 4 * q;
+                if (f < features) EndProject<T>::store4(to + f, t.acc[m][n] * g);
+            }
+        }
+    }
+    // Through LDS, 16 rows at a time, as EndProject::store_rows.
+    template <class Tl>
+    __device__ __forceinline__ void finish(Tl &t, uint32_t, uint32_t f0, uint64_t r0, u32x4 *lds) const
+    {
+        if (!complete(t, f0, r0)) return;
+        constexpr int kMF = Tl::kMF, kRowPieces = 16 * kMF / T::kPiece, kAtOnce = 64 / kRowPieces;
+        const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+        const uint64_t have = places(0, rows, count);
+        const int piece = lane % kRowPieces;
+        const uint32_t f = f0 + piece * T::kPiece;
+#pragma unroll
+        for (int n = 0; n < Tl::kMR; ++n) {
+            const float g = times(r0 + 16 * n + l16, have);
+            wave_lds_sync();
+#pragma unroll
+            for (int m = 0; m < kMF; ++m) {
+                const int four = 4 * m + q, c = four * 4 / T::kPiece;
+                EndProject<T>::store4(reinterpret_cast<E *>(lds + l16 * kRowPieces + (c ^ (l16 % kRowPieces))) + four * 4 % T::kPiece,
+                                      t.acc[m][n] * g);
+            }
+            wave_lds_sync();
+#pragma unroll
+            for (int i = 0; i < 16; i += kAtOnce) {
+                const int r = i + lane / kRowPieces;
+                E *to = row_of(r0 + 16 * n + r, have);
+                const u32x4 v = lds[r * kRowPieces + (piece ^ (r % kRowPieces))];
+                if (to && f < features) *reinterpret_cast<u32x4 *>(to + f) = v;
             }
         }
     }
 };
 
-// dh of the counted rows from the sums, rounded once; zeros for the others.
-template <class T>
-__global__ __launch_bounds__(256) void k_hidden_grad(const float *sum, const int64_t *targets, const uint32_t *list,
-                                                     const uint32_t *count, uint64_t rows, uint32_t d,
-                                                     typename T::elem *out)
+__device__ __forceinline__ void store_zeros(void *p, uint64_t pieces, uint32_t from, uint32_t step)
 {
-    const uint64_t have = places(0, rows, count), each = (rows + gridDim.x - 1) / gridDim.x;
-    const uint64_t hi = (blockIdx.x + 1) * each < rows ? (blockIdx.x + 1) * each : rows;
-    for (uint64_t at = blockIdx.x * each; at < hi; ++at) {
-        if (at < have) {
-            const f32x4 *from = reinterpret_cast<const f32x4 *>(sum + at * d);
-            typename T::elem *to = out + (uint64_t)list[at] * d;
-            for (uint32_t i = threadIdx.x; i < d / 4; i += 256) EndProject<T>::store4(to + 4 * i, from[i]);
-        }
-        if (targets[at] == kIgnoreToken) {
-            typename T::elem *to = out + at * d;
-            for (uint32_t i = threadIdx.x; i < d / 4; i += 256) EndProject<T>::store4(to + 4 * i, f32x4{0, 0, 0, 0});
-        }
-    }
+    for (uint64_t i = from; i < pieces; i += step) static_cast<u32x4 *>(p)[i] = u32x4{0, 0, 0, 0};
+}
+
+// Zeros in the rows that do not count.
+__global__ __launch_bounds__(256) void k_ignored(const int64_t *targets, uint64_t rows, uint64_t row_bytes, char *out)
+{
+    for (uint64_t r = blockIdx.x; r < rows; r += gridDim.x)
+        if (targets[r] == kIgnoreToken) store_zeros(out + r * row_bytes, row_bytes / 16, threadIdx.x, 256);
 }
 
 __global__ __launch_bounds__(256) void k_zeros(u32x4 *p, uint64_t n)
@@ -181,69 +297,219 @@ __global__ __launch_bounds__(256) void k_zeros(u32x4 *p, uint64_t n)
     for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (uint64_t)gridDim.x * 256) p[i] = u32x4{0, 0, 0, 0};
 }
 
+// ---- few rows ---------------------------------------------------------------------------
+
+// Both products of at most kR rows in one pass over W and dW: a wave takes 64 kPer neighbouring
+// columns of kGradChunk features, a lane kPer of them with its values of h and of its sums of dh in
+// registers; D, from the logits, lies in LDS, where the four waves of a workgroup read it at once.
+// All in fp32, D is not rounded.  What bounds it is reading W and writing dW.
+template <class T, int kR, int kPer>
+__global__ __launch_bounds__(256) void k_outer(const float *logits, uint64_t pitch_v, RowsOf a, const typename T::elem *x,
+                                               uint64_t x_stride, const typename T::elem *w, uint32_t d, float *parts,
+                                               typename T::elem *dw)
+{
+    typedef typename T::elem E;
+    constexpr int kAhead = 4;
+    __shared__ float share[kGradChunk][kR];
+    const uint32_t v0 = blockIdx.x * kGradChunk;
+    const uint32_t n = a.features - v0 < kGradChunk ? a.features - v0 : kGradChunk;
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+        const uint32_t v = threadIdx.x;
+        float s = 0.0f;
+        if ((uint64_t)r < a.rows && v < n) {
+            const int64_t tgt = a.targets[r];
+            if (tgt != kIgnoreToken) {
+                const float2 norm = a.norms[r];
+                const float p = fast_exp((logits[r * pitch_v + v0 + v] - norm.x) - norm.y);
+                s = (a.row_grad ? a.row_grad[r] : 1.0f) * (p - (tgt == (int64_t)v0 + v ? 1.0f : 0.0f));
+            }
+        }
+        share[v][r] = s;
+    }
+    __syncthreads();
+    const uint32_t c = (blockIdx.y * 256 + threadIdx.x) * kPer;
+    if (c >= d) return;
+    const auto load = [](const E *p, float *v) {
+#pragma unroll
+        for (int i = 0; i < kPer; i += 4) T::load4(p + i, v + i);
+    };
+    float h[kR][kPer], sum[kR][kPer];
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+        if ((uint64_t)r < a.rows && a.targets[r] != kIgnoreToken) {
+            load(x + r * x_stride + c, h[r]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) h[r][i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) sum[r][i] = 0.0f;
+    }
+    float next[kAhead][kPer];
+    const E *from = w + (uint64_t)v0 * d + c;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) load(from + (uint64_t)((uint32_t)u < n ? u : n - 1) * d, next[u]);
+    for (uint32_t u0 = 0; u0 < n; u0 += kAhead) {
+        float now[kAhead][kPer];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) now[u][i] = next[u][i];
+            const uint32_t v = u0 + kAhead + u;
+            load(from + (uint64_t)(v < n ? v : n - 1) * d, next[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (u0 + u >= n) break;
+            float out[kPer];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) out[i] = 0.0f;
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+                const float s = share[u0 + u][r];
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    sum[r][i] = fmaf(s, now[u][i], sum[r][i]);
+                    out[i] = fmaf(s, h[r][i], out[i]);
+                }
+            }
+            if (dw) {
+                E *to = dw + (uint64_t)(v0 + u0 + u) * d + c;
+#pragma unroll
+                for (int i = 0; i < kPer; i += 4) EndProject<T>::store4(to + i, f32x4{out[i], out[i + 1], out[i + 2], out[i + 3]});
+            }
+        }
+    }
+    if (parts) {
+        float *to = parts + (uint64_t)blockIdx.x * a.rows * d + c;
+#pragma unroll
+        for (int r = 0; r < kR; ++r)
+            if ((uint64_t)r < a.rows)
+#pragma unroll
+                for (int i = 0; i < kPer; i += 4)   // a row that does not count: 0, whatever W holds
+                    *reinterpret_cast<f32x4 *>(to + (uint64_t)r * d + i) =
+                        a.targets[r] == kIgnoreToken ? f32x4{0, 0, 0, 0} : f32x4{sum[r][i], sum[r][i + 1], sum[r][i + 2], sum[r][i + 3]};
+    }
+}
+
+// dh from the sums of the chunks: 16 threads share the chunks of four values.
+template <class T>
+__global__ __launch_bounds__(256) void k_join(const float *parts, uint32_t chunks, uint64_t values, typename T::elem *out)
+{
+    __shared__ f32x4 sums[16][16];
+    const uint32_t of = threadIdx.x % 16, share = threadIdx.x / 16;
+    const uint64_t at = ((uint64_t)blockIdx.x * 16 + of) * 4;
+    f32x4 sum = {0, 0, 0, 0};
+    if (at < values)
+#pragma unroll 4
+        for (uint32_t i = share; i < chunks; i += 16) sum += *reinterpret_cast<const f32x4 *>(parts + i * values + at);
+    sums[share][of] = sum;
+    __syncthreads();
+    if (share || at >= values) return;
+#pragma unroll
+    for (int i = 1; i < 16; ++i) sum += sums[i][of];
+    EndProject<T>::store4(out + at, sum);
+}
+
+// ---- launches ---------------------------------------------------------------------------
+
+template <class T>
+hipError_t few_rows(const HeadGradArgs &h, const HeadGradSpace &s, const typename T::elem *x, const typename T::elem *w,
+                    hipStream_t stream)
+{
+    typedef typename T::elem E;
+    const ProductArgs p = {0, h.rows, h.x_stride, h.d, h.features, nullptr};
+    const uint32_t part = shape_part(Shape::few, h.rows, h.features), parts = (h.features + part - 1) / part;
+    const EndLogits end = {{h.features, 0, h.rows, h.targets, nullptr, nullptr, s.m, s.s, s.t, s.tl}, s.logits, s.pitch_v};
+    hipError_t e = by_shape<T>(Shape::few, p, x, w, nullptr, nullptr, end, stream);
+    if (e != hipSuccess) return e;
+    e = launch_head_join({s.m, s.s, s.t, s.tl, parts, 0, h.rows, nullptr, nullptr, h.targets, h.features, h.logp, nullptr,
+                          s.norms}, stream);
+    if (e != hipSuccess || (!h.hidden_grad && !h.weight_grad)) return e;
+    const RowsOf rows = {h.targets, nullptr, nullptr, static_cast<const float2 *>(s.norms), h.row_grad, h.rows, h.features};
+    const uint32_t chunks = (h.features + kGradChunk - 1) / kGradChunk;
+    float *sums = h.hidden_grad ? s.parts : nullptr;
+    const auto launch = [&](auto most, auto per) {
+        constexpr int kR = decltype(most)::value, kPer = decltype(per)::value;
+        k_outer<T, kR, kPer><<<dim3(chunks, (h.d + 256 * kPer - 1) / (256 * kPer)), 256, 0, stream>>>(
+            s.logits, s.pitch_v, rows, x, h.x_stride, w, h.d, sums, static_cast<E *>(h.weight_grad));
+    };
+    const std::integral_constant<int, 4> four;
+    if (h.rows <= 8) launch(std::integral_constant<int, 8>(), std::integral_constant<int, T::kPiece>());
+    else launch(std::integral_constant<int, kGradFew>(), four);
+    e = hipGetLastError();
+    if (e != hipSuccess || !h.hidden_grad) return e;
+    const uint64_t values = h.rows * h.d;
+    k_join<T><<<(uint32_t)((values + 63) / 64), 256, 0, stream>>>(s.parts, chunks, values, static_cast<E *>(h.hidden_grad));
+    return hipGetLastError();
+}
+
 template <class T>
 hipError_t head_grad(const HeadGradArgs &h, const void *hidden, const void *weight, hipStream_t stream)
 {
     typedef typename T::elem E;
-    const HeadGradSpace s = head_grad_space(h.rows, h.d, h.features, T::kBf16, h.workspace);
-    E *x = static_cast<E *>(s.x), *xt = static_cast<E *>(s.xt), *wt = static_cast<E *>(s.wt);
-    E *d = static_cast<E *>(s.d), *dt = static_cast<E *>(s.dt);
     const E *w = static_cast<const E *>(weight);
     if (h.rows == 0) {
         if (h.weight_grad)
             k_zeros<<<2048, 256, 0, stream>>>(static_cast<u32x4 *>(h.weight_grad), (uint64_t)h.features * h.d / T::kPiece);
         return hipGetLastError();
     }
+    const HeadGradSpace s = head_grad_space(h.rows, h.d, h.features, T::kBf16, h.workspace);
+    if (h.rows <= kGradFew) return few_rows<T>(h, s, static_cast<const E *>(hidden), w, stream);
+    E *x = static_cast<E *>(s.x), *xt = static_cast<E *>(s.xt), *wt = static_cast<E *>(s.wt);
+    E *d = static_cast<E *>(s.d), *dt = static_cast<E *>(s.dt);
     hipError_t e = launch_counted(h.targets, h.rows, s.list, s.count, h.logp, nullptr, stream);
     if (e != hipSuccess) return e;
-    const auto grid = [](uint64_t rows, uint32_t cols) { return dim3((uint32_t)((rows + 63) / 64), (cols + 63) / 64); };
-    k_turn<T, true><<<grid(h.rows, h.d), 256, 0, stream>>>(static_cast<const E *>(hidden), h.x_stride, h.rows, s.count,
-                                                           s.list, h.d, xt, s.pitch, x);
+    k_pieces<<<1, 256, 0, stream>>>(s.count, s.piece, (uint32_t)s.pieces, s.counts);
+    const uint32_t all = (uint32_t)(h.rows < 8192 ? h.rows : 8192);
+    k_gather<T><<<all, 256, 0, stream>>>(static_cast<const E *>(hidden), h.x_stride, h.rows, s.count, s.list, h.d, x);
+    const auto grid = [](uint64_t rows, uint64_t cols) { return dim3((uint32_t)((rows + 63) / 64), (uint32_t)((cols + 63) / 64)); };
+    if (h.hidden_grad) {
+        k_turn<T><<<grid(h.features, h.d), 256, 0, stream>>>(w, h.d, h.features, nullptr, h.d, wt, s.pitch_v);
+        k_ignored<<<all, 256, 0, stream>>>(h.targets, h.rows, (uint64_t)h.d * sizeof(E), static_cast<char *>(h.hidden_grad));
+    }
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    HeadArgs stats = {h.rows, h.d, h.d, h.features, h.targets, h.logp, nullptr, s.head};
-    stats.list = s.list;
-    stats.count = s.count;
-    stats.norms = s.norms;
-    e = launch_head_logprobs(stats, T::kBf16, x, w, stream);
-    if (e != hipSuccess || (!h.hidden_grad && !h.weight_grad)) return e;
-    for (uint32_t i = 0; i < s.pieces; ++i) {
-        const uint32_t first = i * s.piece;
-        const uint32_t n = h.features - first < s.piece ? h.features - first : s.piece;
-        const uint32_t pitch = (n + 7) / 8 * 8;
-        const ProductArgs logits = {0, h.rows, h.d, h.d, n, s.slices};
-        const EndGrad<T> end = {first, n, h.rows, h.targets, s.list, s.count, static_cast<const float2 *>(s.norms), h.row_grad,
-                                h.hidden_grad ? d : nullptr, h.weight_grad ? dt : nullptr, pitch, s.pitch};
-        e = by_shape<T>(product_shape(h.rows, n, h.d, T::kBf16), logits, x, w + (uint64_t)first * h.d, nullptr, s.count, end, stream);
+    const Shape shape = product_shape(s.piece, h.features, h.d, T::kBf16);
+    const uint32_t part = shape_part(shape, s.piece, h.features), parts = (h.features + part - 1) / part;
+    for (uint64_t i = 0; i < s.pieces; ++i) {
+        const uint64_t first = i * s.piece, n = h.rows - first < s.piece ? h.rows - first : s.piece;
+        const uint32_t *count = s.counts + i, *list = s.list + first;
+        const E *px = x + first * h.d;
+        const ProductArgs logits = {0, n, h.d, h.d, h.features, s.slices};
+        const EndLogits end = {{h.features, 0, n, h.targets, list, count, s.m, s.s, s.t, s.tl}, s.logits, s.pitch_v};
+        e = by_shape<T>(shape, logits, px, w, nullptr, count, end, stream);
+        if (e != hipSuccess) return e;
+        e = launch_head_join({s.m, s.s, s.t, s.tl, parts, 0, n, list, count, h.targets, h.features, h.logp, nullptr, s.norms},
+                             stream);
+        if (e != hipSuccess) return e;
+        if (!h.hidden_grad && !h.weight_grad) continue;
+        const RowsOf rows = {h.targets, list, count, static_cast<const float2 *>(s.norms), h.row_grad, n, h.features};
+        k_shares<T><<<dim3((uint32_t)((s.pitch_v + 63) / 64), (uint32_t)((n + 63) / 64)), 256, 0, stream>>>(
+            s.logits, rows, h.hidden_grad ? d : nullptr, h.weight_grad ? dt : nullptr, s.pitch_v, s.pitch_x);
+        e = hipGetLastError();
         if (e != hipSuccess) return e;
         if (h.hidden_grad) {
-            k_turn<T, false><<<grid(n, h.d), 256, 0, stream>>>(w + (uint64_t)first * h.d, h.d, n, nullptr, nullptr, h.d, wt,
-                                                               pitch, nullptr);
-            e = hipGetLastError();
-            if (e != hipSuccess) return e;
-            const ProductArgs p = {0, h.rows, pitch, pitch, h.d, s.slices};
-            const EndSum sum = {h.d, h.rows, s.count, s.sum, i > 0};
-            e = by_shape<T>(product_shape(h.rows, h.d, pitch, T::kBf16), p, d, wt, nullptr, s.count, sum, stream);
+            const uint32_t k = (uint32_t)s.pitch_v;
+            const ProductArgs p = {0, n, k, k, h.d, s.slices};
+            const EndRows<T> out = {h.d, n, list, count, h.row_grad, static_cast<E *>(h.hidden_grad), nullptr, s.count, 0, 0};
+            e = by_shape<T>(product_shape(n, h.d, k, T::kBf16), p, d, wt, nullptr, count, out, stream);
             if (e != hipSuccess) return e;
         }
         if (h.weight_grad) {
-            const ProductArgs p = {0, n, s.pitch, (uint32_t)s.pitch, h.d, s.slices, s.count};
-            AdapterArgs none = {};
-            none.rows = n;
-            none.d_in = (uint32_t)s.pitch;
-            none.d_out = h.d;
-            const EndProject<T> out = {none, nullptr, nullptr, nullptr, nullptr,
-                                       static_cast<E *>(h.weight_grad) + (uint64_t)first * h.d, h.d};
-            e = by_shape<T>(product_shape(n, h.d, (uint32_t)s.pitch, T::kBf16), p, dt, xt, nullptr, nullptr, out, stream);
+            const uint32_t k = (uint32_t)s.pitch_x;
+            k_turn<T><<<grid(n, h.d), 256, 0, stream>>>(px, h.d, n, count, h.d, xt, s.pitch_x);
+            e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            const ProductArgs p = {0, h.features, k, k, h.d, s.slices, count};
+            const EndRows<T> out = {h.d, h.features, nullptr, nullptr, nullptr, static_cast<E *>(h.weight_grad), s.sum, s.count,
+                                    first, first + n};
+            e = by_shape<T>(product_shape(h.features, h.d, k, T::kBf16), p, dt, xt, nullptr, nullptr, out, stream);
             if (e != hipSuccess) return e;
         }
     }
-    if (h.hidden_grad) {
-        k_hidden_grad<T><<<(uint32_t)(h.rows < 4096 ? h.rows : 4096), 256, 0, stream>>>(
-            s.sum, h.targets, s.list, s.count, h.rows, h.d, static_cast<E *>(h.hidden_grad));
-        e = hipGetLastError();
-    }
-    return e;
+    return hipSuccess;
 }
 
 template <class T, class End>
@@ -268,8 +534,8 @@ hipError_t raise_end()
 
 hipError_t prepare_head_grad()
 {
-    const hipError_t all[] = {raise_end<Bf16, EndGrad<Bf16>>(), raise_end<Bf16, EndSum>(), raise_end<Bf16, EndProject<Bf16>>(),
-                              raise_end<Fp32, EndGrad<Fp32>>(), raise_end<Fp32, EndSum>(), raise_end<Fp32, EndProject<Fp32>>()};
+    const hipError_t all[] = {raise_end<Bf16, EndLogits>(), raise_end<Bf16, EndRows<Bf16>>(), raise_end<Fp32, EndLogits>(),
+                              raise_end<Fp32, EndRows<Fp32>>()};
     for (const hipError_t e : all)
         if (e != hipSuccess) return e;
     return hipSuccess;

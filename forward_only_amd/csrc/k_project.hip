@@ -7,78 +7,6 @@
 namespace zo {
 namespace {
 
-// Ending of zo_head_logprobs: per wave tile and row (m, s, t) over the tile's features.
-struct EndHead {
-    static constexpr bool kSlices = false;
-    uint32_t features;
-    uint64_t base, rows;        // places of this launch
-    const int64_t *targets;     // of all rows, or nullptr
-    const uint32_t *list;       // row of each place, or nullptr: place = row
-    const uint32_t *count;
-    float *m, *s, *t;           // [wave tile][place]
-    float *tl;                  // logit of each place's target
-
-    template <class Tl>
-    __device__ __forceinline__ void add_rows(Tl &, int, uint32_t, uint64_t) const {}
-    __device__ __forceinline__ uint32_t begin(uint64_t) const { return 0; }
-    template <class Tl>
-    __device__ __forceinline__ void finish(Tl &tile, uint32_t, uint32_t f0, uint64_t r0, u32x4 *) const
-    {
-        store(tile, f0, r0);
-    }
-
-    template <class Tl>
-    __device__ __forceinline__ void store(Tl &tile, uint32_t f0, uint64_t r0) const
-    {
-        constexpr int kMF = Tl::kMF, kMR = Tl::kMR;
-        const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
-        const uint32_t part = f0 / (16 * kMF);
-        if (f0 >= features) return;
-        const uint64_t have = places(base, rows, count);
-#pragma unroll
-        for (int n = 0; n < kMR; ++n) {
-            const uint64_t at = r0 + 16 * n + l16;
-            SoftStats st = SoftStats::empty();
-            int64_t tgt = -1;
-            if (targets && at < have) tgt = targets[list ? list[base + at] : base + at];
-            const auto feature = [&](int m4, int i) { return f0 + 16 * m4 + 4 * q + i; };
-            if (f0 + 16 * kMF > features) {
-#pragma unroll
-                for (int m4 = 0; m4 < kMF; ++m4)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (feature(m4, i) >= features) tile.acc[m4][n][i] = -INFINITY;
-            }
-            float top = -INFINITY;
-#pragma unroll
-            for (int m4 = 0; m4 < kMF; ++m4)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) top = fmaxf(top, tile.acc[m4][n][i]);
-            st.raise(top);
-#pragma unroll
-            for (int m4 = 0; m4 < kMF; ++m4)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) st.add(tile.acc[m4][n][i]);
-            // few waves hold a row's target
-            const uint32_t in = (uint32_t)(tgt - f0);
-            const bool here = at < have && tgt >= (int64_t)f0 && tgt < (int64_t)features && in < 16 * kMF;
-            if (__any(here)) {
-#pragma unroll
-                for (int m4 = 0; m4 < kMF; ++m4)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (here && feature(m4, i) - f0 == in) tl[at] = tile.acc[m4][n][i];
-            }
-            st.wave_merge(32, 16);
-            if (q == 0 && at < have) {
-                m[(uint64_t)part * rows + at] = st.m;
-                s[(uint64_t)part * rows + at] = st.s;
-                t[(uint64_t)part * rows + at] = st.t;
-            }
-        }
-    }
-};
-
 // ---- joining the head's partial statistics ----------------------------------------------
 
 // The places of the rows that count, in order, and zeros for the others' outputs; one
@@ -216,35 +144,22 @@ hipError_t head(const HeadArgs &h, const void *x, const void *w, hipStream_t str
     typedef typename T::elem E;
     const HeadSpace sp = head_space(h.rows, h.k, h.features, T::kBf16, h.workspace);
     const bool small = sp.shape == Shape::few;
-    // rows of x by place, what each place's row is, and how many there are
-    const uint32_t *from = nullptr, *list = nullptr, *count = nullptr;
-    if (h.count) {
-        list = h.list;
-        count = h.count;
-    } else if (h.targets && !small) {
-        const hipError_t e = launch_counted(h.targets, h.rows, sp.list, sp.count, h.logp, h.entropy, stream);
-        if (e != hipSuccess) return e;
-        from = list = sp.list;
+    uint32_t *list = nullptr, *count = nullptr;
+    if (h.targets && !small) {
+        list = sp.list;
         count = sp.count;
+        const hipError_t e = launch_counted(h.targets, h.rows, list, count, h.logp, h.entropy, stream);
+        if (e != hipSuccess) return e;
     }
     const E *px = static_cast<const E *>(x), *pw = static_cast<const E *>(w);
     for (uint64_t base = 0; base < h.rows; base += kHeadPlaces) {
         const uint64_t rows = h.rows - base < kHeadPlaces ? h.rows - base : kHeadPlaces;
         const ProductArgs p = {base, rows, h.x_stride, h.k, h.features, sp.slices};
         const EndHead end = {h.features, base, rows, h.targets, list, count, sp.m, sp.s, sp.t, sp.tl};
-        hipError_t e = by_shape<T>(sp.shape, p, px, pw, from, count, end, stream);
+        hipError_t e = by_shape<T>(sp.shape, p, px, pw, list, count, end, stream);
         if (e != hipSuccess) return e;
-        const auto join = [&](auto of) {
-            constexpr int kOf = decltype(of)::value;
-            k_head_join<kOf><<<(uint32_t)((rows + kOf - 1) / kOf), 1024, 0, stream>>>(
-                sp.m, sp.s, sp.t, sp.tl, sp.parts, base, rows, list, count, h.targets, h.features, h.logp,
-                h.entropy, static_cast<float2 *>(h.norms));
-        };
-        if (rows <= 256)
-            join(std::integral_constant<int, 1>{});
-        else
-            join(std::integral_constant<int, 8>{});
-        e = hipGetLastError();
+        e = launch_head_join({sp.m, sp.s, sp.t, sp.tl, sp.parts, base, rows, list, count, h.targets, h.features, h.logp,
+                              h.entropy, nullptr}, stream);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
@@ -296,6 +211,21 @@ hipError_t launch_counted(const int64_t *targets, uint64_t rows, uint32_t *list,
                           float *entropy, hipStream_t stream)
 {
     k_counted<<<1, 1024, 0, stream>>>(targets, rows, list, count, logp, entropy);
+    return hipGetLastError();
+}
+
+hipError_t launch_head_join(const HeadJoin &j, hipStream_t stream)
+{
+    const auto join = [&](auto of) {
+        constexpr int kOf = decltype(of)::value;
+        k_head_join<kOf><<<(uint32_t)((j.rows + kOf - 1) / kOf), 1024, 0, stream>>>(
+            j.m, j.s, j.t, j.tl, j.parts, j.base, j.rows, j.list, j.count, j.targets, j.features, j.logp, j.entropy,
+            static_cast<float2 *>(j.norms));
+    };
+    if (j.rows <= 256)
+        join(std::integral_constant<int, 1>{});
+    else
+        join(std::integral_constant<int, 8>{});
     return hipGetLastError();
 }
 

@@ -289,12 +289,21 @@ struct HeadArgs {
     const int64_t *targets;        // nullptr: entropies of all rows
     float *logp, *entropy;
     void *workspace;
-    // Given: x holds the rows that count, one a place, list says which they are, and norms
-    // ([places] of two floats: a row's largest logit and the logarithm of its sum; NaN for a
-    // target outside the vocabulary) may be wanted.
-    const uint32_t *list = nullptr, *count = nullptr;
-    void *norms = nullptr;
 };
+// Joins partial statistics [parts][rows] of rows by place: logp and entropy (or nullptr) of the rows
+// that list says (or nullptr: place = row), of *count (or all) places; norms (or nullptr), [rows] of two
+// floats: a row's largest logit and the logarithm of its sum, NaN for a target outside the vocabulary.
+struct HeadJoin {
+    const float *m, *s, *t, *tl;
+    uint32_t parts;
+    uint64_t base, rows;
+    const uint32_t *list, *count;
+    const int64_t *targets;
+    uint32_t features;
+    float *logp, *entropy;
+    void *norms;
+};
+hipError_t launch_head_join(const HeadJoin &j, hipStream_t stream);
 // list: the rows whose target is not ignored, in order; count: how many; zeros for the others'
 // logp and entropy (or nullptr).
 hipError_t launch_counted(const int64_t *targets, uint64_t rows, uint32_t *list, uint32_t *count, float *logp,
@@ -351,33 +360,28 @@ struct HeadGradArgs {
     void *hidden_grad, *weight_grad;   // of the operands' type; or nullptr
     void *workspace;
 };
-// Bytes of a piece's gradients of the logits, and the most features of a piece.
-constexpr uint64_t kGradPieceBytes = (uint64_t)1 << 29;
-constexpr uint32_t kGradPiece = 32768;
+// Rows are taken in pieces of at most this many logits, and at least 256 rows.
+constexpr uint64_t kGradLogits = (uint64_t)1 << 28;
+// Rows of which the products are formed value by value (k_outer); its values of the vocabulary a wave.
+constexpr uint64_t kGradFew = 16;
+constexpr uint32_t kGradChunk = 256;
 struct HeadGradSpace {
-    uint32_t *count, *list;
-    void *norms, *x, *xt, *d, *dt, *wt, *head;
-    float *sum, *slices;
-    uint32_t piece, pieces;        // features of a piece (a multiple of 8), and their number
-    uint64_t pitch;                // places, to a multiple of 8
+    uint32_t *count, *counts, *list;
+    void *norms, *x, *xt, *d, *dt, *wt;
+    float *m, *s, *t, *tl, *logits, *sum, *parts, *slices;
+    uint64_t piece, pieces;        // rows of a piece, and their number
+    uint64_t pitch_x, pitch_v;     // rows of a piece and features, to a multiple of 8
     uint64_t bytes;
 };
 inline HeadGradSpace head_grad_space(uint64_t rows, uint32_t d, uint32_t features, bool bf16, void *base)
 {
     const uint64_t size = bf16 ? 2 : 4;
-    HeadGradSpace s;
-    s.pitch = (rows + 7) / 8 * 8;
-    // pieces of one size, of whole tiles where there are several
-    const uint64_t fits = s.pitch ? kGradPieceBytes / (s.pitch * size) / 256 * 256 : kGradPiece;
-    const uint64_t most = fits < 256 ? 256 : fits > kGradPiece ? kGradPiece : fits;
-    s.pieces = (uint32_t)(((uint64_t)features + most - 1) / most);
-    const uint64_t each = s.pieces ? ((uint64_t)features + s.pieces - 1) / s.pieces : 0;
-    s.piece = (uint32_t)(s.pieces > 1 ? (each + 255) / 256 * 256 : (each + 7) / 8 * 8);
-    // what never falls as rows grow: at most so much for a piece, at least 256 features
-    const uint64_t whole = ((uint64_t)features + 255) / 256 * 256 < kGradPiece ? ((uint64_t)features + 255) / 256 * 256 : kGradPiece;
-    const uint64_t least = s.pitch * 256 * size;
-    const uint64_t cap = kGradPieceBytes > least ? kGradPieceBytes : least;
-    const uint64_t piece_bytes = s.pitch * whole * size < cap ? s.pitch * whole * size : cap;
+    HeadGradSpace s = {};
+    s.pitch_v = ((uint64_t)features + 7) / 8 * 8;
+    const uint64_t fits = kGradLogits / (s.pitch_v ? s.pitch_v : 1) / 256 * 256, most = fits < 256 ? 256 : fits;
+    s.piece = rows < most ? rows : most;
+    s.pieces = s.piece ? (rows + s.piece - 1) / s.piece : 0;
+    s.pitch_x = (s.piece + 7) / 8 * 8;
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {
         void *p = base ? static_cast<char *>(base) + at : nullptr;
@@ -385,17 +389,28 @@ inline HeadGradSpace head_grad_space(uint64_t rows, uint32_t d, uint32_t feature
         return p;
     };
     s.count = static_cast<uint32_t *>(take(4));
+    s.counts = static_cast<uint32_t *>(take(s.pieces * 4));
     s.list = static_cast<uint32_t *>(take(rows * 4));
-    s.norms = take(rows * 8);
-    s.x = take(rows * d * size);
-    s.xt = take(s.pitch * d * size);
-    s.d = take(piece_bytes);
-    s.dt = take(piece_bytes);
-    s.wt = take(whole * d * size);
-    s.sum = static_cast<float *>(take(rows * d * 4));
-    s.slices = static_cast<float *>(take(kBigSliceBytes));
-    s.head = base ? static_cast<char *>(base) + at : nullptr;
-    s.bytes = at + head_space(rows, d, features, bf16, nullptr).bytes;
+    s.norms = take(s.piece * 8);
+    // partial statistics of 32 features at least
+    const uint64_t stats = s.piece * (((uint64_t)features + 31) / 32) * 4;
+    s.m = static_cast<float *>(take(stats));
+    s.s = static_cast<float *>(take(stats));
+    s.t = static_cast<float *>(take(stats));
+    s.tl = static_cast<float *>(take(s.piece * 4));
+    s.logits = static_cast<float *>(take(s.piece * s.pitch_v * 4));
+    const uint64_t few = rows < kGradFew ? rows : kGradFew;
+    s.parts = static_cast<float *>(take(((uint64_t)features + kGradChunk - 1) / kGradChunk * few * d * 4));
+    if (rows > kGradFew) {
+        s.x = take(rows * d * size);
+        s.xt = take(s.pitch_x * d * size);
+        s.d = take(s.piece * s.pitch_v * size);
+        s.dt = take(s.pitch_x * features * size);
+        s.wt = take(s.pitch_v * d * size);
+        s.slices = static_cast<float *>(take(kBigSliceBytes));
+        if (s.pieces > 1) s.sum = static_cast<float *>(take((uint64_t)features * d * 4));
+    }
+    s.bytes = at;
     return s;
 }
 hipError_t prepare_head_grad();

@@ -663,6 +663,78 @@ struct EndProject {
     }
 };
 
+// Ending of zo_head_logprobs: per wave tile and row (m, s, t) over the tile's features.
+struct EndHead {
+    static constexpr bool kSlices = false;
+    uint32_t features;
+    uint64_t base, rows;        // places of this launch
+    const int64_t *targets;     // of all rows, or nullptr
+    const uint32_t *list;       // row of each place, or nullptr: place = row
+    const uint32_t *count;
+    float *m, *s, *t;           // [wave tile][place]
+    float *tl;                  // logit of each place's target
+
+    template <class Tl>
+    __device__ __forceinline__ void add_rows(Tl &, int, uint32_t, uint64_t) const {}
+    __device__ __forceinline__ uint32_t begin(uint64_t) const { return 0; }
+    template <class Tl>
+    __device__ __forceinline__ void finish(Tl &tile, uint32_t, uint32_t f0, uint64_t r0, u32x4 *) const
+    {
+        store(tile, f0, r0);
+    }
+
+    template <class Tl>
+    __device__ __forceinline__ void store(Tl &tile, uint32_t f0, uint64_t r0) const
+    {
+        constexpr int kMF = Tl::kMF, kMR = Tl::kMR;
+        const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+        const uint32_t part = f0 / (16 * kMF);
+        if (f0 >= features) return;
+        const uint64_t have = places(base, rows, count);
+#pragma unroll
+        for (int n = 0; n < kMR; ++n) {
+            const uint64_t at = r0 + 16 * n + l16;
+            SoftStats st = SoftStats::empty();
+            int64_t tgt = -1;
+            if (targets && at < have) tgt = targets[list ? list[base + at] : base + at];
+            const auto feature = [&](int m4, int i) { return f0 + 16 * m4 + 4 * q + i; };
+            if (f0 + 16 * kMF > features) {
+#pragma unroll
+                for (int m4 = 0; m4 < kMF; ++m4)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (feature(m4, i) >= features) tile.acc[m4][n][i] = -INFINITY;
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int m4 = 0; m4 < kMF; ++m4)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = fmaxf(top, tile.acc[m4][n][i]);
+            st.raise(top);
+#pragma unroll
+            for (int m4 = 0; m4 < kMF; ++m4)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) st.add(tile.acc[m4][n][i]);
+            // few waves hold a row's target
+            const uint32_t in = (uint32_t)(tgt - f0);
+            const bool here = at < have && tgt >= (int64_t)f0 && tgt < (int64_t)features && in < 16 * kMF;
+            if (__any(here)) {
+#pragma unroll
+                for (int m4 = 0; m4 < kMF; ++m4)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (here && feature(m4, i) - f0 == in) tl[at] = tile.acc[m4][n][i];
+            }
+            st.wave_merge(32, 16);
+            if (q == 0 && at < have) {
+                m[(uint64_t)part * rows + at] = st.m;
+                s[(uint64_t)part * rows + at] = st.s;
+                t[(uint64_t)part * rows + at] = st.t;
+            }
+        }
+    }
+};
+
 // Tile t of nf x nr: consecutive tiles run through eight row tiles, then the next features, so
 // that tiles in flight together share rows and weights in L2.
 __device__ __forceinline__ void tile_at(uint32_t t, uint32_t nf, uint32_t nr, uint32_t &f, uint32_t &r)

@@ -523,17 +523,19 @@ zo_status zo_distill_loss(zo_ctx *ctx, const void *d_logits, zo_dtype dtype, uin
  * W [vocab x d], as zo_head_logprobs, with the gradients of sum_row d_row_grad[row] (-logp[row]):
  *   D[row][v] = d_row_grad[row] (softmax(h W^T)[row][v] - [v = target]),
  *   d_hidden_grad = D W [rows x d],  d_weight_grad = D^T h [vocab x d]
- * (d_row_grad, device float [rows], NULL: 1 for each row).  Logits are formed in fp32, tile by tile, and
- * never stored; D is rounded to the dtype, in pieces of the vocabulary that the workspace holds, and
- * multiplied with fp32 sums; the gradients are rounded once.  Rows with the ignored target are not computed
- * in batches of more than 64 rows; their logp and gradient are 0 and they add nothing to d_weight_grad, whatever
- * they hold.  A target outside the vocabulary, or a row that holds NaN or an infinity, makes the row's logp and
+ * (d_row_grad, device float [rows], NULL: 1 for each row).  Rows are taken in pieces of at most 2^28 logits
+ * (at least 256 rows), so that the workspace holds that many in fp32 and no more; the gradients' sums are fp32
+ * and rounded once.  Of more than 16 rows D is rounded to the dtype before its products, with g for
+ * d_weight_grad and without for d_hidden_grad.  Rows with the ignored target are not computed in batches of
+ * more than 16 rows; their logp and gradient are 0 and they add nothing to d_weight_grad, whatever they
+ * hold.  A target outside the vocabulary, or a row that holds NaN or an infinity, makes the row's logp and
  * gradient NaN, and d_weight_grad with them.  Deterministic.
  * d_targets: device int64 [rows].  d_logp, d_hidden_grad and d_weight_grad may each be NULL; the gradients are
  * of `dtype`, contiguous, 16-byte aligned.  d_workspace: device, 256-byte aligned, at least
  * zo_head_grad_workspace_bytes(rows, d, vocab, dtype) bytes, which never fall as rows grow.  rows == 0 gives
  * a d_weight_grad of zeros.
- * Errors: as zo_head_logprobs; ZO_EUNSUPPORTED if rows exceed 2^25, d 2^20, vocab 2^24 or rows * d 2^35. */
+ * Errors: as zo_head_logprobs; ZO_EUNSUPPORTED if rows exceed 2^25, d 2^20, vocab 2^24, or rows * d or
+ * vocab * d 2^35. */
 uint64_t zo_head_grad_workspace_bytes(uint64_t rows, uint32_t d, uint32_t vocab, zo_dtype dtype);
 zo_status zo_head_grad(zo_ctx *ctx, const void *d_hidden, uint64_t hidden_stride,
                        const void *d_weight, zo_dtype dtype, uint64_t rows, uint32_t d,

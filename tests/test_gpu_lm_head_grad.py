@@ -40,7 +40,7 @@ def _check(ctx, h, w, t, g, dtype, x=None, **kw):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
-@pytest.mark.parametrize("rows,d,vocab", [(1, 8, 1), (1, 64, 40), (3, 40, 9), (8, 256, 1003), (33, 72, 260), (64, 128, 777),
+@pytest.mark.parametrize("rows,d,vocab", [(1, 8, 1), (1, 64, 40), (3, 40, 9), (8, 256, 1003), (33, 72, 260), (64, 128, 777), (16, 520, 130), (17, 520, 130), (9, 2568, 1030),
                                           (65, 128, 264), (130, 264, 515), (257, 64, 2050), (300, 776, 300), (1030, 136, 700),
                                           (5, 1032, 5003)])
 def test_matches_reference(ctx, rows, d, vocab, dtype):
@@ -83,11 +83,53 @@ def test_bad_targets_and_values(ctx, rows, dtype):
     assert torch.isfinite(got.hidden_grad[0]).all() and torch.isfinite(got.logp[[0, 2, 3]]).all()
 
 
-def test_pieces_of_the_vocabulary(ctx):
-    """More features than one piece holds, of whole tiles and not."""
+def test_large_vocabularies(ctx):
     for rows, d, vocab, dtype in ((70, 64, 40007, BF), (9, 40, 70001, BF), (70, 16, 33000, F32)):
         h, w, t, g = _case(rows, d, vocab, dtype, ignore=0.2, seed=3)
         _check(ctx, h, w, t, g, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("ignore", [0.0, 0.3, 0.999])
+def test_pieces_of_rows(ctx, ignore, dtype):
+    """More logits than a piece of rows holds: dW is summed over pieces, the last of them perhaps
+    without rows that count."""
+    rows, d, vocab = 600, 16, 524296          # pieces of 256 rows
+    gen = torch.Generator().manual_seed(8)
+    h, w = torch.randn(rows, d, generator=gen).to(dtype), (torch.randn(vocab, d, generator=gen) * 0.6).to(dtype)
+    t = torch.randint(0, vocab, (rows,), generator=gen)
+    t[torch.rand(rows, generator=gen) < ignore] = ref.IGNORE
+    t[5] = 77
+    g = torch.rand(rows, generator=gen) + 0.5
+    got = zo.zo_head_grad(ctx, h.cuda(), w.cuda(), t.cuda(), row_grad=g.cuda())
+    # the definition in 64 bits, 100 rows at a time on the GPU
+    H, W, G, T = h.cuda().double(), w.cuda().double(), g.cuda().double(), t.cuda()
+    half = ref.UBF if dtype == BF else ref.U32
+    dw, bw = torch.zeros_like(W), torch.zeros_like(W)
+    for at in range(0, rows, 100):
+        r = slice(at, at + 100)
+        keep = T[r] != ref.IGNORE
+        p = torch.log_softmax(H[r] @ W.t().contiguous(), dim=1)
+        logp = p.gather(1, T[r].clamp(min=0)[:, None])[:, 0].masked_fill(~keep, 0.0)
+        # products of 16 terms of norms below 30, and sums over 524296 values (lm_ref's E)
+        e = 8 * math.sqrt(d) * ref.U32 * torch.linalg.vector_norm(H[r], dim=1) * torch.linalg.vector_norm(W, dim=1).max()
+        E = (vocab / 256 + 64) * ref.U32
+        ref.assert_close(got.logp[r], logp.cpu(), (2 * e + E + 2 * ref.U32 * 50).cpu(), "logp")
+        p = p.exp()
+        D = p.clone()
+        D[torch.arange(D.shape[0], device="cuda"), T[r].clamp(min=0)] -= 1.0
+        D *= (G[r] * keep)[:, None]
+        off = G[r][:, None] * p * (2 * e[:, None] + E + 200 * ref.U32) + (half + 4 * ref.U32) * D.abs()
+        off *= keep[:, None]
+        dh = D @ W
+        bh = off @ W.abs() + 8 * math.sqrt(vocab) * ref.U32 * torch.linalg.vector_norm(D, dim=1)[:, None] \
+            * torch.linalg.vector_norm(W, dim=0)[None, :] + half * dh.abs() + 1e-30
+        ref.assert_close(got.hidden_grad[r], dh.cpu(), bh.cpu(), "hidden_grad")
+        dw += D.t().contiguous() @ H[r]
+        bw += off.t().contiguous() @ H[r].abs()
+    # sums of 600 terms of at most |D| |h|, in the norms that bw already carries half a step of
+    bw += 8 * math.sqrt(rows) * ref.U32 / half * bw + half * dw.abs() + 1e-30
+    ref.assert_close(got.weight_grad, dw.cpu(), bw.cpu(), "weight_grad")
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])

@@ -299,12 +299,44 @@ __global__ __launch_bounds__(256) void k_zeros(u32x4 *p, uint64_t n)
 
 // ---- few rows ---------------------------------------------------------------------------
 
+// kPer neighbouring values as they are held, read and written past the caches: once each.
+template <class T, int kPer>
+struct Held {
+    static constexpr int kWords = kPer * (int)sizeof(typename T::elem) / 4;
+    typedef uint32_t Words __attribute__((ext_vector_type(kWords)));
+    Words w;
+    __device__ __forceinline__ void load(const typename T::elem *p)
+    {
+        w = __builtin_nontemporal_load(reinterpret_cast<const Words *>(p));
+    }
+    __device__ __forceinline__ void values(float *v) const
+    {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if constexpr (T::kBf16) v[i] = i & 1 ? bf16hi_to_f32(w[i >> 1]) : bf16lo_to_f32(w[i >> 1]);
+            else v[i] = __uint_as_float(w[i]);
+        }
+    }
+    static __device__ __forceinline__ void store(typename T::elem *p, const float *v)
+    {
+        Words o;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            if constexpr (T::kBf16) o[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+            else o[i] = __float_as_uint(v[i]);
+        }
+        __builtin_nontemporal_store(o, reinterpret_cast<Words *>(p));
+    }
+};
+
+constexpr int kOuterThreads = 128;
+
 // Both products of at most kR rows in one pass over W and dW: a wave takes 64 kPer neighbouring
 // columns of kGradChunk features, a lane kPer of them with its values of h and of its sums of dh in
-// registers; D, from the logits, lies in LDS, where the four waves of a workgroup read it at once.
+// registers; D, from the logits, lies in LDS, where the waves of a workgroup read it at once.
 // All in fp32, D is not rounded.  What bounds it is reading W and writing dW.
 template <class T, int kR, int kPer>
-__global__ __launch_bounds__(256) void k_outer(const float *logits, uint64_t pitch_v, RowsOf a, const typename T::elem *x,
+__global__ __launch_bounds__(kOuterThreads) void k_outer(const float *logits, uint64_t pitch_v, RowsOf a, const typename T::elem *x,
                                                uint64_t x_stride, const typename T::elem *w, uint32_t d, float *parts,
                                                typename T::elem *dw)
 {
@@ -313,11 +345,11 @@ __global__ __launch_bounds__(256) void k_outer(const float *logits, uint64_t pit
     __shared__ float share[kGradChunk][kR];
     const uint32_t v0 = blockIdx.x * kGradChunk;
     const uint32_t n = a.features - v0 < kGradChunk ? a.features - v0 : kGradChunk;
-#pragma unroll
-    for (int r = 0; r < kR; ++r) {
-        const uint32_t v = threadIdx.x;
+#pragma unroll 2
+    for (int i = threadIdx.x; i < kR * (int)kGradChunk; i += kOuterThreads) {
+        const uint32_t r = i / kGradChunk, v = i % kGradChunk;
         float s = 0.0f;
-        if ((uint64_t)r < a.rows && v < n) {
+        if (r < a.rows && v < n) {
             const int64_t tgt = a.targets[r];
             if (tgt != kIgnoreToken) {
                 const float2 norm = a.norms[r];
@@ -328,7 +360,7 @@ __global__ __launch_bounds__(256) void k_outer(const float *logits, uint64_t pit
         share[v][r] = s;
     }
     __syncthreads();
-    const uint32_t c = (blockIdx.y * 256 + threadIdx.x) * kPer;
+    const uint32_t c = (blockIdx.y * kOuterThreads + threadIdx.x) * kPer;
     if (c >= d) return;
     const auto load = [](const E *p, float *v) {
 #pragma unroll
@@ -346,49 +378,53 @@ __global__ __launch_bounds__(256) void k_outer(const float *logits, uint64_t pit
 #pragma unroll
         for (int i = 0; i < kPer; ++i) sum[r][i] = 0.0f;
     }
-    float next[kAhead][kPer];
     const E *from = w + (uint64_t)v0 * d + c;
+    E *to = dw ? dw + (uint64_t)v0 * d + c : nullptr;
+    const auto use = [&](const Held<T, kPer> &held, uint32_t v) {
+        float now[kPer], out[kPer];
+        held.values(now);
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) load(from + (uint64_t)((uint32_t)u < n ? u : n - 1) * d, next[u]);
-    for (uint32_t u0 = 0; u0 < n; u0 += kAhead) {
-        float now[kAhead][kPer];
+        for (int i = 0; i < kPer; ++i) out[i] = 0.0f;
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
+        for (int r = 0; r < kR; ++r) {
+            const float s = share[v][r];
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) now[u][i] = next[u][i];
-            const uint32_t v = u0 + kAhead + u;
-            load(from + (uint64_t)(v < n ? v : n - 1) * d, next[u]);
-        }
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            if (u0 + u >= n) break;
-            float out[kPer];
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) out[i] = 0.0f;
-#pragma unroll
-            for (int r = 0; r < kR; ++r) {
-                const float s = share[u0 + u][r];
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    sum[r][i] = fmaf(s, now[u][i], sum[r][i]);
-                    out[i] = fmaf(s, h[r][i], out[i]);
-                }
-            }
-            if (dw) {
-                E *to = dw + (uint64_t)(v0 + u0 + u) * d + c;
-#pragma unroll
-                for (int i = 0; i < kPer; i += 4) EndProject<T>::store4(to + i, f32x4{out[i], out[i + 1], out[i + 2], out[i + 3]});
+            for (int i = 0; i < kPer; ++i) {
+                sum[r][i] = fmaf(s, now[i], sum[r][i]);
+                out[i] = fmaf(s, h[r][i], out[i]);
             }
         }
+        if (to) Held<T, kPer>::store(to + (uint64_t)v * d, out);
+    };
+    Held<T, kPer> next[kAhead];
+    uint32_t v = 0;
+    if (n >= kAhead) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) next[u].load(from + (uint64_t)u * d);
+        for (; v + 2 * kAhead <= n; v += kAhead) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const Held<T, kPer> now = next[u];
+                next[u].load(from + (uint64_t)(v + kAhead + u) * d);
+                use(now, v + u);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) use(next[u], v + u);
+        v += kAhead;
+    }
+    for (; v < n; ++v) {
+        next[0].load(from + (uint64_t)v * d);
+        use(next[0], v);
     }
     if (parts) {
-        float *to = parts + (uint64_t)blockIdx.x * a.rows * d + c;
+        float *own = parts + (uint64_t)blockIdx.x * a.rows * d + c;
 #pragma unroll
         for (int r = 0; r < kR; ++r)
             if ((uint64_t)r < a.rows)
 #pragma unroll
                 for (int i = 0; i < kPer; i += 4)   // a row that does not count: 0, whatever W holds
-                    *reinterpret_cast<f32x4 *>(to + (uint64_t)r * d + i) =
+                    *reinterpret_cast<f32x4 *>(own + (uint64_t)r * d + i) =
                         a.targets[r] == kIgnoreToken ? f32x4{0, 0, 0, 0} : f32x4{sum[r][i], sum[r][i + 1], sum[r][i + 2], sum[r][i + 3]};
     }
 }
@@ -432,7 +468,7 @@ hipError_t few_rows(const HeadGradArgs &h, const HeadGradSpace &s, const typenam
     float *sums = h.hidden_grad ? s.parts : nullptr;
     const auto launch = [&](auto most, auto per) {
         constexpr int kR = decltype(most)::value, kPer = decltype(per)::value;
-        k_outer<T, kR, kPer><<<dim3(chunks, (h.d + 256 * kPer - 1) / (256 * kPer)), 256, 0, stream>>>(
+        k_outer<T, kR, kPer><<<dim3(chunks, (h.d + kOuterThreads * kPer - 1) / (kOuterThreads * kPer)), kOuterThreads, 0, stream>>>(
             s.logits, s.pitch_v, rows, x, h.x_stride, w, h.d, sums, static_cast<E *>(h.weight_grad));
     };
     const std::integral_constant<int, 4> four;

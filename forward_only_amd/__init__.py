@@ -25,7 +25,7 @@ import torch
 
 from . import _lib
 from ._lib import (ZO_BF16, ZO_EHIP, ZO_EINVAL, ZO_ENOMEM, ZO_EUNSUPPORTED, ZO_FP32,  # noqa: F401
-                   ZO_IGNORE_TOKEN, ZO_MAX_NPERT, ZO_MAX_RANK, ZO_MAX_TEACHER, ZO_MAX_TOP_K, ZO_NOALLOC_SCRATCH_BYTES, ZO_OK, ZO_WEIGHTS_POWER, ZO_WEIGHTS_PRECOND,
+                   ZO_IGNORE_TOKEN, ZO_MAX_NPERT, ZO_MAX_RANK, ZO_MAX_TEACHER, ZO_MAX_TOP_K, ZO_NOALLOC_SCRATCH_BYTES, ZO_OK, ZO_Q4_FEW, ZO_WEIGHTS_POWER, ZO_WEIGHTS_PRECOND,
                    ZO_WEIGHTS_SPSA_MEAN, ZOError)
 
 __all__ = [
@@ -851,25 +851,30 @@ class Q4Weight(NamedTuple):
         return self.scales.shape[1], self.d_in
 
 
-def _q4(weight: Q4Weight, dtype=None):
-    """(codes, scales, zeros, d_out, d_in, group) of a matrix in 4 bits."""
+def _q4(weight: Q4Weight, dtype=None, dev: int | None = None):
+    """(codes, scales, zeros, d_out, d_in, group) of a matrix in 4 bits.  dtype, dev: of the
+    activations, where they are known."""
     codes, scales, zeros, d_in = weight
-    sp = _dev(scales, "scales", dtype)
-    _dtype_code(scales)
-    if scales.dim() != 2 or d_in <= 0 or d_in % max(1, scales.shape[0]):
+    # all that a call is to have, at once (a check of each by its name costs 1 us)
+    if not (dev is not None and scales.dtype is dtype and scales.get_device() == dev and scales.is_contiguous()
+            and codes.dtype is torch.uint8 and codes.get_device() == dev and codes.is_contiguous()):
+        _dev(scales, "scales", dtype)
+        _dtype_code(scales)
+        _dev(codes, "codes", torch.uint8)
+    shape = scales.shape
+    if len(shape) != 2 or d_in <= 0 or d_in % max(1, shape[0]):
         raise ValueError(f"scales must have shape (groups, d_out) with d_in = {d_in} a multiple of groups")
-    groups, d_out = scales.shape
-    cp = _dev(codes, "codes", torch.uint8)
-    if tuple(codes.shape) != (-(-d_out // 16), -(-d_in // 128), 1024):
+    groups, d_out = shape
+    if codes.shape != (-(-d_out // 16), -(-d_in // 128), 1024):
         raise ValueError(f"codes must have shape ({-(-d_out // 16)}, {-(-d_in // 128)}, 1024), got {tuple(codes.shape)}")
     zp = None
     if zeros is not None:
         zp = _dev(zeros, "zeros", scales.dtype)
-        if zeros.shape != scales.shape:
-            raise ValueError(f"zeros must have the scales' shape {tuple(scales.shape)}, got {tuple(zeros.shape)}")
+        if zeros.shape != shape:
+            raise ValueError(f"zeros must have the scales' shape {tuple(shape)}, got {tuple(zeros.shape)}")
     if groups == 0 or d_in // groups not in (32, 64, 128):
         raise ValueError(f"groups must hold 32, 64 or 128 values, got {d_in} / {groups}")
-    return cp, sp, zp, d_out, d_in, d_in // groups
+    return codes.data_ptr(), scales.data_ptr(), zp, d_out, d_in, d_in // groups
 
 
 def _codes(d_out: int, d_in: int, out, stream):
@@ -944,7 +949,7 @@ def zo_q4_project(ctx: Context, x: torch.Tensor, weight: Q4Weight, adapters: tor
     xp, rows, d_in, xs = _matrix(x, "x")
     dev = x.get_device()
     code = _dtype_code(x)
-    cp, scp, zp, d_out, k, group = _q4(weight, x.dtype)
+    cp, scp, zp, d_out, k, group = _q4(weight, x.dtype, dev)
     if k != d_in:
         raise ValueError(f"weight must have {d_in} columns, got {k}")
     rank = int(rank)
@@ -962,9 +967,11 @@ def zo_q4_project(ctx: Context, x: torch.Tensor, weight: Q4Weight, adapters: tor
             raise ValueError("ids go with starts")
     bp = _vector(bias, "bias", d_out, x.dtype, dev)
     yp, ys, out = _projected(out, rows, d_out, x.dtype, stream)
-    if workspace is None:
-        wb = int(_lib.lib().zo_q4_workspace_bytes(rows, d_in, d_out, code, n_adapters, rank,
-                                                  n_probes if kp is None else 0))
+    if workspace is None and starts is None and rows <= ZO_Q4_FEW[code]:
+        ws, wb = None, 0
+    elif workspace is None:
+        wb = _lib.lib().zo_q4_workspace_bytes(rows, d_in, d_out, code, n_adapters, rank,
+                                              n_probes if kp is None else 0)
         workspace = _new(wb, torch.uint8, stream)
         ws = workspace.data_ptr()
     else:

@@ -10,6 +10,7 @@
 static_assert(ZO_MAX_NPERT == zo::kMaxNpert, "one probe-count limit");
 static_assert(ZO_MAX_TEACHER == zo::kMaxTeacher && ZO_MAX_TOP_K == zo::kMaxTopK && ZO_MAX_RANK == zo::kMaxRank &&
                   ZO_IGNORE_TOKEN == zo::kIgnoreToken, "one set of limits");
+static_assert(ZO_Q4_FEW_BF16 == zo::kQ4FewBf16 && ZO_Q4_FEW_FP32 == zo::kQ4FewFp32, "one set of limits");
 static_assert(2 * zo::kQuadProbes + 1 <= zo::kLowRankMax + 1,
               "the loss partials hold both signs of every probe of a fused pass and the clean loss");
 
@@ -850,7 +851,8 @@ zo_status zo_q4_project(zo_ctx *c, const void *d_x, uint64_t x_stride, const voi
     const uint64_t params = (uint64_t)n_adapters * rank * ((uint64_t)d_in + d_out);
     const uint32_t regenerated = d_probes && !d_bits && params > 0 ? n_probes : 0;
     if (regenerated > 0 && zo_bits_stride(params) > UINT64_MAX / 2 / regenerated) return ZO_EINVAL;
-    const uint64_t need = zo_q4_workspace_bytes(rows, d_in, d_out, dtype, n_adapters, rank, regenerated);
+    const uint64_t need = plain && zo::q4_few(rows, dtype == ZO_BF16)
+                              ? 0 : zo_q4_workspace_bytes(rows, d_in, d_out, dtype, n_adapters, rank, regenerated);
     if (need > 0 && (!d_workspace || !aligned<256>(d_workspace) || workspace_bytes < need)) return ZO_EINVAL;
     // x A^T and the rows' groups, unpacked weights, slices, signs
     char *at = static_cast<char *>(d_workspace);

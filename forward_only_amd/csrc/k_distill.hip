@@ -78,6 +78,10 @@ struct Sums {
     }
 };
 
+// Keeps a piece as it is held: its values are widened again where they are used next, instead of
+// taking twice the registers from one use to the other.
+__device__ __forceinline__ void as_held(u32x4 &v) { asm volatile("" : "+v"(v)); }
+
 struct Teacher {
     const int64_t *ids;       // [rows][k]; -1: no entry
     const float *logits;
@@ -86,8 +90,10 @@ struct Teacher {
 
 // One workgroup per row.  kHold > 0: the row stays in registers, kHold pieces a thread, between the
 // sums and the gradient; 0: it is read again for the gradient.
-template <class T, int kThreads, int kHold, bool kGrad>
-__global__ __launch_bounds__(kThreads) void k_distill(const T *logits, uint32_t vocab, uint64_t stride,
+template <class T, int kThreads, int kHold, bool kGrad, bool kOnce>
+// 1024 threads of bf16: two workgroups a CU (8192 rows of 50272, kernel 400 -> 330 us; fp32 rows would
+// spill, 515 of 32003 16 -> 19 us).
+__global__ __launch_bounds__(kThreads, kThreads == 1024 && sizeof(T) == 2 ? 8 : 1) void k_distill(const T *logits, uint32_t vocab, uint64_t stride,
                                                       Teacher teacher, const int64_t *targets, float tau,
                                                       float *loss, const float *row_grad, T *grad,
                                                       uint64_t grad_stride)
@@ -105,7 +111,11 @@ __global__ __launch_bounds__(kThreads) void k_distill(const T *logits, uint32_t 
     const uint32_t head_of = (uint32_t)(-(intptr_t)row & 15) / sizeof(T);
     const uint32_t head = head_of < vocab ? head_of : vocab;
     const uint32_t pieces = (vocab - head) / kPiece, rest = head + pieces * kPiece;
-    const auto piece_at = [&](uint32_t i) { return *reinterpret_cast<const u32x4 *>(row + head + (uint64_t)i * kPiece); };
+    const auto piece_at = [&](uint32_t i) {
+        const u32x4 *p = reinterpret_cast<const u32x4 *>(row + head + (uint64_t)i * kPiece);
+        if constexpr (kOnce) return __builtin_nontemporal_load(p);
+        else return *p;
+    };
     const float inv = 1.0f / tau, c = kLog2e * inv;
 
     const auto nothing = [&] {        // a row that counts for nothing
@@ -131,22 +141,63 @@ __global__ __launch_bounds__(kThreads) void k_distill(const T *logits, uint32_t 
     }
     if (has_first) first = widen(row[tid]);
     if (has_last) last = widen(row[rest + tid]);
-    // the teacher's distribution, by the first wave
+    // the teacher's entries, by the first wave; used behind the sums
     float x_of[kEntries] = {}, p_of[kEntries] = {}, t_of[kEntries] = {};
-    int64_t id_of[kEntries];
+    int64_t id_of[kEntries] = {};
     if (wave == 0) {
+#pragma unroll
+        for (int e = 0; e < kEntries; ++e) {
+            const uint32_t j = e * kWave + lane;
+            id_of[e] = j < teacher.k ? teacher.ids[at * teacher.k + j] : -1;
+            t_of[e] = j < teacher.k ? teacher.logits[at * teacher.k + j] : 0.0f;
+        }
+    }
+    if constexpr (kHold > 0) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kHold; ++u)
+#pragma unroll
+            for (int j = 0; j < kPiece; ++j) top = fmaxf(top, P::value(held[u], j));
+        st.m = top;
+#pragma unroll
+        for (int u = 0; u < kHold; ++u) {
+            as_held(held[u]);
+#pragma unroll
+            for (int j = 0; j < kPiece; ++j) st.add(P::value(held[u], j), c);
+            as_held(held[u]);
+        }
+    } else {
+        for (uint32_t i = tid; i < pieces; i += kUnroll * kThreads) {
+            u32x4 v[kUnroll];
+            float top = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) v[u] = i + u * kThreads < pieces ? piece_at(i + u * kThreads) : P::nothing();
+#pragma unroll
+            for (int j = 0; j < kUnroll * kPiece; ++j) top = fmaxf(top, P::value(v[j / kPiece], j % kPiece));
+            st.raise(top, c);
+#pragma unroll
+            for (int j = 0; j < kUnroll * kPiece; ++j) st.add(P::value(v[j / kPiece], j % kPiece), c);
+        }
+    }
+    if (has_first) {
+        st.raise(first, c);
+        st.add(first, c);
+    }
+    if (has_last) {
+        st.raise(last, c);
+        st.add(last, c);
+    }
+    if (wave == 0) {
+        // its distribution, and the model's logits there, before any of them is overwritten
         int n = 0, bad = 0;
         float top = -INFINITY;
 #pragma unroll
         for (int e = 0; e < kEntries; ++e) {
-            const uint32_t j = e * kWave + lane;
-            const bool in = j < teacher.k;
-            id_of[e] = in ? teacher.ids[at * teacher.k + j] : -1;
-            t_of[e] = id_of[e] != -1 ? teacher.logits[at * teacher.k + j] : -INFINITY;
             const bool ok = id_of[e] >= 0 && id_of[e] < (int64_t)vocab;
             x_of[e] = ok ? widen(row[id_of[e]]) : 0.0f;
             n += __popcll(__ballot(id_of[e] != -1));
             bad += __popcll(__ballot(id_of[e] != -1 && !ok));
+            t_of[e] = id_of[e] != -1 ? t_of[e] : -INFINITY;
             top = fmaxf(top, t_of[e]);
         }
         for (int o = kWave / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
@@ -170,38 +221,6 @@ __global__ __launch_bounds__(kThreads) void k_distill(const T *logits, uint32_t 
             state[0] = n;
             state[1] = bad || !(sum > 0.0f);        // NaN: the teacher has no distribution
         }
-    }
-    if constexpr (kHold > 0) {
-        float top = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < kHold; ++u)
-#pragma unroll
-            for (int j = 0; j < kPiece; ++j) top = fmaxf(top, P::value(held[u], j));
-        st.m = top;
-#pragma unroll
-        for (int u = 0; u < kHold; ++u)
-#pragma unroll
-            for (int j = 0; j < kPiece; ++j) st.add(P::value(held[u], j), c);
-    } else {
-        for (uint32_t i = tid; i < pieces; i += kUnroll * kThreads) {
-            u32x4 v[kUnroll];
-            float top = -INFINITY;
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) v[u] = i + u * kThreads < pieces ? piece_at(i + u * kThreads) : P::nothing();
-#pragma unroll
-            for (int j = 0; j < kUnroll * kPiece; ++j) top = fmaxf(top, P::value(v[j / kPiece], j % kPiece));
-            st.raise(top, c);
-#pragma unroll
-            for (int j = 0; j < kUnroll * kPiece; ++j) st.add(P::value(v[j / kPiece], j % kPiece), c);
-        }
-    }
-    if (has_first) {
-        st.raise(first, c);
-        st.add(first, c);
-    }
-    if (has_last) {
-        st.raise(last, c);
-        st.add(last, c);
     }
     for (int o = kWave / 2; o; o >>= 1) {
         const Sums b = {__shfl_xor(st.m, o), __shfl_xor(st.s, o)};
@@ -241,7 +260,9 @@ __global__ __launch_bounds__(kThreads) void k_distill(const T *logits, uint32_t 
             float f[kPiece];
 #pragma unroll
             for (int j = 0; j < kPiece; ++j) f[j] = g * q_of(P::value(v, j));
-            *reinterpret_cast<u32x4_any *>(out + head + (uint64_t)i * kPiece) = P::of(f);
+            u32x4_any *to = reinterpret_cast<u32x4_any *>(out + head + (uint64_t)i * kPiece);
+            if constexpr (kOnce) __builtin_nontemporal_store((u32x4_any)P::of(f), to);
+            else *to = P::of(f);
         };
         if constexpr (kHold > 0) {
 #pragma unroll
@@ -275,7 +296,8 @@ __global__ __launch_bounds__(kThreads) void k_distill(const T *logits, uint32_t 
 
 hipError_t launch_distill(const DistillArgs &a, bool bf16, hipStream_t stream)
 {
-    const auto launch = [&](auto *p, auto threads, auto hold, auto with) {
+    // What the last cache does not hold is read, and the gradient written, past the caches.
+    const auto launch_as = [&](auto *p, auto threads, auto hold, auto with, auto once) {
         using E = std::remove_cv_t<std::remove_pointer_t<decltype(p)>>;
         constexpr int kThreads = decltype(threads)::value;
         const auto from = [](auto *base, uint64_t i) { return base ? base + i : base; };
@@ -284,23 +306,35 @@ hipError_t launch_distill(const DistillArgs &a, bool bf16, hipStream_t stream)
         for (uint64_t r = 0; r < a.rows && e == hipSuccess; r += kRows) {
             const uint32_t n = (uint32_t)(a.rows - r < kRows ? a.rows - r : kRows);
             const Teacher t = {from(a.ids, r * a.k), from(a.teacher, r * a.k), a.k};
-            k_distill<E, kThreads, decltype(hold)::value, decltype(with)::value><<<n, kThreads, 0, stream>>>(
+            k_distill<E, kThreads, decltype(hold)::value, decltype(with)::value, decltype(once)::value><<<n, kThreads, 0, stream>>>(
                 p + r * a.stride, a.vocab, a.stride, t, from(a.targets, r), a.tau, a.loss + r,
                 from(a.row_grad, r), from(static_cast<E *>(a.grad), r * a.grad_stride), a.grad_stride);
             e = hipGetLastError();
         }
         return e;
     };
+    const auto launch = [&](auto *p, auto threads, auto hold, auto with) {
+        const uint64_t bytes = a.rows * a.vocab * sizeof(*p) * (a.grad ? 2 : 1);
+        return bytes > kLastCache && (decltype(hold)::value || !a.grad) ? launch_as(p, threads, hold, with, std::true_type())
+                                                                        : launch_as(p, threads, hold, with, std::false_type());
+    };
     const auto typed = [&](auto *p) {
+        // the fewest threads that hold a row, eight pieces each; fp32 in 1024 threads sixteen (bf16
+        // would spill)
         const uint64_t pieces = (uint64_t)a.vocab * sizeof(*p) / 16;
+        const std::integral_constant<int, 64> wave;
         const std::integral_constant<int, 256> few;
         const std::integral_constant<int, 1024> many;
         const std::integral_constant<int, 0> none;
-        if (!a.grad) return launch(p, few, none, std::false_type());
+        const std::integral_constant<int, 8> eight;
+        if (!a.grad) return pieces <= 768 ? launch(p, wave, none, std::false_type()) : launch(p, few, none, std::false_type());
         const std::true_type with;
-        if (pieces <= 256 * 8) return launch(p, few, std::integral_constant<int, 8>(), with);
-        if (pieces <= 1024 * 8) return launch(p, many, std::integral_constant<int, 8>(), with);
-        if (pieces <= 1024 * 16) return launch(p, many, std::integral_constant<int, 16>(), with);
+        if (pieces <= 64 * 8) return launch(p, wave, eight, with);
+        if (pieces <= 256 * 8) return launch(p, few, eight, with);
+        if (pieces <= 512 * 8) return launch(p, std::integral_constant<int, 512>(), eight, with);
+        if (pieces <= 1024 * 8) return launch(p, many, eight, with);
+        if constexpr (sizeof(*p) == 4)
+            if (pieces <= 1024 * 16) return launch(p, many, std::integral_constant<int, 16>(), with);
         return launch(p, many, none, with);
     };
     return bf16 ? typed(static_cast<const uint16_t *>(a.logits)) : typed(static_cast<const float *>(a.logits));

@@ -19,12 +19,21 @@ __device__ __forceinline__ constexpr int code_shift(int j) { return (j & 1) * 16
 
 // ---- codes ------------------------------------------------------------------------------
 
+// Eight neighbouring weights as they are held.
 template <class T>
-__device__ __forceinline__ void load8(const typename T::elem *p, float *v)
-{
-    T::load4(p, v);
-    T::load4(p + 4, v + 4);
-}
+struct Eight {
+    u32x4 w[8 / T::kPiece];
+    __device__ __forceinline__ void load(const typename T::elem *p)
+    {
+#pragma unroll
+        for (int h = 0; h < 8 / T::kPiece; ++h) w[h] = piece_at<T>(p + h * T::kPiece);
+    }
+    __device__ __forceinline__ void values(float *v) const
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = T::value(w[i / T::kPiece], i % T::kPiece);
+    }
+};
 __device__ __forceinline__ void store8(float *p, const float *v)
 {
     *reinterpret_cast<f32x4 *>(p) = f32x4{v[0], v[1], v[2], v[3]};
@@ -40,11 +49,15 @@ __device__ __forceinline__ float rounded(float v, const uint16_t *) { return bf1
 __device__ __forceinline__ void store1(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store1(uint16_t *p, float v) { *p = (uint16_t)pack_bf16x2(v, 0.0f); }
 
-// A block of codes per wave.
+// A block of codes per wave.  Codes are read and written as they lie, weights four rows of 256 bytes
+// (bf16) at a time: lane 16 r + p takes the values 8 p .. of the rows 4 j + r; between the two they
+// pass through LDS.  Four blocks a wave, one after another, were no faster (bf16 7168 x 28672:
+// quantizing 139 us against 131, unpacking 88 against 80).
 struct BlockAt {
-    uint32_t f, k;          // this lane's feature and first value of k
+    uint32_t f, k;          // the block's first feature and value of k
     uint64_t block;
     bool there;             // the block is
+    int r, p;
     __device__ __forceinline__ BlockAt(uint32_t d_out, uint32_t d_in)
     {
         const uint32_t nk = (d_in + kBlockK - 1) / kBlockK;
@@ -52,106 +65,165 @@ struct BlockAt {
         block = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
         const uint64_t fb = block / nk;
         there = fb * kBlockF < d_out;
-        f = (uint32_t)fb * kBlockF + (lane & 15);
-        k = (uint32_t)(block - fb * nk) * kBlockK + (lane >> 4) * 8;
+        f = (uint32_t)fb * kBlockF;
+        k = (uint32_t)(block - fb * nk) * kBlockK;
+        r = lane >> 4;
+        p = lane & 15;
     }
+    // Where the lane's word of row 4 j + r lies among the block's words.
+    __device__ __forceinline__ int word(int j) const { return (16 * (p & 3) + 4 * j + r) * 4 + (p >> 2); }
 };
+
+// The value of another lane of the 16, by the control of a data-parallel move.
+template <int kControl>
+__device__ __forceinline__ uint32_t lanes(uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kControl, 0xF, 0xF, true);
+}
+
+// A number whose last bits count whole numbers, and hold 8.
+constexpr float kCodeAt = 8388608.0f + 8.0f;
+
+// The codes of eight values of any size and scale.
+__device__ __forceinline__ uint32_t exact_codes(const float *v, float s)
+{
+    if (!(s > 0.0f)) return 0x88888888u;
+    // away from the ends of the exponent's range, where 1 / s would be lost
+    const float up = s < 0x1p-64f ? 0x1p64f : s > 0x1p64f ? 0x1p-64f : 1.0f;
+    const float t = s * up, inv = 1.0f / t, half = 0.5f * t;
+    uint32_t word = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float x = v[i] * up;
+        float q = rintf(x * inv);
+        const float r = fmaf(-q, t, x);
+        const bool odd = ((int)q & 1) != 0;
+        if (r > half || (r == half && odd)) q += 1.0f;
+        else if (r < -half || (r == -half && odd)) q -= 1.0f;
+        word |= (uint32_t)((int)fminf(fmaxf(q, -8.0f), 7.0f) + 8) << code_shift(i);
+    }
+    return word;
+}
 
 // s = max |w| / 7 over a group, rounded to the type; q - 8 is the whole number nearest to w / s,
 // ties to even, found exactly: the remainder w - q s of a quotient that is off by at most one
-// is a number of fp32.  A group of zeros has the scale 0 and the codes 8; one that holds an
-// infinity or a NaN has the scale NaN.
+// is a number of fp32; where it is not below s / 2 the quotient is looked at again.  A group of zeros
+// has the scale 0 and the codes 8; one that holds an infinity or a NaN has the scale NaN.  What bounds
+// it is VALU issue (79% of the cycles; bf16 7168 x 28672, 517 MB: 131 us).
 template <class T, int kGroup>
 __global__ __launch_bounds__(256) void k_quantize(const typename T::elem *w, uint64_t stride, uint32_t d_out,
                                                   uint32_t d_in, u32x4 *codes, typename T::elem *scales)
 {
-    constexpr int kC = kGroup / 32;                 // products of 32 values in a group
+    constexpr int kLanes = kGroup / 8;              // of a group
+    __shared__ u32x4 lds[4][64];
     const BlockAt b(d_out, d_in);
     if (!b.there) return;
     const int lane = threadIdx.x & 63;
-    float v[4][8];
+    uint32_t *words = reinterpret_cast<uint32_t *>(lds[threadIdx.x >> 6]);
+    const uint32_t k = b.k + 8 * b.p;
+    // rows behind the last read the last, values behind the last the first: none of them is kept
+    Eight<T> held[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const bool in = b.f < d_out && b.k + 32 * c < d_in;
-        if (in) load8<T>(w + (uint64_t)b.f * stride + b.k + 32 * c, v[c]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[c][j] = in ? v[c][j] : 0.0f;
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t f = b.f + 4 * j + b.r;
+        held[j].load(w + (uint64_t)(f < d_out ? f : d_out - 1) * stride + (k < d_in ? k : 0));
     }
-    u32x4 out;
 #pragma unroll
-    for (int c0 = 0; c0 < 4; c0 += kC) {
-        float top = 0.0f, sum = 0.0f;
+    for (int j = 0; j < 4; ++j) {
+        float v[8];
+        held[j].values(v);
+        uint32_t top = 0;                           // as whole numbers infinities and NaN are largest
 #pragma unroll
-        for (int c = c0; c < c0 + kC; ++c)
+        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+        top = max(top, lanes<0xB1>(top));           // the neighbour, the other pair, the other four and eight
+        top = max(top, lanes<0x4E>(top));
+        if constexpr (kLanes > 4) top = max(top, lanes<0x141>(top));
+        if constexpr (kLanes > 8) top = max(top, lanes<0x140>(top));
+        const float s = rounded(top < 0x7F800000u ? __uint_as_float(top) / 7.0f : __builtin_nanf(""), w);
+        const float inv = __builtin_amdgcn_rcpf(s), half = 0.5f * s;
+        float t[8], r[8], most = 0.0f;
+        uint32_t word = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                top = fmaxf(top, fabsf(v[c][j]));
-                sum += v[c][j] * 0.0f;              // NaN where something is not finite
-            }
-        for (int o = 16; o < 64; o <<= 1) {
-            top = fmaxf(top, __shfl_xor(top, o));
-            sum += __shfl_xor(sum, o);
+        for (int i = 0; i < 8; ++i) {
+            // rounded by the addition: the code is in the sum's last bits
+            t[i] = fmaf(v[i], inv, kCodeAt);
+            r[i] = fmaf(kCodeAt - t[i], s, v[i]);
+            most = fmaxf(most, fabsf(r[i]));
+            word += (__float_as_uint(t[i]) - __float_as_uint(kCodeAt - 8.0f)) << code_shift(i);
         }
-        const float s = rounded(sum == 0.0f ? top / 7.0f : __builtin_nanf(""), w);
-        // away from the ends of the exponent's range, where 1 / s would be lost
-        const float up = s < 0x1p-64f ? 0x1p64f : s > 0x1p64f ? 0x1p-64f : 1.0f;
-        const float t = s * up, inv = s > 0.0f ? 1.0f / t : 0.0f;
+        if (__any(most >= half)) {
+            // a quotient that its rounding took over one, or a tie (bf16: in most waves), which an
+            // odd code leaves: one further towards the remainder
 #pragma unroll
-        for (int c = c0; c < c0 + kC; ++c) {
-            uint32_t word = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float x = v[c][j] * up;
-                float q = rintf(x * inv);
-                const float r = 2.0f * fmaf(-q, t, x);          // exact
-                const bool odd = ((int)q & 1) != 0;
-                if (r > t || (r == t && odd)) q += 1.0f;
-                else if (r < -t || (r == -t && odd)) q -= 1.0f;
-                q = s > 0.0f ? fminf(fmaxf(q, -8.0f), 7.0f) : 0.0f;
-                word |= (uint32_t)((int)q + 8) << code_shift(j);
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t size = __float_as_uint(r[i]) & 0x7FFFFFFFu, odd = __float_as_uint(t[i]) & 1u;
+                const int to = 1 | ((int)__float_as_uint(r[i]) >> 31);
+                word += (uint32_t)(size + odd > __float_as_uint(half) ? to : 0) << code_shift(i);
             }
-            out[c] = word;
         }
-        const uint32_t k0 = b.k - (lane >> 4) * 8 + 32 * c0;
-        if (lane < 16 && b.f < d_out && k0 < d_in) store1(scales + (uint64_t)(k0 / kGroup) * d_out + b.f, s);
+        // a scale near an end of its range, none, or NaN
+        if (__any(!(s >= 0x1p-64f && s <= 0x1p64f))) word = exact_codes(v, s);
+        words[b.word(j)] = word;
+        const uint32_t f = b.f + 4 * j + b.r;
+        if (b.p % kLanes == 0 && f < d_out && k < d_in) store1(scales + (uint64_t)(k / kGroup) * d_out + f, s);
     }
-    codes[b.block * 64 + lane] = out;
+    wave_lds_sync();
+    codes[b.block * 64 + lane] = lds[threadIdx.x >> 6][lane];
 }
 
 // One value, 0 .. 15, a byte.
 __global__ __launch_bounds__(256) void k_pack(const uint8_t *values, uint32_t d_out, uint32_t d_in, u32x4 *codes)
 {
+    __shared__ u32x4 lds[4][64];
     const BlockAt b(d_out, d_in);
     if (!b.there) return;
-    u32x4 out = {0, 0, 0, 0};
+    const int lane = threadIdx.x & 63;
+    uint32_t *words = reinterpret_cast<uint32_t *>(lds[threadIdx.x >> 6]);
+    const uint32_t k = b.k + 8 * b.p;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        if (b.f >= d_out || b.k + 32 * c >= d_in) continue;
-        const uint2 v = *reinterpret_cast<const uint2 *>(values + (uint64_t)b.f * d_in + b.k + 32 * c);
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t f = b.f + 4 * j + b.r;
+        uint32_t word = 0;
+        if (f < d_out && k < d_in) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(values + (uint64_t)f * d_in + k);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) out[c] |= ((j < 4 ? v.x : v.y) >> 8 * (j & 3) & 15u) << code_shift(j);
+            for (int i = 0; i < 8; ++i) word |= ((i < 4 ? v.x : v.y) >> 8 * (i & 3) & 15u) << code_shift(i);
+        }
+        words[b.word(j)] = word;
     }
-    codes[b.block * 64 + (threadIdx.x & 63)] = out;
+    wave_lds_sync();
+    codes[b.block * 64 + lane] = lds[threadIdx.x >> 6][lane];
 }
 
+// What bounds it is reading and writing (bf16 7168 x 28672, 517 MB: 80 us, 6.4 TB/s).
 template <class T>
 __global__ __launch_bounds__(256) void k_unpack(const u32x4 *codes, const typename T::elem *scales,
                                                 const typename T::elem *zeros, uint32_t d_out, uint32_t d_in,
                                                 uint32_t group, typename T::elem *w)
 {
+    __shared__ u32x4 lds[4][64];
     const BlockAt b(d_out, d_in);
-    if (!b.there || b.f >= d_out) return;
-    const u32x4 word = codes[b.block * 64 + (threadIdx.x & 63)];
+    if (!b.there) return;
+    const int lane = threadIdx.x & 63;
+    const uint32_t *words = reinterpret_cast<const uint32_t *>(lds[threadIdx.x >> 6]);
+    const uint32_t k = b.k + 8 * b.p;
+    lds[threadIdx.x >> 6][lane] = codes[b.block * 64 + lane];
+    float s[4], z[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const uint32_t k = b.k + 32 * c;
-        if (k >= d_in) continue;
-        const uint64_t at = (uint64_t)(k / group) * d_out + b.f;
-        const float s = T::widen(scales[at]), z = zeros ? T::widen(zeros[at]) : 8.0f;
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t f = b.f + 4 * j + b.r;
+        const uint64_t at = (uint64_t)((k < d_in ? k : 0) / group) * d_out + (f < d_out ? f : 0);
+        s[j] = T::widen(scales[at]);
+        z[j] = zeros ? T::widen(zeros[at]) : 8.0f;
+    }
+    wave_lds_sync();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t f = b.f + 4 * j + b.r, word = words[b.word(j)];
         float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = ((float)(word[c] >> code_shift(j) & 15u) - z) * s;
-        store8(w + (uint64_t)b.f * d_in + k, v);
+        for (int i = 0; i < 8; ++i) v[i] = ((float)(word >> code_shift(i) & 15u) - z[j]) * s[j];
+        if (f < d_out && k < d_in) store8(w + (uint64_t)f * d_in + k, v);
     }
 }
 
@@ -461,8 +533,7 @@ uint32_t whole_row(uint32_t d_in) { return (d_in / T::kPiece + 1) * 16; }
 
 uint32_t block_grid(uint32_t d_out, uint32_t d_in)
 {
-    const uint64_t blocks = ((uint64_t)d_out + kBlockF - 1) / kBlockF * (((uint64_t)d_in + kBlockK - 1) / kBlockK);
-    return (uint32_t)((blocks + 3) / 4);
+    return (uint32_t)((q4_blocks(d_out, d_in) + 3) / 4);
 }
 
 struct Q4Call {

@@ -272,7 +272,8 @@ inline uint64_t q4_blocks(uint32_t d_out, uint32_t d_in)
     return ((uint64_t)d_out + 15) / 16 * (((uint64_t)d_in + 127) / 128);
 }
 // Whether so many rows are multiplied with the codes as they are; more with unpacked weights.
-inline bool q4_few(uint64_t rows, bool bf16) { return rows <= (bf16 ? 64 : 32); }
+constexpr uint32_t kQ4FewBf16 = 64, kQ4FewFp32 = 32;
+inline bool q4_few(uint64_t rows, bool bf16) { return rows <= (bf16 ? kQ4FewBf16 : kQ4FewFp32); }
 hipError_t prepare_q4();
 hipError_t launch_q4_quantize(const void *w, uint64_t stride, bool bf16, uint32_t d_out, uint32_t d_in, uint32_t group,
                               void *codes, void *scales, hipStream_t stream);

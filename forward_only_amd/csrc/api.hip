@@ -161,7 +161,7 @@ zo_status adapter_call_ok(const AdapterCall &a, bool &nothing)
 }
 
 // Shapes of weights in 4 bits.
-zo_status q4_shape(zo_dtype dtype, uint32_t d_out, uint32_t d_in, uint32_t group)
+zo_status q4_shape_ok(zo_dtype dtype, uint32_t d_out, uint32_t d_in, uint32_t group)
 {
     if (dtype != ZO_FP32 && dtype != ZO_BF16) return ZO_EINVAL;
     if (group != 32 && group != 64 && group != 128) return ZO_EINVAL;
@@ -175,8 +175,9 @@ inline bool q4_aligned(zo_dtype dtype, const void *p) { return dtype == ZO_BF16 
 // Workspace of the unpacked weights.
 inline uint64_t q4_unpacked_bytes(uint64_t rows, uint32_t d_in, uint32_t d_out, zo_dtype dtype)
 {
+    // the shapes of more rows go back and forth; so that sizes do not fall, all of them have room
     const bool bf16 = dtype == ZO_BF16;
-    return zo::q4_few(rows, bf16) ? 0 : ((uint64_t)d_in * d_out * (bf16 ? 2 : 4) + 255) / 256 * 256;
+    return rows <= (bf16 ? ZO_Q4_FEW_BF16 : ZO_Q4_FEW_FP32) ? 0 : ((uint64_t)d_in * d_out * (bf16 ? 2 : 4) + 255) / 256 * 256;
 }
 
 }  // namespace
@@ -786,7 +787,7 @@ zo_status zo_q4_quantize(zo_ctx *c, const void *d_w, uint64_t w_stride, zo_dtype
                          uint32_t d_in, uint32_t group, void *d_codes, void *d_scales, void *stream)
 {
     if (!ctx_ok(c)) return ZO_EINVAL;
-    const zo_status st = q4_shape(dtype, d_out, d_in, group);
+    const zo_status st = q4_shape_ok(dtype, d_out, d_in, group);
     if (st != ZO_OK) return st;
     if (d_out == 0 || d_in == 0) return ZO_OK;
     if (!d_w || !d_codes || !d_scales || !aligned16(d_w) || !aligned16(d_codes) || !q4_aligned(dtype, d_scales))
@@ -800,7 +801,7 @@ zo_status zo_q4_pack(zo_ctx *c, const uint8_t *d_values, uint32_t d_out, uint32_
                      void *stream)
 {
     if (!ctx_ok(c)) return ZO_EINVAL;
-    const zo_status st = q4_shape(ZO_FP32, d_out, d_in, 32);
+    const zo_status st = q4_shape_ok(ZO_FP32, d_out, d_in, 32);
     if (st != ZO_OK) return st;
     if (d_out == 0 || d_in == 0) return ZO_OK;
     if (!d_values || !d_codes || !aligned<8>(d_values) || !aligned16(d_codes)) return ZO_EINVAL;
@@ -811,7 +812,7 @@ zo_status zo_q4_unpack(zo_ctx *c, const void *d_codes, const void *d_scales, con
                        uint32_t d_out, uint32_t d_in, uint32_t group, void *d_w, void *stream)
 {
     if (!ctx_ok(c)) return ZO_EINVAL;
-    const zo_status st = q4_shape(dtype, d_out, d_in, group);
+    const zo_status st = q4_shape_ok(dtype, d_out, d_in, group);
     if (st != ZO_OK) return st;
     if (d_out == 0 || d_in == 0) return ZO_OK;
     if (!d_codes || !d_scales || !d_w || !aligned16(d_codes) || !aligned16(d_w) || !q4_aligned(dtype, d_scales) ||
@@ -837,7 +838,7 @@ zo_status zo_q4_project(zo_ctx *c, const void *d_x, uint64_t x_stride, const voi
                         uint64_t workspace_bytes, void *d_y, uint64_t y_stride, void *stream)
 {
     if (!ctx_ok(c)) return ZO_EINVAL;
-    zo_status st = q4_shape(dtype, d_out, d_in, group);
+    zo_status st = q4_shape_ok(dtype, d_out, d_in, group);
     if (st != ZO_OK) return st;
     // without groups there are no adapters, probes or signs
     const bool plain = !d_starts && !d_ids && n_groups == 0;
@@ -851,7 +852,7 @@ zo_status zo_q4_project(zo_ctx *c, const void *d_x, uint64_t x_stride, const voi
     const uint64_t params = (uint64_t)n_adapters * rank * ((uint64_t)d_in + d_out);
     const uint32_t regenerated = d_probes && !d_bits && params > 0 ? n_probes : 0;
     if (regenerated > 0 && zo_bits_stride(params) > UINT64_MAX / 2 / regenerated) return ZO_EINVAL;
-    const uint64_t need = plain && zo::q4_few(rows, dtype == ZO_BF16)
+    const uint64_t need = plain && rows <= (dtype == ZO_BF16 ? ZO_Q4_FEW_BF16 : ZO_Q4_FEW_FP32)
                               ? 0 : zo_q4_workspace_bytes(rows, d_in, d_out, dtype, n_adapters, rank, regenerated);
     if (need > 0 && (!d_workspace || !aligned<256>(d_workspace) || workspace_bytes < need)) return ZO_EINVAL;
     // x A^T and the rows' groups, unpacked weights, slices, signs
@@ -861,7 +862,7 @@ zo_status zo_q4_project(zo_ctx *c, const void *d_x, uint64_t x_stride, const voi
     void *unpacked = at;
     at += q4_unpacked_bytes(rows, d_in, d_out, dtype);
     float *slices = nullptr;
-    if (!zo::q4_few(rows, dtype == ZO_BF16) &&
+    if (zo::q4_shape(rows, d_in, d_out, dtype == ZO_BF16) == zo::Q4Shape::unpack &&
         zo::product_shape(rows, d_out, d_in, dtype == ZO_BF16) == zo::Shape::big)
         slices = reinterpret_cast<float *>(at);
     zo::AdapterArgs a = {rows, d_in, d_out, rank, n_adapters, n_groups, n_probes, scale, d_starts,

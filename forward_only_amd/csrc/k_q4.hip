@@ -335,6 +335,7 @@ __global__ __launch_bounds__(kFG * kKG * 64) void k_q4_few(Q4Args p, const typen
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int fg = wave % kFG, kg = wave / kFG;
     const uint32_t f0 = (blockIdx.x * kFG + fg) * (16 * kMF);
+    const uint64_t r0 = (uint64_t)blockIdx.y * (16 * kMR);
     // this wave's part of x: load i is step i / (2 kMR), eight rows i % (2 kMR); pieces placed as in Feed
     const typename T::elem *src[kFeed ? kFeed : 1];
     uint32_t piece[kFeed ? kFeed : 1];
@@ -342,7 +343,7 @@ __global__ __launch_bounds__(kFG * kKG * 64) void k_q4_few(Q4Args p, const typen
     for (int j = 0; j < kFeed; ++j) {
         const int i = fg * kFeed + j, r = i % (2 * kMR) * 8 + (lane >> 3);
         piece[j] = (uint32_t)(i / (2 * kMR) * 8 + ((lane & 7) ^ (r >> 1 & 7))) * T::kPiece;
-        src[j] = x + ((uint64_t)r < p.rows ? r : p.rows - 1) * p.x_stride;
+        src[j] = x + (r0 + r < p.rows ? r0 + r : p.rows - 1) * p.x_stride;
     }
     // features past the last read the last: nothing of theirs is kept
     const uint32_t groups = (p.d_in + kC * 32 - 1) / (kC * 32);
@@ -403,7 +404,7 @@ __global__ __launch_bounds__(kFG * kKG * 64) void k_q4_few(Q4Args p, const typen
     t.clear();
 #pragma unroll
     for (int n = 0; n < kMR; ++n)
-        if (n % kKG == kg) end.add_rows(t, n, f0, 16 * n);
+        if (n % kKG == kg) end.add_rows(t, n, f0, r0 + 16 * n);
     struct Sums {
         f32x4 part[kMF][kMR], sum[kMR], by[kMF], zero[kMF];
     };
@@ -520,7 +521,7 @@ __global__ __launch_bounds__(kFG * kKG * 64) void k_q4_few(Q4Args p, const typen
             for (int v = 1; v < kKG; ++v)                   // the shares after this one, in turn
                 own.acc[m][0] += sums[((((kg + v) % kKG * kFG + fg) * kMF + m) * kMR + n) * 64 + lane];
         }
-        end.store(own, f0, 16 * n);
+        end.store(own, f0, r0 + 16 * n);
     }
 }
 
@@ -542,7 +543,7 @@ struct Q4Call {
     bool zeros;
 };
 
-// f(kernel, features of a workgroup, threads, bytes of LDS) for the kernel that a call takes.
+// f(kernel, features and rows of a workgroup, threads, bytes of LDS) for the kernel that a call takes.
 template <class C, class F>
 void q4_kernel(const Q4Call &a, F f)
 {
@@ -554,9 +555,11 @@ void q4_kernel(const Q4Call &a, F f)
         const auto split = [&](auto kSplit) {
             constexpr int S = decltype(kSplit)::value;
             if (a.zeros)
-                f(&k_q4_few<C, R, M, G, K, S, true, W, EndProject<T>>, 16 * M * G, G * K * 64, q4_lds<T, R, M, G, K, S, true, W>(a.rows, row));
+                f(&k_q4_few<C, R, M, G, K, S, true, W, EndProject<T>>, 16 * M * G, 16 * R, G * K * 64,
+                  q4_lds<T, R, M, G, K, S, true, W>(a.rows, row));
             else
-                f(&k_q4_few<C, R, M, G, K, S, false, W, EndProject<T>>, 16 * M * G, G * K * 64, q4_lds<T, R, M, G, K, S, false, W>(a.rows, row));
+                f(&k_q4_few<C, R, M, G, K, S, false, W, EndProject<T>>, 16 * M * G, 16 * R, G * K * 64,
+                  q4_lds<T, R, M, G, K, S, false, W>(a.rows, row));
         };
         a.group == 128 ? split(std::integral_constant<int, 1>()) : a.group == 64 ? split(std::integral_constant<int, 2>())
                                                                                  : split(std::integral_constant<int, 4>());
@@ -567,8 +570,8 @@ void q4_kernel(const Q4Call &a, F f)
     const std::integral_constant<int, 8> eight;
     const std::true_type whole;
     const std::false_type steps;
-    // workgroups of 128 features where these are enough for the CUs
-    const bool wide = a.d_out >= 128u * 160;
+    const Q4Shape shape = q4_shape(a.rows, a.d_in, a.d_out, T::kBf16);
+    const bool wide = shape == Q4Shape::wide;
     if (a.rows <= 16 && a.rows * row <= kQ4Whole)
         wide ? sized(one, one, two, four, whole) : sized(one, one, one, eight, whole);
     else if (a.rows <= 16)
@@ -576,9 +579,11 @@ void q4_kernel(const Q4Call &a, F f)
     else if (a.rows <= 32) {
         const std::integral_constant<int, T::kBf16 ? 8 : 4> most;   // shares whose steps of x fit into LDS
         wide ? sized(two, two, four, two, steps) : sized(two, one, two, most, steps);
+    } else if constexpr (T::kBf16) {
+        if (wide) sized(four, two, four, two, steps);
+        else if (shape == Q4Shape::middle) sized(four, two, two, four, steps);
+        else if (shape == Q4Shape::narrow) sized(four, one, two, four, steps);
     }
-    else if constexpr (T::kBf16)
-        wide ? sized(four, two, four, two, steps) : sized(four, one, two, four, steps);
 }
 
 template <class C>
@@ -591,8 +596,8 @@ hipError_t few_q4(const AdapterArgs &a, const Q4Weights &w, const void *x, uint6
     const EndProject<T> end = {a, u, reinterpret_cast<int32_t *>(u + a.rows * a.rank), static_cast<const E *>(adapters),
                                static_cast<const E *>(bias), static_cast<E *>(y), y_stride};
     q4_kernel<C>({a.rows, a.d_in, a.d_out, w.group, w.zeros != nullptr},
-                 [&](auto *kernel, uint32_t features, uint32_t threads, uint32_t lds) {
-        kernel<<<(a.d_out + features - 1) / features, threads, lds, stream>>>(
+                 [&](auto *kernel, uint32_t features, uint32_t rows, uint32_t threads, uint32_t lds) {
+        kernel<<<dim3((a.d_out + features - 1) / features, (uint32_t)((a.rows + rows - 1) / rows)), threads, lds, stream>>>(
             p, static_cast<const E *>(x), static_cast<const u32x4 *>(w.codes), static_cast<const E *>(w.scales),
             static_cast<const E *>(w.zeros), end);
     });
@@ -606,10 +611,10 @@ hipError_t prepare_few()
     hipError_t e = hipSuccess;
     for (const uint64_t rows : {1, 16, 32, 64})
         for (const uint32_t d_in : {128u, 1u << 20})
-            for (const uint32_t d_out : {8u, 1u << 20})
+            for (const uint32_t d_out : {8u, 64u * 256, 1u << 20})
                 for (const uint32_t group : {32, 64, 128})
                     for (const bool zeros : {false, true})
-                        q4_kernel<C>({rows, d_in, d_out, group, zeros}, [&](auto *kernel, uint32_t, uint32_t, uint32_t lds) {
+                        q4_kernel<C>({rows, d_in, d_out, group, zeros}, [&](auto *kernel, uint32_t, uint32_t, uint32_t, uint32_t lds) {
                             if (e == hipSuccess)
                                 e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
                                                         lds > kQ4Whole ? lds : kQ4Whole);
@@ -667,7 +672,7 @@ hipError_t launch_q4_project(const AdapterArgs &a, bool bf16, const void *x, uin
                              const void *bias, const void *adapters, float *u, float *slices, void *unpacked, void *y,
                              uint64_t y_stride, hipStream_t stream)
 {
-    if (!q4_few(a.rows, bf16)) {
+    if (q4_shape(a.rows, a.d_in, a.d_out, bf16) == Q4Shape::unpack) {
         const hipError_t e = launch_q4_unpack(w, bf16, a.d_out, a.d_in, unpacked, stream);
         if (e != hipSuccess) return e;
         return launch_adapter_project(a, bf16, x, x_stride, unpacked, bias, adapters, u, slices, y, y_stride, stream);

@@ -204,9 +204,11 @@ __host__ __device__ constexpr uint32_t big_slices(uint32_t over, uint32_t steps)
 // 256 x 256 takes 1.45 us (bf16; fp32 7.5), a round of 512 tiles of 64 x 64 0.48 us (1.17),
 // or 0.33 us (0.77) while they are at most one per CU (fp32 128 rows, 4096 to 8192: 106 us; in
 // sliced tiles of 256 x 256 165); slices cost 25 us to write and add up.
-inline Shape product_shape(uint64_t rows, uint32_t features, uint32_t k, bool bf16)
+struct ProductTime {
+    double mid, big;           // us
+};
+inline ProductTime product_time(uint64_t rows, uint32_t features, uint32_t k, bool bf16)
 {
-    if (rows <= 32 || (rows <= 64 && features <= 32u * 256 * (bf16 ? 1 : 3))) return Shape::few;
     const auto tiles = [&](uint64_t size) {
         return ((uint64_t)features + size - 1) / size * ((rows + size - 1) / size);
     };
@@ -216,7 +218,13 @@ inline Shape product_shape(uint64_t rows, uint32_t features, uint32_t k, bool bf
     const uint32_t slices = big_slices((uint32_t)over, steps);
     const double part = over == 0 ? 0.0 : slices > 1 ? 1.0 / slices : 1.0;
     const double big = (bf16 ? 1.45 : 7.5) * ((double)(b / kBigSlots) + part);
-    return steps * big + (over && slices > 1 ? 25.0 : 0.0) <= steps * mid ? Shape::big : Shape::mid;
+    return {steps * mid, steps * big + (over && slices > 1 ? 25.0 : 0.0)};
+}
+inline Shape product_shape(uint64_t rows, uint32_t features, uint32_t k, bool bf16)
+{
+    if (rows <= 32 || (rows <= 64 && features <= 32u * 256 * (bf16 ? 1 : 3))) return Shape::few;
+    const ProductTime t = product_time(rows, features, k, bf16);
+    return t.big <= t.mid ? Shape::big : Shape::mid;
 }
 // Features of a workgroup of Shape::few.  With more than 16 rows a CU holds one, and a round of
 // 64 features takes 1.6 times one of 32.
@@ -271,15 +279,38 @@ inline uint64_t q4_blocks(uint32_t d_out, uint32_t d_in)
 {
     return ((uint64_t)d_out + 15) / 16 * (((uint64_t)d_in + 127) / 128);
 }
-// Whether so many rows are multiplied with the codes as they are; more with unpacked weights.
-constexpr uint32_t kQ4FewBf16 = 64, kQ4FewFp32 = 32;
-inline bool q4_few(uint64_t rows, bool bf16) { return rows <= (bf16 ? kQ4FewBf16 : kQ4FewFp32); }
+// How rows are multiplied with codes: as they are, in tiles of at most 64 rows (fp32 32) and as many
+// features a workgroup, or unpacked first.
+enum class Q4Shape { narrow, middle, wide, unpack };
+constexpr uint32_t kQ4FewBf16 = 64, kQ4FewFp32 = 32;   // rows that are never unpacked
+// By estimated time.  Measured per block of 128 values of k, 64 rows of bf16, a round of one
+// workgroup a CU: 128 features 0.82 us, 64 features 0.48, 32 features 0.37; unpacking runs at 5.5 TB/s.
+// (bf16 5120 -> 20480, 128 / 256 / 512 rows: 58 / 96 / 164 us as they are, 116 / 129 / 157 unpacked;
+// 5120 -> 5120 19 / 36 / 54 and 45 / 48 / 55.)  Up to 32 rows workgroups of 128 features where these are
+// enough for the CUs.
+inline Q4Shape q4_shape(uint64_t rows, uint32_t d_in, uint32_t d_out, bool bf16)
+{
+    if (rows <= 32) return d_out >= 128u * 160 ? Q4Shape::wide : Q4Shape::narrow;
+    if (!bf16) return Q4Shape::unpack;
+    const double blocks = (d_in + 127) / 128;
+    const auto time = [&](uint32_t features, double each) {
+        const uint64_t groups = ((uint64_t)d_out + features - 1) / features * ((rows + 63) / 64);
+        return (double)((groups + 255) / 256) * each * blocks;
+    };
+    const double n = time(32, 0.37), m = time(64, 0.48), w = time(128, 0.82);
+    const double best = n <= m && n <= w ? n : m <= w ? m : w;
+    if (rows > kQ4FewBf16) {
+        const ProductTime t = product_time(rows, d_out, d_in, true);
+        if ((double)d_in * d_out * 2.5 / 5.5e6 + 4.0 + (t.big < t.mid ? t.big : t.mid) < best) return Q4Shape::unpack;
+    }
+    return best == n ? Q4Shape::narrow : best == m ? Q4Shape::middle : Q4Shape::wide;
+}
 hipError_t prepare_q4();
 hipError_t launch_q4_quantize(const void *w, uint64_t stride, bool bf16, uint32_t d_out, uint32_t d_in, uint32_t group,
                               void *codes, void *scales, hipStream_t stream);
 hipError_t launch_q4_pack(const uint8_t *values, uint32_t d_out, uint32_t d_in, void *codes, hipStream_t stream);
 hipError_t launch_q4_unpack(const Q4Weights &q, bool bf16, uint32_t d_out, uint32_t d_in, void *w, hipStream_t stream);
-// As launch_adapter_project; unpacked: d_out * d_in elements unless q4_few.
+// As launch_adapter_project; unpacked: d_out * d_in elements if the shape asks for them.
 hipError_t launch_q4_project(const AdapterArgs &a, bool bf16, const void *x, uint64_t x_stride, const Q4Weights &w,
                              const void *bias, const void *adapters, float *u, float *slices, void *unpacked, void *y,
                              uint64_t y_stride, hipStream_t stream);

@@ -554,7 +554,7 @@ zo_status zo_head_grad(zo_ctx *ctx, const void *d_hidden, uint64_t hidden_stride
  * half if k / 2 % 2 == 0, else in the high half.  What lies beyond the matrix is not used. */
 uint64_t zo_q4_code_bytes(uint32_t d_out, uint32_t d_in);
 
-/* Most rows that zo_q4_project multiplies with the codes as they are. */
+/* Rows that zo_q4_project always multiplies with the codes as they are. */
 #define ZO_Q4_FEW_BF16 64u
 #define ZO_Q4_FEW_FP32 32u
 
@@ -582,8 +582,9 @@ zo_status zo_q4_unpack(zo_ctx *ctx, const void *d_codes, const void *d_scales, c
 
 /* zo_adapter_project with W in 4 bits: y = x W^T + bias + scale (x A_g^T) B_g^T, all weights read as
  * they are held.  x, scales, zeros, bias, adapters and y share `dtype`.  d_starts and d_ids may both be NULL
- * with n_groups == 0: all rows without adapters.  Up to ZO_Q4_FEW_BF16 rows (or ZO_Q4_FEW_FP32) the weights
- * are not rounded; beyond, they are unpacked into the workspace first, rounded to the dtype.  x beyond 2^100 may
+ * with n_groups == 0: all rows without adapters.  Up to ZO_Q4_FEW_BF16 rows (or ZO_Q4_FEW_FP32), and of
+ * more where that is estimated to be faster (bf16, up to some hundred), the weights are not rounded; else they are
+ * unpacked into the workspace first, rounded to the dtype.  x beyond 2^100 may
  * overflow on the way (a code enters as 128 + q, fp32 sums).  A weight that is NaN or infinite makes its
  * feature NaN or infinite in every row, a value of x that is makes its row so, perhaps NaN.
  * d_workspace: at least zo_q4_workspace_bytes(...) bytes, 256-byte aligned; sizes never fall as rows grow.

@@ -17,31 +17,46 @@
 namespace zo {
 namespace {
 
-// How many of the counted rows are in each piece.
-__global__ void k_pieces(const uint32_t *count, uint64_t piece, uint32_t pieces, uint32_t *counts)
+// y[c][r] = x[row(r)][c] for `rows` places r (as many as *count, if given; list says which row each is,
+// nullptr: place = row) and `cols` columns c, zeros from there to the next multiple of 8 places.  y's rows
+// lie `pitch` apart, a multiple of 8.
+template <class T>
+struct Turn {
+    const typename T::elem *x;
+    uint64_t stride, rows;
+    const uint32_t *list, *count;
+    uint32_t cols;
+    typename T::elem *y;
+    uint64_t pitch;
+    uint32_t tiles_r, tiles;       // tiles of 64 x 64: along the places, and all
+};
+template <class T>
+Turn<T> turn(const typename T::elem *x, uint64_t stride, uint64_t rows, const uint32_t *list, const uint32_t *count,
+             uint32_t cols, typename T::elem *y, uint64_t pitch)
 {
-    for (uint32_t i = threadIdx.x; i < pieces; i += 256) counts[i] = (uint32_t)places(i * piece, piece, count);
+    const uint32_t r = (uint32_t)((rows + 63) / 64);
+    return {x, stride, rows, list, count, cols, y, pitch, r, r * ((cols + 63) / 64)};
 }
 
-// y[c][r] = x[row(r)][c] for `rows` places r (as many as *count, if given) and `cols` columns c, zeros
-// from there to the next multiple of 8 places.  y's rows lie `pitch` apart, a multiple of 8.  A
-// workgroup takes 64 x 64 values through LDS.  What bounds it is reading and writing them.
+// A workgroup takes 64 x 64 values through LDS.  What bounds it is reading and writing them.
 template <class T>
-__global__ __launch_bounds__(256) void k_turn(const typename T::elem *x, uint64_t stride, uint64_t rows,
-                                              const uint32_t *count, uint32_t cols, typename T::elem *y, uint64_t pitch)
+__device__ __forceinline__ void turn_tile(const Turn<T> &a, uint32_t t)
 {
     typedef typename T::elem E;
     constexpr int kPiece = T::kPiece, kRowPieces = 64 / kPiece, kPitch = 64 + 4 / (int)sizeof(E);
     __shared__ E tile[64 * kPitch];
-    const uint64_t have = places(0, rows, count);
-    const uint64_t r0 = (uint64_t)blockIdx.x * 64;
-    const uint32_t c0 = blockIdx.y * 64;
+    const uint64_t have = places(0, a.rows, a.count);
+    const uint64_t r0 = (uint64_t)(t % a.tiles_r) * 64;
+    const uint32_t c0 = t / a.tiles_r * 64;
     if (r0 >= (have + 7) / 8 * 8) return;
 #pragma unroll
     for (int i = threadIdx.x; i < 64 * kRowPieces; i += 256) {
         const int r = i / kRowPieces, c = i % kRowPieces * kPiece;
         u32x4 v = {0, 0, 0, 0};
-        if (r0 + r < have && c0 + c < cols) v = piece_at<T>(x + (r0 + r) * stride + c0 + c);
+        if (r0 + r < have && c0 + c < a.cols) {
+            const uint64_t row = a.list ? a.list[r0 + r] : r0 + r;
+            v = piece_at<T>(a.x + row * a.stride + c0 + c);
+        }
         const E *e = reinterpret_cast<const E *>(&v);
 #pragma unroll
         for (int j = 0; j < kPiece; ++j) tile[r * kPitch + c + j] = e[j];
@@ -50,28 +65,40 @@ __global__ __launch_bounds__(256) void k_turn(const typename T::elem *x, uint64_
 #pragma unroll
     for (int i = threadIdx.x; i < 64 * kRowPieces; i += 256) {
         const int c = i / kRowPieces, r = i % kRowPieces * kPiece;
-        if (c0 + c >= cols || r0 + r >= (have + 7) / 8 * 8) continue;
+        if (c0 + c >= a.cols || r0 + r >= (have + 7) / 8 * 8) continue;
         u32x4 v;
         E *e = reinterpret_cast<E *>(&v);
 #pragma unroll
         for (int j = 0; j < kPiece; ++j) e[j] = tile[(r + j) * kPitch + c];
-        *reinterpret_cast<u32x4 *>(y + (uint64_t)(c0 + c) * pitch + r0 + r) = v;
+        *reinterpret_cast<u32x4 *>(a.y + (uint64_t)(c0 + c) * a.pitch + r0 + r) = v;
     }
 }
 
-// The rows that count, one after another.
+// What the products need of the operands, in one launch: W and h turned over, the rows that count one
+// after another, and zeros in the hidden gradients of the others (a nullptr, or no tiles: not wanted).
 template <class T>
-__global__ __launch_bounds__(256) void k_gather(const typename T::elem *x, uint64_t stride, uint64_t rows,
-                                                const uint32_t *count, const uint32_t *list, uint32_t d,
-                                                typename T::elem *out)
+__global__ __launch_bounds__(256) void k_operands(Turn<T> w, Turn<T> h, const typename T::elem *x, uint64_t stride,
+                                                  uint64_t rows, const int64_t *targets, const uint32_t *count,
+                                                  const uint32_t *list, uint32_t d, typename T::elem *out,
+                                                  typename T::elem *hidden_grad)
 {
+    if (blockIdx.x < w.tiles) return turn_tile(w, blockIdx.x);
+    if (blockIdx.x < w.tiles + h.tiles) return turn_tile(h, blockIdx.x - w.tiles);
     const uint64_t have = places(0, rows, count);
-    for (uint64_t at = blockIdx.x; at < have; at += gridDim.x) {
-        const typename T::elem *from = x + (uint64_t)list[at] * stride;
-        for (uint32_t i = threadIdx.x; i < d / T::kPiece; i += 256)
-            reinterpret_cast<u32x4 *>(out + at * d)[i] = piece_at<T>(from + i * T::kPiece);
+    for (uint64_t at = blockIdx.x - w.tiles - h.tiles; at < rows; at += gridDim.x - w.tiles - h.tiles) {
+        if (at < have) {
+            const typename T::elem *from = x + (uint64_t)list[at] * stride;
+            for (uint32_t i = threadIdx.x; i < d / T::kPiece; i += 256)
+                reinterpret_cast<u32x4 *>(out + at * d)[i] = piece_at<T>(from + i * T::kPiece);
+        }
+        if (hidden_grad && targets[at] == kIgnoreToken)
+            for (uint32_t i = threadIdx.x; i < d / T::kPiece; i += 256)
+                reinterpret_cast<u32x4 *>(hidden_grad + at * d)[i] = u32x4{0, 0, 0, 0};
     }
 }
+
+template <class T>
+__global__ __launch_bounds__(256) void k_turn(Turn<T> a) { turn_tile(a, blockIdx.x); }
 
 // The ending that keeps the logits beside their statistics: [place][pitch] fp32.
 struct EndLogits {
@@ -280,18 +307,6 @@ struct EndRows {
     }
 };
 
-__device__ __forceinline__ void store_zeros(void *p, uint64_t pieces, uint32_t from, uint32_t step)
-{
-    for (uint64_t i = from; i < pieces; i += step) static_cast<u32x4 *>(p)[i] = u32x4{0, 0, 0, 0};
-}
-
-// Zeros in the rows that do not count.
-__global__ __launch_bounds__(256) void k_ignored(const int64_t *targets, uint64_t rows, uint64_t row_bytes, char *out)
-{
-    for (uint64_t r = blockIdx.x; r < rows; r += gridDim.x)
-        if (targets[r] == kIgnoreToken) store_zeros(out + r * row_bytes, row_bytes / 16, threadIdx.x, 256);
-}
-
 __global__ __launch_bounds__(256) void k_zeros(u32x4 *p, uint64_t n)
 {
     for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (uint64_t)gridDim.x * 256) p[i] = u32x4{0, 0, 0, 0};
@@ -329,27 +344,25 @@ struct Held {
     }
 };
 
-constexpr int kOuterThreads = 128;
-
 // Both products of at most kR rows in one pass over W and dW: a wave takes 64 kPer neighbouring
-// columns of kGradChunk features, a lane kPer of them with its values of h and of its sums of dh in
+// columns of `chunk` features, a lane kPer of them with its values of h and of its sums of dh in
 // registers; D, from the logits, lies in LDS, where the waves of a workgroup read it at once.
 // All in fp32, D is not rounded.  What bounds it is reading W and writing dW.
 template <class T, int kR, int kPer>
 __global__ __launch_bounds__(kOuterThreads) void k_outer(const float *logits, uint64_t pitch_v, RowsOf a, const typename T::elem *x,
-                                               uint64_t x_stride, const typename T::elem *w, uint32_t d, float *parts,
-                                               typename T::elem *dw)
+                                               uint64_t x_stride, const typename T::elem *w, uint32_t d, uint32_t chunk,
+                                               float *parts, typename T::elem *dw)
 {
     typedef typename T::elem E;
     constexpr int kAhead = 4;
     __shared__ float share[kGradChunk][kR];
-    const uint32_t v0 = blockIdx.x * kGradChunk;
-    const uint32_t n = a.features - v0 < kGradChunk ? a.features - v0 : kGradChunk;
+    const uint32_t v0 = blockIdx.x * chunk;
+    const uint32_t n = a.features - v0 < chunk ? a.features - v0 : chunk;
 #pragma unroll 2
-    for (int i = threadIdx.x; i < kR * (int)kGradChunk; i += kOuterThreads) {
-        const uint32_t r = i / kGradChunk, v = i % kGradChunk;
+    for (uint32_t i = threadIdx.x; i < kR * n; i += kOuterThreads) {
+        const uint32_t r = i / n, v = i % n;
         float s = 0.0f;
-        if (r < a.rows && v < n) {
+        if (r < a.rows) {
             const int64_t tgt = a.targets[r];
             if (tgt != kIgnoreToken) {
                 const float2 norm = a.norms[r];
@@ -464,12 +477,14 @@ hipError_t few_rows(const HeadGradArgs &h, const HeadGradSpace &s, const typenam
                           s.norms}, stream);
     if (e != hipSuccess || (!h.hidden_grad && !h.weight_grad)) return e;
     const RowsOf rows = {h.targets, nullptr, nullptr, static_cast<const float2 *>(s.norms), h.row_grad, h.rows, h.features};
-    const uint32_t chunks = (h.features + kGradChunk - 1) / kGradChunk;
+    uint32_t chunks = 0;
     float *sums = h.hidden_grad ? s.parts : nullptr;
     const auto launch = [&](auto most, auto per) {
         constexpr int kR = decltype(most)::value, kPer = decltype(per)::value;
+        const uint32_t chunk = grad_chunk(h.features, h.d, kPer);
+        chunks = (h.features + chunk - 1) / chunk;
         k_outer<T, kR, kPer><<<dim3(chunks, (h.d + kOuterThreads * kPer - 1) / (kOuterThreads * kPer)), kOuterThreads, 0, stream>>>(
-            s.logits, s.pitch_v, rows, x, h.x_stride, w, h.d, sums, static_cast<E *>(h.weight_grad));
+            s.logits, s.pitch_v, rows, x, h.x_stride, w, h.d, chunk, sums, static_cast<E *>(h.weight_grad));
     };
     const std::integral_constant<int, 4> four;
     if (h.rows <= 8) launch(std::integral_constant<int, 8>(), std::integral_constant<int, T::kPiece>());
@@ -495,16 +510,15 @@ hipError_t head_grad(const HeadGradArgs &h, const void *hidden, const void *weig
     if (h.rows <= kGradFew) return few_rows<T>(h, s, static_cast<const E *>(hidden), w, stream);
     E *x = static_cast<E *>(s.x), *xt = static_cast<E *>(s.xt), *wt = static_cast<E *>(s.wt);
     E *d = static_cast<E *>(s.d), *dt = static_cast<E *>(s.dt);
-    hipError_t e = launch_counted(h.targets, h.rows, s.list, s.count, h.logp, nullptr, stream);
+    const E *hp = static_cast<const E *>(hidden);
+    hipError_t e = launch_counted(h.targets, h.rows, s.list, s.count, h.logp, nullptr, stream, s.piece, (uint32_t)s.pieces,
+                                  s.counts);
     if (e != hipSuccess) return e;
-    k_pieces<<<1, 256, 0, stream>>>(s.count, s.piece, (uint32_t)s.pieces, s.counts);
-    const uint32_t all = (uint32_t)(h.rows < 8192 ? h.rows : 8192);
-    k_gather<T><<<all, 256, 0, stream>>>(static_cast<const E *>(hidden), h.x_stride, h.rows, s.count, s.list, h.d, x);
-    const auto grid = [](uint64_t rows, uint64_t cols) { return dim3((uint32_t)((rows + 63) / 64), (uint32_t)((cols + 63) / 64)); };
-    if (h.hidden_grad) {
-        k_turn<T><<<grid(h.features, h.d), 256, 0, stream>>>(w, h.d, h.features, nullptr, h.d, wt, s.pitch_v);
-        k_ignored<<<all, 256, 0, stream>>>(h.targets, h.rows, (uint64_t)h.d * sizeof(E), static_cast<char *>(h.hidden_grad));
-    }
+    Turn<T> turn_w = {}, turn_h = {};
+    if (h.hidden_grad) turn_w = turn<T>(w, h.d, h.features, nullptr, nullptr, h.d, wt, s.pitch_v);
+    if (h.weight_grad && s.pieces == 1) turn_h = turn<T>(hp, h.x_stride, h.rows, s.list, s.count, h.d, xt, s.pitch_x);
+    k_operands<T><<<turn_w.tiles + turn_h.tiles + (uint32_t)(h.rows < 8192 ? h.rows : 8192), 256, 0, stream>>>(
+        turn_w, turn_h, hp, h.x_stride, h.rows, h.targets, s.count, s.list, h.d, x, static_cast<E *>(h.hidden_grad));
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     const Shape shape = product_shape(s.piece, h.features, h.d, T::kBf16);
@@ -535,9 +549,12 @@ hipError_t head_grad(const HeadGradArgs &h, const void *hidden, const void *weig
         }
         if (h.weight_grad) {
             const uint32_t k = (uint32_t)s.pitch_x;
-            k_turn<T><<<grid(n, h.d), 256, 0, stream>>>(px, h.d, n, count, h.d, xt, s.pitch_x);
-            e = hipGetLastError();
-            if (e != hipSuccess) return e;
+            if (s.pieces > 1) {
+                const Turn<T> t = turn<T>(px, h.d, n, nullptr, count, h.d, xt, s.pitch_x);
+                k_turn<T><<<t.tiles, 256, 0, stream>>>(t);
+                e = hipGetLastError();
+                if (e != hipSuccess) return e;
+            }
             const ProductArgs p = {0, h.features, k, k, h.d, s.slices, count};
             const EndRows<T> out = {h.d, h.features, nullptr, nullptr, nullptr, static_cast<E *>(h.weight_grad), s.sum, s.count,
                                     first, first + n};

@@ -9,11 +9,13 @@ namespace {
 
 // ---- joining the head's partial statistics ----------------------------------------------
 
-// The places of the rows that count, in order, and zeros for the others' outputs; one
-// workgroup, eight rows of a thread in flight at once.
+// The places of the rows that count, in order, and zeros for the others' outputs; how many are in
+// each of `pieces` pieces of so many places.  One workgroup, eight rows of a thread in flight at
+// once.
 __global__ __launch_bounds__(1024) void k_counted(const int64_t *targets, uint64_t rows,
                                                   uint32_t *list, uint32_t *count, float *logp,
-                                                  float *entropy)
+                                                  float *entropy, uint64_t piece, uint32_t pieces,
+                                                  uint32_t *counts)
 {
     constexpr int kAtOnce = 8;
     __shared__ uint32_t waves[kAtOnce][16];
@@ -51,6 +53,8 @@ __global__ __launch_bounds__(1024) void k_counted(const int64_t *targets, uint64
         __syncthreads();
     }
     if (tid == 0) *count = at;
+    for (uint32_t i = tid; i < pieces; i += 1024)
+        counts[i] = at <= i * piece ? 0 : (uint32_t)(at - i * piece < piece ? at - i * piece : piece);
 }
 
 // Joins the parts of each place: kOf places per workgroup of 1024 threads.  Eight read whole
@@ -208,9 +212,9 @@ hipError_t prepare()
 }  // namespace
 
 hipError_t launch_counted(const int64_t *targets, uint64_t rows, uint32_t *list, uint32_t *count, float *logp,
-                          float *entropy, hipStream_t stream)
+                          float *entropy, hipStream_t stream, uint64_t piece, uint32_t pieces, uint32_t *counts)
 {
-    k_counted<<<1, 1024, 0, stream>>>(targets, rows, list, count, logp, entropy);
+    k_counted<<<1, 1024, 0, stream>>>(targets, rows, list, count, logp, entropy, piece, pieces, counts);
     return hipGetLastError();
 }
 

@@ -337,9 +337,10 @@ struct HeadJoin {
 };
 hipError_t launch_head_join(const HeadJoin &j, hipStream_t stream);
 // list: the rows whose target is not ignored, in order; count: how many; zeros for the others'
-// logp and entropy (or nullptr).
+// logp and entropy (or nullptr); counts: how many are in each of `pieces` pieces of the list.
 hipError_t launch_counted(const int64_t *targets, uint64_t rows, uint32_t *list, uint32_t *count, float *logp,
-                          float *entropy, hipStream_t stream);
+                          float *entropy, hipStream_t stream, uint64_t piece = 0, uint32_t pieces = 0,
+                          uint32_t *counts = nullptr);
 // Rows whose partial statistics are held at once.
 constexpr uint64_t kHeadPlaces = 16384;
 struct HeadSpace {
@@ -394,9 +395,17 @@ struct HeadGradArgs {
 };
 // Rows are taken in pieces of at most this many logits, and at least 256 rows.
 constexpr uint64_t kGradLogits = (uint64_t)1 << 28;
-// Rows of which the products are formed value by value (k_outer); its values of the vocabulary a wave.
+// Rows of which the products are formed value by value (k_outer), its threads, and the features that a
+// workgroup takes: fewer than kGradChunk where that leaves CUs without one (one row, 512 -> 1000: 93 us
+// with 256, 23 with 8).
 constexpr uint64_t kGradFew = 16;
-constexpr uint32_t kGradChunk = 256;
+constexpr uint32_t kGradChunk = 256, kOuterThreads = 128;
+inline uint32_t grad_chunk(uint32_t features, uint32_t d, uint32_t per)
+{
+    const uint64_t columns = ((uint64_t)d + kOuterThreads * per - 1) / (kOuterThreads * per);
+    const uint64_t c = (features * columns / 1024 + 7) / 8 * 8;
+    return c < 8 ? 8 : c > kGradChunk ? kGradChunk : (uint32_t)c;
+}
 struct HeadGradSpace {
     uint32_t *count, *counts, *list;
     void *norms, *x, *xt, *d, *dt, *wt;
@@ -432,7 +441,8 @@ inline HeadGradSpace head_grad_space(uint64_t rows, uint32_t d, uint32_t feature
     s.tl = static_cast<float *>(take(s.piece * 4));
     s.logits = static_cast<float *>(take(s.piece * s.pitch_v * 4));
     const uint64_t few = rows < kGradFew ? rows : kGradFew;
-    s.parts = static_cast<float *>(take(((uint64_t)features + kGradChunk - 1) / kGradChunk * few * d * 4));
+    const auto chunks = [&](uint32_t per) { return ((uint64_t)features + grad_chunk(features, d, per) - 1) / grad_chunk(features, d, per); };
+    s.parts = static_cast<float *>(take((chunks(4) > chunks(8) ? chunks(4) : chunks(8)) * few * d * 4));
     if (rows > kGradFew) {
         s.x = take(rows * d * size);
         s.xt = take(s.pitch_x * d * size);

@@ -11,6 +11,8 @@
 // g, turned over, for dW.  The products take their operands along the neighbouring values that they
 // sum over, so h and W are turned over, too.  Pieces after the first add to dW in fp32.
 //
+// Of large fp32 products the operands are split into bf16 (Split).
+//
 // Few rows: reading W twice and writing dW bounds it (k_outer).
 #include "zo_product.hpp"
 
@@ -18,37 +20,62 @@ namespace zo {
 namespace {
 
 // y[c][r] = x[row(r)][c] for `rows` places r (as many as *count, if given; list says which row each is,
-// nullptr: place = row) and `cols` columns c, zeros from there to the next multiple of 8 places.  y's rows
-// lie `pitch` apart, a multiple of 8.
-template <class T>
+// nullptr: place = row) and `cols` columns c, zeros from there to the next multiple of 8 places, as
+// operands P.  y's rows lie P::pitch(pitch) apart, pitch a multiple of 8.
+template <class T, class P>
 struct Turn {
     const typename T::elem *x;
     uint64_t stride, rows;
     const uint32_t *list, *count;
     uint32_t cols;
-    typename T::elem *y;
+    typename P::elem *y;
     uint64_t pitch;
     uint32_t tiles_r, tiles;       // tiles of 64 x 64: along the places, and all
 };
-template <class T>
-Turn<T> turn(const typename T::elem *x, uint64_t stride, uint64_t rows, const uint32_t *list, const uint32_t *count,
-             uint32_t cols, typename T::elem *y, uint64_t pitch)
+template <class T, class P>
+Turn<T, P> turn(const typename T::elem *x, uint64_t stride, uint64_t rows, const uint32_t *list, const uint32_t *count,
+                uint32_t cols, typename P::elem *y, uint64_t pitch)
 {
     const uint32_t r = (uint32_t)((rows + 63) / 64);
     return {x, stride, rows, list, count, cols, y, pitch, r, r * ((cols + 63) / 64)};
 }
 
-// A workgroup takes 64 x 64 values through LDS.  What bounds it is reading and writing them.
+// 64 x 64 values in LDS, written by rows and read by columns, eight at a time.
 template <class T>
-__device__ __forceinline__ void turn_tile(const Turn<T> &a, uint32_t t)
+struct Square {
+    typedef typename T::elem E;
+    static constexpr int kPitch = 64 + 4 / (int)sizeof(E);
+    E *tile;
+    __device__ __forceinline__ void put(int r, int c, const float *v, int n) const
+    {
+#pragma unroll
+        for (int j = 0; j < n; ++j) {
+            if constexpr (T::kBf16) tile[r * kPitch + c + j] = (E)pack_bf16x2(v[j], 0.0f);
+            else tile[r * kPitch + c + j] = v[j];
+        }
+    }
+    template <class P>
+    __device__ __forceinline__ void store(int c, int r, typename P::elem *row, uint64_t k) const
+    {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = T::widen(tile[(r + j) * kPitch + c]);
+        P::store8(row, k, v);
+    }
+};
+
+// A workgroup takes 64 x 64 values through LDS.  What bounds it is reading and writing them.
+template <class T, class P>
+__device__ __forceinline__ void turn_tile(const Turn<T, P> &a, uint32_t t)
 {
     typedef typename T::elem E;
-    constexpr int kPiece = T::kPiece, kRowPieces = 64 / kPiece, kPitch = 64 + 4 / (int)sizeof(E);
-    __shared__ E tile[64 * kPitch];
-    const uint64_t have = places(0, a.rows, a.count);
+    constexpr int kPiece = T::kPiece, kRowPieces = 64 / kPiece;
+    __shared__ E values[64 * Square<T>::kPitch];
+    const Square<T> tile = {values};
+    const uint64_t have = places(0, a.rows, a.count), padded = (have + 7) / 8 * 8;
     const uint64_t r0 = (uint64_t)(t % a.tiles_r) * 64;
     const uint32_t c0 = t / a.tiles_r * 64;
-    if (r0 >= (have + 7) / 8 * 8) return;
+    if (r0 >= padded) return;
 #pragma unroll
     for (int i = threadIdx.x; i < 64 * kRowPieces; i += 256) {
         const int r = i / kRowPieces, c = i % kRowPieces * kPiece;
@@ -59,46 +86,63 @@ __device__ __forceinline__ void turn_tile(const Turn<T> &a, uint32_t t)
         }
         const E *e = reinterpret_cast<const E *>(&v);
 #pragma unroll
-        for (int j = 0; j < kPiece; ++j) tile[r * kPitch + c + j] = e[j];
+        for (int j = 0; j < kPiece; ++j) values[r * Square<T>::kPitch + c + j] = e[j];
     }
     __syncthreads();
 #pragma unroll
-    for (int i = threadIdx.x; i < 64 * kRowPieces; i += 256) {
-        const int c = i / kRowPieces, r = i % kRowPieces * kPiece;
-        if (c0 + c >= a.cols || r0 + r >= (have + 7) / 8 * 8) continue;
-        u32x4 v;
-        E *e = reinterpret_cast<E *>(&v);
+    for (int i = threadIdx.x; i < 64 * 8; i += 256) {
+        const int c = i / 8, r = i % 8 * 8;
+        // split operands: zeros up to the next multiple of 64
+        if (c0 + c >= a.cols || (P::kTerms == 1 && r0 + r >= padded)) continue;
+        tile.template store<P>(c, r, a.y + (c0 + c) * P::pitch(a.pitch), r0 + r);
+    }
+}
+
+// A row of d values as operands P.
+template <class T, class P>
+__device__ __forceinline__ void copy_row(const typename T::elem *from, uint32_t d, typename P::elem *to)
+{
+    const uint32_t n = P::kTerms == 1 ? d : (d + 63) / 64 * 64;
+    for (uint32_t k = threadIdx.x * 8; k < n; k += 256 * 8) {
+        float v[8];
 #pragma unroll
-        for (int j = 0; j < kPiece; ++j) e[j] = tile[(r + j) * kPitch + c];
-        *reinterpret_cast<u32x4 *>(a.y + (uint64_t)(c0 + c) * a.pitch + r0 + r) = v;
+        for (int i = 0; i < 8; i += T::kPiece) {
+            u32x4 w = {0, 0, 0, 0};
+            if (k < d) w = piece_at<T>(from + k + i);
+#pragma unroll
+            for (int j = 0; j < T::kPiece; ++j) v[i + j] = T::value(w, j);
+        }
+        P::store8(to, k, v);
     }
 }
 
 // What the products need of the operands, in one launch: W and h turned over, the rows that count one
-// after another, and zeros in the hidden gradients of the others (a nullptr, or no tiles: not wanted).
-template <class T>
-__global__ __launch_bounds__(256) void k_operands(Turn<T> w, Turn<T> h, const typename T::elem *x, uint64_t stride,
+// after another, W's rows (if they are to be split), and zeros in the hidden gradients of the rows that
+// do not count (a nullptr, or no tiles: not wanted).
+template <class T, class P>
+__global__ __launch_bounds__(256) void k_operands(Turn<T, P> w, Turn<T, P> h, const typename T::elem *x, uint64_t stride,
                                                   uint64_t rows, const int64_t *targets, const uint32_t *count,
-                                                  const uint32_t *list, uint32_t d, typename T::elem *out,
-                                                  typename T::elem *hidden_grad)
+                                                  const uint32_t *list, uint32_t d, typename P::elem *out,
+                                                  typename T::elem *hidden_grad, const typename T::elem *weight,
+                                                  uint32_t features, typename P::elem *weight_out)
 {
     if (blockIdx.x < w.tiles) return turn_tile(w, blockIdx.x);
     if (blockIdx.x < w.tiles + h.tiles) return turn_tile(h, blockIdx.x - w.tiles);
     const uint64_t have = places(0, rows, count);
-    for (uint64_t at = blockIdx.x - w.tiles - h.tiles; at < rows; at += gridDim.x - w.tiles - h.tiles) {
-        if (at < have) {
-            const typename T::elem *from = x + (uint64_t)list[at] * stride;
-            for (uint32_t i = threadIdx.x; i < d / T::kPiece; i += 256)
-                reinterpret_cast<u32x4 *>(out + at * d)[i] = piece_at<T>(from + i * T::kPiece);
-        }
+    const uint32_t first = blockIdx.x - w.tiles - h.tiles, all = gridDim.x - w.tiles - h.tiles;
+    for (uint64_t at = first; at < rows; at += all) {
+        if (at < have) copy_row<T, P>(x + (uint64_t)list[at] * stride, d, out + at * P::pitch(d));
         if (hidden_grad && targets[at] == kIgnoreToken)
             for (uint32_t i = threadIdx.x; i < d / T::kPiece; i += 256)
                 reinterpret_cast<u32x4 *>(hidden_grad + at * d)[i] = u32x4{0, 0, 0, 0};
     }
+    if constexpr (P::kTerms > 1)
+        for (uint64_t at = first; at < features; at += all)
+            copy_row<T, P>(weight + at * d, d, weight_out + at * P::pitch(d));
 }
 
-template <class T>
-__global__ __launch_bounds__(256) void k_turn(Turn<T> a) { turn_tile(a, blockIdx.x); }
+template <class T, class P>
+__global__ __launch_bounds__(256) void k_turn(Turn<T, P> a) { turn_tile(a, blockIdx.x); }
 
 // The ending that keeps the logits beside their statistics: [place][pitch] fp32.
 struct EndLogits {
@@ -144,64 +188,54 @@ struct RowsOf {
 };
 
 // d[r][v] = p - [v = t_r] and dt[v][r] = g_r (p - [v = t_r]) of a piece's places (either may be
-// nullptr), zeros behind the features and from the last place to the next multiple of 8.  A workgroup
-// takes 64 x 64 values, turned over through LDS.  What bounds it is reading 4 and writing 4 bytes a value.
-template <class T>
-__global__ __launch_bounds__(256) void k_shares(const float *logits, RowsOf a, typename T::elem *d, typename T::elem *dt,
+// nullptr), zeros behind the features and from the last place to the next multiple of 8, as operands
+// P.  A workgroup takes 64 x 64 values, turned over through LDS.  What bounds it is reading 4 bytes
+// and writing 4 (bf16), 8 or 12 (split) a value.
+template <class T, class P>
+__global__ __launch_bounds__(256) void k_shares(const float *logits, RowsOf a, typename P::elem *d, typename P::elem *dt,
                                                 uint64_t pitch_v, uint64_t pitch_x)
 {
-    typedef typename T::elem E;
-    constexpr int kPitch = 64 + 4 / (int)sizeof(E);
-    __shared__ E tile[64 * kPitch];
+    __shared__ typename T::elem values[64 * Square<T>::kPitch];
+    const Square<T> tile = {values};
     const uint64_t have = places(0, a.rows, a.count), padded = (have + 7) / 8 * 8;
     const uint64_t r0 = (uint64_t)blockIdx.y * 64;
     const uint32_t f0 = blockIdx.x * 64;
     if (r0 >= padded) return;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < 64 * 16; i += 256) {
-        const int r = i / 16, f = i % 16 * 4;
+#pragma unroll 2
+    for (int i = threadIdx.x; i < 64 * 8; i += 256) {
+        const int r = i / 8, f = i % 8 * 8;
         const uint64_t at = r0 + r;
-        const bool in = at < have && f0 + f < pitch_v;
-        f32x4 v = {0, 0, 0, 0};
-        float g = 0.0f;
-        if (in) {
+        float v[8], scaled[8], g = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+        if (at < have && f0 + f < pitch_v) {
             const uint64_t row = a.list[at];
             const float2 norm = a.norms[at];
             const int64_t tgt = a.targets[row] - f0;
             g = a.row_grad ? a.row_grad[row] : 1.0f;
-            const f32x4 l = *reinterpret_cast<const f32x4 *>(logits + at * pitch_v + f0 + f);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float p = fast_exp((l[j] - norm.x) - norm.y);
-                v[j] = f0 + f + j < a.features ? p - (tgt == f + j ? 1.0f : 0.0f) : 0.0f;
+            for (int h = 0; h < 2; ++h) {
+                const f32x4 l = *reinterpret_cast<const f32x4 *>(logits + at * pitch_v + f0 + f + 4 * h);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float p = fast_exp((l[j] - norm.x) - norm.y);
+                    const int c = f + 4 * h + j;
+                    v[4 * h + j] = f0 + c < a.features ? p - (tgt == c ? 1.0f : 0.0f) : 0.0f;
+                }
             }
-            if (d) EndProject<T>::store4(d + at * pitch_v + f0 + f, v);
         }
-        f32x4 scaled;
+        if (d && at < have && (P::kTerms > 1 || f0 + f < pitch_v)) P::store8(d + at * P::pitch(pitch_v), f0 + f, v);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) scaled[j] = in ? g * v[j] : 0.0f;
-        E e[4];
-        if constexpr (T::kBf16) {
-            const uint32_t lo = pack_bf16x2(scaled[0], scaled[1]), hi = pack_bf16x2(scaled[2], scaled[3]);
-            e[0] = (E)lo, e[1] = (E)(lo >> 16), e[2] = (E)hi, e[3] = (E)(hi >> 16);
-        } else {
-            for (int j = 0; j < 4; ++j) e[j] = scaled[j];
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) tile[r * kPitch + f + j] = e[j];
+        for (int j = 0; j < 8; ++j) scaled[j] = at < have ? g * v[j] : 0.0f;
+        tile.put(r, f, scaled, 8);
     }
     if (!dt) return;
     __syncthreads();
-    constexpr int kPiece = T::kPiece, kRowPieces = 64 / kPiece;
 #pragma unroll
-    for (int i = threadIdx.x; i < 64 * kRowPieces; i += 256) {
-        const int f = i / kRowPieces, r = i % kRowPieces * kPiece;
-        if (f0 + f >= a.features || r0 + r >= padded) continue;
-        u32x4 v;
-        E *e = reinterpret_cast<E *>(&v);
-#pragma unroll
-        for (int j = 0; j < kPiece; ++j) e[j] = tile[(r + j) * kPitch + f];
-        *reinterpret_cast<u32x4 *>(dt + (uint64_t)(f0 + f) * pitch_x + r0 + r) = v;
+    for (int i = threadIdx.x; i < 64 * 8; i += 256) {
+        const int f = i / 8, r = i % 8 * 8;
+        if (f0 + f >= a.features || (P::kTerms == 1 && r0 + r >= padded)) continue;
+        tile.template store<P>(f, r, dt + (uint64_t)(f0 + f) * P::pitch(pitch_x), r0 + r);
     }
 }
 
@@ -496,73 +530,110 @@ hipError_t few_rows(const HeadGradArgs &h, const HeadGradSpace &s, const typenam
     return hipGetLastError();
 }
 
-template <class T>
-hipError_t head_grad(const HeadGradArgs &h, const void *hidden, const void *weight, hipStream_t stream)
+template <class P, class End>
+hipError_t multiply(const ProductArgs &p, const typename P::elem *x, const typename P::elem *w, const uint32_t *count,
+                    const End &end, hipStream_t stream)
+{
+    if constexpr (P::kTerms > 1) return big<P>(p, x, w, nullptr, count, end, stream);
+    else return by_shape<P>(product_shape(p.rows, p.features, p.k, P::kBf16), p, x, w, nullptr, count, end, stream);
+}
+
+// Rows in pieces, with operands P.
+template <class T, class P>
+hipError_t many_rows(const HeadGradArgs &h, const HeadGradSpace &s, const typename T::elem *hidden,
+                     const typename T::elem *weight, hipStream_t stream)
 {
     typedef typename T::elem E;
-    const E *w = static_cast<const E *>(weight);
-    if (h.rows == 0) {
-        if (h.weight_grad)
-            k_zeros<<<2048, 256, 0, stream>>>(static_cast<u32x4 *>(h.weight_grad), (uint64_t)h.features * h.d / T::kPiece);
-        return hipGetLastError();
-    }
-    const HeadGradSpace s = head_grad_space(h.rows, h.d, h.features, T::kBf16, h.workspace);
-    if (h.rows <= kGradFew) return few_rows<T>(h, s, static_cast<const E *>(hidden), w, stream);
-    E *x = static_cast<E *>(s.x), *xt = static_cast<E *>(s.xt), *wt = static_cast<E *>(s.wt);
-    E *d = static_cast<E *>(s.d), *dt = static_cast<E *>(s.dt);
-    const E *hp = static_cast<const E *>(hidden);
+    typedef typename P::elem O;
+    O *x = static_cast<O *>(s.x), *xt = static_cast<O *>(s.xt), *wt = static_cast<O *>(s.wt);
+    O *d = static_cast<O *>(s.d), *dt = static_cast<O *>(s.dt);
+    const O *w = nullptr;
+    if constexpr (P::kTerms > 1) w = static_cast<const O *>(s.w);
+    else w = weight;
     hipError_t e = launch_counted(h.targets, h.rows, s.list, s.count, h.logp, nullptr, stream, s.piece, (uint32_t)s.pieces,
                                   s.counts);
     if (e != hipSuccess) return e;
-    Turn<T> turn_w = {}, turn_h = {};
-    if (h.hidden_grad) turn_w = turn<T>(w, h.d, h.features, nullptr, nullptr, h.d, wt, s.pitch_v);
-    if (h.weight_grad && s.pieces == 1) turn_h = turn<T>(hp, h.x_stride, h.rows, s.list, s.count, h.d, xt, s.pitch_x);
-    k_operands<T><<<turn_w.tiles + turn_h.tiles + (uint32_t)(h.rows < 8192 ? h.rows : 8192), 256, 0, stream>>>(
-        turn_w, turn_h, hp, h.x_stride, h.rows, h.targets, s.count, s.list, h.d, x, static_cast<E *>(h.hidden_grad));
+    Turn<T, P> turn_w = {}, turn_h = {};
+    if (h.hidden_grad) turn_w = turn<T, P>(weight, h.d, h.features, nullptr, nullptr, h.d, wt, s.pitch_v);
+    if (h.weight_grad && s.pieces == 1)
+        turn_h = turn<T, P>(hidden, h.x_stride, h.rows, s.list, s.count, h.d, xt, s.pitch_x);
+    const uint64_t copies = P::kTerms > 1 && h.features > h.rows ? h.features : h.rows;
+    k_operands<T, P><<<turn_w.tiles + turn_h.tiles + (uint32_t)(copies < 8192 ? copies : 8192), 256, 0, stream>>>(
+        turn_w, turn_h, hidden, h.x_stride, h.rows, h.targets, s.count, s.list, h.d, x, static_cast<E *>(h.hidden_grad),
+        weight, h.features, static_cast<O *>(s.w));
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const Shape shape = product_shape(s.piece, h.features, h.d, T::kBf16);
+    const Shape shape = P::kTerms > 1 ? Shape::big : product_shape(s.piece, h.features, h.d, T::kBf16);
     const uint32_t part = shape_part(shape, s.piece, h.features), parts = (h.features + part - 1) / part;
     for (uint64_t i = 0; i < s.pieces; ++i) {
         const uint64_t first = i * s.piece, n = h.rows - first < s.piece ? h.rows - first : s.piece;
         const uint32_t *count = s.counts + i, *list = s.list + first;
-        const E *px = x + first * h.d;
-        const ProductArgs logits = {0, n, h.d, h.d, h.features, s.slices};
+        const O *px = x + first * P::pitch(h.d);
+        // every piece in the shape of the first, whose statistics are as many
+        const ProductArgs logits = {0, n, P::pitch(h.d), h.d, h.features, s.slices};
         const EndLogits end = {{h.features, 0, n, h.targets, list, count, s.m, s.s, s.t, s.tl}, s.logits, s.pitch_v};
-        e = by_shape<T>(shape, logits, px, w, nullptr, count, end, stream);
+        if constexpr (P::kTerms > 1) e = big<P>(logits, px, w, nullptr, count, end, stream);
+        else e = by_shape<P>(shape, logits, px, w, nullptr, count, end, stream);
         if (e != hipSuccess) return e;
         e = launch_head_join({s.m, s.s, s.t, s.tl, parts, 0, n, list, count, h.targets, h.features, h.logp, nullptr, s.norms},
                              stream);
         if (e != hipSuccess) return e;
         if (!h.hidden_grad && !h.weight_grad) continue;
         const RowsOf rows = {h.targets, list, count, static_cast<const float2 *>(s.norms), h.row_grad, n, h.features};
-        k_shares<T><<<dim3((uint32_t)((s.pitch_v + 63) / 64), (uint32_t)((n + 63) / 64)), 256, 0, stream>>>(
+        k_shares<T, P><<<dim3((uint32_t)((s.pitch_v + 63) / 64), (uint32_t)((n + 63) / 64)), 256, 0, stream>>>(
             s.logits, rows, h.hidden_grad ? d : nullptr, h.weight_grad ? dt : nullptr, s.pitch_v, s.pitch_x);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
         if (h.hidden_grad) {
             const uint32_t k = (uint32_t)s.pitch_v;
-            const ProductArgs p = {0, n, k, k, h.d, s.slices};
+            const ProductArgs p = {0, n, P::pitch(k), k, h.d, s.slices};
             const EndRows<T> out = {h.d, n, list, count, h.row_grad, static_cast<E *>(h.hidden_grad), nullptr, s.count, 0, 0};
-            e = by_shape<T>(product_shape(n, h.d, k, T::kBf16), p, d, wt, nullptr, count, out, stream);
+            e = multiply<P>(p, d, wt, count, out, stream);
             if (e != hipSuccess) return e;
         }
         if (h.weight_grad) {
             const uint32_t k = (uint32_t)s.pitch_x;
             if (s.pieces > 1) {
-                const Turn<T> t = turn<T>(px, h.d, n, nullptr, count, h.d, xt, s.pitch_x);
-                k_turn<T><<<t.tiles, 256, 0, stream>>>(t);
+                const Turn<T, P> t = turn<T, P>(hidden, h.x_stride, n, list, count, h.d, xt, s.pitch_x);
+                k_turn<T, P><<<t.tiles, 256, 0, stream>>>(t);
                 e = hipGetLastError();
                 if (e != hipSuccess) return e;
             }
-            const ProductArgs p = {0, h.features, k, k, h.d, s.slices, count};
+            const ProductArgs p = {0, h.features, P::pitch(k), k, h.d, s.slices, count};
             const EndRows<T> out = {h.d, h.features, nullptr, nullptr, nullptr, static_cast<E *>(h.weight_grad), s.sum, s.count,
                                     first, first + n};
-            e = by_shape<T>(product_shape(h.features, h.d, k, T::kBf16), p, dt, xt, nullptr, nullptr, out, stream);
+            e = multiply<P>(p, dt, xt, nullptr, out, stream);
             if (e != hipSuccess) return e;
         }
     }
     return hipSuccess;
+}
+
+template <class T>
+hipError_t head_grad(const HeadGradArgs &h, const void *hidden, const void *weight, hipStream_t stream)
+{
+    typedef typename T::elem E;
+    const E *x = static_cast<const E *>(hidden), *w = static_cast<const E *>(weight);
+    if (h.rows == 0) {
+        if (h.weight_grad)
+            k_zeros<<<2048, 256, 0, stream>>>(static_cast<u32x4 *>(h.weight_grad), (uint64_t)h.features * h.d / T::kPiece);
+        return hipGetLastError();
+    }
+    const HeadGradSpace s = head_grad_space(h.rows, h.d, h.features, T::kBf16, h.workspace);
+    if (h.rows <= kGradFew) return few_rows<T>(h, s, x, w, stream);
+    if constexpr (!T::kBf16)
+        if (grad_split(s.piece, h.d, h.features)) return many_rows<T, Split>(h, s, x, w, stream);
+    return many_rows<T, T>(h, s, x, w, stream);
+}
+
+template <class End>
+hipError_t raise_split()
+{
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&k_big<Split, End>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, 2 * 512 * 128);
+    return e != hipSuccess ? e
+                           : hipFuncSetAttribute(reinterpret_cast<const void *>(&k_big<Split, EndSlice>),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, 2 * 512 * 128);
 }
 
 template <class T, class End>
@@ -588,7 +659,7 @@ hipError_t raise_end()
 hipError_t prepare_head_grad()
 {
     const hipError_t all[] = {raise_end<Bf16, EndLogits>(), raise_end<Bf16, EndRows<Bf16>>(), raise_end<Fp32, EndLogits>(),
-                              raise_end<Fp32, EndRows<Fp32>>()};
+                              raise_end<Fp32, EndRows<Fp32>>(), raise_split<EndLogits>(), raise_split<EndRows<Fp32>>()};
     for (const hipError_t e : all)
         if (e != hipSuccess) return e;
     return hipSuccess;

@@ -397,7 +397,7 @@ struct HeadGradArgs {
 constexpr uint64_t kGradLogits = (uint64_t)1 << 28;
 // Rows of which the products are formed value by value (k_outer), its threads, and the features that a
 // workgroup takes: fewer than kGradChunk where that leaves CUs without one (one row, 512 -> 1000: 93 us
-// with 256, 23 with 8).
+// with 256, 20 with 8).
 constexpr uint64_t kGradFew = 16;
 constexpr uint32_t kGradChunk = 256, kOuterThreads = 128;
 inline uint32_t grad_chunk(uint32_t features, uint32_t d, uint32_t per)
@@ -406,9 +406,35 @@ inline uint32_t grad_chunk(uint32_t features, uint32_t d, uint32_t per)
     const uint64_t c = (features * columns / 1024 + 7) / 8 * 8;
     return c < 8 ? 8 : c > kGradChunk ? kGradChunk : (uint32_t)c;
 }
+// Values of an fp32 row split into three bf16 each, and the time of a product of such rows: six of
+// bf16's.
+constexpr uint64_t split_bytes(uint64_t k) { return (k + 63) / 64 * 384; }
+inline bool split_fits(uint64_t rows, uint64_t features, uint64_t k)
+{
+    // operands reach 64 GiB, a tile of one 32 bits of 16-byte units
+    return k <= 1u << 22 && rows * split_bytes(k) <= (uint64_t)1 << 36 && features * split_bytes(k) <= (uint64_t)1 << 36;
+}
+inline double split_time(uint64_t rows, uint32_t features, uint32_t k)
+{
+    return product_time(rows, features, (k + 63) / 64 * 384, true).big;
+}
+// Whether the three products of zo_head_grad take split fp32 operands: by their estimated times and the
+// bytes that splitting writes, at 5 TB/s.
+inline bool grad_split(uint64_t rows, uint32_t d, uint32_t features)
+{
+    if (!split_fits(rows, features, d) || !split_fits(rows, d, features) || !split_fits(features, d, (uint32_t)rows)) return false;
+    const auto plain = [](uint64_t r, uint32_t f, uint32_t k) {
+        const ProductTime t = product_time(r, f, k, false);
+        return t.big < t.mid ? t.big : t.mid;
+    };
+    const uint32_t r = (uint32_t)rows;
+    const double as = split_time(rows, features, d) + split_time(rows, d, features) + split_time(features, d, r);
+    const double bytes = 12.0 * features * d + 4.0 * rows * features;
+    return as + bytes / 5e6 < plain(rows, features, d) + plain(rows, d, features) + plain(features, d, r);
+}
 struct HeadGradSpace {
     uint32_t *count, *counts, *list;
-    void *norms, *x, *xt, *d, *dt, *wt;
+    void *norms, *x, *xt, *d, *dt, *wt, *w;
     float *m, *s, *t, *tl, *logits, *sum, *parts, *slices;
     uint64_t piece, pieces;        // rows of a piece, and their number
     uint64_t pitch_x, pitch_v;     // rows of a piece and features, to a multiple of 8
@@ -416,7 +442,6 @@ struct HeadGradSpace {
 };
 inline HeadGradSpace head_grad_space(uint64_t rows, uint32_t d, uint32_t features, bool bf16, void *base)
 {
-    const uint64_t size = bf16 ? 2 : 4;
     HeadGradSpace s = {};
     s.pitch_v = ((uint64_t)features + 7) / 8 * 8;
     const uint64_t fits = kGradLogits / (s.pitch_v ? s.pitch_v : 1) / 256 * 256, most = fits < 256 ? 256 : fits;
@@ -444,11 +469,14 @@ inline HeadGradSpace head_grad_space(uint64_t rows, uint32_t d, uint32_t feature
     const auto chunks = [&](uint32_t per) { return ((uint64_t)features + grad_chunk(features, d, per) - 1) / grad_chunk(features, d, per); };
     s.parts = static_cast<float *>(take((chunks(4) > chunks(8) ? chunks(4) : chunks(8)) * few * d * 4));
     if (rows > kGradFew) {
-        s.x = take(rows * d * size);
-        s.xt = take(s.pitch_x * d * size);
-        s.d = take(s.piece * s.pitch_v * size);
-        s.dt = take(s.pitch_x * features * size);
-        s.wt = take(s.pitch_v * d * size);
+        // fp32: room for split operands; rows that are not split now may be with fewer
+        const auto row = [&](uint64_t k) { return bf16 ? k * 2 : split_bytes(k); };
+        s.x = take(rows * row(d));
+        s.xt = take(d * row(s.pitch_x));
+        s.d = take(s.piece * row(s.pitch_v));
+        s.dt = take(features * row(s.pitch_x));
+        s.wt = take(d * row(s.pitch_v));
+        if (!bf16) s.w = take(features * row(d));
         s.slices = static_cast<float *>(take(kBigSliceBytes));
         if (s.pieces > 1) s.sum = static_cast<float *>(take((uint64_t)features * d * 4));
     }

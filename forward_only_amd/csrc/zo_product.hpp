@@ -29,6 +29,15 @@ struct Bf16 {
     typedef uint16_t elem;
     static constexpr bool kBf16 = true;
     static constexpr int kPiece = 8;    // elements per 16-byte piece
+    static constexpr int kTerms = 1;
+    static __host__ __device__ __forceinline__ uint32_t steps(uint32_t k) { return (k + 8 * kPiece - 1) / (8 * kPiece); }
+    static __host__ __device__ __forceinline__ uint64_t pitch(uint64_t k) { return k; }
+    static __device__ __forceinline__ uint32_t place(uint32_t step, bool) { return step; }
+    static __device__ __forceinline__ void store8(uint16_t *row, uint64_t k, const float *v)
+    {
+        *reinterpret_cast<u32x4 *>(row + k) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                    pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    }
     static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c)
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
@@ -85,6 +94,15 @@ struct Fp32 {
     typedef float elem;
     static constexpr bool kBf16 = false;
     static constexpr int kPiece = 4;
+    static constexpr int kTerms = 1;
+    static __host__ __device__ __forceinline__ uint32_t steps(uint32_t k) { return (k + 8 * kPiece - 1) / (8 * kPiece); }
+    static __host__ __device__ __forceinline__ uint64_t pitch(uint64_t k) { return k; }
+    static __device__ __forceinline__ uint32_t place(uint32_t step, bool) { return step; }
+    static __device__ __forceinline__ void store8(float *row, uint64_t k, const float *v)
+    {
+        *reinterpret_cast<f32x4 *>(row + k) = f32x4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<f32x4 *>(row + k + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    }
     static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c)
     {
 #pragma unroll
@@ -113,6 +131,49 @@ struct Fp32 {
     {
         return Wide{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
                     __float_as_uint(v[3])};
+    }
+};
+
+// fp32 operands as three bf16 each, x = x0 + x1 + x2 exactly (8 bits of x's 24 each, cut off, not
+// rounded), and a product as six of theirs: x0 w0 + x0 w1 + x1 w0 + x0 w2 + x2 w0 + x1 w1.  What is left
+// out is below 2^-21 |x w|, on average 2^-23, as much as an fp32 sum of a few terms rounds.  bf16 MFMA is
+// 9 to 10 times as fast as fp32.  A row holds its values 64 at a time: 64 x0, 64 x1, 64 x2, with
+// zeros behind the last value.  An infinity becomes NaN.
+struct Split {
+    typedef uint16_t elem;
+    static constexpr bool kBf16 = true;
+    static constexpr int kPiece = 8, kTerms = 6;
+    static __host__ __device__ __forceinline__ uint32_t steps(uint32_t k) { return (k + 63) / 64 * kTerms; }
+    static __host__ __device__ __forceinline__ uint64_t pitch(uint64_t k) { return (k + 63) / 64 * 192; }
+    // Where the 64 values of a step lie, in steps.
+    static __device__ __forceinline__ uint32_t place(uint32_t step, bool w)
+    {
+        const uint32_t block = step / kTerms, term = step - block * kTerms;
+        return block * 3 + ((w ? 0x484u : 0x610u) >> (2 * term) & 3u);
+    }
+    static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) { return Bf16::mma(a, b, c); }
+    // Eight values, from value k (a multiple of 8) of a row on.
+    static __device__ __forceinline__ void store8(uint16_t *row, uint64_t k, const float *v)
+    {
+        u32x4 o[3];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t half[3][2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float x = v[2 * i + j];
+                const float r = x - __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
+                const float s = r - __uint_as_float(__float_as_uint(r) & 0xFFFF0000u);
+                half[0][j] = __float_as_uint(x) >> 16;
+                half[1][j] = __float_as_uint(r) >> 16;
+                half[2][j] = __float_as_uint(s) >> 16;
+            }
+#pragma unroll
+            for (int p = 0; p < 3; ++p) o[p][i] = half[p][0] | half[p][1] << 16;
+        }
+        uint16_t *to = row + k / 64 * 192 + k % 64;
+#pragma unroll
+        for (int p = 0; p < 3; ++p) *reinterpret_cast<u32x4 *>(to + 64 * p) = o[p];
     }
 };
 
@@ -801,7 +862,8 @@ __global__ __launch_bounds__(512, 2) void k_big(ProductArgs p, const typename T:
     enum { F0, F1, R0, R1 };
     extern __shared__ u32x4 stage[];                        // [2][F0, F1, R0, R1][128][kPieces]
     const uint64_t rows = places(p.base, p.rows, count);
-    const uint32_t depth = p.depth(), steps = (depth + kStep - 1) / kStep;
+    const uint32_t depth = p.depth(), steps = T::steps(depth);
+    const uint64_t pitch = T::pitch(p.k);
     const Cut cut(p, rows, steps);
     uint32_t tile, first = 0, last = steps;
     if constexpr (End::kSlices) {
@@ -828,7 +890,7 @@ __global__ __launch_bounds__(512, 2) void k_big(ProductArgs p, const typename T:
     const uint32_t piece = (uint32_t)((lane & 7) ^ ((wave * 4 + (lane >> 4)) & 7)) * T::kPiece;
     // Sources in 16-byte units from the tile's first weight and from x: registers are short
     // here, and 32 bits of units reach 64 GiB.
-    const u32x4 *const from_w = reinterpret_cast<const u32x4 *>(w + (uint64_t)f0 * p.k);
+    const u32x4 *const from_w = reinterpret_cast<const u32x4 *>(w + f0 * pitch);
     const u32x4 *const from_x = reinterpret_cast<const u32x4 *>(x);
     uint32_t src[4][2];
 #pragma unroll
@@ -837,17 +899,17 @@ __global__ __launch_bounds__(512, 2) void k_big(ProductArgs p, const typename T:
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const uint32_t f = (i >> 6) * 128 + h * 64 + (i & 63);
-            src[F0 + h][j] = (uint32_t)(((uint64_t)(f0 + f < p.features ? f : p.features - 1 - f0) * p.k + piece) / T::kPiece);
+            src[F0 + h][j] = (uint32_t)(((f0 + f < p.features ? f : p.features - 1 - f0) * pitch + piece) / T::kPiece);
             const uint64_t at = r0 + (i >> 5) * 64 + h * 32 + (i & 31);
             const uint64_t r = at < rows ? at : rows - 1;
             src[R0 + h][j] = (uint32_t)(((list ? list[p.base + r] : p.base + r) * p.x_stride + piece) / T::kPiece);
         }
     }
     const auto issue = [&](int part, uint32_t step) {
-        const bool in = step < last && (uint64_t)step * kStep + piece < depth;
+        const bool in = step < last && (T::kTerms > 1 || (uint64_t)step * kStep + piece < depth);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const u32x4 *g = (part < R0 ? from_w : from_x) + (uint64_t)step * kPieces + src[part][j];
+            const u32x4 *g = (part < R0 ? from_w : from_x) + (uint64_t)T::place(step, part < R0) * kPieces + src[part][j];
             if (!in) g = &kZeros;
             u32x4 *l = stage + ((step & 1) * 4 + part) * kPart + (j * 64 + wave * 8) * kPieces;
             __builtin_amdgcn_global_load_lds((gptr_t)g, (lptr_t)l, 16, 0, 0);
@@ -940,7 +1002,7 @@ __global__ __launch_bounds__(256) void k_slices(ProductArgs p, const uint32_t *c
 {
     __shared__ u32x4 lds[3 * 8 * 64];
     const uint64_t rows = places(p.base, p.rows, count);
-    const Cut cut(p, rows, (p.depth() + 8 * T::kPiece - 1) / (8 * T::kPiece));
+    const Cut cut(p, rows, T::steps(p.depth()));
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t i = blockIdx.x / 32, of = blockIdx.x / 4 % 8, n = blockIdx.x % 4;
@@ -1147,7 +1209,7 @@ hipError_t big(const ProductArgs &p, const typename T::elem *x, const typename T
     if (n > kLaunchThreads / 512) return hipErrorInvalidValue;
     // without a count the tiles are known: no workgroups for slices that there are not
     const uint32_t over = (uint32_t)(n % kBigSlots);
-    const uint32_t steps = (p.k + 8 * T::kPiece - 1) / (8 * T::kPiece);
+    const uint32_t steps = T::steps(p.k);
     const bool sliced = p.slices && steps >= 2 * kBigSliceSteps && (count || big_slices(over, steps) > 1);
     hipError_t e = hipSuccess;
     if (count || p.k_count || !sliced || n > over) {

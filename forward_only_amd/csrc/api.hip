@@ -172,14 +172,6 @@ zo_status q4_shape_ok(zo_dtype dtype, uint32_t d_out, uint32_t d_in, uint32_t gr
 }
 // Four neighbouring scales or zeros are one load.
 inline bool q4_aligned(zo_dtype dtype, const void *p) { return dtype == ZO_BF16 ? aligned<8>(p) : aligned16(p); }
-// Workspace of the unpacked weights.
-inline uint64_t q4_unpacked_bytes(uint64_t rows, uint32_t d_in, uint32_t d_out, zo_dtype dtype)
-{
-    // the shapes of more rows go back and forth; so that sizes do not fall, all of them have room
-    const bool bf16 = dtype == ZO_BF16;
-    return rows <= (bf16 ? ZO_Q4_FEW_BF16 : ZO_Q4_FEW_FP32) ? 0 : ((uint64_t)d_in * d_out * (bf16 ? 2 : 4) + 255) / 256 * 256;
-}
-
 }  // namespace
 
 extern "C" {
@@ -825,8 +817,9 @@ zo_status zo_q4_unpack(zo_ctx *c, const void *d_codes, const void *d_scales, con
 uint64_t zo_q4_workspace_bytes(uint64_t rows, uint32_t d_in, uint32_t d_out, zo_dtype dtype, uint32_t n_adapters,
                                uint32_t rank, uint32_t regenerated)
 {
-    return zo_adapter_workspace_bytes(rows, d_in, d_out, n_adapters, rank, 0, regenerated) +
-           q4_unpacked_bytes(rows, d_in, d_out, dtype);
+    const uint64_t params = (uint64_t)n_adapters * rank * ((uint64_t)d_in + d_out);
+    return zo::adapter_u_bytes(rows, rank) + zo::q4_space(rows, d_in, d_out, dtype == ZO_BF16, nullptr).bytes +
+           (uint64_t)regenerated * zo_bits_stride(params);
 }
 
 zo_status zo_q4_project(zo_ctx *c, const void *d_x, uint64_t x_stride, const void *d_codes, const void *d_scales,
@@ -855,16 +848,10 @@ zo_status zo_q4_project(zo_ctx *c, const void *d_x, uint64_t x_stride, const voi
     const uint64_t need = plain && rows <= (dtype == ZO_BF16 ? ZO_Q4_FEW_BF16 : ZO_Q4_FEW_FP32)
                               ? 0 : zo_q4_workspace_bytes(rows, d_in, d_out, dtype, n_adapters, rank, regenerated);
     if (need > 0 && (!d_workspace || !aligned<256>(d_workspace) || workspace_bytes < need)) return ZO_EINVAL;
-    // x A^T and the rows' groups, unpacked weights, slices, signs
-    char *at = static_cast<char *>(d_workspace);
-    float *u = reinterpret_cast<float *>(at);
-    at += zo::adapter_u_bytes(rows, rank);
-    void *unpacked = at;
-    at += q4_unpacked_bytes(rows, d_in, d_out, dtype);
-    float *slices = nullptr;
-    if (zo::q4_shape(rows, d_in, d_out, dtype == ZO_BF16) == zo::Q4Shape::unpack &&
-        zo::product_shape(rows, d_out, d_in, dtype == ZO_BF16) == zo::Shape::big)
-        slices = reinterpret_cast<float *>(at);
+    // x A^T and the rows' groups, what unpacking takes, signs
+    float *u = static_cast<float *>(d_workspace);
+    const zo::Q4Space space = zo::q4_space(rows, d_in, d_out, dtype == ZO_BF16,
+                                           static_cast<char *>(d_workspace) + zo::adapter_u_bytes(rows, rank));
     zo::AdapterArgs a = {rows, d_in, d_out, rank, n_adapters, n_groups, n_probes, scale, d_starts,
                          d_ids, d_probes, d_alphas, d_bits, zo_bits_stride(params)};
     if (regenerated > 0) {
@@ -876,7 +863,7 @@ zo_status zo_q4_project(zo_ctx *c, const void *d_x, uint64_t x_stride, const voi
         a.bits = bits;
     }
     return from_hip(zo::launch_q4_project(a, dtype == ZO_BF16, d_x, x_stride, {d_codes, d_scales, d_zeros, group},
-                                          d_bias, d_adapters, u, slices, unpacked, d_y, y_stride, as_stream(stream)));
+                                          d_bias, d_adapters, u, space, d_y, y_stride, as_stream(stream)));
 }
 
 uint64_t zo_head_grad_workspace_bytes(uint64_t rows, uint32_t d, uint32_t vocab, zo_dtype dtype)

@@ -34,16 +34,6 @@ struct Eight {
         for (int i = 0; i < 8; ++i) v[i] = T::value(w[i / T::kPiece], i % T::kPiece);
     }
 };
-__device__ __forceinline__ void store8(float *p, const float *v)
-{
-    *reinterpret_cast<f32x4 *>(p) = f32x4{v[0], v[1], v[2], v[3]};
-    *reinterpret_cast<f32x4 *>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
-}
-__device__ __forceinline__ void store8(uint16_t *p, const float *v)
-{
-    *reinterpret_cast<u32x4 *>(p) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                          pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
-}
 __device__ __forceinline__ float rounded(float v, const float *) { return v; }
 __device__ __forceinline__ float rounded(float v, const uint16_t *) { return bf16lo_to_f32(pack_bf16x2(v, 0.0f)); }
 __device__ __forceinline__ void store1(float *p, float v) { *p = v; }
@@ -195,11 +185,12 @@ __global__ __launch_bounds__(256) void k_pack(const uint8_t *values, uint32_t d_
     codes[b.block * 64 + lane] = lds[threadIdx.x >> 6][lane];
 }
 
-// What bounds it is reading and writing (bf16 7168 x 28672, 517 MB: 80 us, 6.4 TB/s).
-template <class T>
+// The weights, as operands P.  What bounds it is reading and writing (bf16 7168 x 28672, 517 MB: 80 us,
+// 6.4 TB/s).
+template <class T, class P>
 __global__ __launch_bounds__(256) void k_unpack(const u32x4 *codes, const typename T::elem *scales,
                                                 const typename T::elem *zeros, uint32_t d_out, uint32_t d_in,
-                                                uint32_t group, typename T::elem *w)
+                                                uint32_t group, typename P::elem *w)
 {
     __shared__ u32x4 lds[4][64];
     const BlockAt b(d_out, d_in);
@@ -223,7 +214,25 @@ __global__ __launch_bounds__(256) void k_unpack(const u32x4 *codes, const typena
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = ((float)(word >> code_shift(i) & 15u) - z[j]) * s[j];
-        if (f < d_out && k < d_in) store8(w + (uint64_t)f * d_in + k, v);
+        if (P::kTerms > 1 && k >= d_in) {       // split operands: zeros up to the next multiple of 64
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+        }
+        if (f < d_out && k < (P::kTerms > 1 ? (d_in + 63) / 64 * 64 : d_in)) P::store8(w + f * P::pitch(d_in), k, v);
+    }
+}
+
+// Rows of x as split operands, one a workgroup.
+__global__ __launch_bounds__(256) void k_split(const float *x, uint64_t stride, uint32_t d, uint16_t *out)
+{
+    const float *from = x + blockIdx.x * stride;
+    for (uint32_t k = threadIdx.x * 8; k < (d + 63) / 64 * 64; k += 256 * 8) {
+        float v[8] = {};
+        if (k < d) {
+            Fp32::load4(from + k, v);
+            Fp32::load4(from + k + 4, v + 4);
+        }
+        Split::store8(out + blockIdx.x * Split::pitch(d), k, v);
     }
 }
 
@@ -626,8 +635,14 @@ hipError_t prepare_few()
 
 hipError_t prepare_q4()
 {
-    const hipError_t e = prepare_few<CodesBf16>();
-    return e == hipSuccess ? prepare_few<CodesFp32>() : e;
+    const auto raise = [](auto *kernel) {
+        return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, 2 * 512 * 128);
+    };
+    const hipError_t all[] = {raise(&k_big<Split, EndProject<Fp32>>), raise(&k_big<Split, EndSlice>), prepare_few<CodesBf16>(),
+                              prepare_few<CodesFp32>()};
+    for (const hipError_t e : all)
+        if (e != hipSuccess) return e;
+    return hipSuccess;
 }
 
 hipError_t launch_q4_quantize(const void *w, uint64_t stride, bool bf16, uint32_t d_out, uint32_t d_in, uint32_t group,
@@ -655,27 +670,54 @@ hipError_t launch_q4_pack(const uint8_t *values, uint32_t d_out, uint32_t d_in, 
     return hipGetLastError();
 }
 
-hipError_t launch_q4_unpack(const Q4Weights &q, bool bf16, uint32_t d_out, uint32_t d_in, void *w, hipStream_t stream)
+namespace {
+
+template <class T, class P>
+hipError_t unpack(const Q4Weights &q, uint32_t d_out, uint32_t d_in, void *w, hipStream_t stream)
 {
-    const auto typed = [&](auto t) {
-        typedef decltype(t) T;
-        typedef typename T::elem E;
-        k_unpack<T><<<block_grid(d_out, d_in), 256, 0, stream>>>(
-            static_cast<const u32x4 *>(q.codes), static_cast<const E *>(q.scales), static_cast<const E *>(q.zeros), d_out,
-            d_in, q.group, static_cast<E *>(w));
-    };
-    bf16 ? typed(Bf16()) : typed(Fp32());
+    typedef typename T::elem E;
+    k_unpack<T, P><<<block_grid(d_out, d_in), 256, 0, stream>>>(
+        static_cast<const u32x4 *>(q.codes), static_cast<const E *>(q.scales), static_cast<const E *>(q.zeros), d_out,
+        d_in, q.group, static_cast<typename P::elem *>(w));
     return hipGetLastError();
 }
 
+// With both operands split.
+hipError_t split_q4(const AdapterArgs &a, const Q4Weights &w, const void *x, uint64_t x_stride, const void *bias,
+                    const void *adapters, float *u, const Q4Space &space, void *y, uint64_t y_stride, hipStream_t stream)
+{
+    hipError_t e = launch_adapter_shrink(a, false, x, x_stride, adapters, u, stream);
+    if (e != hipSuccess) return e;
+    e = unpack<Fp32, Split>(w, a.d_out, a.d_in, space.w, stream);
+    if (e != hipSuccess) return e;
+    uint16_t *xs = static_cast<uint16_t *>(space.x);
+    k_split<<<(uint32_t)a.rows, 256, 0, stream>>>(static_cast<const float *>(x), x_stride, a.d_in, xs);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const ProductArgs p = {0, a.rows, Split::pitch(a.d_in), a.d_in, a.d_out, space.slices};
+    const EndProject<Fp32> end = {a, u, reinterpret_cast<int32_t *>(u + a.rows * a.rank), static_cast<const float *>(adapters),
+                                  static_cast<const float *>(bias), static_cast<float *>(y), y_stride};
+    return big<Split>(p, xs, static_cast<const uint16_t *>(space.w), nullptr, nullptr, end, stream);
+}
+
+}  // namespace
+
+hipError_t launch_q4_unpack(const Q4Weights &q, bool bf16, uint32_t d_out, uint32_t d_in, void *w, hipStream_t stream)
+{
+    return bf16 ? unpack<Bf16, Bf16>(q, d_out, d_in, w, stream) : unpack<Fp32, Fp32>(q, d_out, d_in, w, stream);
+}
+
 hipError_t launch_q4_project(const AdapterArgs &a, bool bf16, const void *x, uint64_t x_stride, const Q4Weights &w,
-                             const void *bias, const void *adapters, float *u, float *slices, void *unpacked, void *y,
+                             const void *bias, const void *adapters, float *u, const Q4Space &space, void *y,
                              uint64_t y_stride, hipStream_t stream)
 {
     if (q4_shape(a.rows, a.d_in, a.d_out, bf16) == Q4Shape::unpack) {
-        const hipError_t e = launch_q4_unpack(w, bf16, a.d_out, a.d_in, unpacked, stream);
+        if (!bf16 && q4_split(a.rows, a.d_in, a.d_out))
+            return split_q4(a, w, x, x_stride, bias, adapters, u, space, y, y_stride, stream);
+        const hipError_t e = launch_q4_unpack(w, bf16, a.d_out, a.d_in, space.w, stream);
         if (e != hipSuccess) return e;
-        return launch_adapter_project(a, bf16, x, x_stride, unpacked, bias, adapters, u, slices, y, y_stride, stream);
+        float *slices = product_shape(a.rows, a.d_out, a.d_in, bf16) == Shape::big ? space.slices : nullptr;
+        return launch_adapter_project(a, bf16, x, x_stride, space.w, bias, adapters, u, slices, y, y_stride, stream);
     }
     const hipError_t e = launch_adapter_shrink(a, bf16, x, x_stride, adapters, u, stream);
     if (e != hipSuccess) return e;

@@ -226,6 +226,18 @@ inline Shape product_shape(uint64_t rows, uint32_t features, uint32_t k, bool bf
     const ProductTime t = product_time(rows, features, k, bf16);
     return t.big <= t.mid ? Shape::big : Shape::mid;
 }
+// Values of an fp32 row split into three bf16 each, and the time of a product of such rows: six of
+// bf16's.
+constexpr uint64_t split_bytes(uint64_t k) { return (k + 63) / 64 * 384; }
+inline bool split_fits(uint64_t rows, uint64_t features, uint64_t k)
+{
+    // operands reach 64 GiB, a tile of one 32 bits of 16-byte units
+    return k <= 1u << 22 && rows * split_bytes(k) <= (uint64_t)1 << 36 && features * split_bytes(k) <= (uint64_t)1 << 36;
+}
+inline double split_time(uint64_t rows, uint32_t features, uint32_t k)
+{
+    return product_time(rows, features, (k + 63) / 64 * 384, true).big;
+}
 // Features of a workgroup of Shape::few.  With more than 16 rows a CU holds one, and a round of
 // 64 features takes 1.6 times one of 32.
 inline uint32_t few_features(uint64_t rows, uint32_t features)
@@ -305,14 +317,43 @@ inline Q4Shape q4_shape(uint64_t rows, uint32_t d_in, uint32_t d_out, bool bf16)
     }
     return best == n ? Q4Shape::narrow : best == m ? Q4Shape::middle : Q4Shape::wide;
 }
+// Whether unpacked fp32 weights are split, by estimated time and the bytes that splitting writes.
+inline bool q4_split(uint64_t rows, uint32_t d_in, uint32_t d_out)
+{
+    const ProductTime t = product_time(rows, d_out, d_in, false);
+    return split_fits(rows, d_out, d_in) && split_time(rows, d_out, d_in) + (10.0 * rows * d_in + 2.0 * d_in * d_out) / 5e6 + 4.0 <
+                                                (t.big < t.mid ? t.big : t.mid);
+}
+// Workspace of unpacked weights; of fp32, split or not, with the split rows of x behind the weights and
+// the product's slices behind these.
+struct Q4Space {
+    void *w, *x;
+    float *slices;
+    uint64_t bytes;
+};
+inline Q4Space q4_space(uint64_t rows, uint32_t d_in, uint32_t d_out, bool bf16, void *base)
+{
+    // the shapes of more rows go back and forth; so that sizes do not fall, all of them have room
+    Q4Space s = {};
+    if (rows <= (bf16 ? kQ4FewBf16 : kQ4FewFp32)) return s;
+    const auto take = [&](uint64_t bytes) {
+        void *p = base ? static_cast<char *>(base) + s.bytes : nullptr;
+        s.bytes += (bytes + 255) / 256 * 256;
+        return p;
+    };
+    s.w = take(d_out * (bf16 ? 2ull * d_in : split_bytes(d_in)));
+    if (!bf16) s.x = take(rows * split_bytes(d_in));
+    s.slices = static_cast<float *>(take(kBigSliceBytes));
+    return s;
+}
 hipError_t prepare_q4();
 hipError_t launch_q4_quantize(const void *w, uint64_t stride, bool bf16, uint32_t d_out, uint32_t d_in, uint32_t group,
                               void *codes, void *scales, hipStream_t stream);
 hipError_t launch_q4_pack(const uint8_t *values, uint32_t d_out, uint32_t d_in, void *codes, hipStream_t stream);
 hipError_t launch_q4_unpack(const Q4Weights &q, bool bf16, uint32_t d_out, uint32_t d_in, void *w, hipStream_t stream);
-// As launch_adapter_project; unpacked: d_out * d_in elements if the shape asks for them.
+// As launch_adapter_project.
 hipError_t launch_q4_project(const AdapterArgs &a, bool bf16, const void *x, uint64_t x_stride, const Q4Weights &w,
-                             const void *bias, const void *adapters, float *u, float *slices, void *unpacked, void *y,
+                             const void *bias, const void *adapters, float *u, const Q4Space &space, void *y,
                              uint64_t y_stride, hipStream_t stream);
 
 struct HeadArgs {
@@ -405,18 +446,6 @@ inline uint32_t grad_chunk(uint32_t features, uint32_t d, uint32_t per)
     const uint64_t columns = ((uint64_t)d + kOuterThreads * per - 1) / (kOuterThreads * per);
     const uint64_t c = (features * columns / 1024 + 7) / 8 * 8;
     return c < 8 ? 8 : c > kGradChunk ? kGradChunk : (uint32_t)c;
-}
-// Values of an fp32 row split into three bf16 each, and the time of a product of such rows: six of
-// bf16's.
-constexpr uint64_t split_bytes(uint64_t k) { return (k + 63) / 64 * 384; }
-inline bool split_fits(uint64_t rows, uint64_t features, uint64_t k)
-{
-    // operands reach 64 GiB, a tile of one 32 bits of 16-byte units
-    return k <= 1u << 22 && rows * split_bytes(k) <= (uint64_t)1 << 36 && features * split_bytes(k) <= (uint64_t)1 << 36;
-}
-inline double split_time(uint64_t rows, uint32_t features, uint32_t k)
-{
-    return product_time(rows, features, (k + 63) / 64 * 384, true).big;
 }
 // Whether the three products of zo_head_grad take split fp32 operands: by their estimated times and the
 // bytes that splitting writes, at 5 TB/s.

@@ -83,6 +83,15 @@ def test_bad_targets_and_values(ctx, rows, dtype):
     assert torch.isfinite(got.hidden_grad[0]).all() and torch.isfinite(got.logp[[0, 2, 3]]).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_large_products(ctx, dtype):
+    """Tiles of 256 x 256, whole and in slices; of fp32 with operands split into bf16, ends of every sum
+    within 64 values."""
+    for rows, d, vocab, ignore in ((1100, 520, 3001, 0.0), (2000, 264, 2050, 0.45)):
+        h, w, t, g = _case(rows, d, vocab, dtype, ignore=ignore, seed=9)
+        _check(ctx, h, w, t, g, dtype)
+
+
 def test_large_vocabularies(ctx):
     for rows, d, vocab, dtype in ((70, 64, 40007, BF), (9, 40, 70001, BF), (70, 16, 33000, F32)):
         h, w, t, g = _case(rows, d, vocab, dtype, ignore=0.2, seed=3)

@@ -202,6 +202,31 @@ def test_row_counts(ctx, rows, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("lengths,d_in,d_out", [([1500, 548], 1056, 1032), ([700] * 3 + [1], 800, 2056), ([3000], 96, 1800)])
+def test_large_batches(ctx, lengths, d_in, d_out, dtype):
+    """Tiles of 256 x 256, whole and in slices; of fp32 with operands split into bf16, ends of k within 64."""
+    p = _problem(lengths, d_in, d_out, 16, 2, dtype, seed=6, tail=1)
+    _check(ctx, p, _weight(d_out, d_in, 32, dtype, True), 16)
+
+
+def test_split_operands_keep_32_bits(ctx):
+    """Sums that cancel: with 16 bits of a factor they would be off by thousands of the bound."""
+    g = torch.Generator().manual_seed(4)
+    rows, d_in, d_out = 2048, 1024, 1024
+    values, scales, _ = _weight(d_out, d_in, 64, F32)
+    x = torch.randn(rows, d_in, generator=g)
+    x = torch.cat([x[:, :512], -x[:, :512] * (1 + 2.0 ** -12)], dim=1)
+    values = torch.cat([values[:, :512], values[:, :512]], dim=1).contiguous()
+    scales = torch.cat([scales[:8], scales[:8]]).contiguous()
+    y = zo.zo_q4_project(ctx, x.cuda(), _held(ctx, values, scales, None))
+    w = more.weights(values, scales, None)
+    want = x.double() @ w.t()
+    norms = torch.linalg.vector_norm(x.double(), dim=1)[:, None] * torch.linalg.vector_norm(w, dim=1)[None, :]
+    # weights round twice (2 u |x| |w|), products lose up to 2^-21 of themselves, sums 8 sqrt(k) u |x| |w|
+    ref.assert_close(y, want, (8 * math.sqrt(d_in) + 16) * ref.U32 * norms, "y")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("lengths", [[4, 0, 9, 1], [1] * 9, [70, 200, 3]])
 def test_probes_equal_perturb_in_place(ctx, lengths, dtype):
     """Stored rows, regenerated rows and adapters moved by zo_perturb give the same bits."""

@@ -1,0 +1,107 @@
+"""Host-side checks of the 4-bit projection, the distillation loss and the head's gradients: refusals that
+need no GPU, workspace sizes, and that the references agree with torch's own float64 functions."""
+import math
+
+import pytest
+import torch
+
+import forward_only_amd as zo
+import lm_more_ref as more
+import lm_ref as ref
+from forward_only_amd import _lib
+
+F32, BF = torch.float32, torch.bfloat16
+
+
+def test_null_context_is_refused():
+    L, bad = _lib.lib(), _lib.ZO_EINVAL
+    assert L.zo_distill_loss(None, None, 0, 1, 8, 8, None, None, 0, None, 1.0, None, None, None, 8, None) == bad
+    assert L.zo_head_grad(None, None, 8, None, 0, 1, 8, 8, None, None, None, None, None, None, 0, None) == bad
+    assert L.zo_q4_quantize(None, None, 32, 0, 8, 32, 32, None, None, None) == bad
+    assert L.zo_q4_pack(None, None, 8, 32, None, None) == bad
+    assert L.zo_q4_unpack(None, None, None, None, 0, 8, 32, 32, None, None) == bad
+    assert L.zo_q4_project(None, None, 32, None, None, None, 32, None, 0, 1, 32, 8, None, 0, 0, 1.0, None, None, 0,
+                           None, None, 0, 0, 0, 0, None, None, 0, None, 8, None) == bad
+
+
+def test_cpu_tensors_are_refused():
+    x, t = torch.zeros(2, 64), torch.zeros(2, dtype=torch.int64)
+    q = zo.Q4Weight(torch.zeros(1, 1, 1024, dtype=torch.uint8), torch.zeros(2, 16), None, 64)
+    for call in (lambda: zo.zo_distill_loss(None, x, t[:, None], x[:, :1]), lambda: zo.zo_head_grad(None, x, x, t),
+                 lambda: zo.zo_q4_quantize(None, x, 32), lambda: zo.zo_q4_pack(None, torch.zeros(8, 32, dtype=torch.uint8)),
+                 lambda: zo.zo_q4_unpack(None, q), lambda: zo.zo_q4_project(None, x, q)):
+        with pytest.raises(ValueError):
+            call()
+    assert q.shape == (16, 64)
+
+
+def test_code_bytes():
+    L = _lib.lib()
+    assert L.zo_q4_code_bytes(8, 32) == 1024
+    assert L.zo_q4_code_bytes(5120, 5120) == 5120 * 5120 // 2
+    assert L.zo_q4_code_bytes(40, 160) == 3 * 2 * 1024
+
+
+@pytest.mark.parametrize("d_in,d_out", [(5120, 5120), (768, 2304), (5120, 20480), (64, 64), (7168, 28672), (2048, 520)])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_a_projection_workspace_for_many_rows_serves_fewer(d_in, d_out, dtype):
+    most = 0
+    for rows in list(range(0, 1200, 7)) + list(range(1200, 9000, 61)) + [1 << 20]:
+        need = zo.zo_q4_workspace_bytes(rows, d_in, d_out, dtype, 1, 16, 3)
+        assert need >= most, rows
+        most = need
+    few = zo.zo_q4_workspace_bytes(32, d_in, d_out, dtype, 1, 16)
+    assert few < 1 << 16                      # so few rows unpack nothing
+
+
+@pytest.mark.parametrize("d,vocab", [(768, 50272), (7168, 50272), (64, 1003), (40, 500000), (5120, 8)])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_a_gradient_workspace_for_many_rows_serves_fewer(d, vocab, dtype):
+    most = 0
+    for rows in list(range(0, 600)) + list(range(600, 20000, 61)) + [1 << 18]:
+        need = zo.zo_head_grad_workspace_bytes(rows, d, vocab, dtype)
+        assert need >= most, rows
+        most = need
+    # a piece's logits and gradients, however many rows: 4 bytes and two operands of 2 or 6 a logit
+    piece = max(1 << 28, 256 * vocab) * (4 + 2 * (2 if dtype == BF else 6)) * 1.1
+    weights = vocab * d * (4 + 3 * (2 if dtype == BF else 6)) * 1.1 + 16 * vocab * d / 8
+    rows = 1 << 18
+    assert most <= piece + weights + rows * (d * 14 + 64) + (1 << 28) + rows * vocab // 32 * 12
+
+
+def test_distill_reference_agrees_with_torch():
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(6, 50, generator=g, dtype=torch.float64, requires_grad=True)
+    ids = torch.stack([torch.randperm(50, generator=g)[:4] for _ in range(6)])
+    ids[2, 3] = -1
+    t = torch.randn(6, 4, generator=g).double()
+    p = torch.softmax((t / 2).masked_fill(ids < 0, -math.inf), dim=1)
+    q = torch.log_softmax(x / 2, dim=1).gather(1, ids.clamp(min=0))
+    kl = 4 * torch.where(ids < 0, torch.zeros_like(p), p * (torch.log(p.clamp(min=1e-300)) - q)).sum(dim=1)
+    kl.sum().backward()
+    loss, grad, lb, gb = more.distill(x.detach(), ids, t, None, 2.0)
+    ref.assert_close(loss, kl.detach(), 1e-12, "loss")
+    ref.assert_close(grad, x.grad, 1e-12, "grad")
+    assert (lb > 0).all() and (gb > 0).all()
+
+
+def test_head_reference_agrees_with_torch():
+    g = torch.Generator().manual_seed(2)
+    h = torch.randn(7, 16, generator=g, dtype=torch.float64, requires_grad=True)
+    w = torch.randn(30, 16, generator=g, dtype=torch.float64, requires_grad=True)
+    t = torch.tensor([3, -100, 29, 0, 5, -100, 7])
+    c = torch.rand(7, generator=g).double()
+    logp = torch.log_softmax(h @ w.t(), dim=1).gather(1, t.clamp(min=0)[:, None])[:, 0].masked_fill(t < 0, 0.0)
+    (-(c * logp).sum()).backward()
+    got = more.head_grad(h.detach(), w.detach(), t, c, F32)
+    for a, b in zip(got[:3], (logp.detach(), h.grad, w.grad)):
+        ref.assert_close(a, b, 1e-12, "gradient")
+
+
+def test_quantize_reference_by_hand():
+    w = torch.zeros(1, 32)
+    w[0, 0], w[0, 1], w[0, 2], w[0, 3] = 7.0, 2.5, -3.5, -0.49
+    q, s = more.quantize(w, 32)
+    assert s.tolist() == [[1.0]] and q[0, :5].tolist() == [15, 10, 4, 8, 8]     # ties to even
+    z, s = more.quantize(torch.zeros(1, 32), 32)
+    assert s.tolist() == [[0.0]] and (z == 8).all()

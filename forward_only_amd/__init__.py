@@ -763,8 +763,8 @@ def zo_distill_loss(ctx: Context, logits: torch.Tensor, teacher_ids: torch.Tenso
     if not 0 <= k <= ZO_MAX_TEACHER:
         raise ValueError(f"at most {ZO_MAX_TEACHER} entries a row")
     idp, hp = _dev(teacher_ids, "teacher_ids", torch.int64), _dev(teacher_logits, "teacher_logits", torch.float32)
-    if not 0.0 < float(temperature) < float("inf"):
-        raise ValueError("temperature must be positive and finite")
+    if not 1e-6 <= float(temperature) <= 1e6:
+        raise ValueError(f"temperature must be in [1e-6, 1e6], got {temperature}")
     tp = _vector(targets, "targets", rows, torch.int64, dev)
     if row_grad is not None and not (grad or (out is not None and out.grad is not None)):
         raise ValueError("row_grad goes with grad")

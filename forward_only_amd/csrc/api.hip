@@ -65,7 +65,10 @@ constexpr uint64_t kMaxRows = 0x7FFFFFFFu;   // of the language-model operators
 // addressed by 32 bits of 16-byte units.
 constexpr uint64_t kMaxWidth = 1u << 26, kMaxFeatures = 1u << 24, kMaxGroups = 1u << 22;
 constexpr uint64_t kMaxProjectRows = 1u << 25, kMaxProjected = (uint64_t)1 << 35;
-constexpr uint64_t kMaxGradWidth = 1u << 20;
+// zo_head_grad's: operands of a fp32 product reach 64 GiB, tiles of 64 x 64 a launch.
+constexpr uint64_t kMaxGradWidth = 1u << 20, kMaxGradValues = (uint64_t)1 << 34;
+// Beyond these an exponent's factor, or a loss times T^2, leaves fp32's range.
+constexpr float kMinTemperature = 1e-6f, kMaxTemperature = 1e6f;
 // The rows of a product's left operand reach at most 64 GiB (32 bits of 16-byte units).
 inline bool reach_ok(uint64_t rows, uint64_t stride, uint64_t k, bool bf16)
 {
@@ -747,7 +750,7 @@ zo_status zo_distill_loss(zo_ctx *c, const void *d_logits, zo_dtype dtype, uint6
 {
     if (!ctx_ok(c)) return ZO_EINVAL;
     if (dtype != ZO_FP32 && dtype != ZO_BF16) return ZO_EINVAL;
-    if (!(temperature > 0.0f) || !(temperature <= 3.402823466e38f)) return ZO_EINVAL;
+    if (!(temperature >= kMinTemperature) || !(temperature <= kMaxTemperature)) return ZO_EINVAL;
     if (rows > kMaxRows || vocab > kMaxRows || k > ZO_MAX_TEACHER) return ZO_EUNSUPPORTED;
     if (rows == 0) return ZO_OK;
     if (vocab == 0 || !d_logits || !d_loss || (k > 0 && (!d_teacher_ids || !d_teacher_logits)))
@@ -878,8 +881,8 @@ zo_status zo_head_grad(zo_ctx *c, const void *d_hidden, uint64_t hidden_stride, 
 {
     if (!ctx_ok(c)) return ZO_EINVAL;
     if (dtype != ZO_FP32 && dtype != ZO_BF16) return ZO_EINVAL;
-    if (rows > kMaxProjectRows || vocab > kMaxFeatures || d > kMaxGradWidth || rows * d > kMaxProjected ||
-        (uint64_t)vocab * d > kMaxProjected)
+    if (rows > kMaxProjectRows || vocab > kMaxFeatures || d > kMaxGradWidth || rows * d > kMaxGradValues ||
+        (uint64_t)vocab * d > kMaxGradValues)
         return ZO_EUNSUPPORTED;
     if (vocab == 0 || d == 0 || d % 8u || hidden_stride % 8u) return ZO_EINVAL;
     if (!aligned16(d_hidden_grad) || !aligned16(d_weight_grad)) return ZO_EINVAL;

@@ -46,10 +46,10 @@ struct Square {
     typedef typename T::elem E;
     static constexpr int kPitch = 64 + 4 / (int)sizeof(E);
     E *tile;
-    __device__ __forceinline__ void put(int r, int c, const float *v, int n) const
+    __device__ __forceinline__ void put(int r, int c, const float *v) const
     {
 #pragma unroll
-        for (int j = 0; j < n; ++j) {
+        for (int j = 0; j < 8; ++j) {
             if constexpr (T::kBf16) tile[r * kPitch + c + j] = (E)pack_bf16x2(v[j], 0.0f);
             else tile[r * kPitch + c + j] = v[j];
         }
@@ -211,7 +211,7 @@ __global__ __launch_bounds__(256) void k_shares(const float *logits, RowsOf a, t
         if (at < have && f0 + f < pitch_v) {
             const uint64_t row = a.list[at];
             const float2 norm = a.norms[at];
-            const int64_t tgt = a.targets[row] - f0;
+            const int64_t tgt = a.targets[row];
             g = a.row_grad ? a.row_grad[row] : 1.0f;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -220,14 +220,14 @@ __global__ __launch_bounds__(256) void k_shares(const float *logits, RowsOf a, t
                 for (int j = 0; j < 4; ++j) {
                     const float p = fast_exp((l[j] - norm.x) - norm.y);
                     const int c = f + 4 * h + j;
-                    v[4 * h + j] = f0 + c < a.features ? p - (tgt == c ? 1.0f : 0.0f) : 0.0f;
+                    v[4 * h + j] = f0 + c < a.features ? p - (tgt == (int64_t)f0 + c ? 1.0f : 0.0f) : 0.0f;
                 }
             }
         }
         if (d && at < have && (P::kTerms > 1 || f0 + f < pitch_v)) P::store8(d + at * P::pitch(pitch_v), f0 + f, v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) scaled[j] = at < have ? g * v[j] : 0.0f;
-        tile.put(r, f, scaled, 8);
+        tile.put(r, f, scaled);
     }
     if (!dt) return;
     __syncthreads();

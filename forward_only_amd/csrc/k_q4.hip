@@ -222,18 +222,18 @@ __global__ __launch_bounds__(256) void k_unpack(const u32x4 *codes, const typena
     }
 }
 
-// Rows of x as split operands, one a workgroup.
-__global__ __launch_bounds__(256) void k_split(const float *x, uint64_t stride, uint32_t d, uint16_t *out)
+// Rows of x as split operands, one a workgroup at a time.
+__global__ __launch_bounds__(256) void k_split(const float *x, uint64_t rows, uint64_t stride, uint32_t d, uint16_t *out)
 {
-    const float *from = x + blockIdx.x * stride;
-    for (uint32_t k = threadIdx.x * 8; k < (d + 63) / 64 * 64; k += 256 * 8) {
-        float v[8] = {};
-        if (k < d) {
-            Fp32::load4(from + k, v);
-            Fp32::load4(from + k + 4, v + 4);
+    for (uint64_t row = blockIdx.x; row < rows; row += gridDim.x)
+        for (uint32_t k = threadIdx.x * 8; k < (d + 63) / 64 * 64; k += 256 * 8) {
+            float v[8] = {};
+            if (k < d) {
+                Fp32::load4(x + row * stride + k, v);
+                Fp32::load4(x + row * stride + k + 4, v + 4);
+            }
+            Split::store8(out + row * Split::pitch(d), k, v);
         }
-        Split::store8(out + blockIdx.x * Split::pitch(d), k, v);
-    }
 }
 
 // ---- few rows ---------------------------------------------------------------------------
@@ -691,7 +691,8 @@ hipError_t split_q4(const AdapterArgs &a, const Q4Weights &w, const void *x, uin
     e = unpack<Fp32, Split>(w, a.d_out, a.d_in, space.w, stream);
     if (e != hipSuccess) return e;
     uint16_t *xs = static_cast<uint16_t *>(space.x);
-    k_split<<<(uint32_t)a.rows, 256, 0, stream>>>(static_cast<const float *>(x), x_stride, a.d_in, xs);
+    k_split<<<(uint32_t)(a.rows < 65536 ? a.rows : 65536), 256, 0, stream>>>(static_cast<const float *>(x), a.rows, x_stride,
+                                                                             a.d_in, xs);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     const ProductArgs p = {0, a.rows, Split::pitch(a.d_in), a.d_in, a.d_out, space.slices};

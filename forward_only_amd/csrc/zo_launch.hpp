@@ -295,6 +295,7 @@ inline uint64_t q4_blocks(uint32_t d_out, uint32_t d_in)
 // features a workgroup, or unpacked first.
 enum class Q4Shape { narrow, middle, wide, unpack };
 constexpr uint32_t kQ4FewBf16 = 64, kQ4FewFp32 = 32;   // rows that are never unpacked
+constexpr uint64_t kMaxGridY = 65535;
 // By estimated time.  Measured per block of 128 values of k, 64 rows of bf16, a round of one
 // workgroup a CU: 128 features 0.82 us, 64 features 0.48, 32 features 0.37; unpacking runs at 5.5 TB/s.
 // (bf16 5120 -> 20480, 128 / 256 / 512 rows: 58 / 96 / 164 us as they are, 116 / 129 / 157 unpacked;
@@ -303,7 +304,7 @@ constexpr uint32_t kQ4FewBf16 = 64, kQ4FewFp32 = 32;   // rows that are never un
 inline Q4Shape q4_shape(uint64_t rows, uint32_t d_in, uint32_t d_out, bool bf16)
 {
     if (rows <= 32) return d_out >= 128u * 160 ? Q4Shape::wide : Q4Shape::narrow;
-    if (!bf16) return Q4Shape::unpack;
+    if (!bf16 || rows > 64 * kMaxGridY) return Q4Shape::unpack;
     const double blocks = (d_in + 127) / 128;
     const auto time = [&](uint32_t features, double each) {
         const uint64_t groups = ((uint64_t)d_out + features - 1) / features * ((rows + 63) / 64);
@@ -434,8 +435,9 @@ struct HeadGradArgs {
     void *hidden_grad, *weight_grad;   // of the operands' type; or nullptr
     void *workspace;
 };
-// Rows are taken in pieces of at most this many logits, and at least 256 rows.
-constexpr uint64_t kGradLogits = (uint64_t)1 << 28;
+// Rows are taken in pieces of at most this many logits, and at least 256 rows; at most so many that a
+// launch holds them (k_shares has 64 to a line of its grid, k_head_join 128 threads to each).
+constexpr uint64_t kGradLogits = (uint64_t)1 << 28, kGradPiece = (uint64_t)1 << 18;
 // Rows of which the products are formed value by value (k_outer), its threads, and the features that a
 // workgroup takes: fewer than kGradChunk where that leaves CUs without one (one row, 512 -> 1000: 93 us
 // with 256, 20 with 8).
@@ -473,7 +475,8 @@ inline HeadGradSpace head_grad_space(uint64_t rows, uint32_t d, uint32_t feature
 {
     HeadGradSpace s = {};
     s.pitch_v = ((uint64_t)features + 7) / 8 * 8;
-    const uint64_t fits = kGradLogits / (s.pitch_v ? s.pitch_v : 1) / 256 * 256, most = fits < 256 ? 256 : fits;
+    const uint64_t fits = kGradLogits / (s.pitch_v ? s.pitch_v : 1) / 256 * 256;
+    const uint64_t most = fits < 256 ? 256 : fits < kGradPiece ? fits : kGradPiece;
     s.piece = rows < most ? rows : most;
     s.pieces = s.piece ? (rows + s.piece - 1) / s.piece : 0;
     s.pitch_x = (s.piece + 7) / 8 * 8;

@@ -497,8 +497,9 @@ zo_status zo_adapter_project(zo_ctx *ctx, const void *d_x, uint64_t x_stride,
  *   d_loss[row] = T^2 sum_j p_j (log p_j - log Q_{id_j}),
  * and, unless d_grad is NULL, the gradient of sum_row d_row_grad[row] d_loss[row],
  *   d_grad[row][v] = d_row_grad[row] T (Q_v - sum_{j: id_j = v} p_j)
- * (d_row_grad NULL: 1 for each row), of the logits' dtype, rounded once.  All sums are fp32; one pass over the
- * logits where a row is at most 256 KiB or no gradient is wanted, deterministic.
+ * (d_row_grad NULL: 1 for each row), of the logits' dtype, rounded once.  All sums are fp32 (the loss is off by
+ * about T^2 2^-23); one pass over the logits where a row has at most 65536 of them or no gradient is
+ * wanted; deterministic.
  * d_teacher_ids: device int64 [rows x k], -1 for no entry; d_teacher_logits: device float [rows x k],
  * logits or log probabilities (zo_token_logprobs' alternatives are both of a teacher).  An id may come
  * twice.  d_targets: NULL, or device int64 [rows], where only ZO_IGNORE_TOKEN has a meaning: such a
@@ -510,7 +511,7 @@ zo_status zo_adapter_project(zo_ctx *ctx, const void *d_x, uint64_t x_stride,
  * contiguous, at any element-aligned address.  d_grad may be d_logits with the same stride: the
  * gradient then takes the logits' place.
  * Errors: ZO_EINVAL for NULL pointers (with rows > 0; the teacher's with k > 0), unknown dtype, vocab == 0
- * (with rows > 0), a temperature that is not positive and finite, grad_stride < vocab (with more than one
+ * (with rows > 0), a temperature outside [1e-6, 1e6], grad_stride < vocab (with more than one
  * row), d_grad within the logits in another way, misaligned pointers; ZO_EUNSUPPORTED if k >
  * ZO_MAX_TEACHER or rows or vocab exceed 2^31 - 1.  rows == 0 launches nothing. */
 zo_status zo_distill_loss(zo_ctx *ctx, const void *d_logits, zo_dtype dtype, uint64_t rows,
@@ -524,8 +525,9 @@ zo_status zo_distill_loss(zo_ctx *ctx, const void *d_logits, zo_dtype dtype, uin
  *   D[row][v] = d_row_grad[row] (softmax(h W^T)[row][v] - [v = target]),
  *   d_hidden_grad = D W [rows x d],  d_weight_grad = D^T h [vocab x d]
  * (d_row_grad, device float [rows], NULL: 1 for each row).  Rows are taken in pieces of at most 2^28 logits
- * (at least 256 rows), so that the workspace holds that many in fp32 and no more; the gradients' sums are fp32
- * and rounded once.  Of more than 16 rows D is rounded to the dtype before its products, with g for
+ * (at least 256 rows, at most 2^18), so that the workspace holds that many in fp32 and no more; the gradients'
+ * sums are fp32 and rounded once.  Large products of fp32 are formed of operands split into three bf16 each,
+ * 24 bits in all, of which products below 2^-21 of the whole are left out.  Of more than 16 rows D is rounded to the dtype before its products, with g for
  * d_weight_grad and without for d_hidden_grad.  Rows with the ignored target are not computed in batches of
  * more than 16 rows; their logp and gradient are 0 and they add nothing to d_weight_grad, whatever they
  * hold.  A target outside the vocabulary, or a row that holds NaN or an infinity, makes the row's logp and
@@ -535,7 +537,7 @@ zo_status zo_distill_loss(zo_ctx *ctx, const void *d_logits, zo_dtype dtype, uin
  * zo_head_grad_workspace_bytes(rows, d, vocab, dtype) bytes, which never fall as rows grow.  rows == 0 gives
  * a d_weight_grad of zeros.
  * Errors: as zo_head_logprobs; ZO_EUNSUPPORTED if rows exceed 2^25, d 2^20, vocab 2^24, or rows * d or
- * vocab * d 2^35. */
+ * vocab * d 2^34. */
 uint64_t zo_head_grad_workspace_bytes(uint64_t rows, uint32_t d, uint32_t vocab, zo_dtype dtype);
 zo_status zo_head_grad(zo_ctx *ctx, const void *d_hidden, uint64_t hidden_stride,
                        const void *d_weight, zo_dtype dtype, uint64_t rows, uint32_t d,
@@ -584,7 +586,8 @@ zo_status zo_q4_unpack(zo_ctx *ctx, const void *d_codes, const void *d_scales, c
  * they are held.  x, scales, zeros, bias, adapters and y share `dtype`.  d_starts and d_ids may both be NULL
  * with n_groups == 0: all rows without adapters.  Up to ZO_Q4_FEW_BF16 rows (or ZO_Q4_FEW_FP32), and of
  * more where that is estimated to be faster (bf16, up to some hundred), the weights are not rounded; else they are
- * unpacked into the workspace first, rounded to the dtype.  x beyond 2^100 may
+ * unpacked into the workspace first, rounded to the dtype; large fp32 products then take both operands split
+ * into three bf16 each, 24 bits in all, of which products below 2^-21 of the whole are left out.  x beyond 2^100 may
  * overflow on the way (a code enters as 128 + q, fp32 sums).  A weight that is NaN or infinite makes its
  * feature NaN or infinite in every row, a value of x that is makes its row so, perhaps NaN.
  * d_workspace: at least zo_q4_workspace_bytes(...) bytes, 256-byte aligned; sizes never fall as rows grow.

@@ -198,10 +198,46 @@ def test_rows_behind_the_last_are_left(ctx):
     assert (loss[3:] == 7).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("T", [2e-6, 0.01, 100.0, 1e6])
+def test_temperatures(ctx, dtype, T):
+    """A gradient's terms at any temperature; losses of a high one are roundings times T^2."""
+    x, ids, t, w = _case(5, 600, 5, dtype, seed=9)
+    _check(ctx, x, ids, t, w, T=float(torch.tensor(T)))
+
+
+def test_more_rows_than_a_launch_holds(ctx):
+    """Rows past 2^25, of 64 threads each, and past 2^32 bytes of the teacher's entries; the same 4096 again and
+    again."""
+    n, vocab, k, rows = 4096, 8, 16, (1 << 25) + 4096
+    x, ids, t, w = _case(n, vocab, k, BF, seed=10)
+    want, grad, lb, gb = more.distill(x, ids, t, None, 1.0)
+    many = lambda v: v.cuda().repeat(rows // n, *([1] * (v.dim() - 1)))  # noqa: E731
+    got = zo.zo_distill_loss(ctx, many(x), many(ids), many(t), grad=True, row_grad=many(w))
+    g = w.double()[:, None]
+    ref.assert_close(got.loss[-n:], want, lb + ref.U32 * want.abs() + 1e-30, "loss")
+    ref.assert_close(got.grad[-n:], g * grad, g.abs() * gb * 1.01 + (ref.UBF + 4 * ref.U32) * (g * grad).abs() + 1e-38, "grad")
+    assert torch.equal(got.loss.view(-1, n), got.loss[:n].expand(rows // n, n))
+    assert torch.equal(got.grad.view(-1, n * vocab), got.grad[:n].reshape(1, -1).expand(rows // n, n * vocab))
+
+
+def test_rows_past_32_bits_of_offsets(ctx):
+    """Rows 2^31 elements apart, read and written past 2^32 bytes and elements."""
+    x, ids, t, w = _case(3, 1003, 4, BF, seed=11)
+    stride = (1 << 31) + 16
+    whole = torch.empty(2 * stride + 1003, dtype=BF, device="cuda")
+    place = whole.as_strided((3, 1003), (stride, 1))
+    place.copy_(x)
+    apart = zo.zo_distill_loss(ctx, x.cuda(), ids.cuda(), t.cuda(), grad=True, row_grad=w.cuda())
+    got = zo.zo_distill_loss(ctx, place, ids.cuda(), t.cuda(), row_grad=w.cuda(),
+                             out=zo.DistillLoss(torch.empty(3, device="cuda"), place))
+    assert torch.equal(got.loss, apart.loss) and torch.equal(place, apart.grad)
+
+
 def test_refusals(ctx):
     x, ids, t, w = (v.cuda() for v in _case(3, 40, 4, F32))
     call = lambda **kw: zo.zo_distill_loss(ctx, kw.pop("x", x), kw.pop("ids", ids), kw.pop("t", t), **kw)  # noqa: E731
-    for bad in (0.0, -1.0, math.nan, math.inf):
+    for bad in (0.0, -1.0, math.nan, math.inf, 1e-7, 1.1e6):
         with pytest.raises(ValueError):
             call(temperature=bad)
     with pytest.raises(ValueError):

@@ -7,6 +7,7 @@ import torch
 import forward_only_amd as zo
 import lm_more_ref as more
 import lm_ref as ref
+from forward_only_amd import _lib
 
 pytestmark = pytest.mark.gpu
 
@@ -139,6 +140,21 @@ def test_pieces_of_rows(ctx, ignore, dtype):
     # sums of 600 terms of at most |D| |h|, in the norms that bw already carries half a step of
     bw += 8 * math.sqrt(rows) * ref.U32 / half * bw + half * dw.abs() + 1e-30
     ref.assert_close(got.weight_grad, dw.cpu(), bw.cpu(), "weight_grad")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_many_rows_of_a_small_vocabulary(ctx, dtype):
+    """Pieces of 2^18 rows."""
+    rows, d, vocab = (1 << 18) * 2 + 70, 8, 5
+    h, w, t, g = _case(rows, d, vocab, dtype, ignore=0.1, seed=12)
+    _check(ctx, h, w, t, g, dtype)
+
+
+def test_sizes_that_are_refused(ctx):
+    """Before any pointer is looked at."""
+    for rows, d, vocab in ((1 << 26, 8, 8), (1, 1 << 21, 8), (1, 8, (1 << 24) + 8), (1 << 25, 520, 8), (1, 1032, 1 << 24)):
+        assert _lib.lib().zo_head_grad(ctx.handle, None, d, None, 0, rows, d, vocab, None, None, None, None, None, None,
+                                       0, None) == _lib.ZO_EUNSUPPORTED
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])

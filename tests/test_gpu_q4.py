@@ -289,6 +289,42 @@ def test_nan_stays_with_its_row_and_feature(ctx, rows, dtype):
     assert torch.isfinite(y[keep]).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_more_rows_than_a_grid_has_lines(ctx, dtype):
+    """More than 65535 tiles of 64 rows; the same 1024 rows again and again."""
+    n, rows = 1024, 65 * 65536
+    p = _problem([n], 32, 8, 8, 1, dtype, seed=5)
+    values, scales, _ = _weight(8, 32, 32, dtype)
+    q = _held(ctx, values, scales, None)
+    y = zo.zo_q4_project(ctx, p["x"].cuda().repeat(rows // n, 1), q)
+    half = ref.UBF if dtype == BF else ref.U32
+    want = p["x"].double() @ zo.zo_q4_unpack(ctx, q).double().cpu().t()
+    # one rounding of y, and (where the weights are not rounded) one of each weight
+    bound = half * want.abs() + 1.01 * half * (p["x"].double().abs() @ more.weights(values, scales, None).abs().t()) \
+        + more.q4_bound(p["x"], scales, None, dtype)
+    ref.assert_close(y[:n], want, bound, "y")
+    assert torch.equal(y.view(-1, n * 8), y[:n].reshape(1, -1).expand(rows // n, n * 8))
+
+
+def test_codes_and_rows_past_32_bits_of_offsets(ctx):
+    """Codes past 2^32 bytes: the last features, of 67 million weights each."""
+    d_in, d_out = 1 << 26, 144
+    codes = torch.zeros(9, d_in // 128, 1024, dtype=torch.uint8, device="cuda")      # 4.8 GB
+    g = torch.Generator().manual_seed(7)
+    scales = torch.ones(d_in // 128, d_out, dtype=BF, device="cuda")
+    tail = torch.randint(0, 256, (8, 1024), generator=g, dtype=torch.uint8)
+    codes[8, -8:] = tail.cuda()
+    x = torch.zeros(3, d_in, dtype=BF)
+    x[:, -1024:] = torch.randn(3, 1024, generator=g).to(BF)
+    x[:, 5] = 1.0
+    y = zo.zo_q4_project(ctx, x.cuda(), zo.Q4Weight(codes, scales, None, d_in))
+    w = more.values_of(tail.view(1, 8, 1024), 16, 1024).double() - 8
+    low = x[:, -1024:].double().sum(dim=1, keepdim=True)
+    want = torch.cat([-8 * (low + 1).expand(3, 128), x[:, -1024:].double() @ w.t() - 8], dim=1)
+    bound = ref.UBF * want.abs() + more.q4_bound(torch.cat([x[:, :128], x[:, -1024:]], dim=1), torch.ones(9, d_out), None, BF)
+    ref.assert_close(y, want, bound, "y")
+
+
 def test_one_workspace_streams_and_graphs(ctx):
     p = _problem([40, 100, 60], 256, 136, 16, 2, BF, seed=4)
     q = _held(ctx, *_weight(136, 256, 64, BF))

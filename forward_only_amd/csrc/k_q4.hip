@@ -240,41 +240,56 @@ __global__ __launch_bounds__(256) void k_split(const float *x, uint64_t rows, ui
 
 constexpr uint32_t kAndOr = 0xEA;                   // (a & b) | c
 
-// Codes as operands, exactly: bf16 kOffset + q (seven bits behind the leading one hold 128 + q),
-// fp32 q.
-struct CodesBf16 {
-    typedef Bf16 T;
-    static constexpr float kOffset = 128.0f;
-    static constexpr int kParts = 1;                // pieces of the eight values
-    static __device__ __forceinline__ u32x4 part(uint32_t w, int)
-    {
-        u32x4 f;
+// Codes as bf16 operands o + q, exactly.  bf16: o = 16, the code in the four bits behind the leading one.
+// fp32: o = 0, by conversion; with 16 sums cancelled so far that the result was off by 1.7e-6 of its size (3e-7;
+// 2112 rows 768 to 2304: 44 us with 16, 52).
+template <class T>
+constexpr float kOffset = T::kBf16 ? 16.0f : 0.0f;
+template <class T>
+__device__ __forceinline__ u32x4 codes_of(uint32_t w)
+{
+    u32x4 f;
+    if constexpr (T::kBf16) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = ZO_BITOP3(w >> (4 * i), 0x000F000Fu, 0x43004300u, kAndOr);
-        return f;
+        for (int i = 0; i < 4; ++i)
+            f[i] = ZO_BITOP3(i ? w >> (4 * i - 3) : w << 3, 0x00780078u, 0x41804180u, kAndOr);
+    } else {
+        // code j in the low half of byte j % 2 * 2 + j / 4 of the codes j / 2 % 2 * 4 to the right
+        const uint32_t of[2] = {w & 0x0F0F0F0Fu, w >> 4 & 0x0F0F0F0Fu};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            f[i] = __builtin_amdgcn_perm(__float_as_uint((float)(of[i & 1] >> (16 + 8 * (i >> 1)) & 255u)),
+                                         __float_as_uint((float)(of[i & 1] >> (8 * (i >> 1)) & 255u)), 0x07060302u);
     }
-    // All ones, or all -(128 + 8).
-    static __device__ __forceinline__ u32x4 all(bool one)
-    {
-        const uint32_t w = one ? 0x3F803F80u : 0xC308C308u;
-        return u32x4{w, w, w, w};
-    }
+    return f;
+}
+// The same number in every place: 1, or -(16 + 8).
+__device__ __forceinline__ u32x4 all_of(bool one)
+{
+    const uint32_t w = one ? 0x3F803F80u : 0xC1C0C1C0u;
+    return u32x4{w, w, w, w};
+}
+// Eight values of x, in pieces as they are held, as kParts bf16 operands whose sum they are: fp32 is split as
+// Split splits it, three products of bf16 instead of eight of fp32 at a ninth of their rate (fp32 5120 to
+// 5120: one row 26 -> 15.4 us, 32 rows 48 -> 19.6).
+template <class T>
+struct Parts;
+template <>
+struct Parts<Bf16> {
+    static constexpr int kParts = 1, kPieces = 1;
+    u32x4 p[1];
+    __device__ __forceinline__ Parts(const u32x4 *v) : p{v[0]} {}
 };
-struct CodesFp32 {
-    typedef Fp32 T;
-    static constexpr float kOffset = 0.0f;
-    static constexpr int kParts = 2;
-    static __device__ __forceinline__ u32x4 part(uint32_t w, int h)
+template <>
+struct Parts<Fp32> {
+    static constexpr int kParts = 3, kPieces = 2;
+    u32x4 p[3];
+    __device__ __forceinline__ Parts(const u32x4 *v)
     {
-        u32x4 f;
+        float x[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = __float_as_uint((float)(w >> code_shift(4 * h + i) & 15u));
-        return f;
-    }
-    static __device__ __forceinline__ u32x4 all(bool one)
-    {
-        const uint32_t w = __float_as_uint(one ? 1.0f : -8.0f);
-        return u32x4{w, w, w, w};
+        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[i / 4][i % 4]);
+        Split::parts(x, p);
     }
 };
 
@@ -295,9 +310,10 @@ struct Q4Args {
 //
 // A group's sum of products with codes is formed apart and enters the row's sum as
 // s (sum x (o + q) - (o + z) sum x), so that the weights are not rounded: every product is exact, all
-// sums are fp32.  The sums of x are products with ones; without zero points with -(o + 8), which
-// the products with the codes then start from.  A group's sums are used one group later, so that
-// the products of the next are under way meanwhile.
+// sums are fp32.  The sums of x are products with ones; of bf16 without zero points with -(o + 8), which
+// the products with the codes then start from.  (Used one group later, with the products of the next
+// under way, a group's sums were no better: bf16 7168 to 28672, one row 23.8 us against 23.2, 32 rows 32.6
+// against 31.4.)
 template <class T, int kMR, int kMF, int kKG, int kSplit, bool kPoints, bool kWhole>
 constexpr int q4_stages()
 {
@@ -324,15 +340,15 @@ __device__ __forceinline__ f32x4 four(uint2 v)
 }
 __device__ __forceinline__ f32x4 four(f32x4 v) { return v; }
 
-template <class C, int kMR, int kMF, int kFG, int kKG, int kSplit, bool kPoints, bool kWhole, class End>
-__global__ __launch_bounds__(kFG * kKG * 64) void k_q4_few(Q4Args p, const typename C::T::elem *x,
-                                                           const u32x4 *codes,
-                                                           const typename C::T::elem *scales,
-                                                           const typename C::T::elem *zeros, End end)
+template <class T, int kMR, int kMF, int kFG, int kKG, int kSplit, bool kPoints, bool kWhole, class End>
+__global__ __launch_bounds__(kFG * kKG * 64) void k_q4_few(Q4Args p, const typename T::elem *x, const u32x4 *codes,
+                                                           const typename T::elem *scales,
+                                                           const typename T::elem *zeros, End end)
 {
-    typedef typename C::T T;
+    typedef Parts<T> X;
     constexpr int kStages = q4_stages<T, kMR, kMF, kKG, kSplit, kPoints, kWhole>(), kC = 4 / kSplit;
-    constexpr bool kLate = kMR <= 2 && !kPoints && kFG * kKG <= 8;   // else registers are short
+    // of fp32 the sums of x are formed beside the products: all parts of a block would not fit registers
+    constexpr bool kFirst = T::kBf16 && !kPoints;
     constexpr int kSteps = kBlockK / (8 * T::kPiece);       // of 128 bytes of x in a block
     constexpr int kStep = kMR * 16 * 8;                     // pieces of such a step
     constexpr int kFeeds = 2 * kMR * kSteps;                // loads of 1024 bytes of x in a block
@@ -413,23 +429,13 @@ __global__ __launch_bounds__(kFG * kKG * 64) void k_q4_few(Q4Args p, const typen
     t.clear();
 #pragma unroll
     for (int n = 0; n < kMR; ++n)
-        if (n % kKG == kg) end.add_rows(t, n, f0, r0 + 16 * n);
-    struct Sums {
-        f32x4 part[kMF][kMR], sum[kMR], by[kMF], zero[kMF];
-    };
-    Sums last = {};
-    const auto add = [&](const Sums &g) {
+        if (n % kKG == kg) {
+            Tile<kMF, 1> own;
+            own.clear();
+            end.add_tile(own, f0, r0 + 16 * n);
 #pragma unroll
-        for (int m = 0; m < kMF; ++m)
-#pragma unroll
-            for (int n = 0; n < kMR; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float v = g.part[m][n][i];
-                    if constexpr (kPoints) v = fmaf(-(C::kOffset + g.zero[m][i]), g.sum[n][i], v);
-                    t.acc[m][n][i] = fmaf(g.by[m][i], v, t.acc[m][n][i]);
-                }
-    };
+            for (int m = 0; m < kMF; ++m) t.acc[m][n] = own.acc[m][0];
+        }
     const auto use = [&](uint32_t step, int u) {
         if (step * kKG + kg >= p.blocks) return;
         const uint32_t b = block_of(step);
@@ -437,11 +443,11 @@ __global__ __launch_bounds__(kFG * kKG * 64) void k_q4_few(Q4Args p, const typen
 #pragma unroll
         for (int g = 0; g < kSplit; ++g) {
             if (kSplit > 1 && b * kSplit + g >= groups) break;
-            u32x4 fx[kC][C::kParts][kMR];
+            u32x4 fx[kC][X::kPieces][kMR];
 #pragma unroll
             for (int c = 0; c < kC; ++c)
 #pragma unroll
-                for (int h = 0; h < C::kParts; ++h) {
+                for (int h = 0; h < X::kPieces; ++h) {
                     // values 32 k + 8 q + 4 h .. of the block: bf16 piece 4 (k % 2) + q of
                     // step k / 2, fp32 piece 2 q + h of step k
                     const int k = g * kC + c, step_of = T::kBf16 ? k / 2 : k, at = T::kBf16 ? 4 * (k & 1) + q : 2 * q + h;
@@ -451,39 +457,46 @@ __global__ __launch_bounds__(kFG * kKG * 64) void k_q4_few(Q4Args p, const typen
                         else fx[c][h][n] = own[step_of * kStep + (n * 16 + l16) * 8 + (at ^ (l16 >> 1))];
                     }
                 }
-            Sums now;
+            f32x4 part[kMF][kMR], sum[kMR];
 #pragma unroll
             for (int n = 0; n < kMR; ++n) {
-                now.sum[n] = f32x4{0, 0, 0, 0};
+                sum[n] = f32x4{0, 0, 0, 0};
+                if constexpr (kFirst)
 #pragma unroll
-                for (int c = 0; c < kC; ++c)
+                    for (int c = 0; c < kC; ++c) sum[n] = Bf16::mma(all_of(false), fx[c][0][n], sum[n]);
 #pragma unroll
-                    for (int h = 0; h < C::kParts; ++h) now.sum[n] = T::mma(C::all(kPoints), fx[c][h][n], now.sum[n]);
+                for (int m = 0; m < kMF; ++m) part[m][n] = sum[n];
             }
 #pragma unroll
-            for (int m = 0; m < kMF; ++m)
+            for (int c = 0; c < kC; ++c) {
+                u32x4 fw[kMF];
 #pragma unroll
-                for (int n = 0; n < kMR; ++n) now.part[m][n] = kPoints ? f32x4{0, 0, 0, 0} : now.sum[n];
+                for (int m = 0; m < kMF; ++m) fw[m] = codes_of<T>(word[u][m][g * kC + c]);
 #pragma unroll
-            for (int c = 0; c < kC; ++c)
+                for (int n = 0; n < kMR; ++n) {
+                    u32x4 held[X::kPieces];
 #pragma unroll
-                for (int h = 0; h < C::kParts; ++h)
+                    for (int h = 0; h < X::kPieces; ++h) held[h] = fx[c][h][n];
+                    const X v(held);
 #pragma unroll
-                    for (int m = 0; m < kMF; ++m) {
-                        const u32x4 fw = C::part(word[u][m][g * kC + c], h);
+                    for (int h = 0; h < X::kParts; ++h) {
+                        if constexpr (!kFirst) sum[n] = Bf16::mma(all_of(true), v.p[h], sum[n]);
 #pragma unroll
-                        for (int n = 0; n < kMR; ++n) now.part[m][n] = T::mma(fw, fx[c][h][n], now.part[m][n]);
+                        for (int m = 0; m < kMF; ++m) part[m][n] = Bf16::mma(fw[m], v.p[h], part[m][n]);
                     }
+                }
+            }
 #pragma unroll
             for (int m = 0; m < kMF; ++m) {
-                now.by[m] = four(s[u][m][g]);
-                now.zero[m] = kPoints ? four(z[u][m][g]) : f32x4{0, 0, 0, 0};
-            }
-            if constexpr (kLate) {
-                add(last);
-                last = now;
-            } else {
-                add(now);
+                const f32x4 by = four(s[u][m][g]), zero = kPoints ? four(z[u][m][g]) : f32x4{8, 8, 8, 8};
+#pragma unroll
+                for (int n = 0; n < kMR; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float v = part[m][n][i];
+                        if constexpr (!kFirst) v = fmaf(-(kOffset<T> + zero[i]), sum[n][i], v);
+                        t.acc[m][n][i] = fmaf(by[i], v, t.acc[m][n][i]);
+                    }
             }
         }
     };
@@ -509,7 +522,6 @@ __global__ __launch_bounds__(kFG * kKG * 64) void k_q4_few(Q4Args p, const typen
             ready(std::integral_constant<int, 0>());
             use(s0 + u, u);
         }
-    if constexpr (kLate) add(last);
     wait_for<0, true>();
     __syncthreads();
     f32x4 *sums = reinterpret_cast<f32x4 *>(stage);         // [share][features][m][n]
@@ -553,10 +565,9 @@ struct Q4Call {
 };
 
 // f(kernel, features and rows of a workgroup, threads, bytes of LDS) for the kernel that a call takes.
-template <class C, class F>
+template <class T, class F>
 void q4_kernel(const Q4Call &a, F f)
 {
-    typedef typename C::T T;
     const uint32_t row = whole_row<T>(a.d_in);
     const auto sized = [&](auto kMR, auto kMF, auto kFG, auto kKG, auto kWhole) {
         constexpr int R = decltype(kMR)::value, M = decltype(kMF)::value, G = decltype(kFG)::value, K = decltype(kKG)::value;
@@ -564,14 +575,16 @@ void q4_kernel(const Q4Call &a, F f)
         const auto split = [&](auto kSplit) {
             constexpr int S = decltype(kSplit)::value;
             if (a.zeros)
-                f(&k_q4_few<C, R, M, G, K, S, true, W, EndProject<T>>, 16 * M * G, 16 * R, G * K * 64,
+                f(&k_q4_few<T, R, M, G, K, S, true, W, EndProject<T>>, 16 * M * G, 16 * R, G * K * 64,
                   q4_lds<T, R, M, G, K, S, true, W>(a.rows, row));
             else
-                f(&k_q4_few<C, R, M, G, K, S, false, W, EndProject<T>>, 16 * M * G, 16 * R, G * K * 64,
+                f(&k_q4_few<T, R, M, G, K, S, false, W, EndProject<T>>, 16 * M * G, 16 * R, G * K * 64,
                   q4_lds<T, R, M, G, K, S, false, W>(a.rows, row));
         };
-        a.group == 128 ? split(std::integral_constant<int, 1>()) : a.group == 64 ? split(std::integral_constant<int, 2>())
-                                                                                 : split(std::integral_constant<int, 4>());
+        // of fp32, four blocks of features with groups of 128 and two with smaller ones alone
+        if constexpr (T::kBf16 || M != 2)
+            if (a.group == 128) return split(std::integral_constant<int, 1>());
+        if constexpr (T::kBf16 || M != 4) a.group == 64 ? split(std::integral_constant<int, 2>()) : split(std::integral_constant<int, 4>());
     };
     const std::integral_constant<int, 1> one;
     const std::integral_constant<int, 2> two;
@@ -579,32 +592,38 @@ void q4_kernel(const Q4Call &a, F f)
     const std::integral_constant<int, 8> eight;
     const std::true_type whole;
     const std::false_type steps;
-    const Q4Shape shape = q4_shape(a.rows, a.d_in, a.d_out, T::kBf16);
+    const Q4Shape shape = q4_shape(a.rows, a.d_in, a.d_out, a.group, T::kBf16);
     const bool wide = shape == Q4Shape::wide;
     if (a.rows <= 16 && a.rows * row <= kQ4Whole)
         wide ? sized(one, one, two, four, whole) : sized(one, one, one, eight, whole);
-    else if (a.rows <= 16)
-        wide ? sized(one, two, four, two, steps) : sized(one, one, two, eight, steps);
-    else if (a.rows <= 32) {
-        const std::integral_constant<int, T::kBf16 ? 8 : 4> most;   // shares whose steps of x fit into LDS
-        wide ? sized(two, two, four, two, steps) : sized(two, one, two, most, steps);
-    } else if constexpr (T::kBf16) {
-        if (wide) sized(four, two, four, two, steps);
+    else if constexpr (T::kBf16) {
+        if (a.rows <= 16) wide ? sized(one, two, four, two, steps) : sized(one, one, two, eight, steps);
+        else if (a.rows <= 32) wide ? sized(two, two, four, two, steps) : sized(two, one, two, eight, steps);
+        else if (wide) sized(four, two, four, two, steps);
         else if (shape == Q4Shape::middle) sized(four, two, two, four, steps);
         else if (shape == Q4Shape::narrow) sized(four, one, two, four, steps);
+    } else {
+        // tiles of 16 rows: with more, splitting a wave's rows takes as long as its products; the scales
+        // of smaller groups leave registers for half the features
+        const auto tile = [&](auto kFG, auto kKG) {
+            a.group == 128 ? sized(one, four, kFG, kKG, steps) : sized(one, two, kFG, kKG, steps);
+        };
+        if (a.rows <= 16) wide ? tile(two, four) : sized(one, one, two, eight, steps);
+        else if (wide) tile(four, two);
+        else if (shape == Q4Shape::middle) tile(two, four);
+        else if (shape == Q4Shape::narrow) tile(one, eight);
     }
 }
 
-template <class C>
+template <class T>
 hipError_t few_q4(const AdapterArgs &a, const Q4Weights &w, const void *x, uint64_t x_stride, const void *bias,
                   const void *adapters, float *u, void *y, uint64_t y_stride, hipStream_t stream)
 {
-    typedef typename C::T T;
     typedef typename T::elem E;
     const Q4Args p = {a.rows, x_stride, a.d_in, a.d_out, (a.d_in + kBlockK - 1) / kBlockK};
     const EndProject<T> end = {a, u, reinterpret_cast<int32_t *>(u + a.rows * a.rank), static_cast<const E *>(adapters),
                                static_cast<const E *>(bias), static_cast<E *>(y), y_stride};
-    q4_kernel<C>({a.rows, a.d_in, a.d_out, w.group, w.zeros != nullptr},
+    q4_kernel<T>({a.rows, a.d_in, a.d_out, w.group, w.zeros != nullptr},
                  [&](auto *kernel, uint32_t features, uint32_t rows, uint32_t threads, uint32_t lds) {
         kernel<<<dim3((a.d_out + features - 1) / features, (uint32_t)((a.rows + rows - 1) / rows)), threads, lds, stream>>>(
             p, static_cast<const E *>(x), static_cast<const u32x4 *>(w.codes), static_cast<const E *>(w.scales),
@@ -614,7 +633,7 @@ hipError_t few_q4(const AdapterArgs &a, const Q4Weights &w, const void *x, uint6
 }
 
 // Raises the LDS limit of every kernel that a call may take.
-template <class C>
+template <class T>
 hipError_t prepare_few()
 {
     hipError_t e = hipSuccess;
@@ -623,7 +642,7 @@ hipError_t prepare_few()
             for (const uint32_t d_out : {8u, 64u * 256, 1u << 20})
                 for (const uint32_t group : {32, 64, 128})
                     for (const bool zeros : {false, true})
-                        q4_kernel<C>({rows, d_in, d_out, group, zeros}, [&](auto *kernel, uint32_t, uint32_t, uint32_t, uint32_t lds) {
+                        q4_kernel<T>({rows, d_in, d_out, group, zeros}, [&](auto *kernel, uint32_t, uint32_t, uint32_t, uint32_t lds) {
                             if (e == hipSuccess)
                                 e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
                                                         lds > kQ4Whole ? lds : kQ4Whole);
@@ -638,8 +657,8 @@ hipError_t prepare_q4()
     const auto raise = [](auto *kernel) {
         return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, 2 * 512 * 128);
     };
-    const hipError_t all[] = {raise(&k_big<Split, EndProject<Fp32>>), raise(&k_big<Split, EndSlice>), prepare_few<CodesBf16>(),
-                              prepare_few<CodesFp32>()};
+    const hipError_t all[] = {raise(&k_big<Split, EndProject<Fp32>>), raise(&k_big<Split, EndSlice>), prepare_few<Bf16>(),
+                              prepare_few<Fp32>()};
     for (const hipError_t e : all)
         if (e != hipSuccess) return e;
     return hipSuccess;
@@ -712,8 +731,8 @@ hipError_t launch_q4_project(const AdapterArgs &a, bool bf16, const void *x, uin
                              const void *bias, const void *adapters, float *u, const Q4Space &space, void *y,
                              uint64_t y_stride, hipStream_t stream)
 {
-    if (q4_shape(a.rows, a.d_in, a.d_out, bf16) == Q4Shape::unpack) {
-        if (!bf16 && q4_split(a.rows, a.d_in, a.d_out))
+    if (q4_shape(a.rows, a.d_in, a.d_out, w.group, bf16) == Q4Shape::unpack) {
+        if (q4_unpacked(a.rows, a.d_in, a.d_out, bf16).split)
             return split_q4(a, w, x, x_stride, bias, adapters, u, space, y, y_stride, stream);
         const hipError_t e = launch_q4_unpack(w, bf16, a.d_out, a.d_in, space.w, stream);
         if (e != hipSuccess) return e;
@@ -722,8 +741,8 @@ hipError_t launch_q4_project(const AdapterArgs &a, bool bf16, const void *x, uin
     }
     const hipError_t e = launch_adapter_shrink(a, bf16, x, x_stride, adapters, u, stream);
     if (e != hipSuccess) return e;
-    return bf16 ? few_q4<CodesBf16>(a, w, x, x_stride, bias, adapters, u, y, y_stride, stream)
-                : few_q4<CodesFp32>(a, w, x, x_stride, bias, adapters, u, y, y_stride, stream);
+    return bf16 ? few_q4<Bf16>(a, w, x, x_stride, bias, adapters, u, y, y_stride, stream)
+                : few_q4<Fp32>(a, w, x, x_stride, bias, adapters, u, y, y_stride, stream);
 }
 
 }  // namespace zo

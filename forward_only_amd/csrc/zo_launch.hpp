@@ -291,8 +291,8 @@ inline uint64_t q4_blocks(uint32_t d_out, uint32_t d_in)
 {
     return ((uint64_t)d_out + 15) / 16 * (((uint64_t)d_in + 127) / 128);
 }
-// How rows are multiplied with codes: as they are, in tiles of at most 64 rows (fp32 32) and as many
-// features a workgroup, or unpacked first.
+// How rows are multiplied with codes: as they are, in tiles of at most 64 rows and 32, 64 or 128 features
+// a workgroup (fp32: 16 rows and 64, 128 or 256 features), or unpacked first.
 enum class Q4Shape { narrow, middle, wide, unpack };
 constexpr uint32_t kQ4FewBf16 = 64, kQ4FewFp32 = 32;   // rows that are never unpacked
 constexpr uint64_t kMaxGridY = 65535;
@@ -301,29 +301,36 @@ constexpr uint64_t kMaxGridY = 65535;
 // (bf16 5120 -> 20480, 128 / 256 / 512 rows: 58 / 96 / 164 us as they are, 116 / 129 / 157 unpacked;
 // 5120 -> 5120 19 / 36 / 54 and 45 / 48 / 55.)  Up to 32 rows workgroups of 128 features where these are
 // enough for the CUs.
-inline Q4Shape q4_shape(uint64_t rows, uint32_t d_in, uint32_t d_out, bool bf16)
+// fp32, 16 rows: 256 features 1.36, 128 features 0.74, 64 features 0.42 (5120 -> 5120, 32 / 128 / 512 rows: 20 /
+// 53 / 151 us as they are, 107 / 112 / 164 unpacked; 768 -> 2304, 2112 rows 52 and 66); with groups of 64 and 32,
+// whose scales leave registers for half the features or fewer, two and three times as long.
+struct Q4Unpacked {
+    double time;               // us, unpacking included
+    bool split;                // fp32 operands
+};
+inline Q4Unpacked q4_unpacked(uint64_t rows, uint32_t d_in, uint32_t d_out, bool bf16)
 {
-    if (rows <= 32) return d_out >= 128u * 160 ? Q4Shape::wide : Q4Shape::narrow;
-    if (!bf16 || rows > 64 * kMaxGridY) return Q4Shape::unpack;
-    const double blocks = (d_in + 127) / 128;
+    const ProductTime t = product_time(rows, d_out, d_in, bf16);
+    const double weights = (double)d_in * d_out, plain = (t.big < t.mid ? t.big : t.mid) + weights * (bf16 ? 2.5 : 4.5) / 5.5e6 + 4.0;
+    if (bf16 || !split_fits(rows, d_out, d_in)) return {plain, false};
+    const double split = split_time(rows, d_out, d_in) + (10.0 * rows * d_in + 6.5 * weights) / 5.5e6 + 8.0;
+    return split < plain ? Q4Unpacked{split, true} : Q4Unpacked{plain, false};
+}
+inline Q4Shape q4_shape(uint64_t rows, uint32_t d_in, uint32_t d_out, uint32_t group, bool bf16)
+{
+    if (rows <= (bf16 ? 32 : 16)) return d_out >= 128u * 160 ? Q4Shape::wide : Q4Shape::narrow;
+    const uint32_t tile = bf16 ? 64 : 16;
+    if (rows > tile * kMaxGridY) return Q4Shape::unpack;
+    const double blocks = (d_in + 127) / 128 * (bf16 || group == 128 ? 1.0 : group == 64 ? 2.0 : 3.0);
     const auto time = [&](uint32_t features, double each) {
-        const uint64_t groups = ((uint64_t)d_out + features - 1) / features * ((rows + 63) / 64);
+        const uint64_t groups = ((uint64_t)d_out + features - 1) / features * ((rows + tile - 1) / tile);
         return (double)((groups + 255) / 256) * each * blocks;
     };
-    const double n = time(32, 0.37), m = time(64, 0.48), w = time(128, 0.82);
+    const double n = bf16 ? time(32, 0.37) : time(64, 0.42), m = bf16 ? time(64, 0.48) : time(128, 0.74),
+                 w = bf16 ? time(128, 0.82) : time(256, 1.36);
     const double best = n <= m && n <= w ? n : m <= w ? m : w;
-    if (rows > kQ4FewBf16) {
-        const ProductTime t = product_time(rows, d_out, d_in, true);
-        if ((double)d_in * d_out * 2.5 / 5.5e6 + 4.0 + (t.big < t.mid ? t.big : t.mid) < best) return Q4Shape::unpack;
-    }
+    if (rows > (bf16 ? kQ4FewBf16 : kQ4FewFp32) && q4_unpacked(rows, d_in, d_out, bf16).time < best) return Q4Shape::unpack;
     return best == n ? Q4Shape::narrow : best == m ? Q4Shape::middle : Q4Shape::wide;
-}
-// Whether unpacked fp32 weights are split, by estimated time and the bytes that splitting writes.
-inline bool q4_split(uint64_t rows, uint32_t d_in, uint32_t d_out)
-{
-    const ProductTime t = product_time(rows, d_out, d_in, false);
-    return split_fits(rows, d_out, d_in) && split_time(rows, d_out, d_in) + (10.0 * rows * d_in + 2.0 * d_in * d_out) / 5e6 + 4.0 <
-                                                (t.big < t.mid ? t.big : t.mid);
 }
 // Workspace of unpacked weights; of fp32, split or not, with the split rows of x behind the weights and
 // the product's slices behind these.

@@ -152,25 +152,30 @@ struct Split {
         return block * 3 + ((w ? 0x484u : 0x610u) >> (2 * term) & 3u);
     }
     static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) { return Bf16::mma(a, b, c); }
-    // Eight values, from value k (a multiple of 8) of a row on.
-    static __device__ __forceinline__ void store8(uint16_t *row, uint64_t k, const float *v)
+    // The parts of eight values.
+    static __device__ __forceinline__ void parts(const float *v, u32x4 *o)
     {
-        u32x4 o[3];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint32_t half[3][2];
+            uint32_t held[3][2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const float x = v[2 * i + j];
                 const float r = x - __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
                 const float s = r - __uint_as_float(__float_as_uint(r) & 0xFFFF0000u);
-                half[0][j] = __float_as_uint(x) >> 16;
-                half[1][j] = __float_as_uint(r) >> 16;
-                half[2][j] = __float_as_uint(s) >> 16;
+                held[0][j] = __float_as_uint(x);
+                held[1][j] = __float_as_uint(r);
+                held[2][j] = __float_as_uint(s);
             }
 #pragma unroll
-            for (int p = 0; p < 3; ++p) o[p][i] = half[p][0] | half[p][1] << 16;
+            for (int p = 0; p < 3; ++p) o[p][i] = __builtin_amdgcn_perm(held[p][1], held[p][0], 0x07060302u);
         }
+    }
+    // Eight values, from value k (a multiple of 8) of a row on.
+    static __device__ __forceinline__ void store8(uint16_t *row, uint64_t k, const float *v)
+    {
+        u32x4 o[3];
+        parts(v, o);
         uint16_t *to = row + k / 64 * 192 + k % 64;
 #pragma unroll
         for (int p = 0; p < 3; ++p) *reinterpret_cast<u32x4 *>(to + 64 * p) = o[p];
@@ -533,36 +538,53 @@ struct EndProject {
         for (uint32_t j = 0; j < a.rank; j += 8) {
             const f32x4 *pu = reinterpret_cast<const f32x4 *>(u + row * a.rank + j);
             const f32x4 ua = pu[0], ub = pu[1];
-            u32x4 fb[kMF][4][8 / T::kPiece];
-            uint8_t sg[kMF][4];
+            constexpr int kAtOnce = T::kBf16 || kMF < 4 ? kMF : 2;     // more would spill
 #pragma unroll
-            for (int m = 0; m < kMF; ++m)
+            for (int m0 = 0; m0 < kMF; m0 += kAtOnce) {
+                if constexpr (kAtOnce < kMF) asm volatile("" ::: "memory");
+                u32x4 fb[kAtOnce][4][8 / T::kPiece];
+                uint8_t sg[kAtOnce][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t f = f0 + 16 * m + 4 * q + i;
-                    const uint64_t at = first + (uint64_t)(f < a.d_out ? f : a.d_out - 1) * a.rank + j;
+                for (int m = 0; m < kAtOnce; ++m)
 #pragma unroll
-                    for (int h = 0; h < 8 / T::kPiece; ++h) fb[m][i][h] = piece_at<T>(adapters + at + h * T::kPiece);
-                    sg[m][i] = *(gr.bits ? gr.bits + (at >> 3) : reinterpret_cast<const uint8_t *>(&kZeros));
-                }
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t f = f0 + 16 * (m0 + m) + 4 * q + i;
+                        const uint64_t at = first + (uint64_t)(f < a.d_out ? f : a.d_out - 1) * a.rank + j;
 #pragma unroll
-            for (int m = 0; m < kMF; ++m)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float s = 0.0f;
-#pragma unroll
-                    for (int h = 0; h < 8 / T::kPiece; ++h) {
-                        const u32x4 v = gr.bits ? T::move(fb[m][i][h], sg[m][i] >> (h * T::kPiece), gr.alpha)
-                                                : fb[m][i][h];
-#pragma unroll
-                        for (int k = 0; k < T::kPiece; ++k) {
-                            const int c = h * T::kPiece + k;
-                            s = fmaf(T::value(v, k), c < 4 ? ua[c & 3] : ub[c & 3], s);
-                        }
+                        for (int h = 0; h < 8 / T::kPiece; ++h) fb[m][i][h] = piece_at<T>(adapters + at + h * T::kPiece);
+                        sg[m][i] = *(gr.bits ? gr.bits + (at >> 3) : reinterpret_cast<const uint8_t *>(&kZeros));
                     }
-                    t.acc[m][n][i] += a.scale * s;
-                }
+#pragma unroll
+                for (int m = 0; m < kAtOnce; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float s = 0.0f;
+#pragma unroll
+                        for (int h = 0; h < 8 / T::kPiece; ++h) {
+                            const u32x4 v = gr.bits ? T::move(fb[m][i][h], sg[m][i] >> (h * T::kPiece), gr.alpha)
+                                                    : fb[m][i][h];
+#pragma unroll
+                            for (int k = 0; k < T::kPiece; ++k) {
+                                const int c = h * T::kPiece + k;
+                                s = fmaf(T::value(v, k), c < 4 ? ua[c & 3] : ub[c & 3], s);
+                            }
+                        }
+                        t.acc[m0 + m][n][i] += a.scale * s;
+                    }
+            }
         }
+    }
+
+    // 16 rows: of one group on MFMA, else each its own.
+    template <class Tl>
+    __device__ __forceinline__ void add_tile(Tl &t, uint32_t f0, uint64_t r0) const
+    {
+        static_assert(Tl::kMR == 1, "16 rows");
+        if (a.n_groups == 0 || r0 >= a.rows) return;
+        const uint64_t row = r0 + (threadIdx.x & 15);
+        const int32_t g = row < a.rows ? group[row] : -1, first = __builtin_amdgcn_readfirstlane(g);
+        if (first >= 0 && (uint32_t)first < a.n_groups && __all(g == first || row >= a.rows)) add_groups(t, (uint32_t)first, f0, r0);
+        else add_rows(t, 0, f0, r0);
     }
 
     template <class Tl>

@@ -588,7 +588,7 @@ zo_status zo_q4_unpack(zo_ctx *ctx, const void *d_codes, const void *d_scales, c
  * more where that is estimated to be faster (bf16, up to some hundred), the weights are not rounded; else they are
  * unpacked into the workspace first, rounded to the dtype; large fp32 products then take both operands split
  * into three bf16 each, 24 bits in all, of which products below 2^-21 of the whole are left out.  x beyond 2^100 may
- * overflow on the way (a code enters as 128 + q, fp32 sums).  A weight that is NaN or infinite makes its
+ * overflow on the way (a bf16 code enters as 16 + q, sums are fp32).  A weight that is NaN or infinite makes its
  * feature NaN or infinite in every row, a value of x that is makes its row so, perhaps NaN.
  * d_workspace: at least zo_q4_workspace_bytes(...) bytes, 256-byte aligned; sizes never fall as rows grow.
  * So few rows without groups need none.

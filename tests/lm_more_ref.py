@@ -1,7 +1,7 @@
 """Plain 64-bit references of the 4-bit projection and the distillation loss, with their bounds
 (u = 2^-24 and the bf16 half step as in lm_ref).
 
-  * 4-bit projection, weights as they are held.  A group's sum of x (o + q) (bf16: o = 128; fp32: 0) and
+  * 4-bit projection, weights as they are held.  A group's sum of x (o + q) (bf16: o = 16; fp32: 0) and
     of x is at most |x_g| |o + q| and |x_g| sqrt(G) (2-norms), each rounded G times: 8 sqrt(G) u of
     these is eight standard deviations of roundings of random sign.  Their difference, formed by one
     fused multiply-add, and the scale's product round once more each, of values no larger.  With
@@ -72,7 +72,7 @@ def q4_bound(x, scales, zeros, dtype):
     d_in = x.shape[1]
     groups = scales.shape[0]
     size = d_in // groups
-    o = 128.0 if dtype == torch.bfloat16 else 0.0
+    o = 16.0 if dtype == torch.bfloat16 else 0.0
     xg = torch.linalg.vector_norm(x.double().view(x.shape[0], groups, size), dim=2)
     z = torch.full_like(scales, 8.0).double() if zeros is None else zeros.double().abs()
     each = scales.double().abs() * (8 * math.sqrt(size) + 2) * U32 * math.sqrt(size) * (2 * o + 15 + z)

@@ -202,6 +202,16 @@ def test_row_counts(ctx, rows, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("group,zeros", [(32, True), (64, False), (128, True), (128, False)])
+@pytest.mark.parametrize("lengths,d_in,d_out", [([1] * 15, 1280, 20488), ([9, 21], 256, 20488), ([23, 17], 128, 16424),
+                                                ([1, 50, 13], 256, 32760), ([200, 56], 256, 8200)])
+def test_many_features(ctx, lengths, d_in, d_out, group, zeros, dtype):
+    """Workgroups of more features, with row tiles."""
+    p = _problem(lengths, d_in, d_out, 8, 3, dtype, seed=8)
+    _check(ctx, p, _weight(d_out, d_in, group, dtype, zeros), 8)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("lengths,d_in,d_out", [([1500, 548], 1056, 1032), ([700] * 3 + [1], 800, 2056), ([3000], 96, 1800)])
 def test_large_batches(ctx, lengths, d_in, d_out, dtype):
     """Tiles of 256 x 256, whole and in slices; of fp32 with operands split into bf16, ends of k within 64."""

@@ -13,7 +13,8 @@ sizes).  All arithmetic runs in the library's HIP kernels; there is no CPU path.
     zo_update(ctx, theta, offset, step, c, eta)             # theta - eta * sum c_i z_i
 
 The language-model operators (zo_adapter_project, zo_q4_project, zo_head_logprobs,
-zo_token_logprobs, zo_distill_loss, zo_group_loss) turn a batch of rows into such losses; their matrices may have rows further
+zo_token_logprobs, zo_distill_loss, zo_group_loss; and zo_head_grad, the last layer's exact
+gradient) turn a batch of rows into such losses; their matrices may have rows further
 apart than their length, and what they allocate belongs to the stream they run on.
 """
 from __future__ import annotations
@@ -25,7 +26,8 @@ import torch
 
 from . import _lib
 from ._lib import (ZO_BF16, ZO_EHIP, ZO_EINVAL, ZO_ENOMEM, ZO_EUNSUPPORTED, ZO_FP32,  # noqa: F401
-                   ZO_IGNORE_TOKEN, ZO_MAX_NPERT, ZO_MAX_RANK, ZO_MAX_TEACHER, ZO_MAX_TOP_K, ZO_NOALLOC_SCRATCH_BYTES, ZO_OK, ZO_Q4_FEW, ZO_WEIGHTS_POWER, ZO_WEIGHTS_PRECOND,
+                   ZO_IGNORE_TOKEN, ZO_MAX_NPERT, ZO_MAX_RANK, ZO_MAX_TEACHER, ZO_MAX_TOP_K,
+                   ZO_NOALLOC_SCRATCH_BYTES, ZO_OK, ZO_Q4_FEW, ZO_WEIGHTS_POWER, ZO_WEIGHTS_PRECOND,
                    ZO_WEIGHTS_SPSA_MEAN, ZOError)
 
 __all__ = [

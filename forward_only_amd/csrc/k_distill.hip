@@ -5,6 +5,10 @@
 //   loss = T^2 sum_j p_j (log p_j - log q_{id_j}),   d loss / d x_v = T (q_v - sum_{id_j = v} p_j).
 // With m = max_v x_v and s = sum_v e^{(x_v - m) / T}, log q_v = (x_v - m) / T - log s; all in
 // fp32, the gradient rounded once.
+//
+// What bounds it: many rows with a gradient, reading and writing each logit once (bf16 8192 x 50272,
+// 1.65 GB: 306 to 330 us, 5.0 to 5.4 TB/s, as fast as a copy); 2080 rows of bf16 without a gradient
+// 26 us; few rows, a row's own latency.
 #include <math.h>
 
 #include <type_traits>
@@ -89,14 +93,12 @@ struct Teacher {
 };
 
 // One workgroup per row.  kHold > 0: the row stays in registers, kHold pieces a thread, between the
-// sums and the gradient; 0: it is read again for the gradient.
+// sums and the gradient; 0: it is read again for the gradient.  1024 threads of bf16: two workgroups a CU
+// (8192 rows of 50272, 400 -> 330 us; fp32 rows would spill, 515 of 32003 16 -> 19 us).
 template <class T, int kThreads, int kHold, bool kGrad, bool kOnce>
-// 1024 threads of bf16: two workgroups a CU (8192 rows of 50272, kernel 400 -> 330 us; fp32 rows would
-// spill, 515 of 32003 16 -> 19 us).
-__global__ __launch_bounds__(kThreads, kThreads == 1024 && sizeof(T) == 2 ? 8 : 1) void k_distill(const T *logits, uint32_t vocab, uint64_t stride,
-                                                      Teacher teacher, const int64_t *targets, float tau,
-                                                      float *loss, const float *row_grad, T *grad,
-                                                      uint64_t grad_stride)
+__global__ __launch_bounds__(kThreads, kThreads == 1024 && sizeof(T) == 2 ? 8 : 1) void k_distill(
+    const T *logits, uint32_t vocab, uint64_t stride, Teacher teacher, const int64_t *targets, float tau, float *loss,
+    const float *row_grad, T *grad, uint64_t grad_stride)
 {
     typedef Piece<T> P;
     constexpr int kPiece = P::kPiece, kWaves = kThreads / kWave, kEntries = kMaxTeacher / kWave;
@@ -296,7 +298,8 @@ __global__ __launch_bounds__(kThreads, kThreads == 1024 && sizeof(T) == 2 ? 8 : 
 
 hipError_t launch_distill(const DistillArgs &a, bool bf16, hipStream_t stream)
 {
-    // What the last cache does not hold is read, and the gradient written, past the caches.
+    // What the last cache does not hold is read, and the gradient written, past the caches (bf16 8192 x
+    // 50272: 387 -> 306 us); not where rows are read twice.
     const auto launch_as = [&](auto *p, auto threads, auto hold, auto with, auto once) {
         using E = std::remove_cv_t<std::remove_pointer_t<decltype(p)>>;
         constexpr int kThreads = decltype(threads)::value;
@@ -320,7 +323,7 @@ hipError_t launch_distill(const DistillArgs &a, bool bf16, hipStream_t stream)
     };
     const auto typed = [&](auto *p) {
         // the fewest threads that hold a row, eight pieces each; fp32 in 1024 threads sixteen (bf16
-        // would spill)
+        // would spill).  Without a gradient nothing is held, and more rows a CU hide each other's ends.
         const uint64_t pieces = (uint64_t)a.vocab * sizeof(*p) / 16;
         const std::integral_constant<int, 64> wave;
         const std::integral_constant<int, 256> few;

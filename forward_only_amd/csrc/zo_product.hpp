@@ -443,9 +443,11 @@ struct ProductArgs {
     // Where the values of k are rows that count: how many do, on the device; both operands hold
     // zeros from there to the next multiple of 8.
     const uint32_t *k_count = nullptr;
+    // For an ending: most never have a count.
+    template <class End>
     __device__ __forceinline__ uint32_t depth() const
     {
-        if (!k_count) return k;
+        if (!End::kCounted || !k_count) return k;
         const uint32_t n = (*k_count + 7) / 8 * 8;
         return n < k ? n : k;
     }
@@ -479,7 +481,7 @@ struct Tile {
 // Ending of zo_adapter_project and zo_q4_project.  Without groups all rows are the product's.
 template <class T>
 struct EndProject {
-    static constexpr bool kSlices = false;
+    static constexpr bool kSlices = false, kCounted = false;
     static constexpr uint32_t kRowwise = 4;
     AdapterArgs a;
     const float *u;
@@ -748,7 +750,7 @@ struct EndProject {
 
 // Ending of zo_head_logprobs: per wave tile and row (m, s, t) over the tile's features.
 struct EndHead {
-    static constexpr bool kSlices = false;
+    static constexpr bool kSlices = false, kCounted = false;
     uint32_t features;
     uint64_t base, rows;        // places of this launch
     const int64_t *targets;     // of all rows, or nullptr
@@ -884,7 +886,7 @@ __global__ __launch_bounds__(512, 2) void k_big(ProductArgs p, const typename T:
     enum { F0, F1, R0, R1 };
     extern __shared__ u32x4 stage[];                        // [2][F0, F1, R0, R1][128][kPieces]
     const uint64_t rows = places(p.base, p.rows, count);
-    const uint32_t depth = p.depth(), steps = T::steps(depth);
+    const uint32_t depth = p.depth<End>(), steps = T::steps(depth);
     const uint64_t pitch = T::pitch(p.k);
     const Cut cut(p, rows, steps);
     uint32_t tile, first = 0, last = steps;
@@ -1002,7 +1004,7 @@ __global__ __launch_bounds__(512, 2) void k_big(ProductArgs p, const typename T:
 
 // The ending of a slice: its sums, to be added by k_slices.
 struct EndSlice {
-    static constexpr bool kSlices = true;
+    static constexpr bool kSlices = true, kCounted = true;
     float *slices;
     __device__ __forceinline__ uint32_t begin(uint64_t) const { return 0; }
     template <class Tl>
@@ -1024,7 +1026,7 @@ __global__ __launch_bounds__(256) void k_slices(ProductArgs p, const uint32_t *c
 {
     __shared__ u32x4 lds[3 * 8 * 64];
     const uint64_t rows = places(p.base, p.rows, count);
-    const Cut cut(p, rows, T::steps(p.depth()));
+    const Cut cut(p, rows, T::steps(p.depth<End>()));
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t i = blockIdx.x / 32, of = blockIdx.x / 4 % 8, n = blockIdx.x % 4;
@@ -1090,7 +1092,7 @@ __global__ __launch_bounds__(256) void k_mid(ProductArgs p, const typename T::el
         const uint64_t r = r0 + i < rows ? r0 + i : rows - 1;
         src[1][j] = x + (list ? list[p.base + r] : p.base + r) * p.x_stride + piece;
     }
-    const uint32_t depth = p.depth(), steps = (depth + kStep - 1) / kStep;
+    const uint32_t depth = p.depth<End>(), steps = (depth + kStep - 1) / kStep;
     const auto issue = [&](uint32_t step) {
         const bool in = (uint64_t)step * kStep + piece < depth;
 #pragma unroll
@@ -1172,7 +1174,7 @@ __global__ __launch_bounds__((kFewWaves + kMR) * 64) void k_few(ProductArgs p,
         end.store(own, f0, 16 * n);
         return;
     }
-    const F feed(stage + wave * kFewStages * F::kStage, p.depth(), [&](int i) {
+    const F feed(stage + wave * kFewStages * F::kStage, p.depth<End>(), [&](int i) {
         if (i < 16 * kMF) {
             const uint32_t f = f0 + i < p.features ? f0 + i : p.features - 1;
             return w + (uint64_t)f * p.k;

@@ -182,7 +182,8 @@ def spsa_step_adapters(ctx, adapters: torch.Tensor, *, step: int, npert: int, ep
     adapter_probe_groups -- its adapted projections with zo_adapter_project(ctx, x, weight,
     adapters, rank, **groups.of_project()) -- and returns the targets' log probabilities,
     float32 [groups * rows] (zo_head_logprobs or zo_token_logprobs, with targets repeated
-    once per group).  With adapters of several projections in the buffer, each beginning at a
+    once per group), or what is to be largest in their place (minus zo_distill_loss).
+    Frozen weights in 4 bits take zo_q4_project with the same groups.  With adapters of several projections in the buffer, each beginning at a
     multiple of 128, a projection takes its part [a, b): adapters[a:b], offset + a, and of
     stored rows bits[:, a // 8:][:, :zo_bits_stride(b - a)].contiguous().  The loss of a group
     is its mean negative log probability (zo_group_loss).  At most probes_per_batch probes go

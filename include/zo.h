@@ -50,7 +50,7 @@
  *    zo_perturb2, zo_stream_rmw) and the plane generator run one chunk per wave in a
  *    non-persistent grid.
  *  - Language-model operators (zo_token_logprobs, zo_head_logprobs, zo_adapter_project,
- *    zo_group_loss): launches only, like the step's calls, and no state in the context; their
+ *    zo_q4_*, zo_distill_loss, zo_head_grad, zo_group_loss): launches only, like the step's calls, and no state in the context; their
  *    workspaces belong to the caller, and two calls that may overlap (on two streams, or in
  *    two captured graphs) need one each.
  */
@@ -364,14 +364,16 @@ zo_status zo_mlp_loss_pair_noalloc(zo_ctx *ctx, const float *d_params, uint64_t 
  * The ends of a language model's forward pass ("N forward passes, loss only" box of the
  * flowchart in "Pretraining Transformers Without Backprop: What Two Zero-Order Papers
  * Actually Measure") for steps whose parameters are low-rank adapters: many probes' rows in
- * one batch share each load of the weights (zo_adapter_project), the last hidden states
- * become log probabilities (zo_head_logprobs, or zo_token_logprobs where logits are at
- * hand), and these one loss per probe and sign (zo_group_loss) for zo_probe_weights.
+ * one batch share each load of the weights (zo_adapter_project, or zo_q4_project with weights
+ * in 4 bits), the last hidden states become log probabilities (zo_head_logprobs, or
+ * zo_token_logprobs where logits are at hand) or a divergence from a teacher (zo_distill_loss),
+ * and these one loss per probe and sign (zo_group_loss) for zo_probe_weights.  The last layer's
+ * exact gradient needs no pass back through the model (zo_head_grad).
  *
  * Row indices on the device (targets, starts, ids, probes) are not seen by the host.  Values
  * outside their range never lead to an access outside a buffer: starts are forced into
  * [0, rows], and what depends on another bad index becomes NaN, so that zo_probe_weights
- * drops the probe.  Inputs and outputs must not overlap.  Workspace sizes never fall as rows
+ * drops the probe.  Inputs and outputs must not overlap (but for zo_distill_loss).  Workspace sizes never fall as rows
  * grow: a workspace for the largest batch serves every smaller one.
  *
  * Every call is deterministic: repeated on the same arguments it gives the same bits.  But the

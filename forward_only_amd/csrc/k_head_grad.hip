@@ -11,8 +11,8 @@
 // g, turned over, for dW.  The products take their operands along the neighbouring values that they
 // sum over, so h and W are turned over, too.  Pieces after the first add to dW in fp32.
 //
-// What bounds it: the three products (bf16 7168 to 50272, 5300 rows that count: 2.17, 2.2 and 2.2 ms of 7.7,
-// 1.3 to 1.4 PFLOP/s, as fast as the library's own); turning W over costs 0.3 and the shares 0.3, both
+// What bounds it: the three products (bf16 7168 to 50272, 4096 rows that count: 2.17, 2.2 and 2.2 ms of 7.6,
+// 1.34 PFLOP/s, as fast as the library's own); turning W over costs 0.3 and the shares 0.3, both
 // at the rate of a copy.  Of large fp32 products the operands are split into bf16 (Split): 2048 rows, 768 to
 // 50272, 4.1 -> 2.7 ms, less than three products of fp32 MFMA at its peak (3.1).
 //

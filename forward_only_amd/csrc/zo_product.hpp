@@ -138,7 +138,7 @@ struct Fp32 {
 // rounded), and a product as six of theirs: x0 w0 + x0 w1 + x1 w0 + x0 w2 + x2 w0 + x1 w1.  What is left
 // out is below 2^-21 |x w|, on average 2^-23, as much as an fp32 sum of a few terms rounds.  bf16 MFMA is
 // 9 to 10 times as fast as fp32.  A row holds its values 64 at a time: 64 x0, 64 x1, 64 x2, with
-// zeros behind the last value.  An infinity becomes NaN.
+// zeros behind the last value.  An infinity becomes NaN; parts below 2^-126 may be lost.
 struct Split {
     typedef uint16_t elem;
     static constexpr bool kBf16 = true;

@@ -529,7 +529,7 @@ zo_status zo_distill_loss(zo_ctx *ctx, const void *d_logits, zo_dtype dtype, uin
  * (d_row_grad, device float [rows], NULL: 1 for each row).  Rows are taken in pieces of at most 2^28 logits
  * (at least 256 rows, at most 2^18), so that the workspace holds that many in fp32 and no more; the gradients'
  * sums are fp32 and rounded once.  Large products of fp32 are formed of operands split into three bf16 each,
- * 24 bits in all, of which products below 2^-21 of the whole are left out.  Of more than 16 rows D is rounded to the dtype before its products, with g for
+ * 24 bits in all (of values below 2^-100 perhaps fewer), of which products below 2^-21 of the whole are left out.  Of more than 16 rows D is rounded to the dtype before its products, with g for
  * d_weight_grad and without for d_hidden_grad.  Rows with the ignored target are not computed in batches of
  * more than 16 rows; their logp and gradient are 0 and they add nothing to d_weight_grad, whatever they
  * hold.  A target outside the vocabulary, or a row that holds NaN or an infinity, makes the row's logp and
@@ -587,10 +587,11 @@ zo_status zo_q4_unpack(zo_ctx *ctx, const void *d_codes, const void *d_scales, c
 /* zo_adapter_project with W in 4 bits: y = x W^T + bias + scale (x A_g^T) B_g^T, all weights read as
  * they are held.  x, scales, zeros, bias, adapters and y share `dtype`.  d_starts and d_ids may both be NULL
  * with n_groups == 0: all rows without adapters.  Up to ZO_Q4_FEW_BF16 rows (or ZO_Q4_FEW_FP32), and of
- * more where that is estimated to be faster (bf16, up to some hundred), the weights are not rounded; else they are
- * unpacked into the workspace first, rounded to the dtype; large fp32 products then take both operands split
- * into three bf16 each, 24 bits in all, of which products below 2^-21 of the whole are left out.  x beyond 2^100 may
- * overflow on the way (a bf16 code enters as 16 + q, sums are fp32).  A weight that is NaN or infinite makes its
+ * more where that is estimated to be faster (up to some hundred, fp32 some thousand), the weights are not
+ * rounded; else they are unpacked into the workspace first, rounded to the dtype; large fp32 products then take
+ * both operands split into three bf16 each, 24 bits in all, of which products below 2^-21 of the whole are left
+ * out.  x beyond 2^100 may overflow on the way (a bf16 code enters as 16 + q, sums are fp32); fp32 values below
+ * 2^-100 may lose bits (their parts are bf16).  A weight that is NaN or infinite makes its
  * feature NaN or infinite in every row, a value of x that is makes its row so, perhaps NaN.
  * d_workspace: at least zo_q4_workspace_bytes(...) bytes, 256-byte aligned; sizes never fall as rows grow.
  * So few rows without groups need none.

@@ -237,6 +237,21 @@ def test_split_operands_keep_32_bits(ctx):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("rows", [5, 40, 2048])
+@pytest.mark.parametrize("power", [-100, 90])
+def test_small_and_large_values(ctx, rows, power, dtype):
+    """A power of two on x is one on y, bit for bit, as far as every part of x and every sum is a normal number."""
+    p = _problem([rows], 256, 264, 8, 1, dtype, seed=12)
+    q = _held(ctx, *_weight(264, 256, 64, dtype, True))
+    x = p["x"].cuda()
+    x = torch.where(x.abs() < 2.0 ** -9, torch.ones_like(x), x)
+    if dtype == F32:                # low parts of 2^-25 and more, or none
+        x = (x * 4096).round() / 4096
+    one = zo.zo_q4_project(ctx, x, q)
+    assert torch.equal(zo.zo_q4_project(ctx, x * 2.0 ** power, q), one * 2.0 ** power)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("lengths", [[4, 0, 9, 1], [1] * 9, [70, 200, 3]])
 def test_probes_equal_perturb_in_place(ctx, lengths, dtype):
     """Stored rows, regenerated rows and adapters moved by zo_perturb give the same bits."""

@@ -301,8 +301,8 @@ struct Q4Args {
 // Few rows.  What bounds the product is reading the codes once: one row, bf16 7168 to 28672, 106 MB in 23
 // us, 4.6 TB/s; with more rows VALU issue and the steps' barriers (32 rows 31 us, of which 24 remain with
 // the codes' unpacking, the sums of x and the scaling left out).  A workgroup takes 16 kMF kFG
-// features and 16 kMR rows (up to that many: all), its waves being kFG of features times kKG that share the blocks of k among
-// them.  Codes go straight to registers, a block a load, kStages - 1 blocks ahead.  The sums of
+// features and 16 kMR rows, its waves being kFG of features times kKG that share the blocks of k
+// among them.  Codes go straight to registers, a block a load, kStages - 1 blocks ahead.  The sums of
 // the shares meet in LDS; before the first block wave (f, g) adds the adapters' products of its
 // features and of the rows g, g + kKG, .. (of 16) to its own (of one group on MFMA: fp32 2112 rows in 33
 // groups, 768 to 2304, 75 -> 58 us).

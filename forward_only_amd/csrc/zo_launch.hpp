@@ -295,18 +295,11 @@ inline uint64_t q4_blocks(uint32_t d_out, uint32_t d_in)
 // a workgroup (fp32: 16 rows and 64, 128 or 256 features), or unpacked first.
 enum class Q4Shape { narrow, middle, wide, unpack };
 constexpr uint32_t kQ4FewBf16 = 64, kQ4FewFp32 = 32;   // rows that are never unpacked
-constexpr uint64_t kMaxGridY = 65535;
-// By estimated time.  Measured per block of 128 values of k, 64 rows of bf16, a round of one
-// workgroup a CU: 128 features 0.82 us, 64 features 0.48, 32 features 0.37; unpacking runs at 5.5 TB/s.
-// (bf16 5120 -> 20480, 128 / 256 / 512 rows: 58 / 96 / 164 us as they are, 116 / 129 / 157 unpacked;
-// 5120 -> 5120 19 / 36 / 54 and 45 / 48 / 55.)  Up to 32 rows workgroups of 128 features where these are
-// enough for the CUs.
-// fp32, 16 rows: 256 features 1.36, 128 features 0.74, 64 features 0.42 (5120 -> 5120, 32 / 128 / 512 rows: 20 /
-// 53 / 151 us as they are, 107 / 112 / 164 unpacked; 768 -> 2304, 2112 rows 52 and 66); with groups of 64 and 32,
-// whose scales leave registers for half the features or fewer, two and three times as long.
+constexpr uint64_t kMaxGridY = 65535;                  // a grid's lines, of one row tile each
+// What unpacking and the product take; of fp32, whether with split operands.
 struct Q4Unpacked {
-    double time;               // us, unpacking included
-    bool split;                // fp32 operands
+    double time;               // us
+    bool split;
 };
 inline Q4Unpacked q4_unpacked(uint64_t rows, uint32_t d_in, uint32_t d_out, bool bf16)
 {
@@ -316,6 +309,13 @@ inline Q4Unpacked q4_unpacked(uint64_t rows, uint32_t d_in, uint32_t d_out, bool
     const double split = split_time(rows, d_out, d_in) + (10.0 * rows * d_in + 6.5 * weights) / 5.5e6 + 8.0;
     return split < plain ? Q4Unpacked{split, true} : Q4Unpacked{plain, false};
 }
+// By estimated time.  Measured per block of 128 values of k, 64 rows of bf16, a round of one
+// workgroup a CU: 128 features 0.82 us, 64 features 0.48, 32 features 0.37; unpacking runs at 5.5 TB/s
+// (bf16 5120 -> 20480, 128 / 256 / 512 rows: 58 / 96 / 164 us as they are, 116 / 129 / 157 unpacked;
+// 5120 -> 5120 19 / 36 / 54 and 45 / 48 / 55).  fp32, 16 rows: 256 features 1.36, 128 features 0.74, 64 features
+// 0.42 (5120 -> 5120, 32 / 128 / 512 rows: 20 / 53 / 151 us as they are, 107 / 112 / 164 unpacked; 768 -> 2304,
+// 2112 rows 52 and 66); with groups of 64 and 32, whose scales leave registers for half the features or fewer,
+// two and three times as long.  Few rows: workgroups of the most features where these are enough for the CUs.
 inline Q4Shape q4_shape(uint64_t rows, uint32_t d_in, uint32_t d_out, uint32_t group, bool bf16)
 {
     if (rows <= (bf16 ? 32 : 16)) return d_out >= 128u * 160 ? Q4Shape::wide : Q4Shape::narrow;
